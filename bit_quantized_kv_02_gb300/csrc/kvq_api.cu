@@ -454,6 +454,7 @@ const char* kvq_status_string(kvq_status s) {
     case KVQ_ERR_BUFFER_TOO_SMALL: return "device buffer too small";
     case KVQ_ERR_CUDA: return "CUDA error";
     case KVQ_ERR_DEVICE_TIMEOUT: return "device-side wait timed out";
+    case KVQ_ERR_BAD_INDEX: return "page, length or position out of range";
   }
   return "unknown status";
 }

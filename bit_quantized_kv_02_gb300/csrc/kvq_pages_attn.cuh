@@ -1,0 +1,267 @@
+// kvq_pages_attn.cuh — what both attention kernels over the paged cache share:
+// the division of the work, bulk copies with bounded waits, and the partial
+// results of items that several CTAs hold.
+//
+// Work.  An item is a (sequence, kv head, block of query rows); its units are
+// the blocks of tokens that its rows may see.  The units of all items stand in
+// one line, sequence by sequence, and CTA c of C takes the units c*W/C ..
+// (c+1)*W/C - 1: every CTA gets the same number, whatever the lengths are, and
+// writes at most two partial results (the item it starts in and the item it
+// ends in), so the workspace depends on the card and not on the lengths.  The
+// line is worked out on the device from the lengths that hold when the kernel
+// runs; a captured launch can be replayed with others.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "kvq_pages.h"
+
+namespace kvq {
+
+// ------------------------------------------------------------- primitives --
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, int bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, int parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
+__device__ __forceinline__ unsigned long long time_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %globaltimer;\n" : "=l"(t));
+  return t;
+}
+// Waits for the phase; gives up (false) after two seconds.
+static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, int parity) {
+  const unsigned long long t0 = time_ns();
+  do {
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try(bar, parity)) return true;
+  } while (time_ns() - t0 < 2000000000ull);
+  return false;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, int parity) {
+  return mbar_try(bar, parity) || mbar_wait_slow(bar, parity);
+}
+// Bulk copy global -> shared; both addresses and the size multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, int bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+__device__ __forceinline__ void fence_mbar_init() {
+  asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+}
+
+// -------------------------------------------------------------------- work --
+
+// A sequence of the call, clamped into the arrays: rows [s0, s0 + n), length
+// len, first new token at position len - n.
+struct Seq {
+  int s0, n, len;
+  int p0;  // len - n, may be negative
+};
+
+__device__ __forceinline__ Seq load_seq(const PagesView& pv, const BatchView& bv, int b, bool* bad) {
+  const int a = bv.q_start[b], e = bv.q_start[b + 1], l = bv.lens[b];
+  const long cap = bv.stride << pv.lg_pt;
+  Seq s;
+  s.s0 = min(max(a, 0), bv.new_tokens);
+  s.n = min(max(e, s.s0), bv.new_tokens) - s.s0;
+  s.len = (int)min((long)max(l, 0), min(cap, 1L << 30));
+  *bad = a != s.s0 || e != s.s0 + s.n || l != s.len;
+  s.p0 = s.len - s.n;
+  return s;
+}
+
+// Tokens that rows [r0, r1) of the sequence may see, in blocks of BK: the
+// first block and their number (at least one: an item without tokens still
+// writes its zeros).
+template <int BK>
+__device__ __forceinline__ void row_blocks(const Seq& s, int rep, int window, int r0, int r1, int* lo, int* nb) {
+  const int hi = max(s.p0 + (r1 - 1) / rep + 1, 0);
+  const int first = window > 0 ? max((long)s.p0 + r0 / rep - window + 1, 0L) : 0;
+  *lo = first / BK;
+  *nb = max((hi + BK - 1) / BK - *lo, 1);
+}
+
+// One CTA's piece of an item.
+struct Piece {
+  int b, head;
+  Seq s;
+  int r0, rows;     // query rows [r0, r0 + rows) of the sequence (token * rep + head of the group)
+  int blk, nblk;    // the piece: blocks [blk, blk + nblk)
+  int has_first, has_last;  // the item's first / last block is in the piece
+  long item0, item1;        // the item's units
+};
+
+// The line of units, as one CTA sees it.  `pre` (shared, kPagesMaxBatch + 1
+// entries) holds the units before each sequence.
+template <int BK, int ROWS>
+struct Work {
+  long pre[kPagesMaxBatch + 1];
+  long total;
+  int ctas;
+  Piece piece;
+};
+
+template <int BK, int ROWS>
+__device__ __forceinline__ long seq_units(const AttnArgs& a, const Seq& s, int lane) {
+  const int R = s.n * a.rep;
+  if (R <= a.rows_lo || R > a.rows_hi) return 0;
+  long sum = 0;
+  for (int m = lane; m < (R + ROWS - 1) / ROWS; m += 32) {
+    int lo, nb;
+    row_blocks<BK>(s, a.rep, a.window, m * ROWS, min(R, (m + 1) * ROWS), &lo, &nb);
+    sum += nb;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// All threads of the CTA; leaves the line in *w.
+template <int BK, int ROWS>
+__device__ __forceinline__ void plan_work(const AttnArgs& a, Work<BK, ROWS>* w) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  if (a.rows_hi <= ROWS && a.window == 0) {
+    // one block of rows per sequence: a thread each
+    for (int b = threadIdx.x; b < a.bv.batch; b += blockDim.x) {
+      bool bad;
+      const Seq s = load_seq(a.pv, a.bv, b, &bad);
+      const int R = s.n * a.rep;
+      if (bad) atomicOr(a.pv.err, 1);
+      w->pre[b + 1] = R <= a.rows_lo || R > a.rows_hi ? 0 : (long)a.pv.heads * max((s.len + BK - 1) / BK, 1);
+    }
+  } else {
+    for (int b = warp; b < a.bv.batch; b += warps) {
+      bool bad;
+      const Seq s = load_seq(a.pv, a.bv, b, &bad);
+      const long u = seq_units<BK, ROWS>(a, s, lane) * a.pv.heads;
+      if (lane == 0) {
+        w->pre[b + 1] = u;
+        if (bad) atomicOr(a.pv.err, 1);
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    long run = 0;
+    for (int b0 = 0; b0 < a.bv.batch; b0 += 32) {
+      const int b = b0 + lane;
+      long x = b < a.bv.batch ? w->pre[b + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      x += run;
+      if (b < a.bv.batch) w->pre[b + 1] = x;
+      run = __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) {
+      w->pre[0] = 0;
+      w->total = run;
+      w->ctas = (int)min((long)gridDim.x, (run + a.min_units - 1) / a.min_units);
+    }
+  }
+  __syncthreads();
+}
+
+template <int BK, int ROWS>
+__device__ __forceinline__ long cta_begin(const Work<BK, ROWS>* w, int c) {
+  return w->total * c / w->ctas;
+}
+// The CTA whose range holds unit u.
+template <int BK, int ROWS>
+__device__ __forceinline__ int cta_of(const Work<BK, ROWS>* w, long u) {
+  int c = (int)(((u + 1) * w->ctas - 1) / w->total);  // largest c with c*total/ctas <= u
+  while (c > 0 && cta_begin(w, c) > u) --c;
+  while (c + 1 < w->ctas && cta_begin(w, c + 1) <= u) ++c;
+  return c;
+}
+
+// The piece that starts at unit u and ends by `end`; one warp, result in w->piece.
+template <int BK, int ROWS>
+__device__ __forceinline__ void find_piece(const AttnArgs& a, Work<BK, ROWS>* w, long u, long end) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = a.bv.batch;  // pre[lo] <= u < pre[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (w->pre[mid] <= u) lo = mid;
+    else hi = mid;
+  }
+  Piece p;
+  p.b = lo;
+  bool bad;
+  p.s = load_seq(a.pv, a.bv, lo, &bad);
+  const long per_head = (w->pre[lo + 1] - w->pre[lo]) / a.pv.heads;
+  p.head = (int)((u - w->pre[lo]) / per_head);
+  const long base = w->pre[lo] + per_head * p.head;
+  const long rel = u - base;
+  const int R = p.s.n * a.rep, tiles = (R + ROWS - 1) / ROWS;
+  long run = 0;
+  int blk0 = 0, nb = 0, m = 0;
+  for (int m0 = 0; m0 < tiles; m0 += 32) {
+    int l = 0, n = 0;
+    if (m0 + lane < tiles) row_blocks<BK>(p.s, a.rep, a.window, (m0 + lane) * ROWS, min(R, (m0 + lane + 1) * ROWS), &l, &n);
+    long x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, run + x > rel);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      nb = __shfl_sync(0xffffffffu, n, src);
+      blk0 = __shfl_sync(0xffffffffu, l, src);
+      run += __shfl_sync(0xffffffffu, x, src) - nb;
+      m = m0 + src;
+      break;
+    }
+    run += __shfl_sync(0xffffffffu, x, 31);
+  }
+  p.r0 = m * ROWS;
+  p.rows = min(R - p.r0, ROWS);
+  p.item0 = base + run;
+  p.item1 = p.item0 + nb;
+  p.blk = blk0 + (int)(u - p.item0);
+  p.nblk = (int)(min(end, p.item1) - u);
+  p.has_first = u == p.item0;
+  p.has_last = u + p.nblk == p.item1;
+  if (lane == 0) w->piece = p;
+}
+
+// Byte address of the record that holds token `tok` of a sequence's head; a bad
+// page index is replaced by page 0 and recorded.
+__device__ __forceinline__ int page_index(const AttnArgs& a, int b, int tok) {
+  return a.bv.table[b * a.bv.stride + (tok >> a.pv.lg_pt)];
+}
+__device__ __forceinline__ const char* tile_addr(const AttnArgs& a, int page, int head, int tok) {
+  if ((unsigned)page >= (unsigned)a.pv.pages) {
+    atomicOr(a.pv.err, 1);
+    page = 0;
+  }
+  return record_of(a.pv, page, head, tok & ((1 << a.pv.lg_pt) - 1));
+}
+
+__device__ __forceinline__ void store_out2(const AttnArgs& a, long at, float x, float y) {
+  if (a.q_bf16) static_cast<__nv_bfloat162*>(a.out)[at >> 1] = __floats2bfloat162_rn(x, y);
+  else static_cast<__half2*>(a.out)[at >> 1] = __floats2half2_rn(x, y);
+}
+
+}  // namespace kvq

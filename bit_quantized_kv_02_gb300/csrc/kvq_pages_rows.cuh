@@ -1,0 +1,562 @@
+// kvq_pages_rows.cuh — paged attention for few query rows per kv head (single
+// tokens, drafted tokens, short chunks): bound by reading the cache once.
+//
+// A CTA of four warps walks its units of 64 tokens; each warp takes 16 of them,
+// one record, brought by a single bulk copy into the warp's own ring of
+// stages, and runs an independent softmax over its tokens, so nothing but the
+// end of an item synchronises the warps.  Query rows are the 16 rows of
+// m16n8k16 (MT tiles of them), so all query heads of a kv head and several new
+// tokens share one read of the cache.
+//  - 16-bit pages: ldmatrix reads keys and (transposed) values straight from
+//    the swizzled rows.
+//  - codes: the contraction does not care about the order of channels, tokens
+//    or output columns, so each lane is given runs that are contiguous in
+//    memory: keys, channels t*D/4 .. of token (n>>1) + 4*(n&1) (n: the lane's
+//    column, t = lane % 4); values, channels g*D/8 .. (g = lane / 4) of tokens
+//    t, t+4, t+8, t+12.  Each run lies in one group (or two), so a lane needs
+//    one (zero, step) per token.  Codes become fp16 by an or with 1024's bits
+//    and one exact subtraction; zero + code * step is one fp16 fma, the value
+//    that the page stands for.
+// Scores, maxima, sums and outputs are fp32.  Probabilities are rounded to the
+// operand type (fp16, or bf16 for bf16 pages) for the value product, where the
+// rounding error of single weights averages out to less than the output's own
+// rounding; they enter as p * 2^7 with a maximum that lags by up to 2^8, so
+// that fp16 weights stay normal down to 2^-21 of the largest.
+#pragma once
+
+#include "kvq_pages_attn.cuh"
+
+namespace kvq {
+
+constexpr int kRowsWarps = 4;
+constexpr int kRowsBlock = 16 * kRowsWarps;  // tokens of a unit
+
+template <int FMT>
+struct Fmt {
+  static constexpr int KB = FMT <= kFmtBf16 ? 16 : (FMT == kFmt88 || FMT == kFmt84 ? 8 : 4);
+  static constexpr int VB = FMT <= kFmtBf16 ? 16 : (FMT == kFmt88 || FMT == kFmt48 ? 8 : 4);
+  static constexpr bool kBf16 = FMT == kFmtBf16;
+  static constexpr bool kQuant = KB < 16;
+};
+
+template <int D, int FMT, int MT>
+struct RowsCfg {
+  using F = Fmt<FMT>;
+  static constexpr int ROWS = 16 * MT;
+  // a record with the most metadata (groups of 32)
+  static constexpr int STAGE = 2 * D * (F::KB + F::VB) + (F::kQuant ? 2 * 16 * (D / 32) * 4 : 0);
+  static constexpr int NS = 20480 / STAGE < 2 ? 2 : (20480 / STAGE > 8 ? 8 : 20480 / STAGE);
+  static constexpr int RING = kRowsWarps * NS * STAGE;
+  static constexpr int MERGE = kRowsWarps * ROWS * (D + 2) * 4;
+  static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool BF16>
+__device__ __forceinline__ void mma16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    mma_16816(c, a[0], a[1], a[2], a[3], b0, b1);
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  if (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t x;
+  asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(x) : "r"(a) : "memory");
+  return x;
+}
+// N 32-bit words from shared memory, in the widest loads
+template <int N>
+__device__ __forceinline__ void ldsv(uint32_t a, uint32_t* x) {
+  if (N == 1) {
+    x[0] = lds32(a);
+  } else if (N == 2) {
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(x[0]), "=r"(x[1]) : "r"(a) : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                   : "=r"(x[4 * i]), "=r"(x[4 * i + 1]), "=r"(x[4 * i + 2]), "=r"(x[4 * i + 3])
+                   : "r"(a + 16 * i)
+                   : "memory");
+  }
+}
+// two codes in the low bits of both halves -> zero + code * step
+__device__ __forceinline__ uint32_t dequant2(uint32_t codes, __half2 s, __half2 z) {
+  const __half2 c = __hsub2(as_h2(codes | 0x64006400u), as_h2(0x64006400u));
+  return as_u32(__hfma2(c, s, z));
+}
+
+// One 16-token record's scores: acc[m][n8 tile] += Q K^T.
+template <int D, int FMT, int MT>
+__device__ __forceinline__ void rows_scores(uint32_t st, const PagesLayout& L, const uint32_t (*q)[D / 16][4], int lane,
+                                            float (*acc)[2][4]) {
+  using F = Fmt<FMT>;
+  if constexpr (!F::kQuant) {
+    const int row = (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
+    const uint32_t base = st + row * 128;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      const int chunk = 2 * ks + ch;
+      uint32_t b[4];
+      ldsm4(base + (chunk >> 3) * 2048 + (((chunk & 7) ^ (row & 7)) << 4), b);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        mma16<F::kBf16>(acc[m][0], q[m][ks], b[0], b[1]);
+        mma16<F::kBf16>(acc[m][1], q[m][ks], b[2], b[3]);
+      }
+    }
+  } else {
+    constexpr int SPAN = D / 4;               // channels a lane reads of a token
+    constexpr int RUN = SPAN < 32 ? SPAN : 32;  // channels in one group at least
+    constexpr int W = RUN * F::KB / 32;       // words of a run
+    const int g = lane >> 2, t = lane & 3;
+    const int tok = (g >> 1) + 4 * (g & 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t row = st + (8 * h + tok) * (D * F::KB / 8) + t * (SPAN * F::KB / 8);
+      const uint32_t meta = st + L.km_off + (8 * h + tok) * ((D >> L.k_lg) * 4);
+#pragma unroll
+      for (int r = 0; r < SPAN / RUN; ++r) {
+        const __half2 zs = as_h2(lds32(meta + ((t * SPAN + r * RUN) >> L.k_lg) * 4));
+        const __half2 z = __low2half2(zs), s = __high2half2(zs);
+        uint32_t w[W];
+        ldsv<W>(row + r * (RUN * F::KB / 8), w);
+#pragma unroll
+        for (int i = 0; i < RUN / 4; ++i) {  // one mma step: 4 channels
+          uint32_t b0, b1;
+          if (F::KB == 8) {
+            b0 = dequant2(__byte_perm(w[i], 0, 0x4140), s, z);
+            b1 = dequant2(__byte_perm(w[i], 0, 0x4342), s, z);
+          } else {
+            const uint32_t x = w[i / 2] >> (8 * (i & 1));
+            b0 = dequant2(x & 0x000f000fu, s, z);
+            b1 = dequant2((x >> 4) & 0x000f000fu, s, z);
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) mma16<false>(acc[m][h], q[m][r * (RUN / 4) + i], b0, b1);
+        }
+      }
+    }
+  }
+}
+
+// o[m][n8 tile] += P V of one record; p: the probabilities as A operands.
+template <int D, int FMT, int MT>
+__device__ __forceinline__ void rows_values(uint32_t st, const PagesLayout& L, const uint32_t (*p)[4], int lane,
+                                            float (*o)[D / 8][4]) {
+  using F = Fmt<FMT>;
+  if constexpr (!F::kQuant) {
+    const int row = (lane & 7) + (((lane >> 3) & 1) << 3), ch = lane >> 4;
+    const uint32_t base = st + L.v_off + row * 128;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+      const int chunk = 2 * j + ch;
+      uint32_t b[4];
+      ldsm4t(base + (chunk >> 3) * 2048 + (((chunk & 7) ^ (row & 7)) << 4), b);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        mma16<F::kBf16>(o[m][2 * j], p[m], b[0], b[1]);
+        mma16<F::kBf16>(o[m][2 * j + 1], p[m], b[2], b[3]);
+      }
+    }
+  } else {
+    constexpr int RUN = D / 8;           // channels a lane reads of a token
+    constexpr int W = RUN * F::VB / 32;  // words of them
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t w[4][W];
+    __half2 zs[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int tok = t + 4 * j;
+      zs[j] = as_h2(lds32(st + L.vm_off + (tok * (D >> L.v_lg) + ((g * RUN) >> L.v_lg)) * 4));
+      ldsv<W>(st + L.v_off + tok * (D * F::VB / 8) + g * (RUN * F::VB / 8), w[j]);
+    }
+    __half2 z[2], s[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      z[h] = __lows2half2(zs[2 * h], zs[2 * h + 1]);
+      s[h] = __highs2half2(zs[2 * h], zs[2 * h + 1]);
+    }
+    if (F::VB == 8) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        uint32_t x[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          x[h][0] = __byte_perm(w[2 * h][i], w[2 * h + 1][i], 0x5140);
+          x[h][1] = __byte_perm(w[2 * h][i], w[2 * h + 1][i], 0x7362);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t sel = (c & 1) ? 0x4342 : 0x4140;
+          const uint32_t b0 = dequant2(__byte_perm(x[0][c >> 1], 0, sel), s[0], z[0]);
+          const uint32_t b1 = dequant2(__byte_perm(x[1][c >> 1], 0, sel), s[1], z[1]);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) mma16<false>(o[m][4 * i + c], p[m], b0, b1);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        uint32_t x[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          x[h][0] = __byte_perm(w[2 * h][i], w[2 * h + 1][i], 0x5410);
+          x[h][1] = __byte_perm(w[2 * h][i], w[2 * h + 1][i], 0x7632);
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t b0 = dequant2((x[0][c & 1] >> (4 * (c >> 1))) & 0x000f000fu, s[0], z[0]);
+          const uint32_t b1 = dequant2((x[1][c & 1] >> (4 * (c >> 1))) & 0x000f000fu, s[1], z[1]);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) mma16<false>(o[m][8 * i + c], p[m], b0, b1);
+        }
+      }
+    }
+  }
+}
+
+// The query rows as A operands, and what their scores are to be multiplied by.
+// Over codes q becomes fp16: a bf16 row is scaled by the power of two that puts
+// its largest magnitude in [2^14, 2^15), so that nothing overflows and its 8
+// significant bits survive down to 2^-28 of the largest.
+template <int D, int FMT, int MT>
+__device__ __forceinline__ void load_queries(const AttnArgs& a, const Piece& p, int lane, uint32_t (*q)[D / 16][4],
+                                             float (*sc)[2]) {
+  using F = Fmt<FMT>;
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = p.r0 + min(m * 16 + g + 8 * e, p.rows - 1);
+      const uint16_t* row = static_cast<const uint16_t*>(a.q) + (long)(p.s.s0 + r / a.rep) * a.q_stride +
+                            (long)(p.head * a.rep + r % a.rep) * D;
+      auto pair = [&](int c) -> uint32_t {
+        if (a.q_aligned) return *reinterpret_cast<const uint32_t*>(row + c);
+        return (uint32_t)row[c] | (uint32_t)row[c + 1] << 16;
+      };
+      sc[m][e] = a.scale_log2;
+      if constexpr (!F::kQuant) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          q[m][ks][e] = pair(ks * 16 + 2 * t);
+          q[m][ks][2 + e] = pair(ks * 16 + 8 + 2 * t);
+        }
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          q[m][ks][e] = pair(t * (D / 4) + 4 * ks);
+          q[m][ks][2 + e] = pair(t * (D / 4) + 4 * ks + 2);
+        }
+        if (a.q_bf16) {
+          float mx = 0.0f;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t w = q[m][ks][e + 2 * i];
+              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))));
+            }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const int E = norm_exp(mx);
+          // 2^E in two factors: E may pass the range of one float
+          const float f0 = exp2i(E / 2), f1 = exp2i(E - E / 2);
+          sc[m][e] = a.scale_log2 * exp2i(-(E / 2)) * exp2i(-(E - E / 2));
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t w = q[m][ks][e + 2 * i];
+              q[m][ks][e + 2 * i] = pack2<false>(__uint_as_float(w << 16) * f0 * f1, __uint_as_float(w & 0xffff0000u) * f0 * f1);
+            }
+        }
+      }
+    }
+}
+
+template <int D, int FMT, int MT>
+__global__ void __launch_bounds__(kRowsWarps * 32) pages_rows_kernel(const __grid_constant__ AttnArgs a) {
+  using C = RowsCfg<D, FMT, MT>;
+  using F = Fmt<FMT>;
+  constexpr int ROWS = C::ROWS, NS = C::NS, BK = kRowsBlock;
+  extern __shared__ __align__(1024) char smem[];
+  __shared__ Work<BK, ROWS> work;
+  __shared__ __align__(8) uint64_t bars[kRowsWarps * NS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * NS * C::STAGE;
+  const uint32_t bar = smem_u32(bars) + warp * NS * 8;
+  if (lane < NS) mbar_init(bar + lane * 8, 1);
+  fence_mbar_init();
+  pdl_wait();
+  plan_work(a, &work);
+  pdl_trigger();
+  if (cta >= work.ctas) {
+    if (threadIdx.x == 0) a.split[cta].parts = 0;
+    return;
+  }
+  long u = cta_begin(&work, cta);
+  const long end = cta_begin(&work, cta + 1);
+  int stage = 0, phase = 0;  // of the next tile to be read; the ring is empty between pieces
+  bool alive = true, joined = false;
+  while (u < end) {
+    if (warp == 0) find_piece(a, &work, u, end);
+    __syncthreads();
+    const Piece p = work.piece;
+    u += p.nblk;
+    // this warp's records: tile index 4 * block + warp, while it holds a visible token
+    const int see1 = max(p.s.p0 + (p.r0 + p.rows - 1) / a.rep + 1, 0);
+    const int see0 = a.window > 0 ? max(p.s.p0 + p.r0 / a.rep - a.window + 1, 0) : 0;
+    const int tiles = (see1 + 15) >> 4;
+    int j = 0;
+    const int nt = max(min((tiles - warp + kRowsWarps - 1) / kRowsWarps - p.blk, p.nblk), 0);
+    if (j < nt && ((p.blk * kRowsWarps + warp) << 4) + 16 <= see0) ++j;
+    const int tok0 = (p.blk * kRowsWarps + warp) << 4;  // token of tile j: tok0 + 64 * j
+
+    // the first stages, one lane each
+    if (lane < min(NS, nt - j) && alive) {
+      const int tok = tok0 + BK * (j + lane);
+      int s = stage + lane;
+      s = s >= NS ? s - NS : s;
+      const char* src = tile_addr(a, page_index(a, p.b, tok), p.head, tok);
+      mbar_expect(bar + s * 8, a.pv.L.tile_bytes);
+      bulk_load(ring + s * C::STAGE, src, a.pv.L.tile_bytes, bar + s * 8);
+    }
+    __syncwarp();
+    int next = j + NS < nt ? page_index(a, p.b, tok0 + BK * (j + NS)) : 0;
+
+    uint32_t q[MT][D / 16][4];
+    float sc[MT][2];
+    load_queries<D, FMT, MT>(a, p, lane, q, sc);
+    float o[MT][D / 8][4], mx[MT][2], sum[MT][2];
+    int pos[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[m][i][e] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[m][e] = -INFINITY;
+        sum[m][e] = 0.0f;
+        pos[m][e] = p.s.p0 + (p.r0 + min(m * 16 + g + 8 * e, p.rows - 1)) / a.rep;
+      }
+    }
+    const int pos_lo = p.s.p0 + p.r0 / a.rep, pos_hi = p.s.p0 + (p.r0 + p.rows - 1) / a.rep;
+
+    for (; j < nt && alive; ++j) {
+      alive = mbar_wait(bar + stage * 8, phase);
+      if (!alive) {
+        if (lane == 0) atomicOr(a.pv.err, 2);
+        break;
+      }
+      const uint32_t st = ring + stage * C::STAGE;
+      const int tok = tok0 + BK * j;
+      if (tok + 16 > p.s.len) {  // the sequence ends inside this record: what lies behind has no effect
+        const int n = p.s.len - tok;
+        if (!F::kQuant) {
+          for (int i = lane; i < (16 - n) * (D / 8); i += 32) {
+            const int r = n + i / (D / 8), c = i % (D / 8);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(st + a.pv.L.v_off + (c >> 3) * 2048 + r * 128 + ((c & 7) << 4)),
+                         "r"(0)
+                         : "memory");
+          }
+        } else {
+          const int per = D >> a.pv.L.v_lg;
+          for (int i = lane; i < (16 - n) * per; i += 32)
+            asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(st + a.pv.L.vm_off + (n * per + i) * 4), "r"(0) : "memory");
+        }
+        fence_async();
+        __syncwarp();
+      }
+      float acc[MT][2][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[m][h][e] = 0.0f;
+      rows_scores<D, FMT, MT>(st, a.pv.L, q, lane, acc);
+      const bool edge = tok + 15 > pos_lo || (a.window > 0 && tok <= pos_hi - a.window);
+      uint32_t pa[MT][4];
+      bool grow = false;
+      float top[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float s = acc[m][h][e] * sc[m][e >> 1];
+            if (edge) {
+              const int c = F::kQuant ? tok + 8 * h + t + 4 * (e & 1) : tok + 8 * h + 2 * t + (e & 1);
+              const int at = pos[m][e >> 1];
+              if (c > at || (a.window > 0 && c <= at - a.window)) s = -INFINITY;
+            }
+            acc[m][h][e] = s;
+          }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(fmaxf(acc[m][0][2 * e], acc[m][0][2 * e + 1]), fmaxf(acc[m][1][2 * e], acc[m][1][2 * e + 1]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          top[m][e] = x;
+          grow = grow || x > mx[m][e] + 8.0f;
+        }
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float to = fmaxf(mx[m][e], top[m][e]);
+            const float f = to == -INFINITY ? 1.0f : fast_exp2(mx[m][e] - to);
+            mx[m][e] = to;
+            sum[m][e] *= f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              o[m][i][2 * e] *= f;
+              o[m][i][2 * e + 1] *= f;
+            }
+          }
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float base = mx[m][e] == -INFINITY ? 0.0f : mx[m][e] - 7.0f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float x = fast_exp2(acc[m][h][2 * e] - base), y = fast_exp2(acc[m][h][2 * e + 1] - base);
+            sum[m][e] += x + y;
+            pa[m][2 * h + e] = pack2<F::kBf16>(x, y);
+          }
+        }
+      }
+      rows_values<D, FMT, MT>(st, a.pv.L, pa, lane, o);
+      __syncwarp();
+      if (j + NS < nt) {
+        if (lane == 0) {
+          const int tn = tok + BK * NS;
+          const char* src = tile_addr(a, next, p.head, tn);
+          mbar_expect(bar + stage * 8, a.pv.L.tile_bytes);
+          bulk_load(st, src, a.pv.L.tile_bytes, bar + stage * 8);
+        }
+        if (j + NS + 1 < nt) next = page_index(a, p.b, tok + BK * (NS + 1));
+      }
+      if (++stage == NS) stage = 0, phase ^= 1;
+    }
+    if (!alive)  // copies still in flight land before their stages are used for anything else
+      for (int s = 0; s < NS; ++s) (void)mbar_wait(bar + s * 8, phase);
+
+    // ---- merge the four warps
+    __syncthreads();
+    float* mo = reinterpret_cast<float*>(smem);                 // [warp][ROWS][D]
+    float* ml = mo + kRowsWarps * ROWS * D;                     // [warp][ROWS][2]
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float s = sum[m][e];
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        const int r = warp * ROWS + m * 16 + g + 8 * e;
+        if (t == 0) ml[2 * r] = mx[m][e], ml[2 * r + 1] = s;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          if (F::kQuant) {
+            mo[r * D + 2 * t * (D / 8) + i] = o[m][i][2 * e];
+            mo[r * D + (2 * t + 1) * (D / 8) + i] = o[m][i][2 * e + 1];
+          } else {
+            *reinterpret_cast<float2*>(mo + r * D + i * 8 + 2 * t) = make_float2(o[m][i][2 * e], o[m][i][2 * e + 1]);
+          }
+        }
+      }
+    __syncthreads();
+    const bool whole = p.has_first && p.has_last;
+    const long slot = (long)cta * 2 + (p.has_first ? 1 : 0);
+    for (int i = threadIdx.x; i < p.rows * (D / 4); i += kRowsWarps * 32) {
+      const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+      float M = -INFINITY, l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kRowsWarps; ++w) M = fmaxf(M, ml[2 * (w * ROWS + r)]);
+      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kRowsWarps; ++w) {
+        const float m = ml[2 * (w * ROWS + r)];
+        const float f = m == -INFINITY ? 0.0f : fast_exp2(m - M);
+        const float4 x = *reinterpret_cast<const float4*>(mo + (w * ROWS + r) * D + c);
+        l += f * ml[2 * (w * ROWS + r) + 1];
+        y.x += f * x.x, y.y += f * x.y, y.z += f * x.z, y.w += f * x.w;
+      }
+      if (whole) {
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const int R = p.r0 + r;
+        const long at = ((long)(p.s.s0 + R / a.rep) * a.q_heads + p.head * a.rep + R % a.rep) * D + c;
+        store_out2(a, at, y.x * inv, y.y * inv);
+        store_out2(a, at + 2, y.z * inv, y.w * inv);
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + (slot * ROWS + r) * D + c) = y;
+        if (c == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * ROWS + r) * 2) = make_float2(M, l);
+      }
+    }
+    if (threadIdx.x == 0 && p.has_first && !p.has_last) {
+      SplitHead h = {};
+      h.parts = cta_of(&work, p.item1 - 1) - cta + 1;
+      h.rows = p.rows, h.row0 = p.r0, h.q_row = p.s.s0, h.head = p.head;
+      a.split[cta] = h;
+      joined = true;
+    }
+    fence_async();  // the merge's plain accesses before the next piece's copies
+    __syncthreads();
+  }
+  if (threadIdx.x == 0 && !joined) a.split[cta].parts = 0;
+}
+
+template <int D, int FMT>
+RowsKernel rows_kernel_fmt(int mt) {
+  if constexpr (D <= 128)
+    if (mt == 2) return {(const void*)pages_rows_kernel<D, FMT, 2>, (size_t)RowsCfg<D, FMT, 2>::SMEM, 0};
+  return {(const void*)pages_rows_kernel<D, FMT, 1>, (size_t)RowsCfg<D, FMT, 1>::SMEM, 0};
+}
+template <int D>
+RowsKernel rows_kernel_dim(int fmt, int mt) {
+  switch (fmt) {
+    case kFmtF16: return rows_kernel_fmt<D, kFmtF16>(mt);
+    case kFmtBf16: return rows_kernel_fmt<D, kFmtBf16>(mt);
+    case kFmt88: return rows_kernel_fmt<D, kFmt88>(mt);
+    case kFmt44: return rows_kernel_fmt<D, kFmt44>(mt);
+    case kFmt84: return rows_kernel_fmt<D, kFmt84>(mt);
+    default: return rows_kernel_fmt<D, kFmt48>(mt);
+  }
+}
+
+}  // namespace kvq

@@ -1,0 +1,6 @@
+// kvq_pages_rows_d64.cu — paged attention for few query rows, head_dim 64.
+#include "kvq_pages_rows.cuh"
+
+namespace kvq {
+RowsKernel rows_kernel_d64(int fmt, int mt) { return rows_kernel_dim<64>(fmt, mt); }
+}  // namespace kvq

@@ -1,0 +1,532 @@
+// kvq_pages_write.cu — the row-wise kernels of the paged cache: norm of queries
+// and keys with the rotary embedding, append of new tokens, and the read-back
+// of what the pages hold.
+//
+// All three move rows of head_dim channels once through registers: a lane owns
+// 8 neighbouring channels (16 bytes of a 16-bit row), head_dim / 8 lanes a row,
+// and a warp one token at a time, so a token's angles are loaded once for all
+// its heads and statistics (mean square, a group's minimum and maximum) are
+// shuffles between a row's lanes.  They are bound by HBM bytes for prompts and
+// by the launch and one chain of loads for single tokens, so a token's heads
+// spread over up to 8 warps when tokens are few.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "kvq_internal.h"
+#include "kvq_pages_attn.cuh"
+
+namespace kvq {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRowWarps = kThreads / 32;
+
+template <typename T>
+__device__ __forceinline__ float to_f(T x);
+template <>
+__device__ __forceinline__ float to_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_f<__half>(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// 8 neighbouring elements as loaded: one or two 16-byte words, or element by
+// element where the row is not 16-byte aligned.
+template <typename T>
+struct Row8 {
+  uint4 w[sizeof(T) / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ Row8<T> load8(const T* p, bool aligned) {
+  Row8<T> r;
+  if (aligned) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
+  } else {
+    T* e = reinterpret_cast<T*>(r.w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = p[i];
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void unpack8(const Row8<T>& r, float* x) {
+  const T* e = reinterpret_cast<const T*>(r.w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = to_f<T>(e[i]);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float* x, bool aligned) {
+  Row8<T> r;
+  T* e = reinterpret_cast<T*>(r.w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = from_f<T>(x[i]);
+  if (aligned) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = r.w[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = e[i];
+  }
+}
+
+// A lane's angles: its 8 channels' cosines and signed sines, the lane that
+// holds the partners (pairs (i, i + dim/2)), and whether the channels turn.
+struct Turn {
+  float c[8], s[8];
+  int partner;
+  bool on, halves;
+};
+
+__device__ __forceinline__ Turn load_turn(const RopeView& rv, long row, int c0, int lane) {
+  Turn t;
+  t.halves = rv.style == KVQ_ROPE_HALVES;
+  t.on = rv.table != nullptr && c0 < rv.dim;
+  t.partner = lane;
+  if (!t.on) return t;
+  const float* tab = rv.table + row * rv.dim;
+  if (!t.halves) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(tab + c0));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(tab + c0) + 1);
+    const float cs[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t.c[2 * i] = t.c[2 * i + 1] = cs[2 * i];
+      t.s[2 * i] = -cs[2 * i + 1];
+      t.s[2 * i + 1] = cs[2 * i + 1];
+    }
+  } else {
+    const int half = rv.dim / 2;
+    const bool hi = c0 >= half;
+    t.partner = lane + (hi ? -half / 8 : half / 8);
+    const float* q = tab + 2 * (hi ? c0 - half : c0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(q) + i);
+      t.c[2 * i] = a.x;
+      t.s[2 * i] = hi ? a.y : -a.y;
+      t.c[2 * i + 1] = a.z;
+      t.s[2 * i + 1] = hi ? a.w : -a.w;
+    }
+  }
+  return t;
+}
+
+// (a c - b s, b c + a s), each product and sum rounded once (the same numbers
+// whatever the compiler fuses elsewhere: quantized pages round from them).
+// Every lane of the warp calls it.
+__device__ __forceinline__ void turn8(const Turn& t, float* x) {
+  float p[8];
+  if (t.halves) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = __shfl_sync(0xffffffffu, x[i], t.partner);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = x[i ^ 1];
+  }
+  if (t.on) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], t.c[i]), __fmul_rn(p[i], t.s[i]));
+  }
+}
+
+// ------------------------------------------------------------- norm + rope --
+
+struct NormArgs {
+  const void *q, *k;
+  void *q_out, *k_out;
+  long qs, ks, qos, kos;
+  const void *qw, *kw;
+  int tokens, q_heads, kv_heads, norm, w_f32;
+  float eps;
+  int lg_wpt;       // log2 of the warps that share a token
+  int aligned;      // every row may be moved 16 bytes at a time
+};
+
+template <typename T>
+__device__ __forceinline__ void load_weight(const void* w, int w_f32, int c0, float* x) {
+  if (!w) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = 1.0f;
+  } else if (w_f32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = static_cast<const float*>(w)[c0 + i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = to_f<T>(static_cast<const T*>(w)[c0 + i]);
+  }
+}
+
+template <typename T, int D, int U>
+__device__ __forceinline__ void norm_rows(const T* src, T* dst, int heads, int sub, int nsub, int lane, bool norm,
+                                          float eps, const float* w, const Turn& turn, bool bad, bool aligned) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  const int rg = lane / LPR, c0 = (lane % LPR) * 8;
+  // U rows in flight per lane
+  for (int h0 = sub * RPW; h0 < heads; h0 += nsub * RPW * U) {
+    Row8<T> r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = min(h0 + u * nsub * RPW + rg, heads - 1);
+      r[u] = load8(src + (long)h * D + c0, aligned);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int hu = h0 + u * nsub * RPW;
+      if (hu >= heads) break;
+      float x[8];
+      unpack8(r[u], x);
+      if (norm) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float inv = 1.0f / sqrtf(ss * (1.0f / D) + eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
+      }
+      turn8(turn, x);
+      if (bad) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __int_as_float(0x7fffffff);
+      }
+      const int h = hu + rg;
+      if (h < heads) store8(dst + (long)h * D + c0, x, aligned);
+    }
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormArgs a, RopeView rv) {
+  constexpr int LPR = D / 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nsub = 1 << a.lg_wpt, sub = warp & (nsub - 1);
+  const int c0 = (lane % LPR) * 8;
+  pdl_wait();
+  pdl_trigger();
+  float qw[8], kw[8];
+  if (a.norm) {
+    load_weight<T>(a.q_heads ? a.qw : nullptr, a.w_f32, c0, qw);
+    load_weight<T>(a.kv_heads ? a.kw : nullptr, a.w_f32, c0, kw);
+  }
+  const long step = (long)gridDim.x * (kRowWarps >> a.lg_wpt);
+  for (long t = (long)blockIdx.x * (kRowWarps >> a.lg_wpt) + (warp >> a.lg_wpt); t < a.tokens; t += step) {
+    const int row = rv.table ? rv.positions[t] : 0;
+    const bool bad = rv.table && (row < 0 || row >= rv.rows);
+    const Turn turn = load_turn(rv, bad ? 0 : row, c0, lane);
+    constexpr int U = sizeof(T) == 2 ? 4 : 2;
+    if (a.q_heads)
+      norm_rows<T, D, U>(static_cast<const T*>(a.q) + t * a.qs, static_cast<T*>(a.q_out) + t * a.qos, a.q_heads, sub, nsub,
+                         lane, a.norm, a.eps, qw, turn, bad, a.aligned);
+    if (a.kv_heads)
+      norm_rows<T, D, 1>(static_cast<const T*>(a.k) + t * a.ks, static_cast<T*>(a.k_out) + t * a.kos, a.kv_heads, sub,
+                         nsub, lane, a.norm, a.eps, kw, turn, bad, a.aligned);
+  }
+}
+
+// Warps per token: as many blocks as two waves of the card need, one warp a
+// token beyond.
+int lg_warps_per_token(long tokens, long rows_per_warp_pass) {
+  int lg = 0;
+  while (lg < 3 && (tokens << lg) < 2L * 152 * kRowWarps && (1L << lg) < rows_per_warp_pass) ++lg;
+  return lg;
+}
+
+template <typename T>
+cudaError_t launch_norm_t(const kvq_norm_rope_args& x, const RopeView& rv, NormArgs a, cudaStream_t st) {
+  const int rpw = 32 / (x.head_dim / 8);
+  a.lg_wpt = lg_warps_per_token(x.tokens, (x.q_heads + x.kv_heads + rpw - 1) / rpw);
+  const long per = kRowWarps >> a.lg_wpt;
+  const long blocks = std::min((x.tokens + per - 1) / per, 152L * 8 * 4);
+  const void* fn = x.head_dim == 64    ? (const void*)norm_rope_kernel<T, 64>
+                   : x.head_dim == 128 ? (const void*)norm_rope_kernel<T, 128>
+                                       : (const void*)norm_rope_kernel<T, 256>;
+  RopeView r = rv;
+  void* args[] = {&a, &r};
+  return launch_pdl(fn, dim3((unsigned)blocks), dim3(kThreads), 0, st, args);
+}
+
+// ------------------------------------------------------------------ append --
+
+// Where the new-token row t of the call goes: page, slot and angle row, or
+// page -1.  Found by the whole block for `count` rows from t0.
+struct Place {
+  int page, slot, turn;
+};
+
+__device__ __forceinline__ void find_places(const PagesView& pv, const BatchView& bv, const RopeView* rv, long t0,
+                                            int count, Place* place, int* first) {
+  if (threadIdx.x == 0) *first = 0;
+  if (t0 == 0) {  // one block looks the arrays over as attention does
+    for (int b = threadIdx.x; b < bv.batch; b += kThreads) {
+      bool bad;
+      (void)load_seq(pv, bv, b, &bad);
+      if (bad) atomicOr(pv.err, 1);
+    }
+  }
+  __syncthreads();
+  // the sequence of row t0: sequences that end at or before it
+  int below = 0;
+  for (int i = threadIdx.x; i < bv.batch; i += kThreads) below += bv.q_start[i + 1] <= t0;
+  below = __reduce_add_sync(0xffffffffu, below);
+  if ((threadIdx.x & 31) == 0 && below) atomicAdd(first, below);
+  __syncthreads();
+  if (threadIdx.x < count) {
+    const long t = t0 + threadIdx.x;
+    int b = *first;
+    while (b < bv.batch && bv.q_start[b + 1] <= t) ++b;
+    Place p = {-1, 0, 0};
+    if (b < bv.batch && t < bv.new_tokens) {
+      const int s0 = bv.q_start[b], s1 = bv.q_start[b + 1], len = bv.lens[b];
+      bool bad = s0 < 0 || t < s0 || s1 > bv.new_tokens || len < 0;
+      const long pos = (long)len - s1 + t;
+      if (!bad && pos >= 0) {
+        const long e = pos >> pv.lg_pt;
+        bad = e >= bv.stride;
+        const int page = bad ? -1 : bv.table[b * bv.stride + e];
+        bad = bad || page < 0 || page >= pv.pages;
+        int turn = 0;
+        if (!bad && rv && rv->table) {
+          const long row = rv->positions ? rv->positions[t] : pos;
+          bad = row < 0 || row >= rv->rows;
+          turn = (int)row;
+        }
+        if (!bad) p = {page, (int)(pos & ((1 << pv.lg_pt) - 1)), turn};
+      }
+      if (bad) atomicOr(pv.err, 1);
+    }
+    place[threadIdx.x] = p;
+  }
+  __syncthreads();
+}
+
+// One row's 8 channels from c0 on into its record (`rec` + `off`): 16-bit, or
+// codes with the group's metadata.  Every lane of the warp calls it.
+template <int D>
+__device__ __forceinline__ void put8(char* rec, int off, int meta_off, int bits, int lg_group, int slot, int c0,
+                                     const float* x, int page_bf16, bool write) {
+  const int t = slot & 15;
+  if (bits == 16) {
+    if (!write) return;
+    char* dst = rec + off + (c0 >> 6) * 2048 + t * 128 + ((((c0 >> 3) & 7) ^ (t & 7)) << 4);
+    if (page_bf16) store8(reinterpret_cast<__nv_bfloat16*>(dst), x, true);
+    else store8(reinterpret_cast<__half*>(dst), x, true);
+    return;
+  }
+  float mn = x[0], mx = x[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    mn = fminf(mn, x[i]);
+    mx = fmaxf(mx, x[i]);
+  }
+  for (int o = 1; o < (1 << (lg_group - 3)); o <<= 1) {
+    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  }
+  float z, s;
+  group_params(mn, mx, 0.0f, bits, 0, 0, &z, &s);
+  if (!write) return;
+  const float r = s == 0.0f ? 0.0f : __frcp_rn(s);
+  uint32_t q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = (uint32_t)quant_code_fast(x[i], z, s, r, bits, 0);
+  if (bits == 8) {
+    const uint2 w = make_uint2(q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24, q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24);
+    *reinterpret_cast<uint2*>(rec + off + t * D + c0) = w;
+  } else {
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w |= q[2 * j] << (4 * j) | q[2 * j + 1] << (16 + 4 * j);
+    *reinterpret_cast<uint32_t*>(rec + off + t * (D / 2) + c0 / 2) = w;
+  }
+  if ((c0 & ((1 << lg_group) - 1)) == 0) {
+    const int g = t * (D >> lg_group) + (c0 >> lg_group);
+    store_meta(rec + meta_off, g, 0, 0, z, s);
+  }
+}
+
+struct AppendRows {
+  const void *k, *v;
+  long ks, vs;
+  int page_bf16, lg_wpt, aligned;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) pages_append_kernel(PagesView pv, BatchView bv, RopeView rv, AppendRows a) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  __shared__ Place place[kRowWarps];
+  __shared__ int first;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nsub = 1 << a.lg_wpt, sub = warp & (nsub - 1), tpb = kRowWarps >> a.lg_wpt;
+  const int rg = lane / LPR, c0 = (lane % LPR) * 8, H = pv.heads;
+  pdl_wait();
+  pdl_trigger();
+  for (long t0 = (long)blockIdx.x * tpb; t0 < bv.new_tokens; t0 += (long)gridDim.x * tpb) {
+    __syncthreads();
+    find_places(pv, bv, &rv, t0, tpb, place, &first);
+    const Place p = place[warp >> a.lg_wpt];
+    if (p.page < 0) continue;
+    const long t = t0 + (warp >> a.lg_wpt);
+    const Turn turn = load_turn(rv, p.turn, c0, lane);
+    const T* k = static_cast<const T*>(a.k) + t * a.ks;
+    const T* v = static_cast<const T*>(a.v) + t * a.vs;
+    constexpr int U = 2;
+    for (int h0 = sub * RPW; h0 < H; h0 += nsub * RPW * U) {
+      Row8<T> kr[U], vr[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = min(h0 + u * nsub * RPW + rg, H - 1);
+        kr[u] = load8(k + (long)h * D + c0, a.aligned);
+        vr[u] = load8(v + (long)h * D + c0, a.aligned);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int hu = h0 + u * nsub * RPW;
+        if (hu >= H) break;
+        const int h = min(hu + rg, H - 1);
+        char* rec = record_of(pv, p.page, h, p.slot);
+        float x[8];
+        unpack8(kr[u], x);
+        turn8(turn, x);
+        put8<D>(rec, 0, pv.L.km_off, pv.L.k_bits, pv.L.k_lg, p.slot, c0, x, a.page_bf16, hu + rg < H);
+        unpack8(vr[u], x);
+        put8<D>(rec, pv.L.v_off, pv.L.vm_off, pv.L.v_bits, pv.L.v_lg, p.slot, c0, x, a.page_bf16, hu + rg < H);
+      }
+    }
+  }
+}
+
+// -------------------------------------------------------------------- read --
+
+template <int D>
+__device__ __forceinline__ uint4 get8(const char* rec, int off, int meta_off, int bits, int lg_group, int slot, int c0) {
+  const int t = slot & 15;
+  if (bits == 16)
+    return *reinterpret_cast<const uint4*>(rec + off + (c0 >> 6) * 2048 + t * 128 + ((((c0 >> 3) & 7) ^ (t & 7)) << 4));
+  const __half2 zs = reinterpret_cast<const __half2*>(rec + meta_off)[t * (D >> lg_group) + (c0 >> lg_group)];
+  const __half2 z = __low2half2(zs), s = __high2half2(zs);
+  uint4 out;
+  uint32_t* o = reinterpret_cast<uint32_t*>(&out);
+  uint2 w;
+  if (bits == 8) w = *reinterpret_cast<const uint2*>(rec + off + t * D + c0);
+  else w.x = *reinterpret_cast<const uint32_t*>(rec + off + t * (D / 2) + c0 / 2);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    int a, b;
+    if (bits == 8) {
+      const uint32_t x = (j < 2 ? w.x : w.y) >> (16 * (j & 1));
+      a = x & 255, b = (x >> 8) & 255;
+    } else {
+      a = (w.x >> (4 * j)) & 15, b = (w.x >> (16 + 4 * j)) & 15;
+    }
+    // zero + code * step, rounded once to fp16
+    const __half2 y = __hfma2(__floats2half2_rn((float)a, (float)b), s, z);
+    o[j] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  return out;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) pages_read_kernel(PagesView pv, BatchView bv, char* k_out, char* v_out,
+                                                              int lg_wpt) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  __shared__ Place place[kRowWarps];
+  __shared__ int first;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nsub = 1 << lg_wpt, sub = warp & (nsub - 1), tpb = kRowWarps >> lg_wpt;
+  const int rg = lane / LPR, c0 = (lane % LPR) * 8, H = pv.heads;
+  pdl_wait();
+  pdl_trigger();
+  for (long t0 = (long)blockIdx.x * tpb; t0 < bv.new_tokens; t0 += (long)gridDim.x * tpb) {
+    __syncthreads();
+    find_places(pv, bv, nullptr, t0, tpb, place, &first);
+    const Place p = place[warp >> lg_wpt];
+    if (p.page < 0) continue;
+    const long row = (t0 + (warp >> lg_wpt)) * H;
+    for (int h = sub * RPW + rg; h < H; h += nsub * RPW) {
+      const char* rec = record_of(pv, p.page, h, p.slot);
+      uint4 a, b;
+      if (k_out) a = get8<D>(rec, 0, pv.L.km_off, pv.L.k_bits, pv.L.k_lg, p.slot, c0);
+      if (v_out) b = get8<D>(rec, pv.L.v_off, pv.L.vm_off, pv.L.v_bits, pv.L.v_lg, p.slot, c0);
+      const long at = ((row + h) * D + c0) * 2;
+      if (k_out) *reinterpret_cast<uint4*>(k_out + at) = a;
+      if (v_out) *reinterpret_cast<uint4*>(v_out + at) = b;
+    }
+  }
+}
+
+unsigned token_blocks(long tokens, int lg_wpt) {
+  const long per = kRowWarps >> lg_wpt;
+  return (unsigned)std::min((tokens + per - 1) / per, 152L * 8 * 4);
+}
+
+template <typename T>
+const void* append_fn(int D) {
+  return D == 64    ? (const void*)pages_append_kernel<T, 64>
+         : D == 128 ? (const void*)pages_append_kernel<T, 128>
+                    : (const void*)pages_append_kernel<T, 256>;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+
+cudaError_t launch_norm_rope(const kvq_norm_rope_args& x, const RopeView& rv, cudaStream_t st) {
+  const int per = x.dtype == KVQ_F32 ? 4 : 8;  // elements of 16 bytes
+  NormArgs a = {};
+  a.q = x.q, a.k = x.k, a.q_out = x.q_out, a.k_out = x.k_out;
+  a.qs = x.q_stride, a.ks = x.k_stride, a.qos = x.q_out_stride, a.kos = x.k_out_stride;
+  a.qw = x.q_weight, a.kw = x.k_weight;
+  a.tokens = x.tokens, a.q_heads = x.q_heads, a.kv_heads = x.kv_heads, a.norm = x.norm, a.eps = x.eps;
+  a.w_f32 = x.weight_dtype == KVQ_F32;
+  a.aligned = (!x.q_heads || (aligned16(x.q) && aligned16(x.q_out) && x.q_stride % per == 0 && x.q_out_stride % per == 0)) &&
+              (!x.kv_heads || (aligned16(x.k) && aligned16(x.k_out) && x.k_stride % per == 0 && x.k_out_stride % per == 0));
+  if (x.dtype == KVQ_F32) return launch_norm_t<float>(x, rv, a, st);
+  if (x.dtype == KVQ_BF16) return launch_norm_t<__nv_bfloat16>(x, rv, a, st);
+  return launch_norm_t<__half>(x, rv, a, st);
+}
+
+cudaError_t launch_pages_append(const PagesView& pv, const BatchView& bv, const RopeView& rv, const void* k,
+                                const void* v, int in_dtype, int page_bf16, long k_stride, long v_stride,
+                                cudaStream_t st) {
+  const int per = in_dtype == KVQ_F32 ? 4 : 8;
+  const int rpw = 32 / (pv.head_dim / 8);
+  AppendRows a = {k, v, k_stride, v_stride, page_bf16, 0, 0};
+  a.aligned = aligned16(k) && aligned16(v) && k_stride % per == 0 && v_stride % per == 0;
+  a.lg_wpt = lg_warps_per_token(bv.new_tokens, (pv.heads + rpw - 1) / rpw);
+  PagesView p = pv;
+  BatchView b = bv;
+  RopeView r = rv;
+  void* args[] = {&p, &b, &r, &a};
+  const void* fn = in_dtype == KVQ_F32    ? append_fn<float>(pv.head_dim)
+                   : in_dtype == KVQ_BF16 ? append_fn<__nv_bfloat16>(pv.head_dim)
+                                          : append_fn<__half>(pv.head_dim);
+  return launch_pdl(fn, dim3(token_blocks(bv.new_tokens, a.lg_wpt)), dim3(kThreads), 0, st, args);
+}
+
+cudaError_t launch_pages_read(const PagesView& pv, const BatchView& bv, void* k_out, void* v_out, cudaStream_t st) {
+  const int rpw = 32 / (pv.head_dim / 8);
+  int lg = lg_warps_per_token(bv.new_tokens, (pv.heads + rpw - 1) / rpw);
+  PagesView p = pv;
+  BatchView b = bv;
+  char *ko = static_cast<char*>(k_out), *vo = static_cast<char*>(v_out);
+  void* args[] = {&p, &b, &ko, &vo, &lg};
+  const void* fn = pv.head_dim == 64    ? (const void*)pages_read_kernel<64>
+                   : pv.head_dim == 128 ? (const void*)pages_read_kernel<128>
+                                        : (const void*)pages_read_kernel<256>;
+  return launch_pdl(fn, dim3(token_blocks(bv.new_tokens, lg)), dim3(kThreads), 0, st, args);
+}
+
+}  // namespace kvq

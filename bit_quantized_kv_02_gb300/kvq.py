@@ -18,11 +18,13 @@ import torch
 
 PER_TOKEN, PER_CHANNEL = 0, 1
 ASYM, SYM = 0, 1
-F16, F32 = 0, 1
+F16, F32, BF16 = 0, 1, 2
 WHOLE_VECTOR = -1
+ROPE_PAIRS, ROPE_HALVES = 0, 1
 
 STATUS = {0: "KVQ_OK", 1: "KVQ_ERR_INVALID_ARG", 2: "KVQ_ERR_UNSUPPORTED", 3: "KVQ_ERR_CAPACITY",
-          4: "KVQ_ERR_BUFFER_TOO_SMALL", 5: "KVQ_ERR_CUDA", 6: "KVQ_ERR_DEVICE_TIMEOUT"}
+          4: "KVQ_ERR_BUFFER_TOO_SMALL", 5: "KVQ_ERR_CUDA", 6: "KVQ_ERR_DEVICE_TIMEOUT",
+          7: "KVQ_ERR_BAD_INDEX"}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libkvq.so")
@@ -51,6 +53,32 @@ class Bytes(ctypes.Structure):
                 ("alloc", ctypes.c_size_t)]
 
 
+class PagesConfig(ctypes.Structure):
+    _fields_ = [("layers", ctypes.c_int), ("pages", ctypes.c_int), ("page_tokens", ctypes.c_int),
+                ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("k", TensorCfg), ("v", TensorCfg), ("dtype", ctypes.c_int)]
+
+
+class _PagesBatch(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("new_tokens", ctypes.c_int), ("max_new", ctypes.c_int),
+                ("q_start", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("rows", ctypes.c_int), ("dim", ctypes.c_int), ("style", ctypes.c_int),
+                ("positions", ctypes.c_void_p)]
+
+
+class _NormRopeArgs(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int), ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("q_out", ctypes.c_void_p),
+                ("k_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64),
+                ("norm", ctypes.c_int), ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -59,7 +87,9 @@ EXPORTED = ["kvq_cache_bytes", "kvq_cache_create", "kvq_cache_destroy", "kvq_pre
             "kvq_device_status", "kvq_last_launches", "kvq_status_string", "kvq_last_error",
             "kvq_set_decode_plan", "kvq_refresh_lens", "kvq_decode_attn_static", "kvq_set_decode_kernel",
             "kvq_decode_kernel_specialized", "kvq_dequantize", "kvq_decode_attn_materialized",
-            "kvq_append_decode_attn", "kvq_decode_cta_warps"]
+            "kvq_append_decode_attn", "kvq_decode_cta_warps", "kvq_pages_bytes", "kvq_pages_create",
+            "kvq_pages_destroy", "kvq_pages_append", "kvq_pages_attn", "kvq_pages_read", "kvq_pages_set_kernel",
+            "kvq_pages_status", "kvq_pages_last_error", "kvq_qk_norm_rope"]
 
 
 def lib():
@@ -101,6 +131,21 @@ def lib():
         L.kvq_refresh_lens.argtypes = [P, P]
         L.kvq_last_error.argtypes = [P]
         L.kvq_last_error.restype = ctypes.c_char_p
+        PB, PR = ctypes.POINTER(_PagesBatch), ctypes.POINTER(_Rope)
+        L.kvq_pages_bytes.argtypes = [ctypes.POINTER(PagesConfig), ctypes.POINTER(Bytes)]
+        L.kvq_pages_create.argtypes = [ctypes.POINTER(PagesConfig), P, ctypes.c_size_t, P, ctypes.POINTER(P)]
+        L.kvq_pages_destroy.argtypes = [P]
+        L.kvq_pages_append.argtypes = [P, I, P, P, I, ctypes.c_int64, ctypes.c_int64, PB, PR, P]
+        L.kvq_pages_attn.argtypes = [P, I, P, I, ctypes.c_int64, PB, ctypes.c_float, I, P, P]
+        L.kvq_pages_read.argtypes = [P, I, PB, P, P, P]
+        L.kvq_pages_set_kernel.argtypes = [P, I]
+        L.kvq_pages_status.argtypes = [P, P]
+        L.kvq_pages_last_error.argtypes = [P]
+        L.kvq_pages_last_error.restype = ctypes.c_char_p
+        L.kvq_qk_norm_rope.argtypes = [ctypes.POINTER(_NormRopeArgs), PR, P]
+        for name in ("kvq_pages_bytes", "kvq_pages_create", "kvq_pages_destroy", "kvq_pages_append", "kvq_pages_attn",
+                     "kvq_pages_read", "kvq_pages_set_kernel", "kvq_pages_status", "kvq_qk_norm_rope"):
+            getattr(L, name).restype = S
         for name in ("kvq_cache_bytes", "kvq_cache_create", "kvq_cache_destroy", "kvq_prefill_quantize",
                      "kvq_append", "kvq_decode_attn", "kvq_export", "kvq_get_lens", "kvq_decode_traffic",
                      "kvq_device_status", "kvq_set_decode_plan", "kvq_refresh_lens", "kvq_decode_attn_static",
@@ -329,3 +374,255 @@ class KVQCache:
 
     def kvq_last_launches(self) -> int:
         return lib().kvq_last_launches(self.handle)
+
+
+# -------------------------------------------------------------- paged cache --
+
+_DTYPES = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+
+
+def make_pages_config(layers, pages, page_tokens, q_heads, kv_heads, head_dim, k=None, v=None,
+                      dtype=F16) -> PagesConfig:
+    """k, v: None for 16-bit values of `dtype` (F16 or BF16), or the (bits, group,
+    axis, mode) of quantized pages: 8 or 4 bits, PER_TOKEN, ASYM."""
+    def tc(t):
+        return TensorCfg(16, 0, PER_TOKEN, ASYM) if t is None else TensorCfg(*t)
+    return PagesConfig(layers, pages, page_tokens, q_heads, kv_heads, head_dim, tc(k), tc(v), dtype)
+
+
+def kvq_pages_bytes(cfg: PagesConfig) -> Bytes:
+    out = Bytes()
+    _check(lib().kvq_pages_bytes(ctypes.byref(cfg), ctypes.byref(out)), "kvq_pages_bytes")
+    return out
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _ints(t, name, device=None):
+    _need(isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.is_cuda, f"{name}: an int32 tensor on the GPU")
+    _need(device is None or t.device == device, f"{name}: on another device")
+    return t
+
+
+def _rows(t, name, heads, head_dim, device):
+    """[tokens][heads][head_dim] with heads and channels packed; returns the stride between tokens."""
+    _need(isinstance(t, torch.Tensor) and t.dim() == 3 and tuple(t.shape[1:]) == (heads, head_dim),
+          f"{name}: [tokens][{heads}][{head_dim}]")
+    _need(t.device == device, f"{name}: on another device")
+    _need(t.stride(2) == 1 and (heads == 1 or t.stride(1) == head_dim), f"{name}: heads and channels not contiguous")
+    return max(t.stride(0), heads * head_dim) if t.shape[0] < 2 else t.stride(0)
+
+
+class _On:
+    """Makes a tensor's device current where it is not, and gives its stream."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream = device, stream
+        self.guard = None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+        return ctypes.c_void_p(s.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+class PagesBatch:
+    """The rows of paged-cache calls (kvq_pages_batch): q_start [batch + 1], lens
+    [batch] and table [batch][pages] are int32 device tensors, read by the kernels
+    when they run, so their contents may change between calls and graph replays.
+    new_tokens: rows of k / v / q / out (at least q_start[batch]); max_new: the
+    most new tokens of any sequence if known (speed only)."""
+
+    def __init__(self, q_start, lens, table, new_tokens: int, max_new: int = 0):
+        _ints(q_start, "q_start")
+        _ints(lens, "lens", q_start.device)
+        _ints(table, "table", q_start.device)
+        _need(lens.dim() == 1 and q_start.dim() == 1 and q_start.shape[0] == lens.shape[0] + 1,
+              "q_start: one entry more than lens")
+        _need(table.dim() == 2 and table.shape[0] == lens.shape[0] and table.shape[1] > 0, "table: [batch][pages]")
+        _need(q_start.is_contiguous() and lens.is_contiguous() and table.is_contiguous(), "batch arrays are contiguous")
+        self.q_start, self.lens, self.table = q_start, lens, table
+        self.device = q_start.device
+        self.new_tokens = int(new_tokens)
+        self.c = _PagesBatch(lens.shape[0], self.new_tokens, int(max_new), q_start.data_ptr(), lens.data_ptr(),
+                             table.data_ptr(), table.shape[1])
+        self.ref = ctypes.byref(self.c)
+
+
+class Rope:
+    """Rotary embedding by a table of angles (kvq_rope): table [rows][dim / 2][2] fp32
+    (cosine, sine); style ROPE_PAIRS (2i, 2i+1) or ROPE_HALVES (i, i + dim/2);
+    positions: int32 [new_tokens] rows of the table, or None where the operator
+    takes the position in the sequence."""
+
+    def __init__(self, table, style: int = ROPE_PAIRS, positions=None):
+        _need(isinstance(table, torch.Tensor) and table.is_cuda and table.dtype == torch.float32 and
+              table.dim() == 3 and table.shape[2] == 2 and table.is_contiguous(), "table: fp32 [rows][dim / 2][2] on the GPU")
+        if positions is not None:
+            _ints(positions, "positions", table.device)
+            _need(positions.dim() == 1 and positions.is_contiguous(), "positions: one a token, contiguous")
+        self.table, self.positions = table, positions
+        self.device = table.device
+        self.c = _Rope(table.data_ptr(), table.shape[0], 2 * table.shape[1], int(style),
+                       positions.data_ptr() if positions is not None else None)
+        self.ref = ctypes.byref(self.c)
+
+
+def kvq_qk_norm_rope(q, k, q_weight=None, k_weight=None, eps: float = 1e-6, rope: Rope | None = None, q_out=None,
+                     k_out=None, norm: bool = True, stream=None):
+    """Norm of queries and keys per head and the rotary embedding, in one pass.
+
+    q [tokens][q_heads][head_dim], k [tokens][kv_heads][head_dim] (either may be
+    None): fp16, bf16 or fp32, slices of a joint projection included; weights
+    [head_dim] of the same type or fp32, or None for ones; norm=False only
+    rotates.  Returns (q_out, k_out), new tensors unless given (q and k themselves
+    work)."""
+    one = q if q is not None else k
+    _need(isinstance(one, torch.Tensor) and one.is_cuda and one.dim() == 3, "q: [tokens][heads][head_dim] on the GPU")
+    _need(one.dtype in _DTYPES, f"unsupported dtype {one.dtype}")
+    tokens, d, dev = one.shape[0], one.shape[2], one.device
+    a = _NormRopeArgs(tokens=tokens, head_dim=d, dtype=_DTYPES[one.dtype], norm=int(bool(norm)), eps=float(eps),
+                      weight_dtype=_DTYPES[one.dtype])
+    outs = []
+    for name, x, out, w in (("q", q, q_out, q_weight), ("k", k, k_out, k_weight)):
+        if x is None:
+            outs.append(None)
+            continue
+        _need(isinstance(x, torch.Tensor) and x.dim() == 3, f"{name}: [tokens][heads][head_dim]")
+        heads = x.shape[1]
+        stride = _rows(x, name, heads, d, dev)
+        if out is None:
+            out = torch.empty((tokens, heads, d), dtype=x.dtype, device=dev)
+        out_stride = _rows(out, name + "_out", heads, d, dev)
+        _need(x.dtype == one.dtype and out.dtype == one.dtype, f"{name}: all rows have one type")
+        _need(x.shape[0] == tokens and out.shape[0] == tokens, f"{name}: all rows are of the same tokens")
+        if name == "q":
+            a.q_heads, a.q, a.q_stride, a.q_out, a.q_out_stride = heads, x.data_ptr(), stride, out.data_ptr(), out_stride
+        else:
+            a.kv_heads, a.k, a.k_stride, a.k_out, a.k_out_stride = heads, x.data_ptr(), stride, out.data_ptr(), out_stride
+        outs.append(out)
+        if w is not None:
+            _need(w.shape == (d,) and w.is_contiguous() and w.device == dev, f"{name}_weight: [{d}]")
+            _need(w.dtype in (one.dtype, torch.float32), f"{name}_weight: {one.dtype} or fp32")
+            a.weight_dtype = _DTYPES[w.dtype]
+            if name == "q":
+                a.q_weight = w.data_ptr()
+            else:
+                a.k_weight = w.data_ptr()
+    if q_weight is not None and k_weight is not None and q is not None and k is not None:
+        _need(q_weight.dtype == k_weight.dtype, "both weights have one type")
+    if rope is not None:
+        _need(rope.device == dev, "rope: on another device")
+        _need(rope.positions is not None and rope.positions.shape[0] >= tokens, "rope: a position for every token")
+    with _On(dev, stream) as st:
+        _check(lib().kvq_qk_norm_rope(ctypes.byref(a), rope.ref if rope is not None else None, st), "kvq_qk_norm_rope")
+    return outs[0], outs[1]
+
+
+class KVQPages:
+    """A paged cache (kvq_pages_t) living in one torch uint8 device buffer."""
+
+    def __init__(self, cfg: PagesConfig, device="cuda", stream=None):
+        self.cfg = cfg
+        self.bytes = kvq_pages_bytes(cfg)
+        self.buffer = torch.empty(self.bytes.alloc, dtype=torch.uint8, device=device)
+        self.device = self.buffer.device
+        self.dtype = torch.bfloat16 if cfg.dtype == BF16 else torch.float16
+        h = ctypes.c_void_p()
+        with _On(self.device, stream) as st:
+            _check(lib().kvq_pages_create(ctypes.byref(cfg), _ptr(self.buffer), self.bytes.alloc, st, ctypes.byref(h)),
+                   "kvq_pages_create")
+        self.handle = h
+
+    def close(self):
+        if getattr(self, "handle", None):
+            lib().kvq_pages_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _fail(self, st, what):
+        raise KVQError(st, what, (lib().kvq_pages_last_error(self.handle) or b"").decode())
+
+    # C-named methods ---------------------------------------------------------
+    def kvq_pages_append(self, layer: int, k: torch.Tensor, v: torch.Tensor, batch: PagesBatch,
+                         rope: Rope | None = None, stream=None):
+        """Store the new tokens of `batch`: k, v [new_tokens][kv_heads][head_dim]
+        fp16, bf16 or fp32; the keys are turned by `rope` on the way."""
+        c = self.cfg
+        ks = _rows(k, "k", c.kv_heads, c.head_dim, self.device)
+        vs = _rows(v, "v", c.kv_heads, c.head_dim, self.device)
+        _need(k.dtype in _DTYPES and k.dtype == v.dtype, "k, v: both fp16, bf16 or fp32")
+        _need(k.shape[0] >= batch.new_tokens and v.shape[0] >= batch.new_tokens, "k, v: fewer rows than new tokens")
+        _need(batch.device == self.device, "batch: on another device")
+        if rope is not None:
+            _need(rope.device == self.device, "rope: on another device")
+            _need(rope.positions is None or rope.positions.shape[0] >= batch.new_tokens, "rope: fewer positions than new tokens")
+        with _On(self.device, stream) as st:
+            r = lib().kvq_pages_append(self.handle, layer, k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], ks, vs,
+                                       batch.ref, rope.ref if rope is not None else None, st)
+        if r:
+            self._fail(r, "kvq_pages_append")
+
+    def kvq_pages_attn(self, layer: int, q: torch.Tensor, batch: PagesBatch, out: torch.Tensor | None = None,
+                       scale: float = 0.0, window: int = 0, stream=None) -> torch.Tensor:
+        """Attention of the new tokens of `batch` over the pages: q [new_tokens][q_heads]
+        [head_dim] fp16 or bf16; returns out of the same shape and type (rows behind
+        the last sequence are left as they were; zeros in a new tensor)."""
+        c = self.cfg
+        qs = _rows(q, "q", c.q_heads, c.head_dim, self.device)
+        _need(q.dtype in (torch.float16, torch.bfloat16), "q: fp16 or bf16")
+        _need(q.shape[0] >= batch.new_tokens, "q: fewer rows than new tokens")
+        _need(batch.device == self.device, "batch: on another device")
+        with _On(self.device, stream) as st:
+            if out is None:
+                out = torch.zeros(q.shape, dtype=q.dtype, device=self.device)
+            _need(out.shape == q.shape and out.dtype == q.dtype and out.device == self.device and out.is_contiguous(),
+                  "out: contiguous, of q's shape and type")
+            r = lib().kvq_pages_attn(self.handle, layer, q.data_ptr(), _DTYPES[q.dtype], qs, batch.ref, float(scale),
+                                     int(window), out.data_ptr(), st)
+        if r:
+            self._fail(r, "kvq_pages_attn")
+        return out
+
+    def kvq_pages_read(self, layer: int, batch: PagesBatch, k_out: torch.Tensor | None = None,
+                       v_out: torch.Tensor | None = None, stream=None):
+        """What the pages hold for the new tokens of `batch`: (k, v), each [new_tokens]
+        [kv_heads][head_dim] of the pages' type (fp16 for quantized pages); rows
+        without a place are left as they were."""
+        c = self.cfg
+        shape = (batch.new_tokens, c.kv_heads, c.head_dim)
+        _need(batch.device == self.device, "batch: on another device")
+        with _On(self.device, stream) as st:
+            if k_out is None:
+                k_out = torch.empty(shape, dtype=self.dtype, device=self.device)
+            if v_out is None:
+                v_out = torch.empty(shape, dtype=self.dtype, device=self.device)
+            for x in (k_out, v_out):
+                _need(tuple(x.shape) == shape and x.dtype == self.dtype and x.device == self.device and x.is_contiguous(),
+                      "k_out, v_out: contiguous [new_tokens][kv_heads][head_dim] of the pages' type")
+            r = lib().kvq_pages_read(self.handle, layer, batch.ref, k_out.data_ptr(), v_out.data_ptr(), st)
+        if r:
+            self._fail(r, "kvq_pages_read")
+        return k_out, v_out
+
+    def kvq_pages_set_kernel(self, which: int):
+        """0: by the rows of each sequence (default); 1: the few-rows kernel; 2: the many-rows kernel."""
+        _check(lib().kvq_pages_set_kernel(self.handle, int(which)), "kvq_pages_set_kernel")
+
+    def kvq_pages_status(self, stream=None) -> int:
+        with _On(self.device, stream) as st:
+            return lib().kvq_pages_status(self.handle, st)

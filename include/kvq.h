@@ -60,12 +60,13 @@ typedef enum {
   KVQ_ERR_CAPACITY = 3,       /* a sequence would exceed max_tokens */
   KVQ_ERR_BUFFER_TOO_SMALL = 4, /* device buffer smaller than kvq_bytes.alloc */
   KVQ_ERR_CUDA = 5,           /* a CUDA runtime error (launch or asynchronous) */
-  KVQ_ERR_DEVICE_TIMEOUT = 6  /* a device-side wait gave up (reserved: no kernel waits today) */
+  KVQ_ERR_DEVICE_TIMEOUT = 6, /* a device-side wait gave up */
+  KVQ_ERR_BAD_INDEX = 7       /* a kernel met a page, length or position out of range and skipped the access */
 } kvq_status;
 
 typedef enum { KVQ_PER_TOKEN = 0, KVQ_PER_CHANNEL = 1 } kvq_axis; /* group along channels / along tokens */
 typedef enum { KVQ_ASYM = 0, KVQ_SYM = 1 } kvq_mode;
-typedef enum { KVQ_F16 = 0, KVQ_F32 = 1 } kvq_dtype;
+typedef enum { KVQ_F16 = 0, KVQ_F32 = 1, KVQ_BF16 = 2 } kvq_dtype; /* KVQ_BF16: paged cache and norm only */
 
 /* group value meaning "all kv_heads*head_dim channels of one token" (per-token axis only) */
 #define KVQ_WHOLE_VECTOR (-1)
@@ -308,6 +309,151 @@ kvq_status kvq_refresh_lens(kvq_cache_t cache, void* stream);
 /* Number of kernel launches the last kvq_decode_attn / kvq_append /
  * kvq_append_decode_attn / kvq_prefill_quantize call on this handle issued. */
 int kvq_last_launches(kvq_cache_t cache);
+
+/* ---------------------------------------------------------- paged cache ---
+ *
+ * A cache whose tokens live in pages of a pool.  The caller deals the pages out
+ * (a table of page indices per sequence), so sequences grow, share a prefix or
+ * leave without moving data, and a call takes any number of new tokens per
+ * sequence: whole prompts, chunks of a prompt, drafted tokens, single tokens,
+ * mixed in one batch.  Lengths and tables are device arrays that the kernels
+ * read when they run: a CUDA graph that captured the calls can be replayed with
+ * other lengths, pages and split of the rows (same batch and new_tokens).
+ *
+ * Pages hold each token's key and value rows as 16-bit values, or quantized per
+ * token along channels under the numerical contract above (KVQ_PER_TOKEN,
+ * KVQ_ASYM, fp16 zero point and step): such a row stands for
+ * fp16(zero + code * step), and |x| <= 65000 keeps that finite.
+ */
+typedef struct {
+  int layers;       /* >= 1 */
+  int pages;        /* pages of the pool, the same count for every layer, >= 1 */
+  int page_tokens;  /* tokens per page: 16, 32, 64 or 128 */
+  int q_heads;      /* q_heads / kv_heads: a whole number, 1..64 */
+  int kv_heads;     /* >= 1 */
+  int head_dim;     /* 64, 128 or 256 */
+  kvq_tensor_cfg k, v; /* bits 16: values of `dtype` (group, axis, mode ignored); bits 8 or 4: codes, groups of 32,
+                          64, 128 or 256 channels dividing head_dim, KVQ_PER_TOKEN, KVQ_ASYM.  Both 16, or neither */
+  int dtype;        /* KVQ_F16 or KVQ_BF16: type of 16-bit pages; KVQ_F16 for quantized ones */
+} kvq_pages_config;
+
+/* Rows of one call.  Sequence b's new tokens are the rows q_start[b] ..
+ * q_start[b+1] - 1 of k / v / q / out, in order; with lens[b] tokens in the
+ * sequence, the new ones included, row i of its n stands at position
+ * lens[b] - n + i.  Rows behind q_start[batch] are neither read nor written.
+ * Position p lives in page table[b * table_stride + p / page_tokens].  Device
+ * arrays; table entries behind a sequence's last page are not read.  A table
+ * entry outside the pool, a length beyond the table or a q_start that
+ * decreases or passes new_tokens is never followed: what it touches is skipped or read from
+ * elsewhere in the pool, and kvq_pages_status reports KVQ_ERR_BAD_INDEX. */
+typedef struct {
+  int batch;              /* sequences, 1..1024 */
+  int new_tokens;         /* rows of k / v / q / out (>= q_start[batch]), >= 0 */
+  int max_new;            /* hint: no sequence has more new tokens than this; 0 = unknown.  Speed only */
+  const int32_t* q_start; /* [batch + 1] */
+  const int32_t* lens;    /* [batch] */
+  const int32_t* table;   /* [batch][table_stride] */
+  int64_t table_stride;   /* >= 1 */
+} kvq_pages_batch;
+
+/* Rotary embedding by a table of angles: channels (a, b) of a pair become
+ * (a c - b s, b c + a s) with (c, s) = table[position][pair].  Pairs are
+ * (2i, 2i+1) (KVQ_ROPE_PAIRS) or (i, i + dim/2) (KVQ_ROPE_HALVES), i < dim/2;
+ * channels from dim on pass through. */
+typedef enum { KVQ_ROPE_PAIRS = 0, KVQ_ROPE_HALVES = 1 } kvq_rope_style;
+typedef struct {
+  const float* table;       /* device [rows][dim / 2][2] (cosine, sine), 16-byte aligned */
+  int rows;                 /* >= 1 */
+  int dim;                  /* rotated channels, a multiple of 16, 16..head_dim */
+  int style;                /* kvq_rope_style */
+  const int32_t* positions; /* device [new_tokens] row -> table row; NULL (kvq_pages_append only): the position in the sequence */
+} kvq_rope;
+
+typedef struct kvq_pages* kvq_pages_t;
+
+/* Sizes of the pool (packed, metadata, elements of all pages and layers, 16-bit
+ * rows counted as packed) and of the buffer kvq_pages_create needs (alloc).
+ * Host only.  KVQ_ERR_INVALID_ARG / KVQ_ERR_UNSUPPORTED for a bad config. */
+kvq_status kvq_pages_bytes(const kvq_pages_config* cfg, kvq_bytes* out);
+
+/* Create a paged cache inside the caller's device buffer (size >= alloc,
+ * 256-byte aligned, on the current device), zero-filled on `stream`.  The
+ * buffer must outlive the handle.  Later calls need the same device current
+ * (KVQ_ERR_INVALID_ARG otherwise).  kvq_pages_attn calls on one handle share
+ * its workspace: order them on one stream, graphs that captured them included. */
+kvq_status kvq_pages_create(const kvq_pages_config* cfg, void* device_buf, size_t buf_bytes, void* stream,
+                            kvq_pages_t* out);
+kvq_status kvq_pages_destroy(kvq_pages_t pages);
+
+/* Store the new tokens' keys and values in layer `layer`, the keys turned by
+ * `rope` on the way (NULL: as given).  k, v: device rows of [kv_heads][head_dim]
+ * elements of in_dtype (KVQ_F16, KVQ_F32, KVQ_BF16), k_stride / v_stride elements
+ * from one token's row to the next (>= kv_heads * head_dim: slices of a joint
+ * projection work).  The rotation is computed in fp32 with one rounding per
+ * operation, then rounded once to a 16-bit page or quantized as is.  A new token
+ * whose position is negative (lens[b] < n) is skipped; one whose angle row is
+ * outside the table is skipped and reported as KVQ_ERR_BAD_INDEX.  A page slot
+ * must not be written twice in one call. */
+kvq_status kvq_pages_append(kvq_pages_t pages, int layer, const void* k, const void* v, int in_dtype,
+                            int64_t k_stride, int64_t v_stride, const kvq_pages_batch* batch, const kvq_rope* rope,
+                            void* stream);
+
+/* Attention of the new tokens over layer `layer`'s pages: row i of a sequence,
+ * at position p, sees the tokens t <= p of its sequence and, with window > 0,
+ * t > p - window; out = sum_t softmax_t(scale * q . k_t) v_t with fp32 scores,
+ * maxima, sums and accumulators.  q: device rows of [q_heads][head_dim] of
+ * q_dtype, q_stride elements apart; out: device [new_tokens][q_heads][head_dim]
+ * of q_dtype, contiguous.  q_dtype: the pages' dtype, or KVQ_F16 / KVQ_BF16 over
+ * quantized pages.  Query head h reads KV head h / (q_heads / kv_heads).
+ * softmax_scale <= 0 means 1/sqrt(head_dim).  A row that sees no token yields
+ * zeros; what pages hold behind a sequence's end has no effect.  Cached values
+ * must be finite: where a row of a sequence sees one token of a 16-token tile
+ * or 128-token block, the others' values enter with weight zero. */
+kvq_status kvq_pages_attn(kvq_pages_t pages, int layer, const void* q, int q_dtype, int64_t q_stride,
+                          const kvq_pages_batch* batch, float softmax_scale, int window, void* out, void* stream);
+
+/* What layer `layer` holds for the new tokens of `batch` (q_start spanning whole
+ * sequences reads them whole): k_out, v_out device [new_tokens][kv_heads]
+ * [head_dim] of the pages' dtype (fp16 for quantized pages), 16-byte aligned;
+ * either may be NULL.  Rows with a negative position or a bad page are left as
+ * they were. */
+kvq_status kvq_pages_read(kvq_pages_t pages, int layer, const kvq_pages_batch* batch, void* k_out, void* v_out,
+                          void* stream);
+
+/* Kernel choice of kvq_pages_attn: 0 (default) by the rows (new tokens x query
+ * heads per KV head) of each sequence; 1 always the kernel for few rows; 2
+ * always the one for many.  Same results up to rounding.  Outside 0..2:
+ * KVQ_ERR_INVALID_ARG. */
+kvq_status kvq_pages_set_kernel(kvq_pages_t pages, int which);
+
+/* Synchronise `stream` and report what a kernel on this handle recorded since
+ * the last call: KVQ_ERR_BAD_INDEX, KVQ_ERR_DEVICE_TIMEOUT, or a pending CUDA
+ * error (KVQ_ERR_CUDA).  Clears the record. */
+kvq_status kvq_pages_status(kvq_pages_t pages, void* stream);
+
+/* Message of the last error seen by this handle ("" if none). */
+const char* kvq_pages_last_error(kvq_pages_t pages);
+
+/* Norm of queries and keys per head with the rotary embedding in the same pass:
+ * y = x / sqrt(mean(x^2) + eps) * weight over the head_dim channels of each head
+ * (norm != 0), then the rotation (rope with positions, or NULL), in fp32,
+ * rounded once to dtype.  q, k: device rows of [heads][head_dim] elements, one
+ * row per token, q_stride / k_stride elements apart; q_out, k_out likewise with
+ * their own strides, and may be q and k themselves.  q or k may be NULL with
+ * zero heads.  A row whose position is outside the table comes out as NaN. */
+typedef struct {
+  int tokens, q_heads, kv_heads, head_dim; /* head_dim 64, 128 or 256; tokens >= 0 */
+  int dtype;                               /* KVQ_F16, KVQ_BF16 or KVQ_F32 of q, k, q_out, k_out */
+  const void *q, *k;
+  int64_t q_stride, k_stride;
+  void *q_out, *k_out;
+  int64_t q_out_stride, k_out_stride;
+  int norm;                              /* 0: rotate only */
+  float eps;                             /* finite, >= 0 */
+  const void *q_weight, *k_weight;       /* [head_dim] of weight_dtype, or NULL for ones */
+  int weight_dtype;                      /* dtype, or KVQ_F32 */
+} kvq_norm_rope_args;
+kvq_status kvq_qk_norm_rope(const kvq_norm_rope_args* args, const kvq_rope* rope, void* stream);
 
 /* Human-readable name of a status code (static string). */
 const char* kvq_status_string(kvq_status status);

@@ -256,7 +256,7 @@ def prepare(case, seed):
         dtype = kvq.BF16 if case["dtype"] == "bf16" and not quantized else kvq.F16
         cfg = kvq.make_pages_config(1, s["pages"], pt, case.get("q_heads", h), h, d, *fmt, dtype=dtype)
         s["cache"] = kvq.KVQPages(cfg)
-        s["batch"] = kvq.PagesBatch(s["q_start"], s["lens"], s["table"], s["n"] + case.get("pad", 0))
+        s["batch"] = kvq.PagesBatch(s["q_start"], s["lens"], s["table"], s["n"] + case.get("pad", 0), s["most_new"])
         if case["op"] == "append":
             s["rope"] = kvq.Rope(s["angles"], case["style"]) if case["rope_dim"] else None
         else:

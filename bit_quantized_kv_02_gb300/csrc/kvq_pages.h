@@ -97,10 +97,11 @@ struct AttnArgs {
   SplitHead* split;  // [CTA]
 };
 
-// A kernel for few query rows: its shared memory and resident CTAs per SM.
-struct RowsKernel {
+// An attention kernel: its shared memory, threads and resident CTAs per SM.
+struct AttnKernel {
   const void* fn;
   size_t smem;
+  int threads;
   int ctas_per_sm;
 };
 
@@ -118,7 +119,8 @@ struct kvq_pages {
   int device = 0;
   int sm_count = 0;
   int which = 0;     // kernel choice (kvq_pages_set_kernel)
-  kvq::RowsKernel rows_fn[2] = {};  // few-rows kernel with one and two row tiles (one only at head_dim 256)
+  kvq::AttnKernel rows_fn[2] = {};  // few-rows kernel with one and two row tiles (one only at head_dim 256)
+  kvq::AttnKernel tile_fn = {};     // many-rows kernel
   std::string last_error;
 };
 
@@ -136,9 +138,12 @@ cudaError_t launch_norm_rope(const kvq_norm_rope_args& a, const RopeView& rv, cu
 // format and number of row tiles
 enum { kFmtF16 = 0, kFmtBf16 = 1, kFmt88 = 2, kFmt44 = 3, kFmt84 = 4, kFmt48 = 5, kFormats = 6 };
 int pages_format(const kvq_pages* P);
-RowsKernel rows_kernel_d64(int fmt, int mt);
-RowsKernel rows_kernel_d128(int fmt, int mt);
-RowsKernel rows_kernel_d256(int fmt, int mt);
+AttnKernel rows_kernel_d64(int fmt, int mt);
+AttnKernel rows_kernel_d128(int fmt, int mt);
+AttnKernel rows_kernel_d256(int fmt, int mt);
+AttnKernel tile_kernel_d64(int fmt);
+AttnKernel tile_kernel_d128(int fmt);
+AttnKernel tile_kernel_d256(int fmt);
 cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, int max_rows, cudaStream_t st);
 cudaError_t pages_attn_setup(kvq_pages* P);
 

@@ -68,24 +68,41 @@ __global__ void __launch_bounds__(kJoinWarps * 32) pages_join_kernel(const __gri
   }
 }
 
-const void* join_fn(int D, int rows) {
-  if (D == 64) return rows == 16 ? (const void*)pages_join_kernel<64, 16> : (const void*)pages_join_kernel<64, 32>;
-  if (D == 128) return rows == 16 ? (const void*)pages_join_kernel<128, 16> : (const void*)pages_join_kernel<128, 32>;
-  return (const void*)pages_join_kernel<256, 16>;
+template <int D>
+const void* join_dim(int rows) {
+  switch (rows) {
+    case 16: return (const void*)pages_join_kernel<D, 16>;
+    case 32: return (const void*)pages_join_kernel<D, 32>;
+    case 128: return (const void*)pages_join_kernel<D, 128>;
+    default: return (const void*)pages_join_kernel<D, 256>;
+  }
+}
+
+// One attention launch and the join of what its CTAs shared; `rows`: query rows
+// a CTA holds, `used`: the most that an item can have.
+cudaError_t launch_kernel(const AttnKernel& k, AttnArgs a, int ctas, int rows, int used, cudaStream_t st) {
+  void* args[] = {&a};
+  cudaError_t e = launch_pdl(k.fn, dim3(ctas), dim3(k.threads), k.smem, st, args);
+  if (e != cudaSuccess) return e;
+  const int D = a.pv.head_dim;
+  const void* join = D == 64 ? join_dim<64>(rows) : D == 128 ? join_dim<128>(rows) : join_dim<256>(rows);
+  const int y = std::max(1, std::min(std::min(rows, used), rows > 32 ? 32 : 4));
+  return launch_pdl(join, dim3(ctas, y), dim3(kJoinWarps * 32), 0, st, args);
 }
 
 cudaError_t launch_rows(kvq_pages* P, AttnArgs a, int max_rows, cudaStream_t st) {
   // Two row tiles per warp where a sequence may have more rows than one holds:
   // the cache is then read once for 32 rows.
   const int mt = max_rows > 16 && P->rows_fn[1].fn ? 2 : 1;
-  const RowsKernel& k = P->rows_fn[mt - 1];
-  const int ctas = std::min(k.ctas_per_sm * P->sm_count, kPagesCtas);
+  const AttnKernel& k = P->rows_fn[mt - 1];
   a.min_units = 2;
-  void* args[] = {&a};
-  cudaError_t e = launch_pdl(k.fn, dim3(ctas), dim3(128), k.smem, st, args);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(join_fn(a.pv.head_dim, 16 * mt), dim3(ctas, std::min(std::max(max_rows, 1), 4)), dim3(kJoinWarps * 32), 0, st,
-                    args);
+  return launch_kernel(k, a, std::min(k.ctas_per_sm * P->sm_count, kPagesCtas), 16 * mt, max_rows, st);
+}
+
+cudaError_t launch_tile(kvq_pages* P, AttnArgs a, int max_rows, cudaStream_t st) {
+  a.min_units = 2;
+  return launch_kernel(P->tile_fn, a, std::min(P->sm_count, kTileCtas), a.pv.head_dim == 256 ? kTileRows / 2 : kTileRows,
+                       max_rows, st);
 }
 
 }  // namespace
@@ -99,21 +116,33 @@ int pages_format(const kvq_pages* P) {
 
 cudaError_t pages_attn_setup(kvq_pages* P) {
   const int D = P->cfg.head_dim, fmt = pages_format(P);
-  for (int mt = 1; mt <= (D == 256 ? 1 : 2); ++mt) {
-    RowsKernel k = D == 64 ? rows_kernel_d64(fmt, mt) : D == 128 ? rows_kernel_d128(fmt, mt) : rows_kernel_d256(fmt, mt);
-    cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k.ctas_per_sm, k.fn, 128, k.smem);
+  P->rows_fn[0] = D == 64 ? rows_kernel_d64(fmt, 1) : D == 128 ? rows_kernel_d128(fmt, 1) : rows_kernel_d256(fmt, 1);
+  if (D < 256) P->rows_fn[1] = D == 64 ? rows_kernel_d64(fmt, 2) : rows_kernel_d128(fmt, 2);
+  P->tile_fn = D == 64 ? tile_kernel_d64(fmt) : D == 128 ? tile_kernel_d128(fmt) : tile_kernel_d256(fmt);
+  for (AttnKernel* k : {&P->rows_fn[0], &P->rows_fn[1], &P->tile_fn}) {
+    if (!k->fn) continue;
+    cudaError_t e = cudaFuncSetAttribute(k->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k->smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k->ctas_per_sm, k->fn, k->threads, k->smem);
     if (e != cudaSuccess) return e;
-    if (k.ctas_per_sm < 1) return cudaErrorInvalidConfiguration;
-    P->rows_fn[mt - 1] = k;
+    if (k->ctas_per_sm < 1) return cudaErrorInvalidConfiguration;
   }
   return cudaSuccess;
 }
 
 cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, int max_rows, cudaStream_t st) {
+  // Sequences with at most `few` rows go to the few-rows kernel, the others to
+  // the many-rows one.  A batch that may hold both kinds launches both.
+  const int few = P->rows_fn[1].fn ? 32 : 16;
   a.rows_lo = 0;
   a.rows_hi = INT_MAX;
-  return launch_rows(P, a, max_rows, st);
+  if (P->which == 1 || (P->which == 0 && max_rows <= few)) return launch_rows(P, a, max_rows, st);
+  if (P->which == 2 || a.bv.batch == 1) return launch_tile(P, a, max_rows, st);
+  a.rows_lo = few;
+  cudaError_t e = launch_tile(P, a, max_rows, st);
+  if (e != cudaSuccess) return e;
+  a.rows_lo = 0;
+  a.rows_hi = few;
+  return launch_rows(P, a, few, st);
 }
 
 }  // namespace kvq

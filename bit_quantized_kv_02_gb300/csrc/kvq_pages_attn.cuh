@@ -115,7 +115,6 @@ struct Work {
   long pre[kPagesMaxBatch + 1];
   long total;
   int ctas;
-  Piece piece;
 };
 
 template <int BK, int ROWS>
@@ -194,9 +193,9 @@ __device__ __forceinline__ int cta_of(const Work<BK, ROWS>* w, long u) {
   return c;
 }
 
-// The piece that starts at unit u and ends by `end`; one warp, result in w->piece.
+// The piece that starts at unit u and ends by `end`; all lanes of a warp.
 template <int BK, int ROWS>
-__device__ __forceinline__ void find_piece(const AttnArgs& a, Work<BK, ROWS>* w, long u, long end) {
+__device__ __forceinline__ Piece find_piece(const AttnArgs& a, const Work<BK, ROWS>* w, long u, long end) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = a.bv.batch;  // pre[lo] <= u < pre[hi]
   while (hi - lo > 1) {
@@ -243,7 +242,7 @@ __device__ __forceinline__ void find_piece(const AttnArgs& a, Work<BK, ROWS>* w,
   p.nblk = (int)(min(end, p.item1) - u);
   p.has_first = u == p.item0;
   p.has_last = u + p.nblk == p.item1;
-  if (lane == 0) w->piece = p;
+  return p;
 }
 
 // Byte address of the record that holds token `tok` of a sequence's head; a bad

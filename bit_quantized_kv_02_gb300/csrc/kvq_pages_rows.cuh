@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32) pages_rows_kernel(const __gri
   constexpr int ROWS = C::ROWS, NS = C::NS, BK = kRowsBlock;
   extern __shared__ __align__(1024) char smem[];
   __shared__ Work<BK, ROWS> work;
+  __shared__ Piece piece;
   __shared__ __align__(8) uint64_t bars[kRowsWarps * NS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
   const int g = lane >> 2, t = lane & 3;
@@ -327,9 +328,12 @@ __global__ void __launch_bounds__(kRowsWarps * 32) pages_rows_kernel(const __gri
   int stage = 0, phase = 0;  // of the next tile to be read; the ring is empty between pieces
   bool alive = true, joined = false;
   while (u < end) {
-    if (warp == 0) find_piece(a, &work, u, end);
+    if (warp == 0) {
+      const Piece x = find_piece(a, &work, u, end);
+      if (lane == 0) piece = x;
+    }
     __syncthreads();
-    const Piece p = work.piece;
+    const Piece p = piece;
     u += p.nblk;
     // this warp's records: tile index 4 * block + warp, while it holds a visible token
     const int see1 = max(p.s.p0 + (p.r0 + p.rows - 1) / a.rep + 1, 0);
@@ -542,13 +546,13 @@ __global__ void __launch_bounds__(kRowsWarps * 32) pages_rows_kernel(const __gri
 }
 
 template <int D, int FMT>
-RowsKernel rows_kernel_fmt(int mt) {
+AttnKernel rows_kernel_fmt(int mt) {
   if constexpr (D <= 128)
-    if (mt == 2) return {(const void*)pages_rows_kernel<D, FMT, 2>, (size_t)RowsCfg<D, FMT, 2>::SMEM, 0};
-  return {(const void*)pages_rows_kernel<D, FMT, 1>, (size_t)RowsCfg<D, FMT, 1>::SMEM, 0};
+    if (mt == 2) return {(const void*)pages_rows_kernel<D, FMT, 2>, (size_t)RowsCfg<D, FMT, 2>::SMEM, kRowsWarps * 32, 0};
+  return {(const void*)pages_rows_kernel<D, FMT, 1>, (size_t)RowsCfg<D, FMT, 1>::SMEM, kRowsWarps * 32, 0};
 }
 template <int D>
-RowsKernel rows_kernel_dim(int fmt, int mt) {
+AttnKernel rows_kernel_dim(int fmt, int mt) {
   switch (fmt) {
     case kFmtF16: return rows_kernel_fmt<D, kFmtF16>(mt);
     case kFmtBf16: return rows_kernel_fmt<D, kFmtBf16>(mt);

@@ -1,0 +1,636 @@
+// kvq_pages_tile.cuh — paged attention for many query rows per kv head (chunks
+// and prompts): bound by the tensor cores.
+//
+// One persistent CTA per SM takes its share of the units (blocks of 128
+// tokens).  Query rows are (token, head of the group) pairs, so one read of a
+// block serves every query head of the kv head; a CTA holds NT tiles of 128
+// rows (two, or one at head_dim 256, where the accumulator alone takes half of
+// the tensor memory).  Roles of the warps:
+//  - loader (16-bit pages): bulk copies of the records' halves into K and V
+//    stages; pages are stored in the operand layout, so no tensor map and no
+//    shuffling is needed;
+//  - dequantizers (codes): a warpgroup turns codes into fp16 operand tiles
+//    (the value the page stands for, one rounding);
+//  - one thread issues the matrix instructions: S = Q K^T (both from shared
+//    memory), O += P V (P from tensor memory, over the scores it came from);
+//  - softmax: a warpgroup per tile, a thread per row, so maxima and sums need
+//    no exchange; scores are read from tensor memory once, weights are written
+//    back as the operand type.  The running maximum is only raised when a score
+//    passes it by 2^8 (then O is rescaled in tensor memory): most blocks leave
+//    it alone.  With two tiles the tensor cores work on one while the other's
+//    softmax runs; with one, the scores are double-buffered instead;
+//  - a scheduler finds the pieces of items ahead of the others.
+// Scores, maxima, sums and O are fp32; weights are rounded once to the operand
+// type (p * 2^7, as in the few-rows kernel).
+#pragma once
+
+#include "kvq_pages_attn.cuh"
+#include "kvq_pages_rows.cuh"
+#include "kvq_tcgen05.cuh"
+
+namespace kvq {
+
+template <int D, int FMT>
+struct TileCfg {
+  using F = Fmt<FMT>;
+  static constexpr int NT = D == 256 ? 1 : 2;      // row tiles of 128
+  static constexpr int ROWS = 128 * NT;
+  static constexpr int BK = 128;                   // tokens of a block
+  static constexpr int NS = D == 256 ? 1 : (D == 128 ? 2 : 3);  // K stages, V stages
+  static constexpr int TILE = 128 * D * 2;         // bytes of a Q, K or V tile
+  static constexpr int Q_OFF = 0, K_OFF = NT * TILE, V_OFF = K_OFF + NS * TILE;
+  static constexpr int SMEM = V_OFF + NS * TILE + 1024;  // + alignment of the tiles
+  static constexpr int PROD = F::kQuant ? 4 : 1;   // warps that fill K and V stages
+  static constexpr int THREADS = F::kQuant ? 512 : 384;
+  static constexpr int PIECES = 4;
+};
+
+template <int D, int FMT>
+struct TileShared {
+  using C = TileCfg<D, FMT>;
+  Work<C::BK, C::ROWS> work;
+  Piece piece[C::PIECES];
+  uint64_t k_full[C::NS], k_empty[C::NS], v_full[C::NS], v_empty[C::NS];
+  uint64_t q_full, q_free, s_full[2], p_full[2], o_done[2], v_land;
+  uint64_t piece_full[C::PIECES], piece_free[C::PIECES];
+  uint32_t tmem;
+  int dead;
+};
+
+// A bounded wait that also ends when another role gave up.
+template <typename SH>
+__device__ __forceinline__ bool tile_wait(SH* sh, const AttnArgs& a, uint64_t* bar, int parity) {
+  const uint32_t b = smem_u32(bar);
+  if (mbar_try(b, parity)) return true;
+  const unsigned long long t0 = time_ns();
+  do {
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try(b, parity)) return true;
+    if (*(volatile int*)&sh->dead) return false;
+  } while (time_ns() - t0 < 2000000000ull);
+  sh->dead = 1;
+  atomicOr(a.pv.err, 2);
+  return false;
+}
+template <typename SH>
+__device__ __forceinline__ bool tile_wait_warp(SH* sh, const AttnArgs& a, uint64_t* bar, int parity) {
+  return __all_sync(0xffffffffu, tile_wait(sh, a, bar, parity));
+}
+
+// ------------------------------------------------------------------ loader --
+
+template <int D, int FMT>
+__device__ __forceinline__ void tile_loader(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int lane) {
+  using C = TileCfg<D, FMT>;
+  constexpr int CB = D / 64;
+  long c = 0;  // blocks so far
+  bool ok = true;
+  int land = 0;
+  for (int k = 0; ok; ++k) {
+    const int slot = k % C::PIECES;
+    if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) break;
+    const Piece p = sh->piece[slot];
+    if (p.nblk == 0) break;
+    for (int j = 0; j < p.nblk; ++j, ++c) {
+      const int st = (int)(c % C::NS), par = (int)((c / C::NS) & 1);
+      const int tok0 = (p.blk + j) * C::BK;
+      const int nt = max(min((p.s.len - tok0 + 15) >> 4, 8), 0);  // records with a token of the sequence
+      // lane -> (record, block of 64 columns); head_dim 64 uses 8 lanes, 128 16, 256 all
+      const int rec = lane / CB, cb = lane % CB;
+      const char* src = nullptr;
+      if (rec < nt) {
+        const int tok = tok0 + 16 * rec;
+        src = tile_addr(a, page_index(a, p.b, tok), p.head, tok) + cb * 2048;
+      }
+      const uint32_t dst = cb * (C::BK * 128) + rec * 2048;
+      ok = tile_wait_warp(sh, a, &sh->k_empty[st], par ^ 1);
+      if (!ok) break;
+      const uint32_t kb = smem_u32(&sh->k_full[st]);
+      if (lane == 0) mbar_expect(kb, nt * CB * 2048);
+      __syncwarp();
+      if (src) bulk_load(smem + C::K_OFF + st * C::TILE + dst, src, 2048, kb);
+      ok = tile_wait_warp(sh, a, &sh->v_empty[st], par ^ 1);
+      if (!ok) break;
+      const uint32_t vt = smem + C::V_OFF + st * C::TILE, vb = smem_u32(&sh->v_full[st]);
+      if (tok0 + C::BK <= p.s.len) {
+        if (lane == 0) mbar_expect(vb, nt * CB * 2048);
+        __syncwarp();
+        if (src) bulk_load(vt + dst, src + a.pv.L.v_off, 2048, vb);
+      } else {
+        // the sequence ends in this block: the rows behind it are cleared (their weights are zero, their contents anything)
+        const uint32_t lb = smem_u32(&sh->v_land);
+        if (lane == 0) mbar_expect(lb, nt * CB * 2048);
+        __syncwarp();
+        if (src) bulk_load(vt + dst, src + a.pv.L.v_off, 2048, lb);
+        ok = tile_wait_warp(sh, a, &sh->v_land, land & 1);
+        ++land;
+        if (!ok) break;
+        const int n = max(p.s.len - tok0, 0);
+        for (int i = lane; i < (C::BK - n) * (D / 8); i += 32) {
+          const int r = n + i / (D / 8), ch = i % (D / 8);
+          asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(vt + (ch >> 3) * (C::BK * 128) + r * 128 + ((ch & 7) << 4)),
+                       "r"(0)
+                       : "memory");
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(vb);
+      }
+    }
+    if (lane == 0) mbar_arrive(smem_u32(&sh->piece_free[slot]));
+  }
+}
+
+// ------------------------------------------------------------- dequantizer --
+
+// A thread turns runs of 32 channels of one token into four 16-byte chunks; 512
+// runs (four a thread) are a unit, fetched one unit ahead.
+template <int BITS>
+struct RawUnit {
+  uint4 w[4][BITS / 4];  // 16 bytes of 4-bit codes, 32 bytes of 8-bit codes
+  uint32_t zs[4];
+};
+
+template <int D, int BITS>
+__device__ __forceinline__ void fetch_unit(const AttnArgs& a, const Piece& p, int tok0, int off, int meta_off, int lg,
+                                           int unit, int tid, RawUnit<BITS>* r) {
+  constexpr int PPT = D / 32;  // runs of a token
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int run = unit * 512 + i * 128 + tid, t = run / PPT, piece = run % PPT;
+    const int tok = tok0 + t;
+    if (t < 128 && tok < p.s.len) {
+      const char* rec = tile_addr(a, page_index(a, p.b, tok), p.head, tok);
+      const char* src = rec + off + (tok & 15) * (D * BITS / 8) + piece * (4 * BITS);
+#pragma unroll
+      for (int k = 0; k < BITS / 4; ++k) r->w[i][k] = reinterpret_cast<const uint4*>(src)[k];
+      r->zs[i] = reinterpret_cast<const uint32_t*>(rec + meta_off)[(tok & 15) * (D >> lg) + ((piece * 32) >> lg)];
+    } else {
+#pragma unroll
+      for (int k = 0; k < BITS / 4; ++k) r->w[i][k] = make_uint4(0, 0, 0, 0);
+      r->zs[i] = 0;  // zero + code * step = 0: behind the sequence's end
+    }
+  }
+}
+
+template <int D, int BITS>
+__device__ __forceinline__ void store_unit(uint32_t tile, int unit, int tid, const RawUnit<BITS>& r) {
+  constexpr int PPT = D / 32;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int run = unit * 512 + i * 128 + tid, t = run / PPT, piece = run % PPT;
+    if (t >= 128) continue;
+    const __half2 z = __low2half2(as_h2(r.zs[i])), s = __high2half2(as_h2(r.zs[i]));
+    const uint32_t row = tile + (piece >> 1) * (128 * 128) + t * 128;
+    uint32_t y[16];
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(r.w[i]);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (BITS == 8) y[k] = dequant2(__byte_perm(w[k / 2], 0, (k & 1) ? 0x4342 : 0x4140), s, z);
+      else y[k] = dequant2((w[k / 4] >> (4 * (k & 3))) & 0x000f000fu, s, z);
+    }
+    // the order of the four stores keeps lanes of other column blocks off the same banks
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = (4 * (piece & 1) + k) ^ (t & 7);
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(row + (c << 4)), "r"(y[4 * k]), "r"(y[4 * k + 1]),
+                   "r"(y[4 * k + 2]), "r"(y[4 * k + 3])
+                   : "memory");
+    }
+  }
+}
+
+template <int D, int FMT>
+__device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int tid) {
+  using C = TileCfg<D, FMT>;
+  using F = typename C::F;
+  constexpr int UNITS = D == 256 ? 2 : 1;  // of a K or V tile
+  constexpr int KB = F::KB == 16 ? 4 : F::KB, VB = F::VB == 16 ? 4 : F::VB;
+  const int lane = tid & 31;
+  long c = 0;
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    const int slot = k % C::PIECES;
+    if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) break;
+    const Piece p = sh->piece[slot];
+    if (p.nblk == 0) break;
+    const PagesLayout& L = a.pv.L;
+    RawUnit<KB> kr;
+    RawUnit<VB> vr;
+    fetch_unit<D, KB>(a, p, p.blk * C::BK, 0, L.km_off, L.k_lg, 0, tid, &kr);
+    for (int j = 0; j < p.nblk; ++j, ++c) {
+      const int st = (int)(c % C::NS), par = (int)((c / C::NS) & 1);
+      const int tok0 = (p.blk + j) * C::BK;
+      fetch_unit<D, VB>(a, p, tok0, L.v_off, L.vm_off, L.v_lg, 0, tid, &vr);
+      ok = tile_wait_warp(sh, a, &sh->k_empty[st], par ^ 1);
+      if (!ok) break;
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        store_unit<D, KB>(smem + C::K_OFF + st * C::TILE, u, tid, kr);
+        if (u + 1 < UNITS) fetch_unit<D, KB>(a, p, tok0, 0, L.km_off, L.k_lg, u + 1, tid, &kr);
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh->k_full[st]));
+      if (j + 1 < p.nblk) fetch_unit<D, KB>(a, p, tok0 + C::BK, 0, L.km_off, L.k_lg, 0, tid, &kr);
+      ok = tile_wait_warp(sh, a, &sh->v_empty[st], par ^ 1);
+      if (!ok) break;
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        store_unit<D, VB>(smem + C::V_OFF + st * C::TILE, u, tid, vr);
+        if (u + 1 < UNITS) fetch_unit<D, VB>(a, p, tok0, L.v_off, L.vm_off, L.v_lg, u + 1, tid, &vr);
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh->v_full[st]));
+    }
+    if (lane == 0) mbar_arrive(smem_u32(&sh->piece_free[slot]));
+  }
+}
+
+// -------------------------------------------------------------- matrix unit --
+
+template <int D, int FMT>
+__device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem) {
+  using C = TileCfg<D, FMT>;
+  constexpr uint32_t S_DESC = mma_desc(128, C::BK, C::F::kBf16, false);
+  constexpr uint32_t O_DESC = mma_desc(128, D, C::F::kBf16, true);
+  const uint32_t tm = sh->tmem;
+  long kc = 0, vc = 0, bc = 0;  // K blocks, V blocks read; score buffers handed out (one tile)
+  int pc[2] = {0, 0};
+  auto scores = [&](int buf, int tile, int st) {
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      const uint32_t at = (ks >> 2) * (128 * 128) + (ks & 3) * 32;
+      mma_ss(tm + buf * 128, smem_desc(smem + C::Q_OFF + tile * C::TILE + at, 16, 1024),
+             smem_desc(smem + C::K_OFF + st * C::TILE + at, 16, 1024), S_DESC, ks > 0);
+    }
+    mma_commit(smem_u32(&sh->s_full[buf]));
+  };
+  auto values = [&](int buf, int tile, int st, bool add) {
+#pragma unroll
+    for (int ks = 0; ks < C::BK / 16; ++ks)
+      mma_ts(tm + 256 + tile * D, tm + buf * 128 + ks * 8, smem_desc(smem + C::V_OFF + st * C::TILE + ks * 2048, C::BK * 128, 1024),
+             O_DESC, add || ks > 0);
+    mma_commit(smem_u32(&sh->o_done[tile]));
+  };
+  for (int k = 0;; ++k) {
+    const int slot = k % C::PIECES;
+    if (!tile_wait(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) return;
+    const int n = sh->piece[slot].nblk, tiles = (sh->piece[slot].rows + 127) / 128;
+    if (n == 0) return;
+    if (!tile_wait(sh, a, &sh->q_full, k & 1)) return;
+    auto next_k = [&](int* st) {
+      *st = (int)(kc % C::NS);
+      const bool ok = tile_wait(sh, a, &sh->k_full[*st], (int)((kc / C::NS) & 1));
+      ++kc;
+      return ok;
+    };
+    int ks, vs;
+    if (!next_k(&ks)) return;
+    tc_after_sync();
+    if (C::NT == 2) {
+      for (int i = 0; i < tiles; ++i) scores(i, i, ks);
+    } else {
+      scores((int)(bc & 1), 0, ks);
+    }
+    mma_commit(smem_u32(&sh->k_empty[ks]));
+    if (n == 1) mma_commit(smem_u32(&sh->q_free));
+    for (int j = 0; j < n; ++j) {
+      vs = (int)(vc % C::NS);
+      if (C::NT == 2) {
+        for (int i = 0; i < tiles; ++i) {
+          if (i == 0 && !tile_wait(sh, a, &sh->v_full[vs], (int)((vc / C::NS) & 1))) return;
+          if (!tile_wait(sh, a, &sh->p_full[i], pc[i]++ & 1)) return;
+          tc_after_sync();
+          values(i, i, vs, j > 0);
+          if (i == tiles - 1) mma_commit(smem_u32(&sh->v_empty[vs]));
+          if (j + 1 < n) {
+            if (i == 0) {
+              if (!next_k(&ks)) return;
+              tc_after_sync();
+            }
+            scores(i, i, ks);
+            if (i == tiles - 1) {
+              mma_commit(smem_u32(&sh->k_empty[ks]));
+              if (j + 2 == n) mma_commit(smem_u32(&sh->q_free));
+            }
+          }
+        }
+      } else {
+        const int buf = (int)(bc & 1);
+        if (j + 1 < n) {
+          if (!next_k(&ks)) return;
+          tc_after_sync();
+          scores(buf ^ 1, 0, ks);
+          mma_commit(smem_u32(&sh->k_empty[ks]));
+          if (j + 2 == n) mma_commit(smem_u32(&sh->q_free));
+        }
+        if (!tile_wait(sh, a, &sh->v_full[vs], (int)((vc / C::NS) & 1))) return;
+        if (!tile_wait(sh, a, &sh->p_full[buf], pc[buf]++ & 1)) return;
+        tc_after_sync();
+        values(buf, 0, vs, j > 0);
+        mma_commit(smem_u32(&sh->v_empty[vs]));
+        ++bc;
+      }
+      ++vc;
+    }
+    mbar_arrive(smem_u32(&sh->piece_free[slot]));
+  }
+}
+
+// ------------------------------------------------------------------ softmax --
+
+// One row of queries into the swizzled operand tile (zeros behind the item's
+// rows); returns what its scores are to be multiplied by.
+template <int D, int FMT>
+__device__ __forceinline__ float tile_query(const AttnArgs& a, const Piece& p, int r, uint32_t tile, int row) {
+  using F = Fmt<FMT>;
+  float sc = a.scale_log2;
+  const bool has = r < p.rows;
+  const int R = p.r0 + (has ? r : 0);
+  const uint16_t* src = static_cast<const uint16_t*>(a.q) + (long)(p.s.s0 + R / a.rep) * a.q_stride +
+                        (long)(p.head * a.rep + R % a.rep) * D;
+  auto chunk = [&](int c) -> uint4 {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (!has) return w;
+    if (a.q_aligned) return *reinterpret_cast<const uint4*>(src + c * 8);
+    uint16_t* e = reinterpret_cast<uint16_t*>(&w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = src[c * 8 + i];
+    return w;
+  };
+  float f0 = 1.0f, f1 = 1.0f;
+  const bool convert = F::kQuant && a.q_bf16;
+  if (convert) {
+    float mx = 0.0f;
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 w = chunk(c);
+      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xffff0000u))));
+    }
+    const int E = norm_exp(mx);
+    f0 = exp2i(E / 2), f1 = exp2i(E - E / 2);
+    sc = a.scale_log2 * exp2i(-(E / 2)) * exp2i(-(E - E / 2));
+  }
+#pragma unroll 4
+  for (int c = 0; c < D / 8; ++c) {
+    uint4 w = chunk(c);
+    if (convert) {
+      uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[i] = pack2<false>(__uint_as_float(x[i] << 16) * f0 * f1, __uint_as_float(x[i] & 0xffff0000u) * f0 * f1);
+      w = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(tile + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)),
+                 "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+                 : "memory");
+  }
+  return sc;
+}
+
+template <int D, int FMT>
+__device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int tile, int tid) {
+  using C = TileCfg<D, FMT>;
+  using F = typename C::F;
+  constexpr int BK = C::BK;
+  const int lane = tid & 31, row = tid & 127;
+  const uint32_t lanes = (uint32_t)((row >> 5) * 32) << 16;
+  const uint32_t tm = sh->tmem + lanes, o_col = 256 + tile * D;
+  int bc = 0, ob = 0;  // blocks read (of this tile), value products
+  for (int k = 0;; ++k) {
+    const int slot = k % C::PIECES;
+    if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) return;
+    const Piece p = sh->piece[slot];
+    if (p.nblk == 0) return;
+    if (k > 0 && !tile_wait_warp(sh, a, &sh->q_free, (k - 1) & 1)) return;
+    const int r = tile * 128 + row;
+    const float sc = tile_query<D, FMT>(a, p, r, smem + C::Q_OFF + tile * C::TILE, row);
+    fence_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh->q_full));
+    if (tile * 128 < p.rows) {
+      const int rr = p.r0 + min(r, p.rows - 1);
+      const int pos = p.s.p0 + rr / a.rep;
+      // the tile's first and last position: blocks between need no mask
+      const int pos_lo = p.s.p0 + (p.r0 + tile * 128) / a.rep;
+      const int pos_hi = p.s.p0 + (p.r0 + min(tile * 128 + 127, p.rows - 1)) / a.rep;
+      float m = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+      for (int j = 0; j < p.nblk; ++j, ++bc, ++ob) {
+        const int buf = C::NT == 2 ? tile : (bc & 1);
+        if (!tile_wait_warp(sh, a, &sh->s_full[buf], C::NT == 2 ? bc & 1 : (bc >> 1) & 1)) return;
+        tc_after_sync();
+        uint32_t s[BK];
+#pragma unroll
+        for (int c = 0; c < BK; c += 32) tmem_ld32(tm + buf * 128 + c, s + c);
+        tmem_wait_ld();
+        const int tok0 = (p.blk + j) * BK;
+        if (tok0 + BK - 1 > pos_lo || (a.window > 0 && tok0 <= pos_hi - a.window)) {
+          const int hi = pos - tok0, lo = a.window > 0 ? pos - a.window - tok0 : -1;  // columns lo < c <= hi
+#pragma unroll
+          for (int c = 0; c < BK; ++c)
+            if (c > hi || c <= lo) s[c] = 0xff800000u;
+        }
+        float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < BK; c += 4) {
+          x0 = fmaxf(x0, __uint_as_float(s[c]));
+          x1 = fmaxf(x1, __uint_as_float(s[c + 1]));
+          x2 = fmaxf(x2, __uint_as_float(s[c + 2]));
+          x3 = fmaxf(x3, __uint_as_float(s[c + 3]));
+        }
+        const float top = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * sc;
+        const bool grow = top > m + 8.0f;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float to = grow ? top : m;
+          if (j > 0) {
+            const float f = to == -INFINITY ? 1.0f : fast_exp2(m - to);
+            if (!tile_wait_warp(sh, a, &sh->o_done[tile], (ob - 1) & 1)) return;
+            tc_after_sync();
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(tm + o_col + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(tm + o_col + c, o);
+            }
+            l0 *= f;
+            l1 *= f;
+          }
+          m = to;
+        }
+        const float base = m == -INFINITY ? 0.0f : m - 7.0f;
+        uint32_t w[32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float x = fast_exp2(fmaf(__uint_as_float(s[h * 64 + 2 * c]), sc, -base));
+            const float y = fast_exp2(fmaf(__uint_as_float(s[h * 64 + 2 * c + 1]), sc, -base));
+            l0 += x;
+            l1 += y;
+            w[c] = pack2<F::kBf16>(x, y);
+          }
+          tmem_st32(tm + buf * 128 + h * 32, w);
+        }
+        tmem_wait_st();
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[buf]));
+      }
+      // ---- the item's output, or this CTA's part of it
+      // (with one tile the last scores do not wait for the product before them,
+      // so that one is waited for too: a barrier's parity tells two phases apart)
+      if (C::NT == 1 && p.nblk > 1 && !tile_wait_warp(sh, a, &sh->o_done[tile], (ob - 2) & 1)) return;
+      if (!tile_wait_warp(sh, a, &sh->o_done[tile], (ob - 1) & 1)) return;
+      tc_after_sync();
+      const float l = l0 + l1;
+      const bool whole = p.has_first && p.has_last, has = r < p.rows;
+      const float f = whole ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+      const long slot_row = ((long)blockIdx.x * 2 + (p.has_first ? 1 : 0)) * C::ROWS + r;
+      const long at = ((long)(p.s.s0 + rr / a.rep) * a.q_heads + p.head * a.rep + rr % a.rep) * D;
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(tm + o_col + c, o);
+        tmem_wait_ld();
+        if (!has) continue;
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint4 w;
+            uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float u = __uint_as_float(o[e + 2 * i]) * f, v = __uint_as_float(o[e + 2 * i + 1]) * f;
+              x[i] = a.q_bf16 ? pack2<true>(u, v) : pack2<false>(u, v);
+            }
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at + c + e) = w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(a.part_o + slot_row * D + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      if (!whole && has) *reinterpret_cast<float2*>(a.part_ml + slot_row * 2) = make_float2(m, l);
+      tc_before_sync();
+    }
+    if (tile == 0 && row == 0 && p.has_first && !p.has_last) {
+      SplitHead h = {};
+      h.parts = cta_of(&sh->work, p.item1 - 1) - (int)blockIdx.x + 1;
+      h.rows = p.rows, h.row0 = p.r0, h.q_row = p.s.s0, h.head = p.head;
+      a.split[blockIdx.x] = h;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh->piece_free[slot]));
+  }
+}
+
+// ------------------------------------------------------------------- kernel --
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel(const __grid_constant__ AttnArgs a) {
+  using C = TileCfg<D, FMT>;
+  using F = typename C::F;
+  extern __shared__ char raw[];
+  __shared__ TileShared<D, FMT> sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t smem = (smem_u32(raw) + 1023) & ~1023u;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(smem_u32(&sh.k_full[i]), C::PROD);
+      mbar_init(smem_u32(&sh.v_full[i]), C::PROD);
+      mbar_init(smem_u32(&sh.k_empty[i]), 1);
+      mbar_init(smem_u32(&sh.v_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh.s_full[i]), 1);
+      mbar_init(smem_u32(&sh.p_full[i]), 4);
+      mbar_init(smem_u32(&sh.o_done[i]), 1);
+    }
+    mbar_init(smem_u32(&sh.q_full), 4 * C::NT);
+    mbar_init(smem_u32(&sh.q_free), 1);
+    mbar_init(smem_u32(&sh.v_land), 1);
+    for (int i = 0; i < C::PIECES; ++i) {
+      mbar_init(smem_u32(&sh.piece_full[i]), 1);
+      mbar_init(smem_u32(&sh.piece_free[i]), 4 * C::NT + 1 + C::PROD);
+    }
+    sh.dead = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  plan_work(a, &sh.work);  // (its barriers also publish the initialisation above)
+  pdl_trigger();
+  if (threadIdx.x == 0) a.split[blockIdx.x].parts = 0;
+  if ((int)blockIdx.x >= sh.work.ctas) return;
+  if (warp == 8) tmem_alloc(smem_u32(&sh.tmem), 512);
+  tc_before_sync();
+  __syncthreads();
+  tc_after_sync();
+
+  // registers: 512 threads start with 128 each (65536); 256 * 176 + 128 * 48 + 128 * 112 = 65536
+  if (warp < 8) {
+    if constexpr (F::kQuant) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
+    if (warp < 4 * C::NT) tile_softmax<D, FMT>(a, &sh, smem, warp >> 2, threadIdx.x);
+  } else if (warp < 12) {
+    if constexpr (F::kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;\n");
+    if (warp == 8) {
+      if (lane == 0) tile_mma<D, FMT>(a, &sh, smem);
+    } else if (warp == 9) {
+      if constexpr (!F::kQuant) tile_loader<D, FMT>(a, &sh, smem, lane);
+    } else if (warp == 10) {
+      // the pieces of this CTA's units, one ahead of the others; nblk 0 ends
+      long u = cta_begin(&sh.work, blockIdx.x);
+      const long end = cta_begin(&sh.work, blockIdx.x + 1);
+      for (int k = 0;; ++k) {
+        const int slot = k % C::PIECES;
+        if (k >= C::PIECES && !tile_wait_warp(&sh, a, &sh.piece_free[slot], (k / C::PIECES - 1) & 1)) break;
+        Piece p = {};
+        if (u < end) p = find_piece(a, &sh.work, u, end);
+        u += p.nblk;
+        if (lane == 0) {
+          sh.piece[slot] = p;
+          mbar_arrive(smem_u32(&sh.piece_full[slot]));
+        }
+        __syncwarp();
+        if (p.nblk == 0) break;
+      }
+    }
+  } else {
+    if constexpr (F::kQuant) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 112;\n");
+      tile_dequantizer<D, FMT>(a, &sh, smem, threadIdx.x - 384);
+    }
+  }
+  __syncwarp();
+  if (*(volatile int*)&sh.dead) {  // given up: what is in flight lands before memory is given back
+    const unsigned long long t0 = time_ns();
+    while (time_ns() - t0 < 5000000ull) __nanosleep(1000);
+  }
+  tc_before_sync();
+  __syncthreads();
+  tc_after_sync();
+  if (warp == 8) tmem_free(sh.tmem, 512);
+}
+
+template <int D>
+AttnKernel tile_kernel_dim(int fmt) {
+  switch (fmt) {
+#define KVQ_TILE(f) \
+  case f: return {(const void*)pages_tile_kernel<D, f>, (size_t)TileCfg<D, f>::SMEM, TileCfg<D, f>::THREADS, 1};
+    KVQ_TILE(kFmtF16)
+    KVQ_TILE(kFmtBf16)
+    KVQ_TILE(kFmt88)
+    KVQ_TILE(kFmt44)
+    KVQ_TILE(kFmt84)
+    KVQ_TILE(kFmt48)
+#undef KVQ_TILE
+  }
+  return {};
+}
+
+}  // namespace kvq

@@ -105,10 +105,16 @@ __device__ __forceinline__ void ldsv(uint32_t a, uint32_t* x) {
                    : "memory");
   }
 }
-// two codes in the low bits of both halves -> zero + code * step
-__device__ __forceinline__ uint32_t dequant2(uint32_t codes, __half2 s, __half2 z) {
-  const __half2 c = __hsub2(as_h2(codes | 0x64006400u), as_h2(0x64006400u));
-  return as_u32(__hfma2(c, s, z));
+// Two codes as the halves 1024 + code -> zero + code * step.
+__device__ __forceinline__ uint32_t dequant2(uint32_t biased, __half2 s, __half2 z) {
+  return as_u32(__hfma2(__hsub2(as_h2(biased), as_h2(0x64006400u)), s, z));
+}
+// The halves 1024 + code of two 4-bit codes (low bits of both halves of x), and
+// of the low / high two of four 8-bit codes.
+__device__ __forceinline__ uint32_t biased4(uint32_t x) { return (x & 0x000f000fu) | 0x64006400u; }
+template <int HIGH>
+__device__ __forceinline__ uint32_t biased8(uint32_t x) {
+  return __byte_perm(x, 0x64646464u, HIGH ? 0x4342 : 0x4140);
 }
 
 // One 16-token record's scores: acc[m][n8 tile] += Q K^T.
@@ -150,12 +156,12 @@ __device__ __forceinline__ void rows_scores(uint32_t st, const PagesLayout& L, c
         for (int i = 0; i < RUN / 4; ++i) {  // one mma step: 4 channels
           uint32_t b0, b1;
           if (F::KB == 8) {
-            b0 = dequant2(__byte_perm(w[i], 0, 0x4140), s, z);
-            b1 = dequant2(__byte_perm(w[i], 0, 0x4342), s, z);
+            b0 = dequant2(biased8<0>(w[i]), s, z);
+            b1 = dequant2(biased8<1>(w[i]), s, z);
           } else {
             const uint32_t x = w[i / 2] >> (8 * (i & 1));
-            b0 = dequant2(x & 0x000f000fu, s, z);
-            b1 = dequant2((x >> 4) & 0x000f000fu, s, z);
+            b0 = dequant2(biased4(x), s, z);
+            b1 = dequant2(biased4(x >> 4), s, z);
           }
 #pragma unroll
           for (int m = 0; m < MT; ++m) mma16<false>(acc[m][h], q[m][r * (RUN / 4) + i], b0, b1);
@@ -213,9 +219,8 @@ __device__ __forceinline__ void rows_values(uint32_t st, const PagesLayout& L, c
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const uint32_t sel = (c & 1) ? 0x4342 : 0x4140;
-          const uint32_t b0 = dequant2(__byte_perm(x[0][c >> 1], 0, sel), s[0], z[0]);
-          const uint32_t b1 = dequant2(__byte_perm(x[1][c >> 1], 0, sel), s[1], z[1]);
+          const uint32_t b0 = dequant2((c & 1) ? biased8<1>(x[0][c >> 1]) : biased8<0>(x[0][c >> 1]), s[0], z[0]);
+          const uint32_t b1 = dequant2((c & 1) ? biased8<1>(x[1][c >> 1]) : biased8<0>(x[1][c >> 1]), s[1], z[1]);
 #pragma unroll
           for (int m = 0; m < MT; ++m) mma16<false>(o[m][4 * i + c], p[m], b0, b1);
         }
@@ -231,8 +236,8 @@ __device__ __forceinline__ void rows_values(uint32_t st, const PagesLayout& L, c
         }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const uint32_t b0 = dequant2((x[0][c & 1] >> (4 * (c >> 1))) & 0x000f000fu, s[0], z[0]);
-          const uint32_t b1 = dequant2((x[1][c & 1] >> (4 * (c >> 1))) & 0x000f000fu, s[1], z[1]);
+          const uint32_t b0 = dequant2(biased4(x[0][c & 1] >> (4 * (c >> 1))), s[0], z[0]);
+          const uint32_t b1 = dequant2(biased4(x[1][c & 1] >> (4 * (c >> 1))), s[1], z[1]);
 #pragma unroll
           for (int m = 0; m < MT; ++m) mma16<false>(o[m][8 * i + c], p[m], b0, b1);
         }

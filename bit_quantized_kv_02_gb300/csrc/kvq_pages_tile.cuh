@@ -11,7 +11,7 @@
 //    shuffling is needed;
 //  - dequantizers (codes): a warpgroup turns codes into fp16 operand tiles
 //    (the value the page stands for, one rounding);
-//  - one thread issues the matrix instructions: S = Q K^T (both from shared
+//  - one warp issues the matrix instructions: S = Q K^T (both from shared
 //    memory), O += P V (P from tensor memory, over the scores it came from);
 //  - softmax: a warpgroup per tile, a thread per row, so maxima and sums need
 //    no exchange; scores are read from tensor memory once, weights are written
@@ -40,7 +40,7 @@ struct TileCfg {
   static constexpr int TILE = 128 * D * 2;         // bytes of a Q, K or V tile
   static constexpr int Q_OFF = 0, K_OFF = NT * TILE, V_OFF = K_OFF + NS * TILE;
   static constexpr int SMEM = V_OFF + NS * TILE + 1024;  // + alignment of the tiles
-  static constexpr int PROD = F::kQuant ? 4 : 1;   // warps that fill K and V stages
+  static constexpr int PROD = F::kQuant ? (NT == 1 ? 8 : 4) : 1;  // warps that fill K and V stages
   static constexpr int THREADS = F::kQuant ? 512 : 384;
   static constexpr int PIECES = 4;
 };
@@ -75,6 +75,23 @@ __device__ __forceinline__ bool tile_wait(SH* sh, const AttnArgs& a, uint64_t* b
 template <typename SH>
 __device__ __forceinline__ bool tile_wait_warp(SH* sh, const AttnArgs& a, uint64_t* bar, int parity) {
   return __all_sync(0xffffffffu, tile_wait(sh, a, bar, parity));
+}
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
+      "fma.rn.f32x2 d, a, b, c;\nmov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nadd.rn.f32x2 d, a, b;\nmov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 // ------------------------------------------------------------------ loader --
@@ -143,24 +160,24 @@ __device__ __forceinline__ void tile_loader(const AttnArgs& a, TileShared<D, FMT
 
 // ------------------------------------------------------------- dequantizer --
 
-// A thread turns runs of 32 channels of one token into four 16-byte chunks; 512
-// runs (four a thread) are a unit, fetched one unit ahead.
-template <int BITS>
-struct RawUnit {
-  uint4 w[4][BITS / 4];  // 16 bytes of 4-bit codes, 32 bytes of 8-bit codes
-  uint32_t zs[4];
+// A thread turns RUNS runs of 32 channels of one token into four 16-byte chunks
+// each.  Codes and metadata are fetched a block ahead, page indices too.
+template <int BITS, int RUNS>
+struct RawTile {
+  uint4 w[RUNS][BITS / 4];  // 16 bytes of 4-bit codes, 32 bytes of 8-bit codes
+  uint32_t zs[RUNS];
 };
 
-template <int D, int BITS>
-__device__ __forceinline__ void fetch_unit(const AttnArgs& a, const Piece& p, int tok0, int off, int meta_off, int lg,
-                                           int unit, int tid, RawUnit<BITS>* r) {
+template <int D, int BITS, int RUNS, int THREADS>
+__device__ __forceinline__ void fetch_raw(const AttnArgs& a, const Piece& p, int tok0, int off, int meta_off, int lg,
+                                          int tid, const int* page, RawTile<BITS, RUNS>* r) {
   constexpr int PPT = D / 32;  // runs of a token
+  const int piece = tid % PPT;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int run = unit * 512 + i * 128 + tid, t = run / PPT, piece = run % PPT;
-    const int tok = tok0 + t;
-    if (t < 128 && tok < p.s.len) {
-      const char* rec = tile_addr(a, page_index(a, p.b, tok), p.head, tok);
+  for (int i = 0; i < RUNS; ++i) {
+    const int tok = tok0 + (i * THREADS + tid) / PPT;
+    if (tok < p.s.len) {
+      const char* rec = tile_addr(a, page[i], p.head, tok);
       const char* src = rec + off + (tok & 15) * (D * BITS / 8) + piece * (4 * BITS);
 #pragma unroll
       for (int k = 0; k < BITS / 4; ++k) r->w[i][k] = reinterpret_cast<const uint4*>(src)[k];
@@ -173,26 +190,42 @@ __device__ __forceinline__ void fetch_unit(const AttnArgs& a, const Piece& p, in
   }
 }
 
-template <int D, int BITS>
-__device__ __forceinline__ void store_unit(uint32_t tile, int unit, int tid, const RawUnit<BITS>& r) {
+template <int D, int BITS, int RUNS, int THREADS>
+__device__ __forceinline__ void store_raw(uint32_t tile, int tid, const RawTile<BITS, RUNS>& r) {
   constexpr int PPT = D / 32;
+  const int piece = tid % PPT;
+  // lanes of other column blocks store their four chunks in another order, so
+  // that the 8 lanes of a phase touch 8 different groups of banks
+  const int turn = D == 64 ? 0 : (D == 128 ? 2 * (piece >> 1) : piece >> 1);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int run = unit * 512 + i * 128 + tid, t = run / PPT, piece = run % PPT;
-    if (t >= 128) continue;
+  for (int i = 0; i < RUNS; ++i) {
+    const int t = (i * THREADS + tid) / PPT;
     const __half2 z = __low2half2(as_h2(r.zs[i])), s = __high2half2(as_h2(r.zs[i]));
     const uint32_t row = tile + (piece >> 1) * (128 * 128) + t * 128;
+    constexpr int WC = BITS / 4;  // words of a chunk
+    uint32_t w[4 * WC];
+#pragma unroll
+    for (int k = 0; k < 4 * WC; ++k) w[k] = reinterpret_cast<const uint32_t*>(r.w[i])[k];
+#pragma unroll
+    for (int b = 1; b < 4; b <<= 1)  // the words of chunk k to place k ^ turn
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (!(k & b))
+#pragma unroll
+          for (int e = 0; e < WC; ++e) {
+            const uint32_t x = w[WC * k + e], y = w[WC * (k ^ b) + e];
+            w[WC * k + e] = (turn & b) ? y : x;
+            w[WC * (k ^ b) + e] = (turn & b) ? x : y;
+          }
     uint32_t y[16];
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(r.w[i]);
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      if (BITS == 8) y[k] = dequant2(__byte_perm(w[k / 2], 0, (k & 1) ? 0x4342 : 0x4140), s, z);
-      else y[k] = dequant2((w[k / 4] >> (4 * (k & 3))) & 0x000f000fu, s, z);
+      if (BITS == 8) y[k] = dequant2((k & 1) ? biased8<1>(w[k / 2]) : biased8<0>(w[k / 2]), s, z);
+      else y[k] = dequant2(biased4(w[k / 4] >> (4 * (k & 3))), s, z);
     }
-    // the order of the four stores keeps lanes of other column blocks off the same banks
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int c = (4 * (piece & 1) + k) ^ (t & 7);
+      const int c = (4 * (piece & 1) + (k ^ turn)) ^ (t & 7);
       asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(row + (c << 4)), "r"(y[4 * k]), "r"(y[4 * k + 1]),
                    "r"(y[4 * k + 2]), "r"(y[4 * k + 3])
                    : "memory");
@@ -204,7 +237,7 @@ template <int D, int FMT>
 __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int tid) {
   using C = TileCfg<D, FMT>;
   using F = typename C::F;
-  constexpr int UNITS = D == 256 ? 2 : 1;  // of a K or V tile
+  constexpr int THREADS = 32 * C::PROD, RUNS = 128 * (D / 32) / THREADS, PPT = D / 32;
   constexpr int KB = F::KB == 16 ? 4 : F::KB, VB = F::VB == 16 ? 4 : F::VB;
   const int lane = tid & 31;
   long c = 0;
@@ -215,34 +248,41 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
     const Piece p = sh->piece[slot];
     if (p.nblk == 0) break;
     const PagesLayout& L = a.pv.L;
-    RawUnit<KB> kr;
-    RawUnit<VB> vr;
-    fetch_unit<D, KB>(a, p, p.blk * C::BK, 0, L.km_off, L.k_lg, 0, tid, &kr);
+    RawTile<KB, RUNS> kr;
+    RawTile<VB, RUNS> vr;
+    int page[RUNS];
+    auto find_pages = [&](int tok0) {
+#pragma unroll
+      for (int i = 0; i < RUNS; ++i) {
+        const int tok = tok0 + (i * THREADS + tid) / PPT;
+        page[i] = tok < p.s.len ? page_index(a, p.b, tok) : 0;
+      }
+    };
+    int tok0 = p.blk * C::BK;
+    find_pages(tok0);
+    fetch_raw<D, KB, RUNS, THREADS>(a, p, tok0, 0, L.km_off, L.k_lg, tid, page, &kr);
+    fetch_raw<D, VB, RUNS, THREADS>(a, p, tok0, L.v_off, L.vm_off, L.v_lg, tid, page, &vr);
+    find_pages(tok0 + C::BK);
     for (int j = 0; j < p.nblk; ++j, ++c) {
       const int st = (int)(c % C::NS), par = (int)((c / C::NS) & 1);
-      const int tok0 = (p.blk + j) * C::BK;
-      fetch_unit<D, VB>(a, p, tok0, L.v_off, L.vm_off, L.v_lg, 0, tid, &vr);
       ok = tile_wait_warp(sh, a, &sh->k_empty[st], par ^ 1);
       if (!ok) break;
-#pragma unroll
-      for (int u = 0; u < UNITS; ++u) {
-        store_unit<D, KB>(smem + C::K_OFF + st * C::TILE, u, tid, kr);
-        if (u + 1 < UNITS) fetch_unit<D, KB>(a, p, tok0, 0, L.km_off, L.k_lg, u + 1, tid, &kr);
-      }
+      store_raw<D, KB, RUNS, THREADS>(smem + C::K_OFF + st * C::TILE, tid, kr);
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh->k_full[st]));
-      if (j + 1 < p.nblk) fetch_unit<D, KB>(a, p, tok0 + C::BK, 0, L.km_off, L.k_lg, 0, tid, &kr);
+      tok0 += C::BK;
+      if (j + 1 < p.nblk) fetch_raw<D, KB, RUNS, THREADS>(a, p, tok0, 0, L.km_off, L.k_lg, tid, page, &kr);
       ok = tile_wait_warp(sh, a, &sh->v_empty[st], par ^ 1);
       if (!ok) break;
-#pragma unroll
-      for (int u = 0; u < UNITS; ++u) {
-        store_unit<D, VB>(smem + C::V_OFF + st * C::TILE, u, tid, vr);
-        if (u + 1 < UNITS) fetch_unit<D, VB>(a, p, tok0, L.v_off, L.vm_off, L.v_lg, u + 1, tid, &vr);
-      }
+      store_raw<D, VB, RUNS, THREADS>(smem + C::V_OFF + st * C::TILE, tid, vr);
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh->v_full[st]));
+      if (j + 1 < p.nblk) {
+        fetch_raw<D, VB, RUNS, THREADS>(a, p, tok0, L.v_off, L.vm_off, L.v_lg, tid, page, &vr);
+        find_pages(tok0 + C::BK);
+      }
     }
     if (lane == 0) mbar_arrive(smem_u32(&sh->piece_free[slot]));
   }
@@ -250,92 +290,95 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
 
 // -------------------------------------------------------------- matrix unit --
 
+// The whole warp follows the barriers; one elected lane issues.
 template <int D, int FMT>
 __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem) {
   using C = TileCfg<D, FMT>;
   constexpr uint32_t S_DESC = mma_desc(128, C::BK, C::F::kBf16, false);
   constexpr uint32_t O_DESC = mma_desc(128, D, C::F::kBf16, true);
-  const uint32_t tm = sh->tmem;
-  long kc = 0, vc = 0, bc = 0;  // K blocks, V blocks read; score buffers handed out (one tile)
+  const uint32_t tm = __shfl_sync(0xffffffffu, sh->tmem, 0);
+  const uint64_t q0 = smem_desc(smem + C::Q_OFF, 16, 1024), k0 = smem_desc(smem + C::K_OFF, 16, 1024);
+  const uint64_t v0 = smem_desc(smem + C::V_OFF, C::BK * 128, 1024);
+  int ks = 0, kpar = 0, vs = 0, vpar = 0;  // stage to read next, its phase
+  int bc = 0;                              // score buffers handed out (one tile)
   int pc[2] = {0, 0};
-  auto scores = [&](int buf, int tile, int st) {
+  auto scores = [&](int buf, int tile, bool last, bool freed) {
+    const uint64_t q = q0 + (uint64_t)(tile * (C::TILE >> 4)), k = k0 + (uint64_t)(ks * (C::TILE >> 4));
+    if (elect_one()) {
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      const uint32_t at = (ks >> 2) * (128 * 128) + (ks & 3) * 32;
-      mma_ss(tm + buf * 128, smem_desc(smem + C::Q_OFF + tile * C::TILE + at, 16, 1024),
-             smem_desc(smem + C::K_OFF + st * C::TILE + at, 16, 1024), S_DESC, ks > 0);
+      for (int i = 0; i < D / 16; ++i) {
+        const uint64_t at = ((i >> 2) * (128 * 128) + (i & 3) * 32) >> 4;
+        mma_ss(tm + buf * 128, q + at, k + at, S_DESC, i > 0);
+      }
+      mma_commit(smem_u32(&sh->s_full[buf]));
+      if (last) mma_commit(smem_u32(&sh->k_empty[ks]));
+      if (freed) mma_commit(smem_u32(&sh->q_free));
     }
-    mma_commit(smem_u32(&sh->s_full[buf]));
+    __syncwarp();
+    if (last && ++ks == C::NS) ks = 0, kpar ^= 1;
   };
-  auto values = [&](int buf, int tile, int st, bool add) {
+  auto values = [&](int buf, int tile, bool last, int add) {
+    const uint64_t v = v0 + (uint64_t)(vs * (C::TILE >> 4));
+    if (elect_one()) {
 #pragma unroll
-    for (int ks = 0; ks < C::BK / 16; ++ks)
-      mma_ts(tm + 256 + tile * D, tm + buf * 128 + ks * 8, smem_desc(smem + C::V_OFF + st * C::TILE + ks * 2048, C::BK * 128, 1024),
-             O_DESC, add || ks > 0);
-    mma_commit(smem_u32(&sh->o_done[tile]));
+      for (int i = 0; i < C::BK / 16; ++i)
+        mma_ts(tm + 256 + tile * D, tm + buf * 128 + i * 8, v + (uint64_t)(i * 2048 >> 4), O_DESC, i > 0 ? 1 : add);
+      mma_commit(smem_u32(&sh->o_done[tile]));
+      if (last) mma_commit(smem_u32(&sh->v_empty[vs]));
+    }
+    __syncwarp();
+    if (last && ++vs == C::NS) vs = 0, vpar ^= 1;
   };
   for (int k = 0;; ++k) {
     const int slot = k % C::PIECES;
-    if (!tile_wait(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) return;
-    const int n = sh->piece[slot].nblk, tiles = (sh->piece[slot].rows + 127) / 128;
+    if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) return;
+    const int n = __shfl_sync(0xffffffffu, sh->piece[slot].nblk, 0);
+    const int tiles = (__shfl_sync(0xffffffffu, sh->piece[slot].rows, 0) + 127) / 128;
     if (n == 0) return;
-    if (!tile_wait(sh, a, &sh->q_full, k & 1)) return;
-    auto next_k = [&](int* st) {
-      *st = (int)(kc % C::NS);
-      const bool ok = tile_wait(sh, a, &sh->k_full[*st], (int)((kc / C::NS) & 1));
-      ++kc;
-      return ok;
-    };
-    int ks, vs;
-    if (!next_k(&ks)) return;
+    if (!tile_wait_warp(sh, a, &sh->q_full, k & 1)) return;
+    if (!tile_wait_warp(sh, a, &sh->k_full[ks], kpar)) return;
     tc_after_sync();
     if (C::NT == 2) {
-      for (int i = 0; i < tiles; ++i) scores(i, i, ks);
+      if (tiles == 2) scores(0, 0, false, false);
+      scores(tiles - 1, tiles - 1, true, n == 1);
     } else {
-      scores((int)(bc & 1), 0, ks);
+      scores(bc & 1, 0, true, n == 1);
     }
-    mma_commit(smem_u32(&sh->k_empty[ks]));
-    if (n == 1) mma_commit(smem_u32(&sh->q_free));
     for (int j = 0; j < n; ++j) {
-      vs = (int)(vc % C::NS);
       if (C::NT == 2) {
-        for (int i = 0; i < tiles; ++i) {
-          if (i == 0 && !tile_wait(sh, a, &sh->v_full[vs], (int)((vc / C::NS) & 1))) return;
-          if (!tile_wait(sh, a, &sh->p_full[i], pc[i]++ & 1)) return;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i >= tiles) break;
+          const bool last = i == tiles - 1;
+          if (i == 0 && !tile_wait_warp(sh, a, &sh->v_full[vs], vpar)) return;
+          if (!tile_wait_warp(sh, a, &sh->p_full[i], pc[i] & 1)) return;
+          ++pc[i];
           tc_after_sync();
-          values(i, i, vs, j > 0);
-          if (i == tiles - 1) mma_commit(smem_u32(&sh->v_empty[vs]));
+          values(i, i, last, j > 0);
           if (j + 1 < n) {
             if (i == 0) {
-              if (!next_k(&ks)) return;
+              if (!tile_wait_warp(sh, a, &sh->k_full[ks], kpar)) return;
               tc_after_sync();
             }
-            scores(i, i, ks);
-            if (i == tiles - 1) {
-              mma_commit(smem_u32(&sh->k_empty[ks]));
-              if (j + 2 == n) mma_commit(smem_u32(&sh->q_free));
-            }
+            scores(i, i, last, last && j + 2 == n);
           }
         }
       } else {
-        const int buf = (int)(bc & 1);
+        const int buf = bc & 1;
         if (j + 1 < n) {
-          if (!next_k(&ks)) return;
+          if (!tile_wait_warp(sh, a, &sh->k_full[ks], kpar)) return;
           tc_after_sync();
-          scores(buf ^ 1, 0, ks);
-          mma_commit(smem_u32(&sh->k_empty[ks]));
-          if (j + 2 == n) mma_commit(smem_u32(&sh->q_free));
+          scores(buf ^ 1, 0, true, j + 2 == n);
         }
-        if (!tile_wait(sh, a, &sh->v_full[vs], (int)((vc / C::NS) & 1))) return;
-        if (!tile_wait(sh, a, &sh->p_full[buf], pc[buf]++ & 1)) return;
+        if (!tile_wait_warp(sh, a, &sh->v_full[vs], vpar)) return;
+        if (!tile_wait_warp(sh, a, &sh->p_full[buf], (bc >> 1) & 1)) return;
         tc_after_sync();
-        values(buf, 0, vs, j > 0);
-        mma_commit(smem_u32(&sh->v_empty[vs]));
+        values(buf, 0, true, j > 0);
         ++bc;
       }
-      ++vc;
     }
-    mbar_arrive(smem_u32(&sh->piece_free[slot]));
+    if (elect_one()) mbar_arrive(smem_u32(&sh->piece_free[slot]));
+    __syncwarp();
   }
 }
 
@@ -418,31 +461,37 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
       // the tile's first and last position: blocks between need no mask
       const int pos_lo = p.s.p0 + (p.r0 + tile * 128) / a.rep;
       const int pos_hi = p.s.p0 + (p.r0 + min(tile * 128 + 127, p.rows - 1)) / a.rep;
-      float m = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+      float m = -INFINITY;
+      float2 l = make_float2(0.0f, 0.0f);
       for (int j = 0; j < p.nblk; ++j, ++bc, ++ob) {
         const int buf = C::NT == 2 ? tile : (bc & 1);
         if (!tile_wait_warp(sh, a, &sh->s_full[buf], C::NT == 2 ? bc & 1 : (bc >> 1) & 1)) return;
         tc_after_sync();
-        uint32_t s[BK];
-#pragma unroll
-        for (int c = 0; c < BK; c += 32) tmem_ld32(tm + buf * 128 + c, s + c);
-        tmem_wait_ld();
+        const uint32_t sb = tm + buf * 128;
         const int tok0 = (p.blk + j) * BK;
-        if (tok0 + BK - 1 > pos_lo || (a.window > 0 && tok0 <= pos_hi - a.window)) {
-          const int hi = pos - tok0, lo = a.window > 0 ? pos - a.window - tok0 : -1;  // columns lo < c <= hi
+        const bool edge = tok0 + BK - 1 > pos_lo || (a.window > 0 && tok0 <= pos_hi - a.window);
+        const int hi = pos - tok0, lo = a.window > 0 ? pos - a.window - tok0 : -1;  // visible columns: lo < c <= hi
+        // the row is read twice, 32 scores at a time: once for its maximum, once for its weights
+        uint32_t s[2][32];
+        float x0 = -INFINITY, x1 = -INFINITY;
+        tmem_ld32(sb, s[0]);
 #pragma unroll
-          for (int c = 0; c < BK; ++c)
-            if (c > hi || c <= lo) s[c] = 0xff800000u;
-        }
-        float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
+        for (int q = 0; q < BK / 32; ++q) {
+          tmem_wait_ld32(s[q & 1]);
+          tmem_ld32(sb + ((q + 1) * 32) % BK, s[(q + 1) & 1]);
+          uint32_t* e = s[q & 1];
+          if (edge) {
 #pragma unroll
-        for (int c = 0; c < BK; c += 4) {
-          x0 = fmaxf(x0, __uint_as_float(s[c]));
-          x1 = fmaxf(x1, __uint_as_float(s[c + 1]));
-          x2 = fmaxf(x2, __uint_as_float(s[c + 2]));
-          x3 = fmaxf(x3, __uint_as_float(s[c + 3]));
+            for (int c = 0; c < 32; ++c)
+              if (q * 32 + c > hi || q * 32 + c <= lo) e[c] = 0xff800000u;
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            x0 = fmaxf(fmaxf(x0, __uint_as_float(e[c])), __uint_as_float(e[c + 1]));
+            x1 = fmaxf(fmaxf(x1, __uint_as_float(e[c + 2])), __uint_as_float(e[c + 3]));
+          }
         }
-        const float top = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * sc;
+        const float top = fmaxf(x0, x1) * sc;
         const bool grow = top > m + 8.0f;
         if (__any_sync(0xffffffffu, grow)) {
           const float to = grow ? top : m;
@@ -450,32 +499,42 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
             const float f = to == -INFINITY ? 1.0f : fast_exp2(m - to);
             if (!tile_wait_warp(sh, a, &sh->o_done[tile], (ob - 1) & 1)) return;
             tc_after_sync();
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(tm + o_col + c, o);
-              tmem_wait_ld();
+              tmem_ld32(tm + o_col + c, s[1]);
+              tmem_wait_ld32(s[1]);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(tm + o_col + c, o);
+              for (int e = 0; e < 32; ++e) s[1][e] = __float_as_uint(__uint_as_float(s[1][e]) * f);
+              tmem_st32(tm + o_col + c, s[1]);
             }
-            l0 *= f;
-            l1 *= f;
+            l.x *= f;
+            l.y *= f;
           }
           m = to;
         }
         const float base = m == -INFINITY ? 0.0f : m - 7.0f;
+        const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(-base, -base);
         uint32_t w[32];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int q = 0; q < BK / 32; ++q) {
+          tmem_wait_ld32(s[q & 1]);  // (the first 32 are on their way since the last step of the maximum)
+          if (q + 1 < BK / 32) tmem_ld32(sb + (q + 1) * 32, s[(q + 1) & 1]);
+          uint32_t* e = s[q & 1];
+          if (edge) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float x = fast_exp2(fmaf(__uint_as_float(s[h * 64 + 2 * c]), sc, -base));
-            const float y = fast_exp2(fmaf(__uint_as_float(s[h * 64 + 2 * c + 1]), sc, -base));
-            l0 += x;
-            l1 += y;
-            w[c] = pack2<F::kBf16>(x, y);
+            for (int c = 0; c < 32; ++c)
+              if (q * 32 + c > hi || q * 32 + c <= lo) e[c] = 0xff800000u;
           }
-          tmem_st32(tm + buf * 128 + h * 32, w);
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            float2 x = fma2(make_float2(__uint_as_float(e[c]), __uint_as_float(e[c + 1])), sc2, nb2);
+            x.x = fast_exp2(x.x);
+            x.y = fast_exp2(x.y);
+            l = add2(l, x);
+            w[(q & 1) * 16 + c / 2] = pack2<F::kBf16>(x.x, x.y);
+          }
+          // 64 weights over scores that have all been read
+          if (q & 1) tmem_st32(sb + (q >> 1) * 32, w);
         }
         tmem_wait_st();
         tc_before_sync();
@@ -488,15 +547,15 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
       if (C::NT == 1 && p.nblk > 1 && !tile_wait_warp(sh, a, &sh->o_done[tile], (ob - 2) & 1)) return;
       if (!tile_wait_warp(sh, a, &sh->o_done[tile], (ob - 1) & 1)) return;
       tc_after_sync();
-      const float l = l0 + l1;
+      const float sum = l.x + l.y;
       const bool whole = p.has_first && p.has_last, has = r < p.rows;
-      const float f = whole ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+      const float f = whole ? (sum > 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
       const long slot_row = ((long)blockIdx.x * 2 + (p.has_first ? 1 : 0)) * C::ROWS + r;
       const long at = ((long)(p.s.s0 + rr / a.rep) * a.q_heads + p.head * a.rep + rr % a.rep) * D;
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
         tmem_ld32(tm + o_col + c, o);
-        tmem_wait_ld();
+        tmem_wait_ld32(o);
         if (!has) continue;
         if (whole) {
 #pragma unroll
@@ -516,7 +575,7 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
             *reinterpret_cast<uint4*>(a.part_o + slot_row * D + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
-      if (!whole && has) *reinterpret_cast<float2*>(a.part_ml + slot_row * 2) = make_float2(m, l);
+      if (!whole && has) *reinterpret_cast<float2*>(a.part_ml + slot_row * 2) = make_float2(m, sum);
       tc_before_sync();
     }
     if (tile == 0 && row == 0 && p.has_first && !p.has_last) {
@@ -572,14 +631,13 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
   __syncthreads();
   tc_after_sync();
 
-  // registers: 512 threads start with 128 each (65536); 256 * 176 + 128 * 48 + 128 * 112 = 65536
-  if (warp < 8) {
-    if constexpr (F::kQuant) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
-    if (warp < 4 * C::NT) tile_softmax<D, FMT>(a, &sh, smem, warp >> 2, threadIdx.x);
+  if (warp < 4 * C::NT) {
+    tile_softmax<D, FMT>(a, &sh, smem, warp >> 2, threadIdx.x);
+  } else if (warp < 8) {
+    if constexpr (F::kQuant) tile_dequantizer<D, FMT>(a, &sh, smem, threadIdx.x);  // one tile: 128 more dequantize
   } else if (warp < 12) {
-    if constexpr (F::kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;\n");
     if (warp == 8) {
-      if (lane == 0) tile_mma<D, FMT>(a, &sh, smem);
+      tile_mma<D, FMT>(a, &sh, smem);
     } else if (warp == 9) {
       if constexpr (!F::kQuant) tile_loader<D, FMT>(a, &sh, smem, lane);
     } else if (warp == 10) {
@@ -601,10 +659,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
       }
     }
   } else {
-    if constexpr (F::kQuant) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 112;\n");
-      tile_dequantizer<D, FMT>(a, &sh, smem, threadIdx.x - 384);
-    }
+    if constexpr (F::kQuant) tile_dequantizer<D, FMT>(a, &sh, smem, threadIdx.x - 384);
   }
   __syncwarp();
   if (*(volatile int*)&sh.dead) {  // given up: what is in flight lands before memory is given back

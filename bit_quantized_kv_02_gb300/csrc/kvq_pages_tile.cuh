@@ -384,53 +384,59 @@ __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* 
 
 // ------------------------------------------------------------------ softmax --
 
-// One row of queries into the swizzled operand tile (zeros behind the item's
-// rows); returns what its scores are to be multiplied by.
+// Address of query row r of a piece (of the whole tensor's rows, in elements).
+__device__ __forceinline__ long row_at(const Piece& p, int rep, int r, long token_stride, int D) {
+  const int R = p.r0 + r;
+  return (long)(p.s.s0 + R / rep) * token_stride + (long)(p.head * rep + R % rep) * D;
+}
+
+// A warp's 32 rows of queries into the swizzled operand tile, D / 8 lanes a row
+// (zeros behind the item's rows); returns what the lane's row's scores are to be
+// multiplied by.  row0: the warp's first row inside the tile.
 template <int D, int FMT>
-__device__ __forceinline__ float tile_query(const AttnArgs& a, const Piece& p, int r, uint32_t tile, int row) {
+__device__ __forceinline__ float tile_query(const AttnArgs& a, const Piece& p, int tile_row, int row0, uint32_t tile, int lane) {
   using F = Fmt<FMT>;
+  constexpr int LPR = D / 8, RPI = 32 / LPR, U = 8;  // lanes a row, rows a step, steps in flight
+  const int g = lane / LPR, c = lane % LPR;
   float sc = a.scale_log2;
-  const bool has = r < p.rows;
-  const int R = p.r0 + (has ? r : 0);
-  const uint16_t* src = static_cast<const uint16_t*>(a.q) + (long)(p.s.s0 + R / a.rep) * a.q_stride +
-                        (long)(p.head * a.rep + R % a.rep) * D;
-  auto chunk = [&](int c) -> uint4 {
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (!has) return w;
-    if (a.q_aligned) return *reinterpret_cast<const uint4*>(src + c * 8);
-    uint16_t* e = reinterpret_cast<uint16_t*>(&w);
+  for (int it0 = 0; it0 < LPR; it0 += U) {
+    uint4 w[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = src[c * 8 + i];
-    return w;
-  };
-  float f0 = 1.0f, f1 = 1.0f;
-  const bool convert = F::kQuant && a.q_bf16;
-  if (convert) {
-    float mx = 0.0f;
-    for (int c = 0; c < D / 8; ++c) {
-      const uint4 w = chunk(c);
-      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    for (int u = 0; u < U; ++u) {
+      const int r = tile_row + row0 + (it0 + u) * RPI + g;
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + row_at(p, a.rep, min(r, p.rows - 1), a.q_stride, D) + c * 8;
+      if (a.q_aligned) {
+        w[u] = *reinterpret_cast<const uint4*>(src);
+      } else {
+        uint16_t* e = reinterpret_cast<uint16_t*>(&w[u]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xffff0000u))));
+        for (int i = 0; i < 8; ++i) e[i] = src[i];
+      }
     }
-    const int E = norm_exp(mx);
-    f0 = exp2i(E / 2), f1 = exp2i(E - E / 2);
-    sc = a.scale_log2 * exp2i(-(E / 2)) * exp2i(-(E - E / 2));
-  }
-#pragma unroll 4
-  for (int c = 0; c < D / 8; ++c) {
-    uint4 w = chunk(c);
-    if (convert) {
-      uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        x[i] = pack2<false>(__uint_as_float(x[i] << 16) * f0 * f1, __uint_as_float(x[i] & 0xffff0000u) * f0 * f1);
-      w = make_uint4(x[0], x[1], x[2], x[3]);
+    for (int u = 0; u < U; ++u) {
+      const int it = it0 + u, row = row0 + it * RPI + g;
+      uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+      if (F::kQuant && a.q_bf16) {
+        float mx = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xffff0000u))));
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const int E = norm_exp(mx);
+        const float f0 = exp2i(E / 2), f1 = exp2i(E - E / 2);
+        const float y = __shfl_sync(0xffffffffu, a.scale_log2 * exp2i(-(E / 2)) * exp2i(-(E - E / 2)), (lane % RPI) * LPR);
+        if (lane / RPI == it) sc = y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[i] = pack2<false>(__uint_as_float(x[i] << 16) * f0 * f1, __uint_as_float(x[i] & 0xffff0000u) * f0 * f1);
+      }
+      if (tile_row + row >= p.rows) x[0] = x[1] = x[2] = x[3] = 0;
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(tile + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)),
+                   "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
+                   : "memory");
     }
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(tile + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)),
-                 "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
-                 : "memory");
   }
   return sc;
 }
@@ -451,7 +457,9 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
     if (p.nblk == 0) return;
     if (k > 0 && !tile_wait_warp(sh, a, &sh->q_free, (k - 1) & 1)) return;
     const int r = tile * 128 + row;
-    const float sc = tile_query<D, FMT>(a, p, r, smem + C::Q_OFF + tile * C::TILE, row);
+    const uint32_t q_tile = smem + C::Q_OFF + tile * C::TILE;
+    float sc = a.scale_log2;
+    if (tile * 128 < p.rows) sc = tile_query<D, FMT>(a, p, tile * 128, row & ~31, q_tile, lane);
     fence_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh->q_full));
@@ -551,29 +559,49 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
       const bool whole = p.has_first && p.has_last, has = r < p.rows;
       const float f = whole ? (sum > 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
       const long slot_row = ((long)blockIdx.x * 2 + (p.has_first ? 1 : 0)) * C::ROWS + r;
-      const long at = ((long)(p.s.s0 + rr / a.rep) * a.q_heads + p.head * a.rep + rr % a.rep) * D;
+      // Whole rows go through the query tile's place (its last product is done),
+      // so that the stores are D / 8 lanes a row.
+#pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
         tmem_ld32(tm + o_col + c, o);
         tmem_wait_ld32(o);
-        if (!has) continue;
         if (whole) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
-            uint4 w;
-            uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+            uint32_t x[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float u = __uint_as_float(o[e + 2 * i]) * f, v = __uint_as_float(o[e + 2 * i + 1]) * f;
               x[i] = a.q_bf16 ? pack2<true>(u, v) : pack2<false>(u, v);
             }
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at + c + e) = w;
+            const int ch = (c + e) / 8;
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(q_tile + (ch >> 3) * (128 * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)),
+                         "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
+                         : "memory");
           }
-        } else {
+        } else if (has) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<uint4*>(a.part_o + slot_row * D + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
+      }
+      if (whole) {
+        constexpr int LPR = D / 8, RPI = 32 / LPR;
+        const int g = lane / LPR, ch = lane % LPR;
+        __syncwarp();
+#pragma unroll 4
+        for (int it = 0; it < LPR; ++it) {
+          const int rw = (row & ~31) + it * RPI + g;
+          uint4 w;
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                       : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                       : "r"(q_tile + (ch >> 3) * (128 * 128) + rw * 128 + (((ch & 7) ^ (rw & 7)) << 4))
+                       : "memory");
+          if (tile * 128 + rw < p.rows)
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row_at(p, a.rep, tile * 128 + rw, (long)a.q_heads * D, D) + ch * 8) = w;
+        }
+        __syncwarp();
       }
       if (!whole && has) *reinterpret_cast<float2*>(a.part_ml + slot_row * 2) = make_float2(m, sum);
       tc_before_sync();

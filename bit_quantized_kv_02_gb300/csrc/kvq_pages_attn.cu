@@ -11,11 +11,12 @@ namespace kvq {
 namespace {
 
 constexpr int kJoinWarps = 8;
+constexpr int kJoinShare = 16;  // parts from which the warps of a block share a row
 
 // Joins the parts of the items that start in CTA blockIdx.x and end in a later
-// one.  A warp per share of the parts and all of a row's columns, then the warps'
-// sums through shared memory: an item over a long context has hundreds of
-// parts, and their reads are what takes the time.
+// one.  Few parts: a warp per row.  Many (an item over a long context has
+// hundreds, and their reads are what takes the time): the block's warps share a
+// row's parts and sum up through shared memory.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinWarps * 32) pages_join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int V = D / 32;  // columns of a lane
@@ -26,7 +27,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) pages_join_kernel(const __gri
   pdl_trigger();
   if (h.parts == 0) return;
   const long first = (long)blockIdx.x * 2 + 1;
-  for (int r = blockIdx.y; r < h.rows; r += gridDim.y) {
+  const bool share = h.parts > kJoinShare;
+  const int step = share ? 1 : kJoinWarps;  // rows a block takes at once
+  for (int r = blockIdx.y * step + (share ? 0 : warp); r < h.rows; r += gridDim.y * step) {
     // part i: slot 1 of the first CTA, slot 0 of the ones after it
     auto slot = [&](int i) { return (i ? first + 2 * i - 1 : first) * ROWS + r; };
     float M = -INFINITY;
@@ -35,7 +38,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) pages_join_kernel(const __gri
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float y[V] = {}, l = 0.0f;
 #pragma unroll 4
-    for (int i = warp; i < h.parts; i += kJoinWarps) {
+    for (int i = share ? warp : 0; i < h.parts; i += share ? kJoinWarps : 1) {
       const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * slot(i));
       const float f = ml.x == -INFINITY ? 0.0f : fast_exp2(ml.x - M);
       l += f * ml.y;
@@ -47,12 +50,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) pages_join_kernel(const __gri
         y[c + 1] += f * x.y;
       }
     }
+    const int R = h.row0 + r;
+    const long at = ((long)(h.q_row + R / a.rep) * a.q_heads + h.head * a.rep + R % a.rep) * D;
+    if (!share) {
+      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+      for (int c = 0; c < V; c += 2) store_out2(a, at + lane * V + c, y[c] * inv, y[c + 1] * inv);
+      continue;
+    }
 #pragma unroll
     for (int c = 0; c < V; ++c) part[warp][lane * V + c] = y[c];
     if (lane == 0) part[warp][D] = l;
     __syncthreads();
-    const int R = h.row0 + r;
-    const long at = ((long)(h.q_row + R / a.rep) * a.q_heads + h.head * a.rep + R % a.rep) * D;
     for (int c = threadIdx.x * 2; c < D; c += kJoinWarps * 64) {
       float s0 = 0.0f, s1 = 0.0f, sl = 0.0f;
 #pragma unroll

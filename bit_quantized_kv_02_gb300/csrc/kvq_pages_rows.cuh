@@ -1,9 +1,9 @@
 // kvq_pages_rows.cuh — paged attention for few query rows per kv head (single
 // tokens, drafted tokens, short chunks): bound by reading the cache once.
 //
-// A CTA of four warps walks its units of 64 tokens; each warp takes 16 of them,
-// one record, brought by a single bulk copy into the warp's own ring of
-// stages, and runs an independent softmax over its tokens, so nothing but the
+// A CTA of four warps walks its units of 64 or 128 tokens; each warp takes a
+// quarter, one or two records, brought by bulk copies into the warp's own ring
+// of stages, and runs an independent softmax over its tokens, so nothing but the
 // end of an item synchronises the warps.  Query rows are the 16 rows of
 // m16n8k16 (MT tiles of them), so all query heads of a kv head and several new
 // tokens share one read of the cache.
@@ -17,11 +17,13 @@
 //    one (zero, step) per token.  Codes become fp16 by an or with 1024's bits
 //    and one exact subtraction; zero + code * step is one fp16 fma, the value
 //    that the page stands for.
-// Scores, maxima, sums and outputs are fp32.  Probabilities are rounded to the
-// operand type (fp16, or bf16 for bf16 pages) for the value product, where the
-// rounding error of single weights averages out to less than the output's own
-// rounding; they enter as p * 2^7 with a maximum that lags by up to 2^8, so
-// that fp16 weights stay normal down to 2^-21 of the largest.
+// Scores, maxima, sums and outputs are fp32.  Weights enter the value product
+// as p * 2^7 with a maximum that lags by up to 2^8, so that fp16 weights stay
+// normal down to 2^-21 of the largest.  Over 16-bit pages with one row tile they
+// are split into the operand type and its remainder (a second product, hidden
+// behind the reads); elsewhere they are rounded to the operand type (fp16, or
+// bf16 for bf16 pages), which adds about as much to the error as the output's own
+// rounding does.
 #pragma once
 
 #include "kvq_pages_attn.cuh"
@@ -29,7 +31,6 @@
 namespace kvq {
 
 constexpr int kRowsWarps = 4;
-constexpr int kRowsBlock = 16 * kRowsWarps;  // tokens of a unit
 
 template <int FMT>
 struct Fmt {
@@ -44,8 +45,17 @@ struct RowsCfg {
   using F = Fmt<FMT>;
   static constexpr int ROWS = 16 * MT;
   // a record with the most metadata (groups of 32)
-  static constexpr int STAGE = 2 * D * (F::KB + F::VB) + (F::kQuant ? 2 * 16 * (D / 32) * 4 : 0);
-  static constexpr int NS = 20480 / STAGE < 2 ? 2 : (20480 / STAGE > 8 ? 8 : 20480 / STAGE);
+  static constexpr int REC = 2 * D * (F::KB + F::VB) + (F::kQuant ? 2 * 16 * (D / 32) * 4 : 0);
+  // records of a warp's step and stage: two where they are small, so that the
+  // softmax's exchanges and the loop cost half as much per token
+  static constexpr int RECS = REC > 4096 ? 1 : 2;
+  static constexpr int STEP = 16 * RECS, BK = STEP * kRowsWarps;  // tokens of a step and of a unit
+  static constexpr int STAGE = RECS * REC;
+  // enough stages for 16 KB a warp in flight, two at least
+  static constexpr int NS = 16384 / STAGE < 2 ? 2 : (16384 / STAGE > 4 ? 4 : 16384 / STAGE);
+  // CTAs per SM that the registers are cut for
+  static constexpr int CTAS = MT == 2 ? 2 : (D == 64 ? 4 : (D == 128 ? 3 : 2));
+  static constexpr bool kSplit = !F::kQuant && MT == 1;  // weights as operand + remainder
   static constexpr int RING = kRowsWarps * NS * STAGE;
   static constexpr int MERGE = kRowsWarps * ROWS * (D + 2) * 4;
   static constexpr int SMEM = RING > MERGE ? RING : MERGE;
@@ -105,16 +115,23 @@ __device__ __forceinline__ void ldsv(uint32_t a, uint32_t* x) {
                    : "memory");
   }
 }
-// Two codes as the halves 1024 + code -> zero + code * step.
-__device__ __forceinline__ uint32_t dequant2(uint32_t biased, __half2 s, __half2 z) {
-  return as_u32(__hfma2(__hsub2(as_h2(biased), as_h2(0x64006400u)), s, z));
+// Two codes -> zero + code * step: the codes' bits or-ed into the mantissas of a
+// power of two give power + code exactly, the power is taken off exactly, and
+// one fma rounds.
+__device__ __forceinline__ uint32_t dequant2(uint32_t biased, uint32_t power, __half2 s, __half2 z) {
+  return as_u32(__hfma2(__hsub2(as_h2(biased), as_h2(power)), s, z));
 }
-// The halves 1024 + code of two 4-bit codes (low bits of both halves of x), and
-// of the low / high two of four 8-bit codes.
-__device__ __forceinline__ uint32_t biased4(uint32_t x) { return (x & 0x000f000fu) | 0x64006400u; }
+// nibble J of both halves: bits 0..3 under 1024 (0x6400), bits 4..7 under 64 (0x5400)
+template <int J>
+__device__ __forceinline__ uint32_t nibbles(uint32_t x, __half2 s, __half2 z) {
+  const uint32_t y = J >= 2 ? x >> 8 : x;
+  return (J & 1) ? dequant2((y & 0x00f000f0u) | 0x54005400u, 0x54005400u, s, z)
+                 : dequant2((y & 0x000f000fu) | 0x64006400u, 0x64006400u, s, z);
+}
+// the low / high two of four 8-bit codes
 template <int HIGH>
-__device__ __forceinline__ uint32_t biased8(uint32_t x) {
-  return __byte_perm(x, 0x64646464u, HIGH ? 0x4342 : 0x4140);
+__device__ __forceinline__ uint32_t bytes(uint32_t x, __half2 s, __half2 z) {
+  return dequant2(__byte_perm(x, 0x64646464u, HIGH ? 0x4342 : 0x4140), 0x64006400u, s, z);
 }
 
 // One 16-token record's scores: acc[m][n8 tile] += Q K^T.
@@ -156,12 +173,14 @@ __device__ __forceinline__ void rows_scores(uint32_t st, const PagesLayout& L, c
         for (int i = 0; i < RUN / 4; ++i) {  // one mma step: 4 channels
           uint32_t b0, b1;
           if (F::KB == 8) {
-            b0 = dequant2(biased8<0>(w[i]), s, z);
-            b1 = dequant2(biased8<1>(w[i]), s, z);
+            b0 = bytes<0>(w[i], s, z);
+            b1 = bytes<1>(w[i], s, z);
+          } else if (i & 1) {
+            b0 = nibbles<2>(w[i / 2], s, z);
+            b1 = nibbles<3>(w[i / 2], s, z);
           } else {
-            const uint32_t x = w[i / 2] >> (8 * (i & 1));
-            b0 = dequant2(biased4(x), s, z);
-            b1 = dequant2(biased4(x >> 4), s, z);
+            b0 = nibbles<0>(w[i / 2], s, z);
+            b1 = nibbles<1>(w[i / 2], s, z);
           }
 #pragma unroll
           for (int m = 0; m < MT; ++m) mma16<false>(acc[m][h], q[m][r * (RUN / 4) + i], b0, b1);
@@ -173,8 +192,8 @@ __device__ __forceinline__ void rows_scores(uint32_t st, const PagesLayout& L, c
 
 // o[m][n8 tile] += P V of one record; p: the probabilities as A operands.
 template <int D, int FMT, int MT>
-__device__ __forceinline__ void rows_values(uint32_t st, const PagesLayout& L, const uint32_t (*p)[4], int lane,
-                                            float (*o)[D / 8][4]) {
+__device__ __forceinline__ void rows_values(uint32_t st, const PagesLayout& L, const uint32_t (*p)[4],
+                                            const uint32_t (*rest)[4], int lane, float (*o)[D / 8][4]) {
   using F = Fmt<FMT>;
   if constexpr (!F::kQuant) {
     const int row = (lane & 7) + (((lane >> 3) & 1) << 3), ch = lane >> 4;
@@ -188,6 +207,10 @@ __device__ __forceinline__ void rows_values(uint32_t st, const PagesLayout& L, c
       for (int m = 0; m < MT; ++m) {
         mma16<F::kBf16>(o[m][2 * j], p[m], b[0], b[1]);
         mma16<F::kBf16>(o[m][2 * j + 1], p[m], b[2], b[3]);
+        if constexpr (RowsCfg<D, FMT, MT>::kSplit) {
+          mma16<F::kBf16>(o[m][2 * j], rest[m], b[0], b[1]);
+          mma16<F::kBf16>(o[m][2 * j + 1], rest[m], b[2], b[3]);
+        }
       }
     }
   } else {
@@ -219,8 +242,8 @@ __device__ __forceinline__ void rows_values(uint32_t st, const PagesLayout& L, c
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const uint32_t b0 = dequant2((c & 1) ? biased8<1>(x[0][c >> 1]) : biased8<0>(x[0][c >> 1]), s[0], z[0]);
-          const uint32_t b1 = dequant2((c & 1) ? biased8<1>(x[1][c >> 1]) : biased8<0>(x[1][c >> 1]), s[1], z[1]);
+          const uint32_t b0 = (c & 1) ? bytes<1>(x[0][c >> 1], s[0], z[0]) : bytes<0>(x[0][c >> 1], s[0], z[0]);
+          const uint32_t b1 = (c & 1) ? bytes<1>(x[1][c >> 1], s[1], z[1]) : bytes<0>(x[1][c >> 1], s[1], z[1]);
 #pragma unroll
           for (int m = 0; m < MT; ++m) mma16<false>(o[m][4 * i + c], p[m], b0, b1);
         }
@@ -236,10 +259,15 @@ __device__ __forceinline__ void rows_values(uint32_t st, const PagesLayout& L, c
         }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const uint32_t b0 = dequant2(biased4(x[0][c & 1] >> (4 * (c >> 1))), s[0], z[0]);
-          const uint32_t b1 = dequant2(biased4(x[1][c & 1] >> (4 * (c >> 1))), s[1], z[1]);
+          uint32_t b[2];
 #pragma unroll
-          for (int m = 0; m < MT; ++m) mma16<false>(o[m][8 * i + c], p[m], b0, b1);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t y = x[h][c & 1];
+            b[h] = c < 2 ? nibbles<0>(y, s[h], z[h]) : c < 4 ? nibbles<1>(y, s[h], z[h])
+                 : c < 6 ? nibbles<2>(y, s[h], z[h]) : nibbles<3>(y, s[h], z[h]);
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) mma16<false>(o[m][8 * i + c], p[m], b[0], b[1]);
         }
       }
     }
@@ -307,10 +335,10 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Piece& p, 
 }
 
 template <int D, int FMT, int MT>
-__global__ void __launch_bounds__(kRowsWarps * 32) pages_rows_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pages_rows_kernel(const __grid_constant__ AttnArgs a) {
   using C = RowsCfg<D, FMT, MT>;
   using F = Fmt<FMT>;
-  constexpr int ROWS = C::ROWS, NS = C::NS, BK = kRowsBlock;
+  constexpr int ROWS = C::ROWS, NS = C::NS, BK = C::BK, RECS = C::RECS, STEP = C::STEP;
   extern __shared__ __align__(1024) char smem[];
   __shared__ Work<BK, ROWS> work;
   __shared__ Piece piece;
@@ -340,26 +368,32 @@ __global__ void __launch_bounds__(kRowsWarps * 32) pages_rows_kernel(const __gri
     __syncthreads();
     const Piece p = piece;
     u += p.nblk;
-    // this warp's records: tile index 4 * block + warp, while it holds a visible token
+    // this warp's steps: STEP tokens at 4 * block + warp, while they hold a visible one
     const int see1 = max(p.s.p0 + (p.r0 + p.rows - 1) / a.rep + 1, 0);
     const int see0 = a.window > 0 ? max(p.s.p0 + p.r0 / a.rep - a.window + 1, 0) : 0;
-    const int tiles = (see1 + 15) >> 4;
+    const int tok0 = (p.blk * kRowsWarps + warp) * STEP;  // of step j: tok0 + BK * j
     int j = 0;
-    const int nt = max(min((tiles - warp + kRowsWarps - 1) / kRowsWarps - p.blk, p.nblk), 0);
-    if (j < nt && ((p.blk * kRowsWarps + warp) << 4) + 16 <= see0) ++j;
-    const int tok0 = (p.blk * kRowsWarps + warp) << 4;  // token of tile j: tok0 + 64 * j
+    const int nt = max(min((see1 - tok0 + BK - 1) / BK, p.nblk), 0);
+    if (j < nt && tok0 + STEP <= see0) ++j;
 
-    // the first stages, one lane each
-    if (lane < min(NS, nt - j) && alive) {
-      const int tok = tok0 + BK * (j + lane);
-      int s = stage + lane;
+    // Copies of a step into stage s: lane r % RECS brings record r % RECS, if it
+    // holds a token of the sequence.  The first NS steps at once, RECS lanes each.
+    auto bring = [&](int tok, int page, int s) {
+      const int rec = lane % RECS;
+      const bool second = RECS == 2 && tok - rec * 16 + 16 < p.s.len;
+      if (rec == 0) mbar_expect(bar + s * 8, second ? 2 * a.pv.L.tile_bytes : a.pv.L.tile_bytes);
+      if (rec == 0 || second)
+        bulk_load(ring + s * C::STAGE + rec * C::REC, tile_addr(a, page, p.head, tok), a.pv.L.tile_bytes, bar + s * 8);
+    };
+    auto page_of = [&](int tok) { return tok < p.s.len ? page_index(a, p.b, tok) : 0; };
+    if (lane < RECS * min(NS, nt - j) && alive) {
+      const int tok = tok0 + BK * (j + lane / RECS) + (lane % RECS) * 16;
+      int s = stage + lane / RECS;
       s = s >= NS ? s - NS : s;
-      const char* src = tile_addr(a, page_index(a, p.b, tok), p.head, tok);
-      mbar_expect(bar + s * 8, a.pv.L.tile_bytes);
-      bulk_load(ring + s * C::STAGE, src, a.pv.L.tile_bytes, bar + s * 8);
+      bring(tok, page_of(tok), s);
     }
     __syncwarp();
-    int next = j + NS < nt ? page_index(a, p.b, tok0 + BK * (j + NS)) : 0;
+    int next = lane < RECS && j + NS < nt ? page_of(tok0 + BK * (j + NS) + lane * 16) : 0;
 
     uint32_t q[MT][D / 16][4];
     float sc[MT][2];
@@ -389,56 +423,65 @@ __global__ void __launch_bounds__(kRowsWarps * 32) pages_rows_kernel(const __gri
       }
       const uint32_t st = ring + stage * C::STAGE;
       const int tok = tok0 + BK * j;
-      if (tok + 16 > p.s.len) {  // the sequence ends inside this record: what lies behind has no effect
+      if (tok + STEP > p.s.len) {  // the sequence ends inside this step: what lies behind has no effect
         const int n = p.s.len - tok;
         if (!F::kQuant) {
-          for (int i = lane; i < (16 - n) * (D / 8); i += 32) {
+          for (int i = lane; i < (STEP - n) * (D / 8); i += 32) {
             const int r = n + i / (D / 8), c = i % (D / 8);
-            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(st + a.pv.L.v_off + (c >> 3) * 2048 + r * 128 + ((c & 7) << 4)),
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(st + (r >> 4) * C::REC + a.pv.L.v_off + (c >> 3) * 2048 + (r & 15) * 128 + ((c & 7) << 4)),
                          "r"(0)
                          : "memory");
           }
         } else {
           const int per = D >> a.pv.L.v_lg;
-          for (int i = lane; i < (16 - n) * per; i += 32)
-            asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(st + a.pv.L.vm_off + (n * per + i) * 4), "r"(0) : "memory");
+          for (int i = lane; i < (STEP - n) * per; i += 32) {
+            const int r = n + i / per, c = i % per;
+            asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(st + (r >> 4) * C::REC + a.pv.L.vm_off + ((r & 15) * per + c) * 4), "r"(0)
+                         : "memory");
+          }
         }
         fence_async();
         __syncwarp();
       }
-      float acc[MT][2][4];
+      float acc[RECS][MT][2][4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int x = 0; x < RECS; ++x) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[m][h][e] = 0.0f;
-      rows_scores<D, FMT, MT>(st, a.pv.L, q, lane, acc);
-      const bool edge = tok + 15 > pos_lo || (a.window > 0 && tok <= pos_hi - a.window);
-      uint32_t pa[MT][4];
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[x][m][h][e] = 0.0f;
+        rows_scores<D, FMT, MT>(st + x * C::REC, a.pv.L, q, lane, acc[x]);
+      }
+      const bool edge = tok + STEP - 1 > pos_lo || (a.window > 0 && tok <= pos_hi - a.window);
       bool grow = false;
       float top[MT][2];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
+        if (edge) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+          for (int x = 0; x < RECS; ++x)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float s = acc[m][h][e] * sc[m][e >> 1];
-            if (edge) {
-              const int c = F::kQuant ? tok + 8 * h + t + 4 * (e & 1) : tok + 8 * h + 2 * t + (e & 1);
-              const int at = pos[m][e >> 1];
-              if (c > at || (a.window > 0 && c <= at - a.window)) s = -INFINITY;
-            }
-            acc[m][h][e] = s;
-          }
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int c = tok + 16 * x + 8 * h + (F::kQuant ? t + 4 * (e & 1) : 2 * t + (e & 1));
+                const int at = pos[m][e >> 1];
+                if (c > at || (a.window > 0 && c <= at - a.window)) acc[x][m][h][e] = -INFINITY;
+              }
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(fmaxf(acc[m][0][2 * e], acc[m][0][2 * e + 1]), fmaxf(acc[m][1][2 * e], acc[m][1][2 * e + 1]));
+          float x = -INFINITY;
+#pragma unroll
+          for (int y = 0; y < RECS; ++y)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) x = fmaxf(fmaxf(x, acc[y][m][h][2 * e]), acc[y][m][h][2 * e + 1]);
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          top[m][e] = x;
-          grow = grow || x > mx[m][e] + 8.0f;
+          top[m][e] = x * sc[m][e];
+          grow = grow || top[m][e] > mx[m][e] + 8.0f;
         }
       }
       if (__any_sync(0xffffffffu, grow)) {
@@ -458,29 +501,37 @@ __global__ void __launch_bounds__(kRowsWarps * 32) pages_rows_kernel(const __gri
           }
       }
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
+      for (int x = 0; x < RECS; ++x) {
+        uint32_t pa[MT][4], pr[MT][4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float base = mx[m][e] == -INFINITY ? 0.0f : mx[m][e] - 7.0f;
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float x = fast_exp2(acc[m][h][2 * e] - base), y = fast_exp2(acc[m][h][2 * e + 1] - base);
-            sum[m][e] += x + y;
-            pa[m][2 * h + e] = pack2<F::kBf16>(x, y);
+          for (int e = 0; e < 2; ++e) {
+            const float base = mx[m][e] == -INFINITY ? 0.0f : mx[m][e] - 7.0f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float u = fast_exp2(fmaf(acc[x][m][h][2 * e], sc[m][e], -base));
+              const float v = fast_exp2(fmaf(acc[x][m][h][2 * e + 1], sc[m][e], -base));
+              sum[m][e] += u + v;
+              const uint32_t w = pack2<F::kBf16>(u, v);
+              pa[m][2 * h + e] = w;
+              if constexpr (C::kSplit) {
+                float2 back;
+                if (F::kBf16) back = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+                else back = __half22float2(as_h2(w));
+                pr[m][2 * h + e] = pack2<F::kBf16>(u - back.x, v - back.y);
+              }
+            }
           }
-        }
+        rows_values<D, FMT, MT>(st + x * C::REC, a.pv.L, pa, pr, lane, o);
       }
-      rows_values<D, FMT, MT>(st, a.pv.L, pa, lane, o);
       __syncwarp();
-      if (j + NS < nt) {
-        if (lane == 0) {
-          const int tn = tok + BK * NS;
-          const char* src = tile_addr(a, next, p.head, tn);
-          mbar_expect(bar + stage * 8, a.pv.L.tile_bytes);
-          bulk_load(st, src, a.pv.L.tile_bytes, bar + stage * 8);
-        }
-        if (j + NS + 1 < nt) next = page_index(a, p.b, tok + BK * (NS + 1));
+      if (lane < RECS && j + NS < nt) {
+        const int tn = tok + BK * NS + lane * 16;
+        bring(tn, next, stage);
+        if (j + NS + 1 < nt) next = page_of(tn + BK);
       }
+      __syncwarp();
       if (++stage == NS) stage = 0, phase ^= 1;
     }
     if (!alive)  // copies still in flight land before their stages are used for anything else

@@ -219,9 +219,18 @@ __device__ __forceinline__ void store_raw(uint32_t tile, int tid, const RawTile<
           }
     uint32_t y[16];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      if (BITS == 8) y[k] = dequant2((k & 1) ? biased8<1>(w[k / 2]) : biased8<0>(w[k / 2]), s, z);
-      else y[k] = dequant2(biased4(w[k / 4] >> (4 * (k & 3))), s, z);
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (BITS == 8) {
+        y[4 * k] = bytes<0>(w[2 * k], s, z);
+        y[4 * k + 1] = bytes<1>(w[2 * k], s, z);
+        y[4 * k + 2] = bytes<0>(w[2 * k + 1], s, z);
+        y[4 * k + 3] = bytes<1>(w[2 * k + 1], s, z);
+      } else {
+        y[4 * k] = nibbles<0>(w[k], s, z);
+        y[4 * k + 1] = nibbles<1>(w[k], s, z);
+        y[4 * k + 2] = nibbles<2>(w[k], s, z);
+        y[4 * k + 3] = nibbles<3>(w[k], s, z);
+      }
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {

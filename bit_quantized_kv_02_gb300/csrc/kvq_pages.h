@@ -97,12 +97,15 @@ struct AttnArgs {
   SplitHead* split;  // [CTA]
 };
 
-// An attention kernel: its shared memory, threads and resident CTAs per SM.
+// An attention kernel: its dynamic shared memory (the batch's line of units comes
+// on top), threads, static shared memory and the CTAs per SM that its registers
+// allow.
 struct AttnKernel {
   const void* fn;
   size_t smem;
   int threads;
-  int ctas_per_sm;
+  int reg_ctas;
+  size_t static_smem;
 };
 
 }  // namespace kvq
@@ -118,6 +121,7 @@ struct kvq_pages {
   kvq::SplitHead* d_split = nullptr;
   int device = 0;
   int sm_count = 0;
+  int sm_smem = 0, cta_smem = 0;  // shared memory of an SM, of it reserved per CTA
   int which = 0;     // kernel choice (kvq_pages_set_kernel)
   kvq::AttnKernel rows_fn[2] = {};  // few-rows kernel with one and two row tiles (one only at head_dim 256)
   kvq::AttnKernel tile_fn = {};     // many-rows kernel

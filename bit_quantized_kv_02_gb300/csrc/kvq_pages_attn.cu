@@ -87,11 +87,19 @@ const void* join_dim(int rows) {
   }
 }
 
+size_t launch_smem(const AttnKernel& k, int batch) { return k.smem + (size_t)(batch + 1) * sizeof(long); }
+
+// CTAs that an SM holds at once.
+int resident(const kvq_pages* P, const AttnKernel& k, int batch) {
+  const size_t each = launch_smem(k, batch) + k.static_smem + P->cta_smem + 127;
+  return std::max(1, std::min(k.reg_ctas, (int)(P->sm_smem / each)));
+}
+
 // One attention launch and the join of what its CTAs shared; `rows`: query rows
 // a CTA holds, `used`: the most that an item can have.
 cudaError_t launch_kernel(const AttnKernel& k, AttnArgs a, int ctas, int rows, int used, cudaStream_t st) {
   void* args[] = {&a};
-  cudaError_t e = launch_pdl(k.fn, dim3(ctas), dim3(k.threads), k.smem, st, args);
+  cudaError_t e = launch_pdl(k.fn, dim3(ctas), dim3(k.threads), launch_smem(k, a.bv.batch), st, args);
   if (e != cudaSuccess) return e;
   const int D = a.pv.head_dim;
   const void* join = D == 64 ? join_dim<64>(rows) : D == 128 ? join_dim<128>(rows) : join_dim<256>(rows);
@@ -105,7 +113,7 @@ cudaError_t launch_rows(kvq_pages* P, AttnArgs a, int max_rows, cudaStream_t st)
   const int mt = max_rows > 16 && P->rows_fn[1].fn ? 2 : 1;
   const AttnKernel& k = P->rows_fn[mt - 1];
   a.min_units = 2;
-  return launch_kernel(k, a, std::min(k.ctas_per_sm * P->sm_count, kPagesCtas), 16 * mt, max_rows, st);
+  return launch_kernel(k, a, std::min(resident(P, k, a.bv.batch) * P->sm_count, kPagesCtas), 16 * mt, max_rows, st);
 }
 
 cudaError_t launch_tile(kvq_pages* P, AttnArgs a, int max_rows, cudaStream_t st) {
@@ -128,12 +136,20 @@ cudaError_t pages_attn_setup(kvq_pages* P) {
   P->rows_fn[0] = D == 64 ? rows_kernel_d64(fmt, 1) : D == 128 ? rows_kernel_d128(fmt, 1) : rows_kernel_d256(fmt, 1);
   if (D < 256) P->rows_fn[1] = D == 64 ? rows_kernel_d64(fmt, 2) : rows_kernel_d128(fmt, 2);
   P->tile_fn = D == 64 ? tile_kernel_d64(fmt) : D == 128 ? tile_kernel_d128(fmt) : tile_kernel_d256(fmt);
+  cudaError_t e = cudaDeviceGetAttribute(&P->sm_smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor, P->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P->cta_smem, cudaDevAttrReservedSharedMemoryPerBlock, P->device);
+  if (e != cudaSuccess) return e;
   for (AttnKernel* k : {&P->rows_fn[0], &P->rows_fn[1], &P->tile_fn}) {
     if (!k->fn) continue;
-    cudaError_t e = cudaFuncSetAttribute(k->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k->smem);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k->ctas_per_sm, k->fn, k->threads, k->smem);
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, k->fn);
     if (e != cudaSuccess) return e;
-    if (k->ctas_per_sm < 1) return cudaErrorInvalidConfiguration;
+    k->static_smem = at.sharedSizeBytes;
+    const size_t most = launch_smem(*k, kPagesMaxBatch);
+    e = cudaFuncSetAttribute(k->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k->reg_ctas, k->fn, k->threads, 0);
+    if (e != cudaSuccess) return e;
+    if (k->reg_ctas < 1) return cudaErrorInvalidConfiguration;
   }
   return cudaSuccess;
 }

@@ -108,11 +108,11 @@ struct Piece {
   long item0, item1;        // the item's units
 };
 
-// The line of units, as one CTA sees it.  `pre` (shared, kPagesMaxBatch + 1
-// entries) holds the units before each sequence.
+// The line of units, as one CTA sees it.  `pre` (shared memory behind the
+// kernel's own, batch + 1 entries) holds the units before each sequence.
 template <int BK, int ROWS>
 struct Work {
-  long pre[kPagesMaxBatch + 1];
+  long* pre;
   long total;
   int ctas;
 };
@@ -132,9 +132,11 @@ __device__ __forceinline__ long seq_units(const AttnArgs& a, const Seq& s, int l
   return sum;
 }
 
-// All threads of the CTA; leaves the line in *w.
+// All threads of the CTA; leaves the line in *w, its units before each sequence
+// in `pre`.
 template <int BK, int ROWS>
-__device__ __forceinline__ void plan_work(const AttnArgs& a, Work<BK, ROWS>* w) {
+__device__ __forceinline__ void plan_work(const AttnArgs& a, Work<BK, ROWS>* w, long* pre) {
+  if (threadIdx.x == 0) w->pre = pre;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   if (a.rows_hi <= ROWS && a.window == 0) {
     // one block of rows per sequence: a thread each
@@ -143,7 +145,7 @@ __device__ __forceinline__ void plan_work(const AttnArgs& a, Work<BK, ROWS>* w) 
       const Seq s = load_seq(a.pv, a.bv, b, &bad);
       const int R = s.n * a.rep;
       if (bad) atomicOr(a.pv.err, 1);
-      w->pre[b + 1] = R <= a.rows_lo || R > a.rows_hi ? 0 : (long)a.pv.heads * max((s.len + BK - 1) / BK, 1);
+      pre[b + 1] = R <= a.rows_lo || R > a.rows_hi ? 0 : (long)a.pv.heads * max((s.len + BK - 1) / BK, 1);
     }
   } else {
     for (int b = warp; b < a.bv.batch; b += warps) {
@@ -151,7 +153,7 @@ __device__ __forceinline__ void plan_work(const AttnArgs& a, Work<BK, ROWS>* w) 
       const Seq s = load_seq(a.pv, a.bv, b, &bad);
       const long u = seq_units<BK, ROWS>(a, s, lane) * a.pv.heads;
       if (lane == 0) {
-        w->pre[b + 1] = u;
+        pre[b + 1] = u;
         if (bad) atomicOr(a.pv.err, 1);
       }
     }
@@ -161,18 +163,18 @@ __device__ __forceinline__ void plan_work(const AttnArgs& a, Work<BK, ROWS>* w) 
     long run = 0;
     for (int b0 = 0; b0 < a.bv.batch; b0 += 32) {
       const int b = b0 + lane;
-      long x = b < a.bv.batch ? w->pre[b + 1] : 0;
+      long x = b < a.bv.batch ? pre[b + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
       x += run;
-      if (b < a.bv.batch) w->pre[b + 1] = x;
+      if (b < a.bv.batch) pre[b + 1] = x;
       run = __shfl_sync(0xffffffffu, x, 31);
     }
     if (lane == 0) {
-      w->pre[0] = 0;
+      pre[0] = 0;
       w->total = run;
       w->ctas = (int)min((long)gridDim.x, (run + a.min_units - 1) / a.min_units);
     }
@@ -245,18 +247,25 @@ __device__ __forceinline__ Piece find_piece(const AttnArgs& a, const Work<BK, RO
   return p;
 }
 
-// Byte address of the record that holds token `tok` of a sequence's head; a bad
-// page index is replaced by page 0 and recorded.
 __device__ __forceinline__ int page_index(const AttnArgs& a, int b, int tok) {
   return a.bv.table[b * a.bv.stride + (tok >> a.pv.lg_pt)];
 }
-__device__ __forceinline__ const char* tile_addr(const AttnArgs& a, int page, int head, int tok) {
-  if ((unsigned)page >= (unsigned)a.pv.pages) {
-    atomicOr(a.pv.err, 1);
-    page = 0;
+// Records of one kv head: address of the one that holds token `tok` of a
+// sequence, in the given page.  A page outside the pool is replaced by page 0
+// and recorded.
+struct PageRun {
+  const char* base;
+  long page_bytes;  // from a page to the next
+  __device__ __forceinline__ PageRun(const PagesView& pv, int head)
+      : base(pv.base + head * page_head_bytes(pv)), page_bytes(pv.heads * page_head_bytes(pv)) {}
+  __device__ __forceinline__ const char* at(const AttnArgs& a, int page, int tok) const {
+    if ((unsigned)page >= (unsigned)a.pv.pages) {
+      atomicOr(a.pv.err, 1);
+      page = 0;
+    }
+    return base + page * page_bytes + ((tok & ((1 << a.pv.lg_pt) - 1)) >> 4) * a.pv.L.tile_bytes;
   }
-  return record_of(a.pv, page, head, tok & ((1 << a.pv.lg_pt) - 1));
-}
+};
 
 __device__ __forceinline__ void store_out2(const AttnArgs& a, long at, float x, float y) {
   if (a.q_bf16) static_cast<__nv_bfloat162*>(a.out)[at >> 1] = __floats2bfloat162_rn(x, y);

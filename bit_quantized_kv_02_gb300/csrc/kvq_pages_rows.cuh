@@ -46,19 +46,19 @@ struct RowsCfg {
   static constexpr int ROWS = 16 * MT;
   // a record with the most metadata (groups of 32)
   static constexpr int REC = 2 * D * (F::KB + F::VB) + (F::kQuant ? 2 * 16 * (D / 32) * 4 : 0);
-  // records of a warp's step and stage: two where they are small, so that the
-  // softmax's exchanges and the loop cost half as much per token
-  static constexpr int RECS = REC > 4096 ? 1 : 2;
+  // CTAs per SM that registers and shared memory are cut for
+  static constexpr int CTAS = MT == 2 ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : (D == 128 && F::kQuant ? 3 : 2));
+  static constexpr int BUDGET = CTAS == 4 ? 12544 : (CTAS == 3 ? 16384 : 24576);  // bytes of a warp's ring
+  // records of a warp's step and stage: two where two such stages fit, so that
+  // the softmax's exchanges and the loop cost half as much per token
+  static constexpr int RECS = 4 * REC > BUDGET ? 1 : 2;
   static constexpr int STEP = 16 * RECS, BK = STEP * kRowsWarps;  // tokens of a step and of a unit
   static constexpr int STAGE = RECS * REC;
-  // enough stages for 16 KB a warp in flight, two at least
-  static constexpr int NS = 16384 / STAGE < 2 ? 2 : (16384 / STAGE > 4 ? 4 : 16384 / STAGE);
-  // CTAs per SM that the registers are cut for
-  static constexpr int CTAS = MT == 2 ? 2 : (D == 64 ? 4 : (D == 128 ? 3 : 2));
+  static constexpr int NS = BUDGET / STAGE < 2 ? 2 : (BUDGET / STAGE > 4 ? 4 : BUDGET / STAGE);
   static constexpr bool kSplit = !F::kQuant && MT == 1;  // weights as operand + remainder
   static constexpr int RING = kRowsWarps * NS * STAGE;
   static constexpr int MERGE = kRowsWarps * ROWS * (D + 2) * 4;
-  static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+  static constexpr int SMEM = (RING > MERGE ? RING : MERGE);
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
@@ -125,8 +125,8 @@ __device__ __forceinline__ uint32_t dequant2(uint32_t biased, uint32_t power, __
 template <int J>
 __device__ __forceinline__ uint32_t nibbles(uint32_t x, __half2 s, __half2 z) {
   const uint32_t y = J >= 2 ? x >> 8 : x;
-  return (J & 1) ? dequant2((y & 0x00f000f0u) | 0x54005400u, 0x54005400u, s, z)
-                 : dequant2((y & 0x000f000fu) | 0x64006400u, 0x64006400u, s, z);
+  return (J & 1) ? dequant2(lop3_and_or(y, 0x00f000f0u, 0x54005400u), 0x54005400u, s, z)
+                 : dequant2(lop3_and_or(y, 0x000f000fu, 0x64006400u), 0x64006400u, s, z);
 }
 // the low / high two of four 8-bit codes
 template <int HIGH>
@@ -134,56 +134,90 @@ __device__ __forceinline__ uint32_t bytes(uint32_t x, __half2 s, __half2 z) {
   return dequant2(__byte_perm(x, 0x64646464u, HIGH ? 0x4342 : 0x4140), 0x64006400u, s, z);
 }
 
-// One 16-token record's scores: acc[m][n8 tile] += Q K^T.
+// Byte offsets inside a record that a lane reads from, fixed for the launch.
+template <int D, int FMT>
+struct LaneOffsets {
+  uint32_t k, v;    // key / value rows of its first token
+  uint32_t km, vm;  // their metadata
+  uint32_t km8, vm4;  // metadata of 8 / 4 tokens
+  __device__ __forceinline__ LaneOffsets(const PagesLayout& L, int lane) {
+    using F = Fmt<FMT>;
+    const int g = lane >> 2, t = lane & 3;
+    if constexpr (!F::kQuant) {
+      k = ((lane & 7) + ((lane >> 4) << 3)) * 128;
+      v = L.v_off + ((lane & 7) + (((lane >> 3) & 1) << 3)) * 128;
+      km = vm = km8 = vm4 = 0;
+    } else {
+      const int tok = (g >> 1) + 4 * (g & 1);
+      k = tok * (D * F::KB / 8) + t * (D / 4 * F::KB / 8);
+      v = L.v_off + t * (D * F::VB / 8) + g * (D / 8 * F::VB / 8);
+      km = L.km_off + (tok * (D >> L.k_lg) + ((t * (D / 4)) >> L.k_lg)) * 4;
+      vm = L.vm_off + (t * (D >> L.v_lg) + ((g * (D / 8)) >> L.v_lg)) * 4;
+      km8 = 8 * (D >> L.k_lg) * 4;
+      vm4 = 4 * (D >> L.v_lg) * 4;
+    }
+  }
+};
+
+// One 16-token record's scores: acc[m][n8 tile] += Q K^T.  sq: the query operands
+// in shared memory, [m][mma step][lane] of four words.
 template <int D, int FMT, int MT>
-__device__ __forceinline__ void rows_scores(uint32_t st, const PagesLayout& L, const uint32_t (*q)[D / 16][4], int lane,
-                                            float (*acc)[2][4]) {
+__device__ __forceinline__ void rows_scores(uint32_t st, const PagesLayout& L, const LaneOffsets<D, FMT>& lo,
+                                            uint32_t sq, int lane, float (*acc)[2][4]) {
   using F = Fmt<FMT>;
+  const uint32_t qa = sq + lane * 16;
   if constexpr (!F::kQuant) {
-    const int row = (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
-    const uint32_t base = st + row * 128;
+    const uint32_t base = st + lo.k, turn = (((lane >> 3) & 1) ^ (lane & 7)) << 4;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-      const int chunk = 2 * ks + ch;
       uint32_t b[4];
-      ldsm4(base + (chunk >> 3) * 2048 + (((chunk & 7) ^ (row & 7)) << 4), b);
+      ldsm4(base + (ks >> 2) * 2048 + (turn ^ ((2 * ks & 7) << 4)), b);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        mma16<F::kBf16>(acc[m][0], q[m][ks], b[0], b[1]);
-        mma16<F::kBf16>(acc[m][1], q[m][ks], b[2], b[3]);
+        uint32_t q[4];
+        ldsv<4>(qa + (m * (D / 16) + ks) * 512, q);
+        mma16<F::kBf16>(acc[m][0], q, b[0], b[1]);
+        mma16<F::kBf16>(acc[m][1], q, b[2], b[3]);
       }
     }
   } else {
     constexpr int SPAN = D / 4;               // channels a lane reads of a token
     constexpr int RUN = SPAN < 32 ? SPAN : 32;  // channels in one group at least
     constexpr int W = RUN * F::KB / 32;       // words of a run
-    const int g = lane >> 2, t = lane & 3;
-    const int tok = (g >> 1) + 4 * (g & 1);
+    const uint32_t row = st + lo.k, meta = st + lo.km;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t row = st + (8 * h + tok) * (D * F::KB / 8) + t * (SPAN * F::KB / 8);
-      const uint32_t meta = st + L.km_off + (8 * h + tok) * ((D >> L.k_lg) * 4);
+    for (int r = 0; r < SPAN / RUN; ++r) {
+      uint32_t w[2][W];
+      __half2 z[2], s[2];
 #pragma unroll
-      for (int r = 0; r < SPAN / RUN; ++r) {
-        const __half2 zs = as_h2(lds32(meta + ((t * SPAN + r * RUN) >> L.k_lg) * 4));
-        const __half2 z = __low2half2(zs), s = __high2half2(zs);
-        uint32_t w[W];
-        ldsv<W>(row + r * (RUN * F::KB / 8), w);
+      for (int h = 0; h < 2; ++h) {
+        // (a lane's run r starts at its span's start: the span is a whole number of groups, or inside one)
+        const __half2 zs = as_h2(lds32(meta + h * lo.km8 + (r ? ((r * RUN) >> L.k_lg) * 4 : 0)));
+        z[h] = __low2half2(zs), s[h] = __high2half2(zs);
+        ldsv<W>(row + h * (D * F::KB) + r * (RUN * F::KB / 8), w[h]);
+      }
 #pragma unroll
-        for (int i = 0; i < RUN / 4; ++i) {  // one mma step: 4 channels
-          uint32_t b0, b1;
+      for (int i = 0; i < RUN / 4; ++i) {  // one mma step: 4 channels
+        uint32_t b[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           if (F::KB == 8) {
-            b0 = bytes<0>(w[i], s, z);
-            b1 = bytes<1>(w[i], s, z);
+            b[h][0] = bytes<0>(w[h][i], s[h], z[h]);
+            b[h][1] = bytes<1>(w[h][i], s[h], z[h]);
           } else if (i & 1) {
-            b0 = nibbles<2>(w[i / 2], s, z);
-            b1 = nibbles<3>(w[i / 2], s, z);
+            b[h][0] = nibbles<2>(w[h][i / 2], s[h], z[h]);
+            b[h][1] = nibbles<3>(w[h][i / 2], s[h], z[h]);
           } else {
-            b0 = nibbles<0>(w[i / 2], s, z);
-            b1 = nibbles<1>(w[i / 2], s, z);
+            b[h][0] = nibbles<0>(w[h][i / 2], s[h], z[h]);
+            b[h][1] = nibbles<1>(w[h][i / 2], s[h], z[h]);
           }
+        }
 #pragma unroll
-          for (int m = 0; m < MT; ++m) mma16<false>(acc[m][h], q[m][r * (RUN / 4) + i], b0, b1);
+        for (int m = 0; m < MT; ++m) {
+          uint32_t q[4];
+          ldsv<4>(qa + (m * (D / 16) + r * (RUN / 4) + i) * 512, q);
+          mma16<false>(acc[m][0], q, b[0][0], b[0][1]);
+          mma16<false>(acc[m][1], q, b[1][0], b[1][1]);
         }
       }
     }
@@ -192,17 +226,15 @@ __device__ __forceinline__ void rows_scores(uint32_t st, const PagesLayout& L, c
 
 // o[m][n8 tile] += P V of one record; p: the probabilities as A operands.
 template <int D, int FMT, int MT>
-__device__ __forceinline__ void rows_values(uint32_t st, const PagesLayout& L, const uint32_t (*p)[4],
+__device__ __forceinline__ void rows_values(uint32_t st, const LaneOffsets<D, FMT>& lo, const uint32_t (*p)[4],
                                             const uint32_t (*rest)[4], int lane, float (*o)[D / 8][4]) {
   using F = Fmt<FMT>;
   if constexpr (!F::kQuant) {
-    const int row = (lane & 7) + (((lane >> 3) & 1) << 3), ch = lane >> 4;
-    const uint32_t base = st + L.v_off + row * 128;
+    const uint32_t base = st + lo.v, turn = ((lane >> 4) ^ (lane & 7)) << 4;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
-      const int chunk = 2 * j + ch;
       uint32_t b[4];
-      ldsm4t(base + (chunk >> 3) * 2048 + (((chunk & 7) ^ (row & 7)) << 4), b);
+      ldsm4t(base + (j >> 2) * 2048 + (turn ^ ((2 * j & 7) << 4)), b);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         mma16<F::kBf16>(o[m][2 * j], p[m], b[0], b[1]);
@@ -216,14 +248,12 @@ __device__ __forceinline__ void rows_values(uint32_t st, const PagesLayout& L, c
   } else {
     constexpr int RUN = D / 8;           // channels a lane reads of a token
     constexpr int W = RUN * F::VB / 32;  // words of them
-    const int g = lane >> 2, t = lane & 3;
     uint32_t w[4][W];
     __half2 zs[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int tok = t + 4 * j;
-      zs[j] = as_h2(lds32(st + L.vm_off + (tok * (D >> L.v_lg) + ((g * RUN) >> L.v_lg)) * 4));
-      ldsv<W>(st + L.v_off + tok * (D * F::VB / 8) + g * (RUN * F::VB / 8), w[j]);
+      zs[j] = as_h2(lds32(st + lo.vm + j * lo.vm4));
+      ldsv<W>(st + lo.v + j * (4 * D * F::VB / 8), w[j]);
     }
     __half2 z[2], s[2];
 #pragma unroll
@@ -274,64 +304,69 @@ __device__ __forceinline__ void rows_values(uint32_t st, const PagesLayout& L, c
   }
 }
 
-// The query rows as A operands, and what their scores are to be multiplied by.
-// Over codes q becomes fp16: a bf16 row is scaled by the power of two that puts
-// its largest magnitude in [2^14, 2^15), so that nothing overflows and its 8
-// significant bits survive down to 2^-28 of the largest.
-template <int D, int FMT, int MT>
-__device__ __forceinline__ void load_queries(const AttnArgs& a, const Piece& p, int lane, uint32_t (*q)[D / 16][4],
-                                             float (*sc)[2]) {
+// Row tile m of a piece's queries as A operands in shared memory (one warp), and
+// what its rows' scores are to be multiplied by.  Over codes q becomes fp16: a
+// bf16 row is scaled by the power of two that puts its largest magnitude in
+// [2^14, 2^15), so that nothing overflows and its 8 significant bits survive
+// down to 2^-28 of the largest.
+template <int D, int FMT>
+__device__ __forceinline__ void load_queries(const AttnArgs& a, const Piece& p, int m, int lane, uint32_t sq, float* sc) {
   using F = Fmt<FMT>;
   const int g = lane >> 2, t = lane & 3;
+  uint32_t q[D / 16][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int e = 0; e < 2; ++e) {
+    const int r = p.r0 + min(m * 16 + g + 8 * e, p.rows - 1);
+    const uint16_t* row = static_cast<const uint16_t*>(a.q) + (long)(p.s.s0 + r / a.rep) * a.q_stride +
+                          (long)(p.head * a.rep + r % a.rep) * D;
+    auto pair = [&](int c) -> uint32_t {
+      if (a.q_aligned) return *reinterpret_cast<const uint32_t*>(row + c);
+      return (uint32_t)row[c] | (uint32_t)row[c + 1] << 16;
+    };
+    float f = a.scale_log2;
+    if constexpr (!F::kQuant) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = p.r0 + min(m * 16 + g + 8 * e, p.rows - 1);
-      const uint16_t* row = static_cast<const uint16_t*>(a.q) + (long)(p.s.s0 + r / a.rep) * a.q_stride +
-                            (long)(p.head * a.rep + r % a.rep) * D;
-      auto pair = [&](int c) -> uint32_t {
-        if (a.q_aligned) return *reinterpret_cast<const uint32_t*>(row + c);
-        return (uint32_t)row[c] | (uint32_t)row[c + 1] << 16;
-      };
-      sc[m][e] = a.scale_log2;
-      if constexpr (!F::kQuant) {
+      for (int ks = 0; ks < D / 16; ++ks) {
+        q[ks][e] = pair(ks * 16 + 2 * t);
+        q[ks][2 + e] = pair(ks * 16 + 8 + 2 * t);
+      }
+    } else {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          q[m][ks][e] = pair(ks * 16 + 2 * t);
-          q[m][ks][2 + e] = pair(ks * 16 + 8 + 2 * t);
-        }
-      } else {
+      for (int ks = 0; ks < D / 16; ++ks) {
+        q[ks][e] = pair(t * (D / 4) + 4 * ks);
+        q[ks][2 + e] = pair(t * (D / 4) + 4 * ks + 2);
+      }
+      if (a.q_bf16) {
+        float mx = 0.0f;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          q[m][ks][e] = pair(t * (D / 4) + 4 * ks);
-          q[m][ks][2 + e] = pair(t * (D / 4) + 4 * ks + 2);
-        }
-        if (a.q_bf16) {
-          float mx = 0.0f;
+        for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w = q[ks][e + 2 * i];
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))));
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int E = norm_exp(mx);
+        // 2^E in two factors: E may pass the range of one float
+        const float f0 = exp2i(E / 2), f1 = exp2i(E - E / 2);
+        f = a.scale_log2 * exp2i(-(E / 2)) * exp2i(-(E - E / 2));
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t w = q[m][ks][e + 2 * i];
-              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))));
-            }
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const int E = norm_exp(mx);
-          // 2^E in two factors: E may pass the range of one float
-          const float f0 = exp2i(E / 2), f1 = exp2i(E - E / 2);
-          sc[m][e] = a.scale_log2 * exp2i(-(E / 2)) * exp2i(-(E - E / 2));
+        for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t w = q[m][ks][e + 2 * i];
-              q[m][ks][e + 2 * i] = pack2<false>(__uint_as_float(w << 16) * f0 * f1, __uint_as_float(w & 0xffff0000u) * f0 * f1);
-            }
-        }
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w = q[ks][e + 2 * i];
+            q[ks][e + 2 * i] = pack2<false>(__uint_as_float(w << 16) * f0 * f1, __uint_as_float(w & 0xffff0000u) * f0 * f1);
+          }
       }
     }
+    if (t == 0) sc[m * 16 + g + 8 * e] = f;
+  }
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks)
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(sq + (m * (D / 16) + ks) * 512 + lane * 16), "r"(q[ks][0]),
+                 "r"(q[ks][1]), "r"(q[ks][2]), "r"(q[ks][3])
+                 : "memory");
 }
 
 template <int D, int FMT, int MT>
@@ -342,15 +377,19 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
   extern __shared__ __align__(1024) char smem[];
   __shared__ Work<BK, ROWS> work;
   __shared__ Piece piece;
+  __shared__ float row_scale[ROWS];
+  __shared__ __align__(16) uint4 queries[MT * (D / 16) * 32];
   __shared__ __align__(8) uint64_t bars[kRowsWarps * NS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
   const int g = lane >> 2, t = lane & 3;
+  const LaneOffsets<D, FMT> offs(a.pv.L, lane);
+  const uint32_t sq = smem_u32(queries);
   const uint32_t ring = smem_u32(smem) + warp * NS * C::STAGE;
   const uint32_t bar = smem_u32(bars) + warp * NS * 8;
   if (lane < NS) mbar_init(bar + lane * 8, 1);
   fence_mbar_init();
   pdl_wait();
-  plan_work(a, &work);
+  plan_work(a, &work, reinterpret_cast<long*>(smem + C::SMEM));
   pdl_trigger();
   if (cta >= work.ctas) {
     if (threadIdx.x == 0) a.split[cta].parts = 0;
@@ -378,12 +417,13 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
 
     // Copies of a step into stage s: lane r % RECS brings record r % RECS, if it
     // holds a token of the sequence.  The first NS steps at once, RECS lanes each.
+    const PageRun run(a.pv, p.head);
     auto bring = [&](int tok, int page, int s) {
       const int rec = lane % RECS;
       const bool second = RECS == 2 && tok - rec * 16 + 16 < p.s.len;
       if (rec == 0) mbar_expect(bar + s * 8, second ? 2 * a.pv.L.tile_bytes : a.pv.L.tile_bytes);
       if (rec == 0 || second)
-        bulk_load(ring + s * C::STAGE + rec * C::REC, tile_addr(a, page, p.head, tok), a.pv.L.tile_bytes, bar + s * 8);
+        bulk_load(ring + s * C::STAGE + rec * C::REC, run.at(a, page, tok), a.pv.L.tile_bytes, bar + s * 8);
     };
     auto page_of = [&](int tok) { return tok < p.s.len ? page_index(a, p.b, tok) : 0; };
     if (lane < RECS * min(NS, nt - j) && alive) {
@@ -395,9 +435,9 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
     __syncwarp();
     int next = lane < RECS && j + NS < nt ? page_of(tok0 + BK * (j + NS) + lane * 16) : 0;
 
-    uint32_t q[MT][D / 16][4];
+    if (warp < MT) load_queries<D, FMT>(a, p, warp, lane, sq, row_scale);
+    __syncthreads();
     float sc[MT][2];
-    load_queries<D, FMT, MT>(a, p, lane, q, sc);
     float o[MT][D / 8][4], mx[MT][2], sum[MT][2];
     int pos[MT][2];
 #pragma unroll
@@ -410,6 +450,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
       for (int e = 0; e < 2; ++e) {
         mx[m][e] = -INFINITY;
         sum[m][e] = 0.0f;
+        sc[m][e] = row_scale[m * 16 + g + 8 * e];
         pos[m][e] = p.s.p0 + (p.r0 + min(m * 16 + g + 8 * e, p.rows - 1)) / a.rep;
       }
     }
@@ -452,7 +493,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[x][m][h][e] = 0.0f;
-        rows_scores<D, FMT, MT>(st + x * C::REC, a.pv.L, q, lane, acc[x]);
+        rows_scores<D, FMT, MT>(st + x * C::REC, a.pv.L, offs, sq, lane, acc[x]);
       }
       const bool edge = tok + STEP - 1 > pos_lo || (a.window > 0 && tok <= pos_hi - a.window);
       bool grow = false;
@@ -523,7 +564,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
               }
             }
           }
-        rows_values<D, FMT, MT>(st + x * C::REC, a.pv.L, pa, pr, lane, o);
+        rows_values<D, FMT, MT>(st + x * C::REC, offs, pa, pr, lane, o);
       }
       __syncwarp();
       if (lane < RECS && j + NS < nt) {
@@ -604,8 +645,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
 template <int D, int FMT>
 AttnKernel rows_kernel_fmt(int mt) {
   if constexpr (D <= 128)
-    if (mt == 2) return {(const void*)pages_rows_kernel<D, FMT, 2>, (size_t)RowsCfg<D, FMT, 2>::SMEM, kRowsWarps * 32, 0};
-  return {(const void*)pages_rows_kernel<D, FMT, 1>, (size_t)RowsCfg<D, FMT, 1>::SMEM, kRowsWarps * 32, 0};
+    if (mt == 2) return {(const void*)pages_rows_kernel<D, FMT, 2>, (size_t)RowsCfg<D, FMT, 2>::SMEM, kRowsWarps * 32, 0, 0};
+  return {(const void*)pages_rows_kernel<D, FMT, 1>, (size_t)RowsCfg<D, FMT, 1>::SMEM, kRowsWarps * 32, 0, 0};
 }
 template <int D>
 AttnKernel rows_kernel_dim(int fmt, int mt) {

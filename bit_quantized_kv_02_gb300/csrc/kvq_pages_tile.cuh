@@ -108,6 +108,7 @@ __device__ __forceinline__ void tile_loader(const AttnArgs& a, TileShared<D, FMT
     if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) break;
     const Piece p = sh->piece[slot];
     if (p.nblk == 0) break;
+    const PageRun run(a.pv, p.head);
     for (int j = 0; j < p.nblk; ++j, ++c) {
       const int st = (int)(c % C::NS), par = (int)((c / C::NS) & 1);
       const int tok0 = (p.blk + j) * C::BK;
@@ -117,7 +118,7 @@ __device__ __forceinline__ void tile_loader(const AttnArgs& a, TileShared<D, FMT
       const char* src = nullptr;
       if (rec < nt) {
         const int tok = tok0 + 16 * rec;
-        src = tile_addr(a, page_index(a, p.b, tok), p.head, tok) + cb * 2048;
+        src = run.at(a, page_index(a, p.b, tok), tok) + cb * 2048;
       }
       const uint32_t dst = cb * (C::BK * 128) + rec * 2048;
       ok = tile_wait_warp(sh, a, &sh->k_empty[st], par ^ 1);
@@ -169,15 +170,15 @@ struct RawTile {
 };
 
 template <int D, int BITS, int RUNS, int THREADS>
-__device__ __forceinline__ void fetch_raw(const AttnArgs& a, const Piece& p, int tok0, int off, int meta_off, int lg,
+__device__ __forceinline__ void fetch_raw(const AttnArgs& a, const PageRun& run, int len, int tok0, int off, int meta_off, int lg,
                                           int tid, const int* page, RawTile<BITS, RUNS>* r) {
   constexpr int PPT = D / 32;  // runs of a token
   const int piece = tid % PPT;
 #pragma unroll
   for (int i = 0; i < RUNS; ++i) {
     const int tok = tok0 + (i * THREADS + tid) / PPT;
-    if (tok < p.s.len) {
-      const char* rec = tile_addr(a, page[i], p.head, tok);
+    if (tok < len) {
+      const char* rec = run.at(a, page[i], tok);
       const char* src = rec + off + (tok & 15) * (D * BITS / 8) + piece * (4 * BITS);
 #pragma unroll
       for (int k = 0; k < BITS / 4; ++k) r->w[i][k] = reinterpret_cast<const uint4*>(src)[k];
@@ -257,6 +258,7 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
     const Piece p = sh->piece[slot];
     if (p.nblk == 0) break;
     const PagesLayout& L = a.pv.L;
+    const PageRun run(a.pv, p.head);
     RawTile<KB, RUNS> kr;
     RawTile<VB, RUNS> vr;
     int page[RUNS];
@@ -269,8 +271,8 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
     };
     int tok0 = p.blk * C::BK;
     find_pages(tok0);
-    fetch_raw<D, KB, RUNS, THREADS>(a, p, tok0, 0, L.km_off, L.k_lg, tid, page, &kr);
-    fetch_raw<D, VB, RUNS, THREADS>(a, p, tok0, L.v_off, L.vm_off, L.v_lg, tid, page, &vr);
+    fetch_raw<D, KB, RUNS, THREADS>(a, run, p.s.len, tok0, 0, L.km_off, L.k_lg, tid, page, &kr);
+    fetch_raw<D, VB, RUNS, THREADS>(a, run, p.s.len, tok0, L.v_off, L.vm_off, L.v_lg, tid, page, &vr);
     find_pages(tok0 + C::BK);
     for (int j = 0; j < p.nblk; ++j, ++c) {
       const int st = (int)(c % C::NS), par = (int)((c / C::NS) & 1);
@@ -281,7 +283,7 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh->k_full[st]));
       tok0 += C::BK;
-      if (j + 1 < p.nblk) fetch_raw<D, KB, RUNS, THREADS>(a, p, tok0, 0, L.km_off, L.k_lg, tid, page, &kr);
+      if (j + 1 < p.nblk) fetch_raw<D, KB, RUNS, THREADS>(a, run, p.s.len, tok0, 0, L.km_off, L.k_lg, tid, page, &kr);
       ok = tile_wait_warp(sh, a, &sh->v_empty[st], par ^ 1);
       if (!ok) break;
       store_raw<D, VB, RUNS, THREADS>(smem + C::V_OFF + st * C::TILE, tid, vr);
@@ -289,7 +291,7 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh->v_full[st]));
       if (j + 1 < p.nblk) {
-        fetch_raw<D, VB, RUNS, THREADS>(a, p, tok0, L.v_off, L.vm_off, L.v_lg, tid, page, &vr);
+        fetch_raw<D, VB, RUNS, THREADS>(a, run, p.s.len, tok0, L.v_off, L.vm_off, L.v_lg, tid, page, &vr);
         find_pages(tok0 + C::BK);
       }
     }
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
     fence_mbar_init();
   }
   pdl_wait();
-  plan_work(a, &sh.work);  // (its barriers also publish the initialisation above)
+  plan_work(a, &sh.work, reinterpret_cast<long*>(raw + C::SMEM));  // (its barriers also publish the initialisation above)
   pdl_trigger();
   if (threadIdx.x == 0) a.split[blockIdx.x].parts = 0;
   if ((int)blockIdx.x >= sh.work.ctas) return;
@@ -713,7 +715,7 @@ template <int D>
 AttnKernel tile_kernel_dim(int fmt) {
   switch (fmt) {
 #define KVQ_TILE(f) \
-  case f: return {(const void*)pages_tile_kernel<D, f>, (size_t)TileCfg<D, f>::SMEM, TileCfg<D, f>::THREADS, 1};
+  case f: return {(const void*)pages_tile_kernel<D, f>, (size_t)TileCfg<D, f>::SMEM, TileCfg<D, f>::THREADS, 0, 0};
     KVQ_TILE(kFmtF16)
     KVQ_TILE(kFmtBf16)
     KVQ_TILE(kFmt88)

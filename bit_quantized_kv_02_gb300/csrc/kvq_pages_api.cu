@@ -126,7 +126,8 @@ kvq_status valid_batch(kvq_pages* P, const kvq_pages_batch* b, BatchView* v) {
   if (!b) return fail(P, KVQ_ERR_INVALID_ARG, "no batch");
   if (b->batch < 1 || b->batch > kPagesMaxBatch) return fail(P, KVQ_ERR_INVALID_ARG, "batch out of range");
   if (b->new_tokens < 0 || b->max_new < 0) return fail(P, KVQ_ERR_INVALID_ARG, "negative count of new tokens");
-  if ((int64_t)b->new_tokens * P->cfg.q_heads > INT_MAX) return fail(P, KVQ_ERR_UNSUPPORTED, "too many new tokens");
+  if ((int64_t)b->new_tokens * P->cfg.q_heads > INT_MAX || (int64_t)b->new_tokens * P->cfg.kv_heads > INT_MAX)
+    return fail(P, KVQ_ERR_UNSUPPORTED, "too many new tokens");
   if (!b->q_start || !b->lens || !b->table) return fail(P, KVQ_ERR_INVALID_ARG, "null batch array");
   if (b->table_stride < 1 || b->table_stride > (1L << 30)) return fail(P, KVQ_ERR_INVALID_ARG, "table stride out of range");
   *v = {b->batch, b->new_tokens, b->q_start, b->lens, b->table, (long)b->table_stride};
@@ -313,6 +314,7 @@ kvq_status kvq_qk_norm_rope(const kvq_norm_rope_args* a, const kvq_rope* rope, v
   const int64_t qr = (int64_t)a->q_heads * a->head_dim, kr = (int64_t)a->kv_heads * a->head_dim;
   if (a->q_stride < qr || a->q_out_stride < qr || a->k_stride < kr || a->k_out_stride < kr) return KVQ_ERR_INVALID_ARG;
   if (a->tokens == 0 || (a->q_heads == 0 && a->kv_heads == 0)) return KVQ_OK;
+  if ((int64_t)a->tokens * ((int64_t)a->q_heads + a->kv_heads) > INT_MAX) return KVQ_ERR_UNSUPPORTED;
   if (a->q_heads && (!a->q || !a->q_out)) return KVQ_ERR_INVALID_ARG;
   if (a->kv_heads && (!a->k || !a->k_out)) return KVQ_ERR_INVALID_ARG;
   return launch_norm_rope(*a, rv, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;

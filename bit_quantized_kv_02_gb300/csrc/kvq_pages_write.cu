@@ -6,9 +6,13 @@
 // 8 neighbouring channels (16 bytes of a 16-bit row), head_dim / 8 lanes a row,
 // and a warp one token at a time, so a token's angles are loaded once for all
 // its heads and statistics (mean square, a group's minimum and maximum) are
-// shuffles between a row's lanes.  They are bound by HBM bytes for prompts and
-// by the launch and one chain of loads for single tokens, so a token's heads
-// spread over up to 8 warps when tokens are few.
+// shuffles between a row's lanes.  For prompts they are bound by HBM bytes and,
+// close behind, by issue slots: fp32 arithmetic goes two values an instruction
+// (head norm of 65521 tokens 255 -> 226 us with the packed mean square and the
+// approximate reciprocal root alone).  Prefetching the next token's rows, and
+// blocks of a single batch of rows, were both slower (287 and 290 us).  Single
+// tokens are bound by the launch and one chain of loads, so a token's heads
+// spread over up to 8 warps.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -137,7 +141,12 @@ __device__ __forceinline__ void turn8(const Turn& t, float* x) {
   }
   if (t.on) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], t.c[i]), __fmul_rn(p[i], t.s[i]));
+    for (int i = 0; i < 8; i += 2) {
+      // (the sums one by one: a packed one may be fused with the products)
+      const float2 y = mul2(make_float2(x[i], x[i + 1]), make_float2(t.c[i], t.c[i + 1]));
+      const float2 z = mul2(make_float2(p[i], p[i + 1]), make_float2(t.s[i], t.s[i + 1]));
+      x[i] = __fadd_rn(y.x, z.x), x[i + 1] = __fadd_rn(y.y, z.y);
+    }
   }
 }
 
@@ -152,19 +161,18 @@ struct NormArgs {
   float eps;
   int lg_wpt;       // log2 of the warps that share a token
   int aligned;      // every row may be moved 16 bytes at a time
+  int w_aligned;    // the weights too
 };
 
 template <typename T>
-__device__ __forceinline__ void load_weight(const void* w, int w_f32, int c0, float* x) {
+__device__ __forceinline__ void load_weight(const void* w, int w_f32, bool aligned, int c0, float* x) {
   if (!w) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = 1.0f;
   } else if (w_f32) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = static_cast<const float*>(w)[c0 + i];
+    unpack8(load8(static_cast<const float*>(w) + c0, aligned), x);
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_f<T>(static_cast<const T*>(w)[c0 + i]);
+    unpack8(load8(static_cast<const T*>(w) + c0, aligned), x);
   }
 }
 
@@ -188,14 +196,18 @@ __device__ __forceinline__ void norm_rows(const T* src, T* dst, int heads, int s
       float x[8];
       unpack8(r[u], x);
       if (norm) {
-        float ss = 0.0f;
+        float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+        for (int i = 0; i < 8; i += 2) s2 = fma2(make_float2(x[i], x[i + 1]), make_float2(x[i], x[i + 1]), s2);
+        float ss = s2.x + s2.y;
 #pragma unroll
         for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float inv = 1.0f / sqrtf(ss * (1.0f / D) + eps);
+        const float inv = rsqrtf(ss * (1.0f / D) + eps);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
+        for (int i = 0; i < 8; i += 2) {
+          const float2 y = mul2(mul2(make_float2(x[i], x[i + 1]), make_float2(inv, inv)), make_float2(w[i], w[i + 1]));
+          x[i] = y.x, x[i + 1] = y.y;
+        }
       }
       turn8(turn, x);
       if (bad) {
@@ -209,7 +221,7 @@ __device__ __forceinline__ void norm_rows(const T* src, T* dst, int heads, int s
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormArgs a, RopeView rv) {
+__global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(NormArgs a, RopeView rv) {
   constexpr int LPR = D / 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nsub = 1 << a.lg_wpt, sub = warp & (nsub - 1);
@@ -218,8 +230,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormArgs a, RopeVie
   pdl_trigger();
   float qw[8], kw[8];
   if (a.norm) {
-    load_weight<T>(a.q_heads ? a.qw : nullptr, a.w_f32, c0, qw);
-    load_weight<T>(a.kv_heads ? a.kw : nullptr, a.w_f32, c0, kw);
+    load_weight<T>(a.q_heads ? a.qw : nullptr, a.w_f32, a.w_aligned, c0, qw);
+    load_weight<T>(a.kv_heads ? a.kw : nullptr, a.w_f32, a.w_aligned, c0, kw);
   }
   const long step = (long)gridDim.x * (kRowWarps >> a.lg_wpt);
   for (long t = (long)blockIdx.x * (kRowWarps >> a.lg_wpt) + (warp >> a.lg_wpt); t < a.tokens; t += step) {
@@ -231,7 +243,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormArgs a, RopeVie
       norm_rows<T, D, U>(static_cast<const T*>(a.q) + t * a.qs, static_cast<T*>(a.q_out) + t * a.qos, a.q_heads, sub, nsub,
                          lane, a.norm, a.eps, qw, turn, bad, a.aligned);
     if (a.kv_heads)
-      norm_rows<T, D, 1>(static_cast<const T*>(a.k) + t * a.ks, static_cast<T*>(a.k_out) + t * a.kos, a.kv_heads, sub,
+      norm_rows<T, D, 2>(static_cast<const T*>(a.k) + t * a.ks, static_cast<T*>(a.k_out) + t * a.kos, a.kv_heads, sub,
                          nsub, lane, a.norm, a.eps, kw, turn, bad, a.aligned);
   }
 }
@@ -260,54 +272,37 @@ cudaError_t launch_norm_t(const kvq_norm_rope_args& x, const RopeView& rv, NormA
 
 // ------------------------------------------------------------------ append --
 
-// Where the new-token row t of the call goes: page, slot and angle row, or
-// page -1.  Found by the whole block for `count` rows from t0.
+// Where a new-token row of the call goes: page, slot and angle row, or page -1.
 struct Place {
   int page, slot, turn;
 };
 
+// Places of `count` rows from t0, by the whole block: every sequence's bounds and
+// length are read at once, and the thread whose sequence holds a row follows its
+// table entry, so a row costs two dependent loads whatever the batch is.
 __device__ __forceinline__ void find_places(const PagesView& pv, const BatchView& bv, const RopeView* rv, long t0,
-                                            int count, Place* place, int* first) {
-  if (threadIdx.x == 0) *first = 0;
-  if (t0 == 0) {  // one block looks the arrays over as attention does
-    for (int b = threadIdx.x; b < bv.batch; b += kThreads) {
-      bool bad;
-      (void)load_seq(pv, bv, b, &bad);
-      if (bad) atomicOr(pv.err, 1);
-    }
-  }
+                                            int count, Place* place) {
+  if (threadIdx.x < count) place[threadIdx.x] = {-1, 0, 0};
   __syncthreads();
-  // the sequence of row t0: sequences that end at or before it
-  int below = 0;
-  for (int i = threadIdx.x; i < bv.batch; i += kThreads) below += bv.q_start[i + 1] <= t0;
-  below = __reduce_add_sync(0xffffffffu, below);
-  if ((threadIdx.x & 31) == 0 && below) atomicAdd(first, below);
-  __syncthreads();
-  if (threadIdx.x < count) {
-    const long t = t0 + threadIdx.x;
-    int b = *first;
-    while (b < bv.batch && bv.q_start[b + 1] <= t) ++b;
-    Place p = {-1, 0, 0};
-    if (b < bv.batch && t < bv.new_tokens) {
-      const int s0 = bv.q_start[b], s1 = bv.q_start[b + 1], len = bv.lens[b];
-      bool bad = s0 < 0 || t < s0 || s1 > bv.new_tokens || len < 0;
-      const long pos = (long)len - s1 + t;
-      if (!bad && pos >= 0) {
-        const long e = pos >> pv.lg_pt;
-        bad = e >= bv.stride;
-        const int page = bad ? -1 : bv.table[b * bv.stride + e];
-        bad = bad || page < 0 || page >= pv.pages;
-        int turn = 0;
-        if (!bad && rv && rv->table) {
-          const long row = rv->positions ? rv->positions[t] : pos;
-          bad = row < 0 || row >= rv->rows;
-          turn = (int)row;
-        }
-        if (!bad) p = {page, (int)(pos & ((1 << pv.lg_pt) - 1)), turn};
+  for (int b = threadIdx.x; b < bv.batch; b += kThreads) {
+    bool bad;
+    const Seq s = load_seq(pv, bv, b, &bad);
+    bad = bad && t0 == 0;  // (one block reports the arrays)
+    const long lo = max(t0, (long)s.s0), hi = min(t0 + count, (long)s.s0 + s.n);
+    for (long t = lo; t < hi; ++t) {
+      const long pos = s.p0 + (t - s.s0);
+      if (pos < 0) continue;
+      const int page = bv.table[b * bv.stride + (pos >> pv.lg_pt)];
+      bool ok = (unsigned)page < (unsigned)pv.pages;
+      long turn = 0;
+      if (rv && rv->table) {
+        turn = rv->positions ? rv->positions[t] : pos;
+        ok = ok && turn >= 0 && turn < rv->rows;
       }
-      if (bad) atomicOr(pv.err, 1);
+      if (ok) place[t - t0] = {page, (int)(pos & ((1 << pv.lg_pt) - 1)), (int)turn};
+      bad = bad || !ok;
     }
-    place[threadIdx.x] = p;
+    if (bad) atomicOr(pv.err, 1);
   }
   __syncthreads();
 }
@@ -364,10 +359,9 @@ struct AppendRows {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) pages_append_kernel(PagesView pv, BatchView bv, RopeView rv, AppendRows a) {
+__global__ void __launch_bounds__(kThreads, 4) pages_append_kernel(PagesView pv, BatchView bv, RopeView rv, AppendRows a) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
   __shared__ Place place[kRowWarps];
-  __shared__ int first;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nsub = 1 << a.lg_wpt, sub = warp & (nsub - 1), tpb = kRowWarps >> a.lg_wpt;
   const int rg = lane / LPR, c0 = (lane % LPR) * 8, H = pv.heads;
@@ -375,7 +369,7 @@ __global__ void __launch_bounds__(kThreads) pages_append_kernel(PagesView pv, Ba
   pdl_trigger();
   for (long t0 = (long)blockIdx.x * tpb; t0 < bv.new_tokens; t0 += (long)gridDim.x * tpb) {
     __syncthreads();
-    find_places(pv, bv, &rv, t0, tpb, place, &first);
+    find_places(pv, bv, &rv, t0, tpb, place);
     const Place p = place[warp >> a.lg_wpt];
     if (p.page < 0) continue;
     const long t = t0 + (warp >> a.lg_wpt);
@@ -443,7 +437,6 @@ __global__ void __launch_bounds__(kThreads) pages_read_kernel(PagesView pv, Batc
                                                               int lg_wpt) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
   __shared__ Place place[kRowWarps];
-  __shared__ int first;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nsub = 1 << lg_wpt, sub = warp & (nsub - 1), tpb = kRowWarps >> lg_wpt;
   const int rg = lane / LPR, c0 = (lane % LPR) * 8, H = pv.heads;
@@ -451,7 +444,7 @@ __global__ void __launch_bounds__(kThreads) pages_read_kernel(PagesView pv, Batc
   pdl_trigger();
   for (long t0 = (long)blockIdx.x * tpb; t0 < bv.new_tokens; t0 += (long)gridDim.x * tpb) {
     __syncthreads();
-    find_places(pv, bv, nullptr, t0, tpb, place, &first);
+    find_places(pv, bv, nullptr, t0, tpb, place);
     const Place p = place[warp >> lg_wpt];
     if (p.page < 0) continue;
     const long row = (t0 + (warp >> lg_wpt)) * H;
@@ -493,6 +486,7 @@ cudaError_t launch_norm_rope(const kvq_norm_rope_args& x, const RopeView& rv, cu
   a.w_f32 = x.weight_dtype == KVQ_F32;
   a.aligned = (!x.q_heads || (aligned16(x.q) && aligned16(x.q_out) && x.q_stride % per == 0 && x.q_out_stride % per == 0)) &&
               (!x.kv_heads || (aligned16(x.k) && aligned16(x.k_out) && x.k_stride % per == 0 && x.k_out_stride % per == 0));
+  a.w_aligned = aligned16(x.q_weight) && aligned16(x.k_weight);
   if (x.dtype == KVQ_F32) return launch_norm_t<float>(x, rv, a, st);
   if (x.dtype == KVQ_BF16) return launch_norm_t<__nv_bfloat16>(x, rv, a, st);
   return launch_norm_t<__half>(x, rv, a, st);

@@ -407,32 +407,33 @@ def _ints(t, name, device=None):
     return t
 
 
-def _rows(t, name, heads, head_dim, device):
-    """[tokens][heads][head_dim] with heads and channels packed; returns the stride between tokens."""
-    _need(isinstance(t, torch.Tensor) and t.dim() == 3 and tuple(t.shape[1:]) == (heads, head_dim),
-          f"{name}: [tokens][{heads}][{head_dim}]")
-    _need(t.device == device, f"{name}: on another device")
-    _need(t.stride(2) == 1 and (heads == 1 or t.stride(1) == head_dim), f"{name}: heads and channels not contiguous")
-    return max(t.stride(0), heads * head_dim) if t.shape[0] < 2 else t.stride(0)
+def _row_stride(t, name, heads, head_dim, index):
+    """Stride between tokens of [tokens][heads][head_dim] with heads and channels packed, on device `index`."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
+        raise ValueError(f"{name}: [tokens][{heads}][{head_dim}]")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on another device")
+    if stride[2] != 1 or (stride[1] != head_dim and heads != 1):
+        raise ValueError(f"{name}: heads and channels not contiguous")
+    return stride[0] if shape[0] > 1 else heads * head_dim
 
 
-class _On:
-    """Makes a tensor's device current where it is not, and gives its stream."""
+# the current stream's handle without the stream object around it, where torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, device, stream):
-        self.device, self.stream = device, stream
-        self.guard = None
 
-    def __enter__(self):
-        if torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
-        return ctypes.c_void_p(s.cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+
+def _on_device(index, stream, call, *args):
+    """call(*args, stream handle) with device `index` current."""
+    handle = stream.cuda_stream if stream is not None else _raw_stream(index)
+    if _current_device() == index:
+        return call(*args, handle)
+    with torch.cuda.device(index):
+        return call(*args, handle)
 
 
 class PagesBatch:
@@ -451,7 +452,7 @@ class PagesBatch:
         _need(table.dim() == 2 and table.shape[0] == lens.shape[0] and table.shape[1] > 0, "table: [batch][pages]")
         _need(q_start.is_contiguous() and lens.is_contiguous() and table.is_contiguous(), "batch arrays are contiguous")
         self.q_start, self.lens, self.table = q_start, lens, table
-        self.device = q_start.device
+        self.index = q_start.get_device()
         self.new_tokens = int(new_tokens)
         self.c = _PagesBatch(lens.shape[0], self.new_tokens, int(max_new), q_start.data_ptr(), lens.data_ptr(),
                              table.data_ptr(), table.shape[1])
@@ -471,10 +472,34 @@ class Rope:
             _ints(positions, "positions", table.device)
             _need(positions.dim() == 1 and positions.is_contiguous(), "positions: one a token, contiguous")
         self.table, self.positions = table, positions
-        self.device = table.device
+        self.index = table.get_device()
+        self.rows_given = positions.shape[0] if positions is not None else 0
         self.c = _Rope(table.data_ptr(), table.shape[0], 2 * table.shape[1], int(style),
                        positions.data_ptr() if positions is not None else None)
         self.ref = ctypes.byref(self.c)
+
+
+def _norm_side(x, out, w, name, tokens, head_dim, dtype, index):
+    """(out, heads, pointers, strides and weight) of one of kvq_qk_norm_rope's two sides."""
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != tokens or x.dtype is not dtype:
+        raise ValueError(f"{name}: queries and keys of the same tokens, type and head_dim")
+    heads = shape[1]
+    stride = _row_stride(x, name, heads, head_dim, index)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+        out_stride = heads * head_dim
+    else:
+        out_stride = _row_stride(out, name + "_out", heads, head_dim, index)
+        if out.shape[0] != tokens or out.dtype is not dtype:
+            raise ValueError(f"{name}_out: of {name}'s shape and type")
+    if w is None:
+        return out, heads, x.data_ptr(), stride, out.data_ptr(), out_stride, None
+    if w.dim() != 1 or w.numel() != head_dim or w.get_device() != index or w.stride(0) != 1:
+        raise ValueError(f"{name}_weight: [{head_dim}], contiguous, on {name}'s device")
+    if w.dtype is not dtype and w.dtype is not torch.float32:
+        raise ValueError(f"{name}_weight: {dtype} or fp32")
+    return out, heads, x.data_ptr(), stride, out.data_ptr(), out_stride, w.data_ptr()
 
 
 def kvq_qk_norm_rope(q, k, q_weight=None, k_weight=None, eps: float = 1e-6, rope: Rope | None = None, q_out=None,
@@ -487,45 +512,38 @@ def kvq_qk_norm_rope(q, k, q_weight=None, k_weight=None, eps: float = 1e-6, rope
     rotates.  Returns (q_out, k_out), new tensors unless given (q and k themselves
     work)."""
     one = q if q is not None else k
-    _need(isinstance(one, torch.Tensor) and one.is_cuda and one.dim() == 3, "q: [tokens][heads][head_dim] on the GPU")
-    _need(one.dtype in _DTYPES, f"unsupported dtype {one.dtype}")
-    tokens, d, dev = one.shape[0], one.shape[2], one.device
-    a = _NormRopeArgs(tokens=tokens, head_dim=d, dtype=_DTYPES[one.dtype], norm=int(bool(norm)), eps=float(eps),
-                      weight_dtype=_DTYPES[one.dtype])
-    outs = []
-    for name, x, out, w in (("q", q, q_out, q_weight), ("k", k, k_out, k_weight)):
-        if x is None:
-            outs.append(None)
-            continue
-        _need(isinstance(x, torch.Tensor) and x.dim() == 3, f"{name}: [tokens][heads][head_dim]")
-        heads = x.shape[1]
-        stride = _rows(x, name, heads, d, dev)
-        if out is None:
-            out = torch.empty((tokens, heads, d), dtype=x.dtype, device=dev)
-        out_stride = _rows(out, name + "_out", heads, d, dev)
-        _need(x.dtype == one.dtype and out.dtype == one.dtype, f"{name}: all rows have one type")
-        _need(x.shape[0] == tokens and out.shape[0] == tokens, f"{name}: all rows are of the same tokens")
-        if name == "q":
-            a.q_heads, a.q, a.q_stride, a.q_out, a.q_out_stride = heads, x.data_ptr(), stride, out.data_ptr(), out_stride
-        else:
-            a.kv_heads, a.k, a.k_stride, a.k_out, a.k_out_stride = heads, x.data_ptr(), stride, out.data_ptr(), out_stride
-        outs.append(out)
-        if w is not None:
-            _need(w.shape == (d,) and w.is_contiguous() and w.device == dev, f"{name}_weight: [{d}]")
-            _need(w.dtype in (one.dtype, torch.float32), f"{name}_weight: {one.dtype} or fp32")
-            a.weight_dtype = _DTYPES[w.dtype]
-            if name == "q":
-                a.q_weight = w.data_ptr()
-            else:
-                a.k_weight = w.data_ptr()
-    if q_weight is not None and k_weight is not None and q is not None and k is not None:
-        _need(q_weight.dtype == k_weight.dtype, "both weights have one type")
+    if not isinstance(one, torch.Tensor) or not one.is_cuda or one.dim() != 3:
+        raise ValueError("q, k: [tokens][heads][head_dim] on the GPU")
+    dtype = one.dtype
+    code = weight_code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype} (fp16, bf16 or fp32)")
+    tokens, _, d = one.shape
+    index = one.get_device()
+    qo = ko = qp = kp = qop = kop = qw = kw = ref = None
+    qh = kh = qs = ks = qos = kos = 0
+    if q is not None:
+        qo, qh, qp, qs, qop, qos, qw = _norm_side(q, q_out, q_weight, "q", tokens, d, dtype, index)
+    if k is not None:
+        ko, kh, kp, ks, kop, kos, kw = _norm_side(k, k_out, k_weight, "k", tokens, d, dtype, index)
+    if qw is not None:
+        weight_code = _DTYPES[q_weight.dtype]
+        if kw is not None and k_weight.dtype is not q_weight.dtype:
+            raise ValueError("both weights have one type")
+    elif kw is not None:
+        weight_code = _DTYPES[k_weight.dtype]
     if rope is not None:
-        _need(rope.device == dev, "rope: on another device")
-        _need(rope.positions is not None and rope.positions.shape[0] >= tokens, "rope: a position for every token")
-    with _On(dev, stream) as st:
-        _check(lib().kvq_qk_norm_rope(ctypes.byref(a), rope.ref if rope is not None else None, st), "kvq_qk_norm_rope")
-    return outs[0], outs[1]
+        ref = rope.ref
+        if rope.index != index:
+            raise ValueError("rope: on another device")
+        if rope.positions is None or rope.rows_given < tokens:
+            raise ValueError("rope: a position for every token")
+    a = _NormRopeArgs(tokens, qh, kh, d, code, qp, kp, qs, ks, qop, kop, qos, kos, 1 if norm else 0, eps, qw, kw,
+                      weight_code)
+    st = _on_device(index, stream, (_lib or lib()).kvq_qk_norm_rope, ctypes.byref(a), ref)
+    if st:
+        raise KVQError(st, "kvq_qk_norm_rope")
+    return qo, ko
 
 
 class KVQPages:
@@ -535,12 +553,13 @@ class KVQPages:
         self.cfg = cfg
         self.bytes = kvq_pages_bytes(cfg)
         self.buffer = torch.empty(self.bytes.alloc, dtype=torch.uint8, device=device)
-        self.device = self.buffer.device
+        self.device, self.index = self.buffer.device, self.buffer.get_device()
         self.dtype = torch.bfloat16 if cfg.dtype == BF16 else torch.float16
+        self._kv, self._q = (cfg.kv_heads, cfg.head_dim), (cfg.q_heads, cfg.head_dim)
+        self._lib = lib()
         h = ctypes.c_void_p()
-        with _On(self.device, stream) as st:
-            _check(lib().kvq_pages_create(ctypes.byref(cfg), _ptr(self.buffer), self.bytes.alloc, st, ctypes.byref(h)),
-                   "kvq_pages_create")
+        _check(_on_device(self.index, stream, lambda s: self._lib.kvq_pages_create(
+            ctypes.byref(cfg), _ptr(self.buffer), self.bytes.alloc, s, ctypes.byref(h))), "kvq_pages_create")
         self.handle = h
 
     def close(self):
@@ -555,25 +574,32 @@ class KVQPages:
             pass
 
     def _fail(self, st, what):
-        raise KVQError(st, what, (lib().kvq_pages_last_error(self.handle) or b"").decode())
+        raise KVQError(st, what, (self._lib.kvq_pages_last_error(self.handle) or b"").decode())
 
     # C-named methods ---------------------------------------------------------
     def kvq_pages_append(self, layer: int, k: torch.Tensor, v: torch.Tensor, batch: PagesBatch,
                          rope: Rope | None = None, stream=None):
         """Store the new tokens of `batch`: k, v [new_tokens][kv_heads][head_dim]
         fp16, bf16 or fp32; the keys are turned by `rope` on the way."""
-        c = self.cfg
-        ks = _rows(k, "k", c.kv_heads, c.head_dim, self.device)
-        vs = _rows(v, "v", c.kv_heads, c.head_dim, self.device)
-        _need(k.dtype in _DTYPES and k.dtype == v.dtype, "k, v: both fp16, bf16 or fp32")
-        _need(k.shape[0] >= batch.new_tokens and v.shape[0] >= batch.new_tokens, "k, v: fewer rows than new tokens")
-        _need(batch.device == self.device, "batch: on another device")
+        index, n, dtype = self.index, batch.new_tokens, k.dtype
+        ks = _row_stride(k, "k", *self._kv, index)
+        vs = _row_stride(v, "v", *self._kv, index)
+        code = _DTYPES.get(dtype)
+        if code is None or v.dtype != dtype:
+            raise ValueError("k, v: both fp16, bf16 or fp32")
+        if k.shape[0] < n or v.shape[0] < n:
+            raise ValueError("k, v: fewer rows than new tokens")
+        if batch.index != index:
+            raise ValueError("batch: on another device")
+        ref = None
         if rope is not None:
-            _need(rope.device == self.device, "rope: on another device")
-            _need(rope.positions is None or rope.positions.shape[0] >= batch.new_tokens, "rope: fewer positions than new tokens")
-        with _On(self.device, stream) as st:
-            r = lib().kvq_pages_append(self.handle, layer, k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], ks, vs,
-                                       batch.ref, rope.ref if rope is not None else None, st)
+            ref = rope.ref
+            if rope.index != index:
+                raise ValueError("rope: on another device")
+            if rope.positions is not None and rope.rows_given < n:
+                raise ValueError("rope: fewer positions than new tokens")
+        r = _on_device(index, stream, self._lib.kvq_pages_append, self.handle, layer, k.data_ptr(), v.data_ptr(), code, ks,
+                       vs, batch.ref, ref)
         if r:
             self._fail(r, "kvq_pages_append")
 
@@ -582,18 +608,24 @@ class KVQPages:
         """Attention of the new tokens of `batch` over the pages: q [new_tokens][q_heads]
         [head_dim] fp16 or bf16; returns out of the same shape and type (rows behind
         the last sequence are left as they were; zeros in a new tensor)."""
-        c = self.cfg
-        qs = _rows(q, "q", c.q_heads, c.head_dim, self.device)
-        _need(q.dtype in (torch.float16, torch.bfloat16), "q: fp16 or bf16")
-        _need(q.shape[0] >= batch.new_tokens, "q: fewer rows than new tokens")
-        _need(batch.device == self.device, "batch: on another device")
-        with _On(self.device, stream) as st:
-            if out is None:
-                out = torch.zeros(q.shape, dtype=q.dtype, device=self.device)
-            _need(out.shape == q.shape and out.dtype == q.dtype and out.device == self.device and out.is_contiguous(),
-                  "out: contiguous, of q's shape and type")
-            r = lib().kvq_pages_attn(self.handle, layer, q.data_ptr(), _DTYPES[q.dtype], qs, batch.ref, float(scale),
-                                     int(window), out.data_ptr(), st)
+        index, dtype = self.index, q.dtype
+        qs = _row_stride(q, "q", *self._q, index)
+        if dtype != torch.float16 and dtype != torch.bfloat16:
+            raise ValueError("q: fp16 or bf16")
+        if q.shape[0] < batch.new_tokens:
+            raise ValueError("q: fewer rows than new tokens")
+        if batch.index != index:
+            raise ValueError("batch: on another device")
+        if out is None:
+            if stream is None:
+                out = torch.zeros(q.shape, dtype=dtype, device=q.device)
+            else:
+                with torch.cuda.stream(stream):
+                    out = torch.zeros(q.shape, dtype=dtype, device=q.device)
+        elif out.shape != q.shape or out.dtype != dtype or out.get_device() != index or not out.is_contiguous():
+            raise ValueError("out: contiguous, of q's shape and type")
+        r = _on_device(index, stream, self._lib.kvq_pages_attn, self.handle, layer, q.data_ptr(), _DTYPES[dtype], qs,
+                       batch.ref, scale, window, out.data_ptr())
         if r:
             self._fail(r, "kvq_pages_attn")
         return out
@@ -603,26 +635,27 @@ class KVQPages:
         """What the pages hold for the new tokens of `batch`: (k, v), each [new_tokens]
         [kv_heads][head_dim] of the pages' type (fp16 for quantized pages); rows
         without a place are left as they were."""
-        c = self.cfg
-        shape = (batch.new_tokens, c.kv_heads, c.head_dim)
-        _need(batch.device == self.device, "batch: on another device")
-        with _On(self.device, stream) as st:
-            if k_out is None:
-                k_out = torch.empty(shape, dtype=self.dtype, device=self.device)
-            if v_out is None:
-                v_out = torch.empty(shape, dtype=self.dtype, device=self.device)
-            for x in (k_out, v_out):
-                _need(tuple(x.shape) == shape and x.dtype == self.dtype and x.device == self.device and x.is_contiguous(),
-                      "k_out, v_out: contiguous [new_tokens][kv_heads][head_dim] of the pages' type")
-            r = lib().kvq_pages_read(self.handle, layer, batch.ref, k_out.data_ptr(), v_out.data_ptr(), st)
+        index = self.index
+        shape = (batch.new_tokens, *self._kv)
+        if batch.index != index:
+            raise ValueError("batch: on another device")
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=self.dtype, device=self.device)
+        elif k_out.shape != shape or k_out.dtype != self.dtype or k_out.get_device() != index or not k_out.is_contiguous():
+            raise ValueError("k_out: contiguous [new_tokens][kv_heads][head_dim] of the pages' type")
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=self.dtype, device=self.device)
+        elif v_out.shape != shape or v_out.dtype != self.dtype or v_out.get_device() != index or not v_out.is_contiguous():
+            raise ValueError("v_out: contiguous [new_tokens][kv_heads][head_dim] of the pages' type")
+        r = _on_device(index, stream, self._lib.kvq_pages_read, self.handle, layer, batch.ref, k_out.data_ptr(),
+                       v_out.data_ptr())
         if r:
             self._fail(r, "kvq_pages_read")
         return k_out, v_out
 
     def kvq_pages_set_kernel(self, which: int):
         """0: by the rows of each sequence (default); 1: the few-rows kernel; 2: the many-rows kernel."""
-        _check(lib().kvq_pages_set_kernel(self.handle, int(which)), "kvq_pages_set_kernel")
+        _check(self._lib.kvq_pages_set_kernel(self.handle, int(which)), "kvq_pages_set_kernel")
 
     def kvq_pages_status(self, stream=None) -> int:
-        with _On(self.device, stream) as st:
-            return lib().kvq_pages_status(self.handle, st)
+        return _on_device(self.index, stream, self._lib.kvq_pages_status, self.handle)

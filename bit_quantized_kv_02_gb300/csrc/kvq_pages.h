@@ -88,6 +88,7 @@ struct AttnArgs {
   long q_stride;
   float scale_log2;  // softmax scale * log2(e)
   int window, rep, q_heads;
+  uint32_t rep_magic;  // ceil(2^16 / rep): n / rep == n * rep_magic >> 16 for n < 1024 and rep <= 64
   int q_bf16;        // type of q and out: 0 fp16, 1 bf16
   int q_aligned;     // rows of q may be read 16 bytes at a time
   int rows_lo, rows_hi;  // sequences with rows_lo < n * rep <= rows_hi are this launch's

@@ -272,6 +272,7 @@ kvq_status kvq_pages_attn(kvq_pages_t P, int layer, const void* q, int q_dtype, 
   a.scale_log2 = softmax_scale * 1.44269504088896340736f;
   a.window = window;
   a.rep = c.q_heads / c.kv_heads;
+  a.rep_magic = (65536 + a.rep - 1) / a.rep;
   a.q_heads = c.q_heads;
   a.q_bf16 = q_dtype == KVQ_BF16;
   a.q_aligned = (reinterpret_cast<uintptr_t>(q) & 15) == 0 && q_stride % 8 == 0;

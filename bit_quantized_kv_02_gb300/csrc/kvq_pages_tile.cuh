@@ -43,6 +43,7 @@ struct TileCfg {
   static constexpr int PROD = F::kQuant ? (NT == 1 ? 8 : 4) : 1;  // warps that fill K and V stages
   static constexpr int THREADS = F::kQuant ? 512 : 384;
   static constexpr int PIECES = 4;
+  static constexpr bool kOnePass = !F::kQuant;  // (needs the registers of the smaller block)
 };
 
 template <int D, int FMT>
@@ -75,6 +76,47 @@ __device__ __forceinline__ bool tile_wait(SH* sh, const AttnArgs& a, uint64_t* b
 template <typename SH>
 __device__ __forceinline__ bool tile_wait_warp(SH* sh, const AttnArgs& a, uint64_t* bar, int parity) {
   return __all_sync(0xffffffffu, tile_wait(sh, a, bar, parity));
+}
+
+// Query rows of a piece: row r is token t0 + (rem + r) / rep of the call's rows,
+// head of the group (rem + r) % rep.
+struct RowMap {
+  int t0, rem, rep, head0, p0;
+  uint32_t magic;
+  __device__ __forceinline__ RowMap(const AttnArgs& a, const Piece& p) {
+    const int t = p.r0 / a.rep;
+    t0 = p.s.s0 + t;
+    p0 = p.s.p0 + t;
+    rem = p.r0 - t * a.rep;
+    rep = a.rep;
+    magic = a.rep_magic;
+    head0 = p.head * a.rep;
+  }
+  __device__ __forceinline__ int token(int r) const { return (int)(((rem + r) * magic) >> 16); }
+  __device__ __forceinline__ int position(int r) const { return p0 + token(r); }
+  // first element of the row in a tensor with `stride` elements a token
+  __device__ __forceinline__ long at(int r, long stride, int D) const {
+    const int t = token(r);
+    return (long)(t0 + t) * stride + (long)(head0 + rem + r - t * rep) * D;
+  }
+};
+
+// Blocks [lo, hi) of a piece that a row tile sees any token of.  (One tile: all
+// of them, the double-buffered scores count on it.)
+template <int D, int FMT>
+__device__ __forceinline__ void tile_range(const AttnArgs& a, const Piece& p, int tile, int* lo, int* hi) {
+  using C = TileCfg<D, FMT>;
+  *lo = 0;
+  *hi = p.nblk;
+  if (C::NT == 1) return;
+  if (tile * 128 >= p.rows) {
+    *hi = 0;
+    return;
+  }
+  const RowMap rm(a, p);
+  const int first = rm.position(tile * 128), last = rm.position(min(tile * 128 + 127, p.rows - 1));
+  *hi = min(max((last < 0 ? 0 : last / C::BK + 1) - p.blk, 0), p.nblk);
+  if (a.window > 0) *lo = min(max((int)(max((long)first - a.window + 1, 0L) / C::BK) - p.blk, 0), *hi);
 }
 
 // ------------------------------------------------------------------ loader --
@@ -144,17 +186,18 @@ __device__ __forceinline__ void tile_loader(const AttnArgs& a, TileShared<D, FMT
 
 // ------------------------------------------------------------- dequantizer --
 
-// A thread turns RUNS runs of 32 channels of one token into four 16-byte chunks
-// each.  Codes and metadata are fetched a block ahead, page indices too.
+// Half of the warps turn keys, half values.  A thread turns runs of 32 channels
+// of one token into four 16-byte chunks each; the runs of half a block are
+// fetched while those of the half before are turned.
 template <int BITS, int RUNS>
-struct RawTile {
+struct RawRuns {
   uint4 w[RUNS][BITS / 4];  // 16 bytes of 4-bit codes, 32 bytes of 8-bit codes
   uint32_t zs[RUNS];
 };
 
 template <int D, int BITS, int RUNS, int THREADS>
-__device__ __forceinline__ void fetch_raw(const AttnArgs& a, const PageRun& run, int len, int tok0, int off, int meta_off, int lg,
-                                          int tid, const int* page, RawTile<BITS, RUNS>* r) {
+__device__ __forceinline__ void fetch_runs(const AttnArgs& a, const PageRun& run, int len, int tok0, int off, int meta_off,
+                                           int lg, int tid, const int* page, RawRuns<BITS, RUNS>* r) {
   constexpr int PPT = D / 32;  // runs of a token
   const int piece = tid % PPT;
 #pragma unroll
@@ -175,7 +218,7 @@ __device__ __forceinline__ void fetch_raw(const AttnArgs& a, const PageRun& run,
 }
 
 template <int D, int BITS, int RUNS, int THREADS>
-__device__ __forceinline__ void store_raw(uint32_t tile, int tid, const RawTile<BITS, RUNS>& r) {
+__device__ __forceinline__ void store_runs(uint32_t tile, int first, int tid, const RawRuns<BITS, RUNS>& r) {
   constexpr int PPT = D / 32;
   const int piece = tid % PPT;
   // lanes of other column blocks store their four chunks in another order, so
@@ -183,7 +226,7 @@ __device__ __forceinline__ void store_raw(uint32_t tile, int tid, const RawTile<
   const int turn = D == 64 ? 0 : (D == 128 ? 2 * (piece >> 1) : piece >> 1);
 #pragma unroll
   for (int i = 0; i < RUNS; ++i) {
-    const int t = (i * THREADS + tid) / PPT;
+    const int t = first + (i * THREADS + tid) / PPT;
     const __half2 z = __low2half2(as_h2(r.zs[i])), s = __high2half2(as_h2(r.zs[i]));
     const uint32_t row = tile + (piece >> 1) * (128 * 128) + t * 128;
     constexpr int WC = BITS / 4;  // words of a chunk
@@ -201,49 +244,46 @@ __device__ __forceinline__ void store_raw(uint32_t tile, int tid, const RawTile<
             w[WC * k + e] = (turn & b) ? y : x;
             w[WC * (k ^ b) + e] = (turn & b) ? x : y;
           }
-    uint32_t y[16];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
+      uint32_t y[4];
       if constexpr (BITS == 8) {
-        y[4 * k] = bytes<0>(w[2 * k], s, z);
-        y[4 * k + 1] = bytes<1>(w[2 * k], s, z);
-        y[4 * k + 2] = bytes<0>(w[2 * k + 1], s, z);
-        y[4 * k + 3] = bytes<1>(w[2 * k + 1], s, z);
+        y[0] = bytes<0>(w[2 * k], s, z);
+        y[1] = bytes<1>(w[2 * k], s, z);
+        y[2] = bytes<0>(w[2 * k + 1], s, z);
+        y[3] = bytes<1>(w[2 * k + 1], s, z);
       } else {
-        y[4 * k] = nibbles<0>(w[k], s, z);
-        y[4 * k + 1] = nibbles<1>(w[k], s, z);
-        y[4 * k + 2] = nibbles<2>(w[k], s, z);
-        y[4 * k + 3] = nibbles<3>(w[k], s, z);
+        y[0] = nibbles<0>(w[k], s, z);
+        y[1] = nibbles<1>(w[k], s, z);
+        y[2] = nibbles<2>(w[k], s, z);
+        y[3] = nibbles<3>(w[k], s, z);
       }
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
       const int c = (4 * (piece & 1) + (k ^ turn)) ^ (t & 7);
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(row + (c << 4)), "r"(y[4 * k]), "r"(y[4 * k + 1]),
-                   "r"(y[4 * k + 2]), "r"(y[4 * k + 3])
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(row + (c << 4)), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
                    : "memory");
     }
   }
 }
 
-template <int D, int FMT>
+// Keys (VALUE 0) or values (1) of all pieces; tid: thread among those of the tensor.
+template <int D, int FMT, int VALUE>
 __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int tid) {
   using C = TileCfg<D, FMT>;
   using F = typename C::F;
-  constexpr int THREADS = 32 * C::PROD, RUNS = 128 * (D / 32) / THREADS, PPT = D / 32;
-  constexpr int KB = F::KB == 16 ? 4 : F::KB, VB = F::VB == 16 ? 4 : F::VB;
+  constexpr int BITS = F::KB == 16 ? 4 : (VALUE ? F::VB : F::KB);
+  constexpr int THREADS = 16 * C::PROD, RUNS = 64 * (D / 32) / THREADS, PPT = D / 32;  // of half a block
   const int lane = tid & 31;
-  long c = 0;
+  const PagesLayout& L = a.pv.L;
+  const int off = VALUE ? L.v_off : 0, meta = VALUE ? L.vm_off : L.km_off, lg = VALUE ? L.v_lg : L.k_lg;
+  const uint32_t base = smem + (VALUE ? C::V_OFF : C::K_OFF);
+  int st = 0, par = 0;
   bool ok = true;
   for (int k = 0; ok; ++k) {
     const int slot = k % C::PIECES;
     if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) break;
     const Piece p = sh->piece[slot];
     if (p.nblk == 0) break;
-    const PagesLayout& L = a.pv.L;
     const PageRun run(a.pv, p.head);
-    RawTile<KB, RUNS> kr;
-    RawTile<VB, RUNS> vr;
     int page[RUNS];
     auto find_pages = [&](int tok0) {
 #pragma unroll
@@ -253,30 +293,26 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
       }
     };
     int tok0 = p.blk * C::BK;
+    const int end = tok0 + p.nblk * C::BK;
+    RawRuns<BITS, RUNS> r0, r1;
     find_pages(tok0);
-    fetch_raw<D, KB, RUNS, THREADS>(a, run, p.s.len, tok0, 0, L.km_off, L.k_lg, tid, page, &kr);
-    fetch_raw<D, VB, RUNS, THREADS>(a, run, p.s.len, tok0, L.v_off, L.vm_off, L.v_lg, tid, page, &vr);
-    find_pages(tok0 + C::BK);
-    for (int j = 0; j < p.nblk; ++j, ++c) {
-      const int st = (int)(c % C::NS), par = (int)((c / C::NS) & 1);
-      ok = tile_wait_warp(sh, a, &sh->k_empty[st], par ^ 1);
+    fetch_runs<D, BITS, RUNS, THREADS>(a, run, p.s.len, tok0, off, meta, lg, tid, page, &r0);
+    find_pages(tok0 + 64);
+    for (; tok0 < end; tok0 += C::BK) {
+      fetch_runs<D, BITS, RUNS, THREADS>(a, run, p.s.len, tok0 + 64, off, meta, lg, tid, page, &r1);
+      if (tok0 + C::BK < end) find_pages(tok0 + C::BK);
+      ok = tile_wait_warp(sh, a, VALUE ? &sh->v_empty[st] : &sh->k_empty[st], par ^ 1);
       if (!ok) break;
-      store_raw<D, KB, RUNS, THREADS>(smem + C::K_OFF + st * C::TILE, tid, kr);
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh->k_full[st]));
-      tok0 += C::BK;
-      if (j + 1 < p.nblk) fetch_raw<D, KB, RUNS, THREADS>(a, run, p.s.len, tok0, 0, L.km_off, L.k_lg, tid, page, &kr);
-      ok = tile_wait_warp(sh, a, &sh->v_empty[st], par ^ 1);
-      if (!ok) break;
-      store_raw<D, VB, RUNS, THREADS>(smem + C::V_OFF + st * C::TILE, tid, vr);
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh->v_full[st]));
-      if (j + 1 < p.nblk) {
-        fetch_raw<D, VB, RUNS, THREADS>(a, run, p.s.len, tok0, L.v_off, L.vm_off, L.v_lg, tid, page, &vr);
-        find_pages(tok0 + C::BK);
+      store_runs<D, BITS, RUNS, THREADS>(base + st * C::TILE, 0, tid, r0);
+      if (tok0 + C::BK < end) {
+        fetch_runs<D, BITS, RUNS, THREADS>(a, run, p.s.len, tok0 + C::BK, off, meta, lg, tid, page, &r0);
+        find_pages(tok0 + C::BK + 64);
       }
+      store_runs<D, BITS, RUNS, THREADS>(base + st * C::TILE, 64, tid, r1);
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(VALUE ? &sh->v_full[st] : &sh->k_full[st]));
+      if (++st == C::NS) st = 0, par ^= 1;
     }
     if (lane == 0) mbar_arrive(smem_u32(&sh->piece_free[slot]));
   }
@@ -296,7 +332,8 @@ __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* 
   int ks = 0, kpar = 0, vs = 0, vpar = 0;  // stage to read next, its phase
   int bc = 0;                              // score buffers handed out (one tile)
   int pc[2] = {0, 0};
-  auto scores = [&](int buf, int tile, bool last, bool freed) {
+  // S of a tile with the keys of stage ks; O of a tile with the values of stage vs
+  auto scores = [&](int buf, int tile) {
     const uint64_t q = q0 + (uint64_t)(tile * (C::TILE >> 4)), k = k0 + (uint64_t)(ks * (C::TILE >> 4));
     if (elect_one()) {
 #pragma unroll
@@ -305,69 +342,93 @@ __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* 
         mma_ss(tm + buf * 128, q + at, k + at, S_DESC, i > 0);
       }
       mma_commit(smem_u32(&sh->s_full[buf]));
-      if (last) mma_commit(smem_u32(&sh->k_empty[ks]));
-      if (freed) mma_commit(smem_u32(&sh->q_free));
     }
     __syncwarp();
-    if (last && ++ks == C::NS) ks = 0, kpar ^= 1;
   };
-  auto values = [&](int buf, int tile, bool last, int add) {
+  auto values = [&](int buf, int tile, int add) {
     const uint64_t v = v0 + (uint64_t)(vs * (C::TILE >> 4));
     if (elect_one()) {
 #pragma unroll
       for (int i = 0; i < C::BK / 16; ++i)
         mma_ts(tm + 256 + tile * D, tm + buf * 128 + i * 8, v + (uint64_t)(i * 2048 >> 4), O_DESC, i > 0 ? 1 : add);
       mma_commit(smem_u32(&sh->o_done[tile]));
-      if (last) mma_commit(smem_u32(&sh->v_empty[vs]));
     }
     __syncwarp();
-    if (last && ++vs == C::NS) vs = 0, vpar ^= 1;
+  };
+  // the stages go back when what was issued so far is done
+  auto free_k = [&](bool queries_too) {
+    if (elect_one()) {
+      mma_commit(smem_u32(&sh->k_empty[ks]));
+      if (queries_too) mma_commit(smem_u32(&sh->q_free));
+    }
+    __syncwarp();
+    if (++ks == C::NS) ks = 0, kpar ^= 1;
+  };
+  auto free_v = [&]() {
+    if (elect_one()) mma_commit(smem_u32(&sh->v_empty[vs]));
+    __syncwarp();
+    if (++vs == C::NS) vs = 0, vpar ^= 1;
   };
   for (int k = 0;; ++k) {
     const int slot = k % C::PIECES;
     if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) return;
     const int n = __shfl_sync(0xffffffffu, sh->piece[slot].nblk, 0);
-    const int tiles = (__shfl_sync(0xffffffffu, sh->piece[slot].rows, 0) + 127) / 128;
     if (n == 0) return;
     if (!tile_wait_warp(sh, a, &sh->q_full, k & 1)) return;
     if (!tile_wait_warp(sh, a, &sh->k_full[ks], kpar)) return;
     tc_after_sync();
     if (C::NT == 2) {
-      if (tiles == 2) scores(0, 0, false, false);
-      scores(tiles - 1, tiles - 1, true, n == 1);
-    } else {
-      scores(bc & 1, 0, true, n == 1);
-    }
-    for (int j = 0; j < n; ++j) {
-      if (C::NT == 2) {
+      int lo[2], hi[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        tile_range<D, FMT>(a, sh->piece[slot], i, &lo[i], &hi[i]);
+        lo[i] = __shfl_sync(0xffffffffu, lo[i], 0);
+        hi[i] = __shfl_sync(0xffffffffu, hi[i], 0);
+      }
+      auto sees = [&](int i, int j) { return j >= lo[i] && j < hi[i]; };
+      if (sees(0, 0)) scores(0, 0);
+      if (sees(1, 0)) scores(1, 1);
+      free_k(n == 1);
+      for (int j = 0; j < n; ++j) {
+        if (!tile_wait_warp(sh, a, &sh->v_full[vs], vpar)) return;
+        bool have_k = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (i >= tiles) break;
-          const bool last = i == tiles - 1;
-          if (i == 0 && !tile_wait_warp(sh, a, &sh->v_full[vs], vpar)) return;
-          if (!tile_wait_warp(sh, a, &sh->p_full[i], pc[i] & 1)) return;
-          ++pc[i];
-          tc_after_sync();
-          values(i, i, last, j > 0);
-          if (j + 1 < n) {
-            if (i == 0) {
-              if (!tile_wait_warp(sh, a, &sh->k_full[ks], kpar)) return;
-              tc_after_sync();
-            }
-            scores(i, i, last, last && j + 2 == n);
+          if (sees(i, j)) {
+            if (!tile_wait_warp(sh, a, &sh->p_full[i], pc[i] & 1)) return;
+            ++pc[i];
+            tc_after_sync();
+            values(i, i, j > lo[i]);
+          }
+          if (i == 1) free_v();
+          if (j + 1 < n && sees(i, j + 1)) {
+            if (!have_k && !tile_wait_warp(sh, a, &sh->k_full[ks], kpar)) return;
+            have_k = true;
+            tc_after_sync();
+            scores(i, i);
           }
         }
-      } else {
+        if (j + 1 < n) {
+          if (!have_k && !tile_wait_warp(sh, a, &sh->k_full[ks], kpar)) return;
+          free_k(j + 2 == n);
+        }
+      }
+    } else {
+      scores(bc & 1, 0);
+      free_k(n == 1);
+      for (int j = 0; j < n; ++j) {
         const int buf = bc & 1;
         if (j + 1 < n) {
           if (!tile_wait_warp(sh, a, &sh->k_full[ks], kpar)) return;
           tc_after_sync();
-          scores(buf ^ 1, 0, true, j + 2 == n);
+          scores(buf ^ 1, 0);
+          free_k(j + 2 == n);
         }
         if (!tile_wait_warp(sh, a, &sh->v_full[vs], vpar)) return;
         if (!tile_wait_warp(sh, a, &sh->p_full[buf], (bc >> 1) & 1)) return;
         tc_after_sync();
-        values(buf, 0, true, j > 0);
+        values(buf, 0, j > 0);
+        free_v();
         ++bc;
       }
     }
@@ -378,19 +439,14 @@ __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* 
 
 // ------------------------------------------------------------------ softmax --
 
-// Address of query row r of a piece (of the whole tensor's rows, in elements).
-__device__ __forceinline__ long row_at(const Piece& p, int rep, int r, long token_stride, int D) {
-  const int R = p.r0 + r;
-  return (long)(p.s.s0 + R / rep) * token_stride + (long)(p.head * rep + R % rep) * D;
-}
-
 // A warp's 32 rows of queries into the swizzled operand tile, D / 8 lanes a row
 // (zeros behind the item's rows); returns what the lane's row's scores are to be
 // multiplied by.  row0: the warp's first row inside the tile.
 template <int D, int FMT>
-__device__ __forceinline__ float tile_query(const AttnArgs& a, const Piece& p, int tile_row, int row0, uint32_t tile, int lane) {
+__device__ __forceinline__ float tile_query(const AttnArgs& a, const RowMap& rm, int rows, int tile_row, int row0,
+                                            uint32_t tile, int lane) {
   using F = Fmt<FMT>;
-  constexpr int LPR = D / 8, RPI = 32 / LPR, U = 8;  // lanes a row, rows a step, steps in flight
+  constexpr int LPR = D / 8, RPI = 32 / LPR, U = LPR < 16 ? LPR : 16;  // lanes a row, rows a step, steps in flight
   const int g = lane / LPR, c = lane % LPR;
   float sc = a.scale_log2;
   for (int it0 = 0; it0 < LPR; it0 += U) {
@@ -398,7 +454,7 @@ __device__ __forceinline__ float tile_query(const AttnArgs& a, const Piece& p, i
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int r = tile_row + row0 + (it0 + u) * RPI + g;
-      const uint16_t* src = static_cast<const uint16_t*>(a.q) + row_at(p, a.rep, min(r, p.rows - 1), a.q_stride, D) + c * 8;
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + rm.at(min(r, rows - 1), a.q_stride, D) + c * 8;
       if (a.q_aligned) {
         w[u] = *reinterpret_cast<const uint4*>(src);
       } else {
@@ -426,7 +482,7 @@ __device__ __forceinline__ float tile_query(const AttnArgs& a, const Piece& p, i
         for (int i = 0; i < 4; ++i)
           x[i] = pack2<false>(__uint_as_float(x[i] << 16) * f0 * f1, __uint_as_float(x[i] & 0xffff0000u) * f0 * f1);
       }
-      if (tile_row + row >= p.rows) x[0] = x[1] = x[2] = x[3] = 0;
+      if (tile_row + row >= rows) x[0] = x[1] = x[2] = x[3] = 0;
       asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(tile + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)),
                    "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
                    : "memory");
@@ -451,21 +507,22 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
     if (p.nblk == 0) return;
     if (k > 0 && !tile_wait_warp(sh, a, &sh->q_free, (k - 1) & 1)) return;
     const int r = tile * 128 + row;
+    const RowMap rm(a, p);
     const uint32_t q_tile = smem + C::Q_OFF + tile * C::TILE;
     float sc = a.scale_log2;
-    if (tile * 128 < p.rows) sc = tile_query<D, FMT>(a, p, tile * 128, row & ~31, q_tile, lane);
+    if (tile * 128 < p.rows) sc = tile_query<D, FMT>(a, rm, p.rows, tile * 128, row & ~31, q_tile, lane);
     fence_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh->q_full));
     if (tile * 128 < p.rows) {
-      const int rr = p.r0 + min(r, p.rows - 1);
-      const int pos = p.s.p0 + rr / a.rep;
+      const int pos = rm.position(min(r, p.rows - 1));
       // the tile's first and last position: blocks between need no mask
-      const int pos_lo = p.s.p0 + (p.r0 + tile * 128) / a.rep;
-      const int pos_hi = p.s.p0 + (p.r0 + min(tile * 128 + 127, p.rows - 1)) / a.rep;
+      const int pos_lo = rm.position(tile * 128), pos_hi = rm.position(min(tile * 128 + 127, p.rows - 1));
+      int j0, j1;
+      tile_range<D, FMT>(a, p, tile, &j0, &j1);
       float m = -INFINITY;
       float2 l = make_float2(0.0f, 0.0f);
-      for (int j = 0; j < p.nblk; ++j, ++bc, ++ob) {
+      for (int j = j0; j < j1; ++j, ++bc, ++ob) {
         const int buf = C::NT == 2 ? tile : (bc & 1);
         if (!tile_wait_warp(sh, a, &sh->s_full[buf], C::NT == 2 ? bc & 1 : (bc >> 1) & 1)) return;
         tc_after_sync();
@@ -473,8 +530,51 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
         const int tok0 = (p.blk + j) * BK;
         const bool edge = tok0 + BK - 1 > pos_lo || (a.window > 0 && tok0 <= pos_hi - a.window);
         const int hi = pos - tok0, lo = a.window > 0 ? pos - a.window - tok0 : -1;  // visible columns: lo < c <= hi
-        // the row is read twice, 32 scores at a time: once for its maximum, once for its weights
         uint32_t s[2][32];
+        // Most blocks leave the running maximum alone, so the weights are taken under
+        // it while the block's maximum is found; only if that passes it by 2^8 (or
+        // there is none yet) the row is read twice as below.
+        if (C::kOnePass && j > j0) {
+          uint32_t w[64];
+          const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(7.0f - m, 7.0f - m);
+          float2 add = make_float2(0.0f, 0.0f);
+          float x0 = -INFINITY, x1 = -INFINITY;
+          tmem_ld32(sb, s[0]);
+#pragma unroll
+          for (int q = 0; q < BK / 32; ++q) {
+            tmem_wait_ld32(s[q & 1]);
+            if (q + 1 < BK / 32) tmem_ld32(sb + (q + 1) * 32, s[(q + 1) & 1]);
+            uint32_t* e = s[q & 1];
+            if (edge) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (q * 32 + c > hi || q * 32 + c <= lo) e[c] = 0xff800000u;
+            }
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              float2 x = make_float2(__uint_as_float(e[c]), __uint_as_float(e[c + 1]));
+              if (c & 2) x1 = fmaxf(fmaxf(x1, x.x), x.y);
+              else x0 = fmaxf(fmaxf(x0, x.x), x.y);
+              x = fma2(x, sc2, nb2);
+              x.x = fast_exp2(x.x);
+              x.y = fast_exp2(x.y);
+              add = add2(add, x);
+              w[q * 16 + c / 2] = pack2<F::kBf16>(x.x, x.y);
+            }
+          }
+          const bool over = m == -INFINITY || fmaxf(x0, x1) * sc > m + 8.0f;
+          if (!__any_sync(0xffffffffu, over)) {
+            l = add2(l, add);
+            tmem_st32(sb, w);
+            tmem_st32(sb + 32, w + 32);
+            tmem_wait_st();
+            tc_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[buf]));
+            continue;
+          }
+        }
+        // the row is read twice, 32 scores at a time: once for its maximum, once for its weights
         float x0 = -INFINITY, x1 = -INFINITY;
         tmem_ld32(sb, s[0]);
 #pragma unroll
@@ -497,7 +597,7 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
         const bool grow = top > m + 8.0f;
         if (__any_sync(0xffffffffu, grow)) {
           const float to = grow ? top : m;
-          if (j > 0) {
+          if (j > j0) {
             const float f = to == -INFINITY ? 1.0f : fast_exp2(m - to);
             if (!tile_wait_warp(sh, a, &sh->o_done[tile], (ob - 1) & 1)) return;
             tc_after_sync();
@@ -546,8 +646,8 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
       // ---- the item's output, or this CTA's part of it
       // (with one tile the last scores do not wait for the product before them,
       // so that one is waited for too: a barrier's parity tells two phases apart)
-      if (C::NT == 1 && p.nblk > 1 && !tile_wait_warp(sh, a, &sh->o_done[tile], (ob - 2) & 1)) return;
-      if (!tile_wait_warp(sh, a, &sh->o_done[tile], (ob - 1) & 1)) return;
+      if (C::NT == 1 && j1 > 1 && !tile_wait_warp(sh, a, &sh->o_done[tile], (ob - 2) & 1)) return;
+      if (j1 > j0 && !tile_wait_warp(sh, a, &sh->o_done[tile], (ob - 1) & 1)) return;
       tc_after_sync();
       const float sum = l.x + l.y;
       const bool whole = p.has_first && p.has_last, has = r < p.rows;
@@ -560,6 +660,10 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
         uint32_t o[32];
         tmem_ld32(tm + o_col + c, o);
         tmem_wait_ld32(o);
+        if (j1 == j0) {  // no block: O was never written
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
         if (whole) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
@@ -593,7 +697,7 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
                        : "r"(q_tile + (ch >> 3) * (128 * 128) + rw * 128 + (((ch & 7) ^ (rw & 7)) << 4))
                        : "memory");
           if (tile * 128 + rw < p.rows)
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row_at(p, a.rep, tile * 128 + rw, (long)a.q_heads * D, D) + ch * 8) = w;
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + rm.at(tile * 128 + rw, (long)a.q_heads * D, D) + ch * 8) = w;
         }
         __syncwarp();
       }
@@ -623,8 +727,8 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
   const uint32_t smem = (smem_u32(raw) + 1023) & ~1023u;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NS; ++i) {
-      mbar_init(smem_u32(&sh.k_full[i]), C::PROD);
-      mbar_init(smem_u32(&sh.v_full[i]), C::PROD);
+      mbar_init(smem_u32(&sh.k_full[i]), F::kQuant ? C::PROD / 2 : 1);
+      mbar_init(smem_u32(&sh.v_full[i]), F::kQuant ? C::PROD / 2 : 1);
       mbar_init(smem_u32(&sh.k_empty[i]), 1);
       mbar_init(smem_u32(&sh.v_empty[i]), 1);
     }
@@ -656,7 +760,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
   if (warp < 4 * C::NT) {
     tile_softmax<D, FMT>(a, &sh, smem, warp >> 2, threadIdx.x);
   } else if (warp < 8) {
-    if constexpr (F::kQuant) tile_dequantizer<D, FMT>(a, &sh, smem, threadIdx.x);  // one tile: 128 more dequantize
+    if constexpr (F::kQuant) tile_dequantizer<D, FMT, 1>(a, &sh, smem, threadIdx.x - 128);  // (one tile) values
   } else if (warp < 12) {
     if (warp == 8) {
       tile_mma<D, FMT>(a, &sh, smem);
@@ -681,7 +785,10 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
       }
     }
   } else {
-    if constexpr (F::kQuant) tile_dequantizer<D, FMT>(a, &sh, smem, threadIdx.x - 384);
+    if constexpr (F::kQuant) {
+      if (C::NT == 1 || warp < 14) tile_dequantizer<D, FMT, 0>(a, &sh, smem, threadIdx.x - 384);
+      else tile_dequantizer<D, FMT, 1>(a, &sh, smem, threadIdx.x - 448);
+    }
   }
   __syncwarp();
   if (*(volatile int*)&sh.dead) {  // given up: what is in flight lands before memory is given back

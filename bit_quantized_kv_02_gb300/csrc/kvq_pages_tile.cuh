@@ -39,11 +39,17 @@ struct TileCfg {
   static constexpr int NS = D == 256 ? 1 : (D == 128 ? 2 : 3);  // K stages, V stages
   static constexpr int TILE = 128 * D * 2;         // bytes of a Q, K or V tile
   static constexpr int Q_OFF = 0, K_OFF = NT * TILE, V_OFF = K_OFF + NS * TILE;
-  static constexpr int SMEM = V_OFF + NS * TILE + 1024;  // + alignment of the tiles
-  static constexpr int PROD = F::kQuant ? (NT == 1 ? 8 : 4) : 1;  // warps that fill K and V stages
+  // codes and metadata of one tensor of a record (groups of 32 have the most metadata)
+  static constexpr int RAW_K = F::kQuant ? 2 * D * F::KB + 2 * D : 0, RAW_V = F::kQuant ? 2 * D * F::VB + 2 * D : 0;
+  // records in flight per tensor: what the 227 KB leave (with the longest line of units)
+  static constexpr int NR = !F::kQuant ? 1 : (D < 256 || RAW_K + RAW_V <= 5500 ? 4 : (RAW_K + RAW_V <= 7300 ? 3 : 2));
+  static constexpr int RK_OFF = V_OFF + NS * TILE, RV_OFF = RK_OFF + NR * RAW_K;
+  static constexpr int SMEM = RV_OFF + NR * RAW_V + 1024;  // + alignment of the tiles
+  static_assert(SMEM + 8 * (kPagesMaxBatch + 1) + 1536 <= 232448, "shared memory of a CTA");
+  static constexpr int PROD = F::kQuant ? (NT == 1 ? 8 : 4) : 0;  // dequantizing warps, half for each tensor
   static constexpr int THREADS = F::kQuant ? 512 : 384;
   static constexpr int PIECES = 4;
-  static constexpr bool kOnePass = !F::kQuant;  // (needs the registers of the smaller block)
+  static constexpr int USERS = 4 * NT + 1 + (F::kQuant ? 2 + PROD : 1);  // warps that read a piece
 };
 
 template <int D, int FMT>
@@ -53,6 +59,7 @@ struct TileShared {
   Piece piece[C::PIECES];
   uint64_t k_full[C::NS], k_empty[C::NS], v_full[C::NS], v_empty[C::NS];
   uint64_t q_full, q_free, s_full[2], p_full[2], o_done[2], v_land;
+  uint64_t raw_full[2][C::NR], raw_free[2][C::NR];
   uint64_t piece_full[C::PIECES], piece_free[C::PIECES];
   uint32_t tmem;
   int dead;
@@ -186,134 +193,140 @@ __device__ __forceinline__ void tile_loader(const AttnArgs& a, TileShared<D, FMT
 
 // ------------------------------------------------------------- dequantizer --
 
-// Half of the warps turn keys, half values.  A thread turns runs of 32 channels
-// of one token into four 16-byte chunks each; the runs of half a block are
-// fetched while those of the half before are turned.
-template <int BITS, int RUNS>
-struct RawRuns {
-  uint4 w[RUNS][BITS / 4];  // 16 bytes of 4-bit codes, 32 bytes of 8-bit codes
-  uint32_t zs[RUNS];
-};
-
-template <int D, int BITS, int RUNS, int THREADS>
-__device__ __forceinline__ void fetch_runs(const AttnArgs& a, const PageRun& run, int len, int tok0, int off, int meta_off,
-                                           int lg, int tid, const int* page, RawRuns<BITS, RUNS>* r) {
-  constexpr int PPT = D / 32;  // runs of a token
-  const int piece = tid % PPT;
-#pragma unroll
-  for (int i = 0; i < RUNS; ++i) {
-    const int tok = tok0 + (i * THREADS + tid) / PPT;
-    if (tok < len) {
-      const char* rec = run.at(a, page[i], tok);
-      const char* src = rec + off + (tok & 15) * (D * BITS / 8) + piece * (4 * BITS);
-#pragma unroll
-      for (int k = 0; k < BITS / 4; ++k) r->w[i][k] = reinterpret_cast<const uint4*>(src)[k];
-      r->zs[i] = reinterpret_cast<const uint32_t*>(rec + meta_off)[(tok & 15) * (D >> lg) + ((piece * 32) >> lg)];
-    } else {
-#pragma unroll
-      for (int k = 0; k < BITS / 4; ++k) r->w[i][k] = make_uint4(0, 0, 0, 0);
-      r->zs[i] = 0;  // zero + code * step = 0: behind the sequence's end
-    }
-  }
-}
-
-template <int D, int BITS, int RUNS, int THREADS>
-__device__ __forceinline__ void store_runs(uint32_t tile, int first, int tid, const RawRuns<BITS, RUNS>& r) {
-  constexpr int PPT = D / 32;
-  const int piece = tid % PPT;
-  // lanes of other column blocks store their four chunks in another order, so
-  // that the 8 lanes of a phase touch 8 different groups of banks
-  const int turn = D == 64 ? 0 : (D == 128 ? 2 * (piece >> 1) : piece >> 1);
-#pragma unroll
-  for (int i = 0; i < RUNS; ++i) {
-    const int t = first + (i * THREADS + tid) / PPT;
-    const __half2 z = __low2half2(as_h2(r.zs[i])), s = __high2half2(as_h2(r.zs[i]));
-    const uint32_t row = tile + (piece >> 1) * (128 * 128) + t * 128;
-    constexpr int WC = BITS / 4;  // words of a chunk
-    uint32_t w[4 * WC];
-#pragma unroll
-    for (int k = 0; k < 4 * WC; ++k) w[k] = reinterpret_cast<const uint32_t*>(r.w[i])[k];
-#pragma unroll
-    for (int b = 1; b < 4; b <<= 1)  // the words of chunk k to place k ^ turn
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (!(k & b))
-#pragma unroll
-          for (int e = 0; e < WC; ++e) {
-            const uint32_t x = w[WC * k + e], y = w[WC * (k ^ b) + e];
-            w[WC * k + e] = (turn & b) ? y : x;
-            w[WC * (k ^ b) + e] = (turn & b) ? x : y;
-          }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint32_t y[4];
-      if constexpr (BITS == 8) {
-        y[0] = bytes<0>(w[2 * k], s, z);
-        y[1] = bytes<1>(w[2 * k], s, z);
-        y[2] = bytes<0>(w[2 * k + 1], s, z);
-        y[3] = bytes<1>(w[2 * k + 1], s, z);
-      } else {
-        y[0] = nibbles<0>(w[k], s, z);
-        y[1] = nibbles<1>(w[k], s, z);
-        y[2] = nibbles<2>(w[k], s, z);
-        y[3] = nibbles<3>(w[k], s, z);
+// Brings the records of one tensor (codes and metadata are neighbours) into a
+// ring of raw records, ahead of the warps that turn them.
+template <int D, int FMT, int VALUE>
+__device__ __forceinline__ void raw_loader(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int lane) {
+  using C = TileCfg<D, FMT>;
+  const PagesLayout& L = a.pv.L;
+  const int from = VALUE ? L.v_off : 0, bytes = VALUE ? L.tile_bytes - L.v_off : L.v_off;
+  const uint32_t ring = smem + (VALUE ? C::RV_OFF : C::RK_OFF);
+  int r = 0, par = 0;
+  for (int k = 0;; ++k) {
+    const int slot = k % C::PIECES;
+    if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) return;
+    const Piece p = sh->piece[slot];
+    if (p.nblk == 0) return;
+    const PageRun run(a.pv, p.head);
+    const int end = min((p.blk + p.nblk) * C::BK, p.s.len);
+    // 32 records' pages at a time
+    for (int tok0 = p.blk * C::BK; tok0 < end; tok0 += 16 * 32) {
+      const int mine = tok0 + 16 * lane;
+      const int page = mine < end ? page_index(a, p.b, mine) : 0;
+      for (int i = 0; i < 32 && tok0 + 16 * i < end; ++i) {
+        const int pg = __shfl_sync(0xffffffffu, page, i);
+        if (!tile_wait_warp(sh, a, &sh->raw_free[VALUE][r], par ^ 1)) return;
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&sh->raw_full[VALUE][r]);
+          mbar_expect(bar, bytes);
+          bulk_load(ring + r * (VALUE ? C::RAW_V : C::RAW_K), run.at(a, pg, tok0 + 16 * i) + from, bytes, bar);
+        }
+        if (++r == C::NR) r = 0, par ^= 1;
       }
-      const int c = (4 * (piece & 1) + (k ^ turn)) ^ (t & 7);
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(row + (c << 4)), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                   : "memory");
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh->piece_free[slot]));
   }
 }
 
-// Keys (VALUE 0) or values (1) of all pieces; tid: thread among those of the tensor.
+// Keys (VALUE 0) or values (1) of all pieces: a thread turns a run of 32 channels
+// of one token into four 16-byte chunks of the operand tile; tid: thread among
+// those of the tensor.  The loop body is kept small: with the many roles of this
+// kernel, unrolled over a block it ran out of the instruction cache.
 template <int D, int FMT, int VALUE>
 __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int tid) {
   using C = TileCfg<D, FMT>;
   using F = typename C::F;
   constexpr int BITS = F::KB == 16 ? 4 : (VALUE ? F::VB : F::KB);
-  constexpr int THREADS = 16 * C::PROD, RUNS = 64 * (D / 32) / THREADS, PPT = D / 32;  // of half a block
-  const int lane = tid & 31;
+  constexpr int THREADS = 16 * C::PROD, PPT = D / 32;
+  constexpr int RECS = THREADS / (16 * PPT);  // records turned at once
+  static_assert(RECS >= 1 && RECS <= C::NR, "");
+  constexpr int WC = BITS / 4;                // words of a chunk of 8 channels
+  const int lane = tid & 31, piece = tid % PPT, rec = tid / (16 * PPT), row = (tid / PPT) & 15;
   const PagesLayout& L = a.pv.L;
-  const int off = VALUE ? L.v_off : 0, meta = VALUE ? L.vm_off : L.km_off, lg = VALUE ? L.v_lg : L.k_lg;
-  const uint32_t base = smem + (VALUE ? C::V_OFF : C::K_OFF);
-  int st = 0, par = 0;
-  bool ok = true;
-  for (int k = 0; ok; ++k) {
+  const int meta = VALUE ? L.vm_off - L.v_off : L.km_off, lg = VALUE ? L.v_lg : L.k_lg;
+  const uint32_t raw = smem + (VALUE ? C::RV_OFF : C::RK_OFF);
+  const uint32_t codes_at = row * (D * BITS / 8) + piece * (4 * BITS);
+  const uint32_t meta_at = meta + (row * (D >> lg) + ((piece * 32) >> lg)) * 4;
+  // lanes of other column blocks store their four chunks in another order, so
+  // that the 8 lanes of a phase touch 8 different groups of banks
+  const int turn = D == 64 ? 0 : (D == 128 ? 2 * (piece >> 1) : piece >> 1);
+  int st = 0, par = 0, r = 0, rpar = 0;
+  for (int k = 0;; ++k) {
     const int slot = k % C::PIECES;
-    if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) break;
+    if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) return;
     const Piece p = sh->piece[slot];
-    if (p.nblk == 0) break;
-    const PageRun run(a.pv, p.head);
-    int page[RUNS];
-    auto find_pages = [&](int tok0) {
+    if (p.nblk == 0) return;
+    int tok = p.blk * C::BK;
+#pragma unroll 1
+    for (int j = 0; j < p.nblk; ++j) {
+      if (!tile_wait_warp(sh, a, VALUE ? &sh->v_empty[st] : &sh->k_empty[st], par ^ 1)) return;
+      uint32_t out = smem + (VALUE ? C::V_OFF : C::K_OFF) + st * C::TILE + (piece >> 1) * (128 * 128) + (rec * 16 + row) * 128;
+#pragma unroll 1
+      for (int u = 0; u < C::BK / (16 * RECS); ++u, tok += 16 * RECS, out += 16 * RECS * 128) {
+        uint32_t w[4 * WC], zs = 0;
 #pragma unroll
-      for (int i = 0; i < RUNS; ++i) {
-        const int tok = tok0 + (i * THREADS + tid) / PPT;
-        page[i] = tok < p.s.len ? page_index(a, p.b, tok) : 0;
+        for (int i = 0; i < 4 * WC; ++i) w[i] = 0;
+        // every record with a token of the sequence arrives; rows behind its end become
+        // zero (zero + code * step = 0), whatever the page holds there
+#pragma unroll
+        for (int i = 0; i < RECS; ++i) {
+          if (tok + 16 * i >= p.s.len) continue;
+          const int ri = r + i < C::NR ? r + i : r + i - C::NR;
+          if (!tile_wait_warp(sh, a, &sh->raw_full[VALUE][ri], r + i < C::NR ? rpar : rpar ^ 1)) return;
+          if (RECS == 1 || rec == i) {
+            const uint32_t from = raw + ri * (VALUE ? C::RAW_V : C::RAW_K);
+            ldsv<4 * WC>(from + codes_at, w);
+            zs = lds32(from + meta_at);
+          }
+        }
+        if (tok + rec * 16 + row >= p.s.len) zs = 0;
+        const __half2 z = __low2half2(as_h2(zs)), s = __high2half2(as_h2(zs));
+#pragma unroll
+        for (int b = 1; b < 4; b <<= 1)  // the words of chunk k to place k ^ turn
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (!(c & b))
+#pragma unroll
+              for (int e = 0; e < WC; ++e) {
+                const uint32_t x = w[WC * c + e], y = w[WC * (c ^ b) + e];
+                w[WC * c + e] = (turn & b) ? y : x;
+                w[WC * (c ^ b) + e] = (turn & b) ? x : y;
+              }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t y[4];
+          if constexpr (BITS == 8) {
+            y[0] = bytes<0>(w[2 * c], s, z);
+            y[1] = bytes<1>(w[2 * c], s, z);
+            y[2] = bytes<0>(w[2 * c + 1], s, z);
+            y[3] = bytes<1>(w[2 * c + 1], s, z);
+          } else {
+            y[0] = nibbles<0>(w[c], s, z);
+            y[1] = nibbles<1>(w[c], s, z);
+            y[2] = nibbles<2>(w[c], s, z);
+            y[3] = nibbles<3>(w[c], s, z);
+          }
+          const int at = (4 * (piece & 1) + (c ^ turn)) ^ (row & 7);
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(out + (at << 4)), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                       : "memory");
+        }
+        // The records go back only here, where every lane's loads have been used: an
+        // arrival right behind them let the next copy overtake loads still under way.
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < RECS; ++i)
+          if (tok + 16 * i < p.s.len) {
+            if (lane == 0) mbar_arrive(smem_u32(&sh->raw_free[VALUE][r]));
+            if (++r == C::NR) r = 0, rpar ^= 1;
+          }
       }
-    };
-    int tok0 = p.blk * C::BK;
-    const int end = tok0 + p.nblk * C::BK;
-    RawRuns<BITS, RUNS> r0, r1;
-    find_pages(tok0);
-    fetch_runs<D, BITS, RUNS, THREADS>(a, run, p.s.len, tok0, off, meta, lg, tid, page, &r0);
-    find_pages(tok0 + 64);
-    for (; tok0 < end; tok0 += C::BK) {
-      fetch_runs<D, BITS, RUNS, THREADS>(a, run, p.s.len, tok0 + 64, off, meta, lg, tid, page, &r1);
-      if (tok0 + C::BK < end) find_pages(tok0 + C::BK);
-      ok = tile_wait_warp(sh, a, VALUE ? &sh->v_empty[st] : &sh->k_empty[st], par ^ 1);
-      if (!ok) break;
-      store_runs<D, BITS, RUNS, THREADS>(base + st * C::TILE, 0, tid, r0);
-      if (tok0 + C::BK < end) {
-        fetch_runs<D, BITS, RUNS, THREADS>(a, run, p.s.len, tok0 + C::BK, off, meta, lg, tid, page, &r0);
-        find_pages(tok0 + C::BK + 64);
-      }
-      store_runs<D, BITS, RUNS, THREADS>(base + st * C::TILE, 64, tid, r1);
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(VALUE ? &sh->v_full[st] : &sh->k_full[st]));
       if (++st == C::NS) st = 0, par ^= 1;
     }
+    __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh->piece_free[slot]));
   }
 }
@@ -332,7 +345,10 @@ __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* 
   int ks = 0, kpar = 0, vs = 0, vpar = 0;  // stage to read next, its phase
   int bc = 0;                              // score buffers handed out (one tile)
   int pc[2] = {0, 0};
-  // S of a tile with the keys of stage ks; O of a tile with the values of stage vs
+  // S of a tile with the keys of stage ks; O of a tile with the values of stage vs.
+  // (Scoring the next block's first 64 keys into the columns that the weights leave
+  // free, ahead of the value product, was slower: 995 us against 820 for a chunk of
+  // 2048 at 32k tokens; products of 64 columns wait for shared memory.)
   auto scores = [&](int buf, int tile) {
     const uint64_t q = q0 + (uint64_t)(tile * (C::TILE >> 4)), k = k0 + (uint64_t)(ks * (C::TILE >> 4));
     if (elect_one()) {
@@ -386,12 +402,13 @@ __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* 
         hi[i] = __shfl_sync(0xffffffffu, hi[i], 0);
       }
       auto sees = [&](int i, int j) { return j >= lo[i] && j < hi[i]; };
-      if (sees(0, 0)) scores(0, 0);
-      if (sees(1, 0)) scores(1, 1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (sees(i, 0)) scores(i, i);
       free_k(n == 1);
       for (int j = 0; j < n; ++j) {
-        if (!tile_wait_warp(sh, a, &sh->v_full[vs], vpar)) return;
         bool have_k = false;
+        if (!tile_wait_warp(sh, a, &sh->v_full[vs], vpar)) return;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (sees(i, j)) {
@@ -499,7 +516,16 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
   const int lane = tid & 31, row = tid & 127;
   const uint32_t lanes = (uint32_t)((row >> 5) * 32) << 16;
   const uint32_t tm = sh->tmem + lanes, o_col = 256 + tile * D;
-  int bc = 0, ob = 0;  // blocks read (of this tile), value products
+  int bc = 0, ob = 0;  // blocks read (of this tile), value products asked for
+  int od = 0;          // value products known to be done
+  // Waits for the first n products.  Each phase is waited for, in order, and before
+  // the next product is asked for: a barrier's parity tells only two phases apart.
+  auto products = [&](int n) {
+    for (; od < n; ++od)
+      if (!tile_wait_warp(sh, a, &sh->o_done[tile], od & 1)) return false;
+    tc_after_sync();
+    return true;
+  };
   for (int k = 0;; ++k) {
     const int slot = k % C::PIECES;
     if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) return;
@@ -530,14 +556,48 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
         const int tok0 = (p.blk + j) * BK;
         const bool edge = tok0 + BK - 1 > pos_lo || (a.window > 0 && tok0 <= pos_hi - a.window);
         const int hi = pos - tok0, lo = a.window > 0 ? pos - a.window - tok0 : -1;  // visible columns: lo < c <= hi
-        uint32_t s[2][32];
+        auto hide = [&](uint32_t* e, int q) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (q * 32 + c > hi || q * 32 + c <= lo) e[c] = 0xff800000u;
+        };
+        uint32_t s[2][32], w[64];
+        float2 add;
         // Most blocks leave the running maximum alone, so the weights are taken under
-        // it while the block's maximum is found; only if that passes it by 2^8 (or
-        // there is none yet) the row is read twice as below.
-        if (C::kOnePass && j > j0) {
-          uint32_t w[64];
-          const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(7.0f - m, 7.0f - m);
-          float2 add = make_float2(0.0f, 0.0f);
+        // it while the block's maximum is found.  Where that passes it by 2^8, and in
+        // an item's first block, the row is read once more for its maximum.
+        bool find_max = j == j0;
+        for (;;) {
+          if (find_max) {
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int q = 0; q < BK / 32; ++q) {
+              tmem_ld32(sb + q * 32, s[0]);
+              tmem_wait_ld32(s[0]);
+              if (edge) hide(s[0], q);
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) top = fmaxf(fmaxf(top, __uint_as_float(s[0][c])), __uint_as_float(s[0][c + 1]));
+            }
+            const float to = fmaxf(m, top * sc);
+            if (j > j0) {
+              const float f = to == -INFINITY ? 1.0f : fast_exp2(m - to);
+              if (!products(ob)) return;
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                tmem_ld32(tm + o_col + c, s[1]);
+                tmem_wait_ld32(s[1]);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) s[1][e] = __float_as_uint(__uint_as_float(s[1][e]) * f);
+                tmem_st32(tm + o_col + c, s[1]);
+              }
+              l.x *= f;
+              l.y *= f;
+            }
+            m = to;
+          }
+          const float base = m == -INFINITY ? 0.0f : 7.0f - m;
+          const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(base, base);
+          add = make_float2(0.0f, 0.0f);
           float x0 = -INFINITY, x1 = -INFINITY;
           tmem_ld32(sb, s[0]);
 #pragma unroll
@@ -545,11 +605,7 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
             tmem_wait_ld32(s[q & 1]);
             if (q + 1 < BK / 32) tmem_ld32(sb + (q + 1) * 32, s[(q + 1) & 1]);
             uint32_t* e = s[q & 1];
-            if (edge) {
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (q * 32 + c > hi || q * 32 + c <= lo) e[c] = 0xff800000u;
-            }
+            if (edge) hide(e, q);
 #pragma unroll
             for (int c = 0; c < 32; c += 2) {
               float2 x = make_float2(__uint_as_float(e[c]), __uint_as_float(e[c + 1]));
@@ -562,93 +618,21 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
               w[q * 16 + c / 2] = pack2<F::kBf16>(x.x, x.y);
             }
           }
-          const bool over = m == -INFINITY || fmaxf(x0, x1) * sc > m + 8.0f;
-          if (!__any_sync(0xffffffffu, over)) {
-            l = add2(l, add);
-            tmem_st32(sb, w);
-            tmem_st32(sb + 32, w + 32);
-            tmem_wait_st();
-            tc_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[buf]));
-            continue;
-          }
+          const bool over = fmaxf(x0, x1) * sc > m + 8.0f;
+          if (find_max || !__any_sync(0xffffffffu, over)) break;
+          find_max = true;
         }
-        // the row is read twice, 32 scores at a time: once for its maximum, once for its weights
-        float x0 = -INFINITY, x1 = -INFINITY;
-        tmem_ld32(sb, s[0]);
-#pragma unroll
-        for (int q = 0; q < BK / 32; ++q) {
-          tmem_wait_ld32(s[q & 1]);
-          tmem_ld32(sb + ((q + 1) * 32) % BK, s[(q + 1) & 1]);
-          uint32_t* e = s[q & 1];
-          if (edge) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (q * 32 + c > hi || q * 32 + c <= lo) e[c] = 0xff800000u;
-          }
-#pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            x0 = fmaxf(fmaxf(x0, __uint_as_float(e[c])), __uint_as_float(e[c + 1]));
-            x1 = fmaxf(fmaxf(x1, __uint_as_float(e[c + 2])), __uint_as_float(e[c + 3]));
-          }
-        }
-        const float top = fmaxf(x0, x1) * sc;
-        const bool grow = top > m + 8.0f;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float to = grow ? top : m;
-          if (j > j0) {
-            const float f = to == -INFINITY ? 1.0f : fast_exp2(m - to);
-            if (!tile_wait_warp(sh, a, &sh->o_done[tile], (ob - 1) & 1)) return;
-            tc_after_sync();
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              tmem_ld32(tm + o_col + c, s[1]);
-              tmem_wait_ld32(s[1]);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) s[1][e] = __float_as_uint(__uint_as_float(s[1][e]) * f);
-              tmem_st32(tm + o_col + c, s[1]);
-            }
-            l.x *= f;
-            l.y *= f;
-          }
-          m = to;
-        }
-        const float base = m == -INFINITY ? 0.0f : m - 7.0f;
-        const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(-base, -base);
-        uint32_t w[32];
-#pragma unroll
-        for (int q = 0; q < BK / 32; ++q) {
-          tmem_wait_ld32(s[q & 1]);  // (the first 32 are on their way since the last step of the maximum)
-          if (q + 1 < BK / 32) tmem_ld32(sb + (q + 1) * 32, s[(q + 1) & 1]);
-          uint32_t* e = s[q & 1];
-          if (edge) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (q * 32 + c > hi || q * 32 + c <= lo) e[c] = 0xff800000u;
-          }
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            float2 x = fma2(make_float2(__uint_as_float(e[c]), __uint_as_float(e[c + 1])), sc2, nb2);
-            x.x = fast_exp2(x.x);
-            x.y = fast_exp2(x.y);
-            l = add2(l, x);
-            w[(q & 1) * 16 + c / 2] = pack2<F::kBf16>(x.x, x.y);
-          }
-          // 64 weights over scores that have all been read
-          if (q & 1) tmem_st32(sb + (q >> 1) * 32, w);
-        }
+        l = add2(l, add);
+        if (!products(ob)) return;
+        tmem_st32(sb, w);
+        tmem_st32(sb + 32, w + 32);
         tmem_wait_st();
         tc_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[buf]));
       }
       // ---- the item's output, or this CTA's part of it
-      // (with one tile the last scores do not wait for the product before them,
-      // so that one is waited for too: a barrier's parity tells two phases apart)
-      if (C::NT == 1 && j1 > 1 && !tile_wait_warp(sh, a, &sh->o_done[tile], (ob - 2) & 1)) return;
-      if (j1 > j0 && !tile_wait_warp(sh, a, &sh->o_done[tile], (ob - 1) & 1)) return;
-      tc_after_sync();
+      if (!products(ob)) return;
       const float sum = l.x + l.y;
       const bool whole = p.has_first && p.has_last, has = r < p.rows;
       const float f = whole ? (sum > 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
@@ -742,8 +726,13 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
     mbar_init(smem_u32(&sh.v_land), 1);
     for (int i = 0; i < C::PIECES; ++i) {
       mbar_init(smem_u32(&sh.piece_full[i]), 1);
-      mbar_init(smem_u32(&sh.piece_free[i]), 4 * C::NT + 1 + C::PROD);
+      mbar_init(smem_u32(&sh.piece_free[i]), C::USERS);
     }
+    for (int i = 0; i < C::NR; ++i)
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(smem_u32(&sh.raw_full[t][i]), 1);
+        mbar_init(smem_u32(&sh.raw_free[t][i]), F::kQuant ? C::PROD / 2 : 1);
+      }
     sh.dead = 0;
     fence_mbar_init();
   }
@@ -757,17 +746,26 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
   __syncthreads();
   tc_after_sync();
 
+  // Registers over codes: 512 threads start with 128 each (65536); two tiles take
+  // 256 * 176 + 128 * 72 + 128 * 88 = 65536 of them, one tile 128 * 176 +
+  // 128 * 72 + 256 * 88 = 54272.
   if (warp < 4 * C::NT) {
+    if constexpr (F::kQuant) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
     tile_softmax<D, FMT>(a, &sh, smem, warp >> 2, threadIdx.x);
   } else if (warp < 8) {
-    if constexpr (F::kQuant) tile_dequantizer<D, FMT, 1>(a, &sh, smem, threadIdx.x - 128);  // (one tile) values
+    if constexpr (F::kQuant) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+      tile_dequantizer<D, FMT, 1>(a, &sh, smem, threadIdx.x - 128);  // (one tile) values
+    }
   } else if (warp < 12) {
+    if constexpr (F::kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
     if (warp == 8) {
       tile_mma<D, FMT>(a, &sh, smem);
     } else if (warp == 9) {
-      if constexpr (!F::kQuant) tile_loader<D, FMT>(a, &sh, smem, lane);
+      if constexpr (F::kQuant) raw_loader<D, FMT, 0>(a, &sh, smem, lane);
+      else tile_loader<D, FMT>(a, &sh, smem, lane);
     } else if (warp == 10) {
-      // the pieces of this CTA's units, one ahead of the others; nblk 0 ends
+      // the pieces of this CTA's units, ahead of the others; nblk 0 ends
       long u = cta_begin(&sh.work, blockIdx.x);
       const long end = cta_begin(&sh.work, blockIdx.x + 1);
       for (int k = 0;; ++k) {
@@ -783,9 +781,12 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
         __syncwarp();
         if (p.nblk == 0) break;
       }
+    } else {
+      if constexpr (F::kQuant) raw_loader<D, FMT, 1>(a, &sh, smem, lane);
     }
   } else {
     if constexpr (F::kQuant) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
       if (C::NT == 1 || warp < 14) tile_dequantizer<D, FMT, 0>(a, &sh, smem, threadIdx.x - 384);
       else tile_dequantizer<D, FMT, 1>(a, &sh, smem, threadIdx.x - 448);
     }

@@ -29,6 +29,7 @@ constexpr int kPagesCtas = 1024;   // most CTAs of an attention launch (partial 
 constexpr int kRowsPerCta = 32;    // most query rows a CTA of the few-rows kernel holds
 constexpr int kTileCtas = 192;     // most CTAs of the many-rows kernel
 constexpr int kTileRows = 256;     // most query rows a CTA of the many-rows kernel holds
+constexpr int kTileRing = 8;       // most raw records per tensor that it has in flight
 
 struct PagesLayout {
   int k_bits, v_bits;
@@ -92,6 +93,7 @@ struct AttnArgs {
   int q_bf16;        // type of q and out: 0 fp16, 1 bf16
   int q_aligned;     // rows of q may be read 16 bytes at a time
   int rows_lo, rows_hi;  // sequences with rows_lo < n * rep <= rows_hi are this launch's
+  int ring;          // raw records per tensor in flight (many rows over codes; 0 otherwise)
   int min_units;     // fewest blocks of tokens worth a CTA of its own
   float* part_o;     // [CTA][2][rows][head_dim] partial sums of the first / last item of a CTA
   float* part_ml;    // [CTA][2][rows][2] their maxima and sums
@@ -123,6 +125,7 @@ struct kvq_pages {
   int device = 0;
   int sm_count = 0;
   int sm_smem = 0, cta_smem = 0;  // shared memory of an SM, of it reserved per CTA
+  int max_smem = 0;               // most that a CTA may have
   int which = 0;     // kernel choice (kvq_pages_set_kernel)
   kvq::AttnKernel rows_fn[2] = {};  // few-rows kernel with one and two row tiles (one only at head_dim 256)
   kvq::AttnKernel tile_fn = {};     // many-rows kernel

@@ -99,7 +99,7 @@ int resident(const kvq_pages* P, const AttnKernel& k, int batch) {
 // a CTA holds, `used`: the most that an item can have.
 cudaError_t launch_kernel(const AttnKernel& k, AttnArgs a, int ctas, int rows, int used, cudaStream_t st) {
   void* args[] = {&a};
-  cudaError_t e = launch_pdl(k.fn, dim3(ctas), dim3(k.threads), launch_smem(k, a.bv.batch), st, args);
+  cudaError_t e = launch_pdl(k.fn, dim3(ctas), dim3(k.threads), launch_smem(k, a.bv.batch) + (size_t)a.ring * a.pv.L.tile_bytes, st, args);
   if (e != cudaSuccess) return e;
   const int D = a.pv.head_dim;
   const void* join = D == 64 ? join_dim<64>(rows) : D == 128 ? join_dim<128>(rows) : join_dim<256>(rows);
@@ -118,6 +118,11 @@ cudaError_t launch_rows(kvq_pages* P, AttnArgs a, int max_rows, cudaStream_t st)
 
 cudaError_t launch_tile(kvq_pages* P, AttnArgs a, int max_rows, cudaStream_t st) {
   a.min_units = 2;
+  if (P->L.k_bits != 16) {
+    const int left = P->max_smem - (int)(P->tile_fn.static_smem + launch_smem(P->tile_fn, a.bv.batch));
+    a.ring = std::min(left / P->L.tile_bytes, kTileRing);
+    if (a.ring < 2) return cudaErrorInvalidConfiguration;  // (not reached: two of the largest records fit)
+  }
   return launch_kernel(P->tile_fn, a, std::min(P->sm_count, kTileCtas), a.pv.head_dim == 256 ? kTileRows / 2 : kTileRows,
                        max_rows, st);
 }
@@ -138,6 +143,7 @@ cudaError_t pages_attn_setup(kvq_pages* P) {
   P->tile_fn = D == 64 ? tile_kernel_d64(fmt) : D == 128 ? tile_kernel_d128(fmt) : tile_kernel_d256(fmt);
   cudaError_t e = cudaDeviceGetAttribute(&P->sm_smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor, P->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P->cta_smem, cudaDevAttrReservedSharedMemoryPerBlock, P->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P->max_smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, P->device);
   if (e != cudaSuccess) return e;
   for (AttnKernel* k : {&P->rows_fn[0], &P->rows_fn[1], &P->tile_fn}) {
     if (!k->fn) continue;
@@ -145,8 +151,7 @@ cudaError_t pages_attn_setup(kvq_pages* P) {
     e = cudaFuncGetAttributes(&at, k->fn);
     if (e != cudaSuccess) return e;
     k->static_smem = at.sharedSizeBytes;
-    const size_t most = launch_smem(*k, kPagesMaxBatch);
-    e = cudaFuncSetAttribute(k->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    e = cudaFuncSetAttribute(k->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, P->max_smem - (int)at.sharedSizeBytes);
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k->reg_ctas, k->fn, k->threads, 0);
     if (e != cudaSuccess) return e;
     if (k->reg_ctas < 1) return cudaErrorInvalidConfiguration;

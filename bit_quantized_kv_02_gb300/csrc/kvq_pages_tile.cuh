@@ -39,13 +39,10 @@ struct TileCfg {
   static constexpr int NS = D == 256 ? 1 : (D == 128 ? 2 : 3);  // K stages, V stages
   static constexpr int TILE = 128 * D * 2;         // bytes of a Q, K or V tile
   static constexpr int Q_OFF = 0, K_OFF = NT * TILE, V_OFF = K_OFF + NS * TILE;
-  // codes and metadata of one tensor of a record (groups of 32 have the most metadata)
-  static constexpr int RAW_K = F::kQuant ? 2 * D * F::KB + 2 * D : 0, RAW_V = F::kQuant ? 2 * D * F::VB + 2 * D : 0;
-  // records in flight per tensor: what the 227 KB leave (with the longest line of units)
-  static constexpr int NR = !F::kQuant ? 1 : (D < 256 || RAW_K + RAW_V <= 5500 ? 4 : (RAW_K + RAW_V <= 7300 ? 3 : 2));
-  static constexpr int RK_OFF = V_OFF + NS * TILE, RV_OFF = RK_OFF + NR * RAW_K;
-  static constexpr int SMEM = RV_OFF + NR * RAW_V + 1024;  // + alignment of the tiles
-  static_assert(SMEM + 8 * (kPagesMaxBatch + 1) + 1536 <= 232448, "shared memory of a CTA");
+  // over codes, rings of raw records come behind the tiles, as deep as the 227 KB
+  // of a CTA allow (a.ring records per tensor)
+  static constexpr int RAW_OFF = V_OFF + NS * TILE;
+  static constexpr int SMEM = RAW_OFF + 1024;  // + alignment of the tiles
   static constexpr int PROD = F::kQuant ? (NT == 1 ? 8 : 4) : 0;  // dequantizing warps, half for each tensor
   static constexpr int THREADS = F::kQuant ? 512 : 384;
   static constexpr int PIECES = 4;
@@ -59,7 +56,7 @@ struct TileShared {
   Piece piece[C::PIECES];
   uint64_t k_full[C::NS], k_empty[C::NS], v_full[C::NS], v_empty[C::NS];
   uint64_t q_full, q_free, s_full[2], p_full[2], o_done[2], v_land;
-  uint64_t raw_full[2][C::NR], raw_free[2][C::NR];
+  uint64_t raw_full[2][kTileRing], raw_free[2][kTileRing];
   uint64_t piece_full[C::PIECES], piece_free[C::PIECES];
   uint32_t tmem;
   int dead;
@@ -200,7 +197,7 @@ __device__ __forceinline__ void raw_loader(const AttnArgs& a, TileShared<D, FMT>
   using C = TileCfg<D, FMT>;
   const PagesLayout& L = a.pv.L;
   const int from = VALUE ? L.v_off : 0, bytes = VALUE ? L.tile_bytes - L.v_off : L.v_off;
-  const uint32_t ring = smem + (VALUE ? C::RV_OFF : C::RK_OFF);
+  const uint32_t ring = smem + C::RAW_OFF + (VALUE ? a.ring * L.v_off : 0);
   int r = 0, par = 0;
   for (int k = 0;; ++k) {
     const int slot = k % C::PIECES;
@@ -219,9 +216,9 @@ __device__ __forceinline__ void raw_loader(const AttnArgs& a, TileShared<D, FMT>
         if (lane == 0) {
           const uint32_t bar = smem_u32(&sh->raw_full[VALUE][r]);
           mbar_expect(bar, bytes);
-          bulk_load(ring + r * (VALUE ? C::RAW_V : C::RAW_K), run.at(a, pg, tok0 + 16 * i) + from, bytes, bar);
+          bulk_load(ring + r * bytes, run.at(a, pg, tok0 + 16 * i) + from, bytes, bar);
         }
-        if (++r == C::NR) r = 0, par ^= 1;
+        if (++r == a.ring) r = 0, par ^= 1;
       }
     }
     __syncwarp();
@@ -240,12 +237,13 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
   constexpr int BITS = F::KB == 16 ? 4 : (VALUE ? F::VB : F::KB);
   constexpr int THREADS = 16 * C::PROD, PPT = D / 32;
   constexpr int RECS = THREADS / (16 * PPT);  // records turned at once
-  static_assert(RECS >= 1 && RECS <= C::NR, "");
+  static_assert(RECS >= 1 && RECS <= 2, "the ring holds two records at least");
   constexpr int WC = BITS / 4;                // words of a chunk of 8 channels
   const int lane = tid & 31, piece = tid % PPT, rec = tid / (16 * PPT), row = (tid / PPT) & 15;
   const PagesLayout& L = a.pv.L;
   const int meta = VALUE ? L.vm_off - L.v_off : L.km_off, lg = VALUE ? L.v_lg : L.k_lg;
-  const uint32_t raw = smem + (VALUE ? C::RV_OFF : C::RK_OFF);
+  const uint32_t raw = smem + C::RAW_OFF + (VALUE ? a.ring * L.v_off : 0);
+  const int raw_bytes = VALUE ? L.tile_bytes - L.v_off : L.v_off;
   const uint32_t codes_at = row * (D * BITS / 8) + piece * (4 * BITS);
   const uint32_t meta_at = meta + (row * (D >> lg) + ((piece * 32) >> lg)) * 4;
   // lanes of other column blocks store their four chunks in another order, so
@@ -258,68 +256,86 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
     const Piece p = sh->piece[slot];
     if (p.nblk == 0) return;
     int tok = p.blk * C::BK;
+    // A unit's codes and metadata.  Every record with a token of the sequence
+    // arrives; rows behind its end become zero (zero + code * step = 0), whatever
+    // the page holds there.  The records go back once every lane has its values: an
+    // arrival right behind the loads let the next copy overtake them (shared memory
+    // is busy with the matrix operands, and loads wait for it).
+    auto take = [&](int tok, uint32_t* w, uint32_t* zs) -> bool {
+#pragma unroll
+      for (int i = 0; i < 4 * WC; ++i) w[i] = 0;
+      *zs = 0;
+      int rr = r, pp = rpar;
+#pragma unroll
+      for (int i = 0; i < RECS; ++i) {
+        if (tok + 16 * i >= p.s.len) continue;
+        if (!tile_wait_warp(sh, a, &sh->raw_full[VALUE][rr], pp)) return false;
+        if (RECS == 1 || rec == i) {
+          const uint32_t from = raw + rr * raw_bytes;
+          ldsv<4 * WC>(from + codes_at, w);
+          *zs = lds32(from + meta_at);
+        }
+        if (++rr == a.ring) rr = 0, pp ^= 1;
+      }
+      return true;
+    };
+    auto give_back = [&](int tok, const uint32_t* w, uint32_t zs) {
+      // (a branch on the loads' results: they are there when it is decided)
+      if (__any_sync(0xffffffffu, (w[0] ^ w[4 * WC - 1] ^ zs) == 0x5bd1e995u)) __nanosleep(20);
+#pragma unroll
+      for (int i = 0; i < RECS; ++i)
+        if (tok + 16 * i < p.s.len) {
+          if (lane == 0) mbar_arrive(smem_u32(&sh->raw_free[VALUE][r]));
+          if (++r == a.ring) r = 0, rpar ^= 1;
+        }
+    };
+    auto turn_unit = [&](int tok, uint32_t* w, uint32_t zs, uint32_t out) {
+      if (tok + rec * 16 + row >= p.s.len) zs = 0;
+      const __half2 z = __low2half2(as_h2(zs)), s = __high2half2(as_h2(zs));
+#pragma unroll
+      for (int b = 1; b < 4; b <<= 1)  // the words of chunk k to place k ^ turn
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (!(c & b))
+#pragma unroll
+            for (int e = 0; e < WC; ++e) {
+              const uint32_t x = w[WC * c + e], y = w[WC * (c ^ b) + e];
+              w[WC * c + e] = (turn & b) ? y : x;
+              w[WC * (c ^ b) + e] = (turn & b) ? x : y;
+            }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t y[4];
+        if constexpr (BITS == 8) {
+          y[0] = bytes<0>(w[2 * c], s, z);
+          y[1] = bytes<1>(w[2 * c], s, z);
+          y[2] = bytes<0>(w[2 * c + 1], s, z);
+          y[3] = bytes<1>(w[2 * c + 1], s, z);
+        } else {
+          y[0] = nibbles<0>(w[c], s, z);
+          y[1] = nibbles<1>(w[c], s, z);
+          y[2] = nibbles<2>(w[c], s, z);
+          y[3] = nibbles<3>(w[c], s, z);
+        }
+        const int at = (4 * (piece & 1) + (c ^ turn)) ^ (row & 7);
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(out + (at << 4)), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                     : "memory");
+      }
+    };
 #pragma unroll 1
     for (int j = 0; j < p.nblk; ++j) {
       if (!tile_wait_warp(sh, a, VALUE ? &sh->v_empty[st] : &sh->k_empty[st], par ^ 1)) return;
       uint32_t out = smem + (VALUE ? C::V_OFF : C::K_OFF) + st * C::TILE + (piece >> 1) * (128 * 128) + (rec * 16 + row) * 128;
+      constexpr int UT = 16 * RECS;  // tokens of a unit; two units a turn, for the latencies of one to hide the other's
 #pragma unroll 1
-      for (int u = 0; u < C::BK / (16 * RECS); ++u, tok += 16 * RECS, out += 16 * RECS * 128) {
-        uint32_t w[4 * WC], zs = 0;
-#pragma unroll
-        for (int i = 0; i < 4 * WC; ++i) w[i] = 0;
-        // every record with a token of the sequence arrives; rows behind its end become
-        // zero (zero + code * step = 0), whatever the page holds there
-#pragma unroll
-        for (int i = 0; i < RECS; ++i) {
-          if (tok + 16 * i >= p.s.len) continue;
-          const int ri = r + i < C::NR ? r + i : r + i - C::NR;
-          if (!tile_wait_warp(sh, a, &sh->raw_full[VALUE][ri], r + i < C::NR ? rpar : rpar ^ 1)) return;
-          if (RECS == 1 || rec == i) {
-            const uint32_t from = raw + ri * (VALUE ? C::RAW_V : C::RAW_K);
-            ldsv<4 * WC>(from + codes_at, w);
-            zs = lds32(from + meta_at);
-          }
-        }
-        if (tok + rec * 16 + row >= p.s.len) zs = 0;
-        const __half2 z = __low2half2(as_h2(zs)), s = __high2half2(as_h2(zs));
-#pragma unroll
-        for (int b = 1; b < 4; b <<= 1)  // the words of chunk k to place k ^ turn
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (!(c & b))
-#pragma unroll
-              for (int e = 0; e < WC; ++e) {
-                const uint32_t x = w[WC * c + e], y = w[WC * (c ^ b) + e];
-                w[WC * c + e] = (turn & b) ? y : x;
-                w[WC * (c ^ b) + e] = (turn & b) ? x : y;
-              }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t y[4];
-          if constexpr (BITS == 8) {
-            y[0] = bytes<0>(w[2 * c], s, z);
-            y[1] = bytes<1>(w[2 * c], s, z);
-            y[2] = bytes<0>(w[2 * c + 1], s, z);
-            y[3] = bytes<1>(w[2 * c + 1], s, z);
-          } else {
-            y[0] = nibbles<0>(w[c], s, z);
-            y[1] = nibbles<1>(w[c], s, z);
-            y[2] = nibbles<2>(w[c], s, z);
-            y[3] = nibbles<3>(w[c], s, z);
-          }
-          const int at = (4 * (piece & 1) + (c ^ turn)) ^ (row & 7);
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(out + (at << 4)), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                       : "memory");
-        }
-        // The records go back only here, where every lane's loads have been used: an
-        // arrival right behind them let the next copy overtake loads still under way.
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < RECS; ++i)
-          if (tok + 16 * i < p.s.len) {
-            if (lane == 0) mbar_arrive(smem_u32(&sh->raw_free[VALUE][r]));
-            if (++r == C::NR) r = 0, rpar ^= 1;
-          }
+      for (int u = 0; u < C::BK; u += 2 * UT, tok += 2 * UT, out += 2 * UT * 128) {
+        uint32_t w0[4 * WC], w1[4 * WC], z0, z1;
+        if (!take(tok, w0, &z0)) return;
+        give_back(tok, w0, z0);
+        if (!take(tok + UT, w1, &z1)) return;
+        give_back(tok + UT, w1, z1);
+        turn_unit(tok, w0, z0, out);
+        turn_unit(tok + UT, w1, z1, out + UT * 128);
       }
       fence_async();
       __syncwarp();
@@ -561,7 +577,7 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
           for (int c = 0; c < 32; ++c)
             if (q * 32 + c > hi || q * 32 + c <= lo) e[c] = 0xff800000u;
         };
-        uint32_t s[2][32], w[64];
+        uint32_t s[64], w[64];
         float2 add;
         // Most blocks leave the running maximum alone, so the weights are taken under
         // it while the block's maximum is found.  Where that passes it by 2^8, and in
@@ -572,11 +588,10 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
             float top = -INFINITY;
 #pragma unroll 1
             for (int q = 0; q < BK / 32; ++q) {
-              tmem_ld32(sb + q * 32, s[0]);
-              tmem_wait_ld32(s[0]);
-              if (edge) hide(s[0], q);
+              tmem_ld32(sb + q * 32, s);
+              if (edge) hide(s, q);
 #pragma unroll
-              for (int c = 0; c < 32; c += 2) top = fmaxf(fmaxf(top, __uint_as_float(s[0][c])), __uint_as_float(s[0][c + 1]));
+              for (int c = 0; c < 32; c += 2) top = fmaxf(fmaxf(top, __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
             }
             const float to = fmaxf(m, top * sc);
             if (j > j0) {
@@ -584,11 +599,10 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
               if (!products(ob)) return;
 #pragma unroll 1
               for (int c = 0; c < D; c += 32) {
-                tmem_ld32(tm + o_col + c, s[1]);
-                tmem_wait_ld32(s[1]);
+                tmem_ld32(tm + o_col + c, s);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) s[1][e] = __float_as_uint(__uint_as_float(s[1][e]) * f);
-                tmem_st32(tm + o_col + c, s[1]);
+                for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * f);
+                tmem_st32(tm + o_col + c, s);
               }
               l.x *= f;
               l.y *= f;
@@ -599,12 +613,10 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
           const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(base, base);
           add = make_float2(0.0f, 0.0f);
           float x0 = -INFINITY, x1 = -INFINITY;
-          tmem_ld32(sb, s[0]);
 #pragma unroll
           for (int q = 0; q < BK / 32; ++q) {
-            tmem_wait_ld32(s[q & 1]);
-            if (q + 1 < BK / 32) tmem_ld32(sb + (q + 1) * 32, s[(q + 1) & 1]);
-            uint32_t* e = s[q & 1];
+            if (q % 2 == 0) tmem_ld64(sb + q * 32, s);
+            uint32_t* e = s + q % 2 * 32;
             if (edge) hide(e, q);
 #pragma unroll
             for (int c = 0; c < 32; c += 2) {
@@ -623,7 +635,8 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
           find_max = true;
         }
         l = add2(l, add);
-        if (!products(ob)) return;
+        if (C::NT == 2) od = ob;  // (two tiles: these scores came after the last product)
+        else if (!products(ob)) return;
         tmem_st32(sb, w);
         tmem_st32(sb + 32, w + 32);
         tmem_wait_st();
@@ -643,7 +656,6 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
         tmem_ld32(tm + o_col + c, o);
-        tmem_wait_ld32(o);
         if (j1 == j0) {  // no block: O was never written
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
@@ -728,7 +740,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
       mbar_init(smem_u32(&sh.piece_full[i]), 1);
       mbar_init(smem_u32(&sh.piece_free[i]), C::USERS);
     }
-    for (int i = 0; i < C::NR; ++i)
+    for (int i = 0; i < kTileRing; ++i)
       for (int t = 0; t < 2; ++t) {
         mbar_init(smem_u32(&sh.raw_full[t][i]), 1);
         mbar_init(smem_u32(&sh.raw_free[t][i]), F::kQuant ? C::PROD / 2 : 1);
@@ -737,7 +749,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
     fence_mbar_init();
   }
   pdl_wait();
-  plan_work(a, &sh.work, reinterpret_cast<long*>(raw + C::SMEM));  // (its barriers also publish the initialisation above)
+  plan_work(a, &sh.work, reinterpret_cast<long*>(raw + C::SMEM + a.ring * a.pv.L.tile_bytes));  // (its barriers also publish the initialisation above)
   pdl_trigger();
   if (threadIdx.x == 0) a.split[blockIdx.x].parts = 0;
   if ((int)blockIdx.x >= sh.work.ctas) return;
@@ -772,7 +784,16 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
         const int slot = k % C::PIECES;
         if (k >= C::PIECES && !tile_wait_warp(&sh, a, &sh.piece_free[slot], (k / C::PIECES - 1) & 1)) break;
         Piece p = {};
-        if (u < end) p = find_piece(a, &sh.work, u, end);
+        if (u < end) {
+          p = find_piece(a, &sh.work, u, end);
+          // its queries to the L2 cache, while the piece before is worked on
+          const RowMap rm(a, p);
+          for (int r = lane; r < p.rows; r += 32) {
+            const char* row = static_cast<const char*>(a.q) + rm.at(r, a.q_stride, D) * 2;
+#pragma unroll
+            for (int c = 0; c < D * 2; c += 128) prefetch_l2(row + c);
+          }
+        }
         u += p.nblk;
         if (lane == 0) {
           sh.piece[slot] = p;

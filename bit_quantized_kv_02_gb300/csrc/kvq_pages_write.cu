@@ -309,11 +309,11 @@ __device__ __forceinline__ void find_places(const PagesView& pv, const BatchView
 
 // One row's 8 channels from c0 on into its record (`rec` + `off`): 16-bit, or
 // codes with the group's metadata.  Every lane of the warp calls it.
-template <int D>
+template <int D, bool QUANT>
 __device__ __forceinline__ void put8(char* rec, int off, int meta_off, int bits, int lg_group, int slot, int c0,
                                      const float* x, int page_bf16, bool write) {
   const int t = slot & 15;
-  if (bits == 16) {
+  if (!QUANT) {
     if (!write) return;
     char* dst = rec + off + (c0 >> 6) * 2048 + t * 128 + ((((c0 >> 3) & 7) ^ (t & 7)) << 4);
     if (page_bf16) store8(reinterpret_cast<__nv_bfloat16*>(dst), x, true);
@@ -335,8 +335,26 @@ __device__ __forceinline__ void put8(char* rec, int off, int meta_off, int bits,
   if (!write) return;
   const float r = s == 0.0f ? 0.0f : __frcp_rn(s);
   uint32_t q[8];
+  // quant_code_fast's codes, two values an instruction: rounded by adding and
+  // removing 1.5 * 2^23, and taken again one by one where a quotient is near a
+  // half-integer.  z <= x <= z + (2^bits - 1) s keeps them in range unclamped.
+  bool sure = r >= 0x1p-125f || s == 0.0f;
+  const float2 big = make_float2(12582912.0f, 12582912.0f), small = make_float2(-12582912.0f, -12582912.0f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = (uint32_t)quant_code_fast(x[i], z, s, r, bits, 0);
+  for (int i = 0; i < 8; i += 2) {
+    const float2 num = add2(make_float2(x[i], x[i + 1]), make_float2(-z, -z));
+    const float2 q0 = make_float2(__fmul_rn(num.x, r), __fmul_rn(num.y, r));
+    const float2 m = add2(q0, big);
+    const float2 c = add2(m, small);
+    sure = sure && fabsf(__fsub_rn(q0.x, c.x)) < 0.499755859375f && fabsf(__fsub_rn(q0.y, c.y)) < 0.499755859375f &&
+           fabsf(q0.x) <= 512.0f && fabsf(q0.y) <= 512.0f;
+    q[i] = __float_as_uint(m.x) - 0x4B400000u;
+    q[i + 1] = __float_as_uint(m.y) - 0x4B400000u;
+  }
+  if (!sure) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = (uint32_t)quant_code_fast(x[i], z, s, r, bits, 0);
+  }
   if (bits == 8) {
     const uint2 w = make_uint2(q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24, q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24);
     *reinterpret_cast<uint2*>(rec + off + t * D + c0) = w;
@@ -358,8 +376,8 @@ struct AppendRows {
   int page_bf16, lg_wpt, aligned;
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 4) pages_append_kernel(PagesView pv, BatchView bv, RopeView rv, AppendRows a) {
+template <typename T, int D, bool QUANT>
+__global__ void __launch_bounds__(kThreads, QUANT ? 5 : 4) pages_append_kernel(PagesView pv, BatchView bv, RopeView rv, AppendRows a) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
   __shared__ Place place[kRowWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -376,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 4) pages_append_kernel(PagesView pv,
     const Turn turn = load_turn(rv, p.turn, c0, lane);
     const T* k = static_cast<const T*>(a.k) + t * a.ks;
     const T* v = static_cast<const T*>(a.v) + t * a.vs;
-    constexpr int U = 2;
+    constexpr int U = QUANT ? 1 : 2;
     for (int h0 = sub * RPW; h0 < H; h0 += nsub * RPW * U) {
       Row8<T> kr[U], vr[U];
 #pragma unroll
@@ -394,9 +412,9 @@ __global__ void __launch_bounds__(kThreads, 4) pages_append_kernel(PagesView pv,
         float x[8];
         unpack8(kr[u], x);
         turn8(turn, x);
-        put8<D>(rec, 0, pv.L.km_off, pv.L.k_bits, pv.L.k_lg, p.slot, c0, x, a.page_bf16, hu + rg < H);
+        put8<D, QUANT>(rec, 0, pv.L.km_off, pv.L.k_bits, pv.L.k_lg, p.slot, c0, x, a.page_bf16, hu + rg < H);
         unpack8(vr[u], x);
-        put8<D>(rec, pv.L.v_off, pv.L.vm_off, pv.L.v_bits, pv.L.v_lg, p.slot, c0, x, a.page_bf16, hu + rg < H);
+        put8<D, QUANT>(rec, pv.L.v_off, pv.L.vm_off, pv.L.v_bits, pv.L.v_lg, p.slot, c0, x, a.page_bf16, hu + rg < H);
       }
     }
   }
@@ -465,11 +483,15 @@ unsigned token_blocks(long tokens, int lg_wpt) {
   return (unsigned)std::min((tokens + per - 1) / per, 152L * 8 * 4);
 }
 
-template <typename T>
+template <typename T, bool QUANT>
 const void* append_fn(int D) {
-  return D == 64    ? (const void*)pages_append_kernel<T, 64>
-         : D == 128 ? (const void*)pages_append_kernel<T, 128>
-                    : (const void*)pages_append_kernel<T, 256>;
+  return D == 64    ? (const void*)pages_append_kernel<T, 64, QUANT>
+         : D == 128 ? (const void*)pages_append_kernel<T, 128, QUANT>
+                    : (const void*)pages_append_kernel<T, 256, QUANT>;
+}
+template <typename T>
+const void* append_fn(int D, bool quant) {
+  return quant ? append_fn<T, true>(D) : append_fn<T, false>(D);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -504,9 +526,10 @@ cudaError_t launch_pages_append(const PagesView& pv, const BatchView& bv, const 
   BatchView b = bv;
   RopeView r = rv;
   void* args[] = {&p, &b, &r, &a};
-  const void* fn = in_dtype == KVQ_F32    ? append_fn<float>(pv.head_dim)
-                   : in_dtype == KVQ_BF16 ? append_fn<__nv_bfloat16>(pv.head_dim)
-                                          : append_fn<__half>(pv.head_dim);
+  const bool quant = pv.L.k_bits != 16;
+  const void* fn = in_dtype == KVQ_F32    ? append_fn<float>(pv.head_dim, quant)
+                   : in_dtype == KVQ_BF16 ? append_fn<__nv_bfloat16>(pv.head_dim, quant)
+                                          : append_fn<__half>(pv.head_dim, quant);
   return launch_pdl(fn, dim3(token_blocks(bv.new_tokens, a.lg_wpt)), dim3(kThreads), 0, st, args);
 }
 

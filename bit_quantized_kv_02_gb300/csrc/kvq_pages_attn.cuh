@@ -7,9 +7,11 @@
 // one line, sequence by sequence, and CTA c of C takes the units c*W/C ..
 // (c+1)*W/C - 1: every CTA gets the same number, whatever the lengths are, and
 // writes at most two partial results (the item it starts in and the item it
-// ends in), so the workspace depends on the card and not on the lengths.  The
-// line is worked out on the device from the lengths that hold when the kernel
-// runs; a captured launch can be replayed with others.
+// ends in), so the workspace depends on the card and not on the lengths.  Where
+// there are fewer items than CTAs (few-rows kernel) each item gets CTAs of its own
+// instead, as many as its length asks for: no CTA then works on two items in
+// turn.  All of it is worked out on the device from the lengths that hold when
+// the kernel runs; a captured launch can be replayed with others.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -129,6 +131,7 @@ struct Piece {
   int r0, rows;     // query rows [r0, r0 + rows) of the sequence (token * rep + head of the group)
   int blk, nblk;    // the piece: blocks [blk, blk + nblk)
   int has_first, has_last;  // the item's first / last block is in the piece
+  int parts;                // pieces of the item, 0: by its units
   long item0, item1;        // the item's units
 };
 
@@ -139,6 +142,7 @@ struct Work {
   long* pre;
   long total;
   int ctas;
+  int own;  // > 0: items have CTAs of their own, one per `own` blocks; pre counts CTAs
 };
 
 template <int BK, int ROWS>
@@ -156,51 +160,82 @@ __device__ __forceinline__ long seq_units(const AttnArgs& a, const Seq& s, int l
   return sum;
 }
 
-// All threads of the CTA; leaves the line in *w, its units before each sequence
-// in `pre`.
+// Units of a sequence's kv head, by one thread; *one: it has a single block of rows.
 template <int BK, int ROWS>
+__device__ __forceinline__ long seq_units_serial(const AttnArgs& a, const Seq& s, bool* one) {
+  const int R = s.n * a.rep;
+  *one = true;
+  if (R <= a.rows_lo || R > a.rows_hi) return 0;
+  *one = R <= ROWS;
+  long sum = 0;
+  for (int r0 = 0; r0 < R; r0 += ROWS) {
+    int lo, nb;
+    row_blocks<BK>(s, a.rep, a.window, r0, min(R, r0 + ROWS), &lo, &nb);
+    sum += nb;
+  }
+  return sum;
+}
+
+// All threads of the CTA; leaves the line in *w, its units before each sequence
+// in `pre`.  FEW: sequences have a block of rows or so, a thread each; else a warp
+// each.
+template <int BK, int ROWS, bool FEW>
 __device__ __forceinline__ void plan_work(const AttnArgs& a, Work<BK, ROWS>* w, long* pre) {
-  if (threadIdx.x == 0) w->pre = pre;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  if (a.rows_hi <= ROWS && a.window == 0) {
-    // one block of rows per sequence: a thread each
+  int alone = 1;
+  if (FEW) {
     for (int b = threadIdx.x; b < a.bv.batch; b += blockDim.x) {
-      bool bad;
+      bool bad, one;
       const Seq s = load_seq(a.pv, a.bv, b, &bad);
-      const int R = s.n * a.rep;
+      pre[b + 1] = seq_units_serial<BK, ROWS>(a, s, &one);
+      alone = alone && one;
       if (bad) atomicOr(a.pv.err, 1);
-      pre[b + 1] = R <= a.rows_lo || R > a.rows_hi ? 0 : (long)a.pv.heads * max((s.len + BK - 1) / BK, 1);
     }
   } else {
     for (int b = warp; b < a.bv.batch; b += warps) {
       bool bad;
       const Seq s = load_seq(a.pv, a.bv, b, &bad);
-      const long u = seq_units<BK, ROWS>(a, s, lane) * a.pv.heads;
+      const long u = seq_units<BK, ROWS>(a, s, lane);
       if (lane == 0) {
         pre[b + 1] = u;
         if (bad) atomicOr(a.pv.err, 1);
       }
     }
   }
-  __syncthreads();
+  alone = __syncthreads_and(alone);
   if (warp == 0) {
-    long run = 0;
-    for (int b0 = 0; b0 < a.bv.batch; b0 += 32) {
-      const int b = b0 + lane;
-      long x = b < a.bv.batch ? pre[b + 1] : 0;
+    // sum over the sequences of f(units of a head), times the heads; stored as a running sum if `keep`
+    auto over = [&](auto f, bool keep) {
+      long run = 0;
+      for (int b0 = 0; b0 < a.bv.batch; b0 += 32) {
+        const int b = b0 + lane;
+        long x = b < a.bv.batch ? f(pre[b + 1]) * a.pv.heads : 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        x += run;
+        if (keep && b < a.bv.batch) pre[b + 1] = x;
+        run = __shfl_sync(0xffffffffu, x, 31);
       }
-      x += run;
-      if (b < a.bv.batch) pre[b + 1] = x;
-      run = __shfl_sync(0xffffffffu, x, 31);
+      return run;
+    };
+    long total, own = 0;
+    if (FEW && alone && over([](long u) { return (long)(u > 0); }, false) <= gridDim.x) {
+      total = over([](long u) { return u; }, false);
+      own = max((total + gridDim.x - 1) / gridDim.x, (long)a.min_units);
+      while (over([&](long u) { return (u + own - 1) / own; }, false) > gridDim.x) own += max(own / 8, 1L);
+      total = over([&](long u) { return (u + own - 1) / own; }, true);
+    } else {
+      total = over([](long u) { return u; }, true);
     }
     if (lane == 0) {
       pre[0] = 0;
-      w->total = run;
-      w->ctas = (int)min((long)gridDim.x, (run + a.min_units - 1) / a.min_units);
+      w->pre = pre;
+      w->total = total;
+      w->own = (int)own;
+      w->ctas = own ? (int)total : (int)min((long)gridDim.x, (total + a.min_units - 1) / a.min_units);
     }
   }
   __syncthreads();
@@ -217,6 +252,36 @@ __device__ __forceinline__ int cta_of(const Work<BK, ROWS>* w, long u) {
   while (c > 0 && cta_begin(w, c) > u) --c;
   while (c + 1 < w->ctas && cta_begin(w, c + 1) <= u) ++c;
   return c;
+}
+
+// CTA cta's piece where items have CTAs of their own.
+template <int BK, int ROWS>
+__device__ __forceinline__ Piece own_piece(const AttnArgs& a, const Work<BK, ROWS>* w, int cta) {
+  int lo = 0, hi = a.bv.batch;  // pre[lo] <= cta < pre[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (w->pre[mid] <= cta) lo = mid;
+    else hi = mid;
+  }
+  Piece p;
+  p.b = lo;
+  bool bad;
+  p.s = load_seq(a.pv, a.bv, lo, &bad);
+  const int per_head = (int)(w->pre[lo + 1] - w->pre[lo]) / a.pv.heads, at = cta - (int)w->pre[lo];
+  p.head = at / per_head;
+  const int part = at - p.head * per_head;
+  int blk0, nb;
+  p.r0 = 0;
+  p.rows = p.s.n * a.rep;
+  row_blocks<BK>(p.s, a.rep, a.window, 0, p.rows, &blk0, &nb);
+  const int from = (int)((long)nb * part / per_head), to = (int)((long)nb * (part + 1) / per_head);
+  p.blk = blk0 + from;
+  p.nblk = to - from;
+  p.has_first = part == 0;
+  p.has_last = part == per_head - 1;
+  p.parts = per_head;
+  p.item0 = p.item1 = 0;
+  return p;
 }
 
 // The piece that starts at unit u and ends by `end`; all lanes of a warp.
@@ -268,6 +333,7 @@ __device__ __forceinline__ Piece find_piece(const AttnArgs& a, const Work<BK, RO
   p.nblk = (int)(min(end, p.item1) - u);
   p.has_first = u == p.item0;
   p.has_last = u + p.nblk == p.item1;
+  p.parts = 0;
   return p;
 }
 

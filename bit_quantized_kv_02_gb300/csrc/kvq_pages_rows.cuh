@@ -389,24 +389,24 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
   if (lane < NS) mbar_init(bar + lane * 8, 1);
   fence_mbar_init();
   pdl_wait();
-  plan_work(a, &work, reinterpret_cast<long*>(smem + C::SMEM));
+  plan_work<BK, ROWS, true>(a, &work, reinterpret_cast<long*>(smem + C::SMEM));
   pdl_trigger();
   if (cta >= work.ctas) {
     if (threadIdx.x == 0) a.split[cta].parts = 0;
     return;
   }
-  long u = cta_begin(&work, cta);
-  const long end = cta_begin(&work, cta + 1);
+  long u = work.own ? 0 : cta_begin(&work, cta);
+  const long end = work.own ? 1 : cta_begin(&work, cta + 1);
   int stage = 0, phase = 0;  // of the next tile to be read; the ring is empty between pieces
   bool alive = true, joined = false;
   while (u < end) {
     if (warp == 0) {
-      const Piece x = find_piece(a, &work, u, end);
+      const Piece x = work.own ? own_piece(a, &work, cta) : find_piece(a, &work, u, end);
       if (lane == 0) piece = x;
     }
     __syncthreads();
     const Piece p = piece;
-    u += p.nblk;
+    u += work.own ? 1 : p.nblk;
     // this warp's steps: STEP tokens at 4 * block + warp, while they hold a visible one
     const int see1 = max(p.s.p0 + (p.r0 + p.rows - 1) / a.rep + 1, 0);
     const int see0 = a.window > 0 ? max(p.s.p0 + p.r0 / a.rep - a.window + 1, 0) : 0;
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
     }
     if (threadIdx.x == 0 && p.has_first && !p.has_last) {
       SplitHead h = {};
-      h.parts = cta_of(&work, p.item1 - 1) - cta + 1;
+      h.parts = p.parts ? p.parts : cta_of(&work, p.item1 - 1) - cta + 1;
       h.rows = p.rows, h.row0 = p.r0, h.q_row = p.s.s0, h.head = p.head;
       a.split[cta] = h;
       joined = true;

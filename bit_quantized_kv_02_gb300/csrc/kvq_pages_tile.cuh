@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
     fence_mbar_init();
   }
   pdl_wait();
-  plan_work(a, &sh.work, reinterpret_cast<long*>(raw + C::SMEM + a.ring * a.pv.L.tile_bytes));  // (its barriers also publish the initialisation above)
+  plan_work<C::BK, C::ROWS, false>(a, &sh.work, reinterpret_cast<long*>(raw + C::SMEM + a.ring * a.pv.L.tile_bytes));  // (its barriers also publish the initialisation above)
   pdl_trigger();
   if (threadIdx.x == 0) a.split[blockIdx.x].parts = 0;
   if ((int)blockIdx.x >= sh.work.ctas) return;

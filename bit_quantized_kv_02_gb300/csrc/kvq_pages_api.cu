@@ -270,7 +270,7 @@ kvq_status kvq_pages_attn(kvq_pages_t P, int layer, const void* q, int q_dtype, 
   a.out = out;
   a.q_stride = q_stride;
   a.scale_log2 = softmax_scale * 1.44269504088896340736f;
-  a.window = window;
+  a.window = window < (1 << 30) ? window : 0;  // (no sequence is longer)
   a.rep = c.q_heads / c.kv_heads;
   a.rep_magic = (65536 + a.rep - 1) / a.rep;
   a.q_heads = c.q_heads;

@@ -160,9 +160,16 @@ cudaError_t pages_attn_setup(kvq_pages* P) {
 }
 
 cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, int max_rows, cudaStream_t st) {
-  // Sequences with at most `few` rows go to the few-rows kernel, the others to
-  // the many-rows one.  A batch that may hold both kinds launches both.
-  const int few = P->rows_fn[1].fn ? 32 : 16;
+  // Sequences with at most `few` rows (new tokens x query heads per kv head) go to
+  // the few-rows kernel, the others to the many-rows one; a batch that may hold
+  // both kinds launches both.  Measured, few / many rows, us, 8 sequences of 8192
+  // tokens: 16-bit pages, 12 heads of 64: 32 rows 47 / 68, 48 rows 87 / 69; 8 heads
+  // of 128: 55 / 65, 96 / 66; 2 heads of 256: 44 / 50, 56 / 52.  Codes cost the
+  // many-rows kernel its dequantizing warps: 4 bits, heads of 64: 128 rows
+  // 124 / 159, 192 rows 182 / 189, 256 rows 235 / 194; heads of 128: 64 rows
+  // 85 / 100, 96 rows 114 / 103; heads of 256: 48 rows 55 / 60, 64 rows 65 / 61.
+  const int D = P->cfg.head_dim;
+  const int few = P->L.k_bits == 16 ? 32 : (D == 64 ? 192 : (D == 128 ? 64 : 48));
   a.rows_lo = 0;
   a.rows_hi = INT_MAX;
   if (P->which == 1 || (P->which == 0 && max_rows <= few)) return launch_rows(P, a, max_rows, st);

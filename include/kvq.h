@@ -403,12 +403,13 @@ kvq_status kvq_pages_append(kvq_pages_t pages, int layer, const void* k, const v
  * t > p - window; out = sum_t softmax_t(scale * q . k_t) v_t with fp32 scores,
  * maxima, sums and accumulators.  q: device rows of [q_heads][head_dim] of
  * q_dtype, q_stride elements apart; out: device [new_tokens][q_heads][head_dim]
- * of q_dtype, contiguous.  q_dtype: the pages' dtype, or KVQ_F16 / KVQ_BF16 over
+ * of q_dtype, contiguous, apart from q.  q_dtype: the pages' dtype, or KVQ_F16 / KVQ_BF16 over
  * quantized pages.  Query head h reads KV head h / (q_heads / kv_heads).
  * softmax_scale <= 0 means 1/sqrt(head_dim).  A row that sees no token yields
  * zeros; what pages hold behind a sequence's end has no effect.  Cached values
- * must be finite: where a row of a sequence sees one token of a 16-token tile
- * or 128-token block, the others' values enter with weight zero. */
+ * must be finite: where a row sees one token of a 16-token tile or 128-token
+ * block, the values of the sequence's other tokens there enter with weight zero.
+ * Results do not change from run to run. */
 kvq_status kvq_pages_attn(kvq_pages_t pages, int layer, const void* q, int q_dtype, int64_t q_stride,
                           const kvq_pages_batch* batch, float softmax_scale, int window, void* out, void* stream);
 

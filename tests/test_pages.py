@@ -452,6 +452,68 @@ def test_shared_pages(which, fmt):
 
 
 @gpu
+@pytest.mark.parametrize("which", [1, 2], ids=["few", "many"])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attention_repeats_bit_for_bit(which, fmt, d):
+    """Short pieces of items, one behind the other in a CTA, many times over: a slot
+    or a column given back too early shows as a run that differs."""
+    for batch, heads, window in ((([200], [450]), (5, 1), 0), (([1, 60, 0, 17, 200], [2000, 60, 0, 500, 450]), (5, 1), 100)):
+        c = make(batch, 32, fmt, heads, d, seed=3)
+        data = fill(c, 1, d)
+        q = c.normal(c.rows, heads[0], d).to(c.dtype)
+        c.cache.kvq_pages_set_kernel(which)
+        dev, b = q.cuda(), c.batch()
+        first = c.cache.kvq_pages_attn(0, dev, b, window=window).clone()
+        check_attention(c, q, first.cpu(), data, window)
+        out = torch.zeros_like(first)
+        differ = torch.zeros((), dtype=torch.int64, device="cuda")
+        for _ in range(60):
+            c.cache.kvq_pages_attn(0, dev, b, out=out, window=window)
+            differ += (out != first).sum()
+        assert int(differ) == 0 and c.cache.kvq_pages_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["bf16", "4_8"])
+def test_no_window_is_an_endless_one(fmt):
+    c = make(([4, 3, 40, 200], [2, 50, 33, 300]), 16, fmt, (4, 2), 64, seed=4)
+    data = fill(c, 2, 64)
+    q = c.normal(c.rows, 4, 64).to(c.dtype)
+    for which in (1, 2):
+        c.cache.kvq_pages_set_kernel(which)
+        a = c.cache.kvq_pages_attn(0, q.cuda(), c.batch())
+        check_attention(c, q, a.cpu(), data)
+        for window in (2 ** 31 - 1, 2 ** 30, 2 ** 30 - 1):
+            b = c.cache.kvq_pages_attn(0, q.cuda(), c.batch(), window=window)
+            check_attention(c, q, b.cpu(), data)
+
+
+@gpu
+def test_two_graphs_of_one_cache_take_turns():
+    """Two captured calls over the same handle (they share its workspace), replayed
+    alternately on one stream, and layers that do not touch one another."""
+    c = make(([3, 90], [700, 600]), 32, "bf16", (8, 2), 128, seed=12, layers=2)
+    layers = [fill(c, 2, 128, layer) for layer in (0, 1)]
+    q = c.normal(c.rows, 8, 128).bfloat16()
+    dev, b, outs, graphs = q.cuda(), c.batch(), [], []
+    for layer in (0, 1):
+        outs.append(c.cache.kvq_pages_attn(layer, dev, b))
+    for layer in (0, 1):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.cache.kvq_pages_attn(layer, dev, b, out=outs[layer])
+        graphs.append(g)
+    for i in range(6):
+        for o in outs:
+            o.zero_()
+        for layer in ((0, 1), (1, 0))[i % 2]:
+            graphs[layer].replay()
+        for layer in (0, 1):
+            check_attention(c, q, outs[layer].cpu(), layers[layer])
+
+
+@gpu
 def test_far_offsets():
     """A pool beyond 4 GiB and 2^31 values: the sequence lives in its last pages."""
     pages = 18000  # 18000 * 128 tokens * 4 heads * 512 bytes = 4.7 GB

@@ -1,5 +1,7 @@
 // kvq_pages_api.cu — the extern "C" boundary of the paged cache: validation,
 // the pool's carve-up and dispatch.
+#include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -112,6 +114,10 @@ kvq_status cuda_result(kvq_pages* P, cudaError_t e) {
   return e == cudaSuccess ? KVQ_OK : fail(P, KVQ_ERR_CUDA, cudaGetErrorString(e));
 }
 
+// Is p a multiple of its elements' size (a power of two)?
+bool fits(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+int element(int dtype) { return dtype == KVQ_F32 ? 4 : 2; }
+
 // Handle, layer and current device.
 kvq_status usable(kvq_pages* P, int layer) {
   if (!P) return KVQ_ERR_INVALID_ARG;
@@ -129,6 +135,8 @@ kvq_status valid_batch(kvq_pages* P, const kvq_pages_batch* b, BatchView* v) {
   if ((int64_t)b->new_tokens * P->cfg.q_heads > INT_MAX || (int64_t)b->new_tokens * P->cfg.kv_heads > INT_MAX)
     return fail(P, KVQ_ERR_UNSUPPORTED, "too many new tokens");
   if (!b->q_start || !b->lens || !b->table) return fail(P, KVQ_ERR_INVALID_ARG, "null batch array");
+  if (!fits(b->q_start, 4) || !fits(b->lens, 4) || !fits(b->table, 4))
+    return fail(P, KVQ_ERR_INVALID_ARG, "batch array not 4-byte aligned");
   if (b->table_stride < 1 || b->table_stride > (1L << 30)) return fail(P, KVQ_ERR_INVALID_ARG, "table stride out of range");
   *v = {b->batch, b->new_tokens, b->q_start, b->lens, b->table, (long)b->table_stride};
   return KVQ_OK;
@@ -144,6 +152,7 @@ const char* rope_fault(const kvq_rope* r, int D, bool positions, RopeView* v) {
   if (r->dim < 16 || r->dim > D || r->dim % 16) return "rotated channels out of range";
   if (r->style != KVQ_ROPE_PAIRS && r->style != KVQ_ROPE_HALVES) return "unknown rope style";
   if (positions && !r->positions) return "no positions";
+  if (!fits(r->positions, 4)) return "positions not 4-byte aligned";
   *v = {r->table, r->rows, r->dim, r->style, r->positions};
   return nullptr;
 }
@@ -228,6 +237,8 @@ kvq_status kvq_pages_append(kvq_pages_t P, int layer, const void* k, const void*
   if (bv.new_tokens == 0) return KVQ_OK;
   const int64_t row = (int64_t)P->cfg.kv_heads * P->cfg.head_dim;
   if (!k || !v) return fail(P, KVQ_ERR_INVALID_ARG, "null keys or values");
+  if (!fits(k, element(in_dtype)) || !fits(v, element(in_dtype)))
+    return fail(P, KVQ_ERR_INVALID_ARG, "keys or values not aligned to their type");
   if (k_stride < row || v_stride < row) return fail(P, KVQ_ERR_INVALID_ARG, "stride shorter than a row");
   return cuda_result(P, launch_pages_append(pages_view(P, layer), bv, rv, k, v, in_dtype, P->cfg.dtype == KVQ_BF16,
                                             k_stride, v_stride, static_cast<cudaStream_t>(stream)));
@@ -257,10 +268,14 @@ kvq_status kvq_pages_attn(kvq_pages_t P, int layer, const void* q, int q_dtype, 
   if (q_dtype != KVQ_F16 && q_dtype != KVQ_BF16) return fail(P, KVQ_ERR_INVALID_ARG, "queries are fp16 or bf16");
   if (c.k.bits == 16 && q_dtype != c.dtype) return fail(P, KVQ_ERR_INVALID_ARG, "queries and 16-bit pages have one type");
   if (window < 0) return fail(P, KVQ_ERR_INVALID_ARG, "negative window");
-  if (!(softmax_scale > 0.0f)) softmax_scale = 1.0f / std::sqrt((float)c.head_dim);
-  if (!std::isfinite(softmax_scale)) return fail(P, KVQ_ERR_INVALID_ARG, "softmax scale not finite");
+  if (!(softmax_scale > 0.0f) && !std::isnan(softmax_scale)) softmax_scale = 1.0f / std::sqrt((float)c.head_dim);
+  // in powers of two; not zero, which would turn a hidden score's -inf into NaN
+  const float scale_log2 = std::max(softmax_scale * 1.44269504088896340736f, FLT_MIN);
+  if (!std::isfinite(softmax_scale) || !std::isfinite(scale_log2))
+    return fail(P, KVQ_ERR_INVALID_ARG, "softmax scale not finite");
   if (bv.new_tokens == 0) return KVQ_OK;
   if (!q || !out) return fail(P, KVQ_ERR_INVALID_ARG, "null queries or output");
+  if (!fits(q, 2)) return fail(P, KVQ_ERR_INVALID_ARG, "queries not aligned to their type");
   if (q_stride < (int64_t)c.q_heads * c.head_dim) return fail(P, KVQ_ERR_INVALID_ARG, "stride shorter than a row");
   if (reinterpret_cast<uintptr_t>(out) & 15) return fail(P, KVQ_ERR_INVALID_ARG, "output not 16-byte aligned");
   AttnArgs a = {};
@@ -269,7 +284,7 @@ kvq_status kvq_pages_attn(kvq_pages_t P, int layer, const void* q, int q_dtype, 
   a.q = q;
   a.out = out;
   a.q_stride = q_stride;
-  a.scale_log2 = softmax_scale * 1.44269504088896340736f;
+  a.scale_log2 = scale_log2;
   a.window = window < (1 << 30) ? window : 0;  // (no sequence is longer)
   a.rep = c.q_heads / c.kv_heads;
   a.rep_magic = (65536 + a.rep - 1) / a.rep;
@@ -309,6 +324,11 @@ kvq_status kvq_qk_norm_rope(const kvq_norm_rope_args* a, const kvq_rope* rope, v
   if (a->dtype != KVQ_F16 && a->dtype != KVQ_F32 && a->dtype != KVQ_BF16) return KVQ_ERR_INVALID_ARG;
   if (a->norm && (!std::isfinite(a->eps) || a->eps < 0.0f)) return KVQ_ERR_INVALID_ARG;
   if (a->norm && (a->q_weight || a->k_weight) && a->weight_dtype != a->dtype && a->weight_dtype != KVQ_F32)
+    return KVQ_ERR_INVALID_ARG;
+  if (!fits(a->q, element(a->dtype)) || !fits(a->q_out, element(a->dtype)) || !fits(a->k, element(a->dtype)) ||
+      !fits(a->k_out, element(a->dtype)))
+    return KVQ_ERR_INVALID_ARG;
+  if (a->norm && (!fits(a->q_weight, element(a->weight_dtype)) || !fits(a->k_weight, element(a->weight_dtype))))
     return KVQ_ERR_INVALID_ARG;
   RopeView rv;
   if (rope_fault(rope, a->head_dim, true, &rv)) return KVQ_ERR_INVALID_ARG;

@@ -26,6 +26,8 @@
 // rounding does.
 #pragma once
 
+#include <cfloat>
+
 #include "kvq_pages_attn.cuh"
 
 namespace kvq {
@@ -304,6 +306,12 @@ __device__ __forceinline__ void rows_values(uint32_t st, const LaneOffsets<D, FM
   }
 }
 
+// What the scores of a row scaled by 2^E are to be multiplied by; never zero, which
+// would turn a hidden score's -inf into NaN.
+__device__ __forceinline__ float row_factor(const AttnArgs& a, int E) {
+  return fmaxf(a.scale_log2 * exp2i(-(E / 2)) * exp2i(-(E - E / 2)), FLT_MIN);
+}
+
 // Row tile m of a piece's queries as A operands in shared memory (one warp), and
 // what its rows' scores are to be multiplied by.  Over codes q becomes fp16: a
 // bf16 row is scaled by the power of two that puts its largest magnitude in
@@ -350,7 +358,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Piece& p, 
         const int E = norm_exp(mx);
         // 2^E in two factors: E may pass the range of one float
         const float f0 = exp2i(E / 2), f1 = exp2i(E - E / 2);
-        f = a.scale_log2 * exp2i(-(E / 2)) * exp2i(-(E - E / 2));
+        f = row_factor(a, E);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll

@@ -9,8 +9,9 @@
 //  - loader (16-bit pages): bulk copies of the records' halves into K and V
 //    stages; pages are stored in the operand layout, so no tensor map and no
 //    shuffling is needed;
-//  - dequantizers (codes): a warpgroup turns codes into fp16 operand tiles
-//    (the value the page stands for, one rounding);
+//  - raw loaders and dequantizers (codes): one warp per tensor copies records
+//    into a ring, two warps per tensor (four with one row tile) turn their codes
+//    into fp16 operand tiles (the value the page stands for, one rounding);
 //  - one warp issues the matrix instructions: S = Q K^T (both from shared
 //    memory), O += P V (P from tensor memory, over the scores it came from);
 //  - softmax: a warpgroup per tile, a thread per row, so maxima and sums need
@@ -509,7 +510,7 @@ __device__ __forceinline__ float tile_query(const AttnArgs& a, const RowMap& rm,
         for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         const int E = norm_exp(mx);
         const float f0 = exp2i(E / 2), f1 = exp2i(E - E / 2);
-        const float y = __shfl_sync(0xffffffffu, a.scale_log2 * exp2i(-(E / 2)) * exp2i(-(E - E / 2)), (lane % RPI) * LPR);
+        const float y = __shfl_sync(0xffffffffu, row_factor(a, E), (lane % RPI) * LPR);
         if (lane / RPI == it) sc = y;
 #pragma unroll
         for (int i = 0; i < 4; ++i)

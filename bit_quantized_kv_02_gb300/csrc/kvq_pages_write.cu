@@ -279,7 +279,8 @@ struct Place {
 
 // Places of `count` rows from t0, by the whole block: every sequence's bounds and
 // length are read at once, and the thread whose sequence holds a row follows its
-// table entry, so a row costs two dependent loads whatever the batch is.
+// table entry, so a row costs two dependent loads whatever the batch is.  A
+// sequence whose length or rows do not fit has no places.
 __device__ __forceinline__ void find_places(const PagesView& pv, const BatchView& bv, const RopeView* rv, long t0,
                                             int count, Place* place) {
   if (threadIdx.x < count) place[threadIdx.x] = {-1, 0, 0};
@@ -287,7 +288,10 @@ __device__ __forceinline__ void find_places(const PagesView& pv, const BatchView
   for (int b = threadIdx.x; b < bv.batch; b += kThreads) {
     bool bad;
     const Seq s = load_seq(pv, bv, b, &bad);
-    bad = bad && t0 == 0;  // (one block reports the arrays)
+    if (bad) {  // its clamped rows would stand at other positions: none is touched
+      if (t0 == 0) atomicOr(pv.err, 1);  // (one block reports)
+      continue;
+    }
     const long lo = max(t0, (long)s.s0), hi = min(t0 + count, (long)s.s0 + s.n);
     for (long t = lo; t < hi; ++t) {
       const long pos = s.p0 + (t - s.s0);

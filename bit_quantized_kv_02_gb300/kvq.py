@@ -479,7 +479,15 @@ class Rope:
         self.ref = ctypes.byref(self.c)
 
 
-def _norm_side(x, out, w, name, tokens, head_dim, dtype, index):
+def _new(shape, dtype, device, stream):
+    """A tensor for a call on `stream` (None: the current one), whose memory is that stream's."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _norm_side(x, out, w, name, tokens, head_dim, dtype, index, stream):
     """(out, heads, pointers, strides and weight) of one of kvq_qk_norm_rope's two sides."""
     shape = x.shape
     if len(shape) != 3 or shape[0] != tokens or x.dtype is not dtype:
@@ -487,7 +495,7 @@ def _norm_side(x, out, w, name, tokens, head_dim, dtype, index):
     heads = shape[1]
     stride = _row_stride(x, name, heads, head_dim, index)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=x.device)
+        out = _new(shape, dtype, x.device, stream)
         out_stride = heads * head_dim
     else:
         out_stride = _row_stride(out, name + "_out", heads, head_dim, index)
@@ -523,9 +531,9 @@ def kvq_qk_norm_rope(q, k, q_weight=None, k_weight=None, eps: float = 1e-6, rope
     qo = ko = qp = kp = qop = kop = qw = kw = ref = None
     qh = kh = qs = ks = qos = kos = 0
     if q is not None:
-        qo, qh, qp, qs, qop, qos, qw = _norm_side(q, q_out, q_weight, "q", tokens, d, dtype, index)
+        qo, qh, qp, qs, qop, qos, qw = _norm_side(q, q_out, q_weight, "q", tokens, d, dtype, index, stream)
     if k is not None:
-        ko, kh, kp, ks, kop, kos, kw = _norm_side(k, k_out, k_weight, "k", tokens, d, dtype, index)
+        ko, kh, kp, ks, kop, kos, kw = _norm_side(k, k_out, k_weight, "k", tokens, d, dtype, index, stream)
     if qw is not None:
         weight_code = _DTYPES[q_weight.dtype]
         if kw is not None and k_weight.dtype is not q_weight.dtype:
@@ -619,7 +627,7 @@ class KVQPages:
         if out is None:
             if stream is None:
                 out = torch.zeros(q.shape, dtype=dtype, device=q.device)
-            else:
+            else:  # (as in _new; rows behind the last sequence are not written)
                 with torch.cuda.stream(stream):
                     out = torch.zeros(q.shape, dtype=dtype, device=q.device)
         elif out.shape != q.shape or out.dtype != dtype or out.get_device() != index or not out.is_contiguous():
@@ -640,11 +648,11 @@ class KVQPages:
         if batch.index != index:
             raise ValueError("batch: on another device")
         if k_out is None:
-            k_out = torch.empty(shape, dtype=self.dtype, device=self.device)
+            k_out = _new(shape, self.dtype, self.device, stream)
         elif k_out.shape != shape or k_out.dtype != self.dtype or k_out.get_device() != index or not k_out.is_contiguous():
             raise ValueError("k_out: contiguous [new_tokens][kv_heads][head_dim] of the pages' type")
         if v_out is None:
-            v_out = torch.empty(shape, dtype=self.dtype, device=self.device)
+            v_out = _new(shape, self.dtype, self.device, stream)
         elif v_out.shape != shape or v_out.dtype != self.dtype or v_out.get_device() != index or not v_out.is_contiguous():
             raise ValueError("v_out: contiguous [new_tokens][kv_heads][head_dim] of the pages' type")
         r = _on_device(index, stream, self._lib.kvq_pages_read, self.handle, layer, batch.ref, k_out.data_ptr(),

@@ -343,9 +343,12 @@ typedef struct {
  * lens[b] - n + i.  Rows behind q_start[batch] are neither read nor written.
  * Position p lives in page table[b * table_stride + p / page_tokens].  Device
  * arrays; table entries behind a sequence's last page are not read.  A table
- * entry outside the pool, a length beyond the table or a q_start that
- * decreases or passes new_tokens is never followed: what it touches is skipped or read from
- * elsewhere in the pool, and kvq_pages_status reports KVQ_ERR_BAD_INDEX. */
+ * entry outside the pool, a length that is negative, beyond the table or beyond
+ * 2^30, or a q_start that decreases or passes new_tokens is never followed:
+ * kvq_pages_append and kvq_pages_read skip the token (the entry) or the sequence
+ * (the others), kvq_pages_attn gives that sequence's rows values of no meaning,
+ * and kvq_pages_status reports KVQ_ERR_BAD_INDEX.  All pointers of these calls
+ * are aligned to their elements. */
 typedef struct {
   int batch;              /* sequences, 1..1024 */
   int new_tokens;         /* rows of k / v / q / out (>= q_start[batch]), >= 0 */
@@ -403,12 +406,14 @@ kvq_status kvq_pages_append(kvq_pages_t pages, int layer, const void* k, const v
  * t > p - window; out = sum_t softmax_t(scale * q . k_t) v_t with fp32 scores,
  * maxima, sums and accumulators.  q: device rows of [q_heads][head_dim] of
  * q_dtype, q_stride elements apart; out: device [new_tokens][q_heads][head_dim]
- * of q_dtype, contiguous, apart from q.  q_dtype: the pages' dtype, or KVQ_F16 / KVQ_BF16 over
- * quantized pages.  Query head h reads KV head h / (q_heads / kv_heads).
- * softmax_scale <= 0 means 1/sqrt(head_dim).  A row that sees no token yields
+ * of q_dtype, contiguous, 16-byte aligned, apart from q.  q_dtype: the pages'
+ * dtype, or KVQ_F16 / KVQ_BF16 over quantized pages.  Query head h reads KV head h / (q_heads / kv_heads).
+ * softmax_scale: finite; <= 0 means 1/sqrt(head_dim).  A row that sees no token yields
  * zeros; what pages hold behind a sequence's end has no effect.  Cached values
- * must be finite: where a row sees one token of a 16-token tile or 128-token
- * block, the values of the sequence's other tokens there enter with weight zero.
+ * must be finite: where a row sees one token of a 128-token block (tokens 128 i
+ * .. 128 i + 127), the values of the sequence's other tokens there enter with
+ * weight zero.  Pages of blocks before a window are not read and may be dealt to
+ * others, their table entries may be anything.
  * Results do not change from run to run. */
 kvq_status kvq_pages_attn(kvq_pages_t pages, int layer, const void* q, int q_dtype, int64_t q_stride,
                           const kvq_pages_batch* batch, float softmax_scale, int window, void* out, void* stream);

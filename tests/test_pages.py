@@ -90,6 +90,8 @@ def test_status_string_of_a_bad_index():
     (dict(k_out_stride=0), None, 1), (dict(q=0), None, 1), (dict(k_out=0), None, 1), (dict(q_heads=-1), None, 1),
     ({}, dict(table=0), 1), ({}, dict(table=72), 1), ({}, dict(rows=0), 1), ({}, dict(dim=8), 1), ({}, dict(dim=72), 1),
     ({}, dict(dim=80), 1), ({}, dict(style=2), 1), ({}, dict(positions=0), 1), (dict(tokens=0), None, 0),
+    (dict(q=65), None, 1), (dict(dtype=1, k=66), None, 1), (dict(q_out=67), None, 1), (dict(k_weight=65), None, 1),
+    (dict(q_weight=66, weight_dtype=1), None, 1), ({}, dict(positions=66), 1),
     (dict(q_heads=0, kv_heads=0), None, 0),
 ])
 def test_norm_rope_refusals(L, kw, rope, status):
@@ -400,6 +402,85 @@ def test_attention_scale_strides_and_magnitudes(which, fmt):
 
 @gpu
 @pytest.mark.parametrize("which", [1, 2], ids=["few", "many"])
+@pytest.mark.parametrize("fmt", ["f16", "bf16", "4_8"])
+def test_attention_of_vanishing_scores(which, fmt):
+    """A scale and queries whose product is below every float: all visible weights
+    are equal, and hidden tokens stay hidden."""
+    c = make(([3, 40], [90, 40]), 16, fmt, (4, 2), 64, seed=2)
+    data = fill(c, 2, 64)
+    dtype = torch.bfloat16 if c.bits[0] < 16 else c.dtype
+    c.cache.kvq_pages_set_kernel(which)
+    small = 1e-30 if dtype == torch.bfloat16 else 2.0 ** -14
+    for scale in (1e-30, 1e-45):
+        q = (c.normal(c.rows, 4, 64) * small).to(dtype)
+        for window in (0, 7):
+            got = c.cache.kvq_pages_attn(0, q.cuda(), c.batch(), scale=scale, window=window)
+            check_attention(c, q, got.cpu(), data, window, scale=scale)
+
+
+@gpu
+@pytest.mark.parametrize("which", [1, 2], ids=["few", "many"])
+@pytest.mark.parametrize("fmt", ["bf16", "4_4"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_pages_before_the_window_may_leave(which, fmt, d):
+    """Table entries of pages whose 128-token block lies before the window are not read."""
+    c = make(([1, 30, 4], [700, 600, 130]), 16, fmt, (4, 2), d, seed=5)
+    data = fill(c, 2, d)
+    window = 150
+    for b, (n, ln) in enumerate(zip(c.news, c.lens)):
+        first = max(ln - n + 1 - window, 0) // 128 * 128
+        c.table[b, :first // 16] = -1
+    q = c.normal(c.rows, 4, d).to(c.dtype)
+    c.cache.kvq_pages_set_kernel(which)
+    got = c.cache.kvq_pages_attn(0, q.cuda(), c.batch(), window=window)
+    assert c.cache.kvq_pages_status() == 0
+    check_attention(c, q, got.cpu(), data, window)
+
+
+@gpu
+@pytest.mark.parametrize("which", [1, 2], ids=["few", "many"])
+def test_two_caches_on_two_streams(which):
+    """Calls of two handles at the same time, outputs made on the calls' own streams."""
+    cases = []
+    for i, fmt in enumerate(("bf16", "4_8")):
+        c = make(([1, 200, 8], [1500, 400, 30]), 32, fmt, (8, 2), 128, seed=20 + i)
+        data = fill(c, 2, 128)
+        c.cache.kvq_pages_set_kernel(which)
+        q = c.normal(c.rows, 8, 128).to(c.dtype)
+        cases.append((c, data, q, q.cuda(), c.batch(), torch.cuda.Stream(), []))
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for c, _, _, dev, batch, stream, outs in cases:
+            turned, _ = kvq.kvq_qk_norm_rope(dev, None, norm=False, stream=stream)
+            outs.append(c.cache.kvq_pages_attn(0, turned, batch, stream=stream))
+            del turned
+            outs.append(c.cache.kvq_pages_read(0, c.whole(), stream=stream)[0])
+    torch.cuda.synchronize()
+    for c, data, q, _, _, _, outs in cases:
+        held_keys = torch.cat([k for k, _ in data])
+        for i in range(0, len(outs), 2):
+            check_attention(c, q, outs[i].cpu(), data)
+            assert torch.equal(outs[i + 1].cpu(), held_keys)
+        assert c.cache.kvq_pages_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("which", [1, 2], ids=["few", "many"])
+@pytest.mark.parametrize("fmt", ["8_8", "4_8"])
+def test_largest_batch_with_the_largest_records(which, fmt):
+    news = [1] * 1024
+    lens = [1 + (i * 29) % 60 for i in range(1024)]
+    c = make((news, lens), 16, fmt, (2, 1), 256, seed=8)
+    data = fill(c, 1, 256)
+    q = c.normal(c.rows, 2, 256).bfloat16()
+    c.cache.kvq_pages_set_kernel(which)
+    got = c.cache.kvq_pages_attn(0, q.cuda(), c.batch(1)).cpu()
+    assert c.cache.kvq_pages_status() == 0
+    check_attention(c, q, got, data)
+
+
+@gpu
+@pytest.mark.parametrize("which", [1, 2], ids=["few", "many"])
 def test_attention_of_a_peaked_softmax(which):
     """Scores that grow along the sequence move the maximum in every tile."""
     c = make(([2, 64], [2000, 1000]), 32, "f16", (2, 1), 64, seed=4)
@@ -580,6 +661,33 @@ def test_bad_lengths_are_reported(q_start, lens):
 
 
 @gpu
+@pytest.mark.parametrize("q_start,lens,bad", [([0, 2, 4], [49, 20], [0]), ([0, 2, 4], [40, -5], [1]),
+                                              ([0, 3, 2], [40, 20], [1]), ([-1, 2, 4], [40, 20], [0]),
+                                              ([0, 2, 9], [40, 20], [1])])
+@pytest.mark.parametrize("fmt", ["f16", "8_8"])
+def test_sequences_out_of_range_keep_what_they_hold(fmt, q_start, lens, bad):
+    """A length or rows that do not fit: the sequence is neither written nor read back."""
+    c = make(([2, 2], [40, 20]), 16, fmt, (2, 2), 64, seed=1)
+    data = fill(c, 2, 64)
+    batch = kvq.PagesBatch(torch.tensor(q_start, dtype=torch.int32).cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                           c.table.cuda(), 4)
+    x = c.normal(4, 2, 64).half().cuda()
+    c.cache.kvq_pages_append(0, x, x, batch)
+    assert c.cache.kvq_pages_status() == 7
+    ko, vo = (y.cpu() for y in c.cache.kvq_pages_read(0, c.whole()))
+    s = c.k_start.tolist()
+    for b in range(2):
+        same = torch.equal(ko[s[b]:s[b + 1]], data[b][0]) and torch.equal(vo[s[b]:s[b + 1]], data[b][1])
+        assert same == (b in bad)
+    out = torch.full((4, 2, 64), 3.0, dtype=torch.float16, device="cuda")
+    got, _ = c.cache.kvq_pages_read(0, batch, out, out.clone())
+    assert c.cache.kvq_pages_status() == 7
+    kept = [bool((row == 3).all()) for row in got]
+    good = [t for b in range(2) if b not in bad for t in range(q_start[b], q_start[b + 1])]
+    assert kept == [t not in good for t in range(4)]
+
+
+@gpu
 def test_rope_rows_too_few_are_reported():
     c = make("ones", 16, "f16", (2, 2), 64)
     x = c.normal(c.rows, 2, 64).half().cuda()
@@ -604,7 +712,7 @@ def test_call_refusals(L):
             cache.kvq_pages_attn(layer, q, b)
         with pytest.raises(kvq.KVQError):
             cache.kvq_pages_read(layer, b)
-    for bad in (dict(window=-1), dict(scale=float("inf"))):
+    for bad in (dict(window=-1), dict(scale=float("inf")), dict(scale=float("nan")), dict(scale=3e38)):
         with pytest.raises(kvq.KVQError):
             cache.kvq_pages_attn(0, q, b, **bad)
     with pytest.raises(kvq.KVQError):
@@ -624,6 +732,17 @@ def test_call_refusals(L):
     assert b"batch" in L.kvq_pages_last_error(cache.handle)
     r = kvq._PagesBatch(3, 2 ** 31 - 1, 0, b.q_start.data_ptr(), b.lens.data_ptr(), b.table.data_ptr(), 3)
     assert L.kvq_pages_read(cache.handle, 0, ctypes.byref(r), None, None, None) == 2
+    # pointers that do not fit their elements are refused on the host
+    r, odd = ctypes.byref(b.c), lambda t, by=1: t.data_ptr() + by
+    assert L.kvq_pages_attn(cache.handle, 0, odd(q), 0, 256, r, 0.0, 0, q.data_ptr(), None) == 1
+    assert L.kvq_pages_append(cache.handle, 0, odd(x), x.data_ptr(), 0, 128, 128, r, None, None) == 1
+    assert L.kvq_pages_append(cache.handle, 0, x.data_ptr(), odd(x, 2), 1, 128, 128, r, None, None) == 1
+    for i in range(3):
+        ptrs = [t.data_ptr() + 2 * (i == j) for j, t in enumerate((b.q_start, b.lens, b.table))]
+        shifted = kvq._PagesBatch(3, 3, 0, *ptrs, b.table.shape[1])
+        assert L.kvq_pages_read(cache.handle, 0, ctypes.byref(shifted), None, None, None) == 1
+    rope = kvq._Rope(x.data_ptr(), 3, 64, 0, b.lens.data_ptr() + 2)
+    assert L.kvq_pages_append(cache.handle, 0, x.data_ptr(), x.data_ptr(), 0, 128, 128, r, ctypes.byref(rope), None) == 1
     # no rows: nothing to do
     empty = kvq.PagesBatch(torch.zeros(2, dtype=torch.int32).cuda(), torch.zeros(1, dtype=torch.int32).cuda(),
                            torch.zeros((1, 1), dtype=torch.int32).cuda(), 0)

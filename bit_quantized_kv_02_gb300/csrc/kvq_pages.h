@@ -127,7 +127,7 @@ struct kvq_pages {
   int sm_smem = 0, cta_smem = 0;  // shared memory of an SM, of it reserved per CTA
   int max_smem = 0;               // most that a CTA may have
   int which = 0;     // kernel choice (kvq_pages_set_kernel)
-  kvq::AttnKernel rows_fn[2] = {};  // few-rows kernel with one and two row tiles (one only at head_dim 256)
+  kvq::AttnKernel rows_fn[3] = {};  // few-rows kernel: up to 8 rows, one and two row tiles (not two at head_dim 256)
   kvq::AttnKernel tile_fn = {};     // many-rows kernel
   std::string last_error;
 };

@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) pages_join_kernel(const __gri
 template <int D>
 const void* join_dim(int rows) {
   switch (rows) {
+    case 8: return (const void*)pages_join_kernel<D, 8>;
     case 16: return (const void*)pages_join_kernel<D, 16>;
     case 32: return (const void*)pages_join_kernel<D, 32>;
     case 128: return (const void*)pages_join_kernel<D, 128>;
@@ -108,12 +109,15 @@ cudaError_t launch_kernel(const AttnKernel& k, AttnArgs a, int ctas, int rows, i
 }
 
 cudaError_t launch_rows(kvq_pages* P, AttnArgs a, int max_rows, cudaStream_t st) {
-  // Two row tiles per warp where a sequence may have more rows than one holds:
-  // the cache is then read once for 32 rows.
-  const int mt = max_rows > 16 && P->rows_fn[1].fn ? 2 : 1;
-  const AttnKernel& k = P->rows_fn[mt - 1];
+  // Up to 8 rows the products are turned (4-bit pages, 32 sequences of 4096 tokens,
+  // turned / one row tile, us: heads of 64 60 / 69, of 128 55 / 86, of 256 36 / 41;
+  // 16-bit 69 / 72, 89 / 89, 52 / 53).  Two row tiles per warp where a sequence may
+  // have more rows than one holds: the cache is then read once for 32 rows (5
+  // drafted tokens, 20 rows, over 8-bit pages: 66 us, with one row tile 98).
+  const int mt = max_rows <= 8 ? 0 : (max_rows > 16 && P->rows_fn[2].fn ? 2 : 1);
+  const AttnKernel& k = P->rows_fn[mt];
   a.min_units = 2;
-  return launch_kernel(k, a, std::min(resident(P, k, a.bv.batch) * P->sm_count, kPagesCtas), 16 * mt, max_rows, st);
+  return launch_kernel(k, a, std::min(resident(P, k, a.bv.batch) * P->sm_count, kPagesCtas), mt ? 16 * mt : 8, max_rows, st);
 }
 
 cudaError_t launch_tile(kvq_pages* P, AttnArgs a, int max_rows, cudaStream_t st) {
@@ -138,14 +142,14 @@ int pages_format(const kvq_pages* P) {
 
 cudaError_t pages_attn_setup(kvq_pages* P) {
   const int D = P->cfg.head_dim, fmt = pages_format(P);
-  P->rows_fn[0] = D == 64 ? rows_kernel_d64(fmt, 1) : D == 128 ? rows_kernel_d128(fmt, 1) : rows_kernel_d256(fmt, 1);
-  if (D < 256) P->rows_fn[1] = D == 64 ? rows_kernel_d64(fmt, 2) : rows_kernel_d128(fmt, 2);
+  for (int mt = 0; mt < (D < 256 ? 3 : 2); ++mt)
+    P->rows_fn[mt] = D == 64 ? rows_kernel_d64(fmt, mt) : D == 128 ? rows_kernel_d128(fmt, mt) : rows_kernel_d256(fmt, mt);
   P->tile_fn = D == 64 ? tile_kernel_d64(fmt) : D == 128 ? tile_kernel_d128(fmt) : tile_kernel_d256(fmt);
   cudaError_t e = cudaDeviceGetAttribute(&P->sm_smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor, P->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P->cta_smem, cudaDevAttrReservedSharedMemoryPerBlock, P->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P->max_smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, P->device);
   if (e != cudaSuccess) return e;
-  for (AttnKernel* k : {&P->rows_fn[0], &P->rows_fn[1], &P->tile_fn}) {
+  for (AttnKernel* k : {&P->rows_fn[0], &P->rows_fn[1], &P->rows_fn[2], &P->tile_fn}) {
     if (!k->fn) continue;
     cudaFuncAttributes at;
     e = cudaFuncGetAttributes(&at, k->fn);

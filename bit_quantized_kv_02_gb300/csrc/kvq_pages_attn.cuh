@@ -9,8 +9,10 @@
 // writes at most two partial results (the item it starts in and the item it
 // ends in), so the workspace depends on the card and not on the lengths.  Where
 // there are fewer items than CTAs (few-rows kernel) each item gets CTAs of its own
-// instead, as many as its length asks for: no CTA then works on two items in
-// turn.  All of it is worked out on the device from the lengths that hold when
+// instead, as many as its length asks for, if that leaves no CTA much more than
+// its even share: no CTA then works on two items in turn.  Own CTAs / one line,
+// us: 16 x 5 drafted tokens over 8-bit pages 68 / 76, 8 sequences of 8192 4-bit
+// tokens 35 / 37, but 48 of 4096 98 / 75 and 64 of 1k to 32k 469 / 317.  All of it is worked out on the device from the lengths that hold when
 // the kernel runs; a captured launch can be replayed with others.
 #pragma once
 
@@ -225,11 +227,11 @@ __device__ __forceinline__ void plan_work(const AttnArgs& a, Work<BK, ROWS>* w, 
     if (FEW && alone && over([](long u) { return (long)(u > 0); }, false) <= gridDim.x) {
       total = over([](long u) { return u; }, false);
       own = max((total + gridDim.x - 1) / gridDim.x, (long)a.min_units);
+      const long even = own;
       while (over([&](long u) { return (u + own - 1) / own; }, false) > gridDim.x) own += max(own / 8, 1L);
-      total = over([&](long u) { return (u + own - 1) / own; }, true);
-    } else {
-      total = over([](long u) { return u; }, true);
+      if (own > even + even / 4 + 2) own = 0;
     }
+    total = own ? over([&](long u) { return (u + own - 1) / own; }, true) : over([](long u) { return u; }, true);
     if (lane == 0) {
       pre[0] = 0;
       w->pre = pre;

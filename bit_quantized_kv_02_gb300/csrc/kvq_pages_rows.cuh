@@ -6,7 +6,10 @@
 // of stages, and runs an independent softmax over its tokens, so nothing but the
 // end of an item synchronises the warps.  Query rows are the 16 rows of
 // m16n8k16 (MT tiles of them), so all query heads of a kv head and several new
-// tokens share one read of the cache.
+// tokens share one read of the cache.  Up to 8 rows are its columns instead (MT
+// 0): half the products, operands and accumulators, and the exchange of a row's
+// maximum only where it has to grow; keys and values become the left operand from
+// the same registers, and the weights are turned by two 8x8 transposes.
 //  - 16-bit pages: ldmatrix reads keys and (transposed) values straight from
 //    the swizzled rows.
 //  - codes: the contraction does not care about the order of channels, tokens
@@ -27,12 +30,12 @@
 //
 // Measured: 16 sequences of 4113 bf16 tokens, 40 heads of 128: 207 us, 96 % of a
 // copy's bandwidth.  64 sequences of 1k to 32k 4-bit tokens, 32 query heads over 8
-// of 128: 375 us, 50 %: a 16-token record of codes costs about as many
-// instructions whatever the rows are, 0.55 of the issue slots are used with three
-// warps a scheduler, and fixed-latency waits and the pipe shared by conversions
-// and matrix instructions take the rest.  5 drafted tokens over 8-bit pages: 66 us
-// (floor 29).  8 sequences of 2048 fp16 tokens, 12 heads of 64: 16 us in a graph,
-// of which 9 are launch, plan and join.
+// of 128: 315 us, 59 % (375 with 16 rows and three CTAs per SM in place of 8 and
+// four; 330 with 8 rows and five): a record of codes costs about as many
+// instructions whatever the rows are, and fixed-latency waits take the slots that
+// are left.  5 drafted tokens over 8-bit pages: 66 us (floor 29), two CTAs per SM.
+// 8 sequences of 2048 fp16 tokens, 12 heads of 64: 15 us in a graph, of which 9 are
+// launch, plan and join.
 #pragma once
 
 #include <cfloat>
@@ -54,11 +57,17 @@ struct Fmt {
 template <int D, int FMT, int MT>
 struct RowsCfg {
   using F = Fmt<FMT>;
-  static constexpr int ROWS = 16 * MT;
+  static constexpr bool kTurned = MT == 0;  // the rows are the products' 8 columns
+  static constexpr int ROWS = kTurned ? 8 : 16 * MT;
+  static constexpr int NM = kTurned ? 1 : MT;           // row tiles
+  static constexpr int NO = kTurned ? D / 16 : D / 8;   // accumulator tiles of a row tile
+  static constexpr int QW = kTurned ? 2 : 4;            // words of a lane's query operand
   // a record with the most metadata (groups of 32)
   static constexpr int REC = 2 * D * (F::KB + F::VB) + (F::kQuant ? 2 * 16 * (D / 32) * 4 : 0);
   // CTAs per SM that registers and shared memory are cut for
-  static constexpr int CTAS = MT == 2 ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : (D == 128 && F::kQuant ? 3 : 2));
+  static constexpr int CTAS = kTurned && F::kQuant ? (D == 256 ? 3 : 4)
+                              : MT == 2            ? (D == 64 ? 3 : 2)
+                                                   : (D == 64 ? 4 : (D == 128 && F::kQuant ? 3 : 2));
   static constexpr int BUDGET = CTAS == 4 ? 12544 : (CTAS == 3 ? 16384 : 24576);  // bytes of a warp's ring
   // records of a warp's step and stage: two where two such stages fit, so that
   // the softmax's exchanges and the loop cost half as much per token
@@ -66,7 +75,7 @@ struct RowsCfg {
   static constexpr int STEP = 16 * RECS, BK = STEP * kRowsWarps;  // tokens of a step and of a unit
   static constexpr int STAGE = RECS * REC;
   static constexpr int NS = BUDGET / STAGE < 2 ? 2 : (BUDGET / STAGE > 4 ? 4 : BUDGET / STAGE);
-  static constexpr bool kSplit = !F::kQuant && MT == 1;  // weights as operand + remainder
+  static constexpr bool kSplit = !F::kQuant && MT <= 1;  // weights as operand + remainder
   static constexpr int RING = kRowsWarps * NS * STAGE;
   static constexpr int MERGE = kRowsWarps * ROWS * (D + 2) * 4;
   static constexpr int SMEM = (RING > MERGE ? RING : MERGE);
@@ -93,6 +102,11 @@ __device__ __forceinline__ void mma16(float* c, const uint32_t* a, uint32_t b0, 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
     mma_16816(c, a[0], a[1], a[2], a[3], b0, b1);
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
 }
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
@@ -170,26 +184,36 @@ struct LaneOffsets {
   }
 };
 
-// One 16-token record's scores: acc[m][n8 tile] += Q K^T.  sq: the query operands
-// in shared memory, [m][mma step][lane] of four words.
+// One 16-token record's scores: acc[m][n8 tile] += Q K^T, or turned acc[0][0] +=
+// K Q^T.  sq: the query operands in shared memory, [m][mma step][lane].
 template <int D, int FMT, int MT>
 __device__ __forceinline__ void rows_scores(uint32_t st, const PagesLayout& L, const LaneOffsets<D, FMT>& lo,
                                             uint32_t sq, int lane, float (*acc)[2][4]) {
   using F = Fmt<FMT>;
-  const uint32_t qa = sq + lane * 16;
+  using C = RowsCfg<D, FMT, MT>;
+  const uint32_t qa = sq + lane * (C::QW * 4);
+  // keys of tokens 0..7 and 8..15 (two words each) of a step
+  auto step = [&](int ks, const uint32_t* b0, const uint32_t* b1) {
+#pragma unroll
+    for (int m = 0; m < C::NM; ++m) {
+      uint32_t q[C::QW];
+      ldsv<C::QW>(qa + (m * (D / 16) + ks) * (C::QW * 128), q);
+      if constexpr (C::kTurned) {
+        const uint32_t k[4] = {b0[0], b1[0], b0[1], b1[1]};
+        mma16<F::kBf16>(acc[m][0], k, q[0], q[1]);
+      } else {
+        mma16<F::kBf16>(acc[m][0], q, b0[0], b0[1]);
+        mma16<F::kBf16>(acc[m][1], q, b1[0], b1[1]);
+      }
+    }
+  };
   if constexpr (!F::kQuant) {
     const uint32_t base = st + lo.k, turn = (((lane >> 3) & 1) ^ (lane & 7)) << 4;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       uint32_t b[4];
       ldsm4(base + (ks >> 2) * 2048 + (turn ^ ((2 * ks & 7) << 4)), b);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        uint32_t q[4];
-        ldsv<4>(qa + (m * (D / 16) + ks) * 512, q);
-        mma16<F::kBf16>(acc[m][0], q, b[0], b[1]);
-        mma16<F::kBf16>(acc[m][1], q, b[2], b[3]);
-      }
+      step(ks, b, b + 2);
     }
   } else {
     constexpr int SPAN = D / 4;               // channels a lane reads of a token
@@ -223,38 +247,44 @@ __device__ __forceinline__ void rows_scores(uint32_t st, const PagesLayout& L, c
             b[h][1] = nibbles<1>(w[h][i / 2], s[h], z[h]);
           }
         }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          uint32_t q[4];
-          ldsv<4>(qa + (m * (D / 16) + r * (RUN / 4) + i) * 512, q);
-          mma16<false>(acc[m][0], q, b[0][0], b[0][1]);
-          mma16<false>(acc[m][1], q, b[1][0], b[1][1]);
-        }
+        step(r * (RUN / 4) + i, b[0], b[1]);
       }
     }
   }
 }
 
-// o[m][n8 tile] += P V of one record; p: the probabilities as A operands.
+// o[m][n8 tile] += P V of one record; p: the probabilities as operands.  Turned:
+// o[0][m16 tile] += V^T P^T.
 template <int D, int FMT, int MT>
 __device__ __forceinline__ void rows_values(uint32_t st, const LaneOffsets<D, FMT>& lo, const uint32_t (*p)[4],
-                                            const uint32_t (*rest)[4], int lane, float (*o)[D / 8][4]) {
+                                            const uint32_t (*rest)[4], int lane, float (*o)[RowsCfg<D, FMT, MT>::NO][4]) {
   using F = Fmt<FMT>;
+  using C = RowsCfg<D, FMT, MT>;
+  // column tiles 2j and 2j + 1: values of tokens 0..7 and 8..15 (one word each)
+  auto step = [&](int j, const uint32_t* b0, const uint32_t* b1) {
+    if constexpr (C::kTurned) {
+      const uint32_t v[4] = {b0[0], b1[0], b0[1], b1[1]};
+      mma16<F::kBf16>(o[0][j], v, p[0][0], p[0][1]);
+      if constexpr (C::kSplit) mma16<F::kBf16>(o[0][j], v, rest[0][0], rest[0][1]);
+    } else {
+#pragma unroll
+      for (int m = 0; m < C::NM; ++m) {
+        mma16<F::kBf16>(o[m][2 * j], p[m], b0[0], b0[1]);
+        mma16<F::kBf16>(o[m][2 * j + 1], p[m], b1[0], b1[1]);
+        if constexpr (C::kSplit) {
+          mma16<F::kBf16>(o[m][2 * j], rest[m], b0[0], b0[1]);
+          mma16<F::kBf16>(o[m][2 * j + 1], rest[m], b1[0], b1[1]);
+        }
+      }
+    }
+  };
   if constexpr (!F::kQuant) {
     const uint32_t base = st + lo.v, turn = ((lane >> 4) ^ (lane & 7)) << 4;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
       uint32_t b[4];
       ldsm4t(base + (j >> 2) * 2048 + (turn ^ ((2 * j & 7) << 4)), b);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        mma16<F::kBf16>(o[m][2 * j], p[m], b[0], b[1]);
-        mma16<F::kBf16>(o[m][2 * j + 1], p[m], b[2], b[3]);
-        if constexpr (RowsCfg<D, FMT, MT>::kSplit) {
-          mma16<F::kBf16>(o[m][2 * j], rest[m], b[0], b[1]);
-          mma16<F::kBf16>(o[m][2 * j + 1], rest[m], b[2], b[3]);
-        }
-      }
+      step(j, b, b + 2);
     }
   } else {
     constexpr int RUN = D / 8;           // channels a lane reads of a token
@@ -282,11 +312,10 @@ __device__ __forceinline__ void rows_values(uint32_t st, const LaneOffsets<D, FM
           x[h][1] = __byte_perm(w[2 * h][i], w[2 * h + 1][i], 0x7362);
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t b0 = (c & 1) ? bytes<1>(x[0][c >> 1], s[0], z[0]) : bytes<0>(x[0][c >> 1], s[0], z[0]);
-          const uint32_t b1 = (c & 1) ? bytes<1>(x[1][c >> 1], s[1], z[1]) : bytes<0>(x[1][c >> 1], s[1], z[1]);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) mma16<false>(o[m][4 * i + c], p[m], b0, b1);
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t b0[2] = {bytes<0>(x[0][c], s[0], z[0]), bytes<0>(x[1][c], s[1], z[1])};
+          const uint32_t b1[2] = {bytes<1>(x[0][c], s[0], z[0]), bytes<1>(x[1][c], s[1], z[1])};
+          step(2 * i + c, b0, b1);
         }
       }
     } else {
@@ -299,16 +328,17 @@ __device__ __forceinline__ void rows_values(uint32_t st, const LaneOffsets<D, FM
           x[h][1] = __byte_perm(w[2 * h][i], w[2 * h + 1][i], 0x7632);
         }
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t b[2];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t b[2][2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t y = x[h][c & 1];
-            b[h] = c < 2 ? nibbles<0>(y, s[h], z[h]) : c < 4 ? nibbles<1>(y, s[h], z[h])
-                 : c < 6 ? nibbles<2>(y, s[h], z[h]) : nibbles<3>(y, s[h], z[h]);
-          }
+          for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int m = 0; m < MT; ++m) mma16<false>(o[m][8 * i + c], p[m], b[0], b[1]);
+            for (int h = 0; h < 2; ++h)
+              b[y][h] = c == 0   ? nibbles<0>(x[h][y], s[h], z[h])
+                        : c == 1 ? nibbles<1>(x[h][y], s[h], z[h])
+                        : c == 2 ? nibbles<2>(x[h][y], s[h], z[h])
+                                 : nibbles<3>(x[h][y], s[h], z[h]);
+          step(4 * i + c, b[0], b[1]);
         }
       }
     }
@@ -326,13 +356,13 @@ __device__ __forceinline__ float row_factor(const AttnArgs& a, int E) {
 // bf16 row is scaled by the power of two that puts its largest magnitude in
 // [2^14, 2^15), so that nothing overflows and its 8 significant bits survive
 // down to 2^-28 of the largest.
-template <int D, int FMT>
+template <int D, int FMT, bool TURNED>
 __device__ __forceinline__ void load_queries(const AttnArgs& a, const Piece& p, int m, int lane, uint32_t sq, float* sc) {
   using F = Fmt<FMT>;
   const int g = lane >> 2, t = lane & 3;
   uint32_t q[D / 16][4];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
+  for (int e = 0; e < (TURNED ? 1 : 2); ++e) {
     const int r = p.r0 + min(m * 16 + g + 8 * e, p.rows - 1);
     const uint16_t* row = static_cast<const uint16_t*>(a.q) + (long)(p.s.s0 + r / a.rep) * a.q_stride +
                           (long)(p.head * a.rep + r % a.rep) * D;
@@ -380,10 +410,14 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Piece& p, 
     if (t == 0) sc[m * 16 + g + 8 * e] = f;
   }
 #pragma unroll
-  for (int ks = 0; ks < D / 16; ++ks)
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(sq + (m * (D / 16) + ks) * 512 + lane * 16), "r"(q[ks][0]),
-                 "r"(q[ks][1]), "r"(q[ks][2]), "r"(q[ks][3])
-                 : "memory");
+  for (int ks = 0; ks < D / 16; ++ks) {
+    if constexpr (TURNED)
+      asm volatile("st.shared.v2.b32 [%0], {%1,%2};\n" ::"r"(sq + ks * 256 + lane * 8), "r"(q[ks][0]), "r"(q[ks][2]) : "memory");
+    else
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(sq + (m * (D / 16) + ks) * 512 + lane * 16), "r"(q[ks][0]),
+                   "r"(q[ks][1]), "r"(q[ks][2]), "r"(q[ks][3])
+                   : "memory");
+  }
 }
 
 template <int D, int FMT, int MT>
@@ -391,11 +425,13 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
   using C = RowsCfg<D, FMT, MT>;
   using F = Fmt<FMT>;
   constexpr int ROWS = C::ROWS, NS = C::NS, BK = C::BK, RECS = C::RECS, STEP = C::STEP;
+  constexpr int NM = C::NM, NO = C::NO;
+  constexpr bool TURNED = C::kTurned;
   extern __shared__ __align__(1024) char smem[];
   __shared__ Work<BK, ROWS> work;
   __shared__ Piece piece;
   __shared__ float row_scale[ROWS];
-  __shared__ __align__(16) uint4 queries[MT * (D / 16) * 32];
+  __shared__ __align__(16) uint32_t queries[NM * (D / 16) * 32 * C::QW];
   __shared__ __align__(8) uint64_t bars[kRowsWarps * NS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
   const int g = lane >> 2, t = lane & 3;
@@ -452,23 +488,25 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
     __syncwarp();
     int next = lane < RECS && j + NS < nt ? page_of(tok0 + BK * (j + NS) + lane * 16) : 0;
 
-    if (warp < MT) load_queries<D, FMT>(a, p, warp, lane, sq, row_scale);
+    if (warp < NM) load_queries<D, FMT, TURNED>(a, p, warp, lane, sq, row_scale);
     __syncthreads();
-    float sc[MT][2];
-    float o[MT][D / 8][4], mx[MT][2], sum[MT][2];
-    int pos[MT][2];
+    // a lane's two rows of a tile
+    auto row_at = [&](int m, int e) { return TURNED ? 2 * t + e : m * 16 + g + 8 * e; };
+    float sc[NM][2];
+    float o[NM][NO][4], mx[NM][2], sum[NM][2];
+    int pos[NM][2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int m = 0; m < NM; ++m) {
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
+      for (int i = 0; i < NO; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[m][i][e] = 0.0f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         mx[m][e] = -INFINITY;
         sum[m][e] = 0.0f;
-        sc[m][e] = row_scale[m * 16 + g + 8 * e];
-        pos[m][e] = p.s.p0 + (p.r0 + min(m * 16 + g + 8 * e, p.rows - 1)) / a.rep;
+        sc[m][e] = row_scale[row_at(m, e)];
+        pos[m][e] = p.s.p0 + (p.r0 + min(row_at(m, e), p.rows - 1)) / a.rep;
       }
     }
     const int pos_lo = p.s.p0 + p.r0 / a.rep, pos_hi = p.s.p0 + (p.r0 + p.rows - 1) / a.rep;
@@ -501,31 +539,37 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
         fence_async();
         __syncwarp();
       }
-      float acc[RECS][MT][2][4];
+      // scores: acc[..][h][2 e + i] is row e of the lane, its token h, i; turned
+      // acc[..][0][2 h + e] is token h of row e (no second tile)
+      constexpr int NH = TURNED ? 1 : 2;
+      float acc[RECS][NM][2][4];
 #pragma unroll
       for (int x = 0; x < RECS; ++x) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < NM; ++m)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < NH; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[x][m][h][e] = 0.0f;
         rows_scores<D, FMT, MT>(st + x * C::REC, a.pv.L, offs, sq, lane, acc[x]);
       }
       const bool edge = tok + STEP - 1 > pos_lo || (a.window > 0 && tok <= pos_hi - a.window);
       bool grow = false;
-      float top[MT][2];
+      float top[NM][2];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
+      for (int m = 0; m < NM; ++m) {
         if (edge) {
 #pragma unroll
           for (int x = 0; x < RECS; ++x)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < NH; ++h)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const int c = tok + 16 * x + 8 * h + (F::kQuant ? t + 4 * (e & 1) : 2 * t + (e & 1));
-                const int at = pos[m][e >> 1];
+                const int c = tok + 16 * x +
+                              (TURNED      ? 8 * (e >> 1) + (F::kQuant ? (g >> 1) + 4 * (g & 1) : g)
+                               : F::kQuant ? 8 * h + t + 4 * (e & 1)
+                                           : 8 * h + 2 * t + (e & 1));
+                const int at = pos[m][TURNED ? e & 1 : e >> 1];
                 if (c > at || (a.window > 0 && c <= at - a.window)) acc[x][m][h][e] = -INFINITY;
               }
         }
@@ -535,34 +579,61 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
 #pragma unroll
           for (int y = 0; y < RECS; ++y)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) x = fmaxf(fmaxf(x, acc[y][m][h][2 * e]), acc[y][m][h][2 * e + 1]);
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            for (int h = 0; h < NH; ++h)
+              x = TURNED ? fmaxf(fmaxf(x, acc[y][m][0][e]), acc[y][m][0][2 + e])
+                         : fmaxf(fmaxf(x, acc[y][m][h][2 * e]), acc[y][m][h][2 * e + 1]);
+          if (!TURNED) {
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          }
           top[m][e] = x * sc[m][e];
           grow = grow || top[m][e] > mx[m][e] + 8.0f;
         }
       }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < NM; ++m)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+            if (TURNED) {  // (a row's tokens lie in eight lanes; only now do they have to agree)
+#pragma unroll
+              for (int w = 4; w < 32; w <<= 1) top[m][e] = fmaxf(top[m][e], __shfl_xor_sync(0xffffffffu, top[m][e], w));
+            }
             const float to = fmaxf(mx[m][e], top[m][e]);
             const float f = to == -INFINITY ? 1.0f : fast_exp2(mx[m][e] - to);
             mx[m][e] = to;
             sum[m][e] *= f;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              o[m][i][2 * e] *= f;
-              o[m][i][2 * e + 1] *= f;
+            for (int i = 0; i < NO; ++i) {
+              o[m][i][TURNED ? e : 2 * e] *= f;
+              o[m][i][TURNED ? 2 + e : 2 * e + 1] *= f;
             }
           }
       }
 #pragma unroll
       for (int x = 0; x < RECS; ++x) {
-        uint32_t pa[MT][4], pr[MT][4];
+        uint32_t pa[NM][4], pr[NM][4];
+        if constexpr (TURNED) {
+          const float b0 = mx[0][0] == -INFINITY ? 0.0f : mx[0][0] - 7.0f;
+          const float b1 = mx[0][1] == -INFINITY ? 0.0f : mx[0][1] - 7.0f;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+          for (int h = 0; h < 2; ++h) {
+            const float u = fast_exp2(fmaf(acc[x][0][0][2 * h], sc[0][0], -b0));
+            const float v = fast_exp2(fmaf(acc[x][0][0][2 * h + 1], sc[0][1], -b1));
+            sum[0][0] += u;
+            sum[0][1] += v;
+            const uint32_t w = pack2<F::kBf16>(u, v);
+            pa[0][h] = transpose8x8(w);
+            if constexpr (C::kSplit) {
+              float2 back;
+              if (F::kBf16) back = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+              else back = __half22float2(as_h2(w));
+              pr[0][h] = transpose8x8(pack2<F::kBf16>(u - back.x, v - back.y));
+            }
+          }
+        } else
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float base = mx[m][e] == -INFINITY ? 0.0f : mx[m][e] - 7.0f;
@@ -600,17 +671,21 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
     float* mo = reinterpret_cast<float*>(smem);                 // [warp][ROWS][D]
     float* ml = mo + kRowsWarps * ROWS * D;                     // [warp][ROWS][2]
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < NM; ++m)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float s = sum[m][e];
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        const int r = warp * ROWS + m * 16 + g + 8 * e;
-        if (t == 0) ml[2 * r] = mx[m][e], ml[2 * r + 1] = s;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          if (F::kQuant) {
+        for (int w = TURNED ? 4 : 1; w < (TURNED ? 32 : 4); w <<= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+        const int r = warp * ROWS + row_at(m, e);
+        if ((TURNED ? g : t) == 0) ml[2 * r] = mx[m][e], ml[2 * r + 1] = s;
+#pragma unroll
+        for (int i = 0; i < NO; ++i) {
+          if (TURNED) {
+            const int c = F::kQuant ? g * (D / 8) + 2 * i : 16 * i + g;
+            mo[r * D + c] = o[m][i][e];
+            mo[r * D + c + (F::kQuant ? 1 : 8)] = o[m][i][2 + e];
+          } else if (F::kQuant) {
             mo[r * D + 2 * t * (D / 8) + i] = o[m][i][2 * e];
             mo[r * D + (2 * t + 1) * (D / 8) + i] = o[m][i][2 * e + 1];
           } else {
@@ -661,6 +736,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
 
 template <int D, int FMT>
 AttnKernel rows_kernel_fmt(int mt) {
+  if (mt == 0) return {(const void*)pages_rows_kernel<D, FMT, 0>, (size_t)RowsCfg<D, FMT, 0>::SMEM, kRowsWarps * 32, 0, 0};
   if constexpr (D <= 128)
     if (mt == 2) return {(const void*)pages_rows_kernel<D, FMT, 2>, (size_t)RowsCfg<D, FMT, 2>::SMEM, kRowsWarps * 32, 0, 0};
   return {(const void*)pages_rows_kernel<D, FMT, 1>, (size_t)RowsCfg<D, FMT, 1>::SMEM, kRowsWarps * 32, 0, 0};

@@ -127,7 +127,7 @@ struct kvq_pages {
   int sm_smem = 0, cta_smem = 0;  // shared memory of an SM, of it reserved per CTA
   int max_smem = 0;               // most that a CTA may have
   int which = 0;     // kernel choice (kvq_pages_set_kernel)
-  kvq::AttnKernel rows_fn[3] = {};  // few-rows kernel: up to 8 rows, one and two row tiles (not two at head_dim 256)
+  kvq::AttnKernel rows_fn[4] = {};  // few-rows kernel for 8, 16, 24 and 32 rows (8 and 16 at head_dim 256)
   kvq::AttnKernel tile_fn = {};     // many-rows kernel
   std::string last_error;
 };
@@ -143,12 +143,12 @@ cudaError_t launch_pages_read(const PagesView& pv, const BatchView& bv, void* k_
 cudaError_t launch_norm_rope(const kvq_norm_rope_args& a, const RopeView& rv, cudaStream_t st);
 
 // the few-rows kernel of each head_dim (one translation unit each) for a page
-// format and number of row tiles
+// format and number of row tiles of 8
 enum { kFmtF16 = 0, kFmtBf16 = 1, kFmt88 = 2, kFmt44 = 3, kFmt84 = 4, kFmt48 = 5, kFormats = 6 };
 int pages_format(const kvq_pages* P);
-AttnKernel rows_kernel_d64(int fmt, int mt);
-AttnKernel rows_kernel_d128(int fmt, int mt);
-AttnKernel rows_kernel_d256(int fmt, int mt);
+AttnKernel rows_kernel_d64(int fmt, int nm);
+AttnKernel rows_kernel_d128(int fmt, int nm);
+AttnKernel rows_kernel_d256(int fmt, int nm);
 AttnKernel tile_kernel_d64(int fmt);
 AttnKernel tile_kernel_d128(int fmt);
 AttnKernel tile_kernel_d256(int fmt);

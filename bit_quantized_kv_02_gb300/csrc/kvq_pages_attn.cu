@@ -82,6 +82,7 @@ const void* join_dim(int rows) {
   switch (rows) {
     case 8: return (const void*)pages_join_kernel<D, 8>;
     case 16: return (const void*)pages_join_kernel<D, 16>;
+    case 24: return (const void*)pages_join_kernel<D, 24>;
     case 32: return (const void*)pages_join_kernel<D, 32>;
     case 128: return (const void*)pages_join_kernel<D, 128>;
     default: return (const void*)pages_join_kernel<D, 256>;
@@ -109,15 +110,16 @@ cudaError_t launch_kernel(const AttnKernel& k, AttnArgs a, int ctas, int rows, i
 }
 
 cudaError_t launch_rows(kvq_pages* P, AttnArgs a, int max_rows, cudaStream_t st) {
-  // Up to 8 rows the products are turned (4-bit pages, 32 sequences of 4096 tokens,
-  // turned / one row tile, us: heads of 64 60 / 69, of 128 55 / 86, of 256 36 / 41;
-  // 16-bit 69 / 72, 89 / 89, 52 / 53).  Two row tiles per warp where a sequence may
-  // have more rows than one holds: the cache is then read once for 32 rows (5
-  // drafted tokens, 20 rows, over 8-bit pages: 66 us, with one row tile 98).
-  const int mt = max_rows <= 8 ? 0 : (max_rows > 16 && P->rows_fn[2].fn ? 2 : 1);
-  const AttnKernel& k = P->rows_fn[mt];
+  // As few row tiles of 8 as hold a sequence's rows, up to 32 rows (16 at head_dim
+  // 256): the cache is then read once for all of them, and no product is made for
+  // rows that are not there.  32 sequences of 4096 4-bit tokens, 8 / 16 / 24 / 32
+  // rows, us: heads of 64 49 / 60 / 71 / 86, of 128 56 / 71 / 78 / 99, of 256
+  // 37 / 44; 20 rows over 8-bit pages 60, in two turns of 16 rows 94.
+  const int most = P->cfg.head_dim == 256 ? 16 : kRowsPerCta;
+  const int blocks = (max_rows + most - 1) / most, nm = ((max_rows + blocks - 1) / blocks + 7) / 8;
+  const AttnKernel& k = P->rows_fn[nm - 1];
   a.min_units = 2;
-  return launch_kernel(k, a, std::min(resident(P, k, a.bv.batch) * P->sm_count, kPagesCtas), mt ? 16 * mt : 8, max_rows, st);
+  return launch_kernel(k, a, std::min(resident(P, k, a.bv.batch) * P->sm_count, kPagesCtas), 8 * nm, max_rows, st);
 }
 
 cudaError_t launch_tile(kvq_pages* P, AttnArgs a, int max_rows, cudaStream_t st) {
@@ -142,14 +144,14 @@ int pages_format(const kvq_pages* P) {
 
 cudaError_t pages_attn_setup(kvq_pages* P) {
   const int D = P->cfg.head_dim, fmt = pages_format(P);
-  for (int mt = 0; mt < (D < 256 ? 3 : 2); ++mt)
-    P->rows_fn[mt] = D == 64 ? rows_kernel_d64(fmt, mt) : D == 128 ? rows_kernel_d128(fmt, mt) : rows_kernel_d256(fmt, mt);
+  for (int nm = 1; nm <= (D < 256 ? 4 : 2); ++nm)
+    P->rows_fn[nm - 1] = D == 64 ? rows_kernel_d64(fmt, nm) : D == 128 ? rows_kernel_d128(fmt, nm) : rows_kernel_d256(fmt, nm);
   P->tile_fn = D == 64 ? tile_kernel_d64(fmt) : D == 128 ? tile_kernel_d128(fmt) : tile_kernel_d256(fmt);
   cudaError_t e = cudaDeviceGetAttribute(&P->sm_smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor, P->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P->cta_smem, cudaDevAttrReservedSharedMemoryPerBlock, P->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P->max_smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, P->device);
   if (e != cudaSuccess) return e;
-  for (AttnKernel* k : {&P->rows_fn[0], &P->rows_fn[1], &P->rows_fn[2], &P->tile_fn}) {
+  for (AttnKernel* k : {&P->rows_fn[0], &P->rows_fn[1], &P->rows_fn[2], &P->rows_fn[3], &P->tile_fn}) {
     if (!k->fn) continue;
     cudaFuncAttributes at;
     e = cudaFuncGetAttributes(&at, k->fn);
@@ -167,13 +169,13 @@ cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, int max_rows, cudaStrea
   // Sequences with at most `few` rows (new tokens x query heads per kv head) go to
   // the few-rows kernel, the others to the many-rows one; a batch that may hold
   // both kinds launches both.  Measured, few / many rows, us, 8 sequences of 8192
-  // tokens: 16-bit pages, 12 heads of 64: 32 rows 47 / 68, 48 rows 87 / 69; 8 heads
-  // of 128: 55 / 65, 96 / 66; 2 heads of 256: 44 / 50, 56 / 52.  Codes cost the
+  // tokens: 16-bit pages, 12 heads of 64: 32 rows 52 / 68, 48 rows 86 / 69; 8 heads
+  // of 128: 57 / 66, 96 / 67; 2 heads of 256: 48 / 51, 61 / 53.  Codes cost the
   // many-rows kernel its dequantizing warps: 4 bits, heads of 64: 128 rows
-  // 124 / 159, 192 rows 182 / 189, 256 rows 235 / 194; heads of 128: 64 rows
-  // 85 / 100, 96 rows 114 / 103; heads of 256: 48 rows 55 / 60, 64 rows 65 / 61.
+  // 138 / 159, 192 rows 204 / 189; heads of 128: 64 rows 91 / 99, 96 rows 125 / 103;
+  // heads of 256: 48 rows 57 / 61, 64 rows 67 / 62.
   const int D = P->cfg.head_dim;
-  const int few = P->L.k_bits == 16 ? 32 : (D == 64 ? 192 : (D == 128 ? 64 : 48));
+  const int few = P->L.k_bits == 16 ? 32 : (D == 64 ? 128 : (D == 128 ? 64 : 48));
   a.rows_lo = 0;
   a.rows_hi = INT_MAX;
   if (P->which == 1 || (P->which == 0 && max_rows <= few)) return launch_rows(P, a, max_rows, st);

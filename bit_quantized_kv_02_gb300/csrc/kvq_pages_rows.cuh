@@ -4,25 +4,24 @@
 // A CTA of four warps walks its units of 64 or 128 tokens; each warp takes a
 // quarter, one or two records, brought by bulk copies into the warp's own ring
 // of stages, and runs an independent softmax over its tokens, so nothing but the
-// end of an item synchronises the warps.  Query rows are the 16 rows of
-// m16n8k16 (MT tiles of them), so all query heads of a kv head and several new
-// tokens share one read of the cache.  Up to 8 rows are its columns instead (MT
-// 0): half the products, operands and accumulators, and the exchange of a row's
-// maximum only where it has to grow; keys and values become the left operand from
-// the same registers, and the weights are turned by two 8x8 transposes.
+// end of an item synchronises the warps.  Query rows are the 8 columns of
+// m16n8k16 (NM tiles of them), so all query heads of a kv head and several new
+// tokens share one read of the cache; keys and values are its left operand, the
+// weights are turned by an 8x8 transpose for the second product, and a row's
+// maximum, whose tokens lie in eight lanes, is exchanged only where it grows.
 //  - 16-bit pages: ldmatrix reads keys and (transposed) values straight from
 //    the swizzled rows.
 //  - codes: the contraction does not care about the order of channels, tokens
-//    or output columns, so each lane is given runs that are contiguous in
-//    memory: keys, channels t*D/4 .. of token (n>>1) + 4*(n&1) (n: the lane's
-//    column, t = lane % 4); values, channels g*D/8 .. (g = lane / 4) of tokens
+//    or output channels, so each lane is given runs that are contiguous in
+//    memory: keys, channels t*D/4 .. of token (g>>1) + 4*(g&1) (g = lane / 4, t =
+//    lane % 4); values, channels g*D/8 .. of tokens
 //    t, t+4, t+8, t+12.  Each run lies in one group (or two), so a lane needs
 //    one (zero, step) per token.  Codes become fp16 by an or with 1024's bits
 //    and one exact subtraction; zero + code * step is one fp16 fma, the value
 //    that the page stands for.
 // Scores, maxima, sums and outputs are fp32.  Weights enter the value product
 // as p * 2^7 with a maximum that lags by up to 2^8, so that fp16 weights stay
-// normal down to 2^-21 of the largest.  Over 16-bit pages with one row tile they
+// normal down to 2^-21 of the largest.  Over 16-bit pages with up to 16 rows they
 // are split into the operand type and its remainder (a second product, hidden
 // behind the reads); elsewhere they are rounded to the operand type (fp16, or
 // bf16 for bf16 pages), which adds about as much to the error as the output's own
@@ -31,9 +30,12 @@
 // Measured: 16 sequences of 4113 bf16 tokens, 40 heads of 128: 207 us, 96 % of a
 // copy's bandwidth.  64 sequences of 1k to 32k 4-bit tokens, 32 query heads over 8
 // of 128: 315 us, 59 % (375 with 16 rows and three CTAs per SM in place of 8 and
-// four; 330 with 8 rows and five): a record of codes costs about as many
+// four; 330 with 8 rows and five CTAs): a record of codes costs about as many
 // instructions whatever the rows are, and fixed-latency waits take the slots that
-// are left.  5 drafted tokens over 8-bit pages: 66 us (floor 29), two CTAs per SM.
+// are left.  5 drafted tokens, 20 rows, over 8-bit pages: 60 us (floor 29), two
+// CTAs per SM; 66 as two 16-row operands.  (That form, the rows as the left
+// operand, was 90 us against 99 for a full 32 rows of 32 sequences of 4096 4-bit
+// tokens, heads of 128, but 88 against 71 for 16 and 86 against 56 for 8.)
 // 8 sequences of 2048 fp16 tokens, 12 heads of 64: 15 us in a graph, of which 9 are
 // launch, plan and join.
 #pragma once
@@ -54,20 +56,16 @@ struct Fmt {
   static constexpr bool kQuant = KB < 16;
 };
 
-template <int D, int FMT, int MT>
+template <int D, int FMT, int NM>
 struct RowsCfg {
   using F = Fmt<FMT>;
-  static constexpr bool kTurned = MT == 0;  // the rows are the products' 8 columns
-  static constexpr int ROWS = kTurned ? 8 : 16 * MT;
-  static constexpr int NM = kTurned ? 1 : MT;           // row tiles
-  static constexpr int NO = kTurned ? D / 16 : D / 8;   // accumulator tiles of a row tile
-  static constexpr int QW = kTurned ? 2 : 4;            // words of a lane's query operand
+  static constexpr int ROWS = 8 * NM;
   // a record with the most metadata (groups of 32)
   static constexpr int REC = 2 * D * (F::KB + F::VB) + (F::kQuant ? 2 * 16 * (D / 32) * 4 : 0);
   // CTAs per SM that registers and shared memory are cut for
-  static constexpr int CTAS = kTurned && F::kQuant ? (D == 256 ? 3 : 4)
-                              : MT == 2            ? (D == 64 ? 3 : 2)
-                                                   : (D == 64 ? 4 : (D == 128 && F::kQuant ? 3 : 2));
+  static constexpr int CTAS = D == 64    ? (NM <= 2 ? 4 : 3)
+                              : D == 128 ? (F::kQuant && NM <= 2 ? 5 - NM : 2)
+                                         : (F::kQuant && NM == 1 ? 3 : 2);
   static constexpr int BUDGET = CTAS == 4 ? 12544 : (CTAS == 3 ? 16384 : 24576);  // bytes of a warp's ring
   // records of a warp's step and stage: two where two such stages fit, so that
   // the softmax's exchanges and the loop cost half as much per token
@@ -75,7 +73,7 @@ struct RowsCfg {
   static constexpr int STEP = 16 * RECS, BK = STEP * kRowsWarps;  // tokens of a step and of a unit
   static constexpr int STAGE = RECS * REC;
   static constexpr int NS = BUDGET / STAGE < 2 ? 2 : (BUDGET / STAGE > 4 ? 4 : BUDGET / STAGE);
-  static constexpr bool kSplit = !F::kQuant && MT <= 1;  // weights as operand + remainder
+  static constexpr bool kSplit = !F::kQuant && NM <= 2;  // weights as operand + remainder
   static constexpr int RING = kRowsWarps * NS * STAGE;
   static constexpr int MERGE = kRowsWarps * ROWS * (D + 2) * 4;
   static constexpr int SMEM = (RING > MERGE ? RING : MERGE);
@@ -184,27 +182,21 @@ struct LaneOffsets {
   }
 };
 
-// One 16-token record's scores: acc[m][n8 tile] += Q K^T, or turned acc[0][0] +=
-// K Q^T.  sq: the query operands in shared memory, [m][mma step][lane].
-template <int D, int FMT, int MT>
+// One 16-token record's scores: acc[m] += K Q_m^T.  sq: the query operands in
+// shared memory, [m][mma step][lane] of two words.
+template <int D, int FMT, int NM>
 __device__ __forceinline__ void rows_scores(uint32_t st, const PagesLayout& L, const LaneOffsets<D, FMT>& lo,
-                                            uint32_t sq, int lane, float (*acc)[2][4]) {
+                                            uint32_t sq, int lane, float (*acc)[4]) {
   using F = Fmt<FMT>;
-  using C = RowsCfg<D, FMT, MT>;
-  const uint32_t qa = sq + lane * (C::QW * 4);
+  const uint32_t qa = sq + lane * 8;
   // keys of tokens 0..7 and 8..15 (two words each) of a step
   auto step = [&](int ks, const uint32_t* b0, const uint32_t* b1) {
+    const uint32_t k[4] = {b0[0], b1[0], b0[1], b1[1]};
 #pragma unroll
-    for (int m = 0; m < C::NM; ++m) {
-      uint32_t q[C::QW];
-      ldsv<C::QW>(qa + (m * (D / 16) + ks) * (C::QW * 128), q);
-      if constexpr (C::kTurned) {
-        const uint32_t k[4] = {b0[0], b1[0], b0[1], b1[1]};
-        mma16<F::kBf16>(acc[m][0], k, q[0], q[1]);
-      } else {
-        mma16<F::kBf16>(acc[m][0], q, b0[0], b0[1]);
-        mma16<F::kBf16>(acc[m][1], q, b1[0], b1[1]);
-      }
+    for (int m = 0; m < NM; ++m) {
+      uint32_t q[2];
+      ldsv<2>(qa + (m * (D / 16) + ks) * 256, q);
+      mma16<F::kBf16>(acc[m], k, q[0], q[1]);
     }
   };
   if constexpr (!F::kQuant) {
@@ -253,29 +245,18 @@ __device__ __forceinline__ void rows_scores(uint32_t st, const PagesLayout& L, c
   }
 }
 
-// o[m][n8 tile] += P V of one record; p: the probabilities as operands.  Turned:
-// o[0][m16 tile] += V^T P^T.
-template <int D, int FMT, int MT>
-__device__ __forceinline__ void rows_values(uint32_t st, const LaneOffsets<D, FMT>& lo, const uint32_t (*p)[4],
-                                            const uint32_t (*rest)[4], int lane, float (*o)[RowsCfg<D, FMT, MT>::NO][4]) {
+// o[m][16 channels] += V^T P_m^T of one record; p: the weights as operands.
+template <int D, int FMT, int NM>
+__device__ __forceinline__ void rows_values(uint32_t st, const LaneOffsets<D, FMT>& lo, const uint32_t (*p)[2],
+                                            const uint32_t (*rest)[2], int lane, float (*o)[D / 16][4]) {
   using F = Fmt<FMT>;
-  using C = RowsCfg<D, FMT, MT>;
-  // column tiles 2j and 2j + 1: values of tokens 0..7 and 8..15 (one word each)
+  // channels 0..7 and 8..15 of step j: values of tokens 0..7 and 8..15 (a word each)
   auto step = [&](int j, const uint32_t* b0, const uint32_t* b1) {
-    if constexpr (C::kTurned) {
-      const uint32_t v[4] = {b0[0], b1[0], b0[1], b1[1]};
-      mma16<F::kBf16>(o[0][j], v, p[0][0], p[0][1]);
-      if constexpr (C::kSplit) mma16<F::kBf16>(o[0][j], v, rest[0][0], rest[0][1]);
-    } else {
+    const uint32_t v[4] = {b0[0], b1[0], b0[1], b1[1]};
 #pragma unroll
-      for (int m = 0; m < C::NM; ++m) {
-        mma16<F::kBf16>(o[m][2 * j], p[m], b0[0], b0[1]);
-        mma16<F::kBf16>(o[m][2 * j + 1], p[m], b1[0], b1[1]);
-        if constexpr (C::kSplit) {
-          mma16<F::kBf16>(o[m][2 * j], rest[m], b0[0], b0[1]);
-          mma16<F::kBf16>(o[m][2 * j + 1], rest[m], b1[0], b1[1]);
-        }
-      }
+    for (int m = 0; m < NM; ++m) {
+      mma16<F::kBf16>(o[m][j], v, p[m][0], p[m][1]);
+      if constexpr (RowsCfg<D, FMT, NM>::kSplit) mma16<F::kBf16>(o[m][j], v, rest[m][0], rest[m][1]);
     }
   };
   if constexpr (!F::kQuant) {
@@ -356,82 +337,72 @@ __device__ __forceinline__ float row_factor(const AttnArgs& a, int E) {
 // bf16 row is scaled by the power of two that puts its largest magnitude in
 // [2^14, 2^15), so that nothing overflows and its 8 significant bits survive
 // down to 2^-28 of the largest.
-template <int D, int FMT, bool TURNED>
+template <int D, int FMT>
 __device__ __forceinline__ void load_queries(const AttnArgs& a, const Piece& p, int m, int lane, uint32_t sq, float* sc) {
   using F = Fmt<FMT>;
   const int g = lane >> 2, t = lane & 3;
-  uint32_t q[D / 16][4];
+  uint32_t q[D / 16][2];
+  const int r = p.r0 + min(m * 8 + g, p.rows - 1);
+  const uint16_t* row = static_cast<const uint16_t*>(a.q) + (long)(p.s.s0 + r / a.rep) * a.q_stride +
+                        (long)(p.head * a.rep + r % a.rep) * D;
+  auto pair = [&](int c) -> uint32_t {
+    if (a.q_aligned) return *reinterpret_cast<const uint32_t*>(row + c);
+    return (uint32_t)row[c] | (uint32_t)row[c + 1] << 16;
+  };
+  float f = a.scale_log2;
+  if constexpr (!F::kQuant) {
 #pragma unroll
-  for (int e = 0; e < (TURNED ? 1 : 2); ++e) {
-    const int r = p.r0 + min(m * 16 + g + 8 * e, p.rows - 1);
-    const uint16_t* row = static_cast<const uint16_t*>(a.q) + (long)(p.s.s0 + r / a.rep) * a.q_stride +
-                          (long)(p.head * a.rep + r % a.rep) * D;
-    auto pair = [&](int c) -> uint32_t {
-      if (a.q_aligned) return *reinterpret_cast<const uint32_t*>(row + c);
-      return (uint32_t)row[c] | (uint32_t)row[c + 1] << 16;
-    };
-    float f = a.scale_log2;
-    if constexpr (!F::kQuant) {
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        q[ks][e] = pair(ks * 16 + 2 * t);
-        q[ks][2 + e] = pair(ks * 16 + 8 + 2 * t);
-      }
-    } else {
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        q[ks][e] = pair(t * (D / 4) + 4 * ks);
-        q[ks][2 + e] = pair(t * (D / 4) + 4 * ks + 2);
-      }
-      if (a.q_bf16) {
-        float mx = 0.0f;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t w = q[ks][e + 2 * i];
-            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))));
-          }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int E = norm_exp(mx);
-        // 2^E in two factors: E may pass the range of one float
-        const float f0 = exp2i(E / 2), f1 = exp2i(E - E / 2);
-        f = row_factor(a, E);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t w = q[ks][e + 2 * i];
-            q[ks][e + 2 * i] = pack2<false>(__uint_as_float(w << 16) * f0 * f1, __uint_as_float(w & 0xffff0000u) * f0 * f1);
-          }
-      }
+    for (int ks = 0; ks < D / 16; ++ks) {
+      q[ks][0] = pair(ks * 16 + 2 * t);
+      q[ks][1] = pair(ks * 16 + 8 + 2 * t);
     }
-    if (t == 0) sc[m * 16 + g + 8 * e] = f;
-  }
+  } else {
 #pragma unroll
-  for (int ks = 0; ks < D / 16; ++ks) {
-    if constexpr (TURNED)
-      asm volatile("st.shared.v2.b32 [%0], {%1,%2};\n" ::"r"(sq + ks * 256 + lane * 8), "r"(q[ks][0]), "r"(q[ks][2]) : "memory");
-    else
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(sq + (m * (D / 16) + ks) * 512 + lane * 16), "r"(q[ks][0]),
-                   "r"(q[ks][1]), "r"(q[ks][2]), "r"(q[ks][3])
-                   : "memory");
+    for (int ks = 0; ks < D / 16; ++ks) {
+      q[ks][0] = pair(t * (D / 4) + 4 * ks);
+      q[ks][1] = pair(t * (D / 4) + 4 * ks + 2);
+    }
+    if (a.q_bf16) {
+      float mx = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t w = q[ks][i];
+          mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))));
+        }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int E = norm_exp(mx);
+      // 2^E in two factors: E may pass the range of one float
+      const float f0 = exp2i(E / 2), f1 = exp2i(E - E / 2);
+      f = row_factor(a, E);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t w = q[ks][i];
+          q[ks][i] = pack2<false>(__uint_as_float(w << 16) * f0 * f1, __uint_as_float(w & 0xffff0000u) * f0 * f1);
+        }
+    }
   }
+  if (t == 0) sc[m * 8 + g] = f;
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks)
+    asm volatile("st.shared.v2.b32 [%0], {%1,%2};\n" ::"r"(sq + (m * (D / 16) + ks) * 256 + lane * 8), "r"(q[ks][0]), "r"(q[ks][1])
+                 : "memory");
 }
 
-template <int D, int FMT, int MT>
-__global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pages_rows_kernel(const __grid_constant__ AttnArgs a) {
-  using C = RowsCfg<D, FMT, MT>;
+template <int D, int FMT, int NM>
+__global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pages_rows_kernel(const __grid_constant__ AttnArgs a) {
+  using C = RowsCfg<D, FMT, NM>;
   using F = Fmt<FMT>;
   constexpr int ROWS = C::ROWS, NS = C::NS, BK = C::BK, RECS = C::RECS, STEP = C::STEP;
-  constexpr int NM = C::NM, NO = C::NO;
-  constexpr bool TURNED = C::kTurned;
   extern __shared__ __align__(1024) char smem[];
   __shared__ Work<BK, ROWS> work;
   __shared__ Piece piece;
   __shared__ float row_scale[ROWS];
-  __shared__ __align__(16) uint32_t queries[NM * (D / 16) * 32 * C::QW];
+  __shared__ __align__(16) uint32_t queries[NM * (D / 16) * 64];
   __shared__ __align__(8) uint64_t bars[kRowsWarps * NS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
   const int g = lane >> 2, t = lane & 3;
@@ -488,17 +459,16 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
     __syncwarp();
     int next = lane < RECS && j + NS < nt ? page_of(tok0 + BK * (j + NS) + lane * 16) : 0;
 
-    if (warp < NM) load_queries<D, FMT, TURNED>(a, p, warp, lane, sq, row_scale);
+    if (warp < NM) load_queries<D, FMT>(a, p, warp, lane, sq, row_scale);
     __syncthreads();
-    // a lane's two rows of a tile
-    auto row_at = [&](int m, int e) { return TURNED ? 2 * t + e : m * 16 + g + 8 * e; };
+    auto row_at = [&](int m, int e) { return m * 8 + 2 * t + e; };  // a lane's two rows of a tile
     float sc[NM][2];
-    float o[NM][NO][4], mx[NM][2], sum[NM][2];
+    float o[NM][D / 16][4], mx[NM][2], sum[NM][2];
     int pos[NM][2];
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
 #pragma unroll
-      for (int i = 0; i < NO; ++i)
+      for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[m][i][e] = 0.0f;
 #pragma unroll
@@ -539,19 +509,14 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
         fence_async();
         __syncwarp();
       }
-      // scores: acc[..][h][2 e + i] is row e of the lane, its token h, i; turned
-      // acc[..][0][2 h + e] is token h of row e (no second tile)
-      constexpr int NH = TURNED ? 1 : 2;
-      float acc[RECS][NM][2][4];
+      float acc[RECS][NM][4];  // [2 h + e]: the lane's token h, its row e
 #pragma unroll
       for (int x = 0; x < RECS; ++x) {
 #pragma unroll
         for (int m = 0; m < NM; ++m)
 #pragma unroll
-          for (int h = 0; h < NH; ++h)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[x][m][h][e] = 0.0f;
-        rows_scores<D, FMT, MT>(st + x * C::REC, a.pv.L, offs, sq, lane, acc[x]);
+          for (int e = 0; e < 4; ++e) acc[x][m][e] = 0.0f;
+        rows_scores<D, FMT, NM>(st + x * C::REC, a.pv.L, offs, sq, lane, acc[x]);
       }
       const bool edge = tok + STEP - 1 > pos_lo || (a.window > 0 && tok <= pos_hi - a.window);
       bool grow = false;
@@ -562,30 +527,17 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
 #pragma unroll
           for (int x = 0; x < RECS; ++x)
 #pragma unroll
-            for (int h = 0; h < NH; ++h)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int c = tok + 16 * x +
-                              (TURNED      ? 8 * (e >> 1) + (F::kQuant ? (g >> 1) + 4 * (g & 1) : g)
-                               : F::kQuant ? 8 * h + t + 4 * (e & 1)
-                                           : 8 * h + 2 * t + (e & 1));
-                const int at = pos[m][TURNED ? e & 1 : e >> 1];
-                if (c > at || (a.window > 0 && c <= at - a.window)) acc[x][m][h][e] = -INFINITY;
-              }
+            for (int e = 0; e < 4; ++e) {
+              const int c = tok + 16 * x + 8 * (e >> 1) + (F::kQuant ? (g >> 1) + 4 * (g & 1) : g);
+              const int at = pos[m][e & 1];
+              if (c > at || (a.window > 0 && c <= at - a.window)) acc[x][m][e] = -INFINITY;
+            }
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float x = -INFINITY;
 #pragma unroll
-          for (int y = 0; y < RECS; ++y)
-#pragma unroll
-            for (int h = 0; h < NH; ++h)
-              x = TURNED ? fmaxf(fmaxf(x, acc[y][m][0][e]), acc[y][m][0][2 + e])
-                         : fmaxf(fmaxf(x, acc[y][m][h][2 * e]), acc[y][m][h][2 * e + 1]);
-          if (!TURNED) {
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          }
+          for (int y = 0; y < RECS; ++y) x = fmaxf(fmaxf(x, acc[y][m][e]), acc[y][m][2 + e]);
           top[m][e] = x * sc[m][e];
           grow = grow || top[m][e] > mx[m][e] + 8.0f;
         }
@@ -595,64 +547,44 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
         for (int m = 0; m < NM; ++m)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            if (TURNED) {  // (a row's tokens lie in eight lanes; only now do they have to agree)
+            // (a row's tokens lie in eight lanes; only now do they have to agree)
 #pragma unroll
-              for (int w = 4; w < 32; w <<= 1) top[m][e] = fmaxf(top[m][e], __shfl_xor_sync(0xffffffffu, top[m][e], w));
-            }
+            for (int w = 4; w < 32; w <<= 1) top[m][e] = fmaxf(top[m][e], __shfl_xor_sync(0xffffffffu, top[m][e], w));
             const float to = fmaxf(mx[m][e], top[m][e]);
             const float f = to == -INFINITY ? 1.0f : fast_exp2(mx[m][e] - to);
             mx[m][e] = to;
             sum[m][e] *= f;
 #pragma unroll
-            for (int i = 0; i < NO; ++i) {
-              o[m][i][TURNED ? e : 2 * e] *= f;
-              o[m][i][TURNED ? 2 + e : 2 * e + 1] *= f;
+            for (int i = 0; i < D / 16; ++i) {
+              o[m][i][e] *= f;
+              o[m][i][2 + e] *= f;
             }
           }
       }
 #pragma unroll
       for (int x = 0; x < RECS; ++x) {
-        uint32_t pa[NM][4], pr[NM][4];
-        if constexpr (TURNED) {
-          const float b0 = mx[0][0] == -INFINITY ? 0.0f : mx[0][0] - 7.0f;
-          const float b1 = mx[0][1] == -INFINITY ? 0.0f : mx[0][1] - 7.0f;
+        uint32_t pa[NM][2], pr[NM][2];
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+          const float b0 = mx[m][0] == -INFINITY ? 0.0f : mx[m][0] - 7.0f;
+          const float b1 = mx[m][1] == -INFINITY ? 0.0f : mx[m][1] - 7.0f;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float u = fast_exp2(fmaf(acc[x][0][0][2 * h], sc[0][0], -b0));
-            const float v = fast_exp2(fmaf(acc[x][0][0][2 * h + 1], sc[0][1], -b1));
-            sum[0][0] += u;
-            sum[0][1] += v;
+            const float u = fast_exp2(fmaf(acc[x][m][2 * h], sc[m][0], -b0));
+            const float v = fast_exp2(fmaf(acc[x][m][2 * h + 1], sc[m][1], -b1));
+            sum[m][0] += u;
+            sum[m][1] += v;
             const uint32_t w = pack2<F::kBf16>(u, v);
-            pa[0][h] = transpose8x8(w);
+            pa[m][h] = transpose8x8(w);
             if constexpr (C::kSplit) {
               float2 back;
               if (F::kBf16) back = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
               else back = __half22float2(as_h2(w));
-              pr[0][h] = transpose8x8(pack2<F::kBf16>(u - back.x, v - back.y));
+              pr[m][h] = transpose8x8(pack2<F::kBf16>(u - back.x, v - back.y));
             }
           }
-        } else
-#pragma unroll
-        for (int m = 0; m < NM; ++m)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float base = mx[m][e] == -INFINITY ? 0.0f : mx[m][e] - 7.0f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float u = fast_exp2(fmaf(acc[x][m][h][2 * e], sc[m][e], -base));
-              const float v = fast_exp2(fmaf(acc[x][m][h][2 * e + 1], sc[m][e], -base));
-              sum[m][e] += u + v;
-              const uint32_t w = pack2<F::kBf16>(u, v);
-              pa[m][2 * h + e] = w;
-              if constexpr (C::kSplit) {
-                float2 back;
-                if (F::kBf16) back = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-                else back = __half22float2(as_h2(w));
-                pr[m][2 * h + e] = pack2<F::kBf16>(u - back.x, v - back.y);
-              }
-            }
-          }
-        rows_values<D, FMT, MT>(st + x * C::REC, offs, pa, pr, lane, o);
+        }
+        rows_values<D, FMT, NM>(st + x * C::REC, offs, pa, pr, lane, o);
       }
       __syncwarp();
       if (lane < RECS && j + NS < nt) {
@@ -676,21 +608,14 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
       for (int e = 0; e < 2; ++e) {
         float s = sum[m][e];
 #pragma unroll
-        for (int w = TURNED ? 4 : 1; w < (TURNED ? 32 : 4); w <<= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+        for (int w = 4; w < 32; w <<= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
         const int r = warp * ROWS + row_at(m, e);
-        if ((TURNED ? g : t) == 0) ml[2 * r] = mx[m][e], ml[2 * r + 1] = s;
+        if (g == 0) ml[2 * r] = mx[m][e], ml[2 * r + 1] = s;
 #pragma unroll
-        for (int i = 0; i < NO; ++i) {
-          if (TURNED) {
-            const int c = F::kQuant ? g * (D / 8) + 2 * i : 16 * i + g;
-            mo[r * D + c] = o[m][i][e];
-            mo[r * D + c + (F::kQuant ? 1 : 8)] = o[m][i][2 + e];
-          } else if (F::kQuant) {
-            mo[r * D + 2 * t * (D / 8) + i] = o[m][i][2 * e];
-            mo[r * D + (2 * t + 1) * (D / 8) + i] = o[m][i][2 * e + 1];
-          } else {
-            *reinterpret_cast<float2*>(mo + r * D + i * 8 + 2 * t) = make_float2(o[m][i][2 * e], o[m][i][2 * e + 1]);
-          }
+        for (int i = 0; i < D / 16; ++i) {
+          const int c = F::kQuant ? g * (D / 8) + 2 * i : 16 * i + g;
+          mo[r * D + c] = o[m][i][e];
+          mo[r * D + c + (F::kQuant ? 1 : 8)] = o[m][i][2 + e];
         }
       }
     __syncthreads();
@@ -735,21 +660,27 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, MT>::CTAS) pa
 }
 
 template <int D, int FMT>
-AttnKernel rows_kernel_fmt(int mt) {
-  if (mt == 0) return {(const void*)pages_rows_kernel<D, FMT, 0>, (size_t)RowsCfg<D, FMT, 0>::SMEM, kRowsWarps * 32, 0, 0};
-  if constexpr (D <= 128)
-    if (mt == 2) return {(const void*)pages_rows_kernel<D, FMT, 2>, (size_t)RowsCfg<D, FMT, 2>::SMEM, kRowsWarps * 32, 0, 0};
-  return {(const void*)pages_rows_kernel<D, FMT, 1>, (size_t)RowsCfg<D, FMT, 1>::SMEM, kRowsWarps * 32, 0, 0};
+AttnKernel rows_kernel_fmt(int nm) {
+#define KVQ_ROWS(n) \
+  if (nm == n) return {(const void*)pages_rows_kernel<D, FMT, n>, (size_t)RowsCfg<D, FMT, n>::SMEM, kRowsWarps * 32, 0, 0};
+  if constexpr (D <= 128) {
+    KVQ_ROWS(4)
+    KVQ_ROWS(3)
+  }
+  KVQ_ROWS(2)
+  KVQ_ROWS(1)
+#undef KVQ_ROWS
+  return {};
 }
 template <int D>
-AttnKernel rows_kernel_dim(int fmt, int mt) {
+AttnKernel rows_kernel_dim(int fmt, int nm) {
   switch (fmt) {
-    case kFmtF16: return rows_kernel_fmt<D, kFmtF16>(mt);
-    case kFmtBf16: return rows_kernel_fmt<D, kFmtBf16>(mt);
-    case kFmt88: return rows_kernel_fmt<D, kFmt88>(mt);
-    case kFmt44: return rows_kernel_fmt<D, kFmt44>(mt);
-    case kFmt84: return rows_kernel_fmt<D, kFmt84>(mt);
-    default: return rows_kernel_fmt<D, kFmt48>(mt);
+    case kFmtF16: return rows_kernel_fmt<D, kFmtF16>(nm);
+    case kFmtBf16: return rows_kernel_fmt<D, kFmtBf16>(nm);
+    case kFmt88: return rows_kernel_fmt<D, kFmt88>(nm);
+    case kFmt44: return rows_kernel_fmt<D, kFmt44>(nm);
+    case kFmt84: return rows_kernel_fmt<D, kFmt84>(nm);
+    default: return rows_kernel_fmt<D, kFmt48>(nm);
   }
 }
 

@@ -2,5 +2,5 @@
 #include "kvq_pages_rows.cuh"
 
 namespace kvq {
-AttnKernel rows_kernel_d128(int fmt, int mt) { return rows_kernel_dim<128>(fmt, mt); }
+AttnKernel rows_kernel_d128(int fmt, int nm) { return rows_kernel_dim<128>(fmt, nm); }
 }  // namespace kvq

@@ -2,5 +2,5 @@
 #include "kvq_pages_rows.cuh"
 
 namespace kvq {
-AttnKernel rows_kernel_d64(int fmt, int mt) { return rows_kernel_dim<64>(fmt, mt); }
+AttnKernel rows_kernel_d64(int fmt, int nm) { return rows_kernel_dim<64>(fmt, nm); }
 }  // namespace kvq

@@ -152,7 +152,7 @@ AttnKernel rows_kernel_d256(int fmt, int nm);
 AttnKernel tile_kernel_d64(int fmt);
 AttnKernel tile_kernel_d128(int fmt);
 AttnKernel tile_kernel_d256(int fmt);
-cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, int max_rows, cudaStream_t st);
+cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, int max_rows, bool rows_given, cudaStream_t st);
 cudaError_t pages_attn_setup(kvq_pages* P);
 
 }  // namespace kvq

@@ -295,7 +295,7 @@ kvq_status kvq_pages_attn(kvq_pages_t P, int layer, const void* q, int q_dtype, 
   a.part_ml = P->d_part_ml;
   a.split = P->d_split;
   const int max_new = batch->max_new > 0 && batch->max_new < bv.new_tokens ? batch->max_new : bv.new_tokens;
-  return cuda_result(P, launch_pages_attn(P, a, max_new * a.rep, static_cast<cudaStream_t>(stream)));
+  return cuda_result(P, launch_pages_attn(P, a, max_new * a.rep, batch->max_new > 0, static_cast<cudaStream_t>(stream)));
 }
 
 kvq_status kvq_pages_set_kernel(kvq_pages_t P, int which) {

@@ -165,11 +165,14 @@ cudaError_t pages_attn_setup(kvq_pages* P) {
   return cudaSuccess;
 }
 
-cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, int max_rows, cudaStream_t st) {
+cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, int max_rows, bool rows_given, cudaStream_t st) {
   // Sequences with at most `few` rows (new tokens x query heads per kv head) go to
   // the few-rows kernel, the others to the many-rows one; a batch that may hold
-  // both kinds launches both.  Measured, few / many rows, us, 8 sequences of 8192
-  // tokens: 16-bit pages, 12 heads of 64: 32 rows 52 / 68, 48 rows 86 / 69; 8 heads
+  // both kinds launches both.  Over 16-bit pages that goes for a single sequence of
+  // unknown rows too, since the kernel decides how its weights are rounded (where
+  // they are given, the second launch would cost 10 us for nothing: 64 tokens at 4k,
+  // 32 over 8 heads of 128, 39 us with one launch and 49 with two).  Measured, few /
+  // many rows, us, 8 sequences of 8192 tokens: 16-bit pages, 12 heads of 64: 32 rows 52 / 68, 48 rows 86 / 69; 8 heads
   // of 128: 57 / 66, 96 / 67; 2 heads of 256: 48 / 51, 61 / 53.  Codes cost the
   // many-rows kernel its dequantizing warps: 4 bits, heads of 64: 128 rows
   // 138 / 159, 192 rows 204 / 189; heads of 128: 64 rows 91 / 99, 96 rows 125 / 103;
@@ -179,7 +182,7 @@ cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, int max_rows, cudaStrea
   a.rows_lo = 0;
   a.rows_hi = INT_MAX;
   if (P->which == 1 || (P->which == 0 && max_rows <= few)) return launch_rows(P, a, max_rows, st);
-  if (P->which == 2 || a.bv.batch == 1) return launch_tile(P, a, max_rows, st);
+  if (P->which == 2 || (a.bv.batch == 1 && (rows_given || P->L.k_bits != 16))) return launch_tile(P, a, max_rows, st);
   a.rows_lo = few;
   cudaError_t e = launch_tile(P, a, max_rows, st);
   if (e != cudaSuccess) return e;

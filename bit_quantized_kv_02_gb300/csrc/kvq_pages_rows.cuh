@@ -21,11 +21,12 @@
 //    that the page stands for.
 // Scores, maxima, sums and outputs are fp32.  Weights enter the value product
 // as p * 2^7 with a maximum that lags by up to 2^8, so that fp16 weights stay
-// normal down to 2^-21 of the largest.  Over 16-bit pages with up to 16 rows they
-// are split into the operand type and its remainder (a second product, hidden
-// behind the reads); elsewhere they are rounded to the operand type (fp16, or
-// bf16 for bf16 pages), which adds about as much to the error as the output's own
-// rounding does.
+// normal down to 2^-21 of the largest.  Over 16-bit pages the weights of a sequence
+// of up to 16 rows (of any at head_dim 256) are split into the operand type and its
+// remainder (a second product, hidden behind the reads); elsewhere they are rounded
+// to the operand type (fp16, or bf16 for bf16 pages), which adds about as much to
+// the error as the output's own rounding does.  The sequence's own rows decide, not
+// the kernel's: its error does not depend on its neighbours in the batch.
 //
 // Measured: 16 sequences of 4113 bf16 tokens, 40 heads of 128: 207 us, 96 % of a
 // copy's bandwidth.  64 sequences of 1k to 32k 4-bit tokens, 32 query heads over 8
@@ -47,6 +48,7 @@
 namespace kvq {
 
 constexpr int kRowsWarps = 4;
+constexpr int kSplitRows = 16;  // most rows of a sequence whose weights the 24- and 32-row kernels split
 
 template <int FMT>
 struct Fmt {
@@ -73,7 +75,8 @@ struct RowsCfg {
   static constexpr int STEP = 16 * RECS, BK = STEP * kRowsWarps;  // tokens of a step and of a unit
   static constexpr int STAGE = RECS * REC;
   static constexpr int NS = BUDGET / STAGE < 2 ? 2 : (BUDGET / STAGE > 4 ? 4 : BUDGET / STAGE);
-  static constexpr bool kSplit = !F::kQuant && NM <= 2;  // weights as operand + remainder
+  // Weights as operand + remainder: always, or for sequences of up to kSplitRows rows
+  static constexpr bool kSplit = !F::kQuant, kSplitSome = kSplit && ROWS > kSplitRows;
   static constexpr int RING = kRowsWarps * NS * STAGE;
   static constexpr int MERGE = kRowsWarps * ROWS * (D + 2) * 4;
   static constexpr int SMEM = (RING > MERGE ? RING : MERGE);
@@ -245,8 +248,9 @@ __device__ __forceinline__ void rows_scores(uint32_t st, const PagesLayout& L, c
   }
 }
 
-// o[m][16 channels] += V^T P_m^T of one record; p: the weights as operands.
-template <int D, int FMT, int NM>
+// o[m][16 channels] += V^T P_m^T of one record, m < NM; p: the weights as operands,
+// rest: their remainders (SPLIT).
+template <int D, int FMT, int NM, bool SPLIT>
 __device__ __forceinline__ void rows_values(uint32_t st, const LaneOffsets<D, FMT>& lo, const uint32_t (*p)[2],
                                             const uint32_t (*rest)[2], int lane, float (*o)[D / 16][4]) {
   using F = Fmt<FMT>;
@@ -256,7 +260,7 @@ __device__ __forceinline__ void rows_values(uint32_t st, const LaneOffsets<D, FM
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
       mma16<F::kBf16>(o[m][j], v, p[m][0], p[m][1]);
-      if constexpr (RowsCfg<D, FMT, NM>::kSplit) mma16<F::kBf16>(o[m][j], v, rest[m][0], rest[m][1]);
+      if constexpr (SPLIT) mma16<F::kBf16>(o[m][j], v, rest[m][0], rest[m][1]);
     }
   };
   if constexpr (!F::kQuant) {
@@ -480,6 +484,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
       }
     }
     const int pos_lo = p.s.p0 + p.r0 / a.rep, pos_hi = p.s.p0 + (p.r0 + p.rows - 1) / a.rep;
+    constexpr int SPLIT_NM = NM < kSplitRows / 8 ? NM : kSplitRows / 8;  // row tiles that are split
+    const bool split = C::kSplit && (!C::kSplitSome || p.s.n * a.rep <= kSplitRows);
 
     for (; j < nt && alive; ++j) {
       alive = mbar_wait(bar + stage * 8, phase);
@@ -563,7 +569,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
       }
 #pragma unroll
       for (int x = 0; x < RECS; ++x) {
-        uint32_t pa[NM][2], pr[NM][2];
+        uint32_t pa[NM][2], pr[SPLIT_NM][2];
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
           const float b0 = mx[m][0] == -INFINITY ? 0.0f : mx[m][0] - 7.0f;
@@ -576,7 +582,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
             sum[m][1] += v;
             const uint32_t w = pack2<F::kBf16>(u, v);
             pa[m][h] = transpose8x8(w);
-            if constexpr (C::kSplit) {
+            if (split && m < SPLIT_NM) {
               float2 back;
               if (F::kBf16) back = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
               else back = __half22float2(as_h2(w));
@@ -584,7 +590,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
             }
           }
         }
-        rows_values<D, FMT, NM>(st + x * C::REC, offs, pa, pr, lane, o);
+        if (split) rows_values<D, FMT, SPLIT_NM, true>(st + x * C::REC, offs, pa, pr, lane, o);
+        else rows_values<D, FMT, NM, false>(st + x * C::REC, offs, pa, pr, lane, o);
       }
       __syncwarp();
       if (lane < RECS && j + NS < nt) {

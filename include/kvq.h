@@ -352,7 +352,9 @@ typedef struct {
 typedef struct {
   int batch;              /* sequences, 1..1024 */
   int new_tokens;         /* rows of k / v / q / out (>= q_start[batch]), >= 0 */
-  int max_new;            /* hint: no sequence has more new tokens than this; 0 = unknown.  Speed only */
+  int max_new;            /* hint: no sequence has more new tokens than this; 0 = unknown.  Speed only: with it a
+                             batch of few rows runs one kernel cut for them, without it those for any number.  A
+                             batch of one sequence is taken to have max_new of them where that is given */
   const int32_t* q_start; /* [batch + 1] */
   const int32_t* lens;    /* [batch] */
   const int32_t* table;   /* [batch][table_stride] */
@@ -404,8 +406,12 @@ kvq_status kvq_pages_append(kvq_pages_t pages, int layer, const void* k, const v
 /* Attention of the new tokens over layer `layer`'s pages: row i of a sequence,
  * at position p, sees the tokens t <= p of its sequence and, with window > 0,
  * t > p - window; out = sum_t softmax_t(scale * q . k_t) v_t with fp32 scores,
- * maxima, sums and accumulators.  q: device rows of [q_heads][head_dim] of
- * q_dtype, q_stride elements apart; out: device [new_tokens][q_heads][head_dim]
+ * maxima, sums and accumulators.  Weights are rounded once to the 16-bit type of
+ * the value product (the pages' dtype; fp16 over quantized pages); in a sequence
+ * of at most 16 query rows (new tokens x query heads per KV head; 32 at head_dim
+ * 256) over 16-bit pages they also keep what that rounding leaves.  A sequence's
+ * rounding depends on its own rows alone (in a batch of one on max_new, if given).
+ * q: device rows of [q_heads][head_dim] of q_dtype, q_stride elements apart; out: device [new_tokens][q_heads][head_dim]
  * of q_dtype, contiguous, 16-byte aligned, apart from q.  q_dtype: the pages'
  * dtype, or KVQ_F16 / KVQ_BF16 over quantized pages.  Query head h reads KV head h / (q_heads / kv_heads).
  * softmax_scale: finite; <= 0 means 1/sqrt(head_dim).  A row that sees no token yields

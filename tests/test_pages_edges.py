@@ -1,0 +1,67 @@
+"""Paged attention and append where a call's surroundings must not matter: the hint,
+the other sequences of the batch, the magnitude of the queries."""
+import math
+
+import pytest
+import torch
+
+from bit_quantized_kv_02_gb300 import kvq
+from tests.pages_ref import HALF_STEP, attention
+from tests.test_pages import L, check_attention, fill, make  # noqa: F401  (L builds the library)
+
+gpu = pytest.mark.gpu
+
+
+# ----------------------------------------------------- rounding of the weights --
+
+# (new tokens, lengths, rows behind them, hint): sequences of up to 16 query rows
+# alone with the hint, without it, beside a prompt, and in a padded batch of one
+SURROUNDINGS = {
+    "hint": ([1, 1, 4, 1], [5, 33, 12, 1500], 0, 4),
+    "no_hint": ([1] * 36 + [4], [3 + 2 * i for i in range(36)] + [700], 0, 0),
+    "prompt": ([1, 4, 90, 1], [6, 40, 200, 1500], 0, 90),
+    "padded": ([1], [9], 70, 0),
+}
+
+
+def cancelling_values(c, q, k, hq, h):
+    """Values whose last visible one cancels the others in the first query head of
+    each group: the output is then far below the terms it is made of, and an error of
+    the weights shows beside the output's own rounding."""
+    s, t = c.q_start.tolist(), c.k_start.tolist()
+    v = c.normal(int(c.k_start[-1]), h, k.shape[2]).to(c.dtype)
+    for b, n in enumerate(c.news):
+        for j in range(h):
+            x = q[s[b + 1] - 1, j * (hq // h)].double()
+            p = torch.softmax(k[t[b]:t[b + 1], j].double() @ x / math.sqrt(k.shape[2]), dim=0)
+            vb = v[t[b]:t[b + 1], j].double()
+            v[t[b + 1] - 1, j] = (-(p[:-1] @ vb[:-1]) / p[-1]).to(c.dtype)
+    return v
+
+
+@gpu
+@pytest.mark.parametrize("name", SURROUNDINGS)
+@pytest.mark.parametrize("fmt", ["f16", "bf16"])
+@pytest.mark.parametrize("d,heads", [(64, (4, 4)), (128, (8, 2)), (256, (4, 1))])
+def test_weights_of_few_rows_keep_their_remainder(name, fmt, d, heads):
+    """Up to 16 query rows over 16-bit pages: weights enter as operand and remainder,
+    so their error is the square of the operand's half step, whatever else the batch
+    holds and whether the hint is given."""
+    news, lens, pad, hint = SURROUNDINGS[name]
+    c = make((news, lens), 32, fmt, heads, d, seed=13, pad=pad)
+    hq, h = heads
+    q = (c.normal(c.rows, hq, d) * 0.3).to(c.dtype)
+    k = (c.normal(int(c.k_start[-1]), h, d) * 0.3).to(c.dtype)
+    v = cancelling_values(c, q, k, hq, h)
+    c.cache.kvq_pages_append(0, k.cuda(), v.cuda(), c.whole())
+    got = c.cache.kvq_pages_attn(0, q.cuda(), c.batch(hint)).cpu()
+    assert c.cache.kvq_pages_status() == 0
+    s, t = c.q_start.tolist(), c.k_start.tolist()
+    for b, n in enumerate(news):
+        few = n * (hq // h) <= 16
+        step = HALF_STEP[c.dtype]
+        ref, tol = attention(q[s[b]:s[b + 1]], k[t[b]:t[b + 1]], v[t[b]:t[b + 1]], torch.arange(lens[b] - n, lens[b]), 0,
+                             1.0 / math.sqrt(d), step * step if few else step)
+        tol = tol + ref.abs() * step + 2.0 ** -25
+        off = (got[s[b]:s[b + 1]].double() - ref).abs()
+        assert (off <= tol).all(), (b, float((off / tol).max()))

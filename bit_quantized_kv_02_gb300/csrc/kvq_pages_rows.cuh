@@ -330,6 +330,13 @@ __device__ __forceinline__ void rows_values(uint32_t st, const LaneOffsets<D, FM
   }
 }
 
+// E so that m * 2^E lies in [2^14, 2^15), for every float; 0 for m = 0.
+__device__ __forceinline__ int query_exp(float m) {
+  if (!(m > 0.0f)) return 0;
+  const bool tiny = m < FLT_MIN;  // (below the normal range the exponent's bits are zero)
+  return 14 + 127 - ((__float_as_int(tiny ? m * 0x1p64f : m) >> 23) & 0xff) + (tiny ? 64 : 0);
+}
+
 // What the scores of a row scaled by 2^E are to be multiplied by; never zero, which
 // would turn a hidden score's -inf into NaN.
 __device__ __forceinline__ float row_factor(const AttnArgs& a, int E) {
@@ -340,7 +347,8 @@ __device__ __forceinline__ float row_factor(const AttnArgs& a, int E) {
 // what its rows' scores are to be multiplied by.  Over codes q becomes fp16: a
 // bf16 row is scaled by the power of two that puts its largest magnitude in
 // [2^14, 2^15), so that nothing overflows and its 8 significant bits survive
-// down to 2^-28 of the largest.
+// down to 2^-28 of the largest, wherever in bf16's range that lies (E is 147 for its
+// smallest number).
 template <int D, int FMT>
 __device__ __forceinline__ void load_queries(const AttnArgs& a, const Piece& p, int m, int lane, uint32_t sq, float* sc) {
   using F = Fmt<FMT>;
@@ -377,7 +385,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Piece& p, 
         }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const int E = norm_exp(mx);
+      const int E = query_exp(mx);
       // 2^E in two factors: E may pass the range of one float
       const float f0 = exp2i(E / 2), f1 = exp2i(E - E / 2);
       f = row_factor(a, E);

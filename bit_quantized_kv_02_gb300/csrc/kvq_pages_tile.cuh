@@ -517,7 +517,7 @@ __device__ __forceinline__ float tile_query(const AttnArgs& a, const RowMap& rm,
           mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xffff0000u))));
 #pragma unroll
         for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const int E = norm_exp(mx);
+        const int E = query_exp(mx);
         const float f0 = exp2i(E / 2), f1 = exp2i(E - E / 2);
         const float y = __shfl_sync(0xffffffffu, row_factor(a, E), (lane % RPI) * LPR);
         if (lane / RPI == it) sc = y;

@@ -65,3 +65,21 @@ def test_weights_of_few_rows_keep_their_remainder(name, fmt, d, heads):
         tol = tol + ref.abs() * step + 2.0 ** -25
         off = (got[s[b]:s[b + 1]].double() - ref).abs()
         assert (off <= tol).all(), (b, float((off / tol).max()))
+
+
+# ------------------------------------------------------- magnitude of the queries --
+
+@gpu
+@pytest.mark.parametrize("which", [1, 2], ids=["few", "many"])
+@pytest.mark.parametrize("fmt", ["8_8", "4_4", "4_8"])
+@pytest.mark.parametrize("power", [-90, -112, -120, -130])
+def test_smallest_queries_over_codes(which, fmt, power):
+    """bf16 queries near the bottom of their range over codes, under a scale that
+    brings the scores back: they count with all their bits."""
+    c = make(([3, 40, 1], [90, 40, 700]), 16, fmt, (4, 2), 64, seed=2)
+    data = fill(c, 2, 64)
+    c.cache.kvq_pages_set_kernel(which)
+    q = (c.normal(c.rows, 4, 64).double() * 2.0 ** power).to(torch.bfloat16)
+    scale = 2.0 ** (min(-power, 126) - 3)
+    got = c.cache.kvq_pages_attn(0, q.cuda(), c.batch(), scale=scale)
+    check_attention(c, q, got.cpu(), data, scale=scale)

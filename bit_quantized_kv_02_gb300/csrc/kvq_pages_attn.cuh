@@ -47,17 +47,43 @@ __device__ __forceinline__ unsigned long long time_ns() {
   asm volatile("mov.u64 %0, %globaltimer;\n" : "=l"(t));
   return t;
 }
-// Waits for the phase; gives up (false) after two seconds.
-static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, int parity) {
+constexpr unsigned long long kWaitNs = 2000000000ull;  // longest wait on a barrier
+// Waits for the phase, by one thread.  False where `limit` ns pass first, which is
+// recorded in *err and *dead (shared memory), or where another thread of the CTA has
+// given up.
+__device__ __forceinline__ bool cta_wait(uint32_t bar, int parity, int* dead, int* err,
+                                         unsigned long long limit = kWaitNs) {
+  if (mbar_try(bar, parity)) return true;
   const unsigned long long t0 = time_ns();
   do {
     for (int i = 0; i < 64; ++i)
       if (mbar_try(bar, parity)) return true;
-  } while (time_ns() - t0 < 2000000000ull);
+    if (*(volatile int*)dead) return false;
+  } while (time_ns() - t0 < limit);
+  *(volatile int*)dead = 1;
+  atomicOr(err, 2);
   return false;
 }
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, int parity) {
-  return mbar_try(bar, parity) || mbar_wait_slow(bar, parity);
+// The same by a warp, whose lanes decide together: each has its own clock, and the
+// warp must not part.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, int parity, int* dead, int* err,
+                                          unsigned long long limit = kWaitNs) {
+  return __all_sync(0xffffffffu, cta_wait(bar, parity, dead, err, limit));
+}
+// After a wait that gave up, by a warp: the copies into the `n` stages from `stage`
+// on (a ring of NS barriers at `bar`) that are still under way land, or `limit` ns
+// pass.  `phase`: parity of stage `stage`; the ones behind the ring's end are a
+// phase further.
+template <int NS>
+__device__ __forceinline__ void ring_drain(uint32_t bar, int stage, int phase, int n,
+                                           unsigned long long limit = kWaitNs) {
+  const unsigned long long t0 = time_ns();
+  for (; n > 0; --n) {
+    while (!mbar_try(bar + stage * 8, phase) && time_ns() - t0 < limit) {
+    }
+    if (++stage == NS) stage = 0, phase ^= 1;
+  }
+  __syncwarp();
 }
 // Bulk copy global -> shared; both addresses and the size multiples of 16 bytes.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, int bytes, uint32_t bar) {

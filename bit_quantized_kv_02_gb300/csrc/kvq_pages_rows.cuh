@@ -405,6 +405,11 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Piece& p, 
                  : "memory");
 }
 
+// (out of line: it is rarely taken, and its registers are not the loop's)
+static __device__ __noinline__ bool rows_wait_slow(uint32_t bar, int phase, int* dead, int* err) {
+  return cta_wait(bar, phase, dead, err);
+}
+
 template <int D, int FMT, int NM>
 __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pages_rows_kernel(const __grid_constant__ AttnArgs a) {
   using C = RowsCfg<D, FMT, NM>;
@@ -416,6 +421,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
   __shared__ float row_scale[ROWS];
   __shared__ __align__(16) uint32_t queries[NM * (D / 16) * 64];
   __shared__ __align__(8) uint64_t bars[kRowsWarps * NS];
+  __shared__ int dead;  // a wait gave up: the CTA leaves
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
   const int g = lane >> 2, t = lane & 3;
   const LaneOffsets<D, FMT> offs(a.pv.L, lane);
@@ -423,6 +429,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
   const uint32_t ring = smem_u32(smem) + warp * NS * C::STAGE;
   const uint32_t bar = smem_u32(bars) + warp * NS * 8;
   if (lane < NS) mbar_init(bar + lane * 8, 1);
+  if (threadIdx.x == 0) dead = 0;
   fence_mbar_init();
   pdl_wait();
   plan_work<BK, ROWS, true>(a, &work, reinterpret_cast<long*>(smem + C::SMEM));
@@ -434,7 +441,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
   long u = work.own ? 0 : cta_begin(&work, cta);
   const long end = work.own ? 1 : cta_begin(&work, cta + 1);
   int stage = 0, phase = 0;  // of the next tile to be read; the ring is empty between pieces
-  bool alive = true, joined = false;
+  bool joined = false;
   while (u < end) {
     if (warp == 0) {
       const Piece x = work.own ? own_piece(a, &work, cta) : find_piece(a, &work, u, end);
@@ -462,7 +469,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
         bulk_load(ring + s * C::STAGE + rec * C::REC, run.at(a, page, tok), a.pv.L.tile_bytes, bar + s * 8);
     };
     auto page_of = [&](int tok) { return tok < p.s.len ? page_index(a, p.b, tok) : 0; };
-    if (lane < RECS * min(NS, nt - j) && alive) {
+    if (lane < RECS * min(NS, nt - j)) {
       const int tok = tok0 + BK * (j + lane / RECS) + (lane % RECS) * 16;
       int s = stage + lane / RECS;
       s = s >= NS ? s - NS : s;
@@ -495,10 +502,10 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
     constexpr int SPLIT_NM = NM < kSplitRows / 8 ? NM : kSplitRows / 8;  // row tiles that are split
     const bool split = C::kSplit && (!C::kSplitSome || p.s.n * a.rep <= kSplitRows);
 
-    for (; j < nt && alive; ++j) {
-      alive = mbar_wait(bar + stage * 8, phase);
-      if (!alive) {
-        if (lane == 0) atomicOr(a.pv.err, 2);
+    for (; j < nt; ++j) {
+      const bool here = mbar_try(bar + stage * 8, phase) || rows_wait_slow(bar + stage * 8, phase, &dead, a.pv.err);
+      if (!__all_sync(0xffffffffu, here)) {  // (each lane has its own clock; the warp decides together)
+        ring_drain<NS>(bar, stage, phase, min(NS, nt - j));
         break;
       }
       const uint32_t st = ring + stage * C::STAGE;
@@ -610,11 +617,10 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
       __syncwarp();
       if (++stage == NS) stage = 0, phase ^= 1;
     }
-    if (!alive)  // copies still in flight land before their stages are used for anything else
-      for (int s = 0; s < NS; ++s) (void)mbar_wait(bar + s * 8, phase);
 
     // ---- merge the four warps
     __syncthreads();
+    if (*(volatile int*)&dead) break;
     float* mo = reinterpret_cast<float*>(smem);                 // [warp][ROWS][D]
     float* ml = mo + kRowsWarps * ROWS * D;                     // [warp][ROWS][2]
 #pragma unroll

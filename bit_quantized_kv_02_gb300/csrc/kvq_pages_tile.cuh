@@ -74,22 +74,8 @@ struct TileShared {
 
 // A bounded wait that also ends when another role gave up.
 template <typename SH>
-__device__ __forceinline__ bool tile_wait(SH* sh, const AttnArgs& a, uint64_t* bar, int parity) {
-  const uint32_t b = smem_u32(bar);
-  if (mbar_try(b, parity)) return true;
-  const unsigned long long t0 = time_ns();
-  do {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try(b, parity)) return true;
-    if (*(volatile int*)&sh->dead) return false;
-  } while (time_ns() - t0 < 2000000000ull);
-  sh->dead = 1;
-  atomicOr(a.pv.err, 2);
-  return false;
-}
-template <typename SH>
 __device__ __forceinline__ bool tile_wait_warp(SH* sh, const AttnArgs& a, uint64_t* bar, int parity) {
-  return __all_sync(0xffffffffu, tile_wait(sh, a, bar, parity));
+  return warp_wait(smem_u32(bar), parity, &sh->dead, a.pv.err);
 }
 
 // Query rows of a piece: row r is token t0 + (rem + r) / rep of the call's rows,

@@ -254,9 +254,7 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
     int tok = p.blk * C::BK;
     // A unit's codes and metadata.  Every record with a token of the sequence
     // arrives; rows behind its end become zero (zero + code * step = 0), whatever
-    // the page holds there.  The records go back once every lane has its values: an
-    // arrival right behind the loads let the next copy overtake them (shared memory
-    // is busy with the matrix operands, and loads wait for it).
+    // the page holds there.
     auto take = [&](int tok, uint32_t* w, uint32_t* zs) -> bool {
 #pragma unroll
       for (int i = 0; i < 4 * WC; ++i) w[i] = 0;
@@ -275,9 +273,14 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
       }
       return true;
     };
-    auto give_back = [&](int tok, const uint32_t* w, uint32_t zs) {
-      // (a branch on the loads' results: they are there when it is decided)
-      if (__any_sync(0xffffffffu, (w[0] ^ w[4 * WC - 1] ^ zs) == 0x5bd1e995u)) __nanosleep(20);
+    // Its records go back: the fence orders each lane's loads before the bulk copies
+    // into the same bytes, which go another way (without it a copy overtook loads that
+    // waited behind the matrix operands), the warp's barrier the lanes before the
+    // arrival.  (The records held until their values are stored: 703 us against 579
+    // for 2 x 600 tokens at 20000, 16 over 2 heads of 256, 8 bits.)
+    auto give_back = [&](int tok) {
+      fence_async();
+      __syncwarp();
 #pragma unroll
       for (int i = 0; i < RECS; ++i)
         if (tok + 16 * i < p.s.len) {
@@ -327,9 +330,9 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
       for (int u = 0; u < C::BK; u += 2 * UT, tok += 2 * UT, out += 2 * UT * 128) {
         uint32_t w0[4 * WC], w1[4 * WC], z0, z1;
         if (!take(tok, w0, &z0)) return;
-        give_back(tok, w0, z0);
+        give_back(tok);
         if (!take(tok + UT, w1, &z1)) return;
-        give_back(tok + UT, w1, z1);
+        give_back(tok + UT);
         turn_unit(tok, w0, z0, out);
         turn_unit(tok + UT, w1, z1, out + UT * 128);
       }

@@ -83,3 +83,26 @@ def test_smallest_queries_over_codes(which, fmt, power):
     scale = 2.0 ** (min(-power, 126) - 3)
     got = c.cache.kvq_pages_attn(0, q.cuda(), c.batch(), scale=scale)
     check_attention(c, q, got.cpu(), data, scale=scale)
+
+
+# ------------------------------------------------------------- reuse of the stages --
+
+@gpu
+@pytest.mark.parametrize("which", [1, 2], ids=["few", "many"])
+@pytest.mark.parametrize("fmt", ["f16", "8_8", "4_4", "8_4", "4_8"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_copies_do_not_overtake_the_reads_before_them(which, fmt, d):
+    """Long sequences that refill every stage many times, over and over: a copy that
+    lands under a read shows as a run that differs."""
+    c = make(([20, 30], [3000, 4100]), 32, fmt, (8, 2), d, seed=3)
+    data = fill(c, 2, d)
+    q = c.normal(c.rows, 8, d).to(c.dtype)
+    c.cache.kvq_pages_set_kernel(which)
+    dev, b = q.cuda(), c.batch()
+    first = c.cache.kvq_pages_attn(0, dev, b).clone()
+    check_attention(c, q, first.cpu(), data)
+    out, differ = torch.zeros_like(first), torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(100):
+        c.cache.kvq_pages_attn(0, dev, b, out=out)
+        differ += (out != first).sum()
+    assert int(differ) == 0 and c.cache.kvq_pages_status() == 0

@@ -608,6 +608,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
         if (split) rows_values<D, FMT, SPLIT_NM, true>(st + x * C::REC, offs, pa, pr, lane, o);
         else rows_values<D, FMT, NM, false>(st + x * C::REC, offs, pa, pr, lane, o);
       }
+      fence_async();  // the step's reads (and cleared rows) before the copy into the same bytes
       __syncwarp();
       if (lane < RECS && j + NS < nt) {
         const int tn = tok + BK * NS + lane * 16;

@@ -44,6 +44,7 @@ __global__ void ring_probe(const uint32_t* src, int lost_warp, int lost_step, in
       break;
     }
     for (int i = lane; i < kProbeBytes / 4; i += 32) sum += reinterpret_cast<volatile uint32_t*>(ring[warp][stage])[i];
+    fence_async();
     __syncwarp();
     if (step + kProbeStages < kProbeSteps) bring(step + kProbeStages);
     if (++stage == kProbeStages) stage = 0, phase ^= 1;

@@ -286,35 +286,55 @@ struct Place {
 // Places of `count` rows from t0, by the whole block: every sequence's bounds and
 // length are read at once, and the thread whose sequence holds a row follows its
 // table entry, so a row costs two dependent loads whatever the batch is.  A
-// sequence whose length or rows do not fit has no places.
+// sequence whose length or rows do not fit has no places.  Only then can two
+// sequences name the same row: the rows are gone through again one by one, and the
+// first sequence that fits has it.
 __device__ __forceinline__ void find_places(const PagesView& pv, const BatchView& bv, const RopeView* rv, long t0,
                                             int count, Place* place) {
   if (threadIdx.x < count) place[threadIdx.x] = {-1, 0, 0};
   __syncthreads();
+  // the place of row t, which sequence b holds; false: an index is out of range
+  auto find = [&](int b, const Seq& s, long t, Place* p) -> bool {
+    const long pos = s.p0 + (t - s.s0);
+    if (pos < 0) return true;
+    const int page = bv.table[b * bv.stride + (pos >> pv.lg_pt)];
+    bool ok = (unsigned)page < (unsigned)pv.pages;
+    long turn = 0;
+    if (rv && rv->table) {
+      turn = rv->positions ? rv->positions[t] : pos;
+      ok = ok && turn >= 0 && turn < rv->rows;
+    }
+    if (ok) *p = {page, (int)(pos & ((1 << pv.lg_pt) - 1)), (int)turn};
+    return ok;
+  };
+  int misfit = 0;
   for (int b = threadIdx.x; b < bv.batch; b += kThreads) {
     bool bad;
     const Seq s = load_seq(pv, bv, b, &bad);
     if (bad) {  // its clamped rows would stand at other positions: none is touched
       if (t0 == 0) atomicOr(pv.err, 1);  // (one block reports)
+      misfit = 1;
       continue;
     }
     const long lo = max(t0, (long)s.s0), hi = min(t0 + count, (long)s.s0 + s.n);
-    for (long t = lo; t < hi; ++t) {
-      const long pos = s.p0 + (t - s.s0);
-      if (pos < 0) continue;
-      const int page = bv.table[b * bv.stride + (pos >> pv.lg_pt)];
-      bool ok = (unsigned)page < (unsigned)pv.pages;
-      long turn = 0;
-      if (rv && rv->table) {
-        turn = rv->positions ? rv->positions[t] : pos;
-        ok = ok && turn >= 0 && turn < rv->rows;
-      }
-      if (ok) place[t - t0] = {page, (int)(pos & ((1 << pv.lg_pt) - 1)), (int)turn};
-      bad = bad || !ok;
-    }
+    for (long t = lo; t < hi; ++t) bad = !find(b, s, t, &place[t - t0]) || bad;
     if (bad) atomicOr(pv.err, 1);
   }
-  __syncthreads();
+  if (__syncthreads_or(misfit)) {
+    const long t = t0 + threadIdx.x;
+    if (threadIdx.x < count) {
+      Place p = {-1, 0, 0};
+      for (int b = 0; b < bv.batch; ++b) {
+        bool bad;
+        const Seq s = load_seq(pv, bv, b, &bad);
+        if (bad || t < s.s0 || t >= (long)s.s0 + s.n) continue;
+        find(b, s, t, &p);
+        break;
+      }
+      place[threadIdx.x] = p;
+    }
+    __syncthreads();
+  }
 }
 
 // One row's 8 channels from c0 on into its record (`rec` + `off`): 16-bit, or

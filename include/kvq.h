@@ -347,7 +347,9 @@ typedef struct {
  * 2^30, or a q_start that decreases or passes new_tokens is never followed:
  * kvq_pages_append and kvq_pages_read skip the token (the entry) or the sequence
  * (the others), kvq_pages_attn gives that sequence's rows values of no meaning,
- * and kvq_pages_status reports KVQ_ERR_BAD_INDEX.  All pointers of these calls
+ * and kvq_pages_status reports KVQ_ERR_BAD_INDEX.  A row that a decreasing q_start
+ * names twice goes with the first of its sequences that is not skipped
+ * (kvq_pages_append, kvq_pages_read) or comes out without meaning (kvq_pages_attn).  All pointers of these calls
  * are aligned to their elements. */
 typedef struct {
   int batch;              /* sequences, 1..1024 */

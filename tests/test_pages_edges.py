@@ -106,3 +106,33 @@ def test_copies_do_not_overtake_the_reads_before_them(which, fmt, d):
         c.cache.kvq_pages_attn(0, dev, b, out=out)
         differ += (out != first).sum()
     assert int(differ) == 0 and c.cache.kvq_pages_status() == 0
+
+
+# ---------------------------------------------------------------- rows named twice --
+
+@gpu
+@pytest.mark.parametrize("fmt", ["f16", "8_8"])
+def test_a_row_that_two_sequences_name(fmt):
+    """q_start falls back at the second sequence, so the first and the third both name
+    row 2: it goes with the first, the second is skipped, and no other token changes."""
+    c = make(([3, 0, 1], [40, 20, 30]), 16, fmt, (2, 2), 64, seed=1)
+    data = fill(c, 2, 64)
+    batch = kvq.PagesBatch(torch.tensor([0, 3, 2, 4], dtype=torch.int32).cuda(),
+                           torch.tensor(c.lens, dtype=torch.int32).cuda(), c.table.cuda(), 4)
+    x = c.normal(4, 2, 64).half().cuda()
+    # what the pages hold of the four rows
+    alone = make(([4], [4]), 16, fmt, (2, 2), 64)
+    alone.cache.kvq_pages_append(0, x, x, alone.batch())
+    rows = [t.cpu() for t in alone.cache.kvq_pages_read(0, alone.batch())]
+    for _ in range(200):
+        c.cache.kvq_pages_append(0, x, x, batch)
+    assert c.cache.kvq_pages_status() == 7
+    s = c.k_start.tolist()
+    for i, got in enumerate(t.cpu() for t in c.cache.kvq_pages_read(0, c.whole())):
+        want = torch.cat([d[i] for d in data])
+        want[s[0] + 37:s[0] + 40] = rows[i][:3]
+        want[s[2] + 29] = rows[i][3]
+        assert torch.equal(got, want)
+    out = torch.full((4, 2, 64), 3.0, dtype=torch.float16, device="cuda")
+    got, _ = c.cache.kvq_pages_read(0, batch, out, out.clone())
+    assert c.cache.kvq_pages_status() == 7 and torch.equal(got.cpu(), rows[0])

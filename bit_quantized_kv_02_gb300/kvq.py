@@ -560,7 +560,7 @@ class KVQPages:
     def __init__(self, cfg: PagesConfig, device="cuda", stream=None):
         self.cfg = cfg
         self.bytes = kvq_pages_bytes(cfg)
-        self.buffer = torch.empty(self.bytes.alloc, dtype=torch.uint8, device=device)
+        self.buffer = _new(self.bytes.alloc, torch.uint8, device, stream)  # (zero-filled on the same stream)
         self.device, self.index = self.buffer.device, self.buffer.get_device()
         self.dtype = torch.bfloat16 if cfg.dtype == BF16 else torch.float16
         self._kv, self._q = (cfg.kv_heads, cfg.head_dim), (cfg.q_heads, cfg.head_dim)

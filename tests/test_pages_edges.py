@@ -136,3 +136,22 @@ def test_a_row_that_two_sequences_name(fmt):
     out = torch.full((4, 2, 64), 3.0, dtype=torch.float16, device="cuda")
     got, _ = c.cache.kvq_pages_read(0, batch, out, out.clone())
     assert c.cache.kvq_pages_status() == 7 and torch.equal(got.cpu(), rows[0])
+
+
+# ------------------------------------------------------------------ memory of calls --
+
+@gpu
+def test_pool_belongs_to_the_stream_that_clears_it():
+    """The buffer of a cache made on a stream comes from that stream's memory: what the
+    current stream still writes to freed memory of its own cannot reach it."""
+    cfg = kvq.make_pages_config(1, 500, 32, 4, 4, 64)
+    size, stream = kvq.kvq_pages_bytes(cfg).alloc, torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        mine = torch.empty(size, dtype=torch.uint8, device="cuda")
+    theirs = torch.empty(size, dtype=torch.uint8, device="cuda")
+    at, other = mine.data_ptr(), theirs.data_ptr()
+    del mine, theirs
+    cache = kvq.KVQPages(cfg, stream=stream)
+    assert cache.buffer.data_ptr() == at != other
+    stream.synchronize()
+    assert not cache.buffer.any() and cache.kvq_pages_status(stream) == 0

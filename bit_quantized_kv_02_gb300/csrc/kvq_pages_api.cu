@@ -118,6 +118,15 @@ kvq_status cuda_result(kvq_pages* P, cudaError_t e) {
 bool fits(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 int element(int dtype) { return dtype == KVQ_F32 ? 4 : 2; }
 
+// Do `rows` rows of `bytes` bytes, contiguous from `out` on, share a byte with as many
+// rows `stride` bytes apart from `in` on?
+bool overlap(const void* out, const void* in, int64_t rows, int64_t bytes, int64_t stride) {
+  const int64_t o = (int64_t)reinterpret_cast<uintptr_t>(out), i = (int64_t)reinterpret_cast<uintptr_t>(in);
+  // the first row of `in` that ends behind the start of `out`
+  const int64_t r = o < i + bytes ? 0 : (o - i - bytes) / stride + 1;
+  return r < rows && i + r * stride < o + rows * bytes;
+}
+
 // Handle, layer and current device.
 kvq_status usable(kvq_pages* P, int layer) {
   if (!P) return KVQ_ERR_INVALID_ARG;
@@ -278,6 +287,8 @@ kvq_status kvq_pages_attn(kvq_pages_t P, int layer, const void* q, int q_dtype, 
   if (!fits(q, 2)) return fail(P, KVQ_ERR_INVALID_ARG, "queries not aligned to their type");
   if (q_stride < (int64_t)c.q_heads * c.head_dim) return fail(P, KVQ_ERR_INVALID_ARG, "stride shorter than a row");
   if (reinterpret_cast<uintptr_t>(out) & 15) return fail(P, KVQ_ERR_INVALID_ARG, "output not 16-byte aligned");
+  if (overlap(out, q, bv.new_tokens, (int64_t)c.q_heads * c.head_dim * 2, q_stride * 2))
+    return fail(P, KVQ_ERR_INVALID_ARG, "output and queries overlap");
   AttnArgs a = {};
   a.pv = pages_view(P, layer);
   a.bv = bv;

@@ -615,7 +615,8 @@ class KVQPages:
                        scale: float = 0.0, window: int = 0, stream=None) -> torch.Tensor:
         """Attention of the new tokens of `batch` over the pages: q [new_tokens][q_heads]
         [head_dim] fp16 or bf16; returns out of the same shape and type (rows behind
-        the last sequence are left as they were; zeros in a new tensor)."""
+        the last sequence are left as they were; zeros in a new tensor).  A given out
+        shares no memory with q."""
         index, dtype = self.index, q.dtype
         qs = _row_stride(q, "q", *self._q, index)
         if dtype != torch.float16 and dtype != torch.bfloat16:
@@ -642,7 +643,7 @@ class KVQPages:
                        v_out: torch.Tensor | None = None, stream=None):
         """What the pages hold for the new tokens of `batch`: (k, v), each [new_tokens]
         [kv_heads][head_dim] of the pages' type (fp16 for quantized pages); rows
-        without a place are left as they were."""
+        without a place are left as they were (new tensors are not cleared)."""
         index = self.index
         shape = (batch.new_tokens, *self._kv)
         if batch.index != index:

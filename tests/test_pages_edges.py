@@ -155,3 +155,25 @@ def test_pool_belongs_to_the_stream_that_clears_it():
     assert cache.buffer.data_ptr() == at != other
     stream.synchronize()
     assert not cache.buffer.any() and cache.kvq_pages_status(stream) == 0
+
+
+@gpu
+def test_output_over_the_queries_is_refused():
+    """Heads are read after others are written; an output beside the queries, or between
+    two of their rows, is taken."""
+    c = make(([3], [40]), 16, "f16", (4, 2), 64)
+    data = fill(c, 2, 64)
+    flat = torch.zeros(3 * 256 * 5, dtype=torch.float16, device="cuda")
+    q = c.normal(3, 4, 64).half()
+
+    def call(at, stride, out_at):
+        dev = flat.as_strided((3, 4, 64), (stride, 64, 1), at)
+        dev.copy_(q)
+        return c.cache.kvq_pages_attn(0, dev, c.batch(), out=flat[out_at:out_at + 768].view(3, 4, 64))
+
+    for at, stride, out_at in ((0, 256, 0), (0, 256, 760), (768, 256, 8), (0, 512, 512), (0, 1024, 264), (256, 1024, 520)):
+        with pytest.raises(kvq.KVQError) as e:
+            call(at, stride, out_at)
+        assert e.value.status == 1 and "overlap" in str(e.value)
+    for at, stride, out_at in ((0, 256, 768), (768, 256, 0), (0, 1024, 256), (256, 1024, 512), (768, 512, 0)):
+        check_attention(c, q, call(at, stride, out_at).cpu(), data)

@@ -64,10 +64,11 @@ struct RowsCfg {
   static constexpr int ROWS = 8 * NM;
   // a record with the most metadata (groups of 32)
   static constexpr int REC = 2 * D * (F::KB + F::VB) + (F::kQuant ? 2 * 16 * (D / 32) * 4 : 0);
-  // CTAs per SM that registers and shared memory are cut for
+  // CTAs per SM that registers and shared memory are cut for (a few bytes a sequence
+  // come on top: 1024 sequences can cost one of them)
   static constexpr int CTAS = D == 64    ? (NM <= 2 ? 4 : 3)
                               : D == 128 ? (F::kQuant && NM <= 2 ? 5 - NM : 2)
-                                         : (F::kQuant && NM == 1 ? 3 : 2);
+                                         : (!F::kQuant ? 1 : (NM == 1 && F::KB + F::VB < 16 ? 3 : 2));
   static constexpr int BUDGET = CTAS == 4 ? 12544 : (CTAS == 3 ? 16384 : 24576);  // bytes of a warp's ring
   // records of a warp's step and stage: two where two such stages fit, so that
   // the softmax's exchanges and the loop cost half as much per token
@@ -80,6 +81,8 @@ struct RowsCfg {
   static constexpr int RING = kRowsWarps * NS * STAGE;
   static constexpr int MERGE = kRowsWarps * ROWS * (D + 2) * 4;
   static constexpr int SMEM = (RING > MERGE ? RING : MERGE);
+  // (the queries and little else are static; 1 KB of a CTA is the system's)
+  static_assert(CTAS * (SMEM + NM * (D / 16) * 256 + 2048) <= 228 * 1024, "CTAs of an SM fit its shared memory");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {

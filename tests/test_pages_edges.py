@@ -177,3 +177,22 @@ def test_output_over_the_queries_is_refused():
         assert e.value.status == 1 and "overlap" in str(e.value)
     for at, stride, out_at in ((0, 256, 768), (768, 256, 0), (0, 1024, 256), (256, 1024, 512), (768, 512, 0)):
         check_attention(c, q, call(at, stride, out_at).cpu(), data)
+
+
+# --------------------------------------------------------- the choice of the kernel --
+
+@gpu
+@pytest.mark.parametrize("fmt", ["f16", "bf16", "8_8", "4_4"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("hint", [True, False])
+def test_rows_around_the_choice_of_the_kernel(fmt, d, hint):
+    """Sequences with as many rows as the few-rows kernel takes by default, one fewer and
+    one more, alone and in one batch."""
+    few = 32 if fmt in ("f16", "bf16") else {64: 128, 128: 64, 256: 48}[d]
+    for news in ([few - 1], [few], [few + 1], [few, 1, few + 1, 16, 17, few - 1]):
+        c = make((news, [n + 75 for n in news]), 32, fmt, (1, 1), d, seed=17, pad=0 if hint else 40)
+        data = fill(c, 1, d)
+        q = c.normal(c.rows, 1, d).to(c.dtype)
+        got = c.cache.kvq_pages_attn(0, q.cuda(), c.batch(max(news) if hint else 0))
+        assert c.cache.kvq_pages_status() == 0 and not got[c.n:].any()
+        check_attention(c, q, got.cpu(), data)

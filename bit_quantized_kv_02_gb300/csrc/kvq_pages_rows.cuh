@@ -30,10 +30,10 @@
 //
 // Measured: 16 sequences of 4113 bf16 tokens, 40 heads of 128: 207 us, 96 % of a
 // copy's bandwidth.  64 sequences of 1k to 32k 4-bit tokens, 32 query heads over 8
-// of 128: 315 us, 59 % (375 with 16 rows and three CTAs per SM in place of 8 and
+// of 128: 310 us, 60 % (375 with 16 rows and three CTAs per SM in place of 8 and
 // four; 330 with 8 rows and five CTAs): a record of codes costs about as many
 // instructions whatever the rows are, and fixed-latency waits take the slots that
-// are left.  5 drafted tokens, 20 rows, over 8-bit pages: 60 us (floor 29), two
+// are left.  5 drafted tokens, 20 rows, over 8-bit pages: 59 us (floor 29), two
 // CTAs per SM; 66 as two 16-row operands.  (That form, the rows as the left
 // operand, was 90 us against 99 for a full 32 rows of 32 sequences of 4096 4-bit
 // tokens, heads of 128, but 88 against 71 for 16 and 86 against 56 for 8.)

@@ -25,13 +25,17 @@
 // type (p * 2^7, as in the few-rows kernel).
 //
 // Measured: 2048 new tokens at 30720, 32 query heads over 8 of 128, bf16 pages:
-// 818 us, 1.31 PFLOP/s (67 % of a large library product).  A tile's chain is what
-// is left: scores, their softmax (1700 clocks), the value product, and the
-// signals between them take 3640 clocks a block against 2048 of the matrix unit.
-// 509 tokens at 130563, 16 query heads over 2 of 256, 4-bit keys and 8-bit values:
-// 1471 us, 0.74 PFLOP/s, bound by the dequantizers (each CTA turns every code for
-// 128 rows).  Prompts of up to 2048 tokens, 40 heads of 128, window 1024: 367 us:
-// short pieces, whose query load and output (15K clocks) no other piece covers.
+// 818 to 833 us on different cards, 1.3 PFLOP/s (66 % of a large library product).
+// A CTA takes 418 blocks of two tiles, so a block takes 1.97 us, of which its
+// products would take 1.30 at the library product's rate: a tile's chain of scores,
+// softmax, value product and the signals between them is what is left (tensor pipe
+// active 54 % on a chunk half as long).  509 tokens at 130563, 16 query heads over 2
+// of 256, 4-bit keys and 8-bit values: 1444 us, 0.75 PFLOP/s (tensor pipe 29 % at
+// 16000), bound by the dequantizers (each CTA turns every code for 128 rows).  Prompts
+// of up to 2048 tokens, 40 heads of 128, window 1024: 367 us, tensor pipe 25 %.  A CTA
+// has 68 blocks there, in 10.5 pieces, which would take 134 us at the chunk's pace;
+// the rest (queries and outputs that no other piece covers, blocks with a mask, a
+// second read of the scores in each piece's first block) was not measured apart.
 #pragma once
 
 #include "kvq_pages_attn.cuh"

@@ -441,7 +441,8 @@ class PagesBatch:
     [batch] and table [batch][pages] are int32 device tensors, read by the kernels
     when they run, so their contents may change between calls and graph replays.
     new_tokens: rows of k / v / q / out (at least q_start[batch]); max_new: the
-    most new tokens of any sequence if known (speed only)."""
+    most new tokens of any sequence if known (speed only; a batch of one is taken
+    to have as many)."""
 
     def __init__(self, q_start, lens, table, new_tokens: int, max_new: int = 0):
         _ints(q_start, "q_start")
@@ -667,4 +668,6 @@ class KVQPages:
         _check(self._lib.kvq_pages_set_kernel(self.handle, int(which)), "kvq_pages_set_kernel")
 
     def kvq_pages_status(self, stream=None) -> int:
+        """Synchronises and returns what kernels recorded since the last call (0: nothing): calls
+        return before their kernels run, so a bad index or a wait that ran out shows only here."""
         return _on_device(self.index, stream, self._lib.kvq_pages_status, self.handle)

@@ -172,9 +172,9 @@ cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, int max_rows, bool rows
   // unknown rows too, since the kernel decides how its weights are rounded (where
   // they are given, the second launch would cost 10 us for nothing: 64 tokens at 4k,
   // 32 over 8 heads of 128, 39 us with one launch and 49 with two).  Measured, few /
-  // many rows, us, 8 sequences of 8192 tokens: 16-bit pages, 12 heads of 64: 32 rows 52 / 68, 48 rows 86 / 69; 8 heads
-  // of 128: 57 / 66, 96 / 67; 2 heads of 256: 48 / 51, 61 / 53.  Codes cost the
-  // many-rows kernel its dequantizing warps: 4 bits, heads of 64: 128 rows
+  // many rows, us, 8 sequences of 8192 tokens: 16-bit pages, 12 heads of 64: 32 rows
+  // 52 / 68, 48 rows 86 / 69; 8 heads of 128: 57 / 66, 96 / 67; 2 heads of 256:
+  // 48 / 51, 61 / 53.  Codes cost the many-rows kernel its dequantizing warps: 4 bits, heads of 64: 128 rows
   // 138 / 159, 192 rows 204 / 189; heads of 128: 64 rows 91 / 99, 96 rows 125 / 103;
   // heads of 256: 48 rows 57 / 61, 64 rows 67 / 62.
   const int D = P->cfg.head_dim;

@@ -25,6 +25,7 @@ namespace kvq {
 
 constexpr int kPageTile = 16;      // tokens per record
 constexpr int kPagesMaxBatch = 1024;
+constexpr int kTreeWords = 4;      // most 64-bit words of a drafted token's mask
 constexpr int kPagesCtas = 1024;   // most CTAs of an attention launch (partial slots are sized by it)
 constexpr int kRowsPerCta = 32;    // most query rows a CTA of the few-rows kernel holds
 constexpr int kTileCtas = 192;     // most CTAs of the many-rows kernel
@@ -44,7 +45,7 @@ struct PagesView {
   PagesLayout L;
   int pages, heads, head_dim;
   int lg_pt;       // log2(page_tokens)
-  int* err;        // bit 0: bad index, bit 1: a wait gave up
+  int* err;        // bit 0: bad index, bit 1: a wait gave up, bit 2: no free pages
 };
 
 __host__ __device__ inline long page_head_bytes(const PagesView& p) {
@@ -94,6 +95,10 @@ struct AttnArgs {
   int q_aligned;     // rows of q may be read 16 bytes at a time
   int rows_lo, rows_hi;  // sequences with rows_lo < n * rep <= rows_hi are this launch's
   int ring;          // raw records per tensor in flight (many rows over codes; 0 otherwise)
+  // the masked kernels: new tokens that a row sees (null: rows see every token of their sequence)
+  const uint32_t* seen;
+  int seen_words;    // 32-bit words a row
+  const int32_t* positions;  // of the rows, for the window
   int min_units;     // fewest blocks of tokens worth a CTA of its own
   float* part_o;     // [CTA][2][rows][head_dim] partial sums of the first / last item of a CTA
   float* part_ml;    // [CTA][2][rows][2] their maxima and sums
@@ -127,8 +132,11 @@ struct kvq_pages {
   int sm_smem = 0, cta_smem = 0;  // shared memory of an SM, of it reserved per CTA
   int max_smem = 0;               // most that a CTA may have
   int which = 0;     // kernel choice (kvq_pages_set_kernel)
-  kvq::AttnKernel rows_fn[4] = {};  // few-rows kernel for 8, 16, 24 and 32 rows (8 and 16 at head_dim 256)
-  kvq::AttnKernel tile_fn = {};     // many-rows kernel
+  // causal and masked kernels
+  kvq::AttnKernel rows_fn[2][4] = {};  // few-rows kernel for 8, 16, 24 and 32 rows (8 and 16 at head_dim 256)
+  kvq::AttnKernel tile_fn[2] = {};     // many-rows kernel
+  int32_t* d_fresh = nullptr;  // kvq_pages_grow: [pages] free pages in the order they are dealt out
+  int32_t* d_copies = nullptr; // pairs of pages to copy: [0] their number, from [4] on sources, then targets
   std::string last_error;
 };
 
@@ -152,7 +160,27 @@ AttnKernel rows_kernel_d256(int fmt, int nm);
 AttnKernel tile_kernel_d64(int fmt);
 AttnKernel tile_kernel_d128(int fmt);
 AttnKernel tile_kernel_d256(int fmt);
-cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, int max_rows, bool rows_given, cudaStream_t st);
+// the same with masks (trees, cross attention), in units of their own
+AttnKernel rows_mask_kernel_d64(int fmt, int nm);
+AttnKernel rows_mask_kernel_d128(int fmt, int nm);
+AttnKernel rows_mask_kernel_d256(int fmt, int nm);
+AttnKernel tile_mask_kernel_d64(int fmt);
+AttnKernel tile_mask_kernel_d128(int fmt);
+AttnKernel tile_mask_kernel_d256(int fmt);
+cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, bool masked, int max_rows, bool rows_given, cudaStream_t st);
 cudaError_t pages_attn_setup(kvq_pages* P);
+
+// kvq_pages_branch.cu
+cudaError_t launch_pages_tree(const PagesView& pv, const BatchView& bv, const int32_t* parents, int words, uint64_t* seen,
+                              int32_t* positions, cudaStream_t st);
+// (layers: how many from pv's on, `layer_bytes` apart)
+cudaError_t launch_pages_keep(const PagesView& pv, int layers, long layer_bytes, const BatchView& bv, const uint8_t* keep,
+                              int32_t* lens_out, cudaStream_t st);
+// `number`: device count of the pairs, of which there are at most `count`; null: count
+cudaError_t launch_pages_copy(const PagesView& pv, int layers, long layer_bytes, const int32_t* src, const int32_t* dst,
+                              int count, const int32_t* number, cudaStream_t st);
+cudaError_t launch_pages_fork(const PagesView& pv, const kvq_pages_fork_args& a, cudaStream_t st);
+cudaError_t launch_pages_grow(const PagesView& pv, const kvq_pages_grow_args& a, int32_t* fresh, int32_t* copies,
+                              cudaStream_t st);
 
 }  // namespace kvq

@@ -92,6 +92,10 @@ size_t carve_pages(const kvq_pages_config& c, kvq_pages* P) {
   off += round256(o * 4);
   const size_t ml = off;
   off += round256(rows * 8);
+  const size_t fresh = off;
+  off += round256((size_t)c.pages * 4);
+  const size_t copies = off;
+  off += round256((4 + 2 * kPagesMaxBatch) * 4);
   if (P) {
     P->L = L;
     P->layer_bytes = layer;
@@ -99,6 +103,8 @@ size_t carve_pages(const kvq_pages_config& c, kvq_pages* P) {
     P->d_split = reinterpret_cast<SplitHead*>(P->base + split);
     P->d_part_o = reinterpret_cast<float*>(P->base + po);
     P->d_part_ml = reinterpret_cast<float*>(P->base + ml);
+    P->d_fresh = reinterpret_cast<int32_t*>(P->base + fresh);
+    P->d_copies = reinterpret_cast<int32_t*>(P->base + copies);
   }
   return off;
 }
@@ -182,6 +188,74 @@ PagesView pages_view(const kvq_pages* P, int layer) {
 }
 }  // namespace kvq
 
+namespace {
+
+// Attention of the rows of `batch`: causal, or masked, by `tree` or (null) over whole sequences.
+kvq_status attend(kvq_pages_t P, int layer, const void* q, int q_dtype, int64_t q_stride, const kvq_pages_batch* batch,
+                  bool masked, const kvq_tree* tree, float softmax_scale, int window, void* out, void* stream) {
+  kvq_status s = usable(P, layer);
+  if (s != KVQ_OK) return s;
+  BatchView bv;
+  s = valid_batch(P, batch, &bv);
+  if (s != KVQ_OK) return s;
+  const kvq_pages_config& c = P->cfg;
+  if (q_dtype != KVQ_F16 && q_dtype != KVQ_BF16) return fail(P, KVQ_ERR_INVALID_ARG, "queries are fp16 or bf16");
+  if (c.k.bits == 16 && q_dtype != c.dtype) return fail(P, KVQ_ERR_INVALID_ARG, "queries and 16-bit pages have one type");
+  if (window < 0) return fail(P, KVQ_ERR_INVALID_ARG, "negative window");
+  if (!(softmax_scale > 0.0f) && !std::isnan(softmax_scale)) softmax_scale = 1.0f / std::sqrt((float)c.head_dim);
+  // in powers of two; not zero, which would turn a hidden score's -inf into NaN
+  const float scale_log2 = std::max(softmax_scale * 1.44269504088896340736f, FLT_MIN);
+  if (!std::isfinite(softmax_scale) || !std::isfinite(scale_log2))
+    return fail(P, KVQ_ERR_INVALID_ARG, "softmax scale not finite");
+  if (bv.new_tokens == 0) return KVQ_OK;
+  if (!q || !out) return fail(P, KVQ_ERR_INVALID_ARG, "null queries or output");
+  if (!fits(q, 2)) return fail(P, KVQ_ERR_INVALID_ARG, "queries not aligned to their type");
+  if (q_stride < (int64_t)c.q_heads * c.head_dim) return fail(P, KVQ_ERR_INVALID_ARG, "stride shorter than a row");
+  if (reinterpret_cast<uintptr_t>(out) & 15) return fail(P, KVQ_ERR_INVALID_ARG, "output not 16-byte aligned");
+  if (overlap(out, q, bv.new_tokens, (int64_t)c.q_heads * c.head_dim * 2, q_stride * 2))
+    return fail(P, KVQ_ERR_INVALID_ARG, "output and queries overlap");
+  AttnArgs a = {};
+  a.pv = pages_view(P, layer);
+  a.bv = bv;
+  a.q = q;
+  a.out = out;
+  a.q_stride = q_stride;
+  a.scale_log2 = scale_log2;
+  a.window = window < (1 << 30) ? window : 0;  // (no sequence is longer)
+  a.rep = c.q_heads / c.kv_heads;
+  a.rep_magic = (65536 + a.rep - 1) / a.rep;
+  a.q_heads = c.q_heads;
+  a.q_bf16 = q_dtype == KVQ_BF16;
+  a.q_aligned = (reinterpret_cast<uintptr_t>(q) & 15) == 0 && q_stride % 8 == 0;
+  a.part_o = P->d_part_o;
+  a.part_ml = P->d_part_ml;
+  a.split = P->d_split;
+  if (tree) {
+    a.seen = reinterpret_cast<const uint32_t*>(tree->seen);
+    a.seen_words = 2 * tree->words;
+    a.positions = tree->positions;
+  }
+  const int max_new = batch->max_new > 0 && batch->max_new < bv.new_tokens ? batch->max_new : bv.new_tokens;
+  return cuda_result(P, launch_pages_attn(P, a, masked, max_new * a.rep, batch->max_new > 0, static_cast<cudaStream_t>(stream)));
+}
+
+// A layer, or all of them: where they begin and how many they are.
+kvq_status usable_layers(kvq_pages* P, int layer, PagesView* pv, int* layers) {
+  const kvq_status s = usable(P, layer == KVQ_ALL_LAYERS ? 0 : layer);
+  if (s != KVQ_OK) return s;
+  *pv = pages_view(P, layer == KVQ_ALL_LAYERS ? 0 : layer);
+  *layers = layer == KVQ_ALL_LAYERS ? P->cfg.layers : 1;
+  return KVQ_OK;
+}
+
+// Do two arrays of 32-bit integers share one?
+bool share(const int32_t* a, int64_t na, const int32_t* b, int64_t nb) {
+  return reinterpret_cast<uintptr_t>(a) < reinterpret_cast<uintptr_t>(b + nb) &&
+         reinterpret_cast<uintptr_t>(b) < reinterpret_cast<uintptr_t>(a + na);
+}
+
+}  // namespace
+
 extern "C" {
 
 kvq_status kvq_pages_bytes(const kvq_pages_config* c, kvq_bytes* out) {
@@ -194,7 +268,7 @@ kvq_status kvq_pages_bytes(const kvq_pages_config* c, kvq_bytes* out) {
   if (c->k.bits != 16) out->metadata = rows * 4.0 * (c->head_dim / c->k.group + c->head_dim / c->v.group);
   size_t o, r;
   part_sizes(*c, &o, &r);
-  out->workspace = 4.0 * (double)o + 8.0 * (double)r;
+  out->workspace = 4.0 * (double)o + 8.0 * (double)r + 4.0 * c->pages + 4.0 * (4 + 2 * kPagesMaxBatch);
   out->total = out->packed + out->metadata + out->workspace;
   out->elements = 2.0 * rows * c->head_dim;
   out->alloc = carve_pages(*c, nullptr);
@@ -268,45 +342,128 @@ kvq_status kvq_pages_read(kvq_pages_t P, int layer, const kvq_pages_batch* batch
 
 kvq_status kvq_pages_attn(kvq_pages_t P, int layer, const void* q, int q_dtype, int64_t q_stride,
                           const kvq_pages_batch* batch, float softmax_scale, int window, void* out, void* stream) {
-  kvq_status s = usable(P, layer);
+  return attend(P, layer, q, q_dtype, q_stride, batch, false, nullptr, softmax_scale, window, out, stream);
+}
+
+kvq_status kvq_pages_cross_attn(kvq_pages_t P, int layer, const void* q, int q_dtype, int64_t q_stride,
+                                const kvq_pages_batch* batch, float softmax_scale, void* out, void* stream) {
+  return attend(P, layer, q, q_dtype, q_stride, batch, true, nullptr, softmax_scale, 0, out, stream);
+}
+
+kvq_status kvq_pages_tree_attn(kvq_pages_t P, int layer, const void* q, int q_dtype, int64_t q_stride,
+                               const kvq_pages_batch* batch, const kvq_tree* tree, float softmax_scale, int window,
+                               void* out, void* stream) {
+  if (!P) return KVQ_ERR_INVALID_ARG;
+  if (!tree || !tree->seen) return fail(P, KVQ_ERR_INVALID_ARG, "no tree");
+  if (tree->words < 1 || tree->words > kTreeWords) return fail(P, KVQ_ERR_INVALID_ARG, "words of a row out of range");
+  if (!fits(tree->seen, 8) || !fits(tree->positions, 4))
+    return fail(P, KVQ_ERR_INVALID_ARG, "tree not aligned to its types");
+  if (window > 0 && window < 64 * tree->words)
+    return fail(P, KVQ_ERR_UNSUPPORTED, "a window shorter than the tree's tokens");
+  if (window > 0 && !tree->positions) return fail(P, KVQ_ERR_INVALID_ARG, "a window needs the tree's positions");
+  return attend(P, layer, q, q_dtype, q_stride, batch, true, tree, softmax_scale, window, out, stream);
+}
+
+kvq_status kvq_pages_tree(kvq_pages_t P, const kvq_pages_batch* batch, const int32_t* parents, int words, uint64_t* seen,
+                          int32_t* positions, void* stream) {
+  kvq_status s = usable(P, 0);
   if (s != KVQ_OK) return s;
   BatchView bv;
   s = valid_batch(P, batch, &bv);
   if (s != KVQ_OK) return s;
-  const kvq_pages_config& c = P->cfg;
-  if (q_dtype != KVQ_F16 && q_dtype != KVQ_BF16) return fail(P, KVQ_ERR_INVALID_ARG, "queries are fp16 or bf16");
-  if (c.k.bits == 16 && q_dtype != c.dtype) return fail(P, KVQ_ERR_INVALID_ARG, "queries and 16-bit pages have one type");
-  if (window < 0) return fail(P, KVQ_ERR_INVALID_ARG, "negative window");
-  if (!(softmax_scale > 0.0f) && !std::isnan(softmax_scale)) softmax_scale = 1.0f / std::sqrt((float)c.head_dim);
-  // in powers of two; not zero, which would turn a hidden score's -inf into NaN
-  const float scale_log2 = std::max(softmax_scale * 1.44269504088896340736f, FLT_MIN);
-  if (!std::isfinite(softmax_scale) || !std::isfinite(scale_log2))
-    return fail(P, KVQ_ERR_INVALID_ARG, "softmax scale not finite");
+  if (words < 1 || words > kTreeWords) return fail(P, KVQ_ERR_INVALID_ARG, "words of a row out of range");
   if (bv.new_tokens == 0) return KVQ_OK;
-  if (!q || !out) return fail(P, KVQ_ERR_INVALID_ARG, "null queries or output");
-  if (!fits(q, 2)) return fail(P, KVQ_ERR_INVALID_ARG, "queries not aligned to their type");
-  if (q_stride < (int64_t)c.q_heads * c.head_dim) return fail(P, KVQ_ERR_INVALID_ARG, "stride shorter than a row");
-  if (reinterpret_cast<uintptr_t>(out) & 15) return fail(P, KVQ_ERR_INVALID_ARG, "output not 16-byte aligned");
-  if (overlap(out, q, bv.new_tokens, (int64_t)c.q_heads * c.head_dim * 2, q_stride * 2))
-    return fail(P, KVQ_ERR_INVALID_ARG, "output and queries overlap");
-  AttnArgs a = {};
-  a.pv = pages_view(P, layer);
-  a.bv = bv;
-  a.q = q;
-  a.out = out;
-  a.q_stride = q_stride;
-  a.scale_log2 = scale_log2;
-  a.window = window < (1 << 30) ? window : 0;  // (no sequence is longer)
-  a.rep = c.q_heads / c.kv_heads;
-  a.rep_magic = (65536 + a.rep - 1) / a.rep;
-  a.q_heads = c.q_heads;
-  a.q_bf16 = q_dtype == KVQ_BF16;
-  a.q_aligned = (reinterpret_cast<uintptr_t>(q) & 15) == 0 && q_stride % 8 == 0;
-  a.part_o = P->d_part_o;
-  a.part_ml = P->d_part_ml;
-  a.split = P->d_split;
-  const int max_new = batch->max_new > 0 && batch->max_new < bv.new_tokens ? batch->max_new : bv.new_tokens;
-  return cuda_result(P, launch_pages_attn(P, a, max_new * a.rep, batch->max_new > 0, static_cast<cudaStream_t>(stream)));
+  if (!parents || !seen) return fail(P, KVQ_ERR_INVALID_ARG, "null parents or masks");
+  if (!fits(parents, 4) || !fits(seen, 8) || !fits(positions, 4))
+    return fail(P, KVQ_ERR_INVALID_ARG, "tree not aligned to its types");
+  return cuda_result(P, launch_pages_tree(pages_view(P, 0), bv, parents, words, seen, positions,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_pages_keep(kvq_pages_t P, int layer, const kvq_pages_batch* batch, const uint8_t* keep, int32_t* lens_out,
+                          void* stream) {
+  PagesView pv;
+  int layers;
+  kvq_status s = usable_layers(P, layer, &pv, &layers);
+  if (s != KVQ_OK) return s;
+  BatchView bv;
+  s = valid_batch(P, batch, &bv);
+  if (s != KVQ_OK) return s;
+  if (!keep && bv.new_tokens > 0) return fail(P, KVQ_ERR_INVALID_ARG, "null marks");
+  if (!fits(lens_out, 4)) return fail(P, KVQ_ERR_INVALID_ARG, "lengths not 4-byte aligned");
+  if (lens_out && share(lens_out, bv.batch, bv.lens, bv.batch))
+    return fail(P, KVQ_ERR_INVALID_ARG, "new lengths over the old ones");
+  if (bv.new_tokens == 0 && !lens_out) return KVQ_OK;
+  return cuda_result(P, launch_pages_keep(pv, layers, (long)P->layer_bytes, bv, keep, lens_out,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_pages_copy(kvq_pages_t P, int layer, const int32_t* src, const int32_t* dst, int count, void* stream) {
+  PagesView pv;
+  int layers;
+  const kvq_status s = usable_layers(P, layer, &pv, &layers);
+  if (s != KVQ_OK) return s;
+  if (count < 0) return fail(P, KVQ_ERR_INVALID_ARG, "negative count of pages");
+  if (count == 0) return KVQ_OK;
+  if (!src || !dst) return fail(P, KVQ_ERR_INVALID_ARG, "null pages");
+  if (!fits(src, 4) || !fits(dst, 4)) return fail(P, KVQ_ERR_INVALID_ARG, "pages not 4-byte aligned");
+  return cuda_result(P, launch_pages_copy(pv, layers, (long)P->layer_bytes, src, dst, count, nullptr,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_pages_fork(kvq_pages_t P, const kvq_pages_fork_args* a, void* stream) {
+  const kvq_status s = usable(P, 0);
+  if (s != KVQ_OK) return s;
+  if (!a) return fail(P, KVQ_ERR_INVALID_ARG, "no arguments");
+  if (a->rows_in < 1 || a->rows_in > kPagesMaxBatch || a->rows_out < 1 || a->rows_out > kPagesMaxBatch)
+    return fail(P, KVQ_ERR_INVALID_ARG, "rows out of range");
+  if (a->stride_in < 1 || a->stride_in > (1L << 30) || a->stride_out < 1 || a->stride_out > (1L << 30))
+    return fail(P, KVQ_ERR_INVALID_ARG, "table stride out of range");
+  if (!a->parent || !a->table_in || !a->lens_in || !a->refs_in || !a->table_out || !a->lens_out || !a->refs_out)
+    return fail(P, KVQ_ERR_INVALID_ARG, "null array");
+  if (!fits(a->parent, 4) || !fits(a->table_in, 4) || !fits(a->lens_in, 4) || !fits(a->refs_in, 4) ||
+      !fits(a->table_out, 4) || !fits(a->lens_out, 4) || !fits(a->refs_out, 4))
+    return fail(P, KVQ_ERR_INVALID_ARG, "array not 4-byte aligned");
+  const int64_t pages = P->cfg.pages;
+  const struct {
+    const int32_t* p;
+    int64_t n;
+  } in[] = {{a->parent, a->rows_out}, {a->table_in, a->rows_in * a->stride_in}, {a->lens_in, a->rows_in}, {a->refs_in, pages}},
+    out[] = {{a->table_out, a->rows_out * a->stride_out}, {a->lens_out, a->rows_out}, {a->refs_out, pages}};
+  for (int o = 0; o < 3; ++o) {
+    for (const auto& i : in)
+      if (share(out[o].p, out[o].n, i.p, i.n) && !(o == 2 && i.p == a->refs_in && a->refs_out == a->refs_in))
+        return fail(P, KVQ_ERR_INVALID_ARG, "what is written lies over what is read");
+    for (int x = 0; x < o; ++x)
+      if (share(out[o].p, out[o].n, out[x].p, out[x].n)) return fail(P, KVQ_ERR_INVALID_ARG, "outputs overlap");
+  }
+  return cuda_result(P, launch_pages_fork(pages_view(P, 0), *a, static_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_pages_grow(kvq_pages_t P, const kvq_pages_grow_args* a, void* stream) {
+  PagesView pv;
+  int layers;
+  const kvq_status s = usable_layers(P, KVQ_ALL_LAYERS, &pv, &layers);
+  if (s != KVQ_OK) return s;
+  if (!a) return fail(P, KVQ_ERR_INVALID_ARG, "no arguments");
+  if (a->sequences < 1 || a->sequences > kPagesMaxBatch) return fail(P, KVQ_ERR_INVALID_ARG, "sequences out of range");
+  if (a->table_stride < 1 || a->table_stride > (1L << 30)) return fail(P, KVQ_ERR_INVALID_ARG, "table stride out of range");
+  if (!a->q_start || !a->lens || !a->table || !a->refs || !a->lens_out) return fail(P, KVQ_ERR_INVALID_ARG, "null array");
+  if (!fits(a->q_start, 4) || !fits(a->lens, 4) || !fits(a->table, 4) || !fits(a->refs, 4) || !fits(a->lens_out, 4))
+    return fail(P, KVQ_ERR_INVALID_ARG, "array not 4-byte aligned");
+  const int64_t n = a->sequences, pages = P->cfg.pages, entries = n * a->table_stride;
+  if ((a->lens_out != a->lens && share(a->lens_out, n, a->lens, n)) || share(a->lens_out, n, a->q_start, n + 1) ||
+      share(a->lens_out, n, a->table, entries) || share(a->lens_out, n, a->refs, pages) ||
+      share(a->table, entries, a->refs, pages) || share(a->table, entries, a->lens, n) ||
+      share(a->table, entries, a->q_start, n + 1) || share(a->refs, pages, a->lens, n) ||
+      share(a->refs, pages, a->q_start, n + 1))
+    return fail(P, KVQ_ERR_INVALID_ARG, "arrays overlap");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_pages_grow(pv, *a, P->d_fresh, P->d_copies, st);
+  if (e == cudaSuccess)
+    e = launch_pages_copy(pv, layers, (long)P->layer_bytes, P->d_copies + 4, P->d_copies + 4 + kPagesMaxBatch,
+                          a->sequences, P->d_copies, st);
+  return cuda_result(P, e);
 }
 
 kvq_status kvq_pages_set_kernel(kvq_pages_t P, int which) {
@@ -324,7 +481,8 @@ kvq_status kvq_pages_status(kvq_pages_t P, void* stream) {
   if (e == cudaSuccess && word) e = cudaMemsetAsync(P->d_err, 0, sizeof(int), st);
   if (e != cudaSuccess) return cuda_result(P, e);
   if (word & 2) return fail(P, KVQ_ERR_DEVICE_TIMEOUT, "a device-side wait gave up");
-  return word ? fail(P, KVQ_ERR_BAD_INDEX, "a page, length or position was out of range") : KVQ_OK;
+  if (word & 1) return fail(P, KVQ_ERR_BAD_INDEX, "a page, length or position was out of range");
+  return word ? fail(P, KVQ_ERR_OUT_OF_PAGES, "fewer free pages than the sequences needed") : KVQ_OK;
 }
 
 const char* kvq_pages_last_error(kvq_pages_t P) { return P ? P->last_error.c_str() : ""; }

@@ -109,7 +109,7 @@ cudaError_t launch_kernel(const AttnKernel& k, AttnArgs a, int ctas, int rows, i
   return launch_pdl(join, dim3(ctas, y), dim3(kJoinWarps * 32), 0, st, args);
 }
 
-cudaError_t launch_rows(kvq_pages* P, AttnArgs a, int max_rows, cudaStream_t st) {
+cudaError_t launch_rows(kvq_pages* P, AttnArgs a, bool masked, int max_rows, cudaStream_t st) {
   // As few row tiles of 8 as hold a sequence's rows, up to 32 rows (16 at head_dim
   // 256): the cache is then read once for all of them, and no product is made for
   // rows that are not there.  32 sequences of 4096 4-bit tokens, 8 / 16 / 24 / 32
@@ -117,19 +117,20 @@ cudaError_t launch_rows(kvq_pages* P, AttnArgs a, int max_rows, cudaStream_t st)
   // 37 / 44; 20 rows over 8-bit pages 60, in two turns of 16 rows 94.
   const int most = P->cfg.head_dim == 256 ? 16 : kRowsPerCta;
   const int blocks = (max_rows + most - 1) / most, nm = ((max_rows + blocks - 1) / blocks + 7) / 8;
-  const AttnKernel& k = P->rows_fn[nm - 1];
+  const AttnKernel& k = P->rows_fn[masked][nm - 1];
   a.min_units = 2;
   return launch_kernel(k, a, std::min(resident(P, k, a.bv.batch) * P->sm_count, kPagesCtas), 8 * nm, max_rows, st);
 }
 
-cudaError_t launch_tile(kvq_pages* P, AttnArgs a, int max_rows, cudaStream_t st) {
+cudaError_t launch_tile(kvq_pages* P, AttnArgs a, bool masked, int max_rows, cudaStream_t st) {
+  const AttnKernel& k = P->tile_fn[masked];
   a.min_units = 2;
   if (P->L.k_bits != 16) {
-    const int left = P->max_smem - (int)(P->tile_fn.static_smem + launch_smem(P->tile_fn, a.bv.batch));
+    const int left = P->max_smem - (int)(k.static_smem + launch_smem(k, a.bv.batch));
     a.ring = std::min(left / P->L.tile_bytes, kTileRing);
     if (a.ring < 2) return cudaErrorInvalidConfiguration;  // (not reached: two of the largest records fit)
   }
-  return launch_kernel(P->tile_fn, a, std::min(P->sm_count, kTileCtas), a.pv.head_dim == 256 ? kTileRows / 2 : kTileRows,
+  return launch_kernel(k, a, std::min(P->sm_count, kTileCtas), a.pv.head_dim == 256 ? kTileRows / 2 : kTileRows,
                        max_rows, st);
 }
 
@@ -144,14 +145,20 @@ int pages_format(const kvq_pages* P) {
 
 cudaError_t pages_attn_setup(kvq_pages* P) {
   const int D = P->cfg.head_dim, fmt = pages_format(P);
-  for (int nm = 1; nm <= (D < 256 ? 4 : 2); ++nm)
-    P->rows_fn[nm - 1] = D == 64 ? rows_kernel_d64(fmt, nm) : D == 128 ? rows_kernel_d128(fmt, nm) : rows_kernel_d256(fmt, nm);
-  P->tile_fn = D == 64 ? tile_kernel_d64(fmt) : D == 128 ? tile_kernel_d128(fmt) : tile_kernel_d256(fmt);
+  for (int nm = 1; nm <= (D < 256 ? 4 : 2); ++nm) {
+    P->rows_fn[0][nm - 1] = D == 64 ? rows_kernel_d64(fmt, nm) : D == 128 ? rows_kernel_d128(fmt, nm) : rows_kernel_d256(fmt, nm);
+    P->rows_fn[1][nm - 1] = D == 64    ? rows_mask_kernel_d64(fmt, nm)
+                            : D == 128 ? rows_mask_kernel_d128(fmt, nm)
+                                       : rows_mask_kernel_d256(fmt, nm);
+  }
+  P->tile_fn[0] = D == 64 ? tile_kernel_d64(fmt) : D == 128 ? tile_kernel_d128(fmt) : tile_kernel_d256(fmt);
+  P->tile_fn[1] = D == 64 ? tile_mask_kernel_d64(fmt) : D == 128 ? tile_mask_kernel_d128(fmt) : tile_mask_kernel_d256(fmt);
   cudaError_t e = cudaDeviceGetAttribute(&P->sm_smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor, P->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P->cta_smem, cudaDevAttrReservedSharedMemoryPerBlock, P->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P->max_smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, P->device);
   if (e != cudaSuccess) return e;
-  for (AttnKernel* k : {&P->rows_fn[0], &P->rows_fn[1], &P->rows_fn[2], &P->rows_fn[3], &P->tile_fn}) {
+  for (int i = 0; i < 10; ++i) {
+    AttnKernel* k = i % 5 == 4 ? &P->tile_fn[i / 5] : &P->rows_fn[i / 5][i % 5];
     if (!k->fn) continue;
     cudaFuncAttributes at;
     e = cudaFuncGetAttributes(&at, k->fn);
@@ -165,7 +172,7 @@ cudaError_t pages_attn_setup(kvq_pages* P) {
   return cudaSuccess;
 }
 
-cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, int max_rows, bool rows_given, cudaStream_t st) {
+cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, bool masked, int max_rows, bool rows_given, cudaStream_t st) {
   // Sequences with at most `few` rows (new tokens x query heads per kv head) go to
   // the few-rows kernel, the others to the many-rows one; a batch that may hold
   // both kinds launches both.  Over 16-bit pages that goes for a single sequence of
@@ -181,14 +188,14 @@ cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, int max_rows, bool rows
   const int few = P->L.k_bits == 16 ? 32 : (D == 64 ? 128 : (D == 128 ? 64 : 48));
   a.rows_lo = 0;
   a.rows_hi = INT_MAX;
-  if (P->which == 1 || (P->which == 0 && max_rows <= few)) return launch_rows(P, a, max_rows, st);
-  if (P->which == 2 || (a.bv.batch == 1 && (rows_given || P->L.k_bits != 16))) return launch_tile(P, a, max_rows, st);
+  if (P->which == 1 || (P->which == 0 && max_rows <= few)) return launch_rows(P, a, masked, max_rows, st);
+  if (P->which == 2 || (a.bv.batch == 1 && (rows_given || P->L.k_bits != 16))) return launch_tile(P, a, masked, max_rows, st);
   a.rows_lo = few;
-  cudaError_t e = launch_tile(P, a, max_rows, st);
+  cudaError_t e = launch_tile(P, a, masked, max_rows, st);
   if (e != cudaSuccess) return e;
   a.rows_lo = 0;
   a.rows_hi = few;
-  return launch_rows(P, a, few, st);
+  return launch_rows(P, a, masked, few, st);
 }
 
 }  // namespace kvq

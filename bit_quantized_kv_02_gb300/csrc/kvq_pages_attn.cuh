@@ -141,13 +141,46 @@ __device__ __forceinline__ Seq load_seq(const PagesView& pv, const BatchView& bv
   return s;
 }
 
+// A sequence as attention takes it.  MASK: rows see the tokens before p0, and of
+// those from p0 on the ones that a.seen names; without a.seen all tokens lie before p0.
+template <bool MASK>
+__device__ __forceinline__ Seq attn_seq(const AttnArgs& a, int b, bool* bad) {
+  Seq s = load_seq(a.pv, a.bv, b, bad);
+  if constexpr (MASK) {
+    if (!a.seen) s.p0 = s.len;
+    else if (s.n > 32 * a.seen_words) *bad = true;
+  }
+  return s;
+}
+
+// Which of the tokens c .. c + 31 a row of the call sees (masked kernels): bit i
+// stands for token c + i.  A window hides none of the new tokens: it is no shorter
+// than they are many.
+__device__ __forceinline__ uint32_t seen_bits(const AttnArgs& a, const Seq& s, int row, int c) {
+  const int o = c - s.p0, n = s.len - s.p0;  // place among the masked tokens, their number
+  uint32_t v = o <= -32 ? 0xffffffffu : (o < 0 ? (1u << -o) - 1 : 0u);
+  if (o > -32 && o < n) {
+    const uint32_t* w = a.seen + (long)row * a.seen_words;
+    const int i = o >> 5;  // -1 where the past ends among the 32
+    const uint32_t lo = i >= 0 && i < a.seen_words ? w[i] : 0u, hi = i + 1 < a.seen_words ? w[i + 1] : 0u;
+    uint32_t m = __funnelshift_r(lo, hi, o & 31);
+    if (n - o < 32) m &= (1u << (n - o)) - 1;
+    v |= m;
+  }
+  if (a.window > 0) {
+    const int gone = max(min(a.positions[row], s.len - 1), s.p0) - a.window + 1 - c;
+    if (gone > 0) v &= gone < 32 ? 0xffffffffu << gone : 0u;
+  }
+  return v;
+}
+
 // Tokens that rows [r0, r1) of the sequence may see, in blocks of BK: the
 // first block and their number (at least one: an item without tokens still
 // writes its zeros).
-template <int BK>
+template <int BK, bool MASK>
 __device__ __forceinline__ void row_blocks(const Seq& s, int rep, int window, int r0, int r1, int* lo, int* nb) {
-  const int hi = max(s.p0 + (r1 - 1) / rep + 1, 0);
-  const int first = window > 0 ? max((long)s.p0 + r0 / rep - window + 1, 0L) : 0;
+  const int hi = MASK ? s.len : max(s.p0 + (r1 - 1) / rep + 1, 0);
+  const int first = window > 0 ? max((long)s.p0 + (MASK ? 0 : r0 / rep) - window + 1, 0L) : 0;
   *lo = first / BK;
   *nb = max((hi + BK - 1) / BK - *lo, 1);
 }
@@ -173,14 +206,14 @@ struct Work {
   int own;  // > 0: items have CTAs of their own, one per `own` blocks; pre counts CTAs
 };
 
-template <int BK, int ROWS>
+template <int BK, int ROWS, bool MASK>
 __device__ __forceinline__ long seq_units(const AttnArgs& a, const Seq& s, int lane) {
   const int R = s.n * a.rep;
   if (R <= a.rows_lo || R > a.rows_hi) return 0;
   long sum = 0;
   for (int m = lane; m < (R + ROWS - 1) / ROWS; m += 32) {
     int lo, nb;
-    row_blocks<BK>(s, a.rep, a.window, m * ROWS, min(R, (m + 1) * ROWS), &lo, &nb);
+    row_blocks<BK, MASK>(s, a.rep, a.window, m * ROWS, min(R, (m + 1) * ROWS), &lo, &nb);
     sum += nb;
   }
 #pragma unroll
@@ -189,7 +222,7 @@ __device__ __forceinline__ long seq_units(const AttnArgs& a, const Seq& s, int l
 }
 
 // Units of a sequence's kv head, by one thread; *one: it has a single block of rows.
-template <int BK, int ROWS>
+template <int BK, int ROWS, bool MASK>
 __device__ __forceinline__ long seq_units_serial(const AttnArgs& a, const Seq& s, bool* one) {
   const int R = s.n * a.rep;
   *one = true;
@@ -198,7 +231,7 @@ __device__ __forceinline__ long seq_units_serial(const AttnArgs& a, const Seq& s
   long sum = 0;
   for (int r0 = 0; r0 < R; r0 += ROWS) {
     int lo, nb;
-    row_blocks<BK>(s, a.rep, a.window, r0, min(R, r0 + ROWS), &lo, &nb);
+    row_blocks<BK, MASK>(s, a.rep, a.window, r0, min(R, r0 + ROWS), &lo, &nb);
     sum += nb;
   }
   return sum;
@@ -207,23 +240,23 @@ __device__ __forceinline__ long seq_units_serial(const AttnArgs& a, const Seq& s
 // All threads of the CTA; leaves the line in *w, its units before each sequence
 // in `pre`.  FEW: sequences have a block of rows or so, a thread each; else a warp
 // each.
-template <int BK, int ROWS, bool FEW>
+template <int BK, int ROWS, bool FEW, bool MASK>
 __device__ __forceinline__ void plan_work(const AttnArgs& a, Work<BK, ROWS>* w, long* pre) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   int alone = 1;
   if (FEW) {
     for (int b = threadIdx.x; b < a.bv.batch; b += blockDim.x) {
       bool bad, one;
-      const Seq s = load_seq(a.pv, a.bv, b, &bad);
-      pre[b + 1] = seq_units_serial<BK, ROWS>(a, s, &one);
+      const Seq s = attn_seq<MASK>(a, b, &bad);
+      pre[b + 1] = seq_units_serial<BK, ROWS, MASK>(a, s, &one);
       alone = alone && one;
       if (bad) atomicOr(a.pv.err, 1);
     }
   } else {
     for (int b = warp; b < a.bv.batch; b += warps) {
       bool bad;
-      const Seq s = load_seq(a.pv, a.bv, b, &bad);
-      const long u = seq_units<BK, ROWS>(a, s, lane);
+      const Seq s = attn_seq<MASK>(a, b, &bad);
+      const long u = seq_units<BK, ROWS, MASK>(a, s, lane);
       if (lane == 0) {
         pre[b + 1] = u;
         if (bad) atomicOr(a.pv.err, 1);
@@ -283,7 +316,7 @@ __device__ __forceinline__ int cta_of(const Work<BK, ROWS>* w, long u) {
 }
 
 // CTA cta's piece where items have CTAs of their own.
-template <int BK, int ROWS>
+template <bool MASK, int BK, int ROWS>
 __device__ __forceinline__ Piece own_piece(const AttnArgs& a, const Work<BK, ROWS>* w, int cta) {
   int lo = 0, hi = a.bv.batch;  // pre[lo] <= cta < pre[hi]
   while (hi - lo > 1) {
@@ -294,14 +327,14 @@ __device__ __forceinline__ Piece own_piece(const AttnArgs& a, const Work<BK, ROW
   Piece p;
   p.b = lo;
   bool bad;
-  p.s = load_seq(a.pv, a.bv, lo, &bad);
+  p.s = attn_seq<MASK>(a, lo, &bad);
   const int per_head = (int)(w->pre[lo + 1] - w->pre[lo]) / a.pv.heads, at = cta - (int)w->pre[lo];
   p.head = at / per_head;
   const int part = at - p.head * per_head;
   int blk0, nb;
   p.r0 = 0;
   p.rows = p.s.n * a.rep;
-  row_blocks<BK>(p.s, a.rep, a.window, 0, p.rows, &blk0, &nb);
+  row_blocks<BK, MASK>(p.s, a.rep, a.window, 0, p.rows, &blk0, &nb);
   const int from = (int)((long)nb * part / per_head), to = (int)((long)nb * (part + 1) / per_head);
   p.blk = blk0 + from;
   p.nblk = to - from;
@@ -313,7 +346,7 @@ __device__ __forceinline__ Piece own_piece(const AttnArgs& a, const Work<BK, ROW
 }
 
 // The piece that starts at unit u and ends by `end`; all lanes of a warp.
-template <int BK, int ROWS>
+template <bool MASK, int BK, int ROWS>
 __device__ __forceinline__ Piece find_piece(const AttnArgs& a, const Work<BK, ROWS>* w, long u, long end) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = a.bv.batch;  // pre[lo] <= u < pre[hi]
@@ -325,7 +358,7 @@ __device__ __forceinline__ Piece find_piece(const AttnArgs& a, const Work<BK, RO
   Piece p;
   p.b = lo;
   bool bad;
-  p.s = load_seq(a.pv, a.bv, lo, &bad);
+  p.s = attn_seq<MASK>(a, lo, &bad);
   const long per_head = (w->pre[lo + 1] - w->pre[lo]) / a.pv.heads;
   p.head = (int)((u - w->pre[lo]) / per_head);
   const long base = w->pre[lo] + per_head * p.head;
@@ -335,7 +368,7 @@ __device__ __forceinline__ Piece find_piece(const AttnArgs& a, const Work<BK, RO
   int blk0 = 0, nb = 0, m = 0;
   for (int m0 = 0; m0 < tiles; m0 += 32) {
     int l = 0, n = 0;
-    if (m0 + lane < tiles) row_blocks<BK>(p.s, a.rep, a.window, (m0 + lane) * ROWS, min(R, (m0 + lane + 1) * ROWS), &l, &n);
+    if (m0 + lane < tiles) row_blocks<BK, MASK>(p.s, a.rep, a.window, (m0 + lane) * ROWS, min(R, (m0 + lane + 1) * ROWS), &l, &n);
     long x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

@@ -1,0 +1,490 @@
+// kvq_pages_branch.cu — sequences that branch, on the paged cache: masks of drafted
+// trees, keeping some of a sequence's tokens, copying pages, and tables whose rows
+// share pages (fork, grow).
+#include <algorithm>
+
+#include "kvq_internal.h"
+#include "kvq_pages_attn.cuh"
+
+namespace kvq {
+
+namespace {
+
+// -------------------------------------------------------------------- tree --
+
+constexpr int kTreeThreads = 64 * kTreeWords;  // a thread per drafted token
+
+// A CTA per sequence.  A row's mask is its chain of parents, followed in shared
+// memory (parents are smaller than their children, so a chain ends); its position is
+// the chain's length behind the past.
+__global__ void __launch_bounds__(kTreeThreads) pages_tree_kernel(PagesView pv, BatchView bv, const int32_t* parents,
+                                                                 int words, uint64_t* seen, int32_t* positions) {
+  __shared__ int up[kTreeThreads];
+  const int b = blockIdx.x, i = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  bool bad;
+  const Seq s = load_seq(pv, bv, b, &bad);
+  if (bad || s.n > 64 * words) {  // (the same for all threads)
+    if (i == 0) atomicOr(pv.err, 1);
+    return;
+  }
+  const long row = (long)s.s0 + i;
+  if (i < s.n) {
+    int p = parents[row];
+    if (p < -1 || p >= i) {
+      atomicOr(pv.err, 1);
+      p = -1;
+    }
+    up[i] = p;
+  }
+  __syncthreads();
+  if (i >= s.n) return;
+  uint64_t m[kTreeWords] = {};
+  int depth = 0;
+  for (int j = i; j >= 0; j = up[j], ++depth) {
+#pragma unroll
+    for (int w = 0; w < kTreeWords; ++w)
+      if (j >> 6 == w) m[w] |= 1ull << (j & 63);
+  }
+#pragma unroll
+  for (int w = 0; w < kTreeWords; ++w)
+    if (w < words) seen[row * words + w] = m[w];
+  if (positions) positions[row] = s.p0 + depth - 1;
+}
+
+// -------------------------------------------------------------------- keep --
+
+constexpr int kKeepThreads = 256;
+
+// What a thread moves of every token of a (layer, head): 16 bytes of a row, or one
+// (zero, step) pair.
+struct Column {
+  long at;        // of token 0 of a record, from the record's head
+  int stride;     // from a token to the next
+  int swizzle;    // 16-bit rows: chunk index inside the 128-byte row, else -1
+  bool wide;      // 16 bytes, else 4
+};
+
+// Columns of one tensor's codes or values, and of its metadata.
+__host__ __device__ __forceinline__ int row_columns(const PagesView& pv, int bits) { return pv.head_dim * bits / 128; }
+__host__ __device__ __forceinline__ int meta_columns(const PagesView& pv, int bits, int lg) {
+  return bits == 16 ? 0 : pv.head_dim >> lg;
+}
+__host__ __device__ __forceinline__ int columns(const PagesView& pv) {
+  return row_columns(pv, pv.L.k_bits) + row_columns(pv, pv.L.v_bits) + meta_columns(pv, pv.L.k_bits, pv.L.k_lg) +
+         meta_columns(pv, pv.L.v_bits, pv.L.v_lg);
+}
+
+__device__ __forceinline__ Column column_of(const PagesView& pv, int c) {
+  const PagesLayout& L = pv.L;
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    const int bits = side ? L.v_bits : L.k_bits, n = row_columns(pv, bits), off = side ? L.v_off : 0;
+    if (c < n) {
+      if (bits == 16) return {off + (c >> 3) * 2048, 128, c & 7, true};
+      return {off + c * 16, pv.head_dim * bits / 8, -1, true};
+    }
+    c -= n;
+  }
+  const int n = meta_columns(pv, L.k_bits, L.k_lg);
+  if (c < n) return {L.km_off + c * 4, n * 4, -1, false};
+  c -= n;
+  return {L.vm_off + c * 4, meta_columns(pv, L.v_bits, L.v_lg) * 4, -1, false};
+}
+
+// A token's place: its record's offset in a layer for head 0, and its number in the
+// record in the low four bits (records are a multiple of 64 bytes).
+__device__ __forceinline__ long place_of(const PagesView& pv, int page, int slot) {
+  return (long)(record_of(pv, page, 0, slot) - pv.base) | (slot & 15);
+}
+
+// The CTAs of column blockIdx.y go through one sequence's marks; each thread moves
+// one column (16 bytes of a row) of one (layer, head) for all kept tokens.  No other
+// thread touches those bytes, and tokens only move down, to places in their order:
+// a thread that reads some tokens, then writes them, then goes on to the next never
+// overwrites what it has yet to read.
+__global__ void __launch_bounds__(kKeepThreads) pages_keep_kernel(PagesView pv, long layer_bytes, long units, BatchView bv,
+                                                                 const uint8_t* keep, int32_t* lens_out) {
+  __shared__ long2 move[kKeepThreads];
+  __shared__ int sums[kKeepThreads / 32];
+  __shared__ int kept_here;
+  const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  pdl_trigger();
+  bool bad;
+  const Seq s = load_seq(pv, bv, b, &bad);
+  if (bad) {
+    if (blockIdx.x == 0 && tid == 0) {
+      atomicOr(pv.err, 1);
+      if (lens_out) lens_out[b] = bv.lens[b];
+    }
+    return;
+  }
+  const long unit = (long)blockIdx.x * kKeepThreads + tid;
+  const int ncol = columns(pv);
+  const bool mine = unit < units;
+  const long lh = mine ? unit / ncol : 0;  // layer * heads + head
+  const Column col = column_of(pv, mine ? (int)(unit - lh * ncol) : 0);
+  char* base = pv.base + (lh / pv.heads) * layer_bytes + (lh % pv.heads) * page_head_bytes(pv) + col.at;
+  auto at = [&](long place) {
+    const int t = (int)(place & 15);
+    return base + (place & ~15L) + t * col.stride + (col.swizzle < 0 ? 0 : (col.swizzle ^ (t & 7)) << 4);
+  };
+  const int skip = max(-s.p0, 0);  // rows that stand before the sequence
+  int first = s.p0 + skip;         // where the next kept token goes
+  for (int i0 = skip; i0 < s.n; i0 += kKeepThreads) {
+    // the marks of 256 rows; places of the kept ones that move
+    const int i = i0 + tid;
+    const bool on = i < s.n && keep[(long)s.s0 + i] != 0;
+    const unsigned ballot = __ballot_sync(0xffffffffu, on);
+    if (lane == 0) sums[warp] = __popc(ballot);
+    __syncthreads();
+    int before = __popc(ballot & ((1u << lane) - 1)), all = 0;
+#pragma unroll
+    for (int w = 0; w < kKeepThreads / 32; ++w) {
+      if (w < warp) before += sums[w];
+      all += sums[w];
+    }
+    if (on) {
+      const int from = s.p0 + i, to = first + before;
+      long2 m = make_long2(-1, -1);
+      if (from != to) {
+        const int pf = bv.table[b * bv.stride + (from >> pv.lg_pt)], pt = bv.table[b * bv.stride + (to >> pv.lg_pt)];
+        if ((unsigned)pf < (unsigned)pv.pages && (unsigned)pt < (unsigned)pv.pages) {
+          m = make_long2(place_of(pv, pf, from & ((1 << pv.lg_pt) - 1)), place_of(pv, pt, to & ((1 << pv.lg_pt) - 1)));
+        } else if (blockIdx.x == 0) {
+          atomicOr(pv.err, 1);
+        }
+      }
+      move[before] = m;
+    }
+    first += all;
+    __syncthreads();
+    if (mine) {
+      constexpr int U = 8;  // tokens in flight
+      for (int j = 0; j < all; j += U) {
+        uint4 x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (j + u < all && move[j + u].x >= 0) {
+            if (col.wide) x[u] = *reinterpret_cast<const uint4*>(at(move[j + u].x));
+            else x[u].x = *reinterpret_cast<const uint32_t*>(at(move[j + u].x));
+          }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (j + u < all && move[j + u].x >= 0) {
+            if (col.wide) *reinterpret_cast<uint4*>(at(move[j + u].y)) = x[u];
+            else *reinterpret_cast<uint32_t*>(at(move[j + u].y)) = x[u].x;
+          }
+      }
+    }
+    __syncthreads();
+  }
+  if (lens_out && blockIdx.x == 0 && tid == 0) lens_out[b] = first;
+}
+
+// -------------------------------------------------------------------- copy --
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 4;
+constexpr int kCopyBytes = kCopyThreads * kCopyUnroll * 16;  // of a page that a CTA moves at a time
+
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(PagesView pv, int layers, long layer_bytes,
+                                                                 const int32_t* src, const int32_t* dst, int count,
+                                                                 const int32_t* number) {
+  pdl_wait();
+  pdl_trigger();
+  const int pairs = number ? min(*number, count) : count;
+  const long bytes = pv.heads * page_head_bytes(pv), chunks = (bytes + kCopyBytes - 1) / kCopyBytes;
+  for (long w = blockIdx.x; w < (long)pairs * layers * chunks; w += gridDim.x) {
+    const long pl = w / chunks, chunk = w - pl * chunks;
+    const int pair = (int)(pl / layers), layer = (int)(pl - (long)pair * layers);
+    const int from = src[pair], to = dst[pair];
+    if (from < 0 || to < 0) continue;
+    if (from >= pv.pages || to >= pv.pages) {
+      if (threadIdx.x == 0) atomicOr(pv.err, 1);
+      continue;
+    }
+    const char* x = pv.base + layer * layer_bytes + from * bytes;
+    char* y = pv.base + layer * layer_bytes + to * bytes;
+    uint4 v[kCopyUnroll];
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u) {
+      const long at = chunk * kCopyBytes + (u * kCopyThreads + threadIdx.x) * 16;
+      if (at < bytes) v[u] = *reinterpret_cast<const uint4*>(x + at);
+    }
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u) {
+      const long at = chunk * kCopyBytes + (u * kCopyThreads + threadIdx.x) * 16;
+      if (at < bytes) *reinterpret_cast<uint4*>(y + at) = v[u];
+    }
+  }
+}
+
+// -------------------------------------------------------------------- fork --
+
+constexpr int kForkThreads = 256;
+
+// Row b of the new table from row parent[b] of the old one.
+__global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(PagesView pv, kvq_pages_fork_args a) {
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.y;
+  const long i0 = (long)blockIdx.x * kForkThreads + threadIdx.x, step = (long)gridDim.x * kForkThreads;
+  if (b == a.rows_out) {  // the last rows of CTAs: reference counts
+    if (a.refs_out != a.refs_in)
+      for (long i = i0; i < pv.pages; i += step) a.refs_out[i] = a.refs_in[i];
+    return;
+  }
+  const int p = a.parent[b];
+  bool bad = p < -1 || p >= a.rows_in;
+  int len = 0;
+  long held = 0;  // pages that hold its tokens
+  if (p >= 0 && !bad) {
+    len = a.lens_in[p];
+    const long tokens = len < 0 ? -1L - len : len;
+    held = (tokens + (1 << pv.lg_pt) - 1) >> pv.lg_pt;
+    bad = held > a.stride_in || held > a.stride_out;
+  }
+  if (bad) len = 0, held = 0;
+  for (long i = i0; i < a.stride_out; i += step) {
+    int page = -1;
+    if (i < held) {
+      page = a.table_in[p * a.stride_in + i];
+      if ((unsigned)page >= (unsigned)pv.pages) bad = true, page = -1;
+    }
+    a.table_out[b * a.stride_out + i] = page;
+  }
+  if (bad) atomicOr(pv.err, 1);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.lens_out[b] = len;
+}
+
+// References: one less for a name that left, one more for one that came.
+__global__ void __launch_bounds__(kForkThreads) pages_refs_kernel(PagesView pv, kvq_pages_fork_args a) {
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.y;
+  const long most = max(a.stride_in, a.stride_out);
+  for (long i = (long)blockIdx.x * kForkThreads + threadIdx.x; i < most; i += (long)gridDim.x * kForkThreads) {
+    const int was = b < a.rows_in && i < a.stride_in ? a.table_in[b * a.stride_in + i] : -1;
+    const int is = b < a.rows_out && i < a.stride_out ? a.table_out[b * a.stride_out + i] : -1;
+    if (was == is) continue;
+    if (was >= pv.pages) atomicOr(pv.err, 1);
+    else if (was >= 0) atomicSub(a.refs_out + was, 1);
+    if (is >= 0) atomicAdd(a.refs_out + is, 1);
+  }
+}
+
+// -------------------------------------------------------------------- grow --
+
+constexpr int kGrowThreads = kPagesMaxBatch;  // a thread per sequence
+constexpr int kGrowWarps = kGrowThreads / 32;
+constexpr int kScan = 16;                     // reference counts that a thread has in flight
+
+struct GrowArgs {
+  kvq_pages_grow_args a;
+  int32_t* fresh;   // [pages]
+  int32_t *number, *src, *dst;
+};
+
+// The whole CTA: exclusive prefix sums of one value a thread; *total: of all.
+__device__ __forceinline__ int block_scan(int x, int* sums, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int y = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
+  }
+  if (lane == 31) sums[warp] = y;
+  __syncthreads();
+  int v = sums[lane], s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += z;
+  }
+  const int base = __shfl_sync(0xffffffffu, s - v, warp);
+  *total = __shfl_sync(0xffffffffu, s, 31);
+  __syncthreads();
+  return base + y - x;
+}
+
+// One CTA deals out the pages: what a sequence gets depends on all before it.
+__global__ void __launch_bounds__(kGrowThreads) pages_grow_kernel(PagesView pv, GrowArgs g) {
+  __shared__ int page[kGrowThreads];     // the page that holds the sequence's last tokens and is grown into, or -1
+  __shared__ int first[kGrowThreads], last[kGrowThreads];  // entries of the table that the new tokens need
+  __shared__ int need[kGrowThreads], from[kGrowThreads];   // fresh pages (then: does it get them?), and the first one's number
+  __shared__ bool copies[kGrowThreads];
+  __shared__ int sums[32], found_in[kScan * kGrowWarps];
+  const kvq_pages_grow_args& a = g.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, S = a.sequences;
+  pdl_wait();
+  pdl_trigger();
+  // ---- each sequence's part of the table
+  const long cap = min(a.table_stride << pv.lg_pt, 1L << 30);
+  int len = 0, n = 0, p = -1;
+  bool bad = false;
+  first[tid] = 0, last[tid] = -1;
+  if (tid < S) {
+    len = a.lens[tid];
+    const long count = (long)a.q_start[tid + 1] - a.q_start[tid];
+    bad = len < 0 || count < 0 || len + count > cap;
+    n = bad ? 0 : (int)count;
+    if (n > 0) {
+      const int f = len >> pv.lg_pt;
+      if (len & ((1 << pv.lg_pt) - 1)) {
+        p = a.table[tid * a.table_stride + f];
+        if ((unsigned)p >= (unsigned)pv.pages) bad = true, n = 0, p = -1;
+      }
+      if (n > 0) first[tid] = f, last[tid] = (len + n - 1) >> pv.lg_pt;
+    }
+    if (bad && (len >= 0 || count < 0)) atomicOr(pv.err, 1);
+  }
+  page[tid] = p;
+  __syncthreads();
+  bool copy = false;
+  if (p >= 0) {
+    const int r = a.refs[p];
+    if (r > 1) {
+      int before = 0;
+      for (int c = 0; c < tid; ++c) before += page[c] == p;
+      copy = before < r - 1;
+    }
+  }
+  copies[tid] = copy;
+  __syncthreads();
+  // Entries that need a fresh page, counted, and marked in the table (nobody's counts
+  // may change before all have decided): -1, or -2 - the page that is replaced.
+  for (int b = warp; b < S; b += kGrowWarps) {
+    int sum = 0;
+    for (int i = first[b] + lane; i <= last[b]; i += 32) {
+      int32_t* e = a.table + b * a.table_stride + i;
+      const int old = *e;
+      if ((unsigned)old >= (unsigned)pv.pages) {
+        if (old >= 0) atomicOr(pv.err, 1);
+        *e = -1;
+      } else if (i == first[b] && page[b] >= 0 ? copies[b] : a.refs[old] > 1) {
+        *e = -2 - old;
+      } else {
+        continue;
+      }
+      ++sum;
+    }
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == 0) need[b] = sum;
+  }
+  __syncthreads();
+  const int mine = tid < S ? need[tid] : 0;
+  int total;
+  const int at = block_scan(mine, sums, &total);
+  from[tid] = at;
+  // ---- as many free pages as are wanted, the lowest first
+  int found = 0;
+  for (long p0 = 0; p0 < pv.pages && found < total; p0 += kScan * kGrowThreads) {
+    unsigned hit[kScan];
+#pragma unroll
+    for (int k = 0; k < kScan; ++k) {
+      const long i = p0 + k * kGrowThreads + tid;
+      hit[k] = __ballot_sync(0xffffffffu, i < pv.pages && a.refs[i] == 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kScan; ++k)
+      if (lane == 0) found_in[k * kGrowWarps + warp] = __popc(hit[k]);
+    __syncthreads();
+    int all;
+    const int run = block_scan(tid < kScan * kGrowWarps ? found_in[tid] : 0, sums, &all);
+    if (tid < kScan * kGrowWarps) found_in[tid] = run;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kScan; ++k)
+      if (hit[k] >> lane & 1) {
+        const int to = found + found_in[k * kGrowWarps + warp] + __popc(hit[k] & ((1u << lane) - 1));
+        if (to < total) g.fresh[to] = (int)(p0 + k * kGrowThreads + tid);
+      }
+    found += all;
+    __syncthreads();
+  }
+  // ---- who gets them: sequences in order, as far as the pages go
+  const bool grows = n > 0, gets = grows && at + mine <= found;
+  if (tid < S) a.lens_out[tid] = bad ? (len < 0 ? len : -1 - len) : gets ? len + n : grows ? -1 - len : len;
+  if (grows && !gets) atomicOr(pv.err, 4);
+  need[tid] = gets;
+  int number;
+  const int slot = block_scan(gets && copy, sums, &number);  // (its barriers publish the above)
+  if (tid == 0) *g.number = number;
+  if (gets && copy) g.src[slot] = p, g.dst[slot] = g.fresh[at];
+  for (int b = warp; b < S; b += kGrowWarps) {
+    int run = from[b];
+    for (int i0 = first[b]; i0 <= last[b]; i0 += 32) {
+      const int i = i0 + lane;
+      int32_t* e = a.table + b * a.table_stride + i;
+      const int was = i <= last[b] ? *e : 0;
+      const unsigned hit = __ballot_sync(0xffffffffu, was < 0);
+      if (was < 0) {
+        if (need[b]) {
+          const int f = g.fresh[run + __popc(hit & ((1u << lane) - 1))];
+          *e = f;
+          a.refs[f] = 1;
+          if (was < -1) atomicSub(a.refs + (-2 - was), 1);
+        } else if (was < -1) {
+          *e = -2 - was;
+        }
+      }
+      run += __popc(hit);
+    }
+  }
+}
+
+unsigned table_blocks(long entries) { return (unsigned)std::max(1L, std::min((entries + kForkThreads - 1) / kForkThreads, 64L)); }
+
+}  // namespace
+
+cudaError_t launch_pages_tree(const PagesView& pv, const BatchView& bv, const int32_t* parents, int words, uint64_t* seen,
+                              int32_t* positions, cudaStream_t st) {
+  PagesView p = pv;
+  BatchView b = bv;
+  void* args[] = {&p, &b, &parents, &words, &seen, &positions};
+  return launch_pdl((const void*)pages_tree_kernel, dim3(bv.batch), dim3(kTreeThreads), 0, st, args);
+}
+
+cudaError_t launch_pages_keep(const PagesView& pv, int layers, long layer_bytes, const BatchView& bv, const uint8_t* keep,
+                              int32_t* lens_out, cudaStream_t st) {
+  PagesView p = pv;
+  BatchView b = bv;
+  long units = (long)layers * pv.heads * columns(pv);
+  void* args[] = {&p, &layer_bytes, &units, &b, &keep, &lens_out};
+  return launch_pdl((const void*)pages_keep_kernel, dim3((unsigned)((units + kKeepThreads - 1) / kKeepThreads), bv.batch),
+                    dim3(kKeepThreads), 0, st, args);
+}
+
+cudaError_t launch_pages_copy(const PagesView& pv, int layers, long layer_bytes, const int32_t* src, const int32_t* dst,
+                              int count, const int32_t* number, cudaStream_t st) {
+  PagesView p = pv;
+  const long bytes = pv.heads * page_head_bytes(pv), chunks = (bytes + kCopyBytes - 1) / kCopyBytes;
+  void* args[] = {&p, &layers, &layer_bytes, &src, &dst, &count, &number};
+  const double work = (double)count * layers * chunks;
+  return launch_pdl((const void*)pages_copy_kernel, dim3((unsigned)std::min(work, 152.0 * 8)), dim3(kCopyThreads), 0, st, args);
+}
+
+cudaError_t launch_pages_fork(const PagesView& pv, const kvq_pages_fork_args& x, cudaStream_t st) {
+  PagesView p = pv;
+  kvq_pages_fork_args a = x;
+  void* args[] = {&p, &a};
+  const long out = std::max<long>(a.stride_out, (pv.pages + 3) / 4);
+  cudaError_t e = launch_pdl((const void*)pages_fork_kernel, dim3(table_blocks(out), a.rows_out + 1), dim3(kForkThreads), 0, st, args);
+  if (e != cudaSuccess) return e;
+  return launch_pdl((const void*)pages_refs_kernel, dim3(table_blocks(std::max(a.stride_in, a.stride_out)), std::max(a.rows_in, a.rows_out)),
+                    dim3(kForkThreads), 0, st, args);
+}
+
+cudaError_t launch_pages_grow(const PagesView& pv, const kvq_pages_grow_args& x, int32_t* fresh, int32_t* copies,
+                              cudaStream_t st) {
+  PagesView p = pv;
+  GrowArgs g = {x, fresh, copies, copies + 4, copies + 4 + kPagesMaxBatch};
+  void* args[] = {&p, &g};
+  return launch_pdl((const void*)pages_grow_kernel, dim3(1), dim3(kGrowThreads), 0, st, args);
+}
+
+}  // namespace kvq

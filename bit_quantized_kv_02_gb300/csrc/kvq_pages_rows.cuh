@@ -413,7 +413,9 @@ static __device__ __noinline__ bool rows_wait_slow(uint32_t bar, int phase, int*
   return cta_wait(bar, phase, dead, err);
 }
 
-template <int D, int FMT, int NM>
+// MASK: rows see what a.seen says (trees of drafted tokens) or everything (cross
+// attention) in place of what lies before them.
+template <int D, int FMT, int NM, bool MASK>
 __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pages_rows_kernel(const __grid_constant__ AttnArgs a) {
   using C = RowsCfg<D, FMT, NM>;
   using F = Fmt<FMT>;
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
   if (threadIdx.x == 0) dead = 0;
   fence_mbar_init();
   pdl_wait();
-  plan_work<BK, ROWS, true>(a, &work, reinterpret_cast<long*>(smem + C::SMEM));
+  plan_work<BK, ROWS, true, MASK>(a, &work, reinterpret_cast<long*>(smem + C::SMEM));
   pdl_trigger();
   if (cta >= work.ctas) {
     if (threadIdx.x == 0) a.split[cta].parts = 0;
@@ -447,15 +449,15 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
   bool joined = false;
   while (u < end) {
     if (warp == 0) {
-      const Piece x = work.own ? own_piece(a, &work, cta) : find_piece(a, &work, u, end);
+      const Piece x = work.own ? own_piece<MASK>(a, &work, cta) : find_piece<MASK>(a, &work, u, end);
       if (lane == 0) piece = x;
     }
     __syncthreads();
     const Piece p = piece;
     u += work.own ? 1 : p.nblk;
     // this warp's steps: STEP tokens at 4 * block + warp, while they hold a visible one
-    const int see1 = max(p.s.p0 + (p.r0 + p.rows - 1) / a.rep + 1, 0);
-    const int see0 = a.window > 0 ? max(p.s.p0 + p.r0 / a.rep - a.window + 1, 0) : 0;
+    const int see1 = MASK ? p.s.len : max(p.s.p0 + (p.r0 + p.rows - 1) / a.rep + 1, 0);
+    const int see0 = a.window > 0 ? max(p.s.p0 + (MASK ? 0 : p.r0 / a.rep) - a.window + 1, 0) : 0;
     const int tok0 = (p.blk * kRowsWarps + warp) * STEP;  // of step j: tok0 + BK * j
     int j = 0;
     const int nt = max(min((see1 - tok0 + BK - 1) / BK, p.nblk), 0);
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
     auto row_at = [&](int m, int e) { return m * 8 + 2 * t + e; };  // a lane's two rows of a tile
     float sc[NM][2];
     float o[NM][D / 16][4], mx[NM][2], sum[NM][2];
-    int pos[NM][2];
+    int pos[NM][2];  // the rows' positions; MASK: their tokens among the call's
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
 #pragma unroll
@@ -498,10 +500,12 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
         mx[m][e] = -INFINITY;
         sum[m][e] = 0.0f;
         sc[m][e] = row_scale[row_at(m, e)];
-        pos[m][e] = p.s.p0 + (p.r0 + min(row_at(m, e), p.rows - 1)) / a.rep;
+        pos[m][e] = (MASK ? p.s.s0 : p.s.p0) + (p.r0 + min(row_at(m, e), p.rows - 1)) / a.rep;
       }
     }
-    const int pos_lo = p.s.p0 + p.r0 / a.rep, pos_hi = p.s.p0 + (p.r0 + p.rows - 1) / a.rep;
+    // the rows' first and last position: steps between need no mask
+    const int pos_lo = MASK ? p.s.p0 - 1 : p.s.p0 + p.r0 / a.rep;
+    const int pos_hi = MASK ? p.s.len - 1 : p.s.p0 + (p.r0 + p.rows - 1) / a.rep;
     constexpr int SPLIT_NM = NM < kSplitRows / 8 ? NM : kSplitRows / 8;  // row tiles that are split
     const bool split = C::kSplit && (!C::kSplitSome || p.s.n * a.rep <= kSplitRows);
 
@@ -548,13 +552,19 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
 #pragma unroll
       for (int m = 0; m < NM; ++m) {
         if (edge) {
+          uint32_t vis[2] = {};
+          if constexpr (MASK) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) vis[e] = seen_bits(a, p.s, pos[m][e], tok);
+          }
 #pragma unroll
           for (int x = 0; x < RECS; ++x)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int c = tok + 16 * x + 8 * (e >> 1) + (F::kQuant ? (g >> 1) + 4 * (g & 1) : g);
-              const int at = pos[m][e & 1];
-              if (c > at || (a.window > 0 && c <= at - a.window)) acc[x][m][e] = -INFINITY;
+              const int in = 16 * x + 8 * (e >> 1) + (F::kQuant ? (g >> 1) + 4 * (g & 1) : g);  // token of the step
+              const int c = tok + in, at = pos[m][e & 1];
+              const bool hidden = MASK ? !(vis[e & 1] >> in & 1) : c > at || (a.window > 0 && c <= at - a.window);
+              if (hidden) acc[x][m][e] = -INFINITY;
             }
         }
 #pragma unroll
@@ -684,10 +694,10 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
   if (threadIdx.x == 0 && !joined) a.split[cta].parts = 0;
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool MASK>
 AttnKernel rows_kernel_fmt(int nm) {
 #define KVQ_ROWS(n) \
-  if (nm == n) return {(const void*)pages_rows_kernel<D, FMT, n>, (size_t)RowsCfg<D, FMT, n>::SMEM, kRowsWarps * 32, 0, 0};
+  if (nm == n) return {(const void*)pages_rows_kernel<D, FMT, n, MASK>, (size_t)RowsCfg<D, FMT, n>::SMEM, kRowsWarps * 32, 0, 0};
   if constexpr (D <= 128) {
     KVQ_ROWS(4)
     KVQ_ROWS(3)
@@ -697,15 +707,15 @@ AttnKernel rows_kernel_fmt(int nm) {
 #undef KVQ_ROWS
   return {};
 }
-template <int D>
+template <int D, bool MASK>
 AttnKernel rows_kernel_dim(int fmt, int nm) {
   switch (fmt) {
-    case kFmtF16: return rows_kernel_fmt<D, kFmtF16>(nm);
-    case kFmtBf16: return rows_kernel_fmt<D, kFmtBf16>(nm);
-    case kFmt88: return rows_kernel_fmt<D, kFmt88>(nm);
-    case kFmt44: return rows_kernel_fmt<D, kFmt44>(nm);
-    case kFmt84: return rows_kernel_fmt<D, kFmt84>(nm);
-    default: return rows_kernel_fmt<D, kFmt48>(nm);
+    case kFmtF16: return rows_kernel_fmt<D, kFmtF16, MASK>(nm);
+    case kFmtBf16: return rows_kernel_fmt<D, kFmtBf16, MASK>(nm);
+    case kFmt88: return rows_kernel_fmt<D, kFmt88, MASK>(nm);
+    case kFmt44: return rows_kernel_fmt<D, kFmt44, MASK>(nm);
+    case kFmt84: return rows_kernel_fmt<D, kFmt84, MASK>(nm);
+    default: return rows_kernel_fmt<D, kFmt48, MASK>(nm);
   }
 }
 

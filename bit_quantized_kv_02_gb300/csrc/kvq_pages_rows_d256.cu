@@ -2,5 +2,5 @@
 #include "kvq_pages_rows.cuh"
 
 namespace kvq {
-AttnKernel rows_kernel_d256(int fmt, int nm) { return rows_kernel_dim<256>(fmt, nm); }
+AttnKernel rows_kernel_d256(int fmt, int nm) { return rows_kernel_dim<256, false>(fmt, nm); }
 }  // namespace kvq

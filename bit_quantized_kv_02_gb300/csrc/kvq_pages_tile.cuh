@@ -106,8 +106,9 @@ struct RowMap {
 };
 
 // Blocks [lo, hi) of a piece that a row tile sees any token of.  (One tile: all
-// of them, the double-buffered scores count on it.)
-template <int D, int FMT>
+// of them, the double-buffered scores count on it.  MASK: all of them too, the rows
+// see past and new tokens alike.)
+template <int D, int FMT, bool MASK>
 __device__ __forceinline__ void tile_range(const AttnArgs& a, const Piece& p, int tile, int* lo, int* hi) {
   using C = TileCfg<D, FMT>;
   *lo = 0;
@@ -117,6 +118,7 @@ __device__ __forceinline__ void tile_range(const AttnArgs& a, const Piece& p, in
     *hi = 0;
     return;
   }
+  if (MASK) return;
   const RowMap rm(a, p);
   const int first = rm.position(tile * 128), last = rm.position(min(tile * 128 + 127, p.rows - 1));
   *hi = min(max((last < 0 ? 0 : last / C::BK + 1) - p.blk, 0), p.nblk);
@@ -353,7 +355,7 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
 // -------------------------------------------------------------- matrix unit --
 
 // The whole warp follows the barriers; one elected lane issues.
-template <int D, int FMT>
+template <int D, int FMT, bool MASK>
 __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem) {
   using C = TileCfg<D, FMT>;
   constexpr uint32_t S_DESC = mma_desc(128, C::BK, C::F::kBf16, false);
@@ -416,7 +418,7 @@ __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* 
       int lo[2], hi[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        tile_range<D, FMT>(a, sh->piece[slot], i, &lo[i], &hi[i]);
+        tile_range<D, FMT, MASK>(a, sh->piece[slot], i, &lo[i], &hi[i]);
         lo[i] = __shfl_sync(0xffffffffu, lo[i], 0);
         hi[i] = __shfl_sync(0xffffffffu, hi[i], 0);
       }
@@ -527,7 +529,7 @@ __device__ __forceinline__ float tile_query(const AttnArgs& a, const RowMap& rm,
   return sc;
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool MASK>
 __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int tile, int tid) {
   using C = TileCfg<D, FMT>;
   using F = typename C::F;
@@ -562,9 +564,10 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
     if (tile * 128 < p.rows) {
       const int pos = rm.position(min(r, p.rows - 1));
       // the tile's first and last position: blocks between need no mask
-      const int pos_lo = rm.position(tile * 128), pos_hi = rm.position(min(tile * 128 + 127, p.rows - 1));
+      const int pos_lo = MASK ? p.s.p0 - 1 : rm.position(tile * 128);
+      const int pos_hi = MASK ? p.s.len - 1 : rm.position(min(tile * 128 + 127, p.rows - 1));
       int j0, j1;
-      tile_range<D, FMT>(a, p, tile, &j0, &j1);
+      tile_range<D, FMT, MASK>(a, p, tile, &j0, &j1);
       float m = -INFINITY;
       float2 l = make_float2(0.0f, 0.0f);
       for (int j = j0; j < j1; ++j, ++bc, ++ob) {
@@ -576,9 +579,16 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
         const bool edge = tok0 + BK - 1 > pos_lo || (a.window > 0 && tok0 <= pos_hi - a.window);
         const int hi = pos - tok0, lo = a.window > 0 ? pos - a.window - tok0 : -1;  // visible columns: lo < c <= hi
         auto hide = [&](uint32_t* e, int q) {
+          if constexpr (MASK) {
+            const uint32_t v = seen_bits(a, p.s, rm.t0 + rm.token(min(r, p.rows - 1)), tok0 + q * 32);
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (q * 32 + c > hi || q * 32 + c <= lo) e[c] = 0xff800000u;
+            for (int c = 0; c < 32; ++c)
+              if (!(v >> c & 1)) e[c] = 0xff800000u;
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (q * 32 + c > hi || q * 32 + c <= lo) e[c] = 0xff800000u;
+          }
         };
         uint32_t s[64], w[64];
         float2 add;
@@ -716,7 +726,7 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
 
 // ------------------------------------------------------------------- kernel --
 
-template <int D, int FMT>
+template <int D, int FMT, bool MASK>
 __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel(const __grid_constant__ AttnArgs a) {
   using C = TileCfg<D, FMT>;
   using F = typename C::F;
@@ -752,7 +762,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
     fence_mbar_init();
   }
   pdl_wait();
-  plan_work<C::BK, C::ROWS, false>(a, &sh.work, reinterpret_cast<long*>(raw + C::SMEM + a.ring * a.pv.L.tile_bytes));  // (its barriers also publish the initialisation above)
+  plan_work<C::BK, C::ROWS, false, MASK>(a, &sh.work, reinterpret_cast<long*>(raw + C::SMEM + a.ring * a.pv.L.tile_bytes));  // (its barriers also publish the initialisation above)
   pdl_trigger();
   if (threadIdx.x == 0) a.split[blockIdx.x].parts = 0;
   if ((int)blockIdx.x >= sh.work.ctas) return;
@@ -766,7 +776,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
   // 128 * 72 + 256 * 88 = 54272.
   if (warp < 4 * C::NT) {
     if constexpr (F::kQuant) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
-    tile_softmax<D, FMT>(a, &sh, smem, warp >> 2, threadIdx.x);
+    tile_softmax<D, FMT, MASK>(a, &sh, smem, warp >> 2, threadIdx.x);
   } else if (warp < 8) {
     if constexpr (F::kQuant) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
@@ -775,7 +785,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
   } else if (warp < 12) {
     if constexpr (F::kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
     if (warp == 8) {
-      tile_mma<D, FMT>(a, &sh, smem);
+      tile_mma<D, FMT, MASK>(a, &sh, smem);
     } else if (warp == 9) {
       if constexpr (F::kQuant) raw_loader<D, FMT, 0>(a, &sh, smem, lane);
       else tile_loader<D, FMT>(a, &sh, smem, lane);
@@ -788,7 +798,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
         if (k >= C::PIECES && !tile_wait_warp(&sh, a, &sh.piece_free[slot], (k / C::PIECES - 1) & 1)) break;
         Piece p = {};
         if (u < end) {
-          p = find_piece(a, &sh.work, u, end);
+          p = find_piece<MASK>(a, &sh.work, u, end);
           // its queries to the L2 cache, while the piece before is worked on
           const RowMap rm(a, p);
           for (int r = lane; r < p.rows; r += 32) {
@@ -826,11 +836,11 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
   if (warp == 8) tmem_free(sh.tmem, 512);
 }
 
-template <int D>
+template <int D, bool MASK>
 AttnKernel tile_kernel_dim(int fmt) {
   switch (fmt) {
 #define KVQ_TILE(f) \
-  case f: return {(const void*)pages_tile_kernel<D, f>, (size_t)TileCfg<D, f>::SMEM, TileCfg<D, f>::THREADS, 0, 0};
+  case f: return {(const void*)pages_tile_kernel<D, f, MASK>, (size_t)TileCfg<D, f>::SMEM, TileCfg<D, f>::THREADS, 0, 0};
     KVQ_TILE(kFmtF16)
     KVQ_TILE(kFmtBf16)
     KVQ_TILE(kFmt88)

@@ -2,5 +2,5 @@
 #include "kvq_pages_tile.cuh"
 
 namespace kvq {
-AttnKernel tile_kernel_d128(int fmt) { return tile_kernel_dim<128>(fmt); }
+AttnKernel tile_kernel_d128(int fmt) { return tile_kernel_dim<128, false>(fmt); }
 }  // namespace kvq

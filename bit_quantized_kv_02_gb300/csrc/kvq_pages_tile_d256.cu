@@ -2,5 +2,5 @@
 #include "kvq_pages_tile.cuh"
 
 namespace kvq {
-AttnKernel tile_kernel_d256(int fmt) { return tile_kernel_dim<256>(fmt); }
+AttnKernel tile_kernel_d256(int fmt) { return tile_kernel_dim<256, false>(fmt); }
 }  // namespace kvq

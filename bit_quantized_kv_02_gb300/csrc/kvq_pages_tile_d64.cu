@@ -2,5 +2,5 @@
 #include "kvq_pages_tile.cuh"
 
 namespace kvq {
-AttnKernel tile_kernel_d64(int fmt) { return tile_kernel_dim<64>(fmt); }
+AttnKernel tile_kernel_d64(int fmt) { return tile_kernel_dim<64, false>(fmt); }
 }  // namespace kvq

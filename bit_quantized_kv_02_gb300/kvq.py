@@ -21,10 +21,11 @@ ASYM, SYM = 0, 1
 F16, F32, BF16 = 0, 1, 2
 WHOLE_VECTOR = -1
 ROPE_PAIRS, ROPE_HALVES = 0, 1
+ALL_LAYERS = -1
 
 STATUS = {0: "KVQ_OK", 1: "KVQ_ERR_INVALID_ARG", 2: "KVQ_ERR_UNSUPPORTED", 3: "KVQ_ERR_CAPACITY",
           4: "KVQ_ERR_BUFFER_TOO_SMALL", 5: "KVQ_ERR_CUDA", 6: "KVQ_ERR_DEVICE_TIMEOUT",
-          7: "KVQ_ERR_BAD_INDEX"}
+          7: "KVQ_ERR_BAD_INDEX", 8: "KVQ_ERR_OUT_OF_PAGES"}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libkvq.so")
@@ -70,6 +71,23 @@ class _Rope(ctypes.Structure):
                 ("positions", ctypes.c_void_p)]
 
 
+class _Tree(ctypes.Structure):
+    _fields_ = [("seen", ctypes.c_void_p), ("words", ctypes.c_int), ("positions", ctypes.c_void_p)]
+
+
+class _ForkArgs(ctypes.Structure):
+    _fields_ = [("rows_in", ctypes.c_int), ("rows_out", ctypes.c_int), ("parent", ctypes.c_void_p),
+                ("table_in", ctypes.c_void_p), ("stride_in", ctypes.c_int64), ("lens_in", ctypes.c_void_p),
+                ("refs_in", ctypes.c_void_p), ("table_out", ctypes.c_void_p), ("stride_out", ctypes.c_int64),
+                ("lens_out", ctypes.c_void_p), ("refs_out", ctypes.c_void_p)]
+
+
+class _GrowArgs(ctypes.Structure):
+    _fields_ = [("sequences", ctypes.c_int), ("q_start", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("refs", ctypes.c_void_p),
+                ("lens_out", ctypes.c_void_p)]
+
+
 class _NormRopeArgs(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int), ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
                 ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
@@ -89,7 +107,8 @@ EXPORTED = ["kvq_cache_bytes", "kvq_cache_create", "kvq_cache_destroy", "kvq_pre
             "kvq_decode_kernel_specialized", "kvq_dequantize", "kvq_decode_attn_materialized",
             "kvq_append_decode_attn", "kvq_decode_cta_warps", "kvq_pages_bytes", "kvq_pages_create",
             "kvq_pages_destroy", "kvq_pages_append", "kvq_pages_attn", "kvq_pages_read", "kvq_pages_set_kernel",
-            "kvq_pages_status", "kvq_pages_last_error", "kvq_qk_norm_rope"]
+            "kvq_pages_status", "kvq_pages_last_error", "kvq_qk_norm_rope", "kvq_pages_tree", "kvq_pages_tree_attn",
+            "kvq_pages_cross_attn", "kvq_pages_keep", "kvq_pages_copy", "kvq_pages_fork", "kvq_pages_grow"]
 
 
 def lib():
@@ -138,6 +157,13 @@ def lib():
         L.kvq_pages_append.argtypes = [P, I, P, P, I, ctypes.c_int64, ctypes.c_int64, PB, PR, P]
         L.kvq_pages_attn.argtypes = [P, I, P, I, ctypes.c_int64, PB, ctypes.c_float, I, P, P]
         L.kvq_pages_read.argtypes = [P, I, PB, P, P, P]
+        L.kvq_pages_tree.argtypes = [P, PB, P, I, P, P, P]
+        L.kvq_pages_tree_attn.argtypes = [P, I, P, I, ctypes.c_int64, PB, ctypes.POINTER(_Tree), ctypes.c_float, I, P, P]
+        L.kvq_pages_cross_attn.argtypes = [P, I, P, I, ctypes.c_int64, PB, ctypes.c_float, P, P]
+        L.kvq_pages_keep.argtypes = [P, I, PB, P, P, P]
+        L.kvq_pages_copy.argtypes = [P, I, P, P, I, P]
+        L.kvq_pages_fork.argtypes = [P, ctypes.POINTER(_ForkArgs), P]
+        L.kvq_pages_grow.argtypes = [P, ctypes.POINTER(_GrowArgs), P]
         L.kvq_pages_set_kernel.argtypes = [P, I]
         L.kvq_pages_status.argtypes = [P, P]
         L.kvq_pages_last_error.argtypes = [P]
@@ -460,6 +486,25 @@ class PagesBatch:
         self.ref = ctypes.byref(self.c)
 
 
+class PagesTree:
+    """A step's trees of drafted tokens (kvq_tree): seen [new_tokens][words] int64, words 1
+    to 4: bit j of word w says that the row sees new token 64 w + j of its sequence;
+    positions [new_tokens] int32, or None (they are needed with a window only).  Device
+    tensors, written by KVQPages.kvq_pages_tree or by the caller."""
+
+    def __init__(self, seen, positions=None):
+        _need(isinstance(seen, torch.Tensor) and seen.dtype == torch.int64 and seen.is_cuda and seen.dim() == 2 and
+              seen.is_contiguous(), "seen: a contiguous int64 tensor [new_tokens][words] on the GPU")
+        if positions is not None:
+            _ints(positions, "positions", seen.device)
+            _need(positions.dim() == 1 and positions.is_contiguous() and positions.shape[0] == seen.shape[0],
+                  "positions: one a row of seen, contiguous")
+        self.seen, self.positions = seen, positions
+        self.index, self.rows = seen.get_device(), seen.shape[0]
+        self.c = _Tree(seen.data_ptr(), seen.shape[1], positions.data_ptr() if positions is not None else None)
+        self.ref = ctypes.byref(self.c)
+
+
 class Rope:
     """Rotary embedding by a table of angles (kvq_rope): table [rows][dim / 2][2] fp32
     (cosine, sine); style ROPE_PAIRS (2i, 2i+1) or ROPE_HALVES (i, i + dim/2);
@@ -618,6 +663,141 @@ class KVQPages:
         [head_dim] fp16 or bf16; returns out of the same shape and type (rows behind
         the last sequence are left as they were; zeros in a new tensor).  A given out
         shares no memory with q."""
+        return self._attend(self._lib.kvq_pages_attn, "kvq_pages_attn", layer, q, batch, out, stream, (scale, window))
+
+    def kvq_pages_tree(self, parents: torch.Tensor, batch: PagesBatch, words: int = 1, tree: PagesTree | None = None,
+                       stream=None) -> PagesTree:
+        """The trees of a step's drafted tokens: parents [new_tokens] int32, each the index, among its
+        sequence's new tokens, of the one that the token hangs on, or -1 for the past.  Returns the
+        masks and positions (a given `tree` is written; new ones hold zeros in rows behind the last
+        sequence).  A sequence has at most 64 * words new tokens.  One call serves all layers."""
+        index, n = self.index, batch.new_tokens
+        _ints(parents, "parents")
+        _need(parents.dim() == 1 and parents.is_contiguous() and parents.shape[0] >= n, "parents: one a new token, contiguous")
+        _need(parents.get_device() == index, "parents: on another device")
+        _need(batch.index == index, "batch: on another device")
+        if tree is None:
+            shape = (parents.shape[0], int(words))
+            with torch.cuda.stream(stream):  # (None: the current one)
+                tree = PagesTree(torch.zeros(shape, dtype=torch.int64, device=self.device),
+                                 torch.zeros(shape[:1], dtype=torch.int32, device=self.device))
+        else:
+            _need(tree.index == index, "tree: on another device")
+            _need(tree.rows >= n, "tree: fewer rows than new tokens")
+        c = tree.c
+        r = _on_device(index, stream, self._lib.kvq_pages_tree, self.handle, batch.ref, parents.data_ptr(), c.words, c.seen,
+                       c.positions)
+        if r:
+            self._fail(r, "kvq_pages_tree")
+        return tree
+
+    def kvq_pages_tree_attn(self, layer: int, q: torch.Tensor, batch: PagesBatch, tree: PagesTree,
+                            out: torch.Tensor | None = None, scale: float = 0.0, window: int = 0, stream=None) -> torch.Tensor:
+        """kvq_pages_attn where the new tokens form a tree: a row sees the past, and of the new tokens those
+        that tree.seen names.  window: 0, or at least 64 * words."""
+        if tree.index != self.index:
+            raise ValueError("tree: on another device")
+        if tree.rows < batch.new_tokens:
+            raise ValueError("tree: fewer rows than new tokens")
+        return self._attend(self._lib.kvq_pages_tree_attn, "kvq_pages_tree_attn", layer, q, batch, out, stream,
+                            (tree.ref, scale, window))
+
+    def kvq_pages_cross_attn(self, layer: int, q: torch.Tensor, batch: PagesBatch, out: torch.Tensor | None = None,
+                             scale: float = 0.0, stream=None) -> torch.Tensor:
+        """Attention of q's rows, as in kvq_pages_attn, over all tokens that the cache holds of their sequence:
+        q_start deals out the queries, lens are those of the encoder's states, say, that were appended."""
+        return self._attend(self._lib.kvq_pages_cross_attn, "kvq_pages_cross_attn", layer, q, batch, out, stream, (scale,))
+
+    def kvq_pages_keep(self, keep: torch.Tensor, batch: PagesBatch, layer: int = ALL_LAYERS,
+                       lens_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Keep the new tokens of `batch` that keep [new_tokens] (bool or uint8) marks, closing the gaps in
+        the sequences' pages; returns the new lengths (int32 [batch])."""
+        index = self.index
+        _need(isinstance(keep, torch.Tensor) and keep.dtype in (torch.bool, torch.uint8) and keep.get_device() == index and
+              keep.dim() == 1 and keep.is_contiguous(), "keep: bool or uint8 [new_tokens], contiguous, on the cache's device")
+        _need(keep.shape[0] >= batch.new_tokens, "keep: fewer rows than new tokens")
+        _need(batch.index == index, "batch: on another device")
+        lens_out = self._ints_out(lens_out, "lens_out", batch.lens.shape, stream)
+        r = _on_device(index, stream, self._lib.kvq_pages_keep, self.handle, layer, batch.ref, keep.data_ptr(),
+                       lens_out.data_ptr())
+        if r:
+            self._fail(r, "kvq_pages_keep")
+        return lens_out
+
+    def kvq_pages_copy(self, src: torch.Tensor, dst: torch.Tensor, layer: int = ALL_LAYERS, stream=None):
+        """Copy page src[i] to page dst[i] (int32 device tensors; negative entries skip the pair)."""
+        index = self.index
+        for t, name in ((src, "src"), (dst, "dst")):
+            _ints(t, name)
+            _need(t.dim() == 1 and t.is_contiguous() and t.get_device() == index, f"{name}: contiguous, on the cache's device")
+        _need(src.shape == dst.shape, "src, dst: one page each a pair")
+        r = _on_device(index, stream, self._lib.kvq_pages_copy, self.handle, layer, src.data_ptr(), dst.data_ptr(),
+                       src.shape[0])
+        if r:
+            self._fail(r, "kvq_pages_copy")
+
+    def _ints_out(self, t, name, shape, stream):
+        """A given int32 output, checked, or a new one."""
+        if t is None:
+            return _new(shape, torch.int32, self.device, stream)
+        _ints(t, name)
+        _need(t.shape == shape and t.is_contiguous() and t.get_device() == self.index,
+              f"{name}: contiguous, of {list(shape)}, on the cache's device")
+        return t
+
+    def _ints_in(self, t, name, shape):
+        _ints(t, name)
+        _need(t.shape == shape and t.is_contiguous() and t.get_device() == self.index,
+              f"{name}: contiguous, of {list(shape)}, on the cache's device")
+        return t.data_ptr()
+
+    def kvq_pages_fork(self, parent: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
+                       table_out: torch.Tensor | None = None, lens_out: torch.Tensor | None = None,
+                       refs_out: torch.Tensor | None = None, stream=None):
+        """A new table whose row b is row parent[b] (-1: empty) of `table` [rows][pages], sharing its pages, and
+        the pages' reference counts with it: returns (table_out, lens_out, refs_out), new tensors unless given
+        (refs itself works as refs_out).  All int32 device tensors; refs [pages]."""
+        index = self.index
+        _ints(table, "table")
+        _ints(parent, "parent")
+        _need(table.dim() == 2 and table.shape[0] > 0 and table.shape[1] > 0, "table: [rows][pages]")
+        _need(parent.dim() == 1 and parent.shape[0] > 0, "parent: one a new row")
+        rows, n = table.shape[0], parent.shape[0]
+        tp, pp = self._ints_in(table, "table", table.shape), self._ints_in(parent, "parent", parent.shape)
+        lp, rp = self._ints_in(lens, "lens", (rows,)), self._ints_in(refs, "refs", (self.cfg.pages,))
+        if table_out is not None:
+            _need(table_out.dim() == 2 and table_out.shape[1] > 0, "table_out: [rows][pages]")
+        width = table.shape[1] if table_out is None else table_out.shape[1]
+        table_out = self._ints_out(table_out, "table_out", (n, width), stream)
+        lens_out = self._ints_out(lens_out, "lens_out", (n,), stream)
+        refs_out = self._ints_out(refs_out, "refs_out", (self.cfg.pages,), stream)
+        a = _ForkArgs(rows, n, pp, tp, table.shape[1], lp, rp, table_out.data_ptr(), width, lens_out.data_ptr(),
+                      refs_out.data_ptr())
+        r = _on_device(index, stream, self._lib.kvq_pages_fork, self.handle, ctypes.byref(a))
+        if r:
+            self._fail(r, "kvq_pages_fork")
+        return table_out, lens_out, refs_out
+
+    def kvq_pages_grow(self, q_start: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
+                       lens_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Pages for q_start[b + 1] - q_start[b] new tokens behind the lens[b] of each row of `table`, dealt out
+        where refs [pages] is zero, a shared last page copied; table and refs are changed in place.  Returns the
+        lengths with the new tokens (lens itself works as lens_out); where pages ran out, -1 - lens[b]."""
+        index = self.index
+        _ints(table, "table")
+        _need(table.dim() == 2 and table.shape[0] > 0 and table.shape[1] > 0, "table: [sequences][pages]")
+        n = table.shape[0]
+        tp, qp = self._ints_in(table, "table", table.shape), self._ints_in(q_start, "q_start", (n + 1,))
+        lp, rp = self._ints_in(lens, "lens", (n,)), self._ints_in(refs, "refs", (self.cfg.pages,))
+        lens_out = self._ints_out(lens_out, "lens_out", (n,), stream)
+        a = _GrowArgs(n, qp, lp, tp, table.shape[1], rp, lens_out.data_ptr())
+        r = _on_device(index, stream, self._lib.kvq_pages_grow, self.handle, ctypes.byref(a))
+        if r:
+            self._fail(r, "kvq_pages_grow")
+        return lens_out
+
+    def _attend(self, call, what, layer, q, batch, out, stream, tail):
+        """call(handle, layer, q, type, stride, batch, *tail, out, stream) with the checks that attention calls share."""
         index, dtype = self.index, q.dtype
         qs = _row_stride(q, "q", *self._q, index)
         if dtype != torch.float16 and dtype != torch.bfloat16:
@@ -634,10 +814,10 @@ class KVQPages:
                     out = torch.zeros(q.shape, dtype=dtype, device=q.device)
         elif out.shape != q.shape or out.dtype != dtype or out.get_device() != index or not out.is_contiguous():
             raise ValueError("out: contiguous, of q's shape and type")
-        r = _on_device(index, stream, self._lib.kvq_pages_attn, self.handle, layer, q.data_ptr(), _DTYPES[dtype], qs,
-                       batch.ref, scale, window, out.data_ptr())
+        r = _on_device(index, stream, call, self.handle, layer, q.data_ptr(), _DTYPES[dtype], qs, batch.ref, *tail,
+                       out.data_ptr())
         if r:
-            self._fail(r, "kvq_pages_attn")
+            self._fail(r, what)
         return out
 
     def kvq_pages_read(self, layer: int, batch: PagesBatch, k_out: torch.Tensor | None = None,

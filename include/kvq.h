@@ -61,7 +61,8 @@ typedef enum {
   KVQ_ERR_BUFFER_TOO_SMALL = 4, /* device buffer smaller than kvq_bytes.alloc */
   KVQ_ERR_CUDA = 5,           /* a CUDA runtime error (launch or asynchronous) */
   KVQ_ERR_DEVICE_TIMEOUT = 6, /* a device-side wait gave up */
-  KVQ_ERR_BAD_INDEX = 7       /* a kernel met a page, length or position out of range and skipped the access */
+  KVQ_ERR_BAD_INDEX = 7,      /* a kernel met a page, length or position out of range and skipped the access */
+  KVQ_ERR_OUT_OF_PAGES = 8    /* kvq_pages_grow found fewer free pages than its sequences need */
 } kvq_status;
 
 typedef enum { KVQ_PER_TOKEN = 0, KVQ_PER_CHANNEL = 1 } kvq_axis; /* group along channels / along tokens */
@@ -386,8 +387,9 @@ kvq_status kvq_pages_bytes(const kvq_pages_config* cfg, kvq_bytes* out);
 /* Create a paged cache inside the caller's device buffer (size >= alloc,
  * 256-byte aligned, on the current device), zero-filled on `stream`.  The
  * buffer must outlive the handle.  Later calls need the same device current
- * (KVQ_ERR_INVALID_ARG otherwise).  kvq_pages_attn calls on one handle share
- * its workspace: order them on one stream, graphs that captured them included. */
+ * (KVQ_ERR_INVALID_ARG otherwise).  Attention calls (kvq_pages_attn and its tree and
+ * cross forms) on one handle share its workspace: order them on one stream, graphs
+ * that captured them included. */
 kvq_status kvq_pages_create(const kvq_pages_config* cfg, void* device_buf, size_t buf_bytes, void* stream,
                             kvq_pages_t* out);
 kvq_status kvq_pages_destroy(kvq_pages_t pages);
@@ -426,6 +428,48 @@ kvq_status kvq_pages_append(kvq_pages_t pages, int layer, const void* k, const v
 kvq_status kvq_pages_attn(kvq_pages_t pages, int layer, const void* q, int q_dtype, int64_t q_stride,
                           const kvq_pages_batch* batch, float softmax_scale, int window, void* out, void* stream);
 
+/* Trees of drafted tokens.  A sequence's new tokens may branch: each hangs on an
+ * earlier one or on the past (the lens[b] - n tokens before them), and sees the past,
+ * its ancestors and itself.  The tokens stand in the cache one behind the other
+ * (row i at position lens[b] - n + i, as kvq_pages_append puts them); for the rotary
+ * embedding and windows a token's position is the one that it would have on its own
+ * branch. */
+typedef struct {
+  const uint64_t* seen;     /* device [new_tokens][words]: bit j of word w says that the row sees new token 64 w + j of
+                               its sequence; bits behind the sequence's last token have no effect */
+  int words;                /* 1..4: a sequence has at most 64 * words new tokens */
+  const int32_t* positions; /* device [new_tokens], lens[b] - n .. lens[b] - 1; may be NULL without a window */
+} kvq_tree;
+
+/* The tree that `parents` describes: parents[row] is the index, among its
+ * sequence's new tokens, of the token that the row hangs on (smaller than its own),
+ * or -1 for the past.  Writes seen (ancestors and the token itself) and, unless
+ * NULL, positions (lens[b] - n + the number of ancestors: the kvq_rope positions of
+ * the step).  A parent that is neither is taken as -1 and reported; the rows of a
+ * sequence whose indices are out of range, or with more than 64 * words new tokens,
+ * are left as they were and reported (KVQ_ERR_BAD_INDEX).  One call serves all
+ * layers of a step. */
+kvq_status kvq_pages_tree(kvq_pages_t pages, const kvq_pages_batch* batch, const int32_t* parents, int words,
+                          uint64_t* seen, int32_t* positions, void* stream);
+
+/* kvq_pages_attn where the new tokens form a tree: row i sees the tokens of its
+ * sequence before the new ones (with window > 0, those at t > positions[i] - window)
+ * and the new tokens that `seen` names, any mask being allowed.  Everything else as
+ * there; cached values of all new tokens must be finite.  window: 0, or at least
+ * 64 * words (KVQ_ERR_UNSUPPORTED otherwise).  The rows of a sequence with more new
+ * tokens than that come out without meaning and are reported. */
+kvq_status kvq_pages_tree_attn(kvq_pages_t pages, int layer, const void* q, int q_dtype, int64_t q_stride,
+                               const kvq_pages_batch* batch, const kvq_tree* tree, float softmax_scale, int window,
+                               void* out, void* stream);
+
+/* Cross attention: every row of sequence b sees all lens[b] tokens that the cache
+ * holds of it (an encoder's states, say; appended once, with q_start spanning them).
+ * The rows q_start[b] .. q_start[b+1] - 1 are queries only: their number has nothing
+ * to do with lens[b], which may be smaller, or zero (then they come out as zeros).
+ * Everything else as in kvq_pages_attn. */
+kvq_status kvq_pages_cross_attn(kvq_pages_t pages, int layer, const void* q, int q_dtype, int64_t q_stride,
+                                const kvq_pages_batch* batch, float softmax_scale, void* out, void* stream);
+
 /* What layer `layer` holds for the new tokens of `batch` (q_start spanning whole
  * sequences reads them whole): k_out, v_out device [new_tokens][kv_heads]
  * [head_dim] of the pages' dtype (fp16 for quantized pages), 16-byte aligned;
@@ -434,15 +478,87 @@ kvq_status kvq_pages_attn(kvq_pages_t pages, int layer, const void* q, int q_dty
 kvq_status kvq_pages_read(kvq_pages_t pages, int layer, const kvq_pages_batch* batch, void* k_out, void* v_out,
                           void* stream);
 
-/* Kernel choice of kvq_pages_attn: 0 (default) by the rows (new tokens x query
+/* `layer` of the calls below: every layer, in one launch. */
+#define KVQ_ALL_LAYERS (-1)
+
+/* Keep some of a sequence's new tokens and close the gaps: keep [new_tokens] (device
+ * bytes) is nonzero for the rows to keep; the j-th kept row of sequence b moves to
+ * position lens[b] - n + j, metadata included, keys as they were turned.  lens_out
+ * (device [batch], apart from lens; NULL: not wanted) becomes lens[b] - n + the number
+ * kept: the accepted branch of a drafted tree, or, with q_start spanning whole
+ * sequences, what is left of an evicted cache.  Positions from lens_out[b] on hold
+ * what they held, or rows that moved.  Rows with a negative position are no tokens;
+ * a row that would come from or go to a page outside the pool stays, and a sequence
+ * whose indices are out of range is left alone (lens_out[b] = lens[b]); both are
+ * reported.  Tokens only move inside their sequence's pages: a page that others
+ * share must not lie at or behind the first token that moves. */
+kvq_status kvq_pages_keep(kvq_pages_t pages, int layer, const kvq_pages_batch* batch, const uint8_t* keep,
+                          int32_t* lens_out, void* stream);
+
+/* Copy page src[i] to page dst[i], i < count (device arrays; a negative entry skips
+ * the pair, one outside the pool skips and reports it), in layer `layer` or
+ * KVQ_ALL_LAYERS.  No page may be written twice, or written and read, in one call. */
+kvq_status kvq_pages_copy(kvq_pages_t pages, int layer, const int32_t* src, const int32_t* dst, int count, void* stream);
+
+/* Sharing pages.  A pool dealt out by the next two calls has, for each page, the
+ * number of table entries that name it (refs, device [pages]; 0: the page is free),
+ * and -1 in every table entry that names none.  The caller may hold pages by counting
+ * more references of its own (a prefix kept for later).
+ *
+ * kvq_pages_fork makes row b of a new table from row parent[b] of the old one, cut
+ * behind its last token: forks share pages, a row that is no one's parent gives its
+ * pages back, parent[b] = b keeps a row (and gives back pages behind its end), -1
+ * leaves an empty one.  refs_out = refs_in - names in table_in + names in table_out.
+ * Pages are not touched.  A parent, length or entry out of range is reported; such
+ * a row comes out empty, such an entry as -1.  Everything that is written lies apart
+ * from what is read, but refs_out may be refs_in. */
+typedef struct {
+  int rows_in, rows_out;       /* 1..1024 */
+  const int32_t* parent;       /* [rows_out] row of table_in, or -1 */
+  const int32_t* table_in;     /* [rows_in][stride_in] */
+  int64_t stride_in;           /* >= 1 */
+  const int32_t* lens_in;      /* [rows_in]; a negative length x, as kvq_pages_grow leaves it, stands for -1 - x tokens */
+  const int32_t* refs_in;      /* [pages] */
+  int32_t* table_out;          /* [rows_out][stride_out] */
+  int64_t stride_out;          /* >= 1 */
+  int32_t* lens_out;           /* [rows_out] lens_in[parent[b]], 0 for an empty row */
+  int32_t* refs_out;           /* [pages] */
+} kvq_pages_fork_args;
+kvq_status kvq_pages_fork(kvq_pages_t pages, const kvq_pages_fork_args* args, void* stream);
+
+/* kvq_pages_grow gives sequence b pages for n = q_start[b+1] - q_start[b] new tokens
+ * behind its lens[b]: lens_out[b] = lens[b] + n, ready for a kvq_pages_batch with the
+ * same q_start and table.  Entries that name a page of the sequence's own are used;
+ * others get the free pages of the lowest numbers, sequence by sequence.  A last page
+ * that holds tokens and is shared is replaced by a copy (of all layers, inside the
+ * call); of the sequences that grow into the same page all but the last copy it where
+ * nobody else names it, else all do.  A page behind a sequence's tokens that is shared
+ * is replaced, not copied.  Pages that become free are dealt out by a later call.
+ * Where the free pages run out, the sequence and all growing ones behind it stay as
+ * they are, with lens_out[b] = -1 - lens[b], a length that every other call skips and
+ * this one hands on (KVQ_ERR_OUT_OF_PAGES from kvq_pages_status); the same goes for a
+ * single sequence whose indices are out of range (KVQ_ERR_BAD_INDEX).  lens_out may be
+ * lens.  Calls on one handle share its workspace: order them on one stream. */
+typedef struct {
+  int sequences;               /* 1..1024 */
+  const int32_t* q_start;      /* [sequences + 1] */
+  const int32_t* lens;         /* [sequences] */
+  int32_t* table;              /* [sequences][table_stride] */
+  int64_t table_stride;        /* >= 1 */
+  int32_t* refs;               /* [pages] */
+  int32_t* lens_out;           /* [sequences] */
+} kvq_pages_grow_args;
+kvq_status kvq_pages_grow(kvq_pages_t pages, const kvq_pages_grow_args* args, void* stream);
+
+/* Kernel choice of the attention calls: 0 (default) by the rows (new tokens x query
  * heads per KV head) of each sequence; 1 always the kernel for few rows; 2
  * always the one for many.  Same results up to rounding.  Outside 0..2:
  * KVQ_ERR_INVALID_ARG. */
 kvq_status kvq_pages_set_kernel(kvq_pages_t pages, int which);
 
 /* Synchronise `stream` and report what a kernel on this handle recorded since
- * the last call: KVQ_ERR_BAD_INDEX, KVQ_ERR_DEVICE_TIMEOUT, or a pending CUDA
- * error (KVQ_ERR_CUDA).  Clears the record. */
+ * the last call: KVQ_ERR_DEVICE_TIMEOUT, KVQ_ERR_BAD_INDEX, KVQ_ERR_OUT_OF_PAGES
+ * (the first that holds), or a pending CUDA error (KVQ_ERR_CUDA).  Clears the record. */
 kvq_status kvq_pages_status(kvq_pages_t pages, void* stream);
 
 /* Message of the last error seen by this handle ("" if none). */

@@ -136,6 +136,7 @@ struct kvq_pages {
   kvq::AttnKernel rows_fn[2][4] = {};  // few-rows kernel for 8, 16, 24 and 32 rows (8 and 16 at head_dim 256)
   kvq::AttnKernel tile_fn[2] = {};     // many-rows kernel
   int32_t* d_fresh = nullptr;  // kvq_pages_grow: [pages] free pages in the order they are dealt out
+  void* d_keep = nullptr;      // kvq_pages_keep
   int32_t* d_copies = nullptr; // pairs of pages to copy: [0] their number, from [4] on sources, then targets
   std::string last_error;
 };
@@ -174,8 +175,10 @@ cudaError_t pages_attn_setup(kvq_pages* P);
 cudaError_t launch_pages_tree(const PagesView& pv, const BatchView& bv, const int32_t* parents, int words, uint64_t* seen,
                               int32_t* positions, cudaStream_t st);
 // (layers: how many from pv's on, `layer_bytes` apart)
-cudaError_t launch_pages_keep(const PagesView& pv, int layers, long layer_bytes, const BatchView& bv, const uint8_t* keep,
-                              int32_t* lens_out, cudaStream_t st);
+cudaError_t launch_pages_keep(const PagesView& pv, int layers, long layer_bytes, const BatchView& bv, int max_new,
+                              const uint8_t* keep, int32_t* lens_out, void* work, cudaStream_t st);
+constexpr int kKeepSegs = 32768;  // segments of rows that its workspace has room for
+size_t pages_keep_bytes();        // of the workspace
 // `number`: device count of the pairs, of which there are at most `count`; null: count
 cudaError_t launch_pages_copy(const PagesView& pv, int layers, long layer_bytes, const int32_t* src, const int32_t* dst,
                               int count, const int32_t* number, cudaStream_t st);

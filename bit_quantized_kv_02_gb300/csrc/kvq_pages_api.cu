@@ -96,6 +96,8 @@ size_t carve_pages(const kvq_pages_config& c, kvq_pages* P) {
   off += round256((size_t)c.pages * 4);
   const size_t copies = off;
   off += round256((4 + 2 * kPagesMaxBatch) * 4);
+  const size_t keep = off;
+  off += round256(pages_keep_bytes());
   if (P) {
     P->L = L;
     P->layer_bytes = layer;
@@ -105,6 +107,7 @@ size_t carve_pages(const kvq_pages_config& c, kvq_pages* P) {
     P->d_part_ml = reinterpret_cast<float*>(P->base + ml);
     P->d_fresh = reinterpret_cast<int32_t*>(P->base + fresh);
     P->d_copies = reinterpret_cast<int32_t*>(P->base + copies);
+    P->d_keep = P->base + keep;
   }
   return off;
 }
@@ -268,7 +271,8 @@ kvq_status kvq_pages_bytes(const kvq_pages_config* c, kvq_bytes* out) {
   if (c->k.bits != 16) out->metadata = rows * 4.0 * (c->head_dim / c->k.group + c->head_dim / c->v.group);
   size_t o, r;
   part_sizes(*c, &o, &r);
-  out->workspace = 4.0 * (double)o + 8.0 * (double)r + 4.0 * c->pages + 4.0 * (4 + 2 * kPagesMaxBatch);
+  out->workspace = 4.0 * (double)o + 8.0 * (double)r + 4.0 * c->pages + 4.0 * (4 + 2 * kPagesMaxBatch) +
+                   (double)pages_keep_bytes();
   out->total = out->packed + out->metadata + out->workspace;
   out->elements = 2.0 * rows * c->head_dim;
   out->alloc = carve_pages(*c, nullptr);
@@ -394,7 +398,8 @@ kvq_status kvq_pages_keep(kvq_pages_t P, int layer, const kvq_pages_batch* batch
   if (lens_out && share(lens_out, bv.batch, bv.lens, bv.batch))
     return fail(P, KVQ_ERR_INVALID_ARG, "new lengths over the old ones");
   if (bv.new_tokens == 0 && !lens_out) return KVQ_OK;
-  return cuda_result(P, launch_pages_keep(pv, layers, (long)P->layer_bytes, bv, keep, lens_out,
+  const int max_new = batch->max_new > 0 && batch->max_new < bv.new_tokens ? batch->max_new : bv.new_tokens;
+  return cuda_result(P, launch_pages_keep(pv, layers, (long)P->layer_bytes, bv, max_new, keep, lens_out, P->d_keep,
                                           static_cast<cudaStream_t>(stream)));
 }
 

@@ -10,6 +10,29 @@ namespace kvq {
 
 namespace {
 
+// The whole CTA of 1024 threads: exclusive prefix sums of one value a thread; *total: of all.
+__device__ __forceinline__ int block_scan(int x, int* sums, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int y = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
+  }
+  if (lane == 31) sums[warp] = y;
+  __syncthreads();
+  int v = sums[lane], s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += z;
+  }
+  const int base = __shfl_sync(0xffffffffu, s - v, warp);
+  *total = __shfl_sync(0xffffffffu, s, 31);
+  __syncthreads();
+  return base + y - x;
+}
+
 // -------------------------------------------------------------------- tree --
 
 constexpr int kTreeThreads = 64 * kTreeWords;  // a thread per drafted token
@@ -99,16 +122,51 @@ __device__ __forceinline__ long place_of(const PagesView& pv, int page, int slot
   return (long)(record_of(pv, page, 0, slot) - pv.base) | (slot & 15);
 }
 
-// The CTAs of column blockIdx.y go through one sequence's marks; each thread moves
-// one column (16 bytes of a row) of one (layer, head) for all kept tokens.  No other
-// thread touches those bytes, and tokens only move down, to places in their order:
-// a thread that reads some tokens, then writes them, then goes on to the next never
-// overwrites what it has yet to read.
+// One column of all layers' heads, by its number: where its bytes lie for a token's place.
+struct ColumnOf {
+  Column col;
+  char* base;
+  __device__ __forceinline__ ColumnOf(const PagesView& pv, long layer_bytes, long unit) {
+    const int ncol = columns(pv);
+    const long lh = unit / ncol;  // layer * heads + head
+    col = column_of(pv, (int)(unit - lh * ncol));
+    base = pv.base + (lh / pv.heads) * layer_bytes + (lh % pv.heads) * page_head_bytes(pv) + col.at;
+  }
+  __device__ __forceinline__ char* at(long place) const {
+    const int t = (int)(place & 15);
+    return base + (place & ~15L) + t * col.stride + (col.swizzle < 0 ? 0 : (col.swizzle ^ (t & 7)) << 4);
+  }
+  __device__ __forceinline__ void load(long place, uint4* x) const {
+    if (col.wide) *x = *reinterpret_cast<const uint4*>(at(place));
+    else x->x = *reinterpret_cast<const uint32_t*>(at(place));
+  }
+  __device__ __forceinline__ void store(long place, const uint4& x) const {
+    if (col.wide) *reinterpret_cast<uint4*>(at(place)) = x;
+    else *reinterpret_cast<uint32_t*>(at(place)) = x.x;
+  }
+};
+
+// Places that token `from` of a sequence leaves and takes (`to`); {-1, -1}: it stays.
+__device__ __forceinline__ long2 move_of(const PagesView& pv, const BatchView& bv, int b, int from, int to, bool report) {
+  if (from == to) return make_long2(-1, -1);
+  const int in = (1 << pv.lg_pt) - 1;
+  const int pf = bv.table[b * bv.stride + (from >> pv.lg_pt)], pt = bv.table[b * bv.stride + (to >> pv.lg_pt)];
+  if ((unsigned)pf >= (unsigned)pv.pages || (unsigned)pt >= (unsigned)pv.pages) {
+    if (report) atomicOr(pv.err, 1);
+    return make_long2(-1, -1);
+  }
+  return make_long2(place_of(pv, pf, from & in), place_of(pv, pt, to & in));
+}
+
+// Short sequences: the CTAs of row blockIdx.y go through one sequence's marks; each
+// thread moves one column of one (layer, head) for all kept tokens.  No other thread
+// touches those bytes, and tokens only move down, to places in their order: a thread
+// that reads some tokens, then writes them, then goes on to the next never overwrites
+// what it has yet to read.
 __global__ void __launch_bounds__(kKeepThreads) pages_keep_kernel(PagesView pv, long layer_bytes, long units, BatchView bv,
                                                                  const uint8_t* keep, int32_t* lens_out) {
   __shared__ long2 move[kKeepThreads];
   __shared__ int sums[kKeepThreads / 32];
-  __shared__ int kept_here;
   const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_trigger();
@@ -122,19 +180,12 @@ __global__ void __launch_bounds__(kKeepThreads) pages_keep_kernel(PagesView pv, 
     return;
   }
   const long unit = (long)blockIdx.x * kKeepThreads + tid;
-  const int ncol = columns(pv);
   const bool mine = unit < units;
-  const long lh = mine ? unit / ncol : 0;  // layer * heads + head
-  const Column col = column_of(pv, mine ? (int)(unit - lh * ncol) : 0);
-  char* base = pv.base + (lh / pv.heads) * layer_bytes + (lh % pv.heads) * page_head_bytes(pv) + col.at;
-  auto at = [&](long place) {
-    const int t = (int)(place & 15);
-    return base + (place & ~15L) + t * col.stride + (col.swizzle < 0 ? 0 : (col.swizzle ^ (t & 7)) << 4);
-  };
+  const ColumnOf col(pv, layer_bytes, mine ? unit : 0);
   const int skip = max(-s.p0, 0);  // rows that stand before the sequence
   int first = s.p0 + skip;         // where the next kept token goes
   for (int i0 = skip; i0 < s.n; i0 += kKeepThreads) {
-    // the marks of 256 rows; places of the kept ones that move
+    // the marks of 256 rows; places of the kept ones
     const int i = i0 + tid;
     const bool on = i < s.n && keep[(long)s.s0 + i] != 0;
     const unsigned ballot = __ballot_sync(0xffffffffu, on);
@@ -146,19 +197,7 @@ __global__ void __launch_bounds__(kKeepThreads) pages_keep_kernel(PagesView pv, 
       if (w < warp) before += sums[w];
       all += sums[w];
     }
-    if (on) {
-      const int from = s.p0 + i, to = first + before;
-      long2 m = make_long2(-1, -1);
-      if (from != to) {
-        const int pf = bv.table[b * bv.stride + (from >> pv.lg_pt)], pt = bv.table[b * bv.stride + (to >> pv.lg_pt)];
-        if ((unsigned)pf < (unsigned)pv.pages && (unsigned)pt < (unsigned)pv.pages) {
-          m = make_long2(place_of(pv, pf, from & ((1 << pv.lg_pt) - 1)), place_of(pv, pt, to & ((1 << pv.lg_pt) - 1)));
-        } else if (blockIdx.x == 0) {
-          atomicOr(pv.err, 1);
-        }
-      }
-      move[before] = m;
-    }
+    if (on) move[before] = move_of(pv, bv, b, s.p0 + i, first + before, blockIdx.x == 0);
     first += all;
     __syncthreads();
     if (mine) {
@@ -167,21 +206,195 @@ __global__ void __launch_bounds__(kKeepThreads) pages_keep_kernel(PagesView pv, 
         uint4 x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (j + u < all && move[j + u].x >= 0) {
-            if (col.wide) x[u] = *reinterpret_cast<const uint4*>(at(move[j + u].x));
-            else x[u].x = *reinterpret_cast<const uint32_t*>(at(move[j + u].x));
-          }
+          if (j + u < all && move[j + u].x >= 0) col.load(move[j + u].x, &x[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (j + u < all && move[j + u].x >= 0) {
-            if (col.wide) *reinterpret_cast<uint4*>(at(move[j + u].y)) = x[u];
-            else *reinterpret_cast<uint32_t*>(at(move[j + u].y)) = x[u].x;
-          }
+          if (j + u < all && move[j + u].x >= 0) col.store(move[j + u].y, x[u]);
       }
     }
     __syncthreads();
   }
   if (lens_out && blockIdx.x == 0 && tid == 0) lens_out[b] = first;
+}
+
+// Long sequences: their rows in segments of 128, which many CTAs move at once.  A first
+// kernel counts the kept rows before each segment.  Then a CTA takes a segment and 32
+// columns, reads all of its kept tokens, says so, waits until the segments that its
+// tokens go to have been read (they are never later ones, two at most), and writes.
+// CTAs draw tickets in the order of the segments, so that of the steps that are not
+// done the first waits for nobody: whoever holds it has nothing older to do, and what it
+// writes to has been read.
+constexpr int kSegRows = 128;
+constexpr int kPlanThreads = 1024;
+
+struct KeepPlan {
+  unsigned long long ticket;
+  int segments;
+};
+// a segment: its sequence, its number there, kept rows before it, CTAs that have read it
+struct KeepSeg {
+  int b, at, before, done;
+};
+
+__device__ __forceinline__ int segments_of(const Seq& s) { return (s.n - max(-s.p0, 0) + kSegRows - 1) / kSegRows; }
+
+__global__ void __launch_bounds__(kPlanThreads) pages_keep_plan_kernel(PagesView pv, BatchView bv, const uint8_t* keep,
+                                                                      int32_t* lens_out, KeepPlan* plan, KeepSeg* seg) {
+  __shared__ int sums[32];
+  const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  pdl_trigger();
+  bool bad;
+  const Seq s = load_seq(pv, bv, b, &bad);
+  // segments of the sequences before this one
+  int ahead = 0;
+  if (tid < b) {
+    bool skip;
+    const Seq x = load_seq(pv, bv, tid, &skip);
+    if (!skip) ahead = max(segments_of(x), 0);
+  }
+  int base;
+  block_scan(ahead, sums, &base);
+  const int rows = s.n - max(-s.p0, 0);
+  const int segs = bad ? 0 : max(segments_of(s), 0);
+  // Rows that several sequences name could make more segments than there is room for:
+  // the line ends before the first sequence that does not fit.
+  const bool full = base + segs > kKeepSegs;
+  if (tid == 0) {
+    if (b == 0) plan->ticket = 0;
+    if (full ? base <= kKeepSegs : b == (int)gridDim.x - 1) plan->segments = full ? base : base + segs;
+    if (bad || full) {
+      atomicOr(pv.err, 1);
+      if (lens_out) lens_out[b] = bv.lens[b];
+    }
+  }
+  bad = bad || full;
+  if (bad) return;
+  const uint8_t* marks = keep + (long)s.s0 + (s.n - rows);
+  constexpr int U = 4;  // segments in flight, a warp each
+  for (int j0 = warp; j0 < segs; j0 += 32 * U) {
+    unsigned hit[U][kSegRows / 32];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int q = 0; q < kSegRows / 32; ++q) {
+        const long i = (long)(j0 + 32 * u) * kSegRows + q * 32 + lane;
+        hit[u][q] = __ballot_sync(0xffffffffu, i < rows && marks[i] != 0);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (lane == 0 && j0 + 32 * u < segs) {
+        int n = 0;
+#pragma unroll
+        for (int q = 0; q < kSegRows / 32; ++q) n += __popc(hit[u][q]);
+        seg[base + j0 + 32 * u] = {b, j0 + 32 * u, n, 0};
+      }
+  }
+  __syncthreads();
+  int run = 0;
+  for (int j0 = 0; j0 < segs; j0 += kPlanThreads) {
+    int all;
+    const int j = j0 + tid, n = j < segs ? seg[base + j].before : 0;
+    const int before = block_scan(n, sums, &all);
+    if (j < segs) seg[base + j].before = run + before;
+    run += all;
+  }
+  if (lens_out && tid == 0) lens_out[b] = max(s.p0, 0) + run;
+}
+
+__global__ void __launch_bounds__(kKeepThreads, 2) pages_keep_move_kernel(PagesView pv, long layer_bytes, long units,
+                                                                         BatchView bv, const uint8_t* keep, KeepPlan* plan,
+                                                                         KeepSeg* seg) {
+  constexpr int U = kSegRows / (kKeepThreads / 32);  // tokens of a warp
+  __shared__ long2 move[2][kSegRows];
+  __shared__ int sums[kSegRows / 32], ready;
+  __shared__ uint32_t arrived[kKeepThreads];
+  __shared__ long drawn;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  pdl_trigger();
+  const long blocks = (units + 31) / 32, total = plan->segments * blocks;
+  // the next ticket's segment, and the places of its kept tokens in `to`
+  struct Step {
+    KeepSeg g;
+    int id, all;
+    long unit;
+  };
+  auto draw = [&](long2* to) {
+    if (tid == 0) drawn = (long)atomicAdd(&plan->ticket, 1ull);
+    __syncthreads();
+    const long ticket = drawn;
+    Step st = {};
+    st.id = -1;
+    if (ticket >= total) return st;  // (all threads)
+    st.id = (int)(ticket / blocks);
+    st.unit = (ticket - st.id * blocks) * 32 + lane;
+    st.g = seg[st.id];
+    bool bad;
+    const Seq s = load_seq(pv, bv, st.g.b, &bad);
+    const int skip = max(-s.p0, 0), first = s.p0 + skip, i = skip + st.g.at * kSegRows + tid;
+    const bool on = tid < kSegRows && i < s.n && keep[(long)s.s0 + i] != 0;
+    const unsigned ballot = __ballot_sync(0xffffffffu, on);
+    if (lane == 0 && warp < kSegRows / 32) sums[warp] = __popc(ballot);
+    __syncthreads();
+    int before = __popc(ballot & ((1u << lane) - 1));
+#pragma unroll
+    for (int w = 0; w < kSegRows / 32; ++w) {
+      if (w < warp) before += sums[w];
+      st.all += sums[w];
+    }
+    if (on) to[before] = move_of(pv, bv, st.g.b, s.p0 + i, first + st.g.before + before, st.unit == lane);
+    return st;
+  };
+  Step now = draw(move[0]);
+  for (int buf = 0; now.id >= 0; buf ^= 1) {
+    __syncthreads();
+    const bool mine = now.unit < units;
+    const ColumnOf col(pv, layer_bytes, mine ? now.unit : 0);
+    uint4 x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = u * (kKeepThreads / 32) + warp;
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (mine && j < now.all && move[buf][j].x >= 0) col.load(move[buf][j].x, &x[u]);
+    }
+    // while they come: what the next step moves
+    const Step next = draw(move[buf ^ 1]);
+    // every load has come back when its values can be stored
+    uint32_t any = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) any |= x[u].x | x[u].y | x[u].z | x[u].w;
+    *(volatile uint32_t*)&arrived[tid] = any;
+    if (tid == 0) ready = 1;
+    __syncthreads();
+    if (tid == 0) {
+      const KeepSeg& g = now.g;
+      __threadfence();
+      atomicAdd(&seg[now.id].done, 1);
+      // the rows that are written: [before, before + all) of the sequence's
+      for (int k = g.before / kSegRows; now.all > 0 && k < g.at && k <= (g.before + now.all - 1) / kSegRows; ++k) {
+        const volatile int* done = &seg[now.id - g.at + k].done;
+        const unsigned long long t0 = time_ns();
+        while (*done < blocks) {
+          if (time_ns() - t0 > kWaitNs) {
+            atomicOr(pv.err, 2);
+            ready = 0;
+            break;
+          }
+        }
+      }
+      __threadfence();
+    }
+    __syncthreads();
+    if (ready) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = u * (kKeepThreads / 32) + warp;
+        if (mine && j < now.all && move[buf][j].x >= 0) col.store(move[buf][j].y, x[u]);
+      }
+    }
+    now = next;
+  }
 }
 
 // -------------------------------------------------------------------- copy --
@@ -225,16 +438,21 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(PagesView pv, 
 // -------------------------------------------------------------------- fork --
 
 constexpr int kForkThreads = 256;
+constexpr int kForkEntries = 4;  // of a thread
 
-// Row b of the new table from row parent[b] of the old one.
-__global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(PagesView pv, kvq_pages_fork_args a) {
+// Row b of the new table from row parent[b] of the old one, kForkEntries entries a
+// thread; the CTAs behind the table's copy reference counts.
+__global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(PagesView pv, kvq_pages_fork_args a, int row_blocks) {
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.y;
-  const long i0 = (long)blockIdx.x * kForkThreads + threadIdx.x, step = (long)gridDim.x * kForkThreads;
-  if (b == a.rows_out) {  // the last rows of CTAs: reference counts
-    if (a.refs_out != a.refs_in)
-      for (long i = i0; i < pv.pages; i += step) a.refs_out[i] = a.refs_in[i];
+  const int b = blockIdx.x / row_blocks;
+  if (b >= a.rows_out) {
+    const long i0 = (long)(blockIdx.x - a.rows_out * row_blocks) * (kForkThreads * kForkEntries) + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < kForkEntries; ++k) {
+      const long i = i0 + k * kForkThreads;
+      if (i < pv.pages) a.refs_out[i] = a.refs_in[i];
+    }
     return;
   }
   const int p = a.parent[b];
@@ -248,16 +466,19 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(PagesView pv, 
     bad = held > a.stride_in || held > a.stride_out;
   }
   if (bad) len = 0, held = 0;
-  for (long i = i0; i < a.stride_out; i += step) {
-    int page = -1;
-    if (i < held) {
-      page = a.table_in[p * a.stride_in + i];
-      if ((unsigned)page >= (unsigned)pv.pages) bad = true, page = -1;
-    }
-    a.table_out[b * a.stride_out + i] = page;
+  const long i0 = (long)(blockIdx.x - b * row_blocks) * (kForkThreads * kForkEntries) + threadIdx.x;
+  int page[kForkEntries];
+#pragma unroll
+  for (int k = 0; k < kForkEntries; ++k) {
+    const long i = i0 + k * kForkThreads;
+    page[k] = i < held ? a.table_in[p * a.stride_in + i] : -1;
+    if (i < held && (unsigned)page[k] >= (unsigned)pv.pages) bad = true, page[k] = -1;
   }
+#pragma unroll
+  for (int k = 0; k < kForkEntries; ++k)
+    if (i0 + k * kForkThreads < a.stride_out) a.table_out[b * a.stride_out + i0 + k * kForkThreads] = page[k];
   if (bad) atomicOr(pv.err, 1);
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.lens_out[b] = len;
+  if (i0 == 0) a.lens_out[b] = len;
 }
 
 // References: one less for a name that left, one more for one that came.
@@ -265,14 +486,22 @@ __global__ void __launch_bounds__(kForkThreads) pages_refs_kernel(PagesView pv, 
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.y;
-  const long most = max(a.stride_in, a.stride_out);
-  for (long i = (long)blockIdx.x * kForkThreads + threadIdx.x; i < most; i += (long)gridDim.x * kForkThreads) {
-    const int was = b < a.rows_in && i < a.stride_in ? a.table_in[b * a.stride_in + i] : -1;
-    const int is = b < a.rows_out && i < a.stride_out ? a.table_out[b * a.stride_out + i] : -1;
-    if (was == is) continue;
-    if (was >= pv.pages) atomicOr(pv.err, 1);
-    else if (was >= 0) atomicSub(a.refs_out + was, 1);
-    if (is >= 0) atomicAdd(a.refs_out + is, 1);
+  const long most = max(a.stride_in, a.stride_out), step = (long)gridDim.x * (kForkThreads * kForkEntries);
+  for (long i0 = (long)blockIdx.x * (kForkThreads * kForkEntries) + threadIdx.x; i0 < most; i0 += step) {
+    int was[kForkEntries], is[kForkEntries];
+#pragma unroll
+    for (int k = 0; k < kForkEntries; ++k) {
+      const long i = i0 + k * kForkThreads;
+      was[k] = b < a.rows_in && i < a.stride_in ? a.table_in[b * a.stride_in + i] : -1;
+      is[k] = b < a.rows_out && i < a.stride_out ? a.table_out[b * a.stride_out + i] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kForkEntries; ++k) {
+      if (was[k] == is[k]) continue;
+      if (was[k] >= pv.pages) atomicOr(pv.err, 1);
+      else if (was[k] >= 0) atomicSub(a.refs_out + was[k], 1);
+      if (is[k] >= 0) atomicAdd(a.refs_out + is[k], 1);
+    }
   }
 }
 
@@ -281,6 +510,7 @@ __global__ void __launch_bounds__(kForkThreads) pages_refs_kernel(PagesView pv, 
 constexpr int kGrowThreads = kPagesMaxBatch;  // a thread per sequence
 constexpr int kGrowWarps = kGrowThreads / 32;
 constexpr int kScan = 16;                     // reference counts that a thread has in flight
+constexpr int kEntries = 4;                   // table entries that it has
 
 struct GrowArgs {
   kvq_pages_grow_args a;
@@ -288,35 +518,16 @@ struct GrowArgs {
   int32_t *number, *src, *dst;
 };
 
-// The whole CTA: exclusive prefix sums of one value a thread; *total: of all.
-__device__ __forceinline__ int block_scan(int x, int* sums, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int y = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int z = __shfl_up_sync(0xffffffffu, y, o);
-    if (lane >= o) y += z;
-  }
-  if (lane == 31) sums[warp] = y;
-  __syncthreads();
-  int v = sums[lane], s = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int z = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += z;
-  }
-  const int base = __shfl_sync(0xffffffffu, s - v, warp);
-  *total = __shfl_sync(0xffffffffu, s, 31);
-  __syncthreads();
-  return base + y - x;
-}
-
-// One CTA deals out the pages: what a sequence gets depends on all before it.
+// One CTA deals out the pages: what a sequence gets depends on all before it.  The
+// entries that the new tokens need, of all sequences one behind the other, are gone
+// through twice, kEntries a thread at a time, so that a pass costs a few loads in a
+// row whatever the sequences are.
 __global__ void __launch_bounds__(kGrowThreads) pages_grow_kernel(PagesView pv, GrowArgs g) {
-  __shared__ int page[kGrowThreads];     // the page that holds the sequence's last tokens and is grown into, or -1
-  __shared__ int first[kGrowThreads], last[kGrowThreads];  // entries of the table that the new tokens need
-  __shared__ int need[kGrowThreads], from[kGrowThreads];   // fresh pages (then: does it get them?), and the first one's number
-  __shared__ bool copies[kGrowThreads];
+  __shared__ int page[kGrowThreads];   // the page that holds the sequence's last tokens and is grown into, or -1
+  __shared__ int first[kGrowThreads];  // first entry of the table that its new tokens need
+  __shared__ int line[kGrowThreads + 1];  // entries that the sequences before it need
+  __shared__ int from[kGrowThreads];   // fresh pages that they need (of sequences that need entries)
+  __shared__ bool copies[kGrowThreads], gets[kGrowThreads];
   __shared__ int sums[32], found_in[kScan * kGrowWarps];
   const kvq_pages_grow_args& a = g.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, S = a.sequences;
@@ -324,9 +535,8 @@ __global__ void __launch_bounds__(kGrowThreads) pages_grow_kernel(PagesView pv, 
   pdl_trigger();
   // ---- each sequence's part of the table
   const long cap = min(a.table_stride << pv.lg_pt, 1L << 30);
-  int len = 0, n = 0, p = -1;
+  int len = 0, n = 0, p = -1, entries = 0;
   bool bad = false;
-  first[tid] = 0, last[tid] = -1;
   if (tid < S) {
     len = a.lens[tid];
     const long count = (long)a.q_start[tid + 1] - a.q_start[tid];
@@ -338,48 +548,82 @@ __global__ void __launch_bounds__(kGrowThreads) pages_grow_kernel(PagesView pv, 
         p = a.table[tid * a.table_stride + f];
         if ((unsigned)p >= (unsigned)pv.pages) bad = true, n = 0, p = -1;
       }
-      if (n > 0) first[tid] = f, last[tid] = (len + n - 1) >> pv.lg_pt;
+      first[tid] = f;
+      if (n > 0) entries = ((len + n - 1) >> pv.lg_pt) - f + 1;
     }
     if (bad && (len >= 0 || count < 0)) atomicOr(pv.err, 1);
   }
   page[tid] = p;
-  __syncthreads();
+  int all;
+  const int mine = block_scan(entries, sums, &all);
+  line[tid] = mine;
+  if (tid == 0) line[kGrowThreads] = all;
   bool copy = false;
   if (p >= 0) {
     const int r = a.refs[p];
     if (r > 1) {
       int before = 0;
+#pragma unroll 8
       for (int c = 0; c < tid; ++c) before += page[c] == p;
       copy = before < r - 1;
     }
   }
   copies[tid] = copy;
   __syncthreads();
-  // Entries that need a fresh page, counted, and marked in the table (nobody's counts
-  // may change before all have decided): -1, or -2 - the page that is replaced.
-  for (int b = warp; b < S; b += kGrowWarps) {
-    int sum = 0;
-    for (int i = first[b] + lane; i <= last[b]; i += 32) {
-      int32_t* e = a.table + b * a.table_stride + i;
-      const int old = *e;
-      if ((unsigned)old >= (unsigned)pv.pages) {
-        if (old >= 0) atomicOr(pv.err, 1);
-        *e = -1;
-      } else if (i == first[b] && page[b] >= 0 ? copies[b] : a.refs[old] > 1) {
-        *e = -2 - old;
-      } else {
-        continue;
-      }
-      ++sum;
+  // the sequence whose entries entry x of the line is among
+  auto owner = [&](int x) {
+    int lo = 0, hi = kGrowThreads;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (line[mid] <= x) lo = mid;
+      else hi = mid;
     }
-    sum = __reduce_add_sync(0xffffffffu, sum);
-    if (lane == 0) need[b] = sum;
+    return lo;
+  };
+  // ---- entries that need a fresh page, counted, and marked in the table (nobody's counts
+  // may change before all have decided): -1, or -2 - the page that is replaced
+  int total = 0;
+  for (int x0 = 0; x0 < all; x0 += kGrowThreads * kEntries) {
+    const int x1 = x0 + tid * kEntries;
+    int32_t* e[kEntries];
+    int was[kEntries], b[kEntries];
+    bool at_first[kEntries];
+#pragma unroll
+    for (int k = 0; k < kEntries; ++k) {
+      b[k] = -1;
+      was[k] = 0;
+      if (x1 + k < all) {
+        b[k] = k && x1 + k < line[b[k - 1] + 1] ? b[k - 1] : owner(x1 + k);
+        const int i = x1 + k - line[b[k]];
+        at_first[k] = i == 0 && page[b[k]] >= 0;
+        e[k] = a.table + b[k] * a.table_stride + first[b[k]] + i;
+        was[k] = *e[k];
+      }
+    }
+    int want[kEntries], sum = 0;
+#pragma unroll
+    for (int k = 0; k < kEntries; ++k) {
+      want[k] = 0;
+      if (x1 + k >= all) continue;
+      if ((unsigned)was[k] >= (unsigned)pv.pages) {
+        if (was[k] >= 0) atomicOr(pv.err, 1);
+        *e[k] = -1;
+        want[k] = 1;
+      } else if (at_first[k] ? copies[b[k]] : a.refs[was[k]] > 1) {
+        *e[k] = -2 - was[k];
+        want[k] = 1;
+      }
+      sum += want[k];
+    }
+    int in, run = total + block_scan(sum, sums, &in);
+#pragma unroll
+    for (int k = 0; k < kEntries; ++k) {
+      if (x1 + k < all && x1 + k == line[b[k]]) from[b[k]] = run;
+      run += want[k];
+    }
+    total += in;
   }
   __syncthreads();
-  const int mine = tid < S ? need[tid] : 0;
-  int total;
-  const int at = block_scan(mine, sums, &total);
-  from[tid] = at;
   // ---- as many free pages as are wanted, the lowest first
   int found = 0;
   for (long p0 = 0; p0 < pv.pages && found < total; p0 += kScan * kGrowThreads) {
@@ -393,8 +637,8 @@ __global__ void __launch_bounds__(kGrowThreads) pages_grow_kernel(PagesView pv, 
     for (int k = 0; k < kScan; ++k)
       if (lane == 0) found_in[k * kGrowWarps + warp] = __popc(hit[k]);
     __syncthreads();
-    int all;
-    const int run = block_scan(tid < kScan * kGrowWarps ? found_in[tid] : 0, sums, &all);
+    int in;
+    const int run = block_scan(tid < kScan * kGrowWarps ? found_in[tid] : 0, sums, &in);
     if (tid < kScan * kGrowWarps) found_in[tid] = run;
     __syncthreads();
 #pragma unroll
@@ -403,41 +647,58 @@ __global__ void __launch_bounds__(kGrowThreads) pages_grow_kernel(PagesView pv, 
         const int to = found + found_in[k * kGrowWarps + warp] + __popc(hit[k] & ((1u << lane) - 1));
         if (to < total) g.fresh[to] = (int)(p0 + k * kGrowThreads + tid);
       }
-    found += all;
+    found += in;
     __syncthreads();
   }
-  // ---- who gets them: sequences in order, as far as the pages go
-  const bool grows = n > 0, gets = grows && at + mine <= found;
-  if (tid < S) a.lens_out[tid] = bad ? (len < 0 ? len : -1 - len) : gets ? len + n : grows ? -1 - len : len;
-  if (grows && !gets) atomicOr(pv.err, 4);
-  need[tid] = gets;
+  // ---- who gets them: sequences in order, as far as the pages go.  What those up to
+  // this one need is what stands before the next one with entries.
+  const bool grows = n > 0;
+  int end = total;
+  if (grows && mine + entries < all) end = from[owner(mine + entries)];
+  const bool get = grows && end <= found;
+  gets[tid] = get;
+  if (tid < S) a.lens_out[tid] = bad ? (len < 0 ? len : -1 - len) : get ? len + n : grows ? -1 - len : len;
+  if (grows && !get) atomicOr(pv.err, 4);
   int number;
-  const int slot = block_scan(gets && copy, sums, &number);  // (its barriers publish the above)
+  const int slot = block_scan(get && copy, sums, &number);  // (its barriers publish the above)
   if (tid == 0) *g.number = number;
-  if (gets && copy) g.src[slot] = p, g.dst[slot] = g.fresh[at];
-  for (int b = warp; b < S; b += kGrowWarps) {
-    int run = from[b];
-    for (int i0 = first[b]; i0 <= last[b]; i0 += 32) {
-      const int i = i0 + lane;
-      int32_t* e = a.table + b * a.table_stride + i;
-      const int was = i <= last[b] ? *e : 0;
-      const unsigned hit = __ballot_sync(0xffffffffu, was < 0);
-      if (was < 0) {
-        if (need[b]) {
-          const int f = g.fresh[run + __popc(hit & ((1u << lane) - 1))];
-          *e = f;
-          a.refs[f] = 1;
-          if (was < -1) atomicSub(a.refs + (-2 - was), 1);
-        } else if (was < -1) {
-          *e = -2 - was;
-        }
+  if (get && copy) g.src[slot] = p, g.dst[slot] = g.fresh[from[tid]];
+  int run = 0;
+  for (int x0 = 0; x0 < all; x0 += kGrowThreads * kEntries) {
+    const int x1 = x0 + tid * kEntries;
+    int32_t* e[kEntries];
+    int was[kEntries], b = -1, sum = 0;
+    bool fill[kEntries];
+#pragma unroll
+    for (int k = 0; k < kEntries; ++k) {
+      was[k] = 0;
+      if (x1 + k < all) {
+        b = k && x1 + k < line[b + 1] ? b : owner(x1 + k);
+        e[k] = a.table + b * a.table_stride + first[b] + (x1 + k - line[b]);
+        fill[k] = gets[b];
+        was[k] = *e[k];
       }
-      run += __popc(hit);
+      sum += was[k] < 0;
     }
+    int in, at = run + block_scan(sum, sums, &in);
+#pragma unroll
+    for (int k = 0; k < kEntries; ++k) {
+      if (was[k] >= 0) continue;
+      if (fill[k]) {
+        const int f = g.fresh[at];
+        *e[k] = f;
+        a.refs[f] = 1;
+        if (was[k] < -1) atomicSub(a.refs + (-2 - was[k]), 1);
+      } else if (was[k] < -1) {
+        *e[k] = -2 - was[k];
+      }
+      ++at;
+    }
+    run += in;
   }
 }
 
-unsigned table_blocks(long entries) { return (unsigned)std::max(1L, std::min((entries + kForkThreads - 1) / kForkThreads, 64L)); }
+int fork_blocks(long entries) { return (int)((entries + kForkThreads * kForkEntries - 1) / (kForkThreads * kForkEntries)); }
 
 }  // namespace
 
@@ -449,15 +710,28 @@ cudaError_t launch_pages_tree(const PagesView& pv, const BatchView& bv, const in
   return launch_pdl((const void*)pages_tree_kernel, dim3(bv.batch), dim3(kTreeThreads), 0, st, args);
 }
 
-cudaError_t launch_pages_keep(const PagesView& pv, int layers, long layer_bytes, const BatchView& bv, const uint8_t* keep,
-                              int32_t* lens_out, cudaStream_t st) {
+cudaError_t launch_pages_keep(const PagesView& pv, int layers, long layer_bytes, const BatchView& bv, int max_new,
+                              const uint8_t* keep, int32_t* lens_out, void* work, cudaStream_t st) {
   PagesView p = pv;
   BatchView b = bv;
   long units = (long)layers * pv.heads * columns(pv);
-  void* args[] = {&p, &layer_bytes, &units, &b, &keep, &lens_out};
-  return launch_pdl((const void*)pages_keep_kernel, dim3((unsigned)((units + kKeepThreads - 1) / kKeepThreads), bv.batch),
-                    dim3(kKeepThreads), 0, st, args);
+  KeepPlan* plan = static_cast<KeepPlan*>(work);
+  KeepSeg* seg = reinterpret_cast<KeepSeg*>(static_cast<char*>(work) + 256);
+  if (max_new <= kKeepThreads || bv.new_tokens / kSegRows + bv.batch > kKeepSegs) {
+    void* args[] = {&p, &layer_bytes, &units, &b, &keep, &lens_out};
+    return launch_pdl((const void*)pages_keep_kernel, dim3((unsigned)((units + kKeepThreads - 1) / kKeepThreads), bv.batch),
+                      dim3(kKeepThreads), 0, st, args);
+  }
+  void* args1[] = {&p, &b, &keep, &lens_out, &plan, &seg};
+  cudaError_t e = launch_pdl((const void*)pages_keep_plan_kernel, dim3(bv.batch), dim3(kPlanThreads), 0, st, args1);
+  if (e != cudaSuccess) return e;
+  void* args2[] = {&p, &layer_bytes, &units, &b, &keep, &plan, &seg};
+  const double most = (bv.new_tokens / kSegRows + bv.batch) * (double)((units + 31) / 32);
+  return launch_pdl((const void*)pages_keep_move_kernel, dim3((unsigned)std::min(most, 152.0 * 2)), dim3(kKeepThreads), 0, st,
+                    args2);
 }
+
+size_t pages_keep_bytes() { return 256 + sizeof(KeepSeg) * kKeepSegs; }
 
 cudaError_t launch_pages_copy(const PagesView& pv, int layers, long layer_bytes, const int32_t* src, const int32_t* dst,
                               int count, const int32_t* number, cudaStream_t st) {
@@ -471,11 +745,14 @@ cudaError_t launch_pages_copy(const PagesView& pv, int layers, long layer_bytes,
 cudaError_t launch_pages_fork(const PagesView& pv, const kvq_pages_fork_args& x, cudaStream_t st) {
   PagesView p = pv;
   kvq_pages_fork_args a = x;
-  void* args[] = {&p, &a};
-  const long out = std::max<long>(a.stride_out, (pv.pages + 3) / 4);
-  cudaError_t e = launch_pdl((const void*)pages_fork_kernel, dim3(table_blocks(out), a.rows_out + 1), dim3(kForkThreads), 0, st, args);
+  int per = fork_blocks(a.stride_out);
+  const int refs = a.refs_out != a.refs_in ? fork_blocks(pv.pages) : 0;
+  void* args[] = {&p, &a, &per};
+  cudaError_t e = launch_pdl((const void*)pages_fork_kernel, dim3((unsigned)(per * a.rows_out + refs)), dim3(kForkThreads), 0, st, args);
   if (e != cudaSuccess) return e;
-  return launch_pdl((const void*)pages_refs_kernel, dim3(table_blocks(std::max(a.stride_in, a.stride_out)), std::max(a.rows_in, a.rows_out)),
+  const long most = std::max(a.stride_in, a.stride_out);
+  return launch_pdl((const void*)pages_refs_kernel,
+                    dim3((unsigned)std::min((long)fork_blocks(most), 4096L), std::max(a.rows_in, a.rows_out)),
                     dim3(kForkThreads), 0, st, args);
 }
 

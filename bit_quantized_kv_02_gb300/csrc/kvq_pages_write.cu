@@ -480,8 +480,11 @@ __device__ __forceinline__ uint4 get8(const char* rec, int off, int meta_off, in
   return out;
 }
 
+// As many warps as an SM holds hide its loads better than several heads in flight a warp:
+// 509 pages of 64 tokens, 40 heads of 128, 8- and 4-bit, four layers, us: 8 CTAs per SM
+// and one head 212 a layer, two heads 213 (6 CTAs) and 237 (8), four heads (3 CTAs) 349.
 template <int D>
-__global__ void __launch_bounds__(kThreads) pages_read_kernel(PagesView pv, BatchView bv, char* k_out, char* v_out,
+__global__ void __launch_bounds__(kThreads, 8) pages_read_kernel(PagesView pv, BatchView bv, char* k_out, char* v_out,
                                                               int lg_wpt) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
   __shared__ Place place[kRowWarps];

@@ -474,6 +474,38 @@ def test_keep(fmt, name, page_tokens, d, h):
 
 
 @gpu
+@pytest.mark.parametrize("fmt", ["bf16", "4_4"])
+@pytest.mark.parametrize("share", [0.03, 0.5, 0.9, 0.999])
+def test_keep_of_long_sequences(fmt, share):
+    """Tens of thousands of tokens in segments that many CTAs move: few and many places between a token's
+    old place and its new one; a hint that is wrong changes nothing."""
+    c = make(([20011, 129, 3, 6000], [20011, 500, 3, 6000]), 32, fmt, (3, 3), 64, layers=2, seed=4, pad=1)
+    for trial in range(3):
+        for i in range(2):
+            fill(c, 3, 64, layer=i)
+        keep = torch.rand(c.rows, generator=c.g) < share
+        before = layers_of(c, 2)
+        lens = c.cache.kvq_pages_keep(keep.cuda(), c.batch(max_new=5 if trial == 2 else 0))
+        assert c.cache.kvq_pages_status() == 0
+        for x, y in zip(layers_of(c, 2), before):
+            want, new = kept(c, keep.tolist(), y)
+            assert all(torch.equal(a, b) for a, b in zip(x, want))
+        assert lens.tolist() == new
+
+
+@gpu
+def test_keep_of_more_rows_than_its_workspace_counts():
+    """Sequences that name the same rows, twice as many as the segments there is room for."""
+    n = 16400 * 128
+    cache = kvq.KVQPages(kvq.make_pages_config(1, 2, 128, 1, 1, 64))
+    table = torch.zeros((4, 16400), dtype=torch.int32, device="cuda")
+    batch = kvq.PagesBatch(ints([0, n, 0, n, n]), ints([n, 7, n, 5]), table, n)
+    lens = cache.kvq_pages_keep(torch.zeros(n, dtype=torch.bool, device="cuda"), batch)
+    assert cache.kvq_pages_status() == 7
+    assert lens.tolist() == [0, 7, n, 5]
+
+
+@gpu
 def test_keep_where_indices_are_bad():
     """A bad page leaves its tokens, a bad sequence all of its own; both are reported, the others are right."""
     c = make(([40, 5, 6], [40, 20, 30]), 16, "f16", (2, 2), 64, layers=1)

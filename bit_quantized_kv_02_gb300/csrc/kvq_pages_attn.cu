@@ -128,6 +128,9 @@ cudaError_t launch_tile(kvq_pages* P, AttnArgs a, bool masked, int max_rows, cud
   if (P->L.k_bits != 16) {
     const int left = P->max_smem - (int)(k.static_smem + launch_smem(k, a.bv.batch));
     a.ring = std::min(left / P->L.tile_bytes, kTileRing);
+    // a multiple of the dequantizing warps of a tensor, where it reaches them
+    const int warps = P->cfg.head_dim == 256 ? 4 : 2;
+    if (a.ring >= warps) a.ring -= a.ring % warps;
     if (a.ring < 2) return cudaErrorInvalidConfiguration;  // (not reached: two of the largest records fit)
   }
   return launch_kernel(k, a, std::min(P->sm_count, kTileCtas), a.pv.head_dim == 256 ? kTileRows / 2 : kTileRows,

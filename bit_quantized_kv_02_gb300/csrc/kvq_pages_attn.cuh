@@ -42,6 +42,16 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, int parity) {
       : "memory");
   return ok;
 }
+// (without waiting at all)
+__device__ __forceinline__ bool mbar_test(uint32_t bar, int parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
 __device__ __forceinline__ unsigned long long time_ns() {
   unsigned long long t;
   asm volatile("mov.u64 %0, %globaltimer;\n" : "=l"(t));
@@ -50,14 +60,17 @@ __device__ __forceinline__ unsigned long long time_ns() {
 constexpr unsigned long long kWaitNs = 2000000000ull;  // longest wait on a barrier
 // Waits for the phase, by one thread.  False where `limit` ns pass first, which is
 // recorded in *err and *dead (shared memory), or where another thread of the CTA has
-// given up.
+// given up.  Short, and its loop not unrolled: a wait is written at many places of a
+// kernel, and what a warp runs while it waits must not drive the others' code out of the
+// instruction cache (64 polls between looks at the clock, which the compiler unrolled,
+// made a kernel 240 KB long, and chunks over 8-bit pages 578 us against 484).
 __device__ __forceinline__ bool cta_wait(uint32_t bar, int parity, int* dead, int* err,
                                          unsigned long long limit = kWaitNs) {
   if (mbar_try(bar, parity)) return true;
   const unsigned long long t0 = time_ns();
+#pragma unroll 1
   do {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try(bar, parity)) return true;
+    if (mbar_try(bar, parity)) return true;
     if (*(volatile int*)dead) return false;
   } while (time_ns() - t0 < limit);
   *(volatile int*)dead = 1;

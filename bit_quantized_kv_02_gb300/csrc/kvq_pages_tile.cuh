@@ -10,8 +10,9 @@
 //    stages; pages are stored in the operand layout, so no tensor map and no
 //    shuffling is needed;
 //  - raw loaders and dequantizers (codes): one warp per tensor copies records
-//    into a ring, two warps per tensor (four with one row tile) turn their codes
-//    into fp16 operand tiles (the value the page stands for, one rounding);
+//    into a ring, a slot a lane; two warps per tensor (four with one row tile) turn
+//    whole records' codes into fp16 operand tiles (the value the page stands for, one
+//    rounding);
 //  - one warp issues the matrix instructions: S = Q K^T (both from shared
 //    memory), O += P V (P from tensor memory, over the scores it came from);
 //  - softmax: a warpgroup per tile, a thread per row, so maxima and sums need
@@ -193,163 +194,198 @@ __device__ __forceinline__ void tile_loader(const AttnArgs& a, TileShared<D, FMT
 // ------------------------------------------------------------- dequantizer --
 
 // Brings the records of one tensor (codes and metadata are neighbours) into a
-// ring of raw records, ahead of the warps that turn them.
-template <int D, int FMT, int VALUE>
-__device__ __forceinline__ void raw_loader(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int lane) {
+// ring of raw records, ahead of the warps that turn them.  Lane i has slot i of the
+// ring: it waits for its slot alone and brings every a.ring-th record, so a copy costs
+// no other copy's wait or issue (one lane for all records: 830 cycles a record, which
+// bounded the kernel).
+template <int D, int FMT>
+__device__ __forceinline__ void raw_loader(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int value, int lane) {
   using C = TileCfg<D, FMT>;
   const PagesLayout& L = a.pv.L;
-  const int from = VALUE ? L.v_off : 0, bytes = VALUE ? L.tile_bytes - L.v_off : L.v_off;
-  const uint32_t ring = smem + C::RAW_OFF + (VALUE ? a.ring * L.v_off : 0);
-  int r = 0, par = 0;
+  const int from = value ? L.v_off : 0, bytes = value ? L.tile_bytes - L.v_off : L.v_off;
+  const uint32_t slot_at = smem + C::RAW_OFF + (value ? a.ring * L.v_off : 0) + lane * bytes;
+  const uint32_t free_bar = smem_u32(&sh->raw_free[value][lane & 7]), full_bar = smem_u32(&sh->raw_full[value][lane & 7]);
+  int r = 0;    // slot of the piece's first record
+  int par = 0;  // the lane's slot: phase of its next use
   for (int k = 0;; ++k) {
     const int slot = k % C::PIECES;
     if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) return;
     const Piece p = sh->piece[slot];
     if (p.nblk == 0) return;
     const PageRun run(a.pv, p.head);
-    const int end = min((p.blk + p.nblk) * C::BK, p.s.len);
-    // 32 records' pages at a time
-    for (int tok0 = p.blk * C::BK; tok0 < end; tok0 += 16 * 32) {
-      const int mine = tok0 + 16 * lane;
-      const int page = mine < end ? page_index(a, p.b, mine) : 0;
-      for (int i = 0; i < 32 && tok0 + 16 * i < end; ++i) {
-        const int pg = __shfl_sync(0xffffffffu, page, i);
-        if (!tile_wait_warp(sh, a, &sh->raw_free[VALUE][r], par ^ 1)) return;
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(&sh->raw_full[VALUE][r]);
-          mbar_expect(bar, bytes);
-          bulk_load(ring + r * bytes, run.at(a, pg, tok0 + 16 * i) + from, bytes, bar);
+    const int tok0 = p.blk * C::BK, n = (min(tok0 + p.nblk * C::BK, p.s.len) - tok0 + 15) >> 4;  // records (none: <= 0)
+    int i = lane < a.ring ? (lane >= r ? lane - r : lane - r + a.ring) : n;  // the lane's next record
+    auto page_of = [&](int i) { return i < n ? page_index(a, p.b, tok0 + 16 * i) : 0; };
+    int page = page_of(i), next = page_of(i + a.ring);
+    unsigned long long since = 0;  // when the lane's wait was first seen to last
+    for (int turns = 1; __any_sync(0xffffffffu, i < n); ++turns) {
+      const bool go = i < n && mbar_test(free_bar, par ^ 1);
+      if (go) {
+        mbar_expect(full_bar, bytes);
+        bulk_load(slot_at, run.at(a, page, tok0 + 16 * i) + from, bytes, full_bar);
+        par ^= 1;
+        i += a.ring;
+        page = next;
+        next = page_of(i + a.ring);
+        since = 0;
+      }
+      if (!__any_sync(0xffffffffu, go)) __nanosleep(40);
+      if ((turns & 255) == 0) {  // the limit of this wait, and the end of another's
+        bool late = *(volatile int*)&sh->dead;
+        if (i < n && !late) {
+          const unsigned long long now = time_ns();
+          if (since == 0) since = now;
+          if (now - since > kWaitNs) {
+            *(volatile int*)&sh->dead = 1;
+            atomicOr(a.pv.err, 2);
+            late = true;
+          }
         }
-        if (++r == a.ring) r = 0, par ^= 1;
+        if (__any_sync(0xffffffffu, late)) return;
       }
     }
+    r = (int)((unsigned)(r + max(n, 0)) % (unsigned)a.ring);
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh->piece_free[slot]));
   }
 }
 
-// Keys (VALUE 0) or values (1) of all pieces: a thread turns a run of 32 channels
-// of one token into four 16-byte chunks of the operand tile; tid: thread among
-// those of the tensor.  The loop body is kept small: with the many roles of this
-// kernel, unrolled over a block it ran out of the instruction cache.
-template <int D, int FMT, int VALUE>
-__device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int tid) {
+// Keys (value 0) or values (1) of all pieces: a warp turns whole records, those of its
+// places in the ring (a place has one warp, whose waits then follow its phases one by
+// one: the ring is a multiple of the warps, or some have no place); a lane turns runs of
+// 32 channels of one token into four 16-byte chunks of the operand tile.  A record is
+// waited for, fenced and given back once, by one warp.  Keys and values share the code
+// where their bits do, and a turn is two runs: with the many roles of this kernel its
+// hot code is what the instruction cache holds (four runs a turn and a copy for each
+// tensor: 8 prompts of up to 448 tokens over 8190 8-bit tokens, 32 over 8 heads of 128,
+// 484 us).  tid: thread among those of the tensor.
+template <int D, int FMT, int BITS>
+__device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int value, int tid) {
   using C = TileCfg<D, FMT>;
-  using F = typename C::F;
-  constexpr int BITS = F::KB == 16 ? 4 : (VALUE ? F::VB : F::KB);
-  constexpr int THREADS = 16 * C::PROD, PPT = D / 32;
-  constexpr int RECS = THREADS / (16 * PPT);  // records turned at once
-  static_assert(RECS >= 1 && RECS <= 2, "the ring holds two records at least");
-  constexpr int WC = BITS / 4;                // words of a chunk of 8 channels
-  const int lane = tid & 31, piece = tid % PPT, rec = tid / (16 * PPT), row = (tid / PPT) & 15;
+  constexpr int WARPS = C::PROD / 2, PPT = D / 32, ROWS = 32 / PPT;  // rows of a run of the warp
+  constexpr int RUNS = 16 / ROWS, TURN = RUNS < 2 ? 1 : 2;           // runs of a record, of a turn
+  constexpr int WC = BITS / 4;                                       // words of a chunk of 8 channels
+  const int with = min(WARPS, a.ring);  // warps that have places
+  const int lane = tid & 31, warp = tid >> 5, piece = lane % PPT, row = lane / PPT;
   const PagesLayout& L = a.pv.L;
-  const int meta = VALUE ? L.vm_off - L.v_off : L.km_off, lg = VALUE ? L.v_lg : L.k_lg;
-  const uint32_t raw = smem + C::RAW_OFF + (VALUE ? a.ring * L.v_off : 0);
-  const int raw_bytes = VALUE ? L.tile_bytes - L.v_off : L.v_off;
+  const int meta = value ? L.vm_off - L.v_off : L.km_off, lg = value ? L.v_lg : L.k_lg;
+  const uint32_t raw = smem + C::RAW_OFF + (value ? a.ring * L.v_off : 0);
+  const int raw_bytes = value ? L.tile_bytes - L.v_off : L.v_off;
   const uint32_t codes_at = row * (D * BITS / 8) + piece * (4 * BITS);
-  const uint32_t meta_at = meta + (row * (D >> lg) + ((piece * 32) >> lg)) * 4;
+  const uint32_t meta_at = meta + (row * (D >> lg) + ((piece * 32) >> lg)) * 4, meta_run = ROWS * (D >> lg) * 4;
+  uint64_t* const empty = value ? sh->v_empty : sh->k_empty;
+  uint64_t* const ready = value ? sh->v_full : sh->k_full;
+  uint64_t* const full = sh->raw_full[value];
+  uint64_t* const unused = sh->raw_free[value];
+  const uint32_t tiles = smem + (value ? C::V_OFF : C::K_OFF) + (piece >> 1) * (128 * 128);
   // lanes of other column blocks store their four chunks in another order, so
   // that the 8 lanes of a phase touch 8 different groups of banks
   const int turn = D == 64 ? 0 : (D == 128 ? 2 * (piece >> 1) : piece >> 1);
-  int st = 0, par = 0, r = 0, rpar = 0;
+  int st = 0, par = 0;
+  int r = 0, rpar = 0;  // slot of the block's first record, its phase
   for (int k = 0;; ++k) {
     const int slot = k % C::PIECES;
     if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) return;
-    const Piece p = sh->piece[slot];
-    if (p.nblk == 0) return;
-    int tok = p.blk * C::BK;
-    // A unit's codes and metadata.  Every record with a token of the sequence
-    // arrives; rows behind its end become zero (zero + code * step = 0), whatever
-    // the page holds there.
-    auto take = [&](int tok, uint32_t* w, uint32_t* zs) -> bool {
+    const int nblk = sh->piece[slot].nblk, len = sh->piece[slot].s.len;
+    if (nblk == 0) return;
+    int tok = sh->piece[slot].blk * C::BK;
+#pragma unroll 1
+    for (int j = 0; j < nblk; ++j, tok += C::BK) {
+      const int n = max(min((len - tok + 15) >> 4, C::BK / 16), 0);  // records that arrive
+      int c = warp - r % with;                                       // the warp's first record of the block
+      if (c < 0) c += with;
+      if (warp >= with) c = C::BK / 16;
+      int s = r + c, spar = rpar;
+      while (s >= a.ring) s -= a.ring, spar ^= 1;
+      if (!tile_wait_warp(sh, a, &empty[st], par ^ 1)) return;
+      const uint32_t tile = tiles + st * C::TILE;
+#pragma unroll 1
+      for (; c < C::BK / 16; c += with) {
+        if (c < n && !tile_wait_warp(sh, a, &full[s], spar)) return;
+        const uint32_t from = raw + s * raw_bytes;
+#pragma unroll 1
+        for (int y0 = 0; y0 < RUNS; y0 += TURN) {
+          // Codes and metadata.  Rows behind the sequence's end become zero (zero + code *
+          // step = 0), whatever the page holds there; records behind it do not arrive.
+          uint32_t w[TURN][4 * WC], zs[TURN];
 #pragma unroll
-      for (int i = 0; i < 4 * WC; ++i) w[i] = 0;
-      *zs = 0;
-      int rr = r, pp = rpar;
+          for (int y = 0; y < TURN; ++y) {
+            if (c < n) {
+              ldsv<4 * WC>(from + codes_at + (y0 + y) * (ROWS * D * BITS / 8), w[y]);
+              zs[y] = lds32(from + meta_at + (y0 + y) * meta_run);
+            } else {
 #pragma unroll
-      for (int i = 0; i < RECS; ++i) {
-        if (tok + 16 * i >= p.s.len) continue;
-        if (!tile_wait_warp(sh, a, &sh->raw_full[VALUE][rr], pp)) return false;
-        if (RECS == 1 || rec == i) {
-          const uint32_t from = raw + rr * raw_bytes;
-          ldsv<4 * WC>(from + codes_at, w);
-          *zs = lds32(from + meta_at);
-        }
-        if (++rr == a.ring) rr = 0, pp ^= 1;
-      }
-      return true;
-    };
-    // Its records go back: the fence orders each lane's loads before the bulk copies
-    // into the same bytes, which go another way (without it a copy overtook loads that
-    // waited behind the matrix operands), the warp's barrier the lanes before the
-    // arrival.  (The records held until their values are stored: 703 us against 579
-    // for 2 x 600 tokens at 20000, 16 over 2 heads of 256, 8 bits.)
-    auto give_back = [&](int tok) {
-      fence_async();
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < RECS; ++i)
-        if (tok + 16 * i < p.s.len) {
-          if (lane == 0) mbar_arrive(smem_u32(&sh->raw_free[VALUE][r]));
-          if (++r == a.ring) r = 0, rpar ^= 1;
-        }
-    };
-    auto turn_unit = [&](int tok, uint32_t* w, uint32_t zs, uint32_t out) {
-      if (tok + rec * 16 + row >= p.s.len) zs = 0;
-      const __half2 z = __low2half2(as_h2(zs)), s = __high2half2(as_h2(zs));
-#pragma unroll
-      for (int b = 1; b < 4; b <<= 1)  // the words of chunk k to place k ^ turn
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (!(c & b))
-#pragma unroll
-            for (int e = 0; e < WC; ++e) {
-              const uint32_t x = w[WC * c + e], y = w[WC * (c ^ b) + e];
-              w[WC * c + e] = (turn & b) ? y : x;
-              w[WC * (c ^ b) + e] = (turn & b) ? x : y;
+              for (int e = 0; e < 4 * WC; ++e) w[y][e] = 0;
             }
+          }
+          // The record goes back: the fence orders each lane's loads before the bulk copy
+          // into the same bytes, which goes another way (without it a copy overtook loads
+          // that waited behind the matrix operands), the warp's barrier the lanes before
+          // the arrival.
+          if (y0 + TURN == RUNS) {
+            fence_async();
+            __syncwarp();
+            if (lane == 0 && c < n) mbar_arrive(smem_u32(&unused[s]));
+          }
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t y[4];
-        if constexpr (BITS == 8) {
-          y[0] = bytes<0>(w[2 * c], s, z);
-          y[1] = bytes<1>(w[2 * c], s, z);
-          y[2] = bytes<0>(w[2 * c + 1], s, z);
-          y[3] = bytes<1>(w[2 * c + 1], s, z);
-        } else {
-          y[0] = nibbles<0>(w[c], s, z);
-          y[1] = nibbles<1>(w[c], s, z);
-          y[2] = nibbles<2>(w[c], s, z);
-          y[3] = nibbles<3>(w[c], s, z);
+          for (int y = 0; y < TURN; ++y) {
+            uint32_t* v = w[y];
+            const int at_row = c * 16 + (y0 + y) * ROWS + row;
+            if (tok + at_row >= len) zs[y] = 0;
+            const __half2 z = __low2half2(as_h2(zs[y])), sc = __high2half2(as_h2(zs[y]));
+#pragma unroll
+            for (int b = 1; b < 4; b <<= 1)  // the words of chunk i to place i ^ turn
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (!(i & b))
+#pragma unroll
+                  for (int e = 0; e < WC; ++e) {
+                    const uint32_t lo = v[WC * i + e], hi = v[WC * (i ^ b) + e];
+                    v[WC * i + e] = (turn & b) ? hi : lo;
+                    v[WC * (i ^ b) + e] = (turn & b) ? lo : hi;
+                  }
+            const uint32_t out = tile + at_row * 128;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t o[4];
+              if constexpr (BITS == 8) {
+                o[0] = bytes<0>(v[2 * i], sc, z);
+                o[1] = bytes<1>(v[2 * i], sc, z);
+                o[2] = bytes<0>(v[2 * i + 1], sc, z);
+                o[3] = bytes<1>(v[2 * i + 1], sc, z);
+              } else {
+                o[0] = nibbles<0>(v[i], sc, z);
+                o[1] = nibbles<1>(v[i], sc, z);
+                o[2] = nibbles<2>(v[i], sc, z);
+                o[3] = nibbles<3>(v[i], sc, z);
+              }
+              const int at = (4 * (piece & 1) + (i ^ turn)) ^ (at_row & 7);
+              asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(out + (at << 4)), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                           : "memory");
+            }
+          }
         }
-        const int at = (4 * (piece & 1) + (c ^ turn)) ^ (row & 7);
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(out + (at << 4)), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                     : "memory");
+        s += with;
+        while (s >= a.ring) s -= a.ring, spar ^= 1;
       }
-    };
-#pragma unroll 1
-    for (int j = 0; j < p.nblk; ++j) {
-      if (!tile_wait_warp(sh, a, VALUE ? &sh->v_empty[st] : &sh->k_empty[st], par ^ 1)) return;
-      uint32_t out = smem + (VALUE ? C::V_OFF : C::K_OFF) + st * C::TILE + (piece >> 1) * (128 * 128) + (rec * 16 + row) * 128;
-      constexpr int UT = 16 * RECS;  // tokens of a unit; two units a turn, for the latencies of one to hide the other's
-#pragma unroll 1
-      for (int u = 0; u < C::BK; u += 2 * UT, tok += 2 * UT, out += 2 * UT * 128) {
-        uint32_t w0[4 * WC], w1[4 * WC], z0, z1;
-        if (!take(tok, w0, &z0)) return;
-        give_back(tok);
-        if (!take(tok + UT, w1, &z1)) return;
-        give_back(tok + UT);
-        turn_unit(tok, w0, z0, out);
-        turn_unit(tok + UT, w1, z1, out + UT * 128);
-      }
+      r += n;
+      while (r >= a.ring) r -= a.ring, rpar ^= 1;
       fence_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(VALUE ? &sh->v_full[st] : &sh->k_full[st]));
+      if (lane == 0) mbar_arrive(smem_u32(&ready[st]));
       if (++st == C::NS) st = 0, par ^= 1;
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh->piece_free[slot]));
   }
+}
+// Both tensors: one body where their bits are the same.
+template <int D, int FMT>
+__device__ __forceinline__ void tile_dequantize(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int value, int tid) {
+  using F = typename TileCfg<D, FMT>::F;
+  if constexpr (F::KB == F::VB) tile_dequantizer<D, FMT, F::KB>(a, sh, smem, value, tid);
+  else if (value) tile_dequantizer<D, FMT, F::VB>(a, sh, smem, 1, tid);
+  else tile_dequantizer<D, FMT, F::KB>(a, sh, smem, 0, tid);
 }
 
 // -------------------------------------------------------------- matrix unit --
@@ -365,7 +401,7 @@ __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* 
   const uint64_t v0 = smem_desc(smem + C::V_OFF, C::BK * 128, 1024);
   int ks = 0, kpar = 0, vs = 0, vpar = 0;  // stage to read next, its phase
   int bc = 0;                              // score buffers handed out (one tile)
-  int pc[2] = {0, 0};
+  int turns = 0;                           // phases of the weights (two tiles, a bit each)
   // S of a tile with the keys of stage ks; O of a tile with the values of stage vs.
   // (Scoring the next block's first 64 keys into the columns that the weights leave
   // free, ahead of the value product, was slower: 995 us against 820 for a chunk of
@@ -406,40 +442,38 @@ __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* 
     __syncwarp();
     if (++vs == C::NS) vs = 0, vpar ^= 1;
   };
+  // (One loop from the block before a piece's first on, one copy of each product's code:
+  // written out for both tiles and the first block the role was 20 KB long.)
   for (int k = 0;; ++k) {
     const int slot = k % C::PIECES;
     if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) return;
     const int n = __shfl_sync(0xffffffffu, sh->piece[slot].nblk, 0);
     if (n == 0) return;
     if (!tile_wait_warp(sh, a, &sh->q_full, k & 1)) return;
-    if (!tile_wait_warp(sh, a, &sh->k_full[ks], kpar)) return;
-    tc_after_sync();
     if (C::NT == 2) {
-      int lo[2], hi[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        tile_range<D, FMT, MASK>(a, sh->piece[slot], i, &lo[i], &hi[i]);
-        lo[i] = __shfl_sync(0xffffffffu, lo[i], 0);
-        hi[i] = __shfl_sync(0xffffffffu, hi[i], 0);
-      }
-      auto sees = [&](int i, int j) { return j >= lo[i] && j < hi[i]; };
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (sees(i, 0)) scores(i, i);
-      free_k(n == 1);
-      for (int j = 0; j < n; ++j) {
+      // the blocks that tile 0 / 1 sees
+      int lo0, hi0, lo1, hi1;
+      tile_range<D, FMT, MASK>(a, sh->piece[slot], 0, &lo0, &hi0);
+      tile_range<D, FMT, MASK>(a, sh->piece[slot], 1, &lo1, &hi1);
+      lo0 = __shfl_sync(0xffffffffu, lo0, 0);
+      hi0 = __shfl_sync(0xffffffffu, hi0, 0);
+      lo1 = __shfl_sync(0xffffffffu, lo1, 0);
+      hi1 = __shfl_sync(0xffffffffu, hi1, 0);
+#pragma unroll 1
+      for (int j = -1; j < n; ++j) {
         bool have_k = false;
-        if (!tile_wait_warp(sh, a, &sh->v_full[vs], vpar)) return;
-#pragma unroll
+        if (j >= 0 && !tile_wait_warp(sh, a, &sh->v_full[vs], vpar)) return;
+#pragma unroll 1
         for (int i = 0; i < 2; ++i) {
-          if (sees(i, j)) {
-            if (!tile_wait_warp(sh, a, &sh->p_full[i], pc[i] & 1)) return;
-            ++pc[i];
+          const int lo = i ? lo1 : lo0, hi = i ? hi1 : hi0;
+          if (j >= lo && j < hi) {  // (lo is not negative)
+            if (!tile_wait_warp(sh, a, &sh->p_full[i], (turns >> i) & 1)) return;
+            turns ^= 1 << i;
             tc_after_sync();
-            values(i, i, j > lo[i]);
+            values(i, i, j > lo);
           }
-          if (i == 1) free_v();
-          if (j + 1 < n && sees(i, j + 1)) {
+          if (i == 1 && j >= 0) free_v();
+          if (j + 1 < n && j + 1 >= lo && j + 1 < hi) {
             if (!have_k && !tile_wait_warp(sh, a, &sh->k_full[ks], kpar)) return;
             have_k = true;
             tc_after_sync();
@@ -452,16 +486,16 @@ __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* 
         }
       }
     } else {
-      scores(bc & 1, 0);
-      free_k(n == 1);
-      for (int j = 0; j < n; ++j) {
-        const int buf = bc & 1;
+#pragma unroll 1
+      for (int j = -1; j < n; ++j) {
+        const int buf = bc & 1;  // (the scores of block j)
         if (j + 1 < n) {
           if (!tile_wait_warp(sh, a, &sh->k_full[ks], kpar)) return;
           tc_after_sync();
-          scores(buf ^ 1, 0);
+          scores(j < 0 ? buf : buf ^ 1, 0);
           free_k(j + 2 == n);
         }
+        if (j < 0) continue;
         if (!tile_wait_warp(sh, a, &sh->v_full[vs], vpar)) return;
         if (!tile_wait_warp(sh, a, &sh->p_full[buf], (bc >> 1) & 1)) return;
         tc_after_sync();
@@ -484,7 +518,7 @@ template <int D, int FMT>
 __device__ __forceinline__ float tile_query(const AttnArgs& a, const RowMap& rm, int rows, int tile_row, int row0,
                                             uint32_t tile, int lane) {
   using F = Fmt<FMT>;
-  constexpr int LPR = D / 8, RPI = 32 / LPR, U = LPR < 16 ? LPR : 16;  // lanes a row, rows a step, steps in flight
+  constexpr int LPR = D / 8, RPI = 32 / LPR, U = 4;  // lanes a row, rows a step, steps in flight (16: 32 KB of code)
   const int g = lane / LPR, c = lane % LPR;
   float sc = a.scale_log2;
   for (int it0 = 0; it0 < LPR; it0 += U) {
@@ -591,6 +625,17 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
           }
         };
         uint32_t s[64], w[64];
+        // Blocks with hidden tokens: minus infinity goes over their scores first, in a pass
+        // of its own (the code of every block stays short).
+        if (edge) {
+#pragma unroll 1
+          for (int q = 0; q < BK / 32; ++q) {
+            tmem_ld32(sb + q * 32, s);
+            hide(s, q);
+            tmem_st32(sb + q * 32, s);
+          }
+          tmem_wait_st();
+        }
         float2 add;
         // Most blocks leave the running maximum alone, so the weights are taken under
         // it while the block's maximum is found.  Where that passes it by 2^8, and in
@@ -602,7 +647,6 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
 #pragma unroll 1
             for (int q = 0; q < BK / 32; ++q) {
               tmem_ld32(sb + q * 32, s);
-              if (edge) hide(s, q);
 #pragma unroll
               for (int c = 0; c < 32; c += 2) top = fmaxf(fmaxf(top, __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
             }
@@ -630,7 +674,6 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
           for (int q = 0; q < BK / 32; ++q) {
             if (q % 2 == 0) tmem_ld64(sb + q * 32, s);
             uint32_t* e = s + q % 2 * 32;
-            if (edge) hide(e, q);
 #pragma unroll
             for (int c = 0; c < 32; c += 2) {
               float2 x = make_float2(__uint_as_float(e[c]), __uint_as_float(e[c + 1]));
@@ -756,7 +799,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
     for (int i = 0; i < kTileRing; ++i)
       for (int t = 0; t < 2; ++t) {
         mbar_init(smem_u32(&sh.raw_full[t][i]), 1);
-        mbar_init(smem_u32(&sh.raw_free[t][i]), F::kQuant ? C::PROD / 2 : 1);
+        mbar_init(smem_u32(&sh.raw_free[t][i]), 1);
       }
     sh.dead = 0;
     fence_mbar_init();
@@ -777,18 +820,10 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
   if (warp < 4 * C::NT) {
     if constexpr (F::kQuant) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
     tile_softmax<D, FMT, MASK>(a, &sh, smem, warp >> 2, threadIdx.x);
-  } else if (warp < 8) {
-    if constexpr (F::kQuant) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-      tile_dequantizer<D, FMT, 1>(a, &sh, smem, threadIdx.x - 128);  // (one tile) values
-    }
-  } else if (warp < 12) {
+  } else if (warp >= 8 && warp < 12) {
     if constexpr (F::kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
     if (warp == 8) {
       tile_mma<D, FMT, MASK>(a, &sh, smem);
-    } else if (warp == 9) {
-      if constexpr (F::kQuant) raw_loader<D, FMT, 0>(a, &sh, smem, lane);
-      else tile_loader<D, FMT>(a, &sh, smem, lane);
     } else if (warp == 10) {
       // the pieces of this CTA's units, ahead of the others; nblk 0 ends
       long u = cta_begin(&sh.work, blockIdx.x);
@@ -815,15 +850,16 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
         __syncwarp();
         if (p.nblk == 0) break;
       }
-    } else {
-      if constexpr (F::kQuant) raw_loader<D, FMT, 1>(a, &sh, smem, lane);
+    } else if constexpr (F::kQuant) {
+      raw_loader<D, FMT>(a, &sh, smem, warp == 11, lane);  // (9: keys)
+    } else if (warp == 9) {
+      tile_loader<D, FMT>(a, &sh, smem, lane);
     }
-  } else {
-    if constexpr (F::kQuant) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-      if (C::NT == 1 || warp < 14) tile_dequantizer<D, FMT, 0>(a, &sh, smem, threadIdx.x - 384);
-      else tile_dequantizer<D, FMT, 1>(a, &sh, smem, threadIdx.x - 448);
-    }
+  } else if constexpr (F::kQuant) {
+    // one tile: warps 4 .. 7 values, 12 .. 15 keys; two tiles: 12 and 13 keys, 14 and 15 values
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+    const int value = C::NT == 1 ? warp < 8 : warp >= 14;
+    tile_dequantize<D, FMT>(a, &sh, smem, value, threadIdx.x & (16 * C::PROD - 1));
   }
   __syncwarp();
   if (*(volatile int*)&sh.dead) {  // given up: what is in flight lands before memory is given back

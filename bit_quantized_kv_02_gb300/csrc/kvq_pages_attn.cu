@@ -187,8 +187,15 @@ cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, bool masked, int max_ro
   // 48 / 51, 61 / 53.  Codes cost the many-rows kernel its dequantizing warps: 4 bits, heads of 64: 128 rows
   // 138 / 159, 192 rows 204 / 189; heads of 128: 64 rows 91 / 99, 96 rows 125 / 103;
   // heads of 256: 48 rows 57 / 61, 64 rows 67 / 62.
+  // The masked kernels over codes were measured after the many-rows kernel had become
+  // faster (the causal ones keep the choice, and with it the rounding, that they had): 8
+  // sequences of 8192 tokens, few / many rows, us: 8 bits, 12 heads of 64: 48 rows 71 / 80,
+  // 64 rows 92 / 81; 8 heads of 128: 32 rows 62 / 72, 48 rows 79 / 73; 2 heads of 256: 16
+  // rows 40 / 48, 32 rows 53 / 51; 4 bits: 65 / 78, 79 / 79; 57 / 64, 70 / 65; 36 / 41, 50 / 44.
   const int D = P->cfg.head_dim;
-  const int few = P->L.k_bits == 16 ? 32 : (D == 64 ? 128 : (D == 128 ? 64 : 48));
+  const int few = P->L.k_bits == 16 ? 32
+                  : masked          ? (D == 64 ? 48 : (D == 128 ? 32 : 16))
+                                    : (D == 64 ? 128 : (D == 128 ? 64 : 48));
   a.rows_lo = 0;
   a.rows_hi = INT_MAX;
   if (P->which == 1 || (P->which == 0 && max_rows <= few)) return launch_rows(P, a, masked, max_rows, st);

@@ -463,7 +463,7 @@ __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* 
       for (int j = -1; j < n; ++j) {
         bool have_k = false;
         if (j >= 0 && !tile_wait_warp(sh, a, &sh->v_full[vs], vpar)) return;
-#pragma unroll 1
+#pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int lo = i ? lo1 : lo0, hi = i ? hi1 : hi0;
           if (j >= lo && j < hi) {  // (lo is not negative)

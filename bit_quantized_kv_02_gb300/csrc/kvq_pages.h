@@ -30,7 +30,7 @@ constexpr int kPagesCtas = 1024;   // most CTAs of an attention launch (partial 
 constexpr int kRowsPerCta = 32;    // most query rows a CTA of the few-rows kernel holds
 constexpr int kTileCtas = 192;     // most CTAs of the many-rows kernel
 constexpr int kTileRows = 256;     // most query rows a CTA of the many-rows kernel holds
-constexpr int kTileRing = 8;       // most raw records per tensor that it has in flight
+constexpr int kTileAhead = 4;      // most units of codes that a warp of it copies ahead
 
 struct PagesLayout {
   int k_bits, v_bits;
@@ -94,7 +94,7 @@ struct AttnArgs {
   int q_bf16;        // type of q and out: 0 fp16, 1 bf16
   int q_aligned;     // rows of q may be read 16 bytes at a time
   int rows_lo, rows_hi;  // sequences with rows_lo < n * rep <= rows_hi are this launch's
-  int ring;          // raw records per tensor in flight (many rows over codes; 0 otherwise)
+  int ring;          // units that a warp copies ahead (many rows over codes; 0 otherwise)
   // the masked kernels: new tokens that a row sees (null: rows see every token of their sequence)
   const uint32_t* seen;
   int seen_words;    // 32-bit words a row
@@ -106,14 +106,15 @@ struct AttnArgs {
 };
 
 // An attention kernel: its dynamic shared memory (the batch's line of units comes
-// on top), threads, static shared memory and the CTAs per SM that its registers
-// allow.
+// on top), threads, the CTAs per SM that its registers allow, static shared memory,
+// and what a unit copied ahead takes on top (many rows over codes).
 struct AttnKernel {
   const void* fn;
   size_t smem;
   int threads;
   int reg_ctas;
   size_t static_smem;
+  int unit;
 };
 
 }  // namespace kvq

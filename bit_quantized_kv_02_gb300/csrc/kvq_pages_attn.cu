@@ -101,7 +101,7 @@ int resident(const kvq_pages* P, const AttnKernel& k, int batch) {
 // a CTA holds, `used`: the most that an item can have.
 cudaError_t launch_kernel(const AttnKernel& k, AttnArgs a, int ctas, int rows, int used, cudaStream_t st) {
   void* args[] = {&a};
-  cudaError_t e = launch_pdl(k.fn, dim3(ctas), dim3(k.threads), launch_smem(k, a.bv.batch) + (size_t)a.ring * a.pv.L.tile_bytes, st, args);
+  cudaError_t e = launch_pdl(k.fn, dim3(ctas), dim3(k.threads), launch_smem(k, a.bv.batch) + (size_t)a.ring * k.unit, st, args);
   if (e != cudaSuccess) return e;
   const int D = a.pv.head_dim;
   const void* join = D == 64 ? join_dim<64>(rows) : D == 128 ? join_dim<128>(rows) : join_dim<256>(rows);
@@ -127,11 +127,8 @@ cudaError_t launch_tile(kvq_pages* P, AttnArgs a, bool masked, int max_rows, cud
   a.min_units = 2;
   if (P->L.k_bits != 16) {
     const int left = P->max_smem - (int)(k.static_smem + launch_smem(k, a.bv.batch));
-    a.ring = std::min(left / P->L.tile_bytes, kTileRing);
-    // a multiple of the dequantizing warps of a tensor, where it reaches them
-    const int warps = P->cfg.head_dim == 256 ? 4 : 2;
-    if (a.ring >= warps) a.ring -= a.ring % warps;
-    if (a.ring < 2) return cudaErrorInvalidConfiguration;  // (not reached: two of the largest records fit)
+    a.ring = std::min(left / k.unit, kTileAhead);
+    if (a.ring < 1) return cudaErrorInvalidConfiguration;  // (not reached: one of the largest units fits)
   }
   return launch_kernel(k, a, std::min(P->sm_count, kTileCtas), a.pv.head_dim == 256 ? kTileRows / 2 : kTileRows,
                        max_rows, st);

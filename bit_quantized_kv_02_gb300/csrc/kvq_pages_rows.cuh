@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, RowsCfg<D, FMT, NM>::CTAS) pa
 template <int D, int FMT, bool MASK>
 AttnKernel rows_kernel_fmt(int nm) {
 #define KVQ_ROWS(n) \
-  if (nm == n) return {(const void*)pages_rows_kernel<D, FMT, n, MASK>, (size_t)RowsCfg<D, FMT, n>::SMEM, kRowsWarps * 32, 0, 0};
+  if (nm == n) return {(const void*)pages_rows_kernel<D, FMT, n, MASK>, (size_t)RowsCfg<D, FMT, n>::SMEM, kRowsWarps * 32, 0, 0, 0};
   if constexpr (D <= 128) {
     KVQ_ROWS(4)
     KVQ_ROWS(3)

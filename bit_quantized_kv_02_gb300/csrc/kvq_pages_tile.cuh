@@ -9,10 +9,9 @@
 //  - loader (16-bit pages): bulk copies of the records' halves into K and V
 //    stages; pages are stored in the operand layout, so no tensor map and no
 //    shuffling is needed;
-//  - raw loaders and dequantizers (codes): one warp per tensor copies records
-//    into a ring, a slot a lane; two warps per tensor (four with one row tile) turn
-//    whole records' codes into fp16 operand tiles (the value the page stands for, one
-//    rounding);
+//  - dequantizers (codes): two warps per tensor (four with one row tile) copy records
+//    ahead and turn their codes into fp16 operand tiles (the value the page stands for,
+//    one rounding);
 //  - one warp issues the matrix instructions: S = Q K^T (both from shared
 //    memory), O += P V (P from tensor memory, over the scores it came from);
 //  - softmax: a warpgroup per tile, a thread per row, so maxima and sums need
@@ -54,14 +53,17 @@ struct TileCfg {
   static constexpr int NS = D == 256 ? 1 : (D == 128 ? 2 : 3);  // K stages, V stages
   static constexpr int TILE = 128 * D * 2;         // bytes of a Q, K or V tile
   static constexpr int Q_OFF = 0, K_OFF = NT * TILE, V_OFF = K_OFF + NS * TILE;
-  // over codes, rings of raw records come behind the tiles, as deep as the 227 KB
-  // of a CTA allow (a.ring records per tensor)
+  // over codes, what the dequantizing warps copied ahead comes behind the tiles, as many
+  // units a warp (a.ring) as the 227 KB of a CTA allow
+  static constexpr int TURN = D == 64 ? 1 : 2;  // runs (32 lanes x 32 channels) of a unit
+  static constexpr __host__ __device__ int unit_bytes(int bits) { return TURN * 32 * (4 * bits + 4); }
   static constexpr int RAW_OFF = V_OFF + NS * TILE;
   static constexpr int SMEM = RAW_OFF + 1024;  // + alignment of the tiles
   static constexpr int PROD = F::kQuant ? (NT == 1 ? 8 : 4) : 0;  // dequantizing warps, half for each tensor
   static constexpr int THREADS = F::kQuant ? 512 : 384;
   static constexpr int PIECES = 4;
-  static constexpr int USERS = 4 * NT + 1 + (F::kQuant ? 2 + PROD : 1);  // warps that read a piece
+  static constexpr int COPIES = F::kQuant ? PROD / 2 * (unit_bytes(F::KB) + unit_bytes(F::VB)) : 0;  // bytes of a unit of every warp
+  static constexpr int USERS = 4 * NT + 1 + (F::kQuant ? PROD : 1);  // warps that read a piece
 };
 
 template <int D, int FMT>
@@ -71,7 +73,6 @@ struct TileShared {
   Piece piece[C::PIECES];
   uint64_t k_full[C::NS], k_empty[C::NS], v_full[C::NS], v_empty[C::NS];
   uint64_t q_full, q_free, s_full[2], p_full[2], o_done[2], v_land;
-  uint64_t raw_full[2][kTileRing], raw_free[2][kTileRing];
   uint64_t piece_full[C::PIECES], piece_free[C::PIECES];
   uint32_t tmem;
   int dead;
@@ -193,187 +194,151 @@ __device__ __forceinline__ void tile_loader(const AttnArgs& a, TileShared<D, FMT
 
 // ------------------------------------------------------------- dequantizer --
 
-// Brings the records of one tensor (codes and metadata are neighbours) into a
-// ring of raw records, ahead of the warps that turn them.  Lane i has slot i of the
-// ring: it waits for its slot alone and brings every a.ring-th record, so a copy costs
-// no other copy's wait or issue (one lane for all records: 830 cycles a record, which
-// bounded the kernel).
-template <int D, int FMT>
-__device__ __forceinline__ void raw_loader(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int value, int lane) {
+// Codes of keys (value 0) or values (1) of all pieces into operand tiles.  A warp turns
+// whole records, every WARPS-th; a lane turns runs of 32 channels of one token into four
+// 16-byte chunks of the tile.  What a lane turns it copies itself, some units (one or two
+// runs and their metadata) ahead, into places in shared memory that no other lane reads:
+// its copies ask for no barrier and no fence, and it waits for its own oldest one alone.
+// (Records brought by bulk copies into a ring that two loader warps filled: 125 drafted
+// tokens at 130900, 16 over 2 heads of 256, 372 us; a record's place, given back and
+// filled again, cost more than turning it.)  Keys and values share the code where their
+// bits do, and a turn is one unit: with the many roles of this kernel its hot code is
+// what the instruction cache holds.  tid: thread among those of the tensor.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+// All of this thread's groups but the last n (0 .. 3) have landed.
+__device__ __forceinline__ void copy_wait(int n) {
+  if (n == 3) asm volatile("cp.async.wait_group 3;\n" ::: "memory");
+  else if (n == 2) asm volatile("cp.async.wait_group 2;\n" ::: "memory");
+  else if (n == 1) asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+}
+
+template <int D, int FMT, int BITS>
+__device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int value, int tid) {
   using C = TileCfg<D, FMT>;
+  constexpr int WARPS = C::PROD / 2, PPT = D / 32, ROWS = 32 / PPT;  // rows of a run of the warp
+  constexpr int RUNS = 16 / ROWS, TURN = C::TURN;                    // runs of a record, of a unit
+  constexpr int WC = BITS / 4;                                       // words of a chunk of 8 channels
+  constexpr int UNITS = RUNS / TURN, PER = C::BK / 16 / WARPS;       // units of a record, a warp's records of a block
+  const int lane = tid & 31, warp = tid >> 5, piece = lane % PPT, row = lane / PPT;
   const PagesLayout& L = a.pv.L;
-  const int from = value ? L.v_off : 0, bytes = value ? L.tile_bytes - L.v_off : L.v_off;
-  const uint32_t slot_at = smem + C::RAW_OFF + (value ? a.ring * L.v_off : 0) + lane * bytes;
-  const uint32_t free_bar = smem_u32(&sh->raw_free[value][lane & 7]), full_bar = smem_u32(&sh->raw_full[value][lane & 7]);
-  int r = 0;    // slot of the piece's first record
-  int par = 0;  // the lane's slot: phase of its next use
+  const int lg = value ? L.v_lg : L.k_lg, meta_run = ROWS * (D >> lg) * 4;
+  const int codes_at = (value ? L.v_off : 0) + row * (D * BITS / 8) + piece * (4 * BITS);
+  const int meta_at = (value ? L.vm_off : L.km_off) + (row * (D >> lg) + ((piece * 32) >> lg)) * 4;
+  uint64_t* const empty = value ? sh->v_empty : sh->k_empty;
+  uint64_t* const ready = value ? sh->v_full : sh->k_full;
+  const uint32_t tiles = smem + (value ? C::V_OFF : C::K_OFF) + (piece >> 1) * (128 * 128);
+  // the lane's places: [unit in flight][run][16 bytes, WC of them], then the metadata
+  constexpr int UNIT = C::unit_bytes(BITS);
+  const uint32_t mine = smem + C::RAW_OFF + (value ? WARPS * a.ring * C::unit_bytes(C::F::KB) : 0) + warp * a.ring * UNIT;
+  const uint32_t my_codes = mine + lane * 16, my_meta = mine + TURN * WC * 512 + lane * 4;
+  // lanes of other column blocks store their four chunks in another order, so
+  // that the 8 lanes of a phase touch 8 different groups of banks
+  const int turn = D == 64 ? 0 : (D == 128 ? 2 * (piece >> 1) : piece >> 1);
+  int st = 0, par = 0;
   for (int k = 0;; ++k) {
     const int slot = k % C::PIECES;
     if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) return;
     const Piece p = sh->piece[slot];
     if (p.nblk == 0) return;
     const PageRun run(a.pv, p.head);
-    const int tok0 = p.blk * C::BK, n = (min(tok0 + p.nblk * C::BK, p.s.len) - tok0 + 15) >> 4;  // records (none: <= 0)
-    int i = lane < a.ring ? (lane >= r ? lane - r : lane - r + a.ring) : n;  // the lane's next record
-    auto page_of = [&](int i) { return i < n ? page_index(a, p.b, tok0 + 16 * i) : 0; };
-    int page = page_of(i), next = page_of(i + a.ring);
-    unsigned long long since = 0;  // when the lane's wait was first seen to last
-    for (int turns = 1; __any_sync(0xffffffffu, i < n); ++turns) {
-      const bool go = i < n && mbar_test(free_bar, par ^ 1);
-      if (go) {
-        mbar_expect(full_bar, bytes);
-        bulk_load(slot_at, run.at(a, page, tok0 + 16 * i) + from, bytes, full_bar);
-        par ^= 1;
-        i += a.ring;
-        page = next;
-        next = page_of(i + a.ring);
-        since = 0;
-      }
-      if (!__any_sync(0xffffffffu, go)) __nanosleep(40);
-      if ((turns & 255) == 0) {  // the limit of this wait, and the end of another's
-        bool late = *(volatile int*)&sh->dead;
-        if (i < n && !late) {
-          const unsigned long long now = time_ns();
-          if (since == 0) since = now;
-          if (now - since > kWaitNs) {
-            *(volatile int*)&sh->dead = 1;
-            atomicOr(a.pv.err, 2);
-            late = true;
-          }
+    const int all = p.nblk * (PER * UNITS);
+    // Unit u is part u % UNITS of the warp's record u / UNITS, 16 * WARPS tokens from the
+    // one before.  A record's page is read while the one before is copied.
+    int tok = p.blk * C::BK + warp * 16, part = 0, put = 0;  // of the next unit to be copied; its place
+    const int end = min((p.blk + p.nblk) * C::BK, p.s.len);
+    int page = tok < end ? page_index(a, p.b, tok) : 0;
+    const char* src = nullptr;
+    auto bring = [&]() {
+      if (tok < end) {
+        if (part == 0) {
+          src = run.at(a, page, tok);
+          if (tok + 16 * WARPS < end) page = page_index(a, p.b, tok + 16 * WARPS);
         }
-        if (__any_sync(0xffffffffu, late)) return;
-      }
-    }
-    r = (int)((unsigned)(r + max(n, 0)) % (unsigned)a.ring);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sh->piece_free[slot]));
-  }
-}
-
-// Keys (value 0) or values (1) of all pieces: a warp turns whole records, those of its
-// places in the ring (a place has one warp, whose waits then follow its phases one by
-// one: the ring is a multiple of the warps, or some have no place); a lane turns runs of
-// 32 channels of one token into four 16-byte chunks of the operand tile.  A record is
-// waited for, fenced and given back once, by one warp.  Keys and values share the code
-// where their bits do, and a turn is two runs: with the many roles of this kernel its
-// hot code is what the instruction cache holds (four runs a turn and a copy for each
-// tensor: 8 prompts of up to 448 tokens over 8190 8-bit tokens, 32 over 8 heads of 128,
-// 484 us).  tid: thread among those of the tensor.
-template <int D, int FMT, int BITS>
-__device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int value, int tid) {
-  using C = TileCfg<D, FMT>;
-  constexpr int WARPS = C::PROD / 2, PPT = D / 32, ROWS = 32 / PPT;  // rows of a run of the warp
-  constexpr int RUNS = 16 / ROWS, TURN = RUNS < 2 ? 1 : 2;           // runs of a record, of a turn
-  constexpr int WC = BITS / 4;                                       // words of a chunk of 8 channels
-  const int with = min(WARPS, a.ring);  // warps that have places
-  const int lane = tid & 31, warp = tid >> 5, piece = lane % PPT, row = lane / PPT;
-  const PagesLayout& L = a.pv.L;
-  const int meta = value ? L.vm_off - L.v_off : L.km_off, lg = value ? L.v_lg : L.k_lg;
-  const uint32_t raw = smem + C::RAW_OFF + (value ? a.ring * L.v_off : 0);
-  const int raw_bytes = value ? L.tile_bytes - L.v_off : L.v_off;
-  const uint32_t codes_at = row * (D * BITS / 8) + piece * (4 * BITS);
-  const uint32_t meta_at = meta + (row * (D >> lg) + ((piece * 32) >> lg)) * 4, meta_run = ROWS * (D >> lg) * 4;
-  uint64_t* const empty = value ? sh->v_empty : sh->k_empty;
-  uint64_t* const ready = value ? sh->v_full : sh->k_full;
-  uint64_t* const full = sh->raw_full[value];
-  uint64_t* const unused = sh->raw_free[value];
-  const uint32_t tiles = smem + (value ? C::V_OFF : C::K_OFF) + (piece >> 1) * (128 * 128);
-  // lanes of other column blocks store their four chunks in another order, so
-  // that the 8 lanes of a phase touch 8 different groups of banks
-  const int turn = D == 64 ? 0 : (D == 128 ? 2 * (piece >> 1) : piece >> 1);
-  int st = 0, par = 0;
-  int r = 0, rpar = 0;  // slot of the block's first record, its phase
-  for (int k = 0;; ++k) {
-    const int slot = k % C::PIECES;
-    if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) return;
-    const int nblk = sh->piece[slot].nblk, len = sh->piece[slot].s.len;
-    if (nblk == 0) return;
-    int tok = sh->piece[slot].blk * C::BK;
-#pragma unroll 1
-    for (int j = 0; j < nblk; ++j, tok += C::BK) {
-      const int n = max(min((len - tok + 15) >> 4, C::BK / 16), 0);  // records that arrive
-      int c = warp - r % with;                                       // the warp's first record of the block
-      if (c < 0) c += with;
-      if (warp >= with) c = C::BK / 16;
-      int s = r + c, spar = rpar;
-      while (s >= a.ring) s -= a.ring, spar ^= 1;
-      if (!tile_wait_warp(sh, a, &empty[st], par ^ 1)) return;
-      const uint32_t tile = tiles + st * C::TILE;
-#pragma unroll 1
-      for (; c < C::BK / 16; c += with) {
-        if (c < n && !tile_wait_warp(sh, a, &full[s], spar)) return;
-        const uint32_t from = raw + s * raw_bytes;
-#pragma unroll 1
-        for (int y0 = 0; y0 < RUNS; y0 += TURN) {
-          // Codes and metadata.  Rows behind the sequence's end become zero (zero + code *
-          // step = 0), whatever the page holds there; records behind it do not arrive.
-          uint32_t w[TURN][4 * WC], zs[TURN];
+        const uint32_t to = put * UNIT;
+        const char* codes = src + codes_at + part * (TURN * ROWS * D * BITS / 8);
+        const char* meta = src + meta_at + part * TURN * meta_run;
 #pragma unroll
-          for (int y = 0; y < TURN; ++y) {
-            if (c < n) {
-              ldsv<4 * WC>(from + codes_at + (y0 + y) * (ROWS * D * BITS / 8), w[y]);
-              zs[y] = lds32(from + meta_at + (y0 + y) * meta_run);
+        for (int y = 0; y < TURN; ++y) {
+#pragma unroll
+          for (int e = 0; e < WC; ++e) copy_async16(my_codes + to + (y * WC + e) * 512, codes + y * (ROWS * D * BITS / 8) + e * 16);
+          copy_async4(my_meta + to + y * 128, meta + y * meta_run);
+        }
+      }
+      copy_commit();  // (a group a unit, empty ones included)
+      if (++part == UNITS) part = 0, tok += 16 * WARPS;
+      if (++put == a.ring) put = 0;
+    };
+    int get = 0;
+#pragma unroll 1
+    for (int u = -a.ring; u < all; ++u) {
+      if (u >= 0) {  // (the first rounds only copy)
+        if (u % (PER * UNITS) == 0 && !tile_wait_warp(sh, a, &empty[st], par ^ 1)) return;
+        copy_wait(a.ring - 1);
+        uint32_t w[TURN][4 * WC], zs[TURN];
+#pragma unroll
+        for (int y = 0; y < TURN; ++y) {
+#pragma unroll
+          for (int e = 0; e < WC; ++e) ldsv<4>(my_codes + get * UNIT + (y * WC + e) * 512, w[y] + 4 * e);
+          zs[y] = lds32(my_meta + get * UNIT + y * 128);
+        }
+        if (++get == a.ring) get = 0;
+        // row of the block's tile; rows behind the sequence's end become zero (zero + code *
+        // step = 0), whatever the page, or the place of a record that was not brought, holds
+        const int v = u % (PER * UNITS), at0 = (v / UNITS * WARPS + warp) * 16 + v % UNITS * (TURN * ROWS) + row;
+        const int left = p.s.len - (p.blk + u / (PER * UNITS)) * C::BK;
+        const uint32_t tile = tiles + st * C::TILE;
+#pragma unroll
+        for (int y = 0; y < TURN; ++y) {
+          uint32_t* x = w[y];
+          const int at_row = at0 + y * ROWS;
+          if (at_row >= left) zs[y] = 0;
+          const __half2 z = __low2half2(as_h2(zs[y])), sc = __high2half2(as_h2(zs[y]));
+#pragma unroll
+          for (int b = 1; b < 4; b <<= 1)  // the words of chunk i to place i ^ turn
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!(i & b))
+#pragma unroll
+                for (int e = 0; e < WC; ++e) {
+                  const uint32_t lo = x[WC * i + e], hi = x[WC * (i ^ b) + e];
+                  x[WC * i + e] = (turn & b) ? hi : lo;
+                  x[WC * (i ^ b) + e] = (turn & b) ? lo : hi;
+                }
+          const uint32_t out = tile + at_row * 128;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o[4];
+            if constexpr (BITS == 8) {
+              o[0] = bytes<0>(x[2 * i], sc, z);
+              o[1] = bytes<1>(x[2 * i], sc, z);
+              o[2] = bytes<0>(x[2 * i + 1], sc, z);
+              o[3] = bytes<1>(x[2 * i + 1], sc, z);
             } else {
-#pragma unroll
-              for (int e = 0; e < 4 * WC; ++e) w[y][e] = 0;
+              o[0] = nibbles<0>(x[i], sc, z);
+              o[1] = nibbles<1>(x[i], sc, z);
+              o[2] = nibbles<2>(x[i], sc, z);
+              o[3] = nibbles<3>(x[i], sc, z);
             }
-          }
-          // The record goes back: the fence orders each lane's loads before the bulk copy
-          // into the same bytes, which goes another way (without it a copy overtook loads
-          // that waited behind the matrix operands), the warp's barrier the lanes before
-          // the arrival.
-          if (y0 + TURN == RUNS) {
-            fence_async();
-            __syncwarp();
-            if (lane == 0 && c < n) mbar_arrive(smem_u32(&unused[s]));
-          }
-#pragma unroll
-          for (int y = 0; y < TURN; ++y) {
-            uint32_t* v = w[y];
-            const int at_row = c * 16 + (y0 + y) * ROWS + row;
-            if (tok + at_row >= len) zs[y] = 0;
-            const __half2 z = __low2half2(as_h2(zs[y])), sc = __high2half2(as_h2(zs[y]));
-#pragma unroll
-            for (int b = 1; b < 4; b <<= 1)  // the words of chunk i to place i ^ turn
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (!(i & b))
-#pragma unroll
-                  for (int e = 0; e < WC; ++e) {
-                    const uint32_t lo = v[WC * i + e], hi = v[WC * (i ^ b) + e];
-                    v[WC * i + e] = (turn & b) ? hi : lo;
-                    v[WC * (i ^ b) + e] = (turn & b) ? lo : hi;
-                  }
-            const uint32_t out = tile + at_row * 128;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t o[4];
-              if constexpr (BITS == 8) {
-                o[0] = bytes<0>(v[2 * i], sc, z);
-                o[1] = bytes<1>(v[2 * i], sc, z);
-                o[2] = bytes<0>(v[2 * i + 1], sc, z);
-                o[3] = bytes<1>(v[2 * i + 1], sc, z);
-              } else {
-                o[0] = nibbles<0>(v[i], sc, z);
-                o[1] = nibbles<1>(v[i], sc, z);
-                o[2] = nibbles<2>(v[i], sc, z);
-                o[3] = nibbles<3>(v[i], sc, z);
-              }
-              const int at = (4 * (piece & 1) + (i ^ turn)) ^ (at_row & 7);
-              asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(out + (at << 4)), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                           : "memory");
-            }
+            const int at = (4 * (piece & 1) + (i ^ turn)) ^ (at_row & 7);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(out + (at << 4)), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                         : "memory");
           }
         }
-        s += with;
-        while (s >= a.ring) s -= a.ring, spar ^= 1;
       }
-      r += n;
-      while (r >= a.ring) r -= a.ring, rpar ^= 1;
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ready[st]));
-      if (++st == C::NS) st = 0, par ^= 1;
+      bring();  // (into the place that was read: its values have been used)
+      if (u >= 0 && (u + 1) % (PER * UNITS) == 0) {
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ready[st]));
+        if (++st == C::NS) st = 0, par ^= 1;
+      }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh->piece_free[slot]));
@@ -796,16 +761,11 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
       mbar_init(smem_u32(&sh.piece_full[i]), 1);
       mbar_init(smem_u32(&sh.piece_free[i]), C::USERS);
     }
-    for (int i = 0; i < kTileRing; ++i)
-      for (int t = 0; t < 2; ++t) {
-        mbar_init(smem_u32(&sh.raw_full[t][i]), 1);
-        mbar_init(smem_u32(&sh.raw_free[t][i]), 1);
-      }
     sh.dead = 0;
     fence_mbar_init();
   }
   pdl_wait();
-  plan_work<C::BK, C::ROWS, false, MASK>(a, &sh.work, reinterpret_cast<long*>(raw + C::SMEM + a.ring * a.pv.L.tile_bytes));  // (its barriers also publish the initialisation above)
+  plan_work<C::BK, C::ROWS, false, MASK>(a, &sh.work, reinterpret_cast<long*>(raw + C::SMEM + a.ring * C::COPIES));  // (its barriers also publish the initialisation above)
   pdl_trigger();
   if (threadIdx.x == 0) a.split[blockIdx.x].parts = 0;
   if ((int)blockIdx.x >= sh.work.ctas) return;
@@ -850,9 +810,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
         __syncwarp();
         if (p.nblk == 0) break;
       }
-    } else if constexpr (F::kQuant) {
-      raw_loader<D, FMT>(a, &sh, smem, warp == 11, lane);  // (9: keys)
-    } else if (warp == 9) {
+    } else if (!F::kQuant && warp == 9) {
       tile_loader<D, FMT>(a, &sh, smem, lane);
     }
   } else if constexpr (F::kQuant) {
@@ -876,7 +834,7 @@ template <int D, bool MASK>
 AttnKernel tile_kernel_dim(int fmt) {
   switch (fmt) {
 #define KVQ_TILE(f) \
-  case f: return {(const void*)pages_tile_kernel<D, f, MASK>, (size_t)TileCfg<D, f>::SMEM, TileCfg<D, f>::THREADS, 0, 0};
+  case f: return {(const void*)pages_tile_kernel<D, f, MASK>, (size_t)TileCfg<D, f>::SMEM, TileCfg<D, f>::THREADS, 0, 0, TileCfg<D, f>::COPIES};
     KVQ_TILE(kFmtF16)
     KVQ_TILE(kFmtBf16)
     KVQ_TILE(kFmt88)

@@ -51,6 +51,10 @@ struct TileCfg {
   static constexpr int ROWS = 128 * NT;
   static constexpr int BK = 128;                   // tokens of a block
   static constexpr int NS = D == 256 ? 1 : (D == 128 ? 2 : 3);  // K stages, V stages
+  // Where only one stage fits it is handed over by halves: the next block's first half is
+  // made while the products take the second.
+  static constexpr int PT = D == 256 ? 64 : 128;   // tokens of a part of a stage
+  static constexpr int SP = NS * (BK / PT);        // parts of the stages
   static constexpr int TILE = 128 * D * 2;         // bytes of a Q, K or V tile
   static constexpr int Q_OFF = 0, K_OFF = NT * TILE, V_OFF = K_OFF + NS * TILE;
   // over codes, what the dequantizing warps copied ahead comes behind the tiles, as many
@@ -71,7 +75,7 @@ struct TileShared {
   using C = TileCfg<D, FMT>;
   Work<C::BK, C::ROWS> work;
   Piece piece[C::PIECES];
-  uint64_t k_full[C::NS], k_empty[C::NS], v_full[C::NS], v_empty[C::NS];
+  uint64_t k_full[C::SP], k_empty[C::SP], v_full[C::SP], v_empty[C::SP];
   uint64_t q_full, q_free, s_full[2], p_full[2], o_done[2], v_land;
   uint64_t piece_full[C::PIECES], piece_free[C::PIECES];
   uint32_t tmem;
@@ -133,60 +137,65 @@ template <int D, int FMT>
 __device__ __forceinline__ void tile_loader(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int lane) {
   using C = TileCfg<D, FMT>;
   constexpr int CB = D / 64;
-  long c = 0;  // blocks so far
-  bool ok = true;
+  constexpr int HALVES = C::BK / C::PT;
+  int st = 0, par = 0;  // first part of the block's stage, its phase
   int land = 0;
-  for (int k = 0; ok; ++k) {
+  for (int k = 0;; ++k) {
     const int slot = k % C::PIECES;
-    if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) break;
+    if (!tile_wait_warp(sh, a, &sh->piece_full[slot], (k / C::PIECES) & 1)) return;
     const Piece p = sh->piece[slot];
-    if (p.nblk == 0) break;
+    if (p.nblk == 0) return;
     const PageRun run(a.pv, p.head);
-    for (int j = 0; j < p.nblk; ++j, ++c) {
-      const int st = (int)(c % C::NS), par = (int)((c / C::NS) & 1);
-      const int tok0 = (p.blk + j) * C::BK;
-      const int nt = max(min((p.s.len - tok0 + 15) >> 4, 8), 0);  // records with a token of the sequence
+    for (int j = 0; j < p.nblk; ++j) {
       // lane -> (record, block of 64 columns); head_dim 64 uses 8 lanes, 128 16, 256 all
-      const int rec = lane / CB, cb = lane % CB;
+      const int rec = lane / CB, cb = lane % CB, blk0 = (p.blk + j) * C::BK;
       const char* src = nullptr;
-      if (rec < nt) {
-        const int tok = tok0 + 16 * rec;
+      if (rec < C::BK / 16 && blk0 + 16 * rec < p.s.len) {
+        const int tok = blk0 + 16 * rec;
         src = run.at(a, page_index(a, p.b, tok), tok) + cb * 2048;
       }
-      const uint32_t dst = cb * (C::BK * 128) + rec * 2048;
-      ok = tile_wait_warp(sh, a, &sh->k_empty[st], par ^ 1);
-      if (!ok) break;
-      const uint32_t kb = smem_u32(&sh->k_full[st]);
-      if (lane == 0) mbar_expect(kb, nt * CB * 2048);
-      __syncwarp();
-      if (src) bulk_load(smem + C::K_OFF + st * C::TILE + dst, src, 2048, kb);
-      ok = tile_wait_warp(sh, a, &sh->v_empty[st], par ^ 1);
-      if (!ok) break;
-      const uint32_t vt = smem + C::V_OFF + st * C::TILE, vb = smem_u32(&sh->v_full[st]);
-      if (tok0 + C::BK <= p.s.len) {
-        if (lane == 0) mbar_expect(vb, nt * CB * 2048);
+      const uint32_t stage = smem + st / HALVES * C::TILE, dst = cb * (C::BK * 128) + rec * 2048;
+      // Keys, all parts of the block, before values: the products of the next block's
+      // scores come before those of this one's values.
+      for (int h = 0; h < HALVES; ++h) {
+        const int tok0 = blk0 + h * C::PT, nt = max(min((p.s.len - tok0 + 15) >> 4, C::PT / 16), 0);  // records with a token of the sequence
+        const bool mine = src && (HALVES == 1 || rec / (C::PT / 16) == h);
+        if (!tile_wait_warp(sh, a, &sh->k_empty[st + h], par ^ 1)) return;
+        const uint32_t kb = smem_u32(&sh->k_full[st + h]);
+        if (lane == 0) mbar_expect(kb, nt * CB * 2048);
         __syncwarp();
-        if (src) bulk_load(vt + dst, src + a.pv.L.v_off, 2048, vb);
-      } else {
-        // the sequence ends in this block: the rows behind it are cleared (their weights are zero, their contents anything)
-        const uint32_t lb = smem_u32(&sh->v_land);
-        if (lane == 0) mbar_expect(lb, nt * CB * 2048);
-        __syncwarp();
-        if (src) bulk_load(vt + dst, src + a.pv.L.v_off, 2048, lb);
-        ok = tile_wait_warp(sh, a, &sh->v_land, land & 1);
-        ++land;
-        if (!ok) break;
-        const int n = max(p.s.len - tok0, 0);
-        for (int i = lane; i < (C::BK - n) * (D / 8); i += 32) {
-          const int r = n + i / (D / 8), ch = i % (D / 8);
-          asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(vt + (ch >> 3) * (C::BK * 128) + r * 128 + ((ch & 7) << 4)),
-                       "r"(0)
-                       : "memory");
-        }
-        fence_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(vb);
+        if (mine) bulk_load(stage + C::K_OFF + dst, src, 2048, kb);
       }
+      for (int h = 0; h < HALVES; ++h) {
+        const int tok0 = blk0 + h * C::PT, nt = max(min((p.s.len - tok0 + 15) >> 4, C::PT / 16), 0);
+        const bool mine = src && (HALVES == 1 || rec / (C::PT / 16) == h);
+        if (!tile_wait_warp(sh, a, &sh->v_empty[st + h], par ^ 1)) return;
+        const uint32_t vt = stage + C::V_OFF, vb = smem_u32(&sh->v_full[st + h]);
+        if (tok0 + C::PT <= p.s.len) {
+          if (lane == 0) mbar_expect(vb, nt * CB * 2048);
+          __syncwarp();
+          if (mine) bulk_load(vt + dst, src + a.pv.L.v_off, 2048, vb);
+        } else {
+          // the sequence ends in this part: the rows behind it are cleared (their weights are zero, their contents anything)
+          const uint32_t lb = smem_u32(&sh->v_land);
+          if (lane == 0) mbar_expect(lb, nt * CB * 2048);
+          __syncwarp();
+          if (mine) bulk_load(vt + dst, src + a.pv.L.v_off, 2048, lb);
+          if (!tile_wait_warp(sh, a, &sh->v_land, land & 1)) return;
+          ++land;
+          const int n = max(p.s.len - tok0, 0);
+          for (int i = lane; i < (C::PT - n) * (D / 8); i += 32) {
+            const int r = h * C::PT + n + i / (D / 8), ch = i % (D / 8);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(vt + (ch >> 3) * (C::BK * 128) + r * 128 + ((ch & 7) << 4)),
+                         "r"(0)
+                         : "memory");
+          }
+          fence_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(vb);
+        }
+      }
+      if ((st += HALVES) == C::SP) st = 0, par ^= 1;
     }
     if (lane == 0) mbar_arrive(smem_u32(&sh->piece_free[slot]));
   }
@@ -225,7 +234,7 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
   constexpr int WARPS = C::PROD / 2, PPT = D / 32, ROWS = 32 / PPT;  // rows of a run of the warp
   constexpr int RUNS = 16 / ROWS, TURN = C::TURN;                    // runs of a record, of a unit
   constexpr int WC = BITS / 4;                                       // words of a chunk of 8 channels
-  constexpr int UNITS = RUNS / TURN, PER = C::BK / 16 / WARPS;       // units of a record, a warp's records of a block
+  constexpr int UNITS = RUNS / TURN, PER = C::PT / 16 / WARPS;       // units of a record, a warp's records of a part
   const int lane = tid & 31, warp = tid >> 5, piece = lane % PPT, row = lane / PPT;
   const PagesLayout& L = a.pv.L;
   const int lg = value ? L.v_lg : L.k_lg, meta_run = ROWS * (D >> lg) * 4;
@@ -248,7 +257,7 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
     const Piece p = sh->piece[slot];
     if (p.nblk == 0) return;
     const PageRun run(a.pv, p.head);
-    const int all = p.nblk * (PER * UNITS);
+    const int all = p.nblk * (C::BK / C::PT) * (PER * UNITS);
     // Unit u is part u % UNITS of the warp's record u / UNITS, 16 * WARPS tokens from the
     // one before.  A record's page is read while the one before is copied.
     int tok = p.blk * C::BK + warp * 16, part = 0, put = 0;  // of the next unit to be copied; its place
@@ -289,11 +298,11 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
           zs[y] = lds32(my_meta + get * UNIT + y * 128);
         }
         if (++get == a.ring) get = 0;
-        // row of the block's tile; rows behind the sequence's end become zero (zero + code *
+        // row of the part's tile; rows behind the sequence's end become zero (zero + code *
         // step = 0), whatever the page, or the place of a record that was not brought, holds
         const int v = u % (PER * UNITS), at0 = (v / UNITS * WARPS + warp) * 16 + v % UNITS * (TURN * ROWS) + row;
-        const int left = p.s.len - (p.blk + u / (PER * UNITS)) * C::BK;
-        const uint32_t tile = tiles + st * C::TILE;
+        const int left = p.s.len - p.blk * C::BK - u / (PER * UNITS) * C::PT;
+        const uint32_t tile = tiles + st / (C::BK / C::PT) * C::TILE + st % (C::BK / C::PT) * (C::PT * 128);
 #pragma unroll
         for (int y = 0; y < TURN; ++y) {
           uint32_t* x = w[y];
@@ -337,7 +346,7 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
         fence_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ready[st]));
-        if (++st == C::NS) st = 0, par ^= 1;
+        if (++st == C::SP) st = 0, par ^= 1;
       }
     }
     __syncwarp();
@@ -359,37 +368,41 @@ __device__ __forceinline__ void tile_dequantize(const AttnArgs& a, TileShared<D,
 template <int D, int FMT, bool MASK>
 __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem) {
   using C = TileCfg<D, FMT>;
-  constexpr uint32_t S_DESC = mma_desc(128, C::BK, C::F::kBf16, false);
+  constexpr uint32_t S_DESC = mma_desc(128, C::PT, C::F::kBf16, false);
   constexpr uint32_t O_DESC = mma_desc(128, D, C::F::kBf16, true);
   const uint32_t tm = __shfl_sync(0xffffffffu, sh->tmem, 0);
   const uint64_t q0 = smem_desc(smem + C::Q_OFF, 16, 1024), k0 = smem_desc(smem + C::K_OFF, 16, 1024);
   const uint64_t v0 = smem_desc(smem + C::V_OFF, C::BK * 128, 1024);
-  int ks = 0, kpar = 0, vs = 0, vpar = 0;  // stage to read next, its phase
+  int ks = 0, kpar = 0, vs = 0, vpar = 0;  // part of the stages to read next, its phase
   int bc = 0;                              // score buffers handed out (one tile)
   int turns = 0;                           // phases of the weights (two tiles, a bit each)
-  // S of a tile with the keys of stage ks; O of a tile with the values of stage vs.
+  constexpr int HALVES = C::BK / C::PT;
+  // S of a tile with the keys of part ks; O of a tile with the values of part vs (`half`:
+  // which part of its block it is; the block is done with the last).
   // (Scoring the next block's first 64 keys into the columns that the weights leave
   // free, ahead of the value product, was slower: 995 us against 820 for a chunk of
   // 2048 at 32k tokens; products of 64 columns wait for shared memory.)
-  auto scores = [&](int buf, int tile) {
-    const uint64_t q = q0 + (uint64_t)(tile * (C::TILE >> 4)), k = k0 + (uint64_t)(ks * (C::TILE >> 4));
+  auto scores = [&](int buf, int tile, int half) {
+    const uint64_t q = q0 + (uint64_t)(tile * (C::TILE >> 4));
+    const uint64_t k = k0 + (uint64_t)((ks / HALVES * C::TILE + half * (C::PT * 128)) >> 4);
     if (elect_one()) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         const uint64_t at = ((i >> 2) * (128 * 128) + (i & 3) * 32) >> 4;
-        mma_ss(tm + buf * 128, q + at, k + at, S_DESC, i > 0);
+        mma_ss(tm + buf * 128 + half * C::PT, q + at, k + at, S_DESC, i > 0);
       }
-      mma_commit(smem_u32(&sh->s_full[buf]));
+      if (half == HALVES - 1) mma_commit(smem_u32(&sh->s_full[buf]));
     }
     __syncwarp();
   };
-  auto values = [&](int buf, int tile, int add) {
-    const uint64_t v = v0 + (uint64_t)(vs * (C::TILE >> 4));
+  auto values = [&](int buf, int tile, int half, int add) {
+    const uint64_t v = v0 + (uint64_t)((vs / HALVES * C::TILE + half * (C::PT * 128)) >> 4);
     if (elect_one()) {
 #pragma unroll
-      for (int i = 0; i < C::BK / 16; ++i)
-        mma_ts(tm + 256 + tile * D, tm + buf * 128 + i * 8, v + (uint64_t)(i * 2048 >> 4), O_DESC, i > 0 ? 1 : add);
-      mma_commit(smem_u32(&sh->o_done[tile]));
+      for (int i = 0; i < C::PT / 16; ++i)
+        mma_ts(tm + 256 + tile * D, tm + buf * 128 + half * (C::PT / 2) + i * 8, v + (uint64_t)(i * 2048 >> 4), O_DESC,
+               i > 0 ? 1 : add);
+      if (half == HALVES - 1) mma_commit(smem_u32(&sh->o_done[tile]));
     }
     __syncwarp();
   };
@@ -400,12 +413,12 @@ __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* 
       if (queries_too) mma_commit(smem_u32(&sh->q_free));
     }
     __syncwarp();
-    if (++ks == C::NS) ks = 0, kpar ^= 1;
+    if (++ks == C::SP) ks = 0, kpar ^= 1;
   };
   auto free_v = [&]() {
     if (elect_one()) mma_commit(smem_u32(&sh->v_empty[vs]));
     __syncwarp();
-    if (++vs == C::NS) vs = 0, vpar ^= 1;
+    if (++vs == C::SP) vs = 0, vpar ^= 1;
   };
   // (One loop from the block before a piece's first on, one copy of each product's code:
   // written out for both tiles and the first block the role was 20 KB long.)
@@ -435,14 +448,14 @@ __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* 
             if (!tile_wait_warp(sh, a, &sh->p_full[i], (turns >> i) & 1)) return;
             turns ^= 1 << i;
             tc_after_sync();
-            values(i, i, j > lo);
+            values(i, i, 0, j > lo);
           }
           if (i == 1 && j >= 0) free_v();
           if (j + 1 < n && j + 1 >= lo && j + 1 < hi) {
             if (!have_k && !tile_wait_warp(sh, a, &sh->k_full[ks], kpar)) return;
             have_k = true;
             tc_after_sync();
-            scores(i, i);
+            scores(i, i, 0);
           }
         }
         if (j + 1 < n) {
@@ -455,17 +468,23 @@ __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* 
       for (int j = -1; j < n; ++j) {
         const int buf = bc & 1;  // (the scores of block j)
         if (j + 1 < n) {
-          if (!tile_wait_warp(sh, a, &sh->k_full[ks], kpar)) return;
-          tc_after_sync();
-          scores(j < 0 ? buf : buf ^ 1, 0);
-          free_k(j + 2 == n);
+#pragma unroll 1
+          for (int h = 0; h < HALVES; ++h) {
+            if (!tile_wait_warp(sh, a, &sh->k_full[ks], kpar)) return;
+            tc_after_sync();
+            scores(j < 0 ? buf : buf ^ 1, 0, h);
+            free_k(h == HALVES - 1 && j + 2 == n);
+          }
         }
         if (j < 0) continue;
-        if (!tile_wait_warp(sh, a, &sh->v_full[vs], vpar)) return;
         if (!tile_wait_warp(sh, a, &sh->p_full[buf], (bc >> 1) & 1)) return;
-        tc_after_sync();
-        values(buf, 0, j > 0);
-        free_v();
+#pragma unroll 1
+        for (int h = 0; h < HALVES; ++h) {
+          if (!tile_wait_warp(sh, a, &sh->v_full[vs], vpar)) return;
+          tc_after_sync();
+          values(buf, 0, h, j > 0 || h > 0);
+          free_v();
+        }
         ++bc;
       }
     }
@@ -743,7 +762,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t smem = (smem_u32(raw) + 1023) & ~1023u;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::NS; ++i) {
+    for (int i = 0; i < C::SP; ++i) {
       mbar_init(smem_u32(&sh.k_full[i]), F::kQuant ? C::PROD / 2 : 1);
       mbar_init(smem_u32(&sh.v_full[i]), F::kQuant ? C::PROD / 2 : 1);
       mbar_init(smem_u32(&sh.k_empty[i]), 1);

@@ -184,11 +184,13 @@ cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, bool masked, int max_ro
   // 48 / 51, 61 / 53.  Codes cost the many-rows kernel its dequantizing warps: 4 bits, heads of 64: 128 rows
   // 138 / 159, 192 rows 204 / 189; heads of 128: 64 rows 91 / 99, 96 rows 125 / 103;
   // heads of 256: 48 rows 57 / 61, 64 rows 67 / 62.
-  // The masked kernels over codes were measured after the many-rows kernel had become
-  // faster (the causal ones keep the choice, and with it the rounding, that they had): 8
-  // sequences of 8192 tokens, few / many rows, us: 8 bits, 12 heads of 64: 48 rows 71 / 80,
-  // 64 rows 92 / 81; 8 heads of 128: 32 rows 62 / 72, 48 rows 79 / 73; 2 heads of 256: 16
-  // rows 40 / 48, 32 rows 53 / 51; 4 bits: 65 / 78, 79 / 79; 57 / 64, 70 / 65; 36 / 41, 50 / 44.
+  // The masked kernels were measured after the many-rows kernel had become faster (over
+  // codes the causal ones keep the choice, and with it the rounding, that they had).  8
+  // sequences of 8192 tokens, few / many rows, us: 16-bit pages, 12 heads of 64: 32 rows
+  // 53 / 58, 48 rows 104 / 58; 8 heads of 128: 60 / 63, 99 / 64; 2 heads of 256: 50 / 52,
+  // 64 / 53.  8 bits, heads of 64: 48 rows 71 / 72, 64 rows 89 / 73; heads of 128: 32 rows
+  // 62 / 66, 48 rows 79 / 67; heads of 256: 16 rows 40 / 44, 32 rows 53 / 47.  4 bits:
+  // 65 / 71, 81 / 72; 57 / 60, 70 / 61; 36 / 40, 50 / 42.
   const int D = P->cfg.head_dim;
   const int few = P->L.k_bits == 16 ? 32
                   : masked          ? (D == 64 ? 48 : (D == 128 ? 32 : 16))
@@ -197,6 +199,12 @@ cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, bool masked, int max_ro
   a.rows_hi = INT_MAX;
   if (P->which == 1 || (P->which == 0 && max_rows <= few)) return launch_rows(P, a, masked, max_rows, st);
   if (P->which == 2 || (a.bv.batch == 1 && (rows_given || P->L.k_bits != 16))) return launch_tile(P, a, masked, max_rows, st);
+  // Over codes the masked kernels take a mixed batch in one launch: the weights are
+  // rounded alike by both, the few-rows kernel would be its largest form, and its launch
+  // and join cost 10 us.  32 trees of 1 to 31 tokens over 500 to 8192 4-bit tokens, 32 over
+  // 8 heads of 128: 205 us with both, 202 with one (187 with three dequantizing warps a
+  // tensor).
+  if (masked && P->L.k_bits != 16) return launch_tile(P, a, masked, max_rows, st);
   a.rows_lo = few;
   cudaError_t e = launch_tile(P, a, masked, max_rows, st);
   if (e != cudaSuccess) return e;

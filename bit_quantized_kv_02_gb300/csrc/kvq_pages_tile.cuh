@@ -63,7 +63,7 @@ struct TileCfg {
   static constexpr __host__ __device__ int unit_bytes(int bits) { return TURN * 32 * (4 * bits + 4); }
   static constexpr int RAW_OFF = V_OFF + NS * TILE;
   static constexpr int SMEM = RAW_OFF + 1024;  // + alignment of the tiles
-  static constexpr int PROD = F::kQuant ? (NT == 1 ? 8 : 4) : 0;  // dequantizing warps, half for each tensor
+  static constexpr int PROD = F::kQuant ? (NT == 1 ? 8 : 6) : 0;  // dequantizing warps, half for each tensor
   static constexpr int THREADS = F::kQuant ? 512 : 384;
   static constexpr int PIECES = 4;
   static constexpr int COPIES = F::kQuant ? PROD / 2 * (unit_bytes(F::KB) + unit_bytes(F::VB)) : 0;  // bytes of a unit of every warp
@@ -78,6 +78,8 @@ struct TileShared {
   uint64_t k_full[C::SP], k_empty[C::SP], v_full[C::SP], v_empty[C::SP];
   uint64_t q_full, q_free, s_full[2], p_full[2], o_done[2], v_land;
   uint64_t piece_full[C::PIECES], piece_free[C::PIECES];
+  uint64_t met[4];         // warps of both tiles that hold the same rows
+  float2 stats[2][C::NT == 2 ? 128 : 1];  // maxima and sums that they exchange
   uint32_t tmem;
   int dead;
 };
@@ -110,6 +112,16 @@ struct RowMap {
     return (long)(t0 + t) * stride + (long)(head0 + rem + r - t * rep) * D;
   }
 };
+
+// Do the two row tiles share a piece's blocks between them, both holding its rows?  One
+// tile alone leaves the tensor cores to wait for its softmax: 8 trees of 64 tokens over
+// 8192, 16-bit pages, 12 heads of 64 88 -> 59 us, 16 tokens, 32 over 8 heads of 128 72 ->
+// 66.  Over codes the dequantizing warps bound both forms (71 us and 68).  (Masked kernels
+// only: the causal ones keep their order of sums.)
+template <int D, int FMT, bool MASK>
+__device__ __forceinline__ bool shared_rows(int rows) {
+  return MASK && TileCfg<D, FMT>::NT == 2 && !Fmt<FMT>::kQuant && rows <= 128;
+}
 
 // Blocks [lo, hi) of a piece that a row tile sees any token of.  (One tile: all
 // of them, the double-buffered scores count on it.  MASK: all of them too, the rows
@@ -212,7 +224,7 @@ __device__ __forceinline__ void tile_loader(const AttnArgs& a, TileShared<D, FMT
 // tokens at 130900, 16 over 2 heads of 256, 372 us; a record's place, given back and
 // filled again, cost more than turning it.)  Keys and values share the code where their
 // bits do, and a turn is one unit: with the many roles of this kernel its hot code is
-// what the instruction cache holds.  tid: thread among those of the tensor.
+// what the instruction cache holds.  warp: among those of the tensor.
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
 }
@@ -229,13 +241,14 @@ __device__ __forceinline__ void copy_wait(int n) {
 }
 
 template <int D, int FMT, int BITS>
-__device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int value, int tid) {
+__device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int value, int warp, int lane) {
   using C = TileCfg<D, FMT>;
   constexpr int WARPS = C::PROD / 2, PPT = D / 32, ROWS = 32 / PPT;  // rows of a run of the warp
   constexpr int RUNS = 16 / ROWS, TURN = C::TURN;                    // runs of a record, of a unit
   constexpr int WC = BITS / 4;                                       // words of a chunk of 8 channels
-  constexpr int UNITS = RUNS / TURN, PER = C::PT / 16 / WARPS;       // units of a record, a warp's records of a part
-  const int lane = tid & 31, warp = tid >> 5, piece = lane % PPT, row = lane / PPT;
+  constexpr int UNITS = RUNS / TURN, PER = C::PT / 16;               // units of a record, records of a part
+  static_assert(WARPS <= PER, "each warp has a record of each part");
+  const int piece = lane % PPT, row = lane / PPT;
   const PagesLayout& L = a.pv.L;
   const int lg = value ? L.v_lg : L.k_lg, meta_run = ROWS * (D >> lg) * 4;
   const int codes_at = (value ? L.v_off : 0) + row * (D * BITS / 8) + piece * (4 * BITS);
@@ -257,7 +270,7 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
     const Piece p = sh->piece[slot];
     if (p.nblk == 0) return;
     const PageRun run(a.pv, p.head);
-    const int all = p.nblk * (C::BK / C::PT) * (PER * UNITS);
+    const int all = (p.nblk * (C::BK / 16) - warp + WARPS - 1) / WARPS * UNITS;  // the warp's units
     // Unit u is part u % UNITS of the warp's record u / UNITS, 16 * WARPS tokens from the
     // one before.  A record's page is read while the one before is copied.
     int tok = p.blk * C::BK + warp * 16, part = 0, put = 0;  // of the next unit to be copied; its place
@@ -284,11 +297,19 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
       if (++part == UNITS) part = 0, tok += 16 * WARPS;
       if (++put == a.ring) put = 0;
     };
-    int get = 0;
+    int get = 0, now = 0;  // place of the next unit to be turned; the part that is being made
+    auto part_done = [&]() {
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ready[st]));
+      if (++st == C::SP) st = 0, par ^= 1;
+    };
 #pragma unroll 1
     for (int u = -a.ring; u < all; ++u) {
       if (u >= 0) {  // (the first rounds only copy)
-        if (u % (PER * UNITS) == 0 && !tile_wait_warp(sh, a, &empty[st], par ^ 1)) return;
+        const int rec = warp + u / UNITS * WARPS, of = rec / PER;
+        if (of != now) part_done(), now = of;
+        if (u % UNITS == 0 && rec - of * PER < WARPS && !tile_wait_warp(sh, a, &empty[st], par ^ 1)) return;  // (its first record of the part)
         copy_wait(a.ring - 1);
         uint32_t w[TURN][4 * WC], zs[TURN];
 #pragma unroll
@@ -300,8 +321,8 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
         if (++get == a.ring) get = 0;
         // row of the part's tile; rows behind the sequence's end become zero (zero + code *
         // step = 0), whatever the page, or the place of a record that was not brought, holds
-        const int v = u % (PER * UNITS), at0 = (v / UNITS * WARPS + warp) * 16 + v % UNITS * (TURN * ROWS) + row;
-        const int left = p.s.len - p.blk * C::BK - u / (PER * UNITS) * C::PT;
+        const int at0 = (rec - of * PER) * 16 + u % UNITS * (TURN * ROWS) + row;
+        const int left = p.s.len - p.blk * C::BK - of * C::PT;
         const uint32_t tile = tiles + st / (C::BK / C::PT) * C::TILE + st % (C::BK / C::PT) * (C::PT * 128);
 #pragma unroll
         for (int y = 0; y < TURN; ++y) {
@@ -342,24 +363,19 @@ __device__ __forceinline__ void tile_dequantizer(const AttnArgs& a, TileShared<D
         }
       }
       bring();  // (into the place that was read: its values have been used)
-      if (u >= 0 && (u + 1) % (PER * UNITS) == 0) {
-        fence_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ready[st]));
-        if (++st == C::SP) st = 0, par ^= 1;
-      }
     }
+    part_done();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh->piece_free[slot]));
   }
 }
 // Both tensors: one body where their bits are the same.
 template <int D, int FMT>
-__device__ __forceinline__ void tile_dequantize(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int value, int tid) {
+__device__ __forceinline__ void tile_dequantize(const AttnArgs& a, TileShared<D, FMT>* sh, uint32_t smem, int value, int warp, int lane) {
   using F = typename TileCfg<D, FMT>::F;
-  if constexpr (F::KB == F::VB) tile_dequantizer<D, FMT, F::KB>(a, sh, smem, value, tid);
-  else if (value) tile_dequantizer<D, FMT, F::VB>(a, sh, smem, 1, tid);
-  else tile_dequantizer<D, FMT, F::KB>(a, sh, smem, 0, tid);
+  if constexpr (F::KB == F::VB) tile_dequantizer<D, FMT, F::KB>(a, sh, smem, value, warp, lane);
+  else if (value) tile_dequantizer<D, FMT, F::VB>(a, sh, smem, 1, warp, lane);
+  else tile_dequantizer<D, FMT, F::KB>(a, sh, smem, 0, warp, lane);
 }
 
 // -------------------------------------------------------------- matrix unit --
@@ -428,7 +444,27 @@ __device__ __forceinline__ void tile_mma(const AttnArgs& a, TileShared<D, FMT>* 
     const int n = __shfl_sync(0xffffffffu, sh->piece[slot].nblk, 0);
     if (n == 0) return;
     if (!tile_wait_warp(sh, a, &sh->q_full, k & 1)) return;
-    if (C::NT == 2) {
+    if (shared_rows<D, FMT, MASK>(sh->piece[slot].rows)) {
+      // block j is tile j % 2's; the scores are two blocks ahead of the values
+#pragma unroll 1
+      for (int j = -2; j < n; ++j) {
+        const int i = j & 1;
+        if (j >= 0) {
+          if (!tile_wait_warp(sh, a, &sh->v_full[vs], vpar)) return;
+          if (!tile_wait_warp(sh, a, &sh->p_full[i], (turns >> i) & 1)) return;
+          turns ^= 1 << i;
+          tc_after_sync();
+          values(i, i, 0, j >= 2);
+          free_v();
+        }
+        if (j + 2 < n) {
+          if (!tile_wait_warp(sh, a, &sh->k_full[ks], kpar)) return;
+          tc_after_sync();
+          scores(i, i, 0);
+          free_k(j + 3 == n);
+        }
+      }
+    } else if (C::NT == 2) {
       // the blocks that tile 0 / 1 sees
       int lo0, hi0, lo1, hi1;
       tile_range<D, FMT, MASK>(a, sh->piece[slot], 0, &lo0, &hi0);
@@ -571,24 +607,26 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
     const Piece p = sh->piece[slot];
     if (p.nblk == 0) return;
     if (k > 0 && !tile_wait_warp(sh, a, &sh->q_free, (k - 1) & 1)) return;
-    const int r = tile * 128 + row;
+    const bool dual = shared_rows<D, FMT, MASK>(p.rows);
+    const int row0 = dual ? 0 : tile * 128, r = row0 + row;  // the tile's first row, the thread's
     const RowMap rm(a, p);
     const uint32_t q_tile = smem + C::Q_OFF + tile * C::TILE;
     float sc = a.scale_log2;
-    if (tile * 128 < p.rows) sc = tile_query<D, FMT>(a, rm, p.rows, tile * 128, row & ~31, q_tile, lane);
+    if (row0 < p.rows) sc = tile_query<D, FMT>(a, rm, p.rows, row0, row & ~31, q_tile, lane);
     fence_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh->q_full));
-    if (tile * 128 < p.rows) {
+    if (row0 < p.rows) {
       const int pos = rm.position(min(r, p.rows - 1));
       // the tile's first and last position: blocks between need no mask
       const int pos_lo = MASK ? p.s.p0 - 1 : rm.position(tile * 128);
       const int pos_hi = MASK ? p.s.len - 1 : rm.position(min(tile * 128 + 127, p.rows - 1));
       int j0, j1;
-      tile_range<D, FMT, MASK>(a, p, tile, &j0, &j1);
+      tile_range<D, FMT, MASK>(a, p, dual ? 0 : tile, &j0, &j1);
+      if (dual) j0 += tile;
       float m = -INFINITY;
       float2 l = make_float2(0.0f, 0.0f);
-      for (int j = j0; j < j1; ++j, ++bc, ++ob) {
+      for (int j = j0; j < j1; j += dual ? 2 : 1, ++bc, ++ob) {
         const int buf = C::NT == 2 ? tile : (bc & 1);
         if (!tile_wait_warp(sh, a, &sh->s_full[buf], C::NT == 2 ? bc & 1 : (bc >> 1) & 1)) return;
         tc_after_sync();
@@ -686,19 +724,47 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
       }
       // ---- the item's output, or this CTA's part of it
       if (!products(ob)) return;
-      const float sum = l.x + l.y;
+      float sum = l.x + l.y;
       const bool whole = p.has_first && p.has_last, has = r < p.rows;
+      // Shared rows: both tiles' maxima and sums are exchanged, and each tile puts half of
+      // the columns together, from both accumulators (the same lanes of tensor memory).
+      int c_lo = 0, c_hi = D;
+      float f0 = 1.0f, f1 = 0.0f;
+      if (dual) {
+        sh->stats[tile][row & (C::NT == 2 ? 127 : 0)] = make_float2(m, sum);
+        tc_before_sync();
+        __syncwarp();
+        uint64_t* met = &sh->met[(row >> 5) & 3];
+        if (lane == 0) mbar_arrive(smem_u32(met));
+        if (!tile_wait_warp(sh, a, met, 0)) return;
+        tc_after_sync();
+        const float2 s0 = sh->stats[0][row & (C::NT == 2 ? 127 : 0)], s1 = sh->stats[1][row & (C::NT == 2 ? 127 : 0)];
+        m = fmaxf(s0.x, s1.x);
+        f0 = s0.x == -INFINITY ? 0.0f : fast_exp2(s0.x - m);
+        f1 = s1.x == -INFINITY ? 0.0f : fast_exp2(s1.x - m);
+        sum = f0 * s0.y + f1 * s1.y;
+        c_lo = tile * (D / 2), c_hi = c_lo + D / 2;
+      }
       const float f = whole ? (sum > 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
       const long slot_row = ((long)blockIdx.x * 2 + (p.has_first ? 1 : 0)) * C::ROWS + r;
       // Whole rows go through the query tile's place (its last product is done),
-      // so that the stores are D / 8 lanes a row.
+      // so that the stores are D / 8 lanes a row (half as many where tiles share them).
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = c_lo; c < c_hi; c += 32) {
         uint32_t o[32];
-        tmem_ld32(tm + o_col + c, o);
-        if (j1 == j0) {  // no block: O was never written
+        tmem_ld32(tm + (dual ? 256 : o_col) + c, o);
+        if (j1 <= j0 && !dual) {  // no block: O was never written
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+        if (dual) {
+          uint32_t y[32];
+          if (p.nblk > 1) tmem_ld32(tm + 256 + D + c, y);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float u = __uint_as_float(o[e]) * f0;
+            o[e] = __float_as_uint(p.nblk > 1 ? fmaf(__uint_as_float(y[e]), f1, u) : u);
+          }
         }
         if (whole) {
 #pragma unroll
@@ -721,23 +787,29 @@ __device__ __forceinline__ void tile_softmax(const AttnArgs& a, TileShared<D, FM
         }
       }
       if (whole) {
-        constexpr int LPR = D / 8, RPI = 32 / LPR;
-        const int g = lane / LPR, ch = lane % LPR;
+        const int lpr = dual ? D / 16 : D / 8;  // lanes a row, iterations of 32 / lpr rows
+        const int g = lane / lpr, ch = c_lo / 8 + lane % lpr;
         __syncwarp();
 #pragma unroll 4
-        for (int it = 0; it < LPR; ++it) {
-          const int rw = (row & ~31) + it * RPI + g;
+        for (int it = 0; it < lpr; ++it) {
+          const int rw = (row & ~31) + it * (32 / lpr) + g;
           uint4 w;
           asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
                        : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
                        : "r"(q_tile + (ch >> 3) * (128 * 128) + rw * 128 + (((ch & 7) ^ (rw & 7)) << 4))
                        : "memory");
-          if (tile * 128 + rw < p.rows)
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + rm.at(tile * 128 + rw, (long)a.q_heads * D, D) + ch * 8) = w;
+          if (row0 + rw < p.rows)
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + rm.at(row0 + rw, (long)a.q_heads * D, D) + ch * 8) = w;
         }
         __syncwarp();
       }
-      if (!whole && has) *reinterpret_cast<float2*>(a.part_ml + slot_row * 2) = make_float2(m, sum);
+      if (!whole && has && (!dual || tile == 0)) *reinterpret_cast<float2*>(a.part_ml + slot_row * 2) = make_float2(m, sum);
+      if (dual) {  // neither accumulator nor the exchanged values are written before both are done with them
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh->met[(row >> 5) & 3]));
+        if (!tile_wait_warp(sh, a, &sh->met[(row >> 5) & 3], 1)) return;
+      }
       tc_before_sync();
     }
     if (tile == 0 && row == 0 && p.has_first && !p.has_last) {
@@ -776,6 +848,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
     mbar_init(smem_u32(&sh.q_full), 4 * C::NT);
     mbar_init(smem_u32(&sh.q_free), 1);
     mbar_init(smem_u32(&sh.v_land), 1);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.met[i]), 2);
     for (int i = 0; i < C::PIECES; ++i) {
       mbar_init(smem_u32(&sh.piece_full[i]), 1);
       mbar_init(smem_u32(&sh.piece_free[i]), C::USERS);
@@ -794,13 +867,12 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
   tc_after_sync();
 
   // Registers over codes: 512 threads start with 128 each (65536); two tiles take
-  // 256 * 176 + 128 * 72 + 128 * 88 = 65536 of them, one tile 128 * 176 +
-  // 128 * 72 + 256 * 88 = 54272.
+  // 256 * 176 + 256 * 80 = 65536 of them, one tile 128 * 176 + 384 * 80 = 53248.
   if (warp < 4 * C::NT) {
     if constexpr (F::kQuant) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
     tile_softmax<D, FMT, MASK>(a, &sh, smem, warp >> 2, threadIdx.x);
-  } else if (warp >= 8 && warp < 12) {
-    if constexpr (F::kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+  } else {
+    if constexpr (F::kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
     if (warp == 8) {
       tile_mma<D, FMT, MASK>(a, &sh, smem);
     } else if (warp == 10) {
@@ -829,14 +901,16 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::THREADS, 1) pages_tile_kernel
         __syncwarp();
         if (p.nblk == 0) break;
       }
-    } else if (!F::kQuant && warp == 9) {
+    } else if constexpr (F::kQuant) {
+      // one tile: warps 4 .. 7 values, 12 .. 15 keys; two tiles: 12, 13 and 9 keys, 14, 15 and 11 values
+      if (C::NT == 1) {
+        if (warp < 8 || warp >= 12) tile_dequantize<D, FMT>(a, &sh, smem, warp < 8, warp & 3, lane);
+      } else {
+        tile_dequantize<D, FMT>(a, &sh, smem, warp == 11 || warp >= 14, warp < 12 ? 2 : warp & 1, lane);
+      }
+    } else if (warp == 9) {
       tile_loader<D, FMT>(a, &sh, smem, lane);
     }
-  } else if constexpr (F::kQuant) {
-    // one tile: warps 4 .. 7 values, 12 .. 15 keys; two tiles: 12 and 13 keys, 14 and 15 values
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-    const int value = C::NT == 1 ? warp < 8 : warp >= 14;
-    tile_dequantize<D, FMT>(a, &sh, smem, value, threadIdx.x & (16 * C::PROD - 1));
   }
   __syncwarp();
   if (*(volatile int*)&sh.dead) {  // given up: what is in flight lands before memory is given back

@@ -283,30 +283,16 @@ struct Place {
   int page, slot, turn;
 };
 
-// Places of `count` rows from t0, by the whole block: every sequence's bounds and
-// length are read at once, and the thread whose sequence holds a row follows its
-// table entry, so a row costs two dependent loads whatever the batch is.  A
-// sequence whose length or rows do not fit has no places.  Only then can two
-// sequences name the same row: the rows are gone through again one by one, and the
-// first sequence that fits has it.
+// Places of `count` rows from t0 (no more than threads), by the whole block: every
+// sequence's bounds and length are read at once, each row learns its sequence, and a
+// thread a row follows the table, so a row costs two dependent loads whatever the batch
+// and the count are.  A sequence whose length or rows do not fit has no places.  Only then
+// can two sequences name the same row: the rows look for theirs one by one, and the first
+// sequence that fits has it.
 __device__ __forceinline__ void find_places(const PagesView& pv, const BatchView& bv, const RopeView* rv, long t0,
                                             int count, Place* place) {
-  if (threadIdx.x < count) place[threadIdx.x] = {-1, 0, 0};
+  if (threadIdx.x < count) place[threadIdx.x] = {-1, -1, 0};  // (slot: the row's sequence, until it has a place)
   __syncthreads();
-  // the place of row t, which sequence b holds; false: an index is out of range
-  auto find = [&](int b, const Seq& s, long t, Place* p) -> bool {
-    const long pos = s.p0 + (t - s.s0);
-    if (pos < 0) return true;
-    const int page = bv.table[b * bv.stride + (pos >> pv.lg_pt)];
-    bool ok = (unsigned)page < (unsigned)pv.pages;
-    long turn = 0;
-    if (rv && rv->table) {
-      turn = rv->positions ? rv->positions[t] : pos;
-      ok = ok && turn >= 0 && turn < rv->rows;
-    }
-    if (ok) *p = {page, (int)(pos & ((1 << pv.lg_pt) - 1)), (int)turn};
-    return ok;
-  };
   int misfit = 0;
   for (int b = threadIdx.x; b < bv.batch; b += kThreads) {
     bool bad;
@@ -317,24 +303,39 @@ __device__ __forceinline__ void find_places(const PagesView& pv, const BatchView
       continue;
     }
     const long lo = max(t0, (long)s.s0), hi = min(t0 + count, (long)s.s0 + s.n);
-    for (long t = lo; t < hi; ++t) bad = !find(b, s, t, &place[t - t0]) || bad;
-    if (bad) atomicOr(pv.err, 1);
+    for (long t = lo; t < hi; ++t) place[t - t0].slot = b;
   }
-  if (__syncthreads_or(misfit)) {
+  misfit = __syncthreads_or(misfit);
+  if (threadIdx.x < count) {
     const long t = t0 + threadIdx.x;
-    if (threadIdx.x < count) {
-      Place p = {-1, 0, 0};
-      for (int b = 0; b < bv.batch; ++b) {
-        bool bad;
-        const Seq s = load_seq(pv, bv, b, &bad);
-        if (bad || t < s.s0 || t >= (long)s.s0 + s.n) continue;
-        find(b, s, t, &p);
-        break;
+    int b = place[threadIdx.x].slot;
+    bool bad = false;
+    Seq s = {};
+    if (misfit) {
+      for (b = 0; b < bv.batch; ++b) {
+        s = load_seq(pv, bv, b, &bad);
+        if (!bad && t >= s.s0 && t < (long)s.s0 + s.n) break;
       }
-      place[threadIdx.x] = p;
+      if (b == bv.batch) b = -1;
+    } else if (b >= 0) {
+      s = load_seq(pv, bv, b, &bad);
     }
-    __syncthreads();
+    Place p = {-1, 0, 0};
+    const long pos = s.p0 + (t - s.s0);
+    if (b >= 0 && pos >= 0) {
+      const int page = bv.table[b * bv.stride + (pos >> pv.lg_pt)];
+      bool ok = (unsigned)page < (unsigned)pv.pages;
+      long turn = 0;
+      if (rv && rv->table) {
+        turn = rv->positions ? rv->positions[t] : pos;
+        ok = ok && turn >= 0 && turn < rv->rows;
+      }
+      if (ok) p = {page, (int)(pos & ((1 << pv.lg_pt) - 1)), (int)turn};
+      else atomicOr(pv.err, 1);
+    }
+    place[threadIdx.x] = p;
   }
+  __syncthreads();
 }
 
 // One row's 8 channels from c0 on into its record (`rec` + `off`): 16-bit, or
@@ -483,30 +484,36 @@ __device__ __forceinline__ uint4 get8(const char* rec, int off, int meta_off, in
 // As many warps as an SM holds hide its loads better than several heads in flight a warp:
 // 509 pages of 64 tokens, 40 heads of 128, 8- and 4-bit, four layers, us: 8 CTAs per SM
 // and one head 212 a layer, two heads 213 (6 CTAs) and 237 (8), four heads (3 CTAs) 349.
+// `turns`: rows that a warp takes one after the other of those whose places are found at
+// once; where there are many rows, looking for places is a third of the time at one.
+constexpr int kReadTurns = 8;
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 8) pages_read_kernel(PagesView pv, BatchView bv, char* k_out, char* v_out,
-                                                              int lg_wpt) {
+                                                              int lg_wpt, int turns) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
-  __shared__ Place place[kRowWarps];
+  __shared__ Place place[kRowWarps * kReadTurns];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nsub = 1 << lg_wpt, sub = warp & (nsub - 1), tpb = kRowWarps >> lg_wpt;
   const int rg = lane / LPR, c0 = (lane % LPR) * 8, H = pv.heads;
   pdl_wait();
   pdl_trigger();
-  for (long t0 = (long)blockIdx.x * tpb; t0 < bv.new_tokens; t0 += (long)gridDim.x * tpb) {
+  for (long t0 = (long)blockIdx.x * tpb * turns; t0 < bv.new_tokens; t0 += (long)gridDim.x * tpb * turns) {
     __syncthreads();
-    find_places(pv, bv, nullptr, t0, tpb, place);
-    const Place p = place[warp >> lg_wpt];
-    if (p.page < 0) continue;
-    const long row = (t0 + (warp >> lg_wpt)) * H;
-    for (int h = sub * RPW + rg; h < H; h += nsub * RPW) {
-      const char* rec = record_of(pv, p.page, h, p.slot);
-      uint4 a, b;
-      if (k_out) a = get8<D>(rec, 0, pv.L.km_off, pv.L.k_bits, pv.L.k_lg, p.slot, c0);
-      if (v_out) b = get8<D>(rec, pv.L.v_off, pv.L.vm_off, pv.L.v_bits, pv.L.v_lg, p.slot, c0);
-      const long at = ((row + h) * D + c0) * 2;
-      if (k_out) *reinterpret_cast<uint4*>(k_out + at) = a;
-      if (v_out) *reinterpret_cast<uint4*>(v_out + at) = b;
+    find_places(pv, bv, nullptr, t0, tpb * turns, place);
+    for (int i = warp >> lg_wpt; i < tpb * turns; i += tpb) {
+      const Place p = place[i];
+      if (p.page < 0) continue;
+      const long row = (t0 + i) * H;
+      for (int h = sub * RPW + rg; h < H; h += nsub * RPW) {
+        const char* rec = record_of(pv, p.page, h, p.slot);
+        uint4 a, b;
+        if (k_out) a = get8<D>(rec, 0, pv.L.km_off, pv.L.k_bits, pv.L.k_lg, p.slot, c0);
+        if (v_out) b = get8<D>(rec, pv.L.v_off, pv.L.vm_off, pv.L.v_bits, pv.L.v_lg, p.slot, c0);
+        const long at = ((row + h) * D + c0) * 2;
+        if (k_out) *reinterpret_cast<uint4*>(k_out + at) = a;
+        if (v_out) *reinterpret_cast<uint4*>(v_out + at) = b;
+      }
     }
   }
 }
@@ -572,11 +579,14 @@ cudaError_t launch_pages_read(const PagesView& pv, const BatchView& bv, void* k_
   PagesView p = pv;
   BatchView b = bv;
   char *ko = static_cast<char*>(k_out), *vo = static_cast<char*>(v_out);
-  void* args[] = {&p, &b, &ko, &vo, &lg};
+  const long per = kRowWarps >> lg;
+  int turns = 1;  // (doubled while the blocks fill the card twice)
+  while (turns < kReadTurns && bv.new_tokens >= per * turns * 2 * 152 * 8 * 2) turns *= 2;
+  void* args[] = {&p, &b, &ko, &vo, &lg, &turns};
   const void* fn = pv.head_dim == 64    ? (const void*)pages_read_kernel<64>
                    : pv.head_dim == 128 ? (const void*)pages_read_kernel<128>
                                         : (const void*)pages_read_kernel<256>;
-  return launch_pdl(fn, dim3(token_blocks(bv.new_tokens, lg)), dim3(kThreads), 0, st, args);
+  return launch_pdl(fn, dim3(token_blocks((bv.new_tokens + turns - 1) / turns, lg)), dim3(kThreads), 0, st, args);
 }
 
 }  // namespace kvq

@@ -85,8 +85,8 @@ constexpr int kKeepThreads = 256;
 struct Column {
   long at;        // of token 0 of a record, from the record's head
   int stride;     // from a token to the next
-  int swizzle;    // 16-bit rows: chunk index inside the 128-byte row, else -1
-  bool wide;      // 16 bytes, else 4
+  int chunk, turn;  // 16-bit rows: chunk index inside the 128-byte row, 7 (its swizzle); else 0
+  bool wide;        // 16 bytes, else 4
 };
 
 // Columns of one tensor's codes or values, and of its metadata.
@@ -105,15 +105,15 @@ __device__ __forceinline__ Column column_of(const PagesView& pv, int c) {
   for (int side = 0; side < 2; ++side) {
     const int bits = side ? L.v_bits : L.k_bits, n = row_columns(pv, bits), off = side ? L.v_off : 0;
     if (c < n) {
-      if (bits == 16) return {off + (c >> 3) * 2048, 128, c & 7, true};
-      return {off + c * 16, pv.head_dim * bits / 8, -1, true};
+      if (bits == 16) return {off + (c >> 3) * 2048, 128, c & 7, 7, true};
+      return {off + c * 16, pv.head_dim * bits / 8, 0, 0, true};
     }
     c -= n;
   }
   const int n = meta_columns(pv, L.k_bits, L.k_lg);
-  if (c < n) return {L.km_off + c * 4, n * 4, -1, false};
+  if (c < n) return {L.km_off + c * 4, n * 4, 0, 0, false};
   c -= n;
-  return {L.vm_off + c * 4, meta_columns(pv, L.v_bits, L.v_lg) * 4, -1, false};
+  return {L.vm_off + c * 4, meta_columns(pv, L.v_bits, L.v_lg) * 4, 0, 0, false};
 }
 
 // A token's place: its record's offset in a layer for head 0, and its number in the
@@ -134,7 +134,7 @@ struct ColumnOf {
   }
   __device__ __forceinline__ char* at(long place) const {
     const int t = (int)(place & 15);
-    return base + (place & ~15L) + t * col.stride + (col.swizzle < 0 ? 0 : (col.swizzle ^ (t & 7)) << 4);
+    return base + (place - t) + (t * col.stride + ((col.chunk ^ (t & col.turn)) << 4));
   }
   __device__ __forceinline__ void load(long place, uint4* x) const {
     if (col.wide) *x = *reinterpret_cast<const uint4*>(at(place));
@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(kKeepThreads, 2) pages_keep_move_kernel(PagesV
       if (w < warp) before += sums[w];
       st.all += sums[w];
     }
+    if (tid >= st.all && tid < kSegRows) to[tid] = make_long2(-1, -1);
     if (on) to[before] = move_of(pv, bv, st.g.b, s.p0 + i, first + st.g.before + before, st.unit == lane);
     return st;
   };
@@ -356,7 +357,8 @@ __global__ void __launch_bounds__(kKeepThreads, 2) pages_keep_move_kernel(PagesV
     for (int u = 0; u < U; ++u) {
       const int j = u * (kKeepThreads / 32) + warp;
       x[u] = make_uint4(0, 0, 0, 0);
-      if (mine && j < now.all && move[buf][j].x >= 0) col.load(move[buf][j].x, &x[u]);
+      const long from = move[buf][j].x;
+      if (mine && from >= 0) col.load(from, &x[u]);
     }
     // while they come: what the next step moves
     const Step next = draw(move[buf ^ 1]);
@@ -390,7 +392,8 @@ __global__ void __launch_bounds__(kKeepThreads, 2) pages_keep_move_kernel(PagesV
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int j = u * (kKeepThreads / 32) + warp;
-        if (mine && j < now.all && move[buf][j].x >= 0) col.store(move[buf][j].y, x[u]);
+        const long to = move[buf][j].y;
+        if (mine && to >= 0) col.store(to, x[u]);
       }
     }
     now = next;

@@ -25,6 +25,7 @@
 
 #include "kvq_internal.h"
 #include "kvq_pages_attn.cuh"
+#include "kvq_pages_rows.cuh"  // (codes to values)
 
 namespace kvq {
 
@@ -453,49 +454,65 @@ __global__ void __launch_bounds__(kThreads, QUANT ? 5 : 4) pages_append_kernel(P
 
 // -------------------------------------------------------------------- read --
 
-template <int D>
-__device__ __forceinline__ uint4 get8(const char* rec, int off, int meta_off, int bits, int lg_group, int slot, int c0) {
-  const int t = slot & 15;
-  if (bits == 16)
-    return *reinterpret_cast<const uint4*>(rec + off + (c0 >> 6) * 2048 + t * 128 + ((((c0 >> 3) & 7) ^ (t & 7)) << 4));
-  const __half2 zs = reinterpret_cast<const __half2*>(rec + meta_off)[t * (D >> lg_group) + (c0 >> lg_group)];
-  const __half2 z = __low2half2(zs), s = __high2half2(zs);
-  uint4 out;
-  uint32_t* o = reinterpret_cast<uint32_t*>(&out);
-  uint2 w;
-  if (bits == 8) w = *reinterpret_cast<const uint2*>(rec + off + t * D + c0);
-  else w.x = *reinterpret_cast<const uint32_t*>(rec + off + t * (D / 2) + c0 / 2);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    int a, b;
-    if (bits == 8) {
-      const uint32_t x = (j < 2 ? w.x : w.y) >> (16 * (j & 1));
-      a = x & 255, b = (x >> 8) & 255;
+// 8 channels of one tensor's row as the page holds them.
+template <int BITS>
+struct Held8 {
+  uint32_t w[BITS / 4];
+  uint32_t zs;  // (zero, step) of their group
+};
+
+template <int BITS>
+__device__ __forceinline__ Held8<BITS> load_held(const char* row, const char* meta) {
+  Held8<BITS> x;
+  if constexpr (BITS == 16) {
+    const uint4 w = *reinterpret_cast<const uint4*>(row);
+    x.w[0] = w.x, x.w[1] = w.y, x.w[2] = w.z, x.w[3] = w.w;
+    x.zs = 0;
+  } else {
+    if constexpr (BITS == 8) {
+      const uint2 w = *reinterpret_cast<const uint2*>(row);
+      x.w[0] = w.x, x.w[1] = w.y;
     } else {
-      a = (w.x >> (4 * j)) & 15, b = (w.x >> (16 + 4 * j)) & 15;
+      x.w[0] = *reinterpret_cast<const uint32_t*>(row);
     }
-    // zero + code * step, rounded once to fp16
-    const __half2 y = __hfma2(__floats2half2_rn((float)a, (float)b), s, z);
-    o[j] = *reinterpret_cast<const uint32_t*>(&y);
+    x.zs = *reinterpret_cast<const uint32_t*>(meta);
   }
-  return out;
+  return x;
 }
 
-// As many warps as an SM holds hide its loads better than several heads in flight a warp:
-// 509 pages of 64 tokens, 40 heads of 128, 8- and 4-bit, four layers, us: 8 CTAs per SM
-// and one head 212 a layer, two heads 213 (6 CTAs) and 237 (8), four heads (3 CTAs) 349.
-// `turns`: rows that a warp takes one after the other of those whose places are found at
-// once; where there are many rows, looking for places is a third of the time at one.
-constexpr int kReadTurns = 8;
+// zero + code * step, rounded once to fp16
+template <int BITS>
+__device__ __forceinline__ uint4 held_values(const Held8<BITS>& x) {
+  if constexpr (BITS == 16) {
+    return make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+  } else {
+    const __half2 z = __low2half2(as_h2(x.zs)), s = __high2half2(as_h2(x.zs));
+    if constexpr (BITS == 8)
+      return make_uint4(bytes<0>(x.w[0], s, z), bytes<1>(x.w[0], s, z), bytes<0>(x.w[1], s, z), bytes<1>(x.w[1], s, z));
+    else
+      return make_uint4(nibbles<0>(x.w[0], s, z), nibbles<1>(x.w[0], s, z), nibbles<2>(x.w[0], s, z), nibbles<3>(x.w[0], s, z));
+  }
+}
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 8) pages_read_kernel(PagesView pv, BatchView bv, char* k_out, char* v_out,
+// A warp takes a token's heads, kReadHeads of a lane in flight; what lies in a record does
+// not change from head to head, so a head costs four loads, its values and two stores.
+// (Offsets worked out head by head took 169 instructions a pass and, in the registers of 8
+// CTAs per SM, spills.)  509 pages of 64 tokens, 40 heads of 128, 8- and 4-bit, copied and
+// read in four layers, us: that form 1165; now 927 with two heads in flight and 5 CTAs per
+// SM, 949 with one and 8, 918 with four and 4, which costs short reads more.
+// `turns`: rows that a warp takes one after the other of those whose places are found at
+// once.
+constexpr int kReadTurns = 8, kReadHeads = 2;
+
+template <int D, int KB, int VB>
+__global__ void __launch_bounds__(kThreads, 5) pages_read_kernel(PagesView pv, BatchView bv, char* k_out, char* v_out,
                                                               int lg_wpt, int turns) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  constexpr int LPR = D / 8, RPW = 32 / LPR, U = kReadHeads;
   __shared__ Place place[kRowWarps * kReadTurns];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nsub = 1 << lg_wpt, sub = warp & (nsub - 1), tpb = kRowWarps >> lg_wpt;
-  const int rg = lane / LPR, c0 = (lane % LPR) * 8, H = pv.heads;
+  const int h_first = sub * RPW + lane / LPR, c0 = (lane % LPR) * 8, H = pv.heads, h_step = nsub * RPW;
+  const long head_bytes = page_head_bytes(pv), rec_step = h_step * head_bytes;
   pdl_wait();
   pdl_trigger();
   for (long t0 = (long)blockIdx.x * tpb * turns; t0 < bv.new_tokens; t0 += (long)gridDim.x * tpb * turns) {
@@ -504,18 +521,44 @@ __global__ void __launch_bounds__(kThreads, 8) pages_read_kernel(PagesView pv, B
     for (int i = warp >> lg_wpt; i < tpb * turns; i += tpb) {
       const Place p = place[i];
       if (p.page < 0) continue;
-      const long row = (t0 + i) * H;
-      for (int h = sub * RPW + rg; h < H; h += nsub * RPW) {
-        const char* rec = record_of(pv, p.page, h, p.slot);
-        uint4 a, b;
-        if (k_out) a = get8<D>(rec, 0, pv.L.km_off, pv.L.k_bits, pv.L.k_lg, p.slot, c0);
-        if (v_out) b = get8<D>(rec, pv.L.v_off, pv.L.vm_off, pv.L.v_bits, pv.L.v_lg, p.slot, c0);
-        const long at = ((row + h) * D + c0) * 2;
-        if (k_out) *reinterpret_cast<uint4*>(k_out + at) = a;
-        if (v_out) *reinterpret_cast<uint4*>(v_out + at) = b;
+      const int t = p.slot & 15;
+      const char* rec = record_of(pv, p.page, h_first, p.slot);
+      auto row_at = [&](int bits) { return bits == 16 ? (c0 >> 6) * 2048 + t * 128 + ((((c0 >> 3) & 7) ^ (t & 7)) << 4) : t * (D * bits / 8) + c0 * bits / 8; };
+      const int k_row = row_at(KB), v_row = pv.L.v_off + row_at(VB);
+      const int k_meta = pv.L.km_off + (t * (D >> pv.L.k_lg) + (c0 >> pv.L.k_lg)) * 4;
+      const int v_meta = pv.L.vm_off + (t * (D >> pv.L.v_lg) + (c0 >> pv.L.v_lg)) * 4;
+      long at = (((t0 + i) * H + h_first) * D + c0) * 2;
+      for (int h = h_first; h < H; h += h_step * U) {
+        Held8<KB> k[U];
+        Held8<VB> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const char* r = rec + u * rec_step;
+          if (h + u * h_step < H) {
+            if (k_out) k[u] = load_held<KB>(r + k_row, r + k_meta);
+            if (v_out) v[u] = load_held<VB>(r + v_row, r + v_meta);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const long o = at + (long)u * h_step * (D * 2);
+          if (h + u * h_step < H) {
+            if (k_out) *reinterpret_cast<uint4*>(k_out + o) = held_values<KB>(k[u]);
+            if (v_out) *reinterpret_cast<uint4*>(v_out + o) = held_values<VB>(v[u]);
+          }
+        }
+        rec += U * rec_step;
+        at += (long)U * h_step * (D * 2);
       }
     }
   }
+}
+
+template <int D>
+const void* read_fn(const PagesLayout& L) {
+  if (L.k_bits == 16) return (const void*)pages_read_kernel<D, 16, 16>;
+  if (L.k_bits == 8) return L.v_bits == 8 ? (const void*)pages_read_kernel<D, 8, 8> : (const void*)pages_read_kernel<D, 8, 4>;
+  return L.v_bits == 8 ? (const void*)pages_read_kernel<D, 4, 8> : (const void*)pages_read_kernel<D, 4, 4>;
 }
 
 unsigned token_blocks(long tokens, int lg_wpt) {
@@ -583,9 +626,7 @@ cudaError_t launch_pages_read(const PagesView& pv, const BatchView& bv, void* k_
   int turns = 1;  // (doubled while the blocks fill the card twice)
   while (turns < kReadTurns && bv.new_tokens >= per * turns * 2 * 152 * 8 * 2) turns *= 2;
   void* args[] = {&p, &b, &ko, &vo, &lg, &turns};
-  const void* fn = pv.head_dim == 64    ? (const void*)pages_read_kernel<64>
-                   : pv.head_dim == 128 ? (const void*)pages_read_kernel<128>
-                                        : (const void*)pages_read_kernel<256>;
+  const void* fn = pv.head_dim == 64 ? read_fn<64>(pv.L) : pv.head_dim == 128 ? read_fn<128>(pv.L) : read_fn<256>(pv.L);
   return launch_pdl(fn, dim3(token_blocks((bv.new_tokens + turns - 1) / turns, lg)), dim3(kThreads), 0, st, args);
 }
 

@@ -746,9 +746,8 @@ class KVQPages:
         return t
 
     def _ints_in(self, t, name, shape):
-        _ints(t, name)
-        _need(t.shape == shape and t.is_contiguous() and t.get_device() == self.index,
-              f"{name}: contiguous, of {list(shape)}, on the cache's device")
+        if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != self.index or not t.is_contiguous():
+            raise ValueError(f"{name}: int32, contiguous, of {list(shape)}, on the cache's device")
         return t.data_ptr()
 
     def kvq_pages_fork(self, parent: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
@@ -757,13 +756,13 @@ class KVQPages:
         """A new table whose row b is row parent[b] (-1: empty) of `table` [rows][pages], sharing its pages, and
         the pages' reference counts with it: returns (table_out, lens_out, refs_out), new tensors unless given
         (refs itself works as refs_out).  All int32 device tensors; refs [pages]."""
-        index = self.index
-        _ints(table, "table")
-        _ints(parent, "parent")
-        _need(table.dim() == 2 and table.shape[0] > 0 and table.shape[1] > 0, "table: [rows][pages]")
-        _need(parent.dim() == 1 and parent.shape[0] > 0, "parent: one a new row")
-        rows, n = table.shape[0], parent.shape[0]
-        tp, pp = self._ints_in(table, "table", table.shape), self._ints_in(parent, "parent", parent.shape)
+        index, shape = self.index, table.shape
+        if len(shape) != 2 or not shape[0] or not shape[1]:
+            raise ValueError("table: [rows][pages]")
+        if parent.dim() != 1 or not parent.shape[0]:
+            raise ValueError("parent: one a new row")
+        rows, n = shape[0], parent.shape[0]
+        tp, pp = self._ints_in(table, "table", shape), self._ints_in(parent, "parent", (n,))
         lp, rp = self._ints_in(lens, "lens", (rows,)), self._ints_in(refs, "refs", (self.cfg.pages,))
         if table_out is not None:
             _need(table_out.dim() == 2 and table_out.shape[1] > 0, "table_out: [rows][pages]")
@@ -783,11 +782,11 @@ class KVQPages:
         """Pages for q_start[b + 1] - q_start[b] new tokens behind the lens[b] of each row of `table`, dealt out
         where refs [pages] is zero, a shared last page copied; table and refs are changed in place.  Returns the
         lengths with the new tokens (lens itself works as lens_out); where pages ran out, -1 - lens[b]."""
-        index = self.index
-        _ints(table, "table")
-        _need(table.dim() == 2 and table.shape[0] > 0 and table.shape[1] > 0, "table: [sequences][pages]")
-        n = table.shape[0]
-        tp, qp = self._ints_in(table, "table", table.shape), self._ints_in(q_start, "q_start", (n + 1,))
+        index, shape = self.index, table.shape
+        if len(shape) != 2 or not shape[0] or not shape[1]:
+            raise ValueError("table: [sequences][pages]")
+        n = shape[0]
+        tp, qp = self._ints_in(table, "table", shape), self._ints_in(q_start, "q_start", (n + 1,))
         lp, rp = self._ints_in(lens, "lens", (n,)), self._ints_in(refs, "refs", (self.cfg.pages,))
         lens_out = self._ints_out(lens_out, "lens_out", (n,), stream)
         a = _GrowArgs(n, qp, lp, tp, table.shape[1], rp, lens_out.data_ptr())

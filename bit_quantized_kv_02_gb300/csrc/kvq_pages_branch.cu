@@ -227,6 +227,12 @@ __global__ void __launch_bounds__(kKeepThreads) pages_keep_kernel(PagesView pv, 
 constexpr int kSegRows = 128;
 constexpr int kPlanThreads = 1024;
 
+__device__ __forceinline__ int load_acquire(const int* p) {
+  int x;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];\n" : "=r"(x) : "l"(p) : "memory");
+  return x;
+}
+
 struct KeepPlan {
   unsigned long long ticket;
   int segments;
@@ -302,6 +308,9 @@ __global__ void __launch_bounds__(kPlanThreads) pages_keep_plan_kernel(PagesView
   if (lens_out && tid == 0) lens_out[b] = max(s.p0, 0) + run;
 }
 
+// A step's chain of loads (ticket, segment, marks, page table, tokens) is spread over the
+// steps before it: while a step's tokens come, the places of the next one's are found, the
+// segment of the one after is read and the ticket of a third is drawn.
 __global__ void __launch_bounds__(kKeepThreads, 2) pages_keep_move_kernel(PagesView pv, long layer_bytes, long units,
                                                                          BatchView bv, const uint8_t* keep, KeepPlan* plan,
                                                                          KeepSeg* seg) {
@@ -309,31 +318,34 @@ __global__ void __launch_bounds__(kKeepThreads, 2) pages_keep_move_kernel(PagesV
   __shared__ long2 move[2][kSegRows];
   __shared__ int sums[kSegRows / 32], ready;
   __shared__ uint32_t arrived[kKeepThreads];
-  __shared__ long drawn;
+  __shared__ long drawn[3];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_trigger();
   const long blocks = (units + 31) / 32, total = plan->segments * blocks;
-  // the next ticket's segment, and the places of its kept tokens in `to`
   struct Step {
     KeepSeg g;
-    int id, all;
+    Seq s;
+    int id, all;  // segment (-1: none), kept rows
     long unit;
   };
-  auto draw = [&](long2* to) {
-    if (tid == 0) drawn = (long)atomicAdd(&plan->ticket, 1ull);
-    __syncthreads();
-    const long ticket = drawn;
+  // what a ticket stands for
+  auto step_of = [&](long ticket) {
     Step st = {};
     st.id = -1;
-    if (ticket >= total) return st;  // (all threads)
+    if (ticket >= total) return st;
     st.id = (int)(ticket / blocks);
     st.unit = (ticket - st.id * blocks) * 32 + lane;
     st.g = seg[st.id];
     bool bad;
-    const Seq s = load_seq(pv, bv, st.g.b, &bad);
-    const int skip = max(-s.p0, 0), first = s.p0 + skip, i = skip + st.g.at * kSegRows + tid;
-    const bool on = tid < kSegRows && i < s.n && keep[(long)s.s0 + i] != 0;
+    st.s = load_seq(pv, bv, st.g.b, &bad);
+    return st;
+  };
+  // the places of its kept tokens
+  auto find = [&](Step& st, long2* to) {
+    if (st.id < 0) return;  // (all threads)
+    const int skip = max(-st.s.p0, 0), first = st.s.p0 + skip, i = skip + st.g.at * kSegRows + tid;
+    const bool on = tid < kSegRows && i < st.s.n && keep[(long)st.s.s0 + i] != 0;
     const unsigned ballot = __ballot_sync(0xffffffffu, on);
     if (lane == 0 && warp < kSegRows / 32) sums[warp] = __popc(ballot);
     __syncthreads();
@@ -344,10 +356,14 @@ __global__ void __launch_bounds__(kKeepThreads, 2) pages_keep_move_kernel(PagesV
       st.all += sums[w];
     }
     if (tid >= st.all && tid < kSegRows) to[tid] = make_long2(-1, -1);
-    if (on) to[before] = move_of(pv, bv, st.g.b, s.p0 + i, first + st.g.before + before, st.unit == lane);
-    return st;
+    if (on) to[before] = move_of(pv, bv, st.g.b, st.s.p0 + i, first + st.g.before + before, st.unit == lane);
   };
-  Step now = draw(move[0]);
+  if (tid == 0)
+    for (int i = 0; i < 3; ++i) drawn[i] = (long)atomicAdd(&plan->ticket, 1ull);
+  __syncthreads();
+  Step now = step_of(drawn[0]), next = step_of(drawn[1]);
+  long third = drawn[2];
+  find(now, move[0]);
   for (int buf = 0; now.id >= 0; buf ^= 1) {
     __syncthreads();
     const bool mine = now.unit < units;
@@ -360,34 +376,44 @@ __global__ void __launch_bounds__(kKeepThreads, 2) pages_keep_move_kernel(PagesV
       const long from = move[buf][j].x;
       if (mine && from >= 0) col.load(from, &x[u]);
     }
-    // while they come: what the next step moves
-    const Step next = draw(move[buf ^ 1]);
+    // while they come
+    const KeepSeg& g = now.g;
+    // segments that hold the rows which are written, [before, before + all) of the sequence's
+    const int seg0 = g.before / kSegRows, seg1 = now.all > 0 ? min((g.before + now.all - 1) / kSegRows, g.at - 1) : -1;
+    long fourth = 0;
+    if (tid == 0) {
+      fourth = (long)atomicAdd(&plan->ticket, 1ull);
+      bool read = true;  // (mostly they have been read long ago)
+      for (int k = seg0; k <= seg1; ++k) read = read && load_acquire(&seg[now.id - g.at + k].done) >= blocks;
+      ready = read;
+    }
+    const Step after = step_of(third);
+    find(next, move[buf ^ 1]);
     // every load has come back when its values can be stored
     uint32_t any = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) any |= x[u].x | x[u].y | x[u].z | x[u].w;
     *(volatile uint32_t*)&arrived[tid] = any;
-    if (tid == 0) ready = 1;
+    if (tid == 0) drawn[0] = fourth;
     __syncthreads();
-    if (tid == 0) {
-      const KeepSeg& g = now.g;
+    third = drawn[0];
+    if (tid == 32) {  // (this step's tokens have been read)
       __threadfence();
       atomicAdd(&seg[now.id].done, 1);
-      // the rows that are written: [before, before + all) of the sequence's
-      for (int k = g.before / kSegRows; now.all > 0 && k < g.at && k <= (g.before + now.all - 1) / kSegRows; ++k) {
-        const volatile int* done = &seg[now.id - g.at + k].done;
-        const unsigned long long t0 = time_ns();
-        while (*done < blocks) {
-          if (time_ns() - t0 > kWaitNs) {
-            atomicOr(pv.err, 2);
-            ready = 0;
-            break;
-          }
-        }
-      }
-      __threadfence();
     }
+    const bool wait = !ready;
     __syncthreads();
+    if (wait) {
+      if (tid == 0) {
+        const unsigned long long t0 = time_ns();
+        bool late = false;
+        for (int k = seg0; k <= seg1; ++k)
+          while (!late && load_acquire(&seg[now.id - g.at + k].done) < blocks) late = time_ns() - t0 > kWaitNs;
+        if (late) atomicOr(pv.err, 2);
+        ready = !late;
+      }
+      __syncthreads();
+    }
     if (ready) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -397,6 +423,7 @@ __global__ void __launch_bounds__(kKeepThreads, 2) pages_keep_move_kernel(PagesV
       }
     }
     now = next;
+    next = after;
   }
 }
 

@@ -395,8 +395,9 @@ kvq_status kvq_pages_keep(kvq_pages_t P, int layer, const kvq_pages_batch* batch
   if (s != KVQ_OK) return s;
   if (!keep && bv.new_tokens > 0) return fail(P, KVQ_ERR_INVALID_ARG, "null marks");
   if (!fits(lens_out, 4)) return fail(P, KVQ_ERR_INVALID_ARG, "lengths not 4-byte aligned");
-  if (lens_out && share(lens_out, bv.batch, bv.lens, bv.batch))
-    return fail(P, KVQ_ERR_INVALID_ARG, "new lengths over the old ones");
+  if (lens_out && (share(lens_out, bv.batch, bv.lens, bv.batch) || share(lens_out, bv.batch, bv.q_start, bv.batch + 1) ||
+                   share(lens_out, bv.batch, bv.table, bv.batch * bv.stride)))
+    return fail(P, KVQ_ERR_INVALID_ARG, "new lengths over the batch's arrays");
   if (bv.new_tokens == 0 && !lens_out) return KVQ_OK;
   const int max_new = batch->max_new > 0 && batch->max_new < bv.new_tokens ? batch->max_new : bv.new_tokens;
   return cuda_result(P, launch_pages_keep(pv, layers, (long)P->layer_bytes, bv, max_new, keep, lens_out, P->d_keep,
@@ -457,6 +458,7 @@ kvq_status kvq_pages_grow(kvq_pages_t P, const kvq_pages_grow_args* a, void* str
   if (!fits(a->q_start, 4) || !fits(a->lens, 4) || !fits(a->table, 4) || !fits(a->refs, 4) || !fits(a->lens_out, 4))
     return fail(P, KVQ_ERR_INVALID_ARG, "array not 4-byte aligned");
   const int64_t n = a->sequences, pages = P->cfg.pages, entries = n * a->table_stride;
+  if (entries > INT_MAX) return fail(P, KVQ_ERR_UNSUPPORTED, "a table of more entries than 32 bits count");
   if ((a->lens_out != a->lens && share(a->lens_out, n, a->lens, n)) || share(a->lens_out, n, a->q_start, n + 1) ||
       share(a->lens_out, n, a->table, entries) || share(a->lens_out, n, a->refs, pages) ||
       share(a->table, entries, a->refs, pages) || share(a->table, entries, a->lens, n) ||

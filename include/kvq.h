@@ -484,7 +484,7 @@ kvq_status kvq_pages_read(kvq_pages_t pages, int layer, const kvq_pages_batch* b
 /* Keep some of a sequence's new tokens and close the gaps: keep [new_tokens] (device
  * bytes) is nonzero for the rows to keep; the j-th kept row of sequence b moves to
  * position lens[b] - n + j, metadata included, keys as they were turned.  lens_out
- * (device [batch], apart from lens; NULL: not wanted) becomes lens[b] - n + the number
+ * (device [batch], apart from the batch's arrays; NULL: not wanted) becomes lens[b] - n + the number
  * kept: the accepted branch of a drafted tree, or, with q_start spanning whole
  * sequences, what is left of an evicted cache.  Positions from lens_out[b] on hold
  * what they held, or rows that moved.  Rows with a negative position are no tokens;
@@ -545,7 +545,7 @@ typedef struct {
   const int32_t* q_start;      /* [sequences + 1] */
   const int32_t* lens;         /* [sequences] */
   int32_t* table;              /* [sequences][table_stride] */
-  int64_t table_stride;        /* >= 1 */
+  int64_t table_stride;        /* >= 1, sequences * table_stride < 2^31 */
   int32_t* refs;               /* [pages] */
   int32_t* lens_out;           /* [sequences] */
 } kvq_pages_grow_args;

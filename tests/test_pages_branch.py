@@ -113,6 +113,7 @@ def test_call_refusals(L):
         assert grow(**{name: None}) == 1 and grow(**{name: p + 202}) == 1, name
     assert L.kvq_pages_grow(cache.handle, None, None) == 1
     assert grow(sequences=0) == 1 and grow(sequences=1025) == 1 and grow(table_stride=0) == 1
+    assert grow(sequences=1024, table_stride=1 << 21) == 2
     assert grow(lens_out=p + 20) == 1 and grow(lens_out=p + 8) == 1 and grow(table=p + 60) == 1 and grow(table=p + 12) == 1
     assert grow(refs=p + 4) == 1 and grow(lens_out=p + 84) == 1
     assert cache.kvq_pages_status() == 0

@@ -24,18 +24,21 @@
 // Scores, maxima, sums and O are fp32; weights are rounded once to the operand
 // type (p * 2^7, as in the few-rows kernel).
 //
-// Measured: 2048 new tokens at 30720, 32 query heads over 8 of 128, bf16 pages:
-// 818 to 833 us on different cards, 1.3 PFLOP/s (66 % of a large library product).
-// A CTA takes 418 blocks of two tiles, so a block takes 1.97 us, of which its
-// products would take 1.30 at the library product's rate: a tile's chain of scores,
-// softmax, value product and the signals between them is what is left (tensor pipe
-// active 54 % on a chunk half as long).  509 tokens at 130563, 16 query heads over 2
-// of 256, 4-bit keys and 8-bit values: 1444 us, 0.75 PFLOP/s (tensor pipe 29 % at
-// 16000), bound by the dequantizers (each CTA turns every code for 128 rows).  Prompts
-// of up to 2048 tokens, 40 heads of 128, window 1024: 367 us, tensor pipe 25 %.  A CTA
-// has 68 blocks there, in 10.5 pieces, which would take 134 us at the chunk's pace;
-// the rest (queries and outputs that no other piece covers, blocks with a mask, a
-// second read of the scores in each piece's first block) was not measured apart.
+// Measured: 2048 new tokens at 30720, 32 query heads over 8 of 128, bf16 pages: 790 us,
+// 1.35 PFLOP/s (71 % of a large library product).  A CTA takes 418 blocks of two tiles, so
+// a block takes 1.89 us, of which its products would take 1.34 at the library product's
+// rate: a tile's chain of scores, softmax, value product and the signals between them is
+// what is left.  509 tokens at 130563, 16 query heads over 2 of 256, 4-bit keys and 8-bit
+// values: 1261 us, 0.87 PFLOP/s: the dequantizers' traffic in shared memory slows the
+// products (each CTA turns every code for 128 rows), and keys come as two products of 64
+// columns.  Prompts of up to 2048 tokens, 40 heads of 128, window 1024: 335 us.  A CTA has
+// 68 blocks there, in 10.5 pieces, which would take 128 us at the chunk's pace; the rest
+// (queries and outputs that no other piece covers, blocks with a mask, a second read of
+// the scores in each piece's first block) was not measured apart.
+// Masked: 16 sequences with trees of 64 tokens over 1k to 16k bf16 tokens, 32 over 8 heads
+// of 128, 186 us (floor 105, bytes and products near each other); 125 drafted tokens at
+// 130900, 16 over 2 heads of 256, 4 and 8 bits, 342 us (floor 141, products); 8 decoder
+// prompts of up to 448 tokens over 8190 8-bit tokens, 326 us (floor 83, products).
 #pragma once
 
 #include "kvq_pages_attn.cuh"

@@ -15,9 +15,9 @@
 // spread over up to 8 warps.
 // Measured: norm of 65521 tokens, 18 heads of 256, fp16, 225 us (5.4 TB/s read and
 // written; a copy would take 180); append of 16 prompts of up to 4113 tokens, 40
-// heads of 128, fp16 pages, 401 us with a read-back of the stored rows; 8 prompts
+// heads of 128, fp16 pages, 392 us with a read-back of the stored rows; 8 prompts
 // of about 2000 tokens, 12 heads of 64, into 8- and 4-bit pages with the read-back
-// 51 us (floor 18: the codes' arithmetic); 64 single tokens, in a graph: norm
+// 46 us (floor 18: the codes' arithmetic); 64 single tokens, in a graph: norm
 // 3.7 us, append 6.6 us.
 #include <cuda_bf16.h>
 

@@ -7,10 +7,9 @@
 // tokens and copying pages are bound by memory.  Measured, each kernel alone with cold
 // caches: masks of 16 trees of 64 tokens 6 us; fork of 64 rows of 250 pages 6 + 4 us (table,
 // counts), of 256 rows of 1900 pages over a pool of 60000 6 + 5; growth of 64 rows by a
-// token 18 us and 6 for the copies of shared last pages, of 256 rows by up to 600 tokens
-// 31 + 6 (a warp a sequence instead of the line of entries: 10 and 23); 509 pages of 64
-// tokens, 40 heads of 128, 8- and 4-bit, four layers: 334 us, 6.5 TB/s read and written (96 %
-// of a copy).  Half of 8 sequences of 9k to 16k 4-bit tokens, 8 heads of 128, four layers at
+// token 10 us and 6 for the copies of shared last pages, of 256 rows by up to 600 tokens
+// 23 + 6; 509 pages of 64 tokens, 40 heads of 128, 8- and 4-bit, four layers: 334 us, 6.5
+// TB/s read and written (96 % of a copy).  Half of 8 sequences of 9k to 16k 4-bit tokens, 8 heads of 128, four layers at
 // once: 7 + 140 us, 3.0 TB/s: a (head, token) is 144 bytes in four pieces, and a warp's
 // access touches eleven lines of the L1 cache for four lines' worth of bytes.
 #include <algorithm>
@@ -552,7 +551,6 @@ __global__ void __launch_bounds__(kForkThreads) pages_refs_kernel(PagesView pv, 
 constexpr int kGrowThreads = kPagesMaxBatch;  // a thread per sequence
 constexpr int kGrowWarps = kGrowThreads / 32;
 constexpr int kScan = 16;                     // reference counts that a thread has in flight
-constexpr int kEntries = 4;                   // table entries that it has
 
 struct GrowArgs {
   kvq_pages_grow_args a;
@@ -560,16 +558,14 @@ struct GrowArgs {
   int32_t *number, *src, *dst;
 };
 
-// One CTA deals out the pages: what a sequence gets depends on all before it.  The
-// entries that the new tokens need, of all sequences one behind the other, are gone
-// through twice, kEntries a thread at a time, so that a pass costs a few loads in a
-// row whatever the sequences are.
+// One CTA deals out the pages: what a sequence gets depends on all before it.  A warp goes
+// through a sequence's entries.  (All entries in one line, four a thread: 18 us against 10
+// for 64 rows by a token, 31 against 23 for 256 rows by up to 600.)
 __global__ void __launch_bounds__(kGrowThreads) pages_grow_kernel(PagesView pv, GrowArgs g) {
-  __shared__ int page[kGrowThreads];   // the page that holds the sequence's last tokens and is grown into, or -1
-  __shared__ int first[kGrowThreads];  // first entry of the table that its new tokens need
-  __shared__ int line[kGrowThreads + 1];  // entries that the sequences before it need
-  __shared__ int from[kGrowThreads];   // fresh pages that they need (of sequences that need entries)
-  __shared__ bool copies[kGrowThreads], gets[kGrowThreads];
+  __shared__ int page[kGrowThreads];     // the page that holds the sequence's last tokens and is grown into, or -1
+  __shared__ int first[kGrowThreads], last[kGrowThreads];  // entries of the table that the new tokens need
+  __shared__ int need[kGrowThreads], from[kGrowThreads];   // fresh pages (then: does it get them?), and the first one's number
+  __shared__ bool copies[kGrowThreads];
   __shared__ int sums[32], found_in[kScan * kGrowWarps];
   const kvq_pages_grow_args& a = g.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, S = a.sequences;
@@ -577,8 +573,9 @@ __global__ void __launch_bounds__(kGrowThreads) pages_grow_kernel(PagesView pv, 
   pdl_trigger();
   // ---- each sequence's part of the table
   const long cap = min(a.table_stride << pv.lg_pt, 1L << 30);
-  int len = 0, n = 0, p = -1, entries = 0;
+  int len = 0, n = 0, p = -1;
   bool bad = false;
+  first[tid] = 0, last[tid] = -1;
   if (tid < S) {
     len = a.lens[tid];
     const long count = (long)a.q_start[tid + 1] - a.q_start[tid];
@@ -590,82 +587,48 @@ __global__ void __launch_bounds__(kGrowThreads) pages_grow_kernel(PagesView pv, 
         p = a.table[tid * a.table_stride + f];
         if ((unsigned)p >= (unsigned)pv.pages) bad = true, n = 0, p = -1;
       }
-      first[tid] = f;
-      if (n > 0) entries = ((len + n - 1) >> pv.lg_pt) - f + 1;
+      if (n > 0) first[tid] = f, last[tid] = (len + n - 1) >> pv.lg_pt;
     }
     if (bad && (len >= 0 || count < 0)) atomicOr(pv.err, 1);
   }
   page[tid] = p;
-  int all;
-  const int mine = block_scan(entries, sums, &all);
-  line[tid] = mine;
-  if (tid == 0) line[kGrowThreads] = all;
+  __syncthreads();
   bool copy = false;
   if (p >= 0) {
     const int r = a.refs[p];
     if (r > 1) {
       int before = 0;
-#pragma unroll 8
       for (int c = 0; c < tid; ++c) before += page[c] == p;
       copy = before < r - 1;
     }
   }
   copies[tid] = copy;
   __syncthreads();
-  // the sequence whose entries entry x of the line is among
-  auto owner = [&](int x) {
-    int lo = 0, hi = kGrowThreads;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (line[mid] <= x) lo = mid;
-      else hi = mid;
-    }
-    return lo;
-  };
-  // ---- entries that need a fresh page, counted, and marked in the table (nobody's counts
-  // may change before all have decided): -1, or -2 - the page that is replaced
-  int total = 0;
-  for (int x0 = 0; x0 < all; x0 += kGrowThreads * kEntries) {
-    const int x1 = x0 + tid * kEntries;
-    int32_t* e[kEntries];
-    int was[kEntries], b[kEntries];
-    bool at_first[kEntries];
-#pragma unroll
-    for (int k = 0; k < kEntries; ++k) {
-      b[k] = -1;
-      was[k] = 0;
-      if (x1 + k < all) {
-        b[k] = k && x1 + k < line[b[k - 1] + 1] ? b[k - 1] : owner(x1 + k);
-        const int i = x1 + k - line[b[k]];
-        at_first[k] = i == 0 && page[b[k]] >= 0;
-        e[k] = a.table + b[k] * a.table_stride + first[b[k]] + i;
-        was[k] = *e[k];
+  // Entries that need a fresh page, counted, and marked in the table (nobody's counts
+  // may change before all have decided): -1, or -2 - the page that is replaced.
+  for (int b = warp; b < S; b += kGrowWarps) {
+    int sum = 0;
+    for (int i = first[b] + lane; i <= last[b]; i += 32) {
+      int32_t* e = a.table + b * a.table_stride + i;
+      const int old = *e;
+      if ((unsigned)old >= (unsigned)pv.pages) {
+        if (old >= 0) atomicOr(pv.err, 1);
+        *e = -1;
+      } else if (i == first[b] && page[b] >= 0 ? copies[b] : a.refs[old] > 1) {
+        *e = -2 - old;
+      } else {
+        continue;
       }
+      ++sum;
     }
-    int want[kEntries], sum = 0;
-#pragma unroll
-    for (int k = 0; k < kEntries; ++k) {
-      want[k] = 0;
-      if (x1 + k >= all) continue;
-      if ((unsigned)was[k] >= (unsigned)pv.pages) {
-        if (was[k] >= 0) atomicOr(pv.err, 1);
-        *e[k] = -1;
-        want[k] = 1;
-      } else if (at_first[k] ? copies[b[k]] : a.refs[was[k]] > 1) {
-        *e[k] = -2 - was[k];
-        want[k] = 1;
-      }
-      sum += want[k];
-    }
-    int in, run = total + block_scan(sum, sums, &in);
-#pragma unroll
-    for (int k = 0; k < kEntries; ++k) {
-      if (x1 + k < all && x1 + k == line[b[k]]) from[b[k]] = run;
-      run += want[k];
-    }
-    total += in;
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == 0) need[b] = sum;
   }
   __syncthreads();
+  const int mine = tid < S ? need[tid] : 0;
+  int total;
+  const int at = block_scan(mine, sums, &total);
+  from[tid] = at;
   // ---- as many free pages as are wanted, the lowest first
   int found = 0;
   for (long p0 = 0; p0 < pv.pages && found < total; p0 += kScan * kGrowThreads) {
@@ -679,8 +642,8 @@ __global__ void __launch_bounds__(kGrowThreads) pages_grow_kernel(PagesView pv, 
     for (int k = 0; k < kScan; ++k)
       if (lane == 0) found_in[k * kGrowWarps + warp] = __popc(hit[k]);
     __syncthreads();
-    int in;
-    const int run = block_scan(tid < kScan * kGrowWarps ? found_in[tid] : 0, sums, &in);
+    int all;
+    const int run = block_scan(tid < kScan * kGrowWarps ? found_in[tid] : 0, sums, &all);
     if (tid < kScan * kGrowWarps) found_in[tid] = run;
     __syncthreads();
 #pragma unroll
@@ -689,54 +652,37 @@ __global__ void __launch_bounds__(kGrowThreads) pages_grow_kernel(PagesView pv, 
         const int to = found + found_in[k * kGrowWarps + warp] + __popc(hit[k] & ((1u << lane) - 1));
         if (to < total) g.fresh[to] = (int)(p0 + k * kGrowThreads + tid);
       }
-    found += in;
+    found += all;
     __syncthreads();
   }
-  // ---- who gets them: sequences in order, as far as the pages go.  What those up to
-  // this one need is what stands before the next one with entries.
-  const bool grows = n > 0;
-  int end = total;
-  if (grows && mine + entries < all) end = from[owner(mine + entries)];
-  const bool get = grows && end <= found;
-  gets[tid] = get;
-  if (tid < S) a.lens_out[tid] = bad ? (len < 0 ? len : -1 - len) : get ? len + n : grows ? -1 - len : len;
-  if (grows && !get) atomicOr(pv.err, 4);
+  // ---- who gets them: sequences in order, as far as the pages go
+  const bool grows = n > 0, gets = grows && at + mine <= found;
+  if (tid < S) a.lens_out[tid] = bad ? (len < 0 ? len : -1 - len) : gets ? len + n : grows ? -1 - len : len;
+  if (grows && !gets) atomicOr(pv.err, 4);
+  need[tid] = gets;
   int number;
-  const int slot = block_scan(get && copy, sums, &number);  // (its barriers publish the above)
+  const int slot = block_scan(gets && copy, sums, &number);  // (its barriers publish the above)
   if (tid == 0) *g.number = number;
-  if (get && copy) g.src[slot] = p, g.dst[slot] = g.fresh[from[tid]];
-  int run = 0;
-  for (int x0 = 0; x0 < all; x0 += kGrowThreads * kEntries) {
-    const int x1 = x0 + tid * kEntries;
-    int32_t* e[kEntries];
-    int was[kEntries], b = -1, sum = 0;
-    bool fill[kEntries];
-#pragma unroll
-    for (int k = 0; k < kEntries; ++k) {
-      was[k] = 0;
-      if (x1 + k < all) {
-        b = k && x1 + k < line[b + 1] ? b : owner(x1 + k);
-        e[k] = a.table + b * a.table_stride + first[b] + (x1 + k - line[b]);
-        fill[k] = gets[b];
-        was[k] = *e[k];
+  if (gets && copy) g.src[slot] = p, g.dst[slot] = g.fresh[at];
+  for (int b = warp; b < S; b += kGrowWarps) {
+    int run = from[b];
+    for (int i0 = first[b]; i0 <= last[b]; i0 += 32) {
+      const int i = i0 + lane;
+      int32_t* e = a.table + b * a.table_stride + i;
+      const int was = i <= last[b] ? *e : 0;
+      const unsigned hit = __ballot_sync(0xffffffffu, was < 0);
+      if (was < 0) {
+        if (need[b]) {
+          const int f = g.fresh[run + __popc(hit & ((1u << lane) - 1))];
+          *e = f;
+          a.refs[f] = 1;
+          if (was < -1) atomicSub(a.refs + (-2 - was), 1);
+        } else if (was < -1) {
+          *e = -2 - was;
+        }
       }
-      sum += was[k] < 0;
+      run += __popc(hit);
     }
-    int in, at = run + block_scan(sum, sums, &in);
-#pragma unroll
-    for (int k = 0; k < kEntries; ++k) {
-      if (was[k] >= 0) continue;
-      if (fill[k]) {
-        const int f = g.fresh[at];
-        *e[k] = f;
-        a.refs[f] = 1;
-        if (was[k] < -1) atomicSub(a.refs + (-2 - was[k]), 1);
-      } else if (was[k] < -1) {
-        *e[k] = -2 - was[k];
-      }
-      ++at;
-    }
-    run += in;
   }
 }
 

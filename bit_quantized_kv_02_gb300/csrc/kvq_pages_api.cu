@@ -488,8 +488,9 @@ kvq_status kvq_pages_status(kvq_pages_t P, void* stream) {
   if (e == cudaSuccess && word) e = cudaMemsetAsync(P->d_err, 0, sizeof(int), st);
   if (e != cudaSuccess) return cuda_result(P, e);
   if (word & 2) return fail(P, KVQ_ERR_DEVICE_TIMEOUT, "a device-side wait gave up");
-  if (word & 1) return fail(P, KVQ_ERR_BAD_INDEX, "a page, length or position was out of range");
-  return word ? fail(P, KVQ_ERR_OUT_OF_PAGES, "fewer free pages than the sequences needed") : KVQ_OK;
+  // (before the bad indices: the lengths of sequences without pages are such to the other calls)
+  if (word & 4) return fail(P, KVQ_ERR_OUT_OF_PAGES, "fewer free pages than the sequences needed");
+  return word ? fail(P, KVQ_ERR_BAD_INDEX, "a page, length or position was out of range") : KVQ_OK;
 }
 
 const char* kvq_pages_last_error(kvq_pages_t P) { return P ? P->last_error.c_str() : ""; }

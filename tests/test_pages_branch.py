@@ -746,6 +746,65 @@ def test_grow_reports_what_it_cannot_do():
 
 
 @gpu
+def test_a_step_of_sequences_without_pages_touches_nothing():
+    """The lengths that a refused growth leaves are skipped by every other call of the step."""
+    cache = kvq.KVQPages(kvq.make_pages_config(2, 2, 16, 2, 2, 64))
+    per = int(cache.bytes.packed)
+    cache.buffer[:per].random_(0, 256)
+    table, refs = ints([[0, -1], [1, -1]]), ints([1, 1])
+    lens = cache.kvq_pages_grow(starts([1, 1]), table, ints([16, 10]), refs)
+    # (the second has room in its page, but stands behind the first, which has none)
+    assert lens.tolist() == [-17, -11] and table.tolist() == [[0, -1], [1, -1]] and refs.tolist() == [1, 1]
+    before = cache.buffer[:per].clone()
+    batch = kvq.PagesBatch(starts([1, 1]), lens, table, 2, 1)
+    x = torch.randn((2, 2, 64), device="cuda").half()
+    fill_ = torch.full_like(x, 7.0)
+    tree = cache.kvq_pages_tree(ints([-1, -1]), batch)
+    for i in range(2):
+        cache.kvq_pages_append(i, x, x, batch)
+        cache.kvq_pages_tree_attn(i, x, batch, tree)  # (values of no meaning)
+        cache.kvq_pages_cross_attn(i, x, batch)
+        ko, vo = cache.kvq_pages_read(i, batch, fill_.clone(), fill_.clone())
+        assert (ko == 7).all() and (vo == 7).all()
+    kept_lens = cache.kvq_pages_keep(torch.ones(2, dtype=torch.bool, device="cuda"), batch)
+    assert cache.kvq_pages_status() == 8 and cache.kvq_pages_status() == 0
+    assert not tree.seen.any() and not tree.positions.any()
+    assert kept_lens.tolist() == [-17, -11]
+    assert torch.equal(cache.buffer[:per], before)
+    # the first gives its page back, the second grows into its own
+    table, lens, refs = cache.kvq_pages_fork(ints([-1, 1]), table, lens, refs)
+    again = ints([0, -1 - int(lens[1])])
+    assert cache.kvq_pages_grow(starts([0, 1]), table, again, refs).tolist() == [0, 11]
+    assert cache.kvq_pages_status() == 0 and refs.tolist() == [0, 1]
+
+
+@gpu
+def test_tree_and_cross_in_two_graphs_that_take_turns():
+    """Two captured attention calls of one cache share its workspace; replayed in turn on one stream, each
+    gives what it gives alone."""
+    c = make(([9, 40, 1], [900, 300, 2500]), 32, "bf16", (8, 2), 64, seed=11)
+    fill(c, 2, 64)
+    q = c.normal(c.rows, 8, 64).to(c.dtype).cuda()
+    batch = c.batch()
+    tree = c.cache.kvq_pages_tree(ints(sum([drafted(n, c.g) for n in c.news], [])), batch)
+    outs = [torch.zeros_like(q) for _ in range(2)]
+    calls = [lambda: c.cache.kvq_pages_tree_attn(0, q, batch, tree, out=outs[0]),
+             lambda: c.cache.kvq_pages_cross_attn(0, q, batch, out=outs[1])]
+    want = [call().clone() for call in calls]
+    graphs = []
+    for call in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append(g)
+    for turn in range(6):
+        outs[turn % 2].zero_()
+        graphs[turn % 2].replay()
+        graphs[1 - turn % 2].replay()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+@gpu
 def test_fork_of_bad_rows():
     cache = kvq.KVQPages(kvq.make_pages_config(1, 8, 16, 1, 1, 64))
     table = ints([[0, 1, 2], [3, 99, -1]])

@@ -199,12 +199,13 @@ cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, bool masked, int max_ro
   a.rows_hi = INT_MAX;
   if (P->which == 1 || (P->which == 0 && max_rows <= few)) return launch_rows(P, a, masked, max_rows, st);
   if (P->which == 2 || (a.bv.batch == 1 && (rows_given || P->L.k_bits != 16))) return launch_tile(P, a, masked, max_rows, st);
-  // Over codes the masked kernels take a mixed batch in one launch: the weights are
+  // Over codes the masked kernels take a batch that is known to be mixed in one launch (of
+  // one without the hint all sequences may have few rows): the weights are
   // rounded alike by both, the few-rows kernel would be its largest form, and its launch
   // and join cost 10 us.  32 trees of 1 to 31 tokens over 500 to 8192 4-bit tokens, 32 over
   // 8 heads of 128: 205 us with both, 202 with one (187 with three dequantizing warps a
   // tensor).
-  if (masked && P->L.k_bits != 16) return launch_tile(P, a, masked, max_rows, st);
+  if (masked && rows_given && P->L.k_bits != 16) return launch_tile(P, a, masked, max_rows, st);
   a.rows_lo = few;
   cudaError_t e = launch_tile(P, a, masked, max_rows, st);
   if (e != cudaSuccess) return e;

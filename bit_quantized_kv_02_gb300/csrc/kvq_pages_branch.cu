@@ -559,14 +559,18 @@ struct GrowArgs {
 };
 
 // One CTA deals out the pages: what a sequence gets depends on all before it.  A warp goes
-// through a sequence's entries.  (All entries in one line, four a thread: 18 us against 10
-// for 64 rows by a token, 31 against 23 for 256 rows by up to 600.)
+// through a sequence's entries, once to count the fresh pages that they need and, where the
+// sequence gets them, once to deal them out; one that does not get them, or that needs an
+// entry outside the pool, has not been written to (marks in the table, which the first
+// look left for the second, were 0.8 us faster).  (All entries in one line, four a
+// thread: 18 us against 10 for 64 rows by a token, 31 against 23 for 256 rows by up to 600.)
 __global__ void __launch_bounds__(kGrowThreads) pages_grow_kernel(PagesView pv, GrowArgs g) {
   __shared__ int page[kGrowThreads];     // the page that holds the sequence's last tokens and is grown into, or -1
   __shared__ int first[kGrowThreads], last[kGrowThreads];  // entries of the table that the new tokens need
   __shared__ int need[kGrowThreads], from[kGrowThreads];   // fresh pages (then: does it get them?), and the first one's number
   __shared__ bool copies[kGrowThreads];
   __shared__ int sums[32], found_in[kScan * kGrowWarps];
+  __shared__ int dealt;                  // fresh pages that are dealt out
   const kvq_pages_grow_args& a = g.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, S = a.sequences;
   pdl_wait();
@@ -576,6 +580,7 @@ __global__ void __launch_bounds__(kGrowThreads) pages_grow_kernel(PagesView pv, 
   int len = 0, n = 0, p = -1;
   bool bad = false;
   first[tid] = 0, last[tid] = -1;
+  if (tid == 0) dealt = 0;
   if (tid < S) {
     len = a.lens[tid];
     const long count = (long)a.q_start[tid + 1] - a.q_start[tid];
@@ -593,6 +598,27 @@ __global__ void __launch_bounds__(kGrowThreads) pages_grow_kernel(PagesView pv, 
   }
   page[tid] = p;
   __syncthreads();
+  // entries that need a fresh page, but for the one that is grown into; -1: one lies outside the pool
+  for (int b = warp; b < S; b += kGrowWarps) {
+    int sum = 0;
+    bool out = false;
+    for (int i = first[b] + lane; i <= last[b]; i += 32) {
+      const int old = a.table[b * a.table_stride + i];
+      if (old >= pv.pages) out = true;
+      else if (old < 0 || ((i != first[b] || page[b] < 0) && a.refs[old] > 1)) ++sum;
+    }
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (__any_sync(0xffffffffu, out)) sum = -1;
+    if (lane == 0) need[b] = sum;
+  }
+  __syncthreads();
+  // (before the growers into a page are counted: a sequence that stays holds on to it)
+  if (tid < S && need[tid] < 0) {
+    atomicOr(pv.err, 1);
+    bad = true, n = 0, p = -1;
+    page[tid] = -1, last[tid] = first[tid] - 1, need[tid] = 0;
+  }
+  __syncthreads();
   bool copy = false;
   if (p >= 0) {
     const int r = a.refs[p];
@@ -603,29 +629,7 @@ __global__ void __launch_bounds__(kGrowThreads) pages_grow_kernel(PagesView pv, 
     }
   }
   copies[tid] = copy;
-  __syncthreads();
-  // Entries that need a fresh page, counted, and marked in the table (nobody's counts
-  // may change before all have decided): -1, or -2 - the page that is replaced.
-  for (int b = warp; b < S; b += kGrowWarps) {
-    int sum = 0;
-    for (int i = first[b] + lane; i <= last[b]; i += 32) {
-      int32_t* e = a.table + b * a.table_stride + i;
-      const int old = *e;
-      if ((unsigned)old >= (unsigned)pv.pages) {
-        if (old >= 0) atomicOr(pv.err, 1);
-        *e = -1;
-      } else if (i == first[b] && page[b] >= 0 ? copies[b] : a.refs[old] > 1) {
-        *e = -2 - old;
-      } else {
-        continue;
-      }
-      ++sum;
-    }
-    sum = __reduce_add_sync(0xffffffffu, sum);
-    if (lane == 0) need[b] = sum;
-  }
-  __syncthreads();
-  const int mine = tid < S ? need[tid] : 0;
+  const int mine = tid < S ? need[tid] + copy : 0;
   int total;
   const int at = block_scan(mine, sums, &total);
   from[tid] = at;
@@ -660,30 +664,37 @@ __global__ void __launch_bounds__(kGrowThreads) pages_grow_kernel(PagesView pv, 
   if (tid < S) a.lens_out[tid] = bad ? (len < 0 ? len : -1 - len) : gets ? len + n : grows ? -1 - len : len;
   if (grows && !gets) atomicOr(pv.err, 4);
   need[tid] = gets;
+  if (gets) atomicMax(&dealt, at + mine);
+  const int target = gets && copy ? g.fresh[at] : 0;  // (a copy is its sequence's first)
   int number;
   const int slot = block_scan(gets && copy, sums, &number);  // (its barriers publish the above)
   if (tid == 0) *g.number = number;
-  if (gets && copy) g.src[slot] = p, g.dst[slot] = g.fresh[at];
+  if (gets && copy) g.src[slot] = p, g.dst[slot] = target;
+  // An entry takes its fresh page and leaves there what it named: nobody's count may fall
+  // before all have been looked at.  (The count of a page that was free is not above 1
+  // before or after.)
   for (int b = warp; b < S; b += kGrowWarps) {
+    if (!need[b]) continue;
     int run = from[b];
     for (int i0 = first[b]; i0 <= last[b]; i0 += 32) {
       const int i = i0 + lane;
       int32_t* e = a.table + b * a.table_stride + i;
-      const int was = i <= last[b] ? *e : 0;
-      const unsigned hit = __ballot_sync(0xffffffffu, was < 0);
-      if (was < 0) {
-        if (need[b]) {
-          const int f = g.fresh[run + __popc(hit & ((1u << lane) - 1))];
-          *e = f;
-          a.refs[f] = 1;
-          if (was < -1) atomicSub(a.refs + (-2 - was), 1);
-        } else if (was < -1) {
-          *e = -2 - was;
-        }
+      const bool in = i <= last[b];
+      const int old = in ? *e : 0;
+      const bool takes = in && (old < 0 || (i == first[b] && page[b] >= 0 ? copies[b] : a.refs[old] > 1));
+      const unsigned hit = __ballot_sync(0xffffffffu, takes);
+      if (takes) {
+        const int k = run + __popc(hit & ((1u << lane) - 1)), f = g.fresh[k];
+        *e = f;
+        a.refs[f] = 1;
+        g.fresh[k] = old;
       }
       run += __popc(hit);
     }
   }
+  __syncthreads();
+  for (int k = tid; k < dealt; k += kGrowThreads)
+    if (g.fresh[k] >= 0) atomicSub(a.refs + g.fresh[k], 1);
 }
 
 int fork_blocks(long entries) { return (int)((entries + kForkThreads * kForkEntries - 1) / (kForkThreads * kForkEntries)); }

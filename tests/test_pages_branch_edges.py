@@ -1,0 +1,69 @@
+"""Branching sequences on the paged cache where tables, lengths and arguments are not as they should be."""
+import os
+
+import pytest
+import torch
+
+from bit_quantized_kv_02_gb300 import build, kvq
+from tests.test_pages_branch import ints, starts
+
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def L():
+    if not os.path.exists(kvq.LIB_PATH):
+        build.build()
+    return kvq.lib()
+
+
+# ---------------------------------------------------------------------- grow --
+
+@gpu
+@pytest.mark.parametrize("bad_first", [True, False])
+@pytest.mark.parametrize("entry", [8, 99, 2 ** 31 - 1])
+def test_grow_leaves_a_sequence_that_needs_an_entry_outside_the_pool(entry, bad_first):
+    """Such a sequence stays as it was, table and length, wherever among the needed entries the bad one stands; the
+    others grow, and one that shares its last page copies it, as the sequence that stayed still holds it."""
+    cache = kvq.KVQPages(kvq.make_pages_config(2, 8, 16, 1, 1, 64))
+    per = int(cache.bytes.packed) // 2
+    cache.buffer[:2 * per].copy_(torch.randint(0, 256, (2 * per,), generator=torch.Generator().manual_seed(0)).to(torch.uint8))
+    pages = cache.buffer[:2 * per].clone().view(2, 8, -1)
+    rows = [([2, entry, -1], 5, 15),   # shares page 2; needs entries 0 and 1
+            ([2, -1, -1], 5, 3),       # grows into page 2
+            ([4, -1, entry], 16, 20),  # a free page, then the bad entry
+            ([5, entry, -1], 16, 0),   # needs nothing
+            ([6, -1, entry], 10, 10)]  # the bad entry stands behind what it needs
+    if not bad_first:
+        rows[0], rows[1] = rows[1], rows[0]
+    table, lens, refs = ints([r[0] for r in rows]), ints([r[1] for r in rows]), ints([0, 0, 2, 0, 1, 1, 1, 0])
+    out = cache.kvq_pages_grow(starts([r[2] for r in rows]), table, lens, refs)
+    assert cache.kvq_pages_status() == 7
+    want = [list(r[0]) for r in rows]
+    grown = 1 if bad_first else 0
+    want[grown][0], want[4][1] = 0, 1
+    assert table.tolist() == want
+    assert out.tolist() == [-6 if b != grown else 8 for b in range(2)] + [-17, 16, 20]
+    assert refs.tolist() == [1, 1, 1, 0, 1, 1, 1, 0]
+    pages[:, 0] = pages[:, 2]
+    assert torch.equal(cache.buffer[:2 * per].view(2, 8, -1), pages)
+    assert cache.kvq_pages_status() == 0
+
+
+@gpu
+def test_grow_without_pages_changes_no_entry():
+    """Sequences that find no page keep their tables: any negative entry is none and stays what it was, shared pages
+    and pages behind the tokens included."""
+    cache = kvq.KVQPages(kvq.make_pages_config(1, 4, 16, 1, 1, 64))
+    before = [[0, -5, -1], [1, 2, -7], [1, 2, -2147483648], [3, -3, -4]]
+    table, refs = ints(before), ints([1, 2, 2, 1])
+    lens = ints([16, 20, 12, 16])
+    out = cache.kvq_pages_grow(starts([1, 20, 9, 0]), table, lens, refs)
+    assert cache.kvq_pages_status() == 8
+    assert out.tolist() == [-17, -21, -13, 16]
+    assert table.tolist() == before and refs.tolist() == [1, 2, 2, 1]
+    # with pages, the same entries are taken as none
+    table, refs = ints([[0, -5, -1], [1, -7, -2147483648]]), ints([1, 1, 0, 0])
+    out = cache.kvq_pages_grow(starts([3, 16]), table, ints([16, 8]), refs)
+    assert cache.kvq_pages_status() == 0 and out.tolist() == [19, 24]
+    assert table.tolist() == [[0, 2, -1], [1, 3, -2147483648]] and refs.tolist() == [1, 1, 1, 1]

@@ -136,6 +136,18 @@ bool overlap(const void* out, const void* in, int64_t rows, int64_t bytes, int64
   return r < rows && i + r * stride < o + rows * bytes;
 }
 
+// Do two arrays of so many bytes share one?
+bool meet(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+// Does an array of so many bytes share one with those of the batch?
+bool over_batch(const void* a, int64_t bytes, const BatchView& v) {
+  return meet(a, bytes, v.q_start, 4 * (v.batch + 1L)) || meet(a, bytes, v.lens, 4L * v.batch) ||
+         meet(a, bytes, v.table, 4L * v.batch * v.stride);
+}
+
 // Handle, layer and current device.
 kvq_status usable(kvq_pages* P, int layer) {
   if (!P) return KVQ_ERR_INVALID_ARG;
@@ -252,10 +264,7 @@ kvq_status usable_layers(kvq_pages* P, int layer, PagesView* pv, int* layers) {
 }
 
 // Do two arrays of 32-bit integers share one?
-bool share(const int32_t* a, int64_t na, const int32_t* b, int64_t nb) {
-  return reinterpret_cast<uintptr_t>(a) < reinterpret_cast<uintptr_t>(b + nb) &&
-         reinterpret_cast<uintptr_t>(b) < reinterpret_cast<uintptr_t>(a + na);
-}
+bool share(const int32_t* a, int64_t na, const int32_t* b, int64_t nb) { return meet(a, 4 * na, b, 4 * nb); }
 
 }  // namespace
 
@@ -395,9 +404,10 @@ kvq_status kvq_pages_keep(kvq_pages_t P, int layer, const kvq_pages_batch* batch
   if (s != KVQ_OK) return s;
   if (!keep && bv.new_tokens > 0) return fail(P, KVQ_ERR_INVALID_ARG, "null marks");
   if (!fits(lens_out, 4)) return fail(P, KVQ_ERR_INVALID_ARG, "lengths not 4-byte aligned");
-  if (lens_out && (share(lens_out, bv.batch, bv.lens, bv.batch) || share(lens_out, bv.batch, bv.q_start, bv.batch + 1) ||
-                   share(lens_out, bv.batch, bv.table, bv.batch * bv.stride)))
+  if (lens_out && over_batch(lens_out, 4L * bv.batch, bv))
     return fail(P, KVQ_ERR_INVALID_ARG, "new lengths over the batch's arrays");
+  if (lens_out && meet(lens_out, 4L * bv.batch, keep, bv.new_tokens))
+    return fail(P, KVQ_ERR_INVALID_ARG, "new lengths over the marks");
   if (bv.new_tokens == 0 && !lens_out) return KVQ_OK;
   const int max_new = batch->max_new > 0 && batch->max_new < bv.new_tokens ? batch->max_new : bv.new_tokens;
   return cuda_result(P, launch_pages_keep(pv, layers, (long)P->layer_bytes, bv, max_new, keep, lens_out, P->d_keep,

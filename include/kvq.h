@@ -484,7 +484,7 @@ kvq_status kvq_pages_read(kvq_pages_t pages, int layer, const kvq_pages_batch* b
 /* Keep some of a sequence's new tokens and close the gaps: keep [new_tokens] (device
  * bytes) is nonzero for the rows to keep; the j-th kept row of sequence b moves to
  * position lens[b] - n + j, metadata included, keys as they were turned.  lens_out
- * (device [batch], apart from the batch's arrays; NULL: not wanted) becomes lens[b] - n + the number
+ * (device [batch], apart from keep and the batch's arrays; NULL: not wanted) becomes lens[b] - n + the number
  * kept: the accepted branch of a drafted tree, or, with q_start spanning whole
  * sequences, what is left of an evicted cache.  Positions from lens_out[b] on hold
  * what they held, or rows that moved.  Rows with a negative position are no tokens;

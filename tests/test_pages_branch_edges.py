@@ -1,4 +1,5 @@
 """Branching sequences on the paged cache where tables, lengths and arguments are not as they should be."""
+import ctypes
 import os
 
 import pytest
@@ -67,3 +68,38 @@ def test_grow_without_pages_changes_no_entry():
     out = cache.kvq_pages_grow(starts([3, 16]), table, ints([16, 8]), refs)
     assert cache.kvq_pages_status() == 0 and out.tolist() == [19, 24]
     assert table.tolist() == [[0, 2, -1], [1, 3, -2147483648]] and refs.tolist() == [1, 1, 1, 1]
+
+
+# ----------------------------------------------------- outputs over what is read --
+
+class Room:
+    """Arrays of a batch of two sequences with 70 new tokens in all, each in a kilobyte of its own."""
+
+    def __init__(self):
+        self.cache = kvq.KVQPages(kvq.make_pages_config(1, 8, 16, 4, 2, 64))
+        self.memory = torch.zeros(64 << 10, dtype=torch.uint8, device="cuda")
+        self.q_start, self.lens, self.table = (self.memory.data_ptr() + 1024 * i for i in range(1, 4))
+        self.batch = kvq._PagesBatch(2, 70, 0, self.q_start, self.lens, self.table, 5)
+        self.ref = ctypes.byref(self.batch)
+        # (all lengths and sequences are empty: a call that is not refused has nothing to do)
+
+    def at(self, kilobyte):
+        return self.memory.data_ptr() + 1024 * kilobyte
+
+    def over_the_batch(self, size):
+        """Addresses of an array of `size` bytes that meets one of the batch's in its first or last integer."""
+        for a, n in ((self.q_start, 3), (self.lens, 2), (self.table, 10)):
+            yield from (a + 4 * (n - 1), a - size + 4)
+
+
+@gpu
+def test_keep_refuses_lengths_over_the_marks(L):
+    r = Room()
+    for marks in (r.at(8), r.at(8) + 3):
+        for lens_out in range(r.at(8) - 16, r.at(8) + 96, 4):
+            meets = lens_out < marks + 70 and marks < lens_out + 8
+            assert L.kvq_pages_keep(r.cache.handle, 0, r.ref, marks, lens_out, None) == int(meets), lens_out - marks
+    assert L.kvq_pages_keep(r.cache.handle, 0, r.ref, r.at(8), None, None) == 0
+    for lens_out in r.over_the_batch(8):
+        assert L.kvq_pages_keep(r.cache.handle, 0, r.ref, r.at(8), lens_out, None) == 1
+    assert r.cache.kvq_pages_status() == 0

@@ -389,6 +389,10 @@ kvq_status kvq_pages_tree(kvq_pages_t P, const kvq_pages_batch* batch, const int
   if (!parents || !seen) return fail(P, KVQ_ERR_INVALID_ARG, "null parents or masks");
   if (!fits(parents, 4) || !fits(seen, 8) || !fits(positions, 4))
     return fail(P, KVQ_ERR_INVALID_ARG, "tree not aligned to its types");
+  const int64_t ints = 4L * bv.new_tokens, masks = 8L * bv.new_tokens * words;
+  if (meet(seen, masks, parents, ints) || over_batch(seen, masks, bv) ||
+      (positions && (meet(positions, ints, parents, ints) || over_batch(positions, ints, bv) || meet(positions, ints, seen, masks))))
+    return fail(P, KVQ_ERR_INVALID_ARG, "masks or positions over each other or over what is read");
   return cuda_result(P, launch_pages_tree(pages_view(P, 0), bv, parents, words, seen, positions,
                                           static_cast<cudaStream_t>(stream)));
 }

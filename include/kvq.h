@@ -447,8 +447,9 @@ typedef struct {
  * NULL, positions (lens[b] - n + the number of ancestors: the kvq_rope positions of
  * the step).  A parent that is neither is taken as -1 and reported; the rows of a
  * sequence whose indices are out of range, or with more than 64 * words new tokens,
- * are left as they were and reported (KVQ_ERR_BAD_INDEX).  One call serves all
- * layers of a step. */
+ * are left as they were and reported (KVQ_ERR_BAD_INDEX).  seen and positions lie
+ * apart from each other, from parents and from the batch's arrays.  One call serves
+ * all layers of a step. */
 kvq_status kvq_pages_tree(kvq_pages_t pages, const kvq_pages_batch* batch, const int32_t* parents, int words,
                           uint64_t* seen, int32_t* positions, void* stream);
 

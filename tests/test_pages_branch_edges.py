@@ -86,10 +86,10 @@ class Room:
     def at(self, kilobyte):
         return self.memory.data_ptr() + 1024 * kilobyte
 
-    def over_the_batch(self, size):
-        """Addresses of an array of `size` bytes that meets one of the batch's in its first or last integer."""
+    def over_the_batch(self, size, align=4):
+        """Addresses of an array of `size` bytes that meets one of the batch's at its end or its beginning."""
         for a, n in ((self.q_start, 3), (self.lens, 2), (self.table, 10)):
-            yield from (a + 4 * (n - 1), a - size + 4)
+            yield from (a + 4 * (n - 1) & -align, a - size + 4 + align - 1 & -align)
 
 
 @gpu
@@ -102,4 +102,30 @@ def test_keep_refuses_lengths_over_the_marks(L):
     assert L.kvq_pages_keep(r.cache.handle, 0, r.ref, r.at(8), None, None) == 0
     for lens_out in r.over_the_batch(8):
         assert L.kvq_pages_keep(r.cache.handle, 0, r.ref, r.at(8), lens_out, None) == 1
+    assert r.cache.kvq_pages_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("words", [1, 3])
+def test_tree_refuses_outputs_over_each_other_and_over_what_it_reads(L, words):
+    r = Room()
+    masks = 70 * 8 * words
+
+    def tree(parents=r.at(8), seen=r.at(16), positions=r.at(24)):
+        return L.kvq_pages_tree(r.cache.handle, r.ref, parents, words, seen, positions, None)
+
+    assert tree() == 0 and tree(positions=None) == 0
+    # parents end where the masks begin, the positions where parents do, and so on
+    assert tree(parents=r.at(16) - 280) == 0 and tree(parents=r.at(16) + masks) == 0
+    assert tree(positions=r.at(8) - 280) == 0 and tree(positions=r.at(8) + 280) == 0
+    assert tree(positions=r.at(16) - 280) == 0 and tree(positions=r.at(16) + masks) == 0
+    # one integer further
+    assert tree(parents=r.at(16) - 276) == 1 and tree(parents=r.at(16) + masks - 4) == 1
+    assert tree(positions=r.at(8)) == 1 and tree(positions=r.at(8) - 276) == 1 and tree(positions=r.at(8) + 276) == 1
+    assert tree(positions=r.at(16) - 276) == 1 and tree(positions=r.at(16) + masks - 4) == 1
+    assert tree(seen=r.at(8)) == 1 and tree(seen=r.at(8), positions=None) == 1
+    for a in r.over_the_batch(masks, 8):
+        assert tree(seen=a) == 1
+    for a in r.over_the_batch(280):
+        assert tree(positions=a) == 1
     assert r.cache.kvq_pages_status() == 0

@@ -229,6 +229,11 @@ kvq_status attend(kvq_pages_t P, int layer, const void* q, int q_dtype, int64_t 
   if (reinterpret_cast<uintptr_t>(out) & 15) return fail(P, KVQ_ERR_INVALID_ARG, "output not 16-byte aligned");
   if (overlap(out, q, bv.new_tokens, (int64_t)c.q_heads * c.head_dim * 2, q_stride * 2))
     return fail(P, KVQ_ERR_INVALID_ARG, "output and queries overlap");
+  const int64_t out_bytes = (int64_t)bv.new_tokens * c.q_heads * c.head_dim * 2;
+  if (over_batch(out, out_bytes, bv)) return fail(P, KVQ_ERR_INVALID_ARG, "output over the batch's arrays");
+  if (tree && (meet(out, out_bytes, tree->seen, 8L * bv.new_tokens * tree->words) ||
+               (tree->positions && meet(out, out_bytes, tree->positions, 4L * bv.new_tokens))))
+    return fail(P, KVQ_ERR_INVALID_ARG, "output over the tree's arrays");
   AttnArgs a = {};
   a.pv = pages_view(P, layer);
   a.bv = bv;

@@ -416,7 +416,7 @@ kvq_status kvq_pages_append(kvq_pages_t pages, int layer, const void* k, const v
  * 256) over 16-bit pages they also keep what that rounding leaves.  A sequence's
  * rounding depends on its own rows alone (in a batch of one on max_new, if given).
  * q: device rows of [q_heads][head_dim] of q_dtype, q_stride elements apart; out: device [new_tokens][q_heads][head_dim]
- * of q_dtype, contiguous, 16-byte aligned, apart from q.  q_dtype: the pages'
+ * of q_dtype, contiguous, 16-byte aligned, apart from q and the batch's arrays.  q_dtype: the pages'
  * dtype, or KVQ_F16 / KVQ_BF16 over quantized pages.  Query head h reads KV head h / (q_heads / kv_heads).
  * softmax_scale: finite; <= 0 means 1/sqrt(head_dim).  A row that sees no token yields
  * zeros; what pages hold behind a sequence's end has no effect.  Cached values
@@ -456,7 +456,7 @@ kvq_status kvq_pages_tree(kvq_pages_t pages, const kvq_pages_batch* batch, const
 /* kvq_pages_attn where the new tokens form a tree: row i sees the tokens of its
  * sequence before the new ones (with window > 0, those at t > positions[i] - window)
  * and the new tokens that `seen` names, any mask being allowed.  Everything else as
- * there; cached values of all new tokens must be finite.  window: 0, or at least
+ * there, out apart from the tree's arrays too; cached values of all new tokens must be finite.  window: 0, or at least
  * 64 * words (KVQ_ERR_UNSUPPORTED otherwise).  The rows of a sequence with more new
  * tokens than that come out without meaning and are reported. */
 kvq_status kvq_pages_tree_attn(kvq_pages_t pages, int layer, const void* q, int q_dtype, int64_t q_stride,

@@ -129,3 +129,29 @@ def test_tree_refuses_outputs_over_each_other_and_over_what_it_reads(L, words):
     for a in r.over_the_batch(280):
         assert tree(positions=a) == 1
     assert r.cache.kvq_pages_status() == 0
+
+
+@gpu
+def test_attention_refuses_an_output_over_what_it_reads(L):
+    r = Room()
+    size = 70 * 4 * 64 * 2
+    q = torch.zeros((70, 4, 64), dtype=torch.float16, device="cuda")
+    free = r.at(12)
+    assert size == 35 << 10
+
+    def calls(out, seen=r.at(5), words=2, positions=r.at(8)):
+        tree = ctypes.byref(kvq._Tree(seen, words, positions))
+        return (L.kvq_pages_tree_attn(r.cache.handle, 0, q.data_ptr(), 0, 256, r.ref, tree, 0.0, 0, out, None),
+                L.kvq_pages_attn(r.cache.handle, 0, q.data_ptr(), 0, 256, r.ref, 0.0, 0, out, None),
+                L.kvq_pages_cross_attn(r.cache.handle, 0, q.data_ptr(), 0, 256, r.ref, 0.0, out, None))
+
+    assert calls(free) == (0, 0, 0)
+    for out in r.over_the_batch(size, 16):
+        assert calls(out) == (1, 1, 1)
+    # masks and positions that end where the output begins and begin where it ends, and ones that meet it
+    assert calls(free, seen=free - 1120) == calls(free, positions=free - 280) == (0, 0, 0)
+    assert calls(free, seen=free + size) == calls(free, positions=free + size) == (0, 0, 0)
+    for kw in (dict(seen=free - 1112), dict(seen=free + size - 8), dict(positions=free - 276), dict(positions=free + size - 4)):
+        assert calls(free, **kw) == (1, 0, 0), kw
+    assert calls(free, positions=None) == (0, 0, 0)
+    assert r.cache.kvq_pages_status() == 0

@@ -45,7 +45,7 @@ struct PagesView {
   PagesLayout L;
   int pages, heads, head_dim;
   int lg_pt;       // log2(page_tokens)
-  int* err;        // bit 0: bad index, bit 1: a wait gave up, bit 2: no free pages
+  int* err;        // bit 0: bad index, bit 1: a wait gave up, bit 2: no free pages, bit 3: negative length
 };
 
 __host__ __device__ inline long page_head_bytes(const PagesView& p) {

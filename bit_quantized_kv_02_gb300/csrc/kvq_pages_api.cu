@@ -4,6 +4,7 @@
 #include <cfloat>
 #include <climits>
 #include <cmath>
+#include <cstdio>
 #include <cstring>
 #include <new>
 
@@ -506,10 +507,21 @@ kvq_status kvq_pages_status(kvq_pages_t P, void* stream) {
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e == cudaSuccess && word) e = cudaMemsetAsync(P->d_err, 0, sizeof(int), st);
   if (e != cudaSuccess) return cuda_result(P, e);
-  if (word & 2) return fail(P, KVQ_ERR_DEVICE_TIMEOUT, "a device-side wait gave up");
-  // (before the bad indices: the lengths of sequences without pages are such to the other calls)
-  if (word & 4) return fail(P, KVQ_ERR_OUT_OF_PAGES, "fewer free pages than the sequences needed");
-  return word ? fail(P, KVQ_ERR_BAD_INDEX, "a page, length or position was out of range") : KVQ_OK;
+  if (!word) return KVQ_OK;
+  // A wrong page shows nowhere else, so it goes before pages that ran out, which the
+  // lengths tell; the lengths that those leave go behind.
+  const kvq_status first = word & 2   ? KVQ_ERR_DEVICE_TIMEOUT
+                           : word & 1 ? KVQ_ERR_BAD_INDEX
+                           : word & 4 ? KVQ_ERR_OUT_OF_PAGES
+                                      : KVQ_ERR_BAD_INDEX;
+  const char* const index = word & 1   ? "a page, length or position was out of range"
+                            : word & 4 ? nullptr
+                                       : "a length was negative";
+  char why[160] = "";
+  for (const char* s : {word & 2 ? "a device-side wait gave up" : nullptr, index,
+                        word & 4 ? "fewer free pages than the sequences needed" : nullptr})
+    if (s) std::snprintf(why + std::strlen(why), sizeof(why) - std::strlen(why), "%s%s", *why ? "; " : "", s);
+  return fail(P, first, why);
 }
 
 const char* kvq_pages_last_error(kvq_pages_t P) { return P ? P->last_error.c_str() : ""; }

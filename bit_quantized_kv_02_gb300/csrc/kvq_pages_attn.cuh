@@ -154,6 +154,12 @@ __device__ __forceinline__ Seq load_seq(const PagesView& pv, const BatchView& bv
   return s;
 }
 
+// What is recorded of a sequence that load_seq calls bad.  A negative length, which growth
+// leaves where pages ran out, has a bit of its own.
+__device__ __forceinline__ int seq_error(const BatchView& bv, int b, const Seq& s) {
+  return bv.lens[b] < 0 && bv.q_start[b] == s.s0 && bv.q_start[b + 1] == s.s0 + s.n ? 8 : 1;
+}
+
 // A sequence as attention takes it.  MASK: rows see the tokens before p0, and of
 // those from p0 on the ones that a.seen names; without a.seen all tokens lie before p0.
 template <bool MASK>
@@ -263,7 +269,7 @@ __device__ __forceinline__ void plan_work(const AttnArgs& a, Work<BK, ROWS>* w, 
       const Seq s = attn_seq<MASK>(a, b, &bad);
       pre[b + 1] = seq_units_serial<BK, ROWS, MASK>(a, s, &one);
       alone = alone && one;
-      if (bad) atomicOr(a.pv.err, 1);
+      if (bad) atomicOr(a.pv.err, seq_error(a.bv, b, s));
     }
   } else {
     for (int b = warp; b < a.bv.batch; b += warps) {
@@ -272,7 +278,7 @@ __device__ __forceinline__ void plan_work(const AttnArgs& a, Work<BK, ROWS>* w, 
       const long u = seq_units<BK, ROWS, MASK>(a, s, lane);
       if (lane == 0) {
         pre[b + 1] = u;
-        if (bad) atomicOr(a.pv.err, 1);
+        if (bad) atomicOr(a.pv.err, seq_error(a.bv, b, s));
       }
     }
   }

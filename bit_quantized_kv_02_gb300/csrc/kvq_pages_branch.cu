@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kTreeThreads) pages_tree_kernel(PagesView pv, 
   bool bad;
   const Seq s = load_seq(pv, bv, b, &bad);
   if (bad || s.n > 64 * words) {  // (the same for all threads)
-    if (i == 0) atomicOr(pv.err, 1);
+    if (i == 0) atomicOr(pv.err, seq_error(bv, b, s));
     return;
   }
   const long row = (long)s.s0 + i;
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kKeepThreads) pages_keep_kernel(PagesView pv, 
   const Seq s = load_seq(pv, bv, b, &bad);
   if (bad) {
     if (blockIdx.x == 0 && tid == 0) {
-      atomicOr(pv.err, 1);
+      atomicOr(pv.err, seq_error(bv, b, s));
       if (lens_out) lens_out[b] = bv.lens[b];
     }
     return;
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_keep_plan_kernel(PagesView
     if (b == 0) plan->ticket = 0;
     if (full ? base <= kKeepSegs : b == (int)gridDim.x - 1) plan->segments = full ? base : base + segs;
     if (bad || full) {
-      atomicOr(pv.err, 1);
+      atomicOr(pv.err, full ? 1 : seq_error(bv, b, s));
       if (lens_out) lens_out[b] = bv.lens[b];
     }
   }

@@ -299,7 +299,7 @@ __device__ __forceinline__ void find_places(const PagesView& pv, const BatchView
     bool bad;
     const Seq s = load_seq(pv, bv, b, &bad);
     if (bad) {  // its clamped rows would stand at other positions: none is touched
-      if (t0 == 0) atomicOr(pv.err, 1);  // (one block reports)
+      if (t0 == 0) atomicOr(pv.err, seq_error(bv, b, s));  // (one block reports)
       misfit = 1;
       continue;
     }

@@ -560,8 +560,10 @@ kvq_status kvq_pages_grow(kvq_pages_t pages, const kvq_pages_grow_args* args, vo
 kvq_status kvq_pages_set_kernel(kvq_pages_t pages, int which);
 
 /* Synchronise `stream` and report what a kernel on this handle recorded since
- * the last call: KVQ_ERR_DEVICE_TIMEOUT, KVQ_ERR_OUT_OF_PAGES, KVQ_ERR_BAD_INDEX
- * (the first that holds), or a pending CUDA error (KVQ_ERR_CUDA).  Clears the record. */
+ * the last call, or a pending CUDA error (KVQ_ERR_CUDA).  Of several the first in
+ * this order: KVQ_ERR_DEVICE_TIMEOUT, KVQ_ERR_BAD_INDEX, KVQ_ERR_OUT_OF_PAGES (the
+ * lengths of kvq_pages_grow tell it too), KVQ_ERR_BAD_INDEX of negative lengths alone
+ * (which such a growth leaves); kvq_pages_last_error names all.  Clears the record. */
 kvq_status kvq_pages_status(kvq_pages_t pages, void* stream);
 
 /* Message of the last error seen by this handle ("" if none). */

@@ -18,6 +18,10 @@ def L():
     return kvq.lib()
 
 
+def said(cache):
+    return cache._lib.kvq_pages_last_error(cache.handle).decode()
+
+
 # ---------------------------------------------------------------------- grow --
 
 @gpu
@@ -68,6 +72,39 @@ def test_grow_without_pages_changes_no_entry():
     out = cache.kvq_pages_grow(starts([3, 16]), table, ints([16, 8]), refs)
     assert cache.kvq_pages_status() == 0 and out.tolist() == [19, 24]
     assert table.tolist() == [[0, 2, -1], [1, 3, -2147483648]] and refs.tolist() == [1, 1, 1, 1]
+
+
+# -------------------------------------------------------------------- status --
+
+@gpu
+def test_a_bad_page_is_reported_in_a_step_that_runs_out_of_pages():
+    """Lengths tell that pages ran out; that a page was wrong shows in the status alone, so it comes first.  The
+    lengths that such a growth leaves are no fault of their own beside it."""
+    cache = kvq.KVQPages(kvq.make_pages_config(1, 2, 16, 2, 2, 64))
+    x = torch.randn((2, 2, 64), device="cuda").half()
+
+    def step(second_page):
+        lens = cache.kvq_pages_grow(starts([1, 1]), ints([[0, -1], [1, -1]]), ints([16, 10]), ints([1, 1]))
+        assert lens.tolist() == [-17, -11]
+        cache.kvq_pages_append(0, x, x, kvq.PagesBatch(starts([1, 1]), lens, ints([[0, -1], [1, -1]]), 2, 1))
+        cache.kvq_pages_append(0, x, x, kvq.PagesBatch(starts([1, 1]), ints([1, 1]), ints([[0], [second_page]]), 2, 1))
+
+    step(1)
+    assert cache.kvq_pages_status() == 8 and "free pages" in said(cache) and "range" not in said(cache)
+    assert cache.kvq_pages_status() == 0
+    step(9)
+    assert cache.kvq_pages_status() == 7 and "range" in said(cache) and "free pages" in said(cache)
+    assert cache.kvq_pages_status() == 0
+    # a negative length alone is an index out of range
+    batch = kvq.PagesBatch(starts([1, 1]), ints([-17, 1]), ints([[0], [1]]), 2, 1)
+    tree = kvq.PagesTree(torch.ones((2, 1), dtype=torch.int64, device="cuda"), ints([0, 0]))
+    for call in (lambda: cache.kvq_pages_append(0, x, x, batch), lambda: cache.kvq_pages_read(0, batch),
+                 lambda: cache.kvq_pages_attn(0, x, batch), lambda: cache.kvq_pages_cross_attn(0, x, batch),
+                 lambda: cache.kvq_pages_tree_attn(0, x, batch, tree),
+                 lambda: cache.kvq_pages_tree(ints([-1, -1]), batch),
+                 lambda: cache.kvq_pages_keep(torch.ones(2, dtype=torch.bool, device="cuda"), batch)):
+        call()
+        assert cache.kvq_pages_status() == 7 and "free pages" not in said(cache)
 
 
 # ----------------------------------------------------- outputs over what is read --

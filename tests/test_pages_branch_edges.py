@@ -6,7 +6,8 @@ import pytest
 import torch
 
 from bit_quantized_kv_02_gb300 import build, kvq
-from tests.test_pages_branch import ints, starts
+from tests.test_pages import fill, make
+from tests.test_pages_branch import ints, kept, layers_of, starts
 
 gpu = pytest.mark.gpu
 
@@ -105,6 +106,66 @@ def test_a_bad_page_is_reported_in_a_step_that_runs_out_of_pages():
                  lambda: cache.kvq_pages_keep(torch.ones(2, dtype=torch.bool, device="cuda"), batch)):
         call()
         assert cache.kvq_pages_status() == 7 and "free pages" not in said(cache)
+
+
+# ---------------------------------------------------------------------- keep --
+
+KEPT = pytest.mark.parametrize("fmt,h,d", [("bf16", 3, 64), ("4_8", 2, 256), ("8_4", 5, 128)])
+
+
+@gpu
+@KEPT
+@pytest.mark.parametrize("share", [0.1, 0.6, 0.99])
+def test_keep_of_long_sequences_that_begin_before_their_first_token(fmt, h, d, share):
+    """Rows with negative positions are no tokens, marked or not; segments are counted behind them."""
+    c = make(([600, 5, 300, 2, 1000], [450, 5, 20, 0, 1000]), 32, fmt, (h, h), d, layers=2, seed=6, pad=3)
+    for i in range(2):
+        fill(c, h, d, layer=i)
+    for layer in (kvq.ALL_LAYERS, 1):
+        keep = torch.rand(c.rows, generator=c.g) < share
+        before = layers_of(c, 2)
+        lens = c.cache.kvq_pages_keep(keep.cuda(), c.batch(), layer=layer)
+        assert c.cache.kvq_pages_status() == 0
+        for i, (x, y) in enumerate(zip(layers_of(c, 2), before)):
+            want, new = kept(c, keep.tolist(), y) if layer in (kvq.ALL_LAYERS, i) else (y, None)
+            assert all(torch.equal(a, b) for a, b in zip(x, want))
+        assert lens.tolist() == kept(c, keep.tolist(), before[0])[1]
+
+
+@gpu
+@KEPT
+def test_keep_of_long_sequences_with_bad_pages_and_lengths(fmt, h, d):
+    """A row that would leave or enter a page outside the pool stays, a sequence whose length does not fit is left
+    alone; what stands before and behind them is right."""
+    news, lens, pt = [700, 400, 1000, 900], [700, 400, 1000, 1300], 64
+    c = make((news, lens), pt, fmt, (h, h), d, layers=1, seed=9)
+    fill(c, h, d)
+    before = layers_of(c, 1)[0]
+    keep = torch.rand(c.rows, generator=c.g) < 0.7
+    bad = {(0, 4), (0, 10), (2, 7), (3, 12)}  # (sequence, entry of its table)
+    table = c.table.clone()
+    for k, (b, e) in enumerate(sorted(bad)):
+        table[b, e] = c.pages + 5 if k % 2 else -3
+    told = [700, 1 << 20, 1000, 1300]
+    got = c.cache.kvq_pages_keep(keep.cuda(), kvq.PagesBatch(c.q_start.cuda(), ints(told), table.cuda(), c.rows))
+    assert c.cache.kvq_pages_status() == 7
+    after = layers_of(c, 1)[0]
+    row = at = 0
+    for b, (n, ln) in enumerate(zip(news, lens)):
+        first, to = ln - n, ln - n
+        want = [x[at:at + ln].clone() for x in before]
+        for i in range(n if b != 1 else 0):
+            if not keep[row + i]:
+                continue
+            if (b, to // pt) not in bad and (b, (first + i) // pt) not in bad:
+                for w, x in zip(want, before):
+                    w[to] = x[at + first + i]
+            to += 1
+        assert got[b] == (told[1] if b == 1 else to)
+        for w, x in zip(want, after):
+            assert torch.equal(x[at:at + ln], w), b
+        row += n
+        at += ln
 
 
 # ----------------------------------------------------- outputs over what is read --

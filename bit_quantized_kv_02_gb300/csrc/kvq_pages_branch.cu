@@ -321,10 +321,11 @@ __global__ void __launch_bounds__(kPlanThreads) pages_keep_plan_kernel(PagesView
 
 // A step's chain of loads (ticket, segment, marks, page table, tokens) is spread over the
 // steps before it: while a step's tokens come, the places of the next one's are found, the
-// segment of the one after is read and the ticket of a third is drawn.
+// segment of the one after is read and the ticket of a third is drawn.  A step whose wait
+// passes `limit` ns leaves its tokens where they are and is recorded.
 __global__ void __launch_bounds__(kKeepThreads, 2) pages_keep_move_kernel(PagesView pv, long layer_bytes, long units,
                                                                          BatchView bv, const uint8_t* keep, KeepPlan* plan,
-                                                                         KeepSeg* seg) {
+                                                                         KeepSeg* seg, unsigned long long limit) {
   constexpr int U = kSegRows / (kKeepThreads / 32);  // tokens of a warp
   __shared__ long2 move[2][kSegRows];
   __shared__ int sums[kSegRows / 32], ready;
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kKeepThreads, 2) pages_keep_move_kernel(PagesV
         const unsigned long long t0 = time_ns();
         bool late = false;
         for (int k = seg0; k <= seg1; ++k)
-          while (!late && load_acquire(&seg[now.id - g.at + k].done) < blocks) late = time_ns() - t0 > kWaitNs;
+          while (!late && load_acquire(&seg[now.id - g.at + k].done) < blocks) late = time_ns() - t0 > limit;
         if (late) atomicOr(pv.err, 2);
         ready = !late;
       }
@@ -724,7 +725,8 @@ cudaError_t launch_pages_keep(const PagesView& pv, int layers, long layer_bytes,
   void* args1[] = {&p, &b, &keep, &lens_out, &plan, &seg};
   cudaError_t e = launch_pdl((const void*)pages_keep_plan_kernel, dim3(bv.batch), dim3(kPlanThreads), 0, st, args1);
   if (e != cudaSuccess) return e;
-  void* args2[] = {&p, &layer_bytes, &units, &b, &keep, &plan, &seg};
+  unsigned long long limit = kWaitNs;
+  void* args2[] = {&p, &layer_bytes, &units, &b, &keep, &plan, &seg, &limit};
   const double most = (bv.new_tokens / kSegRows + bv.batch) * (double)((units + 31) / 32);
   return launch_pdl((const void*)pages_keep_move_kernel, dim3((unsigned)std::min(most, 152.0 * 2)), dim3(kKeepThreads), 0, st,
                     args2);

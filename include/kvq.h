@@ -492,8 +492,10 @@ kvq_status kvq_pages_read(kvq_pages_t pages, int layer, const kvq_pages_batch* b
  * a row that would come from or go to a page outside the pool stays, and a sequence
  * whose indices are out of range is left alone (lens_out[b] = lens[b]); both are
  * reported.  Tokens only move inside their sequence's pages: a page that others
- * share must not lie at or behind the first token that moves.  Calls on one handle
- * share its workspace: order them on one stream. */
+ * share must not lie at or behind the first token that moves.  After a
+ * KVQ_ERR_DEVICE_TIMEOUT some tokens have moved and others not, whatever lens_out
+ * says: what the batch's sequences hold from their first new token on is lost.  Calls
+ * on one handle share its workspace: order them on one stream. */
 kvq_status kvq_pages_keep(kvq_pages_t pages, int layer, const kvq_pages_batch* batch, const uint8_t* keep,
                           int32_t* lens_out, void* stream);
 

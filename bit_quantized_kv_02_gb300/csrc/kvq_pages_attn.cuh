@@ -42,16 +42,6 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, int parity) {
       : "memory");
   return ok;
 }
-// (without waiting at all)
-__device__ __forceinline__ bool mbar_test(uint32_t bar, int parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok;
-}
 __device__ __forceinline__ unsigned long long time_ns() {
   unsigned long long t;
   asm volatile("mov.u64 %0, %globaltimer;\n" : "=l"(t));

@@ -9,7 +9,7 @@
 //  - loader (16-bit pages): bulk copies of the records' halves into K and V
 //    stages; pages are stored in the operand layout, so no tensor map and no
 //    shuffling is needed;
-//  - dequantizers (codes): two warps per tensor (four with one row tile) copy records
+//  - dequantizers (codes): three warps per tensor (four with one row tile) copy records
 //    ahead and turn their codes into fp16 operand tiles (the value the page stands for,
 //    one rounding);
 //  - one warp issues the matrix instructions: S = Q K^T (both from shared

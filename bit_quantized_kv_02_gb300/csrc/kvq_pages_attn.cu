@@ -179,18 +179,19 @@ cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, bool masked, int max_ro
   // unknown rows too, since the kernel decides how its weights are rounded (where
   // they are given, the second launch would cost 10 us for nothing: 64 tokens at 4k,
   // 32 over 8 heads of 128, 39 us with one launch and 49 with two).  Measured, few /
-  // many rows, us, 8 sequences of 8192 tokens: 16-bit pages, 12 heads of 64: 32 rows
-  // 52 / 68, 48 rows 86 / 69; 8 heads of 128: 57 / 66, 96 / 67; 2 heads of 256:
-  // 48 / 51, 61 / 53.  Codes cost the many-rows kernel its dequantizing warps: 4 bits, heads of 64: 128 rows
-  // 138 / 159, 192 rows 204 / 189; heads of 128: 64 rows 91 / 99, 96 rows 125 / 103;
-  // heads of 256: 48 rows 57 / 61, 64 rows 67 / 62.
-  // The masked kernels were measured after the many-rows kernel had become faster (over
-  // codes the causal ones keep the choice, and with it the rounding, that they had).  8
-  // sequences of 8192 tokens, few / many rows, us: 16-bit pages, 12 heads of 64: 32 rows
-  // 53 / 58, 48 rows 104 / 58; 8 heads of 128: 60 / 63, 99 / 64; 2 heads of 256: 50 / 52,
-  // 64 / 53.  8 bits, heads of 64: 48 rows 71 / 72, 64 rows 89 / 73; heads of 128: 32 rows
-  // 62 / 66, 48 rows 79 / 67; heads of 256: 16 rows 40 / 44, 32 rows 53 / 47.  4 bits:
-  // 65 / 71, 81 / 72; 57 / 60, 70 / 61; 36 / 40, 50 / 42.
+  // many rows, us, 8 sequences of 8192 tokens, causal: 16-bit pages, 12 heads of 64: 32 rows
+  // 52 / 61, 48 rows 97 / 61; 8 heads of 128: 59 / 62, 98 / 64; 2 heads of 256:
+  // 48 / 52, 61 / 55.  4 bits, heads of 64: 48 rows 63 / 71, 64 rows 81 / 72, 128 rows 134 / 74;
+  // heads of 128: 32 rows 55 / 61, 48 rows 69 / 62, 64 rows 88 / 63; heads of 256: 16 rows
+  // 35 / 41, 32 rows 48 / 43, 48 rows 56 / 45.
+  // So the causal limits over codes (128, 64 and 48 rows) stand above the crossing.  They are
+  // where a many-rows kernel of 159, 99 and 61 us there crossed, and have been kept while it
+  // became faster: both kernels round the weights alike over codes, but a lower limit would
+  // change the order of sums of the calls between.
+  // Masked: 16-bit pages, heads of 64: 32 rows 53 / 58, 48 rows 104 / 58; of 128: 60 / 63,
+  // 99 / 65; of 256: 50 / 52, 64 / 53.  8 bits, heads of 64: 48 rows 71 / 72, 64 rows 90 / 73;
+  // heads of 128: 32 rows 62 / 66, 48 rows 78 / 67; heads of 256: 16 rows 40 / 44, 32 rows
+  // 53 / 47.  4 bits: 65 / 71, 82 / 71; 57 / 60, 69 / 61; 36 / 40, 49 / 42.
   const int D = P->cfg.head_dim;
   const int few = P->L.k_bits == 16 ? 32
                   : masked          ? (D == 64 ? 48 : (D == 128 ? 32 : 16))
@@ -204,7 +205,11 @@ cudaError_t launch_pages_attn(kvq_pages* P, AttnArgs& a, bool masked, int max_ro
   // rounded alike by both, the few-rows kernel would be its largest form, and its launch
   // and join cost 10 us.  32 trees of 1 to 31 tokens over 500 to 8192 4-bit tokens, 32 over
   // 8 heads of 128: 205 us with both, 202 with one (187 with three dequantizing warps a
-  // tensor).
+  // tensor).  The rule does not look at how many sequences have few rows, and loses where
+  // most have: one launch / both, us, single tokens and trees of 64 over 4096 4-bit tokens,
+  // 12 heads of 64, 32 over 8 of 128, 16 over 2 of 256: 63 and 1 242 / 138, 239 / 203, 111 /
+  // 108; 32 and 32 244 / 206, 254 / 253, 240 / 248; 4 and 60 246 / 256, 261 / 281, 345 / 377;
+  // 15 and 1 72 / 60, 78 / 89, 42 / 63; 8 and 8 73 / 70, 81 / 99, 78 / 100.
   if (masked && rows_given && P->L.k_bits != 16) return launch_tile(P, a, masked, max_rows, st);
   a.rows_lo = few;
   cudaError_t e = launch_tile(P, a, masked, max_rows, st);

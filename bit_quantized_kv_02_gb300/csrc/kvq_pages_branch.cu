@@ -5,12 +5,12 @@
 // A tree's masks and a table's entries are a few KB: what these kernels cost is their
 // launch and one chain of loads after another, so each keeps the chain short.  Moving
 // tokens and copying pages are bound by memory.  Measured, each kernel alone with cold
-// caches: masks of 16 trees of 64 tokens 6 us; fork of 64 rows of 250 pages 6 + 4 us (table,
-// counts), of 256 rows of 1900 pages over a pool of 60000 6 + 5; growth of 64 rows by a
-// token 10 us and 6 for the copies of shared last pages, of 256 rows by up to 600 tokens
-// 23 + 6; 509 pages of 64 tokens, 40 heads of 128, 8- and 4-bit, four layers: 334 us, 6.5
+// caches: masks of 16 trees of 64 tokens 6 us; fork of 64 rows of 250 pages 5 + 3 us (table,
+// counts), of 256 rows of 1900 pages over a pool of 60000 6 + 4; growth of 64 rows by a
+// token 12 us and 5 for the copies of shared last pages, of 256 rows by up to 600 tokens
+// 24 + 4; 509 pages of 64 tokens, 40 heads of 128, 8- and 4-bit, four layers: 334 us, 6.5
 // TB/s read and written (96 % of a copy).  Half of 8 sequences of 9k to 16k 4-bit tokens, 8 heads of 128, four layers at
-// once: 7 + 140 us, 3.0 TB/s: a (head, token) is 144 bytes in four pieces, and a warp's
+// once: 6 + 138 us, 3.0 TB/s: a (head, token) is 144 bytes in four pieces, and a warp's
 // access touches eleven lines of the L1 cache for four lines' worth of bytes.
 #include <algorithm>
 
@@ -562,9 +562,9 @@ struct GrowArgs {
 // One CTA deals out the pages: what a sequence gets depends on all before it.  A warp goes
 // through a sequence's entries, once to count the fresh pages that they need and, where the
 // sequence gets them, once to deal them out; one that does not get them, or that needs an
-// entry outside the pool, has not been written to (marks in the table, which the first
-// look left for the second, were 0.8 us faster).  (All entries in one line, four a
-// thread: 18 us against 10 for 64 rows by a token, 31 against 23 for 256 rows by up to 600.)
+// entry outside the pool, has not been written to.  (Marks in the table, which the first
+// look left for the second, were 1 to 2 us faster; all entries in one line, four a thread,
+// 8 us slower.)
 __global__ void __launch_bounds__(kGrowThreads) pages_grow_kernel(PagesView pv, GrowArgs g) {
   __shared__ int page[kGrowThreads];     // the page that holds the sequence's last tokens and is grown into, or -1
   __shared__ int first[kGrowThreads], last[kGrowThreads];  // entries of the table that the new tokens need

@@ -848,5 +848,7 @@ class KVQPages:
 
     def kvq_pages_status(self, stream=None) -> int:
         """Synchronises and returns what kernels recorded since the last call (0: nothing): calls
-        return before their kernels run, so a bad index or a wait that ran out shows only here."""
+        return before their kernels run, so a bad index or a wait that ran out shows only here.
+        Of several the first in this order: 6 (a wait), 7 (an index), 8 (pages ran out), 7 for
+        negative lengths alone; kvq_pages_last_error names all."""
         return _on_device(self.index, stream, self._lib.kvq_pages_status, self.handle)

@@ -540,7 +540,7 @@ kvq_status kvq_pages_fork(kvq_pages_t pages, const kvq_pages_fork_args* args, vo
  * is replaced, not copied.  Pages that become free are dealt out by a later call.
  * Where the free pages run out, the sequence and all growing ones behind it stay as
  * they are, with lens_out[b] = -1 - lens[b], a length that every other call skips and
- * this one hands on (KVQ_ERR_OUT_OF_PAGES from kvq_pages_status); the same goes for a
+ * this one hands on until the caller turns it back (KVQ_ERR_OUT_OF_PAGES from kvq_pages_status); the same goes for a
  * single sequence whose indices are out of range, the table entries that its new tokens
  * need among them (KVQ_ERR_BAD_INDEX; a negative entry names none).  lens_out may be
  * lens.  Calls on one handle share its workspace: order them on one stream. */
